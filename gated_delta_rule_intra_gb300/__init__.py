@@ -19,6 +19,10 @@ The functions carry the C names of ``include/kda.h``:
   fixed device array (``HOST_STATIC_MAX_BYTES``) for callers that cannot allocate
 * ``kda_intra_fwd``       -- the forward score matrices Aqk, Akk (grouped value heads
   and variable-length sequences through ``kda_intra_fwd_ex``)
+* ``kda_chunk_fwd``, ``kda_chunk_bwd`` -- the gated delta-rule recurrence over whole
+  sequences, forward and backward (``recurrence.py``)
+* ``kda_step``            -- its single-token form, states updated in place
+* ``kda_layer_norm_fwd``, ``kda_layer_norm_bwd`` -- layer norm (``norm.py``)
 * ``kda_status_str``, ``kda_abi_version``
 * ``use_library``, ``kda_debug_checks``, ``kda_debug_set_flags`` -- run the same calls
   through the bounds-checked debug build ``libkda_debug.so`` (tests)
@@ -32,13 +36,17 @@ import os
 
 import torch
 
+from . import _common
+from .norm import kda_layer_norm_bwd, kda_layer_norm_fwd
+from .recurrence import kda_chunk_bwd, kda_chunk_fwd, kda_step
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkda.so")
 DEBUG_LIB_PATH = os.path.join(_HERE, "libkda_debug.so")
 
 # KDA_ABI_VERSION of the include/kda.h these ctypes mirrors follow (option structs,
 # signatures); a library of any other version is refused at load.
-ABI_VERSION = 9
+ABI_VERSION = 10
 KDA_OK = 0
 KDA_BF16 = 0
 KDA_FP16 = 1
@@ -110,6 +118,8 @@ def load_library(path: str | None = None):
     lib.kda_abi_version.restype = i
     lib.kda_debug_checks.argtypes = []
     lib.kda_debug_checks.restype = i
+    if hasattr(lib, "kda_chunk_fwd"):  # not in a library of an older ABI version, refused below
+        _common.declare(lib)
     lib.kda_debug_set_flags.argtypes = [vp]
     lib.kda_debug_set_flags.restype = st
     if lib.kda_abi_version() != ABI_VERSION:

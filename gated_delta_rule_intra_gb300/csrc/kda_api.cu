@@ -220,6 +220,11 @@ kda_status_t host_pipe(HostPipe **out) {
 
 }  // namespace
 
+namespace kda {
+kda_status_t require_device() { return check_device(); }
+unsigned *debug_flags() { return g_debug_flags; }
+}  // namespace kda
+
 extern "C" {
 
 kda_status_t kda_intra_bwd_fp32(const void *q, const void *k, const float *g,

@@ -1,0 +1,284 @@
+// Shared parts of the gated delta-rule recurrence kernels (forward and backward).
+//
+// Per value head the state S is [128 dk, 128 dv] in FP32.  A token decays it per channel,
+// S~ = diag(2^gate) S, and corrects it towards its value: e = v - S~^T k,
+// S' = S~ + beta k e^T, o = scale S'^T q.  The kernels walk a sequence in steps of C = 16
+// tokens.  With g the inclusive cumsum of the gate inside the step and g_l its last row,
+//   kw = k 2^g,  qw = scale q 2^g,  kd = k 2^(g_l - g),
+//   M[r,s] = sum_d k_r k_s 2^(g_r - g_s) (s < r),  P[r,s] = scale sum_d q_r k_s 2^(..) (s <= r)
+//   e = T2 (v - kw S) with T2 = (I + M diag(beta))^-1,   n = beta e,
+//   o = qw S + P n,   S' = diag(2^g_l) S + kd^T n
+// and backwards, with T = (I + diag(beta) M)^-1,
+//   dn = P^T do + kd dS',  Y = T^T dn,  dv = beta Y,
+//   dS = diag(2^g_l) dS' + qw^T do - kw^T (beta Y).
+// Every exponent is <= 0 for gates <= 0.  e, n and Y do not depend on where steps begin.
+//
+// The state never leaves the registers: each consumer warp owns 16 of the 128 dv columns of
+// S as the accumulators of S^T [16 dv, 128 dk], which are also the fragments of the next
+// product's left operand, so the chain S -> kw S -> e -> S' has no shared-memory round trip
+// and no exchange between warps.  That is why these kernels use mma.sync: a step's products
+// have 16 or 32 columns, and a tensor-memory accumulator would have to come back through the
+// registers (to be rounded to operands) three times a step.
+//
+// Precision: products of FP32 values are taken as three BF16 products with FP32 sums, x being
+// hi + lo with hi = bf16(x), lo = bf16(x - hi): 16 bits of x are kept (2^-17 relative), the
+// dropped lo * lo is below 2^-16 of the product, and BF16 keeps FP32's range, which a state
+// that a user may scale freely needs.  A TF32 operand would keep 11 bits at half the rate.
+#pragma once
+
+#include "kda_common.cuh"
+#include "tc_ptx.cuh"
+
+namespace kda {
+namespace chunk {
+
+constexpr int C = 16;            // tokens a step
+constexpr int D = KD;            // channels of q and k, and of v
+constexpr int kPrepWarps = 8;
+constexpr int kPrepThreads = 32 * kPrepWarps;
+constexpr int kPlane = C * D * 2;      // bytes of a BF16 [16][128] operand plane
+constexpr int kTile = C * C * 2;       // bytes of a BF16 [16][16] tile
+constexpr size_t kCkptBytes = 2 * D * D * 2;  // a state checkpoint: hi and lo planes
+constexpr size_t kRowPlane = BT * D * 2;      // one BF16 plane of 64 rows of dv
+constexpr size_t kRowsBytes = 2 * kRowPlane;  // e or Y of 64 tokens: hi and lo planes
+constexpr size_t kTilesBytes = 4 * kTile;     // T hi, T lo, P hi, P lo of a step
+
+// Gates below this are taken as this: 2^-160 is 0 in FP32 either way, and differences of the
+// cumulative gate stay finite for gates of the type's lowest value or -infinity.  The
+// comparison keeps NaN.
+__device__ __forceinline__ float floor_gate(float x) { return x < -160.f ? -160.f : x; }
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// (x, y) as two BF16 pairs: hi = bf16(.), lo = bf16(. - hi)
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = pack_bf16(x, y);
+    lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// Transpose of an 8x8 matrix of 16-bit values held in fragment order by a warp.
+__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void bar_sync(int id, int n) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int n) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+// cp.async of 16 (or 4) bytes, zeros when !ok.
+__device__ __forceinline__ void cp16z(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(ok ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp4z(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+                 "r"(ok ? 4 : 0)
+                 : "memory");
+}
+template <int N> __device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Byte offset of the 16-byte chunk c of row r in a swizzled [16][128] BF16 plane: the eight
+// rows that one ldmatrix phase reads fall into different banks.
+__device__ __forceinline__ uint32_t plane_off(int r, int c) {
+    return (uint32_t)(r * 256 + ((c ^ (r & 7)) << 4));
+}
+
+// A sequence: its rows in the [rows, heads, 128] tensors and its slots of 64 tokens.
+struct Seq {
+    long long row0;  // first token
+    int len;         // tokens
+    int slot0;       // first 64-token slot in the checkpoint buffers
+};
+
+// Sequence n of the launch.  Fixed length: n = batch index.  Variable length: the tokens
+// [cu[n], cu[n+1]) clamped to the packed length, slots from cu[n] / 64 + n on (no two
+// sequences' slots meet, and T / 64 + num_seqs + 1 slots cover every input).
+__device__ __forceinline__ Seq seq_of(int n, int T, const int *cu) {
+    Seq s;
+    if (cu) {
+        int a = cu[n], b = cu[n + 1];
+        a = a < 0 ? 0 : a > T ? T : a;
+        b = b < a ? a : b > T ? T : b;
+        s.row0 = a;
+        s.len = b - a;
+        s.slot0 = a / BT + n;
+    } else {
+        s.row0 = (long long)n * T;
+        s.len = T;
+        s.slot0 = n * ((T + BT - 1) / BT);
+    }
+    return s;
+}
+
+// Raw inputs of a step in shared memory.
+struct __align__(16) RawStage {
+    uint16_t q[C][D];
+    uint16_t k[C][D];
+    float gate[C][D];
+};
+
+template <typename T16> __device__ __forceinline__ float2 unpack2(uint32_t x);
+template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t x) {
+    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t x) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&x));
+}
+template <typename T16> __device__ __forceinline__ uint32_t pack2(float x, float y);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) {
+    return pack_bf16(x, y);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float x, float y) {
+    __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+
+// The six operand planes of a step.
+enum { KW_HI = 0, KW_LO, QW_HI, QW_LO, KD_HI, KD_LO, kPlanes };
+
+// Operand planes from the raw inputs: 256 threads, each two channels of four rows.  Writes
+// the cumulative gate (gbuf, when asked for), the planes and 2^g_l.
+template <typename T16, bool WRITE_G>
+__device__ __forceinline__ void prep_planes(const RawStage &raw, char *planes, float *decay,
+                                            float (*gbuf)[D], float scale, int tid) {
+    const int c2 = tid & 63, r0 = (tid >> 6) * 4;
+    float2 g[4], acc = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < C; ++r) {
+        const float2 x = *reinterpret_cast<const float2 *>(&raw.gate[r][2 * c2]);
+        acc.x += floor_gate(x.x);
+        acc.y += floor_gate(x.y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (r == r0 + i) g[i] = acc;
+    }
+    if (r0 == 0) *reinterpret_cast<float2 *>(&decay[2 * c2]) = make_float2(ex2(acc.x), ex2(acc.y));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + i;
+        if (WRITE_G) *reinterpret_cast<float2 *>(&gbuf[r][2 * c2]) = g[i];
+        const float2 q = unpack2<T16>(*reinterpret_cast<const uint32_t *>(&raw.q[r][2 * c2]));
+        const float2 k = unpack2<T16>(*reinterpret_cast<const uint32_t *>(&raw.k[r][2 * c2]));
+        const float2 up = make_float2(ex2(g[i].x), ex2(g[i].y));
+        const float2 dn = make_float2(ex2(acc.x - g[i].x), ex2(acc.y - g[i].y));
+        const uint32_t off = plane_off(r, c2 >> 2) + (c2 & 3) * 4;
+        uint32_t hi, lo;
+        split2(k.x * up.x, k.y * up.y, hi, lo);
+        *reinterpret_cast<uint32_t *>(planes + KW_HI * kPlane + off) = hi;
+        *reinterpret_cast<uint32_t *>(planes + KW_LO * kPlane + off) = lo;
+        split2(scale * q.x * up.x, scale * q.y * up.y, hi, lo);
+        *reinterpret_cast<uint32_t *>(planes + QW_HI * kPlane + off) = hi;
+        *reinterpret_cast<uint32_t *>(planes + QW_LO * kPlane + off) = lo;
+        split2(k.x * dn.x, k.y * dn.y, hi, lo);
+        *reinterpret_cast<uint32_t *>(planes + KD_HI * kPlane + off) = hi;
+        *reinterpret_cast<uint32_t *>(planes + KD_LO * kPlane + off) = lo;
+    }
+}
+
+// Sums of 32 values over the 32 lanes; lane i returns the sum of v[i].
+__device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const bool up = lane & off;
+#pragma unroll
+        for (int i = 0; i < off; ++i) {
+            const float keep = up ? v[i + off] : v[i], send = up ? v[i] : v[i + off];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+        }
+    }
+    return v[0];
+}
+
+// hi and lo A-fragments of a 16x16 FP32 block held as two adjacent 16x8 accumulators.
+__device__ __forceinline__ void split_frag(const float (&c0)[4], const float (&c1)[4],
+                                           uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+    split2(c0[0], c0[1], hi[0], lo[0]);
+    split2(c0[2], c0[3], hi[1], lo[1]);
+    split2(c1[0], c1[1], hi[2], lo[2]);
+    split2(c1[2], c1[3], hi[3], lo[3]);
+}
+
+// acc[2] (16x16) += A (hi, lo) * B, B's hi and lo fragments of two 8-column tiles.
+__device__ __forceinline__ void mma3(float (&c0)[4], float (&c1)[4], const uint32_t (&ah)[4],
+                                     const uint32_t (&al)[4], const uint32_t (&bh)[4],
+                                     const uint32_t (&bl)[4]) {
+    mma16816(c0, ah, bh[0], bh[1]);
+    mma16816(c1, ah, bh[2], bh[3]);
+    mma16816(c0, ah, bl[0], bl[1]);
+    mma16816(c1, ah, bl[2], bl[3]);
+    mma16816(c0, al, bh[0], bh[1]);
+    mma16816(c1, al, bh[2], bh[3]);
+}
+
+// Per-lane byte offsets of ldmatrix.x4 in a [16][16] tile with 32-byte rows: matrices
+// (rows 0-7, cols 0-7), (rows 0-7, cols 8-15), (rows 8-15, cols 0-7), (rows 8-15, cols 8-15).
+__device__ __forceinline__ uint32_t tile_lane(int lane) {
+    return (uint32_t)(((lane & 7) + ((lane >> 4) & 1) * 8) * 32 + ((lane >> 3) & 1) * 16);
+}
+
+// The accumulators of S^T [16 dv, 128 dk] as BF16 hi/lo planes in 8x8 blocks
+// [dk / 8][dv / 8][8 dk][8 dv] (128 contiguous bytes a block): rows of dk, dv contiguous, the
+// K-major operand of every product that sums over dv.
+__device__ __forceinline__ void store_checkpoint(char *base, const float (&S)[16][4], int dv0,
+                                                 int lane) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        uint32_t h0, l0, h1, l1;
+        split2(S[j][0], S[j][1], h0, l0);
+        split2(S[j][2], S[j][3], h1, l1);
+        char *p = base + ((size_t)j * 16 + dv0 / 8) * 128 + lane * 4;
+        *reinterpret_cast<uint32_t *>(p) = movm_t(h0);
+        *reinterpret_cast<uint32_t *>(p + 128) = movm_t(h1);
+        *reinterpret_cast<uint32_t *>(p + D * D * 2) = movm_t(l0);
+        *reinterpret_cast<uint32_t *>(p + D * D * 2 + 128) = movm_t(l1);
+    }
+}
+
+// A [16 dv, 16 token] accumulator pair as hi/lo planes of rows of tokens, in 8x8 blocks
+// [token / 8][dv / 8][8 token][8 dv]; t0 is the step's first token in its 64-token slot.
+__device__ __forceinline__ void store_rows(char *base, const float (&x)[2][4], int t0, int dv0,
+                                           int lane) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t h0, l0, h1, l1;
+        split2(x[j][0], x[j][1], h0, l0);
+        split2(x[j][2], x[j][3], h1, l1);
+        char *p = base + ((size_t)(t0 / 8 + j) * 16 + dv0 / 8) * 128 + lane * 4;
+        *reinterpret_cast<uint32_t *>(p) = movm_t(h0);
+        *reinterpret_cast<uint32_t *>(p + 128) = movm_t(h1);
+        *reinterpret_cast<uint32_t *>(p + kRowPlane) = movm_t(l0);
+        *reinterpret_cast<uint32_t *>(p + kRowPlane + 128) = movm_t(l1);
+    }
+}
+
+}  // namespace chunk
+}  // namespace kda

@@ -1,0 +1,249 @@
+// Backward of the gated delta-rule recurrence, first pass: the state's gradient walks each
+// (sequence, value head) backwards in steps of 16 tokens, as the forward walks it forwards
+// (see kda_chunk.cuh).  Writes dv, Y (the gradient of beta e's source, dv = beta Y) and the
+// state's gradient at the end of each 64-token slot, from which the second pass takes the
+// other gradients of all slots at once.
+#include <type_traits>
+
+#include "kda_chunk.cuh"
+#include "kda_ops.h"
+
+namespace kda {
+namespace chunk {
+namespace {
+
+constexpr int kRaw = 3, kRing = 4, kStages = 2;
+
+enum { BAR_PREP = 1, BAR_FULL = 2, BAR_EMPTY = 4 };  // FULL, EMPTY + stage
+
+struct __align__(128) Prepared {
+    char planes[kPlanes * kPlane];
+    float decay[D];
+};
+
+struct __align__(128) Smem {
+    Prepared prep[kStages];
+    RawStage raw[kRaw];
+    uint16_t dout[kRing][C][D];   // rows of the CTA's dv slice, swizzled chunks
+    char tiles[kRing][kTilesBytes];
+    float beta[kRing][C];
+};
+
+// Step i of the walk (the last step of the sequence first): token 16 * step on.
+template <int NC>
+__device__ __forceinline__ void load_step(Smem &sm, const ChunkBwdArgs &a, const Seq &sq, int h,
+                                          int hv, int dv0, int i, int step, int tid) {
+    const int row = tid >> 4, c = tid & 15;
+    const int t = step * C + row;
+    const bool ok = t < sq.len;
+    const size_t tok = (size_t)sq.row0 + (ok ? t : 0);
+    RawStage &raw = sm.raw[i % kRaw];
+    const size_t iq = (tok * a.H + h) * D + c * 8, iv = (tok * a.HV + hv) * D;
+    cp16z(tc::smem_u32(&raw.q[row][c * 8]), (const uint16_t *)a.q + iq, ok);
+    cp16z(tc::smem_u32(&raw.k[row][c * 8]), (const uint16_t *)a.k + iq, ok);
+    cp16z(tc::smem_u32(&raw.gate[row][c * 4]), a.gate + iv + c * 4, ok);
+    cp16z(tc::smem_u32(&raw.gate[row][64 + c * 4]), a.gate + iv + 64 + c * 4, ok);
+    if (c < 2 * NC)
+        cp16z(tc::smem_u32(sm.dout[i % kRing]) + plane_off(row, c),
+              (const uint16_t *)a.dout + iv + dv0 + c * 8, ok);
+    if (c == 0) cp4z(tc::smem_u32(&sm.beta[i % kRing][row]), a.beta + tok * a.HV + hv, ok);
+    if (tid < (int)kTilesBytes / 16)
+        cp16z(tc::smem_u32(sm.tiles[i % kRing]) + tid * 16,
+              a.tiles +
+                  (((size_t)(sq.slot0 + step / 4) * a.HV + hv) * 4 + step % 4) * kTilesBytes +
+                  tid * 16,
+              true);
+}
+
+// acc += A B with A a 16-bit input fragment: exact in BF16, split in two for FP16.
+template <typename T16>
+__device__ __forceinline__ void mma_in(float (&c0)[4], float (&c1)[4], const uint32_t (&ah)[4],
+                                       const uint32_t (&al)[4], const uint32_t (&bh)[4],
+                                       const uint32_t (&bl)[4]) {
+    mma16816(c0, ah, bh[0], bh[1]);
+    mma16816(c1, ah, bh[2], bh[3]);
+    mma16816(c0, ah, bl[0], bl[1]);
+    mma16816(c1, ah, bl[2], bl[3]);
+    if (sizeof(T16) == 2 && !std::is_same<T16, __nv_bfloat16>::value) {
+        mma16816(c0, al, bh[0], bh[1]);
+        mma16816(c1, al, bh[2], bh[3]);
+    }
+}
+
+template <typename T16, int NC>
+__global__ void __launch_bounds__(kPrepThreads + 32 * NC, 1)
+    kda_chunk_bwd_state_kernel(const ChunkBwdArgs a) {
+    extern __shared__ __align__(128) char smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
+    constexpr int kSplit = 8 / NC;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int unit = blockIdx.x / kSplit, dv0 = (blockIdx.x % kSplit) * NC * 16;
+    const int n = unit / a.HV, hv = unit - n * a.HV, h = hv / (a.HV / a.H);
+    const Seq sq = seq_of(n, a.T, a.cu_seqlens);
+    const int steps = (sq.len + BT - 1) / BT * (BT / C);
+
+    if (warp < kPrepWarps) {
+        if (NC == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        for (int i = 0; i < kRaw - 1; ++i) {
+            if (i < steps) load_step<NC>(sm, a, sq, h, hv, dv0, i, steps - 1 - i, tid);
+            cp_async_commit();
+        }
+        for (int i = 0; i < steps; ++i) {
+            const int st = i & 1;
+            cp_wait<kRaw - 2>();
+            if (i >= kStages) bar_sync(BAR_EMPTY + st, kPrepThreads + 32 * NC);
+            bar_sync(BAR_PREP, kPrepThreads);
+            if (i + kRaw - 1 < steps)
+                load_step<NC>(sm, a, sq, h, hv, dv0, i + kRaw - 1, steps - kRaw - i, tid);
+            cp_async_commit();
+            prep_planes<T16, false>(sm.raw[i % kRaw], sm.prep[st].planes, sm.prep[st].decay,
+                                    nullptr, a.scale, tid);
+            bar_arrive(BAR_FULL + st, kPrepThreads + 32 * NC);
+        }
+        cp_async_wait_all();
+        return;
+    }
+
+    if (NC == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    const int cw = warp - kPrepWarps, d0 = dv0 + cw * 16;
+    const int gr = lane >> 2, tc2 = (lane & 3) * 2;
+    const size_t sbase = ((size_t)n * a.HV + hv) * D * D;
+    float S[16][4];  // dS^T: rows dv d0 + gr, + 8; columns dk 8j + tc2, + 1
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        if (a.d_final_state) {
+            const float *p = a.d_final_state + sbase + (size_t)(8 * j + tc2) * D + d0 + gr;
+            S[j][0] = p[0];
+            S[j][1] = p[D];
+            S[j][2] = p[8];
+            S[j][3] = p[D + 8];
+        } else {
+            S[j][0] = S[j][1] = S[j][2] = S[j][3] = 0.f;
+        }
+    }
+    const int lrow = (lane & 7) + ((lane >> 4) & 1) * 8, lcol = (lane >> 3) & 1;
+    const int trow = lane & 15, tcol = lane >> 4;
+    // transposed reads of a [16][16] tile: B fragments of its rows as the summed dimension
+    const uint32_t ttile = (uint32_t)(((lane & 7) + ((lane >> 3) & 1) * 8) * 32 + (lane >> 4) * 16);
+
+    for (int i = 0; i < steps; ++i) {
+        const int st = i & 1, step = steps - 1 - i;
+        const size_t slot = (size_t)(sq.slot0 + step / 4) * a.HV + hv;
+        if (step % 4 == 3) store_checkpoint(a.dckpt + slot * kCkptBytes, S, d0, lane);
+        bar_sync(BAR_FULL + st, kPrepThreads + 32 * NC);
+        const Prepared &in = sm.prep[st];
+        const uint32_t pl = tc::smem_u32(in.planes);
+        uint32_t bh[4], bl[4], ah[4], al[4], oh[4], ol[4];
+        // do^T as left operand (dv rows, tokens summed)
+        ldsm4t(oh, tc::smem_u32(sm.dout[i % kRing]) +
+                       plane_off((lane & 7) + ((lane >> 4) & 1) * 8, cw * 2 + ((lane >> 3) & 1)));
+        if (!std::is_same<T16, __nv_bfloat16>::value) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 x = unpack2<T16>(oh[j]);
+                split2(x.x, x.y, oh[j], ol[j]);
+            }
+        }
+        // dn^T = dS'^T kd^T + do^T P
+        float dn[2][4] = {};
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+            split_frag(S[2 * kk], S[2 * kk + 1], ah, al);
+            const uint32_t off = plane_off(lrow, 2 * kk + lcol);
+            ldsm4(bh, pl + KD_HI * kPlane + off);
+            ldsm4(bl, pl + KD_LO * kPlane + off);
+            mma3(dn[0], dn[1], ah, al, bh, bl);
+        }
+        const uint32_t tl = tc::smem_u32(sm.tiles[i % kRing]) + ttile;
+        ldsm4t(bh, tl + 2 * kTile);
+        ldsm4t(bl, tl + 3 * kTile);
+        mma_in<T16>(dn[0], dn[1], oh, ol, bh, bl);
+        // Y^T = dn^T T
+        float y[2][4] = {};
+        split_frag(dn[0], dn[1], ah, al);
+        ldsm4t(bh, tl);
+        ldsm4t(bl, tl + kTile);
+        mma3(y[0], y[1], ah, al, bh, bl);
+        store_rows(a.y + slot * kRowsBytes, y, (step % 4) * C, d0, lane);
+        // dv = beta Y; -dv is the left operand of the state's update
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float2 b = *reinterpret_cast<const float2 *>(&sm.beta[i % kRing][8 * j + tc2]);
+            y[j][0] *= -b.x;
+            y[j][1] *= -b.y;
+            y[j][2] *= -b.x;
+            y[j][3] *= -b.y;
+            const uint32_t u = movm_t(pack2<T16>(-y[j][0], -y[j][1]));
+            const uint32_t w = movm_t(pack2<T16>(-y[j][2], -y[j][3]));
+            const int t = step * C + 8 * j + gr;
+            if (t < sq.len) {
+                const size_t idx = ((size_t)(sq.row0 + t) * a.HV + hv) * D + d0 + tc2;
+                if (dbg_ok(a.dbg, idx + 9, a.rows_o * D, DBG_STORE)) {
+                    *reinterpret_cast<uint32_t *>((uint16_t *)a.dv + idx) = u;
+                    *reinterpret_cast<uint32_t *>((uint16_t *)a.dv + idx + 8) = w;
+                }
+            }
+        }
+        split_frag(y[0], y[1], ah, al);
+        // dS = diag(2^g_l) dS' + qw^T do - kw^T dv
+#pragma unroll
+        for (int jj = 0; jj < 8; ++jj) {
+            const float2 u = *reinterpret_cast<const float2 *>(&in.decay[16 * jj + tc2]);
+            const float2 w = *reinterpret_cast<const float2 *>(&in.decay[16 * jj + 8 + tc2]);
+            S[2 * jj][0] *= u.x;
+            S[2 * jj][1] *= u.y;
+            S[2 * jj][2] *= u.x;
+            S[2 * jj][3] *= u.y;
+            S[2 * jj + 1][0] *= w.x;
+            S[2 * jj + 1][1] *= w.y;
+            S[2 * jj + 1][2] *= w.x;
+            S[2 * jj + 1][3] *= w.y;
+            const uint32_t off = plane_off(trow, 2 * jj + tcol);
+            ldsm4t(bh, pl + QW_HI * kPlane + off);
+            ldsm4t(bl, pl + QW_LO * kPlane + off);
+            mma_in<T16>(S[2 * jj], S[2 * jj + 1], oh, ol, bh, bl);
+            ldsm4t(bh, pl + KW_HI * kPlane + off);
+            ldsm4t(bl, pl + KW_LO * kPlane + off);
+            mma3(S[2 * jj], S[2 * jj + 1], ah, al, bh, bl);
+        }
+        if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kPrepThreads + 32 * NC);
+    }
+    if (a.d_initial_state) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            float *p = a.d_initial_state + sbase + (size_t)(8 * j + tc2) * D + d0 + gr;
+            p[0] = S[j][0];
+            p[D] = S[j][1];
+            p[8] = S[j][2];
+            p[D + 8] = S[j][3];
+        }
+    }
+}
+
+template <typename T16, int NC>
+cudaError_t launch(const ChunkBwdArgs &a, int dev, cudaStream_t stream) {
+    static volatile int done[kMaxDev];
+    cudaError_t e =
+        smem_limit_once(kda_chunk_bwd_state_kernel<T16, NC>, (int)sizeof(Smem), dev, done);
+    if (e != cudaSuccess) return e;
+    kda_chunk_bwd_state_kernel<T16, NC>
+        <<<a.num_seqs * a.HV * (8 / NC), kPrepThreads + 32 * NC, sizeof(Smem), stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T16>
+cudaError_t launch_nc(const ChunkBwdArgs &a, int dev, cudaStream_t stream) {
+    const long long heads = (long long)a.num_seqs * a.HV;
+    if (heads * 2 > kSMs) return launch<T16, 8>(a, dev, stream);
+    if (heads * 4 > kSMs) return launch<T16, 4>(a, dev, stream);
+    return launch<T16, 2>(a, dev, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_bwd_state(const ChunkBwdArgs &a, int dev, cudaStream_t stream) {
+    return a.fp16 ? launch_nc<__half>(a, dev, stream) : launch_nc<__nv_bfloat16>(a, dev, stream);
+}
+
+}  // namespace chunk
+}  // namespace kda

@@ -1,0 +1,104 @@
+// Shared parts of the layer-norm kernels: a row is held in registers, eight elements a
+// thread, by a group of TPR threads (16 to 1024, the smallest power of two that holds it).
+#pragma once
+
+#include "kda_common.cuh"
+#include "kda_ops.h"
+
+namespace kda {
+namespace norm {
+
+constexpr int E = 8;                 // elements of a row held by one thread
+constexpr int kMaxWidth = 1024 * E;  // widest row that one CTA holds in registers
+
+__device__ __forceinline__ float as_f32(float x) { return x; }
+__device__ __forceinline__ float as_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float as_f32(__half x) { return __half2float(x); }
+template <typename T> __device__ __forceinline__ T from_f32(float x);
+template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
+    return __float2bfloat16_rn(x);
+}
+template <> __device__ __forceinline__ __half from_f32<__half>(float x) {
+    return __float2half_rn(x);
+}
+
+// Eight elements of a row.  WIDE: 16-byte accesses to consecutive columns; otherwise single
+// elements TPR columns apart (rows that start at no 16-byte boundary).
+template <typename T, bool WIDE, int TPR> struct Part {
+    T v[E];
+    static constexpr int kVec = 16 / (int)sizeof(T);
+
+    static __device__ __forceinline__ int col(int t, int i) { return WIDE ? t * E + i : t + i * TPR; }
+
+    __device__ __forceinline__ void load(const T *row, int t, int width, bool ok) {
+        if (WIDE) {
+#pragma unroll
+            for (int i = 0; i < E; i += kVec) {
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (ok && col(t, i) < width)
+                    x = __ldcs(reinterpret_cast<const uint4 *>(row + col(t, i)));
+                *reinterpret_cast<uint4 *>(&v[i]) = x;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                v[i] = ok && col(t, i) < width ? row[col(t, i)] : from_f32<T>(0.f);
+        }
+    }
+    __device__ __forceinline__ void store(T *row, int t, int width, bool ok) const {
+        if (WIDE) {
+#pragma unroll
+            for (int i = 0; i < E; i += kVec)
+                if (ok && col(t, i) < width)
+                    *reinterpret_cast<uint4 *>(row + col(t, i)) =
+                        *reinterpret_cast<const uint4 *>(&v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (ok && col(t, i) < width) row[col(t, i)] = v[i];
+        }
+    }
+};
+
+// An element of weight or bias, whose type may be x's or FP32.
+__device__ __forceinline__ float param(const void *p, int dtype, int c, float none) {
+    if (!p) return none;
+    if (dtype == NORM_FP32) return ((const float *)p)[c];
+    if (dtype == NORM_BF16) return as_f32(((const __nv_bfloat16 *)p)[c]);
+    return as_f32(((const __half *)p)[c]);
+}
+
+template <int TPR> constexpr int threads() { return TPR < 256 ? 256 : TPR; }
+
+// Barrier of one row's group of threads (TPR > 32).
+template <int TPR> __device__ __forceinline__ void group_sync(int group) {
+    if (threads<TPR>() == TPR)
+        __syncthreads();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
+}
+
+template <int N> __device__ __forceinline__ float lanes_sum(float x) {
+#pragma unroll
+    for (int off = N / 2; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+}
+
+// Threads of a row for a width, 0 when one CTA's registers do not hold it.
+inline int group_of(int width) {
+    if (width > kMaxWidth) return 0;
+    int t = 16;
+    while (t * E < width) t *= 2;
+    return t;
+}
+
+inline int esize(int dtype) { return dtype == NORM_FP32 ? 4 : 2; }
+
+inline bool wide_ok(int dtype, int width, const void *p, long long stride, bool with = true) {
+    const int vec = 16 / esize(dtype);
+    return !with || (width % vec == 0 && (uintptr_t)p % 16 == 0 && stride % vec == 0);
+}
+
+}  // namespace norm
+}  // namespace kda

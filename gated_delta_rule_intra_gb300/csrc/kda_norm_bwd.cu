@@ -1,0 +1,239 @@
+// Layer norm, backward: with xhat = (x - mean) rstd and h = dy weight,
+//   dx = rstd (h - mean(h) - xhat mean(h xhat)),
+//   dweight = sum over rows of dy xhat,  dbias = sum over rows of dy.
+//
+// Bound by memory: x and dy are read once, dx is written once.  A resident CTA walks rows
+// grid-stride and keeps its columns' sums of dy xhat and dy in registers; at the end it writes
+// them to its own row of `partial`, and a second kernel adds the rows up in a fixed order, so
+// the result does not depend on which CTA finished first.
+#include "kda_norm.cuh"
+
+namespace kda {
+namespace norm {
+namespace {
+
+template <typename T, bool WIDE, int TPR>
+__global__ void __launch_bounds__(threads<TPR>()) kda_layer_norm_bwd_kernel(const NormArgs a) {
+    constexpr int kThreads = threads<TPR>(), kGroups = kThreads / TPR;
+    constexpr int kWarps = TPR > 32 ? TPR / 32 : 1;
+    using P = Part<T, WIDE, TPR>;
+    __shared__ float2 red[2][kGroups][kWarps];
+    __shared__ float sums[kGroups > 1 ? kGroups : 1][kGroups > 1 ? TPR * E : 1];
+    const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR, lane = threadIdx.x & 31;
+    const int w = t / 32;
+    float wt[E], dw[E] = {}, db[E] = {};
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const int c = P::col(t, i);
+        wt[i] = c < a.width ? param(a.weight, a.wdtype, c, 1.f) : 0.f;
+    }
+    const float inv_n = 1.f / (float)a.width;
+    const long long step = (long long)gridDim.x * kGroups;
+    long long row0 = (long long)blockIdx.x * kGroups;
+    P x, dy, nx, ndy;
+    float mean = 0.f, rstd = 0.f, nmean = 0.f, nrstd = 0.f;
+    auto fetch = [&](P &px, P &pdy, float &m, float &r, long long row) {
+        const bool ok = row < a.rows;
+        px.load((const T *)a.x + row * a.x_stride, t, a.width, ok);
+        pdy.load((const T *)a.dy + row * a.dy_stride, t, a.width, ok);
+        m = ok ? a.mean[row] : 0.f;
+        r = ok ? a.rstd[row] : 0.f;
+    };
+    fetch(x, dy, mean, rstd, row0 + grp);
+    for (int it = 0; row0 < a.rows; row0 += step, it ^= 1) {
+        const long long row = row0 + grp;
+        fetch(nx, ndy, nmean, nrstd, row + step);
+        float s1 = 0.f, s2 = 0.f, xh[E], h[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const float d = as_f32(dy.v[i]);
+            xh[i] = (as_f32(x.v[i]) - mean) * rstd;
+            h[i] = d * wt[i];
+            s1 += h[i];
+            s2 += h[i] * xh[i];
+            if (WIDE || P::col(t, i) < a.width) {
+                dw[i] += d * xh[i];
+                db[i] += d;
+            }
+        }
+        constexpr int kLanes = TPR < 32 ? TPR : 32;
+        s1 = lanes_sum<kLanes>(s1);
+        s2 = lanes_sum<kLanes>(s2);
+        if (TPR > 32) {
+            if (lane == 0) red[it][grp][w] = make_float2(s1, s2);
+            group_sync<TPR>(grp);
+            const float2 p = lane < kWarps ? red[it][grp][lane] : make_float2(0.f, 0.f);
+            s1 = lanes_sum<32>(p.x);
+            s2 = lanes_sum<32>(p.y);
+        }
+        s1 *= inv_n;
+        s2 *= inv_n;
+        P out;
+#pragma unroll
+        for (int i = 0; i < E; ++i) out.v[i] = from_f32<T>(rstd * (h[i] - s1 - xh[i] * s2));
+        out.store((T *)a.dx + row * a.dx_stride, t, a.width, row < a.rows);
+        x = nx;
+        dy = ndy;
+        mean = nmean;
+        rstd = nrstd;
+    }
+    if (!a.dweight) return;
+    float *to = a.partial + (size_t)blockIdx.x * 2 * a.width;
+    if constexpr (kGroups == 1) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int c = P::col(t, i);
+            if (c < a.width) {
+                to[c] = dw[i];
+                to[a.width + c] = db[i];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int pass = 0; pass < 2; ++pass) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < E; ++i) sums[grp][P::col(t, i)] = pass ? db[i] : dw[i];
+            __syncthreads();
+            for (int c = threadIdx.x; c < a.width; c += kThreads) {
+                float s = 0.f;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) s += sums[g][c];
+                to[pass * a.width + c] = s;
+            }
+        }
+    }
+}
+
+// Column sums of `partial` [n][cols]: 32 columns a CTA, 32 slices of rows side by side.
+__global__ void __launch_bounds__(1024)
+    kda_layer_norm_sum_kernel(const float *partial, int n, int width, float *dweight, float *dbias) {
+    __shared__ float red[32][33];
+    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    const long long cols = 2LL * width, c = (long long)blockIdx.x * 32 + lane;
+    float s = 0.f;
+    if (c < cols) {
+#pragma unroll 4
+        for (int i = slice; i < n; i += 32) s += partial[(size_t)i * cols + c];
+    }
+    red[slice][lane] = s;
+    __syncthreads();
+    s = lanes_sum<32>(red[lane][slice]);
+    const long long col = (long long)blockIdx.x * 32 + slice;
+    if (lane == 0 && col < cols) {
+        if (col < width)
+            dweight[col] = s;
+        else
+            dbias[col - width] = s;
+    }
+}
+
+// Rows that no CTA's registers hold: dx by one CTA a row ...
+template <typename T> __global__ void __launch_bounds__(1024) kda_layer_norm_bwd_long_kernel(const NormArgs a) {
+    __shared__ float2 red[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const T *x = (const T *)a.x + row * a.x_stride, *dy = (const T *)a.dy + row * a.dy_stride;
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        float s1 = 0.f, s2 = 0.f;
+        for (int c = tid; c < a.width; c += 1024) {
+            const float h = as_f32(dy[c]) * param(a.weight, a.wdtype, c, 1.f);
+            s1 += h;
+            s2 += h * (as_f32(x[c]) - mean) * rstd;
+        }
+        s1 = lanes_sum<32>(s1);
+        s2 = lanes_sum<32>(s2);
+        if (lane == 0) red[warp] = make_float2(s1, s2);
+        __syncthreads();
+        s1 = lanes_sum<32>(red[lane].x) / (float)a.width;
+        s2 = lanes_sum<32>(red[lane].y) / (float)a.width;
+        T *dx = (T *)a.dx + row * a.dx_stride;
+        for (int c = tid; c < a.width; c += 1024) {
+            const float xh = (as_f32(x[c]) - mean) * rstd;
+            dx[c] = from_f32<T>(
+                rstd * (as_f32(dy[c]) * param(a.weight, a.wdtype, c, 1.f) - s1 - xh * s2));
+        }
+        __syncthreads();
+    }
+}
+
+// ... and the column sums by a pass of their own: 256 columns a CTA, one slice of the rows.
+template <typename T> __global__ void __launch_bounds__(256) kda_layer_norm_bwd_cols_kernel(const NormArgs a) {
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= a.width) return;
+    float dw = 0.f, db = 0.f;
+    for (long long row = blockIdx.y; row < a.rows; row += gridDim.y) {
+        const float d = as_f32(((const T *)a.dy)[row * a.dy_stride + c]);
+        dw += d * (as_f32(((const T *)a.x)[row * a.x_stride + c]) - a.mean[row]) * a.rstd[row];
+        db += d;
+    }
+    float *to = a.partial + (size_t)blockIdx.y * 2 * a.width;
+    to[c] = dw;
+    to[a.width + c] = db;
+}
+
+int ctas(long long rows, int width) {
+    const int tpr = group_of(width);
+    if (!tpr) return (int)(rows < 64 ? rows : 64);  // slices of the column pass
+    const int threads = tpr < 256 ? 256 : tpr, groups = threads / tpr;
+    const long long want = (rows + groups - 1) / groups, most = (long long)kSMs * (1024 / threads);
+    return (int)(want < most ? want : most);
+}
+
+cudaError_t sum_partials(const NormArgs &a, int n, cudaStream_t stream) {
+    if (!a.dweight) return cudaSuccess;
+    kda_layer_norm_sum_kernel<<<(unsigned)((2LL * a.width + 31) / 32), 1024, 0, stream>>>(
+        a.partial, n, a.width, a.dweight, a.dbias);
+    return cudaGetLastError();
+}
+
+template <typename T, bool WIDE, int TPR>
+cudaError_t launch(const NormArgs &a, cudaStream_t stream) {
+    const int n = ctas(a.rows, a.width);
+    kda_layer_norm_bwd_kernel<T, WIDE, TPR><<<n, threads<TPR>(), 0, stream>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : sum_partials(a, n, stream);
+}
+
+template <typename T, bool WIDE> cudaError_t pick(const NormArgs &a, cudaStream_t stream) {
+    switch (group_of(a.width)) {
+        case 16: return launch<T, WIDE, 16>(a, stream);
+        case 32: return launch<T, WIDE, 32>(a, stream);
+        case 64: return launch<T, WIDE, 64>(a, stream);
+        case 128: return launch<T, WIDE, 128>(a, stream);
+        case 256: return launch<T, WIDE, 256>(a, stream);
+        case 512: return launch<T, WIDE, 512>(a, stream);
+        case 1024: return launch<T, WIDE, 1024>(a, stream);
+    }
+    const long long most = 2 * kSMs;
+    kda_layer_norm_bwd_long_kernel<T>
+        <<<(unsigned)(a.rows < most ? a.rows : most), 1024, 0, stream>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !a.dweight) return e;
+    const int n = ctas(a.rows, a.width);
+    kda_layer_norm_bwd_cols_kernel<T>
+        <<<dim3((unsigned)((a.width + 255) / 256), (unsigned)n), 256, 0, stream>>>(a);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : sum_partials(a, n, stream);
+}
+
+template <typename T> cudaError_t pick_wide(const NormArgs &a, cudaStream_t stream) {
+    const bool wide = wide_ok(a.dtype, a.width, a.x, a.x_stride) &&
+                      wide_ok(a.dtype, a.width, a.dy, a.dy_stride) &&
+                      wide_ok(a.dtype, a.width, a.dx, a.dx_stride);
+    return wide ? pick<T, true>(a, stream) : pick<T, false>(a, stream);
+}
+
+}  // namespace
+}  // namespace norm
+
+int norm_bwd_ctas(long long rows, int width) { return norm::ctas(rows, width); }
+
+cudaError_t launch_norm_bwd(const NormArgs &a, cudaStream_t stream) {
+    if (a.rows == 0) return norm::sum_partials(a, 0, stream);  // sums of nothing: zeros
+    if (a.dtype == NORM_BF16) return norm::pick_wide<__nv_bfloat16>(a, stream);
+    if (a.dtype == NORM_FP16) return norm::pick_wide<__half>(a, stream);
+    return norm::pick_wide<float>(a, stream);
+}
+
+}  // namespace kda

@@ -1,0 +1,85 @@
+// Internal launch interface of the recurrence, single-token and layer-norm operators.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+
+namespace kda {
+
+constexpr int kSMs = 152;
+
+struct ChunkFwdArgs {
+    const void *q, *k, *v;  // 16-bit, [rows, H, 128] and [rows, HV, 128]
+    const float *gate, *beta;
+    void *o;
+    const float *initial_state;  // [num_seqs, HV, 128 dk, 128 dv] or null
+    float *final_state;          // the same, or null
+    char *ckpt, *e, *tiles;      // the backward's buffers, all or none
+    int T, H, HV, num_seqs;      // T = tokens of a sequence, or of the packed row
+    const int *cu_seqlens;       // [num_seqs + 1] or null
+    float scale;
+    bool fp16;
+    size_t rows_o;               // rows of o (tokens * HV), for the debug build's checks
+    unsigned *dbg;
+};
+
+cudaError_t launch_chunk_fwd(const ChunkFwdArgs &a, cudaStream_t stream);
+
+struct ChunkBwdArgs {
+    const void *q, *k, *dout;  // 16-bit
+    const float *gate, *beta;
+    void *dq, *dk, *dv, *dgate, *dbeta;  // 16-bit; dq, dk [rows, H, 128]
+    const float *d_final_state;          // [num_seqs, HV, 128 dk, 128 dv] or null
+    float *d_initial_state;              // the same, or null
+    const char *ckpt, *e, *tiles;        // what the forward saved
+    char *dckpt, *y;                     // workspace: state gradients at slot ends, Y
+    float *dq_hv, *dk_hv;                // workspace [rows, HV, 128], only when HV > H
+    int B, T, H, HV, num_seqs, slots;
+    const int *cu_seqlens;
+    float scale;
+    bool fp16;
+    size_t rows_o;
+    unsigned *dbg;
+};
+
+cudaError_t launch_chunk_bwd(const ChunkBwdArgs &a, cudaStream_t stream);
+
+struct StepArgs {
+    const void *q, *k, *v;  // 16-bit, [N, H, 128] and [N, HV, 128]
+    const float *gate, *beta;
+    float *state;           // [num_states, HV, 128 dk, 128 dv]
+    void *o;
+    int N, H, HV;
+    const int *state_indices;  // [N] or null (request n has state n)
+    long long num_states;
+    float scale;
+    bool fp16;
+    unsigned *dbg;
+};
+
+cudaError_t launch_step(const StepArgs &a, cudaStream_t stream);
+
+// Element types of the layer norm's tensors.
+enum { NORM_BF16 = 0, NORM_FP16 = 1, NORM_FP32 = 2 };
+
+struct NormArgs {
+    const void *x, *weight, *bias;  // weight, bias: null = ones, zeros
+    void *y;
+    float *mean, *rstd;             // [rows]; forward: null = not wanted
+    // backward
+    const void *dy;
+    void *dx;
+    float *dweight, *dbias;         // [width], both or none
+    float *partial;                 // [norm_bwd_ctas(rows, width)][2][width]
+    long long rows;
+    int width, dtype, wdtype;
+    long long x_stride, y_stride, dy_stride, dx_stride;  // elements between rows
+    float eps;
+    unsigned *dbg;
+};
+
+cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t stream);
+cudaError_t launch_norm_bwd(const NormArgs &a, cudaStream_t stream);
+int norm_bwd_ctas(long long rows, int width);  // rows of `partial`
+
+}  // namespace kda

@@ -1,0 +1,206 @@
+"""The gated delta-rule recurrence over whole sequences (``kda_chunk_fwd``,
+``kda_chunk_bwd``) and its single-token form (``kda_step``).
+
+Per value head the state S is [128 dk, 128 dv] in fp32; a token decays it per channel and
+corrects it towards its value::
+
+    S~ = diag(2^gate) S,  e = v - S~^T k,  S' = S~ + beta k e^T,  o = scale S'^T q
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from ._common import DTYPES16, F32, K, check, ptr, run, takes_stream
+
+
+class ChunkFwdOpts(ctypes.Structure):
+    """Mirror of kda_chunk_fwd_opts_t."""
+    _fields_ = [("HV", ctypes.c_int), ("scale", ctypes.c_float),
+                ("initial_state", ctypes.c_void_p), ("final_state", ctypes.c_void_p),
+                ("saved", ctypes.c_void_p), ("saved_bytes", ctypes.c_size_t),
+                ("cu_seqlens", ctypes.c_void_p), ("num_seqs", ctypes.c_int)]
+
+
+class ChunkBwdOpts(ctypes.Structure):
+    """Mirror of kda_chunk_bwd_opts_t."""
+    _fields_ = [("HV", ctypes.c_int), ("scale", ctypes.c_float),
+                ("d_final_state", ctypes.c_void_p), ("d_initial_state", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("num_seqs", ctypes.c_int),
+                ("saved", ctypes.c_void_p), ("saved_bytes", ctypes.c_size_t),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class StepOpts(ctypes.Structure):
+    """Mirror of kda_step_opts_t."""
+    _fields_ = [("HV", ctypes.c_int), ("scale", ctypes.c_float),
+                ("state_indices", ctypes.c_void_p), ("num_states", ctypes.c_int)]
+
+
+def _lib():
+    from . import load_library
+    return load_library()
+
+
+def _inputs(fn, q, k, v, gate, beta, lead):
+    """Checks of the five inputs; (H, HV)."""
+    if q.device.type != "cuda":
+        raise ValueError(f"{fn} needs CUDA tensors (no CPU path exists)")
+    if q.dtype not in DTYPES16:
+        raise ValueError(f"q/k/v dtype must be bf16 or fp16, got {q.dtype}")
+    if q.dim() != lead + 2 or q.shape[-1] != K:
+        raise ValueError(f"q must be [{'N' if lead == 1 else 'B, T'}, H, {K}], got "
+                         f"{tuple(q.shape)}")
+    if v.dim() != lead + 2:
+        raise ValueError(f"v must be [{'N' if lead == 1 else 'B, T'}, HV, {K}], got "
+                         f"{tuple(v.shape)}")
+    H, HV, dev = q.shape[lead], v.shape[lead], q.device
+    if H == 0 or HV % H:
+        raise ValueError(f"v's {HV} heads must be a multiple of q's {H}")
+    rows = q.shape[:lead]
+    check("k", k, q.shape, q.dtype, dev)
+    check("v", v, (*rows, HV, K), q.dtype, dev)
+    check("gate", gate, v.shape, F32, dev)
+    check("beta", beta, (*rows, HV), F32, dev)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    return H, HV
+
+
+def _scale(scale):
+    if scale is None:
+        return 0.0  # the library's default
+    if scale == 0:
+        raise ValueError("scale must not be 0")
+    return float(scale)
+
+
+def _seqs(cu_seqlens, B, dev):
+    if cu_seqlens is None:
+        return 0
+    if B != 1:
+        raise ValueError("cu_seqlens packs sequences along T: B must be 1")
+    if cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must have at least two entries")
+    check("cu_seqlens", cu_seqlens, (cu_seqlens.numel(),), torch.int32, dev)
+    return cu_seqlens.numel() - 1
+
+
+@takes_stream
+def kda_chunk_fwd(q, k, v, gate, beta, scale=None, initial_state=None, *,
+                  output_final_state=False, save=False, cu_seqlens=None, o=None):
+    """The recurrence over whole sequences.  Returns (o, final_state, saved).
+
+    q, k [B, T, H, 128] and v [B, T, HV, 128] bf16/fp16 (value head hv reads q/k head
+    hv // (HV // H)); gate [B, T, HV, 128] fp32 per-step log2 decays, <= 0 (not cumulative);
+    beta [B, T, HV] fp32; any T.  ``scale`` defaults to 128 ** -0.5.  ``initial_state``
+    [sequences, HV, 128 dk, 128 dv] fp32 defaults to zeros.  o is in q's dtype, with zeros at
+    tokens in no sequence when it is allocated here.  final_state (fp32) is None unless
+    ``output_final_state``.  saved is what ``kda_chunk_bwd`` needs (about 1.7 KB a token and
+    value head), None unless ``save``.  ``cu_seqlens`` (int32 [N + 1] on the device, B = 1)
+    packs N sequences along T; it is read on the device only.
+    """
+    H, HV = _inputs("kda_chunk_fwd", q, k, v, gate, beta, 2)
+    B, T, dev = q.shape[0], q.shape[1], q.device
+    N = _seqs(cu_seqlens, B, dev)
+    if o is None:
+        o = torch.zeros_like(v) if N else torch.empty_like(v)
+    else:
+        check("o", o, v.shape, v.dtype, dev)
+    states = (N or B, HV, K, K)
+    lib = _lib()
+    op = ChunkFwdOpts(HV=HV, scale=_scale(scale), num_seqs=N, cu_seqlens=ptr(cu_seqlens))
+    if initial_state is not None:
+        check("initial_state", initial_state, states, F32, dev)
+        op.initial_state = initial_state.data_ptr()
+    final = saved = None
+    if output_final_state:
+        final = torch.empty(states, dtype=F32, device=dev)
+        op.final_state = final.data_ptr()
+    if save:
+        saved = torch.empty(lib.kda_chunk_saved_bytes(B, T, HV, N), dtype=torch.uint8, device=dev)
+        op.saved, op.saved_bytes = saved.data_ptr(), saved.numel()
+    if B == 0:
+        return o, final, saved
+    run("kda_chunk_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(),
+        beta.data_ptr(), o.data_ptr(), B, T, H, DTYPES16[q.dtype], ctypes.addressof(op))
+    return o, final, saved
+
+
+@takes_stream
+def kda_chunk_bwd(q, k, v, gate, beta, do, saved, scale=None, d_final_state=None, *,
+                  output_d_initial_state=False, cu_seqlens=None, dq=None, dk=None, dv=None,
+                  dgate=None, dbeta=None):
+    """Gradients of ``kda_chunk_fwd``.  Returns (dq, dk, dv, dgate, dbeta, d_initial_state).
+
+    The five inputs, ``scale`` and ``cu_seqlens`` as given to the forward, do like its o,
+    ``saved`` what it returned with ``save=True`` (read only).  The gradients are in q's dtype;
+    dq and dk are summed over the value heads of their head.  ``d_final_state`` (fp32, the
+    final state's shape) defaults to zeros; d_initial_state (fp32) is None unless
+    ``output_d_initial_state``.  Deterministic.
+    """
+    H, HV = _inputs("kda_chunk_bwd", q, k, v, gate, beta, 2)
+    B, T, dev, dt = q.shape[0], q.shape[1], q.device, q.dtype
+    N = _seqs(cu_seqlens, B, dev)
+    check("do", do, v.shape, dt, dev)
+    lib = _lib()
+    saved_bytes = lib.kda_chunk_saved_bytes(B, T, HV, N)
+    check("saved", saved, (saved_bytes,), torch.uint8, dev)
+    new = torch.zeros_like if N else torch.empty_like
+    out = []
+    for name, t, like, shape in (("dq", dq, q, q.shape), ("dk", dk, k, q.shape),
+                                 ("dv", dv, v, v.shape), ("dgate", dgate, v, v.shape),
+                                 ("dbeta", dbeta, None, beta.shape)):
+        if t is not None:
+            check(name, t, shape, dt, dev)
+        elif like is not None:
+            t = new(like)
+        else:
+            t = new(beta, dtype=dt)
+        out.append(t)
+    states = (N or B, HV, K, K)
+    op = ChunkBwdOpts(HV=HV, scale=_scale(scale), num_seqs=N, cu_seqlens=ptr(cu_seqlens),
+                      saved=saved.data_ptr(), saved_bytes=saved_bytes)
+    if d_final_state is not None:
+        check("d_final_state", d_final_state, states, F32, dev)
+        op.d_final_state = d_final_state.data_ptr()
+    d_initial = None
+    if output_d_initial_state:
+        d_initial = torch.empty(states, dtype=F32, device=dev)
+        op.d_initial_state = d_initial.data_ptr()
+    if B == 0:
+        return (*out, d_initial)
+    work = lib.kda_chunk_bwd_workspace_bytes(B, T, H, HV, N)
+    ws = torch.empty(work, dtype=torch.uint8, device=dev)
+    op.workspace, op.workspace_bytes = ws.data_ptr(), work
+    run("kda_chunk_bwd", dev, q.data_ptr(), k.data_ptr(), gate.data_ptr(), beta.data_ptr(),
+        do.data_ptr(), *(t.data_ptr() for t in out), B, T, H, DTYPES16[dt], ctypes.addressof(op))
+    return (*out, d_initial)
+
+
+@takes_stream
+def kda_step(q, k, v, gate, beta, state, scale=None, *, state_indices=None, o=None):
+    """One token for each of N requests, the states updated in place.  Returns o [N, HV, 128].
+
+    q, k [N, H, 128], v [N, HV, 128] bf16/fp16, gate [N, HV, 128] and beta [N, HV] fp32 as in
+    ``kda_chunk_fwd``; state [N, HV, 128 dk, 128 dv] fp32 -- or, with ``state_indices`` (int32
+    [N] on the device), [num_states, ...], request n's being state[state_indices[n]].  An index
+    outside the states marks a padding row (its o is zero); no two rows may name one state.
+    """
+    H, HV = _inputs("kda_step", q, k, v, gate, beta, 1)
+    N, dev = q.shape[0], q.device
+    check("state", state, (N if state_indices is None else state.shape[0], HV, K, K), F32, dev)
+    op = StepOpts(HV=HV, scale=_scale(scale), num_states=state.shape[0])
+    if state_indices is not None:
+        check("state_indices", state_indices, (N,), torch.int32, dev)
+        op.state_indices = state_indices.data_ptr()
+    if o is None:
+        o = torch.empty_like(v)
+    else:
+        check("o", o, v.shape, v.dtype, dev)
+    run("kda_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(),
+        beta.data_ptr(), state.data_ptr(), o.data_ptr(), N, H, DTYPES16[q.dtype],
+        ctypes.addressof(op))
+    return o

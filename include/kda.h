@@ -69,6 +69,8 @@ extern "C" {
 
 /*
  * ABI versions (kda_abi_version() returns the loaded library's):
+ *   10 kda_chunk_fwd, kda_chunk_bwd, kda_step, kda_layer_norm_fwd, kda_layer_norm_bwd
+ *      and their option structs and size queries
  *   9  kda_intra_bwd_opts_t gains split_tf32 (appended; the struct grew)
  *   8  kda_intra_bwd_host_static, KDA_HOST_STATIC_MAX_BYTES, KDA_ERR_TOO_LARGE
  *   7  kda_debug_checks, kda_debug_set_flags (the bounds-checked debug build)
@@ -84,7 +86,7 @@ extern "C" {
  * must check at start-up that kda_abi_version() equals the KDA_ABI_VERSION it was
  * compiled with (the Python binding refuses to load any other version).
  */
-#define KDA_ABI_VERSION 9
+#define KDA_ABI_VERSION 10
 #define KDA_BT 64  /* chunk length */
 #define KDA_BC 16  /* sub-block length inside a chunk */
 #define KDA_K 128  /* head dimension */
@@ -325,6 +327,138 @@ kda_status_t kda_intra_fwd_ex(const void *q, const void *k, const float *g,
                               const float *beta, float *Aqk, float *Akk,
                               int B, int T, int H, kda_dtype_t qk_dtype,
                               const kda_intra_fwd_opts_t *opts, kda_stream_t stream);
+
+/*
+ * The gated delta-rule recurrence over whole sequences.  Per value head the state S is
+ * [128 dk, 128 dv]; a token first decays it per channel, then corrects it towards its value:
+ *
+ *   S~_t = diag(2^gate_t) S_{t-1},   e_t = v_t - S~_t^T k_t,
+ *   S_t  = S~_t + beta_t k_t e_t^T,  o_t = scale S_t^T q_t
+ *
+ * (the intra-chunk step above is what this recurrence is made of inside a chunk).  All
+ * pointers are device memory, contiguous row-major, 16-byte aligned (beta: 4):
+ *   q, k        [B, T, H, 128]   bf16 or fp16 (dtype)
+ *   v, o        [B, T, HV, 128]  dtype; o fully overwritten
+ *   gate        [B, T, HV, 128]  fp32 per-step log2 decay, <= 0 (NOT cumulative; the
+ *                                kda_intra_* calls take its chunk-local cumsum).  Values below
+ *                                -160, the type's lowest and -infinity among them, clear the
+ *                                channel.
+ *   beta        [B, T, HV]       fp32
+ * HV is a multiple of H; value head hv reads q/k head hv / (HV / H).  Any T >= 0.
+ *
+ * Accuracy: o within a rounding to dtype plus 1e-5, the final state within 1e-5 (2-norm of
+ * the error over 2-norm of the result): states, sums and the solve are FP32 and every product
+ * of FP32 values is taken in three BF16 tensor-core products.
+ *
+ * Options (zero-initialise; NULL = none):
+ *   HV             0 means HV = H
+ *   scale          0 means 128^-0.5
+ *   initial_state  [sequences, HV, 128 dk, 128 dv] fp32, NULL = zeros
+ *   final_state    the same shape, written (a sequence of no tokens: a copy of its initial
+ *                  state); must not overlap initial_state
+ *   saved          what kda_chunk_bwd needs, kda_chunk_saved_bytes() bytes, 256-byte aligned;
+ *   saved_bytes    NULL when no backward follows.  About 1.7 KB a token and value head.
+ *   cu_seqlens     variable-length sequences packed along T (B == 1): device int32
+ *   num_seqs       [num_seqs + 1], sequence n is tokens [cu_seqlens[n], cu_seqlens[n+1]).
+ *                  Values are read on the device only and clamped to [0, T]; tokens in no
+ *                  sequence are left untouched.
+ */
+typedef struct {
+    int HV;
+    float scale;
+    const float *initial_state;
+    float *final_state;
+    void *saved;
+    size_t saved_bytes;
+    const int *cu_seqlens;
+    int num_seqs;
+} kda_chunk_fwd_opts_t;
+
+/* Bytes of `saved` (num_seqs: 0 for fixed-length calls); 0 for sizes that no call accepts. */
+size_t kda_chunk_saved_bytes(int B, int T, int HV, int num_seqs);
+
+kda_status_t kda_chunk_fwd(const void *q, const void *k, const void *v, const float *gate,
+                           const float *beta, void *o, int B, int T, int H, kda_dtype_t dtype,
+                           const kda_chunk_fwd_opts_t *opts, kda_stream_t stream);
+
+/*
+ * Gradients of kda_chunk_fwd from dout [B, T, HV, 128] (dtype) and what it saved: dq, dk
+ * [B, T, H, 128] (summed over the value heads of a q/k head), dv, dgate [B, T, HV, 128] and
+ * dbeta [B, T, HV], all in dtype, rounded once from FP32 sums.  q, k, gate, beta, scale, HV
+ * and cu_seqlens as given to the forward.  No atomics: the same inputs give the same bits.
+ *   d_final_state    gradient of the final state, [sequences, HV, 128, 128] fp32, NULL = zeros
+ *   d_initial_state  gradient of the initial state, the same shape, written; NULL = not wanted
+ *   saved            the forward's, read only (a backward may run again from it)
+ *   workspace        kda_chunk_bwd_workspace_bytes() bytes, 256-byte aligned
+ * Accuracy: within a rounding to dtype plus 1e-4; the initial state's gradient within 1e-5.
+ */
+typedef struct {
+    int HV;
+    float scale;
+    const float *d_final_state;
+    float *d_initial_state;
+    const int *cu_seqlens;
+    int num_seqs;
+    const void *saved;
+    size_t saved_bytes;
+    void *workspace;
+    size_t workspace_bytes;
+} kda_chunk_bwd_opts_t;
+
+size_t kda_chunk_bwd_workspace_bytes(int B, int T, int H, int HV, int num_seqs);
+
+kda_status_t kda_chunk_bwd(const void *q, const void *k, const float *gate, const float *beta,
+                           const void *dout, void *dq, void *dk, void *dv, void *dgate,
+                           void *dbeta, int B, int T, int H, kda_dtype_t dtype,
+                           const kda_chunk_bwd_opts_t *opts, kda_stream_t stream);
+
+/*
+ * One token of the recurrence for each of N requests (serving): o [N, HV, 128] from q, k
+ * [N, H, 128], v [N, HV, 128], gate [N, HV, 128], beta [N, HV]; each request's state in
+ * `state` [num_states, HV, 128 dk, 128 dv] fp32 is updated in place.  state_indices (device
+ * int32 [N], NULL = request n has state n) names the states; no two requests may name the
+ * same one, and an index outside [0, num_states) marks a row without a request (a padded
+ * batch): its o is zero and no state is touched.  scale 0 means 128^-0.5.  FP32 throughout.
+ */
+typedef struct {
+    int HV;
+    float scale;
+    const int *state_indices;
+    int num_states; /* 0 means N */
+} kda_step_opts_t;
+
+kda_status_t kda_step(const void *q, const void *k, const void *v, const float *gate,
+                      const float *beta, float *state, void *o, int N, int H, kda_dtype_t dtype,
+                      const kda_step_opts_t *opts, kda_stream_t stream);
+
+/*
+ * Layer norm over the last dimension of x [rows, width] (any width >= 1):
+ *   y = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ * x, y, dy and dx have one type (KDA_BF16, KDA_FP16 or KDA_FP32) and a row stride each, in
+ * elements (0 = width); weight and bias have `wdtype`, which is the same type or KDA_FP32, and
+ * may be NULL (ones, zeros).  mean and rstd [rows] fp32 are what the backward needs (NULL =
+ * not wanted).  Statistics, sums and gradients of weight and bias are FP32.  Pointers need
+ * their element's alignment; rows on 16-byte boundaries are read and written 16 bytes at a
+ * time, others element by element.
+ *
+ * Backward: dx, and dweight, dbias [width] fp32 (both or neither), summed over the rows in a
+ * fixed order.  `workspace` holds kda_layer_norm_bwd_workspace_bytes() bytes of partial sums
+ * (16-byte aligned; not needed without dweight).
+ */
+#define KDA_FP32 2 /* layer norm only */
+
+kda_status_t kda_layer_norm_fwd(const void *x, const void *weight, const void *bias, void *y,
+                                float *mean, float *rstd, long long rows, int width, float eps,
+                                int dtype, int wdtype, long long x_stride, long long y_stride,
+                                kda_stream_t stream);
+
+size_t kda_layer_norm_bwd_workspace_bytes(long long rows, int width);
+
+kda_status_t kda_layer_norm_bwd(const void *dy, const void *x, const void *weight,
+                                const float *mean, const float *rstd, void *dx, float *dweight,
+                                float *dbias, long long rows, int width, int dtype, int wdtype,
+                                long long dy_stride, long long x_stride, long long dx_stride,
+                                void *workspace, size_t workspace_bytes, kda_stream_t stream);
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *kda_status_str(kda_status_t status);
