@@ -44,9 +44,38 @@ constexpr size_t kRowsBytes = 2 * kRowPlane;  // e or Y of 64 tokens: hi and lo 
 constexpr size_t kTilesBytes = 4 * kTile;     // T hi, T lo, P hi, P lo of a step
 
 // Gates below this are taken as this: 2^-160 is 0 in FP32 either way, and differences of the
-// cumulative gate stay finite for gates of the type's lowest value or -infinity.  The
-// comparison keeps NaN.
-__device__ __forceinline__ float floor_gate(float x) { return x < -160.f ? -160.f : x; }
+// cumulative gate stay finite for gates of the type's lowest value or -infinity.  NaN stays.
+__device__ __forceinline__ float floor_gate(float x) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(-160.f));
+    return y;
+}
+
+// Two FP32 operations in one instruction (the pair in a 64-bit register).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\n"
+        "mul.rn.f32x2 z, x, y;\nmov.b64 {%0, %1}, z;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\n"
+        "add.rn.f32x2 z, x, y;\nmov.b64 {%0, %1}, z;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\n"
+        "mov.b64 z, {%6, %7};\nfma.rn.f32x2 z, x, y, z;\nmov.b64 {%0, %1}, z;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
@@ -56,7 +85,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // (x, y) as two BF16 pairs: hi = bf16(.), lo = bf16(. - hi)
 __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
     hi = pack_bf16(x, y);
-    lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+    const float2 d = fma2(make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)),
+                          make_float2(-1.f, -1.f), make_float2(x, y));
+    lo = pack_bf16(d.x, d.y);
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -90,6 +121,16 @@ __device__ __forceinline__ void bar_sync(int id, int n) {
 }
 __device__ __forceinline__ void bar_arrive(int id, int n) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+// bar_sync() that also tells whether any of its threads passed true.
+__device__ __forceinline__ bool bar_or(int id, int n, bool x) {
+    int r;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 p, %3, 0;\nbarrier.cta.red.or.pred q, %1, %2, p;\n"
+                 "selp.b32 %0, 1, 0, q;\n}"
+                 : "=r"(r)
+                 : "r"(id), "r"(n), "r"((int)x)
+                 : "memory");
+    return r != 0;
 }
 // cp.async of 16 (or 4) bytes, zeros when !ok.
 __device__ __forceinline__ void cp16z(uint32_t dst, const void *src, bool ok) {
@@ -165,43 +206,55 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float x, float y) 
 // The six operand planes of a step.
 enum { KW_HI = 0, KW_LO, QW_HI, QW_LO, KD_HI, KD_LO, kPlanes };
 
-// Operand planes from the raw inputs: 256 threads, each two channels of four rows.  Writes
-// the cumulative gate (gbuf, when asked for), the planes and 2^g_l.
-template <typename T16, bool WRITE_G>
-__device__ __forceinline__ void prep_planes(const RawStage &raw, char *planes, float *decay,
-                                            float (*gbuf)[D], float scale, int tid) {
-    const int c2 = tid & 63, r0 = (tid >> 6) * 4;
-    float2 g[4], acc = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int r = 0; r < C; ++r) {
+__device__ __forceinline__ void put_split(char *hi_plane, uint32_t off, float x, float y) {
+    uint32_t hi, lo;
+    split2(x, y, hi, lo);
+    *reinterpret_cast<uint32_t *>(hi_plane + off) = hi;
+    *reinterpret_cast<uint32_t *>(hi_plane + kPlane + off) = lo;
+}
+
+// Operand planes of a step from its raw inputs: NT threads, each two channels of C * 64 / NT
+// rows.  Writes kw, qw, 2^g_l and the key plane: k 2^(g_l - g), or with FROM_START k 2^-g,
+// which may grow without bound.  Returns whether one of these grew past 2^96.
+template <typename T16, int NT, bool FROM_START>
+__device__ __forceinline__ bool prep_planes(const RawStage &raw, char *planes, float *decay,
+                                            float scale, int tid) {
+    constexpr int kRows = C * 64 / NT;
+    const int c2 = tid & 63, r0 = (tid >> 6) * kRows;
+    auto gate = [&](int r) {
         const float2 x = *reinterpret_cast<const float2 *>(&raw.gate[r][2 * c2]);
-        acc.x += floor_gate(x.x);
-        acc.y += floor_gate(x.y);
+        return make_float2(floor_gate(x.x), floor_gate(x.y));
+    };
+    float2 g = make_float2(0.f, 0.f), ref = g;
+    if (FROM_START) {
+#pragma unroll 8
+        for (int r = 0; r < r0; ++r) g = add2(g, gate(r));
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (r == r0 + i) g[i] = acc;
+        for (int r = 0; r < C; ++r) {
+            if (r == r0) g = ref;
+            ref = add2(ref, gate(r));
+        }
     }
-    if (r0 == 0) *reinterpret_cast<float2 *>(&decay[2 * c2]) = make_float2(ex2(acc.x), ex2(acc.y));
+    float big = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kRows; ++i) {
         const int r = r0 + i;
-        if (WRITE_G) *reinterpret_cast<float2 *>(&gbuf[r][2 * c2]) = g[i];
+        g = add2(g, gate(r));
         const float2 q = unpack2<T16>(*reinterpret_cast<const uint32_t *>(&raw.q[r][2 * c2]));
         const float2 k = unpack2<T16>(*reinterpret_cast<const uint32_t *>(&raw.k[r][2 * c2]));
-        const float2 up = make_float2(ex2(g[i].x), ex2(g[i].y));
-        const float2 dn = make_float2(ex2(acc.x - g[i].x), ex2(acc.y - g[i].y));
+        const float2 up = make_float2(ex2(g.x), ex2(g.y));
+        const float2 dn = make_float2(ex2(ref.x - g.x), ex2(ref.y - g.y));
         const uint32_t off = plane_off(r, c2 >> 2) + (c2 & 3) * 4;
-        uint32_t hi, lo;
-        split2(k.x * up.x, k.y * up.y, hi, lo);
-        *reinterpret_cast<uint32_t *>(planes + KW_HI * kPlane + off) = hi;
-        *reinterpret_cast<uint32_t *>(planes + KW_LO * kPlane + off) = lo;
-        split2(scale * q.x * up.x, scale * q.y * up.y, hi, lo);
-        *reinterpret_cast<uint32_t *>(planes + QW_HI * kPlane + off) = hi;
-        *reinterpret_cast<uint32_t *>(planes + QW_LO * kPlane + off) = lo;
-        split2(k.x * dn.x, k.y * dn.y, hi, lo);
-        *reinterpret_cast<uint32_t *>(planes + KD_HI * kPlane + off) = hi;
-        *reinterpret_cast<uint32_t *>(planes + KD_LO * kPlane + off) = lo;
+        const float2 kw = mul2(k, up), kd = mul2(k, dn);
+        const float2 qw = mul2(mul2(q, make_float2(scale, scale)), up);
+        put_split(planes + KW_HI * kPlane, off, kw.x, kw.y);
+        put_split(planes + QW_HI * kPlane, off, qw.x, qw.y);
+        put_split(planes + KD_HI * kPlane, off, kd.x, kd.y);
+        if (r == C - 1) *reinterpret_cast<float2 *>(&decay[2 * c2]) = up;
+        if (FROM_START) big = fmaxf(big, fmaxf(fabsf(kd.x), fabsf(kd.y)));
     }
+    return big > 0x1p96f;
 }
 
 // Sums of 32 values over the 32 lanes; lane i returns the sum of v[i].

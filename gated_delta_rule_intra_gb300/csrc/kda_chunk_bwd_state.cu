@@ -96,8 +96,8 @@ __global__ void __launch_bounds__(kPrepThreads + 32 * NC, 1)
             if (i + kRaw - 1 < steps)
                 load_step<NC>(sm, a, sq, h, hv, dv0, i + kRaw - 1, steps - kRaw - i, tid);
             cp_async_commit();
-            prep_planes<T16, false>(sm.raw[i % kRaw], sm.prep[st].planes, sm.prep[st].decay,
-                                    nullptr, a.scale, tid);
+            prep_planes<T16, kPrepThreads, false>(sm.raw[i % kRaw], sm.prep[st].planes,
+                                                  sm.prep[st].decay, a.scale, tid);
             bar_arrive(BAR_FULL + st, kPrepThreads + 32 * NC);
         }
         cp_async_wait_all();

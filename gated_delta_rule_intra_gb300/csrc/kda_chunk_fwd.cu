@@ -7,55 +7,116 @@ namespace kda {
 namespace chunk {
 namespace {
 
-constexpr int kRaw = 3;    // raw input stages
-constexpr int kV = 4;      // value stages (read by the consumers, so they live longer)
-constexpr int kStages = 2; // prepared stages
+constexpr int kStages = 3;         // prepared stages
+constexpr int kRaw = kStages + 2;  // raw input stages: two ahead, and as far back as a stage lives
+constexpr int kHalf = 128;         // threads of each half of the preparing warps
 
-enum { BAR_PREP = 1, BAR_FULL = 2, BAR_EMPTY = 4 };  // FULL, EMPTY + stage
+// Named barriers; PLANES, FULL, EMPTY + stage.
+enum { BAR_PREP = 1, BAR_SCORE = 2, BAR_PLANES = 3, BAR_FULL = 6, BAR_EMPTY = 9 };
 
 struct __align__(128) Prepared {
     char planes[kPlanes * kPlane];
     char t2[2 * kTile];  // hi, lo
     char p[2 * kTile];
     float decay[D];
+    int from_start;      // the key plane is k 2^-g (decay after adding), not k 2^(g_l - g)
 };
 
 struct __align__(128) Smem {
     Prepared prep[kStages];
     RawStage raw[kRaw];
-    uint16_t v[kV][C][D];   // rows of the CTA's dv slice, swizzled chunks
-    float beta[kV][C];
-    float g[C][D];
-    float a2[2][C][C + 4];  // M diag(beta), two steps' worth
-    float a1[2][C][C + 4];  // diag(beta) M
-    char t[2 * kTile];      // T hi, lo on the way to the saved tiles
+    uint16_t v[kRaw][C][D];  // rows of the CTA's dv slice, swizzled chunks
+    float beta[kRaw][C];
+    float a2[2][C][C + 4];   // M diag(beta), two steps' worth
+    float a1[2][C][C + 4];   // diag(beta) M
+    char t[2 * kTile];       // T hi, lo on the way to the saved tiles
 };
 
 template <typename T16, int NC>
 __device__ __forceinline__ void load_step(Smem &sm, const ChunkFwdArgs &a, const Seq &sq, int h,
                                           int hv, int dv0, int step, int tid) {
-    const int row = tid >> 4, c = tid & 15;
-    const int t = step * C + row;
-    const bool ok = t < sq.len;
-    const size_t tok = (size_t)sq.row0 + (ok ? t : 0);
     RawStage &raw = sm.raw[step % kRaw];
-    const size_t iq = (tok * a.H + h) * D + c * 8, iv = (tok * a.HV + hv) * D;
-    cp16z(tc::smem_u32(&raw.q[row][c * 8]), (const uint16_t *)a.q + iq, ok);
-    cp16z(tc::smem_u32(&raw.k[row][c * 8]), (const uint16_t *)a.k + iq, ok);
-    cp16z(tc::smem_u32(&raw.gate[row][c * 4]), a.gate + iv + c * 4, ok);
-    cp16z(tc::smem_u32(&raw.gate[row][64 + c * 4]), a.gate + iv + 64 + c * 4, ok);
-    if (c < 2 * NC)
-        cp16z(tc::smem_u32(sm.v[step % kV]) + plane_off(row, c),
-              (const uint16_t *)a.v + iv + dv0 + c * 8, ok);
-    if (c == 0)
-        cp4z(tc::smem_u32(&sm.beta[step % kV][row]), a.beta + tok * a.HV + hv, ok);
+    const int c = tid & 15;
+#pragma unroll
+    for (int i = 0; i < C * 16 / kHalf; ++i) {
+        const int row = (tid >> 4) + i * (kHalf / 16), t = step * C + row;
+        const bool ok = t < sq.len;
+        const size_t tok = (size_t)sq.row0 + (ok ? t : 0);
+        const size_t iq = (tok * a.H + h) * D + c * 8, iv = (tok * a.HV + hv) * D;
+        cp16z(tc::smem_u32(&raw.q[row][c * 8]), (const uint16_t *)a.q + iq, ok);
+        cp16z(tc::smem_u32(&raw.k[row][c * 8]), (const uint16_t *)a.k + iq, ok);
+        cp16z(tc::smem_u32(&raw.gate[row][c * 4]), a.gate + iv + c * 4, ok);
+        cp16z(tc::smem_u32(&raw.gate[row][64 + c * 4]), a.gate + iv + 64 + c * 4, ok);
+        if (c < 2 * NC)
+            cp16z(tc::smem_u32(sm.v[step % kRaw]) + plane_off(row, c),
+                  (const uint16_t *)a.v + iv + dv0 + c * 8, ok);
+        if (c == 0)
+            cp4z(tc::smem_u32(&sm.beta[step % kRaw][row]), a.beta + tok * a.HV + hv, ok);
+    }
 }
 
-// M and P of a step, 17 (r, s) pairs a warp (rows w and 15 - w), one exp2 per (r, s, channel):
-// every exponent is <= 0, so nothing can overflow.  Lane l holds channels 4l .. 4l + 3.
+// M and P of a step are one product each, M = kw (k 2^-g)^T and P = qw (k 2^-g)^T: the
+// exponents cancel in each term and no term is above |q_r k_s|.  One warp an 8-column half.
+// The halves' other entries (s > r) may be of any size and are dropped.
+__device__ __forceinline__ void scores(Smem &sm, Prepared &out, const float *beta, int buf, int w,
+                                       int lane) {
+    const bool is_p = w & 1;
+    const int nt = w >> 1, m = lane >> 3;
+    const uint32_t pl = tc::smem_u32(out.planes);
+    const uint32_t left = pl + (is_p ? QW_HI : KW_HI) * kPlane;
+    const uint32_t right = pl + (KD_HI + (m >> 1)) * kPlane;
+    const int arow = (lane & 7) + (m & 1) * 8;
+    float c0[4] = {}, c1[4] = {}, c2[4] = {};
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+        uint32_t ah[4], al[4], b[4];
+        const uint32_t off = plane_off(arow, 2 * kk + (m >> 1));
+        ldsm4(ah, left + off);
+        ldsm4(al, left + kPlane + off);
+        ldsm4(b, right + plane_off(8 * nt + (lane & 7), 2 * kk + (m & 1)));
+        mma16816(c0, ah, b[0], b[1]);
+        mma16816(c1, ah, b[2], b[3]);
+        mma16816(c2, al, b[0], b[1]);
+    }
+    const int s = 8 * nt + (lane & 3) * 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = (lane >> 2) + 8 * i;
+        float x = c0[2 * i] + (c1[2 * i] + c2[2 * i]);
+        float y = c0[2 * i + 1] + (c1[2 * i + 1] + c2[2 * i + 1]);
+        if (is_p) {
+            uint32_t hi, lo;
+            split2(s <= r ? x : 0.f, s + 1 <= r ? y : 0.f, hi, lo);
+            *reinterpret_cast<uint32_t *>(out.p + (r * C + s) * 2) = hi;
+            *reinterpret_cast<uint32_t *>(out.p + kTile + (r * C + s) * 2) = lo;
+        } else {
+            if (s < r) {
+                sm.a2[buf][r][s] = x * beta[s];
+                sm.a1[buf][r][s] = x * beta[r];
+            }
+            if (s + 1 < r) {
+                sm.a2[buf][r][s + 1] = y * beta[s + 1];
+                sm.a1[buf][r][s + 1] = y * beta[r];
+            }
+        }
+    }
+}
+
+// Gates so strong that k 2^-g leaves FP32's range inside a step (a channel loses more than
+// 2^-96 in 16 tokens): the key plane in its bounded form, the gate replaced by its cumsum ...
 template <typename T16>
-__device__ __forceinline__ void pair_sums(Smem &sm, const RawStage &raw, const float *beta,
-                                          Prepared &out, int buf, float scale, int w, int lane) {
+__device__ __noinline__ void prep_strong(RawStage &raw, Prepared &out, float scale, int tid) {
+    prep_planes<T16, kHalf, false>(raw, out.planes, out.decay, scale, tid);
+    bar_sync(BAR_PREP, kHalf);
+    float acc = 0.f;
+    for (int r = 0; r < C; ++r) raw.gate[r][tid] = acc += floor_gate(raw.gate[r][tid]);
+}
+
+// ... and M and P pair by pair, one exp2 per (r, s, channel), every exponent <= 0: 17 pairs of
+// the rows w and 15 - w a call.  Lane l holds channels 4l .. 4l + 3.
+template <typename T16>
+__device__ __noinline__ void scores_strong(Smem &sm, const RawStage &raw, const float *beta,
+                                           Prepared &out, int buf, float scale, int w, int lane) {
     auto row4 = [&](const uint16_t *p, float (&x)[4]) {
         const uint2 u = *reinterpret_cast<const uint2 *>(p + 4 * lane);
         const float2 lo = unpack2<T16>(u.x), hi = unpack2<T16>(u.y);
@@ -67,8 +128,8 @@ __device__ __forceinline__ void pair_sums(Smem &sm, const RawStage &raw, const f
     row4(raw.k[r1], k1);
     row4(raw.q[r2], q2);
     row4(raw.k[r2], k2);
-    const float4 g1 = *reinterpret_cast<const float4 *>(&sm.g[r1][4 * lane]);
-    const float4 g2 = *reinterpret_cast<const float4 *>(&sm.g[r2][4 * lane]);
+    const float4 g1 = *reinterpret_cast<const float4 *>(&raw.gate[r1][4 * lane]);
+    const float4 g2 = *reinterpret_cast<const float4 *>(&raw.gate[r2][4 * lane]);
     float v[32], lastp = 0.f;
 #pragma unroll
     for (int j = 0; j < 17; ++j) {
@@ -76,7 +137,7 @@ __device__ __forceinline__ void pair_sums(Smem &sm, const RawStage &raw, const f
         const int s = first ? j : j - w - 1;
         float ks[4];
         row4(raw.k[s], ks);
-        const float4 gs = *reinterpret_cast<const float4 *>(&sm.g[s][4 * lane]);
+        const float4 gs = *reinterpret_cast<const float4 *>(&raw.gate[s][4 * lane]);
         const float4 gr = first ? g1 : g2;
         const float e[4] = {ex2(gr.x - gs.x) * ks[0], ex2(gr.y - gs.y) * ks[1],
                             ex2(gr.z - gs.z) * ks[2], ex2(gr.w - gs.w) * ks[3]};
@@ -97,7 +158,7 @@ __device__ __forceinline__ void pair_sums(Smem &sm, const RawStage &raw, const f
     for (int off = 16; off > 0; off >>= 1) lastp += __shfl_xor_sync(0xffffffffu, lastp, off);
     const float sum = transpose_sum(v, lane);
     auto put = [&](int r, int s, float x, bool is_p) {
-        if (is_p) {
+        if (is_p) {  // the entries above the diagonal are zero from the start or from scores()
             const uint32_t b = pack_bf16(x * scale, 0.f) & 0xffffu;
             const float rest = x * scale - __uint_as_float(b << 16);
             reinterpret_cast<uint16_t *>(out.p)[r * C + s] = (uint16_t)b;
@@ -158,20 +219,25 @@ __device__ __forceinline__ bool any_bad(const float (&x)[2][4]) {
 // acc += X L^T for a lower-triangular [16][16] tile L (hi, lo) where X [16 dv, 16 tokens] has
 // values that are not finite: times the zeros above L's diagonal they would spoil tokens
 // before their own.  Each token's column is taken from the tokens up to it alone.
-__device__ __noinline__ void mma_causal(float (&acc)[2][4], const float (&x)[2][4], uint32_t hi,
+__device__ __forceinline__ void mma_causal(float (&acc)[2][4], const float (&x)[2][4], uint32_t hi,
                                         uint32_t lo, int lane) {
     uint32_t bh[4], bl[4];
     ldsm4(bh, hi + tile_lane(lane));
     ldsm4(bl, lo + tile_lane(lane));
     const int tc2 = (lane & 3) * 2;
+#pragma unroll 1
     for (int r = 0; r < C; ++r) {
         float m[2][4], c[2][4] = {};
         uint32_t ah[4], al[4];
+#pragma unroll
         for (int j = 0; j < 2; ++j)
+#pragma unroll
             for (int p = 0; p < 4; ++p) m[j][p] = 8 * j + tc2 + (p & 1) <= r ? x[j][p] : 0.f;
         split_frag(m[0], m[1], ah, al);
         mma3(c[0], c[1], ah, al, bh, bl);
+#pragma unroll
         for (int j = 0; j < 2; ++j)
+#pragma unroll
             for (int p = 0; p < 4; ++p)
                 if (8 * j + tc2 + (p & 1) == r) acc[j][p] += c[j][p];
     }
@@ -197,54 +263,69 @@ __global__ void __launch_bounds__(kPrepThreads + 32 * NC, 1)
     __syncthreads();
 
     if (warp < kPrepWarps) {
-#if __CUDA_ARCH__ >= 900
-        if (NC == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-#endif
-        for (int i = 0; i < kRaw - 1; ++i) {
-            if (i < steps) load_step<T16, NC>(sm, a, sq, h, hv, dv0, i, tid);
-            cp_async_commit();
+        if (NC == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+        if (tid < kHalf) {  // raw inputs -> operand planes
+            for (int i = 0; i < 2; ++i) {
+                if (i < steps) load_step<T16, NC>(sm, a, sq, h, hv, dv0, i, tid);
+                cp_async_commit();
+            }
+            for (int i = 0; i < steps; ++i) {
+                const int st = i % kStages;
+                Prepared &out = sm.prep[st];
+                RawStage &raw = sm.raw[i % kRaw];
+                cp_wait<1>();
+                // the consumers are done with this stage's previous step (and its values)
+                if (i >= kStages) bar_sync(BAR_EMPTY + st, kHalf + 32 * NC);
+                bar_sync(BAR_PREP, kHalf);
+                if (i + 2 < steps) load_step<T16, NC>(sm, a, sq, h, hv, dv0, i + 2, tid);
+                cp_async_commit();
+                const bool big = prep_planes<T16, kHalf, true>(raw, out.planes, out.decay, a.scale,
+                                                               tid);
+                const bool strong = bar_or(BAR_PREP, kHalf, big);
+                if (strong) prep_strong<T16>(raw, out, a.scale, tid);
+                if (tid == 0) out.from_start = !strong;
+                bar_arrive(BAR_PLANES + st, 2 * kHalf);
+            }
+            cp_async_wait_all();
+            return;
         }
+        // planes -> scores -> T2 and T
+        const int w = warp - kHalf / 32;
         for (int i = 0; i < steps; ++i) {
-            const int st = i & 1;
+            const int st = i % kStages;
             Prepared &out = sm.prep[st];
-            cp_wait<kRaw - 2>();
-            // the consumers are done with this stage's previous step (and with its values)
-            if (i >= kStages) bar_sync(BAR_EMPTY + st, kPrepThreads + 32 * NC);
-            bar_sync(BAR_PREP, kPrepThreads);
-            if (i + kRaw - 1 < steps)
-                load_step<T16, NC>(sm, a, sq, h, hv, dv0, i + kRaw - 1, tid);
-            cp_async_commit();
-            const RawStage &raw = sm.raw[i % kRaw];
-            prep_planes<T16, true>(raw, out.planes, out.decay, sm.g, a.scale, tid);
-            bar_sync(BAR_PREP, kPrepThreads);
-            pair_sums<T16>(sm, raw, sm.beta[i % kV], out, st, a.scale, warp, lane);
-            bar_sync(BAR_PREP, kPrepThreads);
-            if (warp == 0) {
-                if (SAVE || lane < 16) solve(sm, out, st, lane);
+            const float *beta = sm.beta[i % kRaw];
+            bar_sync(BAR_PLANES + st, 2 * kHalf);
+            if (out.from_start) {
+                scores(sm, out, beta, i & 1, w, lane);
+            } else {
+                scores_strong<T16>(sm, sm.raw[i % kRaw], beta, out, i & 1, a.scale, w, lane);
+                scores_strong<T16>(sm, sm.raw[i % kRaw], beta, out, i & 1, a.scale, w + 4, lane);
+            }
+            bar_sync(BAR_SCORE, kHalf);
+            if (w == 0) {
+                if (SAVE || lane < 16) solve(sm, out, i & 1, lane);
                 __syncwarp();
                 bar_arrive(BAR_FULL + st, 32 + 32 * NC);
                 if (SAVE && dv0 == 0) {
-                    char *to = a.tiles + (((size_t)(sq.slot0 + i / 4) * a.HV + hv) * 4 + i % 4) *
-                                             kTilesBytes;
-                    reinterpret_cast<uint4 *>(to)[lane] = reinterpret_cast<uint4 *>(sm.t)[lane];
-                    reinterpret_cast<uint4 *>(to)[32 + lane] =
-                        reinterpret_cast<uint4 *>(sm.t)[32 + lane];
-                    reinterpret_cast<uint4 *>(to)[64 + lane] =
-                        reinterpret_cast<uint4 *>(out.p)[lane];
-                    reinterpret_cast<uint4 *>(to)[96 + lane] =
-                        reinterpret_cast<uint4 *>(out.p)[32 + lane];
+                    uint4 *to = reinterpret_cast<uint4 *>(
+                        a.tiles +
+                        (((size_t)(sq.slot0 + i / 4) * a.HV + hv) * 4 + i % 4) * kTilesBytes);
+                    const uint4 *t = reinterpret_cast<const uint4 *>(sm.t);
+                    const uint4 *p = reinterpret_cast<const uint4 *>(out.p);
+                    to[lane] = t[lane];
+                    to[32 + lane] = t[32 + lane];
+                    to[64 + lane] = p[lane];
+                    to[96 + lane] = p[32 + lane];
                     __syncwarp();
                 }
             }
         }
-        cp_async_wait_all();
         return;
     }
 
     // ------------------------------------------------------------------ consumers
-#if __CUDA_ARCH__ >= 900
-    if (NC == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-#endif
+    if (NC == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     const int cw = warp - kPrepWarps, d0 = dv0 + cw * 16;  // this warp's dv columns
     const int gr = lane >> 2, tc2 = (lane & 3) * 2;
     const size_t sbase = ((size_t)n * a.HV + hv) * D * D;
@@ -267,7 +348,7 @@ __global__ void __launch_bounds__(kPrepThreads + 32 * NC, 1)
     const int trow = lane & 15, tcol = lane >> 4;
 
     for (int i = 0; i < steps; ++i) {
-        const int st = i & 1;
+        const int st = i % kStages;
         if (SAVE && i % 4 == 0)
             store_checkpoint(a.ckpt + ((size_t)(sq.slot0 + i / 4) * a.HV + hv) * kCkptBytes, S, d0,
                              lane);
@@ -292,7 +373,7 @@ __global__ void __launch_bounds__(kPrepThreads + 32 * NC, 1)
         {
             // transposed 8x8 blocks (tokens 0-7, dv 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
             const int rr = (lane & 7) + ((lane >> 4) & 1) * 8, cc = (lane >> 3) & 1;
-            ldsm4t(vr, tc::smem_u32(sm.v[i % kV]) + plane_off(rr, cw * 2 + cc));
+            ldsm4t(vr, tc::smem_u32(sm.v[i % kRaw]) + plane_off(rr, cw * 2 + cc));
         }
         float R[2][4];
 #pragma unroll
@@ -319,7 +400,7 @@ __global__ void __launch_bounds__(kPrepThreads + 32 * NC, 1)
                        d0, lane);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const float2 b = *reinterpret_cast<const float2 *>(&sm.beta[i % kV][8 * j + tc2]);
+            const float2 b = *reinterpret_cast<const float2 *>(&sm.beta[i % kRaw][8 * j + tc2]);
             e[j][0] *= b.x;
             e[j][1] *= b.y;
             e[j][2] *= b.x;
@@ -333,25 +414,34 @@ __global__ void __launch_bounds__(kPrepThreads + 32 * NC, 1)
             ldsm4(bl, tc::smem_u32(in.p) + kTile + tl);
             mma3(xq[0], xq[1], ah, al, bh, bl);
         }
-        // S' = diag(2^g_l) S + kd^T n
+        // S' = 2^g_l (S + (k 2^-g)^T n), or with strong gates 2^g_l S + (k 2^(g_l - g))^T n
+        auto decayed = [&](int jj) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float2 d = *reinterpret_cast<const float2 *>(&in.decay[16 * jj + 8 * x + tc2]);
+                float(&s)[4] = S[2 * jj + x];
+                const float2 u = mul2(make_float2(s[0], s[1]), d);
+                const float2 w = mul2(make_float2(s[2], s[3]), d);
+                s[0] = u.x; s[1] = u.y; s[2] = w.x; s[3] = w.y;
+            }
+        };
+        const bool from_start = in.from_start;
+        if (!from_start) {
+#pragma unroll
+            for (int jj = 0; jj < 8; ++jj) decayed(jj);
+        }
 #pragma unroll
         for (int jj = 0; jj < 8; ++jj) {
-            const float2 x = *reinterpret_cast<const float2 *>(&in.decay[16 * jj + tc2]);
-            const float2 y = *reinterpret_cast<const float2 *>(&in.decay[16 * jj + 8 + tc2]);
-            S[2 * jj][0] *= x.x;
-            S[2 * jj][1] *= x.y;
-            S[2 * jj][2] *= x.x;
-            S[2 * jj][3] *= x.y;
-            S[2 * jj + 1][0] *= y.x;
-            S[2 * jj + 1][1] *= y.y;
-            S[2 * jj + 1][2] *= y.x;
-            S[2 * jj + 1][3] *= y.y;
             const uint32_t off = plane_off(trow, 2 * jj + tcol);
             ldsm4t(bh, pl + KD_HI * kPlane + off);
             ldsm4t(bl, pl + KD_LO * kPlane + off);
             mma3(S[2 * jj], S[2 * jj + 1], ah, al, bh, bl);
         }
-        if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kPrepThreads + 32 * NC);
+        if (from_start) {
+#pragma unroll
+            for (int jj = 0; jj < 8; ++jj) decayed(jj);
+        }
+        if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kHalf + 32 * NC);
         // o: rows of tokens after the transpose
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
