@@ -2,19 +2,23 @@
 // 64-token slot of every head at once, from the state at the slot's start (saved by the
 // forward), the state's gradient at its end, e and Y (first pass).
 //
-// Eight warps own 16 dk channels each and hold S [16 dk, 128 dv] in registers: a step of 16
-// tokens is
-//   F (forwards):  dq = scale 2^g (do S^T),  dk += -beta 2^g (Y S^T),  S <- 2^g_l S + kd^T (beta e)
-//   R (backwards): dk += beta 2^(g_l - g) (e dS'^T),  dS <- 2^g_l dS' + qw^T do - kw^T (beta Y)
-// with e and Y known, so nothing is solved, every product is the warp's own (the accumulators
-// of S are the left operand's fragments of the products that sum over dv), and what is left
-// inside a step is the 16x16 triangle of pairs, taken with one exp2 per (r, s, channel):
-//   a[r,s] = scale beta_s do_r.e_s,  b[r,s] = -beta_r beta_s Y_r.e_s  (s <= r, s < r)
-//   dq_r += a k_s E,  dk_r += b k_s E,  dk_s += (a q_r + b k_r) E,  E = 2^(g_r - g_s)
-// (the pair (t, t) carries no gate: dq_t += a k_t, dk_t += a q_t, apart from x below).
-// dbeta_t = Y_t.e_t.  Every term carries 2^(G_r - G_s) of the whole-sequence cumulative gate,
-// so with x_t = q dq_t + k (dk as row - dk as column), dgate_t = ln2 (sum of x over the slot's
-// tokens from t on + sum_dv S' dS' at the slot's end).
+// Eight warps own 16 dk channels each and hold S [16 dk, 128 dv], or its gradient, in registers.
+// A step of 16 tokens is, with e and Y known (nothing is solved),
+//   R (backwards): dk_col = beta 2^-g (2^g_l (e dS'^T) + qw^T G1 - (beta kw)^T G2)
+//                  dS <- 2^g_l dS' + qw^T do - (beta kw)^T Y
+//   F (forwards):  dq = scale 2^g (do S^T + G1 (beta k 2^-g)),
+//                  dk_row = -beta 2^g (Y S^T + G2 (beta k 2^-g)),
+//                  S <- 2^g_l (S + (beta k 2^-g)^T e)
+// where G1[r,s] = do_r.e_s and G2[r,s] = Y_r.e_s (s < r) carry the step's own pairs, whose decay
+// 2^(g_r - g_s) is the product of the two sides' factors; dk = dk_row + dk_col, dbeta_t = Y_t.e_t.
+// (The pair (t, t) has no decay: scale beta_t do_t.e_t times k_t and q_t, added at the end.)
+// Every product is the warp's own: the accumulators of S are the left operand's fragments of
+// the products that sum over dv, and a thread's elements of q, k and g, of the left operands
+// that sum over tokens and of the results are the same (channel, token) pairs.
+//
+// Every term carries 2^(G_r - G_s) of the whole-sequence cumulative gate, so with
+// x_t = q dq_t + k (dk_row - dk_col)_t the gate's gradient falls by ln2 x_t from a token to the
+// next; at a slot's first token it is ln2 sum_dv S dS.
 #include <type_traits>
 
 #include "kda_chunk.cuh"
@@ -36,11 +40,9 @@ struct __align__(128) Smem {
     char dout[kRowsBytes];              // the same; BF16 has no lo plane
     uint16_t q[BT][QS], k[BT][QS];
     float g[BT][GS];                    // cumulative inside each 16-token step
-    float beta[BT];
-    float a[4][C][C], b[4][C][C];
-    float x[3][C][D];                   // dq, dk as row, dk as column of a step
-    float col2[C][D];                   // dk as column from rows 11 .. 15
-    float tail[D];                      // sum_dv S' dS' at the slot's end
+    float beta[BT], diag[BT];           // diag: do_t.e_t
+    char g1[4][2 * kTile], g2[4][2 * kTile];  // hi, lo of each step, zero from the diagonal on
+    float col[4][8][kThreads];          // dk_col from R to F, each thread's own
 };
 
 __device__ __forceinline__ uint32_t block_addr(uint32_t base, int rb, int cb, int lane) {
@@ -77,36 +79,95 @@ template <typename T16> __device__ __forceinline__ uint16_t to16(float x) {
     return (uint16_t)(pack2<T16>(x, 0.f) & 0xffffu);
 }
 
-// Pairs (r, s), R0 <= r < R1, s < r, of one channel.
-template <typename T16, int R0, int R1>
-__device__ __forceinline__ void pairs(Smem &sm, int j, int ch) {
-    float g[R1], k[R1], col[R1] = {};
+// A thread's elements of a step: channels gr, gr + 8 (i) of its warp's 16, tokens tc2, tc2 + 1,
+// 8 + tc2, 9 + tc2 (p).
+struct Elems {
+    float v[2][4];
+};
+__device__ __forceinline__ int token_of(int p, int tc2) { return tc2 + (p & 1) + (p >> 1) * 8; }
+
+// The elements as a left operand [16 channels, 16 tokens].
+__device__ __forceinline__ void split_elems(const Elems &x, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+    split2(x.v[0][0], x.v[0][1], hi[0], lo[0]);
+    split2(x.v[1][0], x.v[1][1], hi[1], lo[1]);
+    split2(x.v[0][2], x.v[0][3], hi[2], lo[2]);
+    split2(x.v[1][2], x.v[1][3], hi[3], lo[3]);
+}
+
+// q or k of a step (row-major rows of QS elements).
+template <typename T16>
+__device__ __forceinline__ Elems load_elems(const uint16_t (*rows)[QS], int c0, int lane) {
+    uint32_t r[4];
+    ldsm4t(r, tc::smem_u32(&rows[(lane & 7) + ((lane >> 4) & 1) * 8][c0 + ((lane >> 3) & 1) * 8]));
+    Elems x;
 #pragma unroll
-    for (int s = 0; s < R1; ++s) {
-        g[s] = sm.g[j * C + s][ch];
-        k[s] = one<T16>(sm.k[j * C + s][ch]);
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2<T16>(r[i]);
+        x.v[i & 1][(i >> 1) * 2] = f.x;
+        x.v[i & 1][(i >> 1) * 2 + 1] = f.y;
     }
+    return x;
+}
+
+__device__ __forceinline__ void decay_rows(float (&S)[16][4], float d0, float d1) {
 #pragma unroll
-    for (int r = R0; r < R1; ++r) {
-        const float q = one<T16>(sm.q[j * C + r][ch]);
-        float dq = 0.f, dk = 0.f;
+    for (int j = 0; j < 16; ++j) {
+        const float2 u = mul2(make_float2(S[j][0], S[j][1]), make_float2(d0, d0));
+        const float2 w = mul2(make_float2(S[j][2], S[j][3]), make_float2(d1, d1));
+        S[j][0] = u.x; S[j][1] = u.y; S[j][2] = w.x; S[j][3] = w.y;
+    }
+}
+
+// S[16 channels, 128 dv] += A [16 channels, 16 tokens] B, B the step's rows of a block layout.
+template <bool LO>
+__device__ __forceinline__ void add_rows(float (&S)[16][4], const uint32_t (&ah)[4],
+                                         const uint32_t (&al)[4], uint32_t rows, int j, int lane) {
+    const int m = lane >> 3;
 #pragma unroll
-        for (int s = 0; s < r; ++s) {
-            const float a = sm.a[j][r][s], b = sm.b[j][r][s];
-            const float e = ex2(g[r] - g[s]), ke = k[s] * e;
-            dq += a * ke;
-            dk += b * ke;
-            col[s] += (a * q + b * k[r]) * e;
+    for (int jj = 0; jj < 8; ++jj) {
+        uint32_t bh[4], bl[4];
+        const uint32_t off = block_addr(rows, 2 * j + (m & 1), 2 * jj + (m >> 1), lane);
+        ldsm4t(bh, off);
+        if (LO) ldsm4t(bl, off + kRowPlane);
+        mma_b<LO>(S[2 * jj], S[2 * jj + 1], ah, al, bh, bl);
+    }
+}
+
+// A step's pairs where k 2^-g would leave FP32's range: one exp2 per (r, s, channel), the
+// thread's tokens as rows (dq, dk_row; add to what is there) or as columns (dk_col).
+template <typename T16>
+__device__ __noinline__ void pairs_strong(Smem &sm, int j, int c0, int lane, float scale,
+                                          bool columns, Elems &x, Elems &y) {
+    auto tile = [](const char *t, int r, int s) {
+        const uint16_t *h = reinterpret_cast<const uint16_t *>(t) + r * C + s;
+        return __uint_as_float((uint32_t)h[0] << 16) + __uint_as_float((uint32_t)h[C * C] << 16);
+    };
+    const int gr = lane >> 2, tc2 = (lane & 3) * 2;
+    for (int i = 0; i < 2; ++i) {
+        const int ch = c0 + gr + 8 * i;
+        for (int p = 0; p < 4; ++p) {
+            const int t = token_of(p, tc2);
+            const float gt = sm.g[j * C + t][ch];
+            float u = 0.f, w = 0.f;
+            if (!columns) {
+                for (int s = 0; s < t; ++s) {
+                    const float kb = sm.beta[j * C + s] * one<T16>(sm.k[j * C + s][ch]) *
+                                     ex2(gt - sm.g[j * C + s][ch]);
+                    u += tile(sm.g1[j], t, s) * kb;
+                    w += tile(sm.g2[j], t, s) * kb;
+                }
+                x.v[i][p] += scale * u;
+                y.v[i][p] -= sm.beta[j * C + t] * w;
+            } else {
+                for (int r = t + 1; r < C; ++r) {
+                    const float q = scale * one<T16>(sm.q[j * C + r][ch]);
+                    const float k = sm.beta[j * C + r] * one<T16>(sm.k[j * C + r][ch]);
+                    u += (tile(sm.g1[j], r, t) * q - tile(sm.g2[j], r, t) * k) *
+                         ex2(sm.g[j * C + r][ch] - gt);
+                }
+                x.v[i][p] += sm.beta[j * C + t] * u;
+            }
         }
-        sm.x[0][r][ch] += dq;
-        sm.x[1][r][ch] += dk;
-    }
-#pragma unroll
-    for (int s = 0; s < R1; ++s) {
-        if (R0 == 0)
-            sm.x[2][s][ch] += col[s];
-        else
-            sm.col2[s][ch] = col[s];
     }
 }
 
@@ -116,17 +177,18 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     constexpr bool kLo = !In<T16>::exact;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int gr = lane >> 2, tc2 = (lane & 3) * 2;
+    const int gr = lane >> 2, tc2 = (lane & 3) * 2, m = lane >> 3;
     const int c0 = warp * 16;  // this warp's channels
     const uint32_t se = tc::smem_u32(sm.e), sy = tc::smem_u32(sm.y), so = tc::smem_u32(sm.dout);
+    // lanes' offsets of a [16][16] tile as right operand: rows as columns, or rows summed over
+    const uint32_t tn = tile_lane(lane);
+    const uint32_t tt = (uint32_t)(((lane & 7) + ((lane >> 3) & 1) * 8) * 32 + (lane >> 4) * 16);
     const long long units = (long long)a.slots * a.HV;
 
     for (long long u = blockIdx.x; u < units; u += gridDim.x) {
         const int slot = (int)(u / a.HV), hv = (int)(u - (long long)slot * a.HV);
         const int h = hv / (a.HV / a.H);
-        // the slot's sequence and its first token there
-        int n, t0, len;
-        long long row0;
+        int n;  // the slot's sequence
         if (a.cu_seqlens) {
             int lo = 0, hi = a.num_seqs - 1;
             while (lo < hi) {  // the last sequence whose slots begin at or before this one
@@ -138,14 +200,13 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
             n = slot / ((a.T + BT - 1) / BT);
         }
         const Seq sq = seq_of(n, a.T, a.cu_seqlens);
-        t0 = (slot - sq.slot0) * BT;
-        len = sq.len;
-        row0 = sq.row0 + t0;
-        if (t0 < 0 || t0 >= len) continue;  // no tokens here (the same for every thread)
-        const int rows = min(BT, len - t0);
+        const int t0 = (slot - sq.slot0) * BT;
+        const long long row0 = sq.row0 + t0;
+        if (t0 < 0 || t0 >= sq.len) continue;  // no tokens here (the same for every thread)
+        const int rows = min(BT, sq.len - t0);
         const size_t su = (size_t)u;
 
-        // ---- loads
+        // ---- loads; the next unit's large blocks are asked into L2 meanwhile
         for (int i = tid; i < (int)kRowsBytes / 16; i += kThreads) {
             cp16z(se + i * 16, a.e + su * kRowsBytes + i * 16, true);
             cp16z(sy + i * 16, a.y + su * kRowsBytes + i * 16, true);
@@ -179,6 +240,13 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
         }
         if (tid < BT) sm.beta[tid] = tid < rows ? a.beta[(size_t)(row0 + tid) * a.HV + hv] : 0.f;
         cp_async_commit();
+        if (tid == 0 && u + gridDim.x < units) {
+            const size_t nu = su + gridDim.x;
+            tc::prefetch_l2(a.dckpt + nu * kCkptBytes, (uint32_t)kCkptBytes);
+            tc::prefetch_l2(a.e + nu * kRowsBytes, (uint32_t)kRowsBytes);
+            tc::prefetch_l2(a.y + nu * kRowsBytes, (uint32_t)kRowsBytes);
+            tc::prefetch_l2(a.ckpt + nu * kCkptBytes, (uint32_t)kCkptBytes);
+        }
         float S[16][4];  // rows dk c0 + gr, + 8; columns dv 8j + tc2, + 1
         auto load_state = [&](const char *base, int j, float (&x)[4]) {
             const char *p = base + su * kCkptBytes + ((size_t)(c0 / 8) * 16 + j) * 128 + lane * 4;
@@ -192,11 +260,11 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
             x[3] = __uint_as_float(h1 & 0xffff0000u) + __uint_as_float(l1 & 0xffff0000u);
         };
 #pragma unroll
-        for (int j = 0; j < 16; ++j) load_state(a.ckpt, j, S[j]);
+        for (int j = 0; j < 16; ++j) load_state(a.dckpt, j, S[j]);
         cp_async_wait_all();
         __syncthreads();
 
-        // ---- cumulative gate inside each step, and the pair coefficients
+        // ---- cumulative gate inside each step, and the pairs' products
         for (int i = tid; i < 4 * D; i += kThreads) {
             const int ch = i & (D - 1), j = i / D;
             float acc = 0.f;
@@ -211,10 +279,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
             const uint32_t left = warp < 4 ? so : sy;
             const bool left_lo = warp >= 4 || kLo;
             float c[2][4] = {};
-#pragma unroll
+#pragma unroll 4
             for (int kk = 0; kk < 8; ++kk) {
                 uint32_t ah[4], al[4] = {0u, 0u, 0u, 0u}, bh[4], bl[4];
-                const int m = lane >> 3;
                 const uint32_t ao = block_addr(left, 2 * j + (m & 1), 2 * kk + (m >> 1), lane);
                 const uint32_t bo = block_addr(se, 2 * j + (m >> 1), 2 * kk + (m & 1), lane);
                 ldsm4(ah, ao);
@@ -223,35 +290,118 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
                 ldsm4(bl, bo + kRowPlane);
                 mma3(c[0], c[1], ah, al, bh, bl);
             }
+            char *to = warp < 4 ? sm.g1[j] : sm.g2[j];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const int r = gr + (p >> 1) * 8, s = 8 * i + tc2 + (p & 1);
-                    const float bs = sm.beta[j * C + s];
-                    if (warp < 4) {
-                        sm.a[j][r][s] = a.scale * bs * c[i][p];
-                    } else {
-                        sm.b[j][r][s] = -sm.beta[j * C + r] * bs * c[i][p];
-                        const int t = j * C + r;
-                        if (r == s && t < rows)
-                            ((uint16_t *)a.dbeta)[(size_t)(row0 + t) * a.HV + hv] =
-                                to16<T16>(c[i][p]);
+                for (int p = 0; p < 4; p += 2) {
+                    const int r = gr + p * 4, s = 8 * i + tc2, t = j * C + r;
+                    uint32_t hi, lo;
+                    split2(s < r ? c[i][p] : 0.f, s + 1 < r ? c[i][p + 1] : 0.f, hi, lo);
+                    *reinterpret_cast<uint32_t *>(to + (r * C + s) * 2) = hi;
+                    *reinterpret_cast<uint32_t *>(to + kTile + (r * C + s) * 2) = lo;
+                    if (r == s || r == s + 1) {
+                        const float d = r == s ? c[i][p] : c[i][p + 1];
+                        if (warp < 4)
+                            sm.diag[t] = d;
+                        else if (t < rows)
+                            ((uint16_t *)a.dbeta)[(size_t)(row0 + t) * a.HV + hv] = to16<T16>(d);
                     }
                 }
         }
         __syncthreads();
 
-        // this thread's elements of a step: channels c0 + gr, + 8 (i), tokens tc2, tc2 + 1,
-        // 8 + tc2, 9 + tc2 (p) -- the fragments' and the accumulators' common layout
-        auto token = [&](int p) { return tc2 + (p & 1) + (p >> 1) * 8; };
-        float fq[4][2][4], fk[4][2][4];  // [step][channel][token]
-
-        // ---- F
+        // ---- R
+#pragma unroll 1
+        for (int j = 3; j >= 0; --j) {
+            float cd[2][4] = {};
 #pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+                uint32_t ah[4], al[4], bh[4], bl[4];
+                split_frag(S[2 * kk], S[2 * kk + 1], ah, al);
+                const uint32_t off = block_addr(se, 2 * j + (m >> 1), 2 * kk + (m & 1), lane);
+                ldsm4(bh, off);
+                ldsm4(bl, off + kRowPlane);
+                mma_b<true>(cd[0], cd[1], ah, al, bh, bl);
+            }
+            const Elems q = load_elems<T16>(&sm.q[j * C], c0, lane);
+            const Elems k = load_elems<T16>(&sm.k[j * C], c0, lane);
+            Elems qw, kw, g;
+            float gl[2], big = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int ch = c0 + gr + 8 * i;
+                gl[i] = sm.g[j * C + C - 1][ch];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const int t = j * C + token_of(p, tc2);
+                    g.v[i][p] = sm.g[t][ch];
+                    const float up = ex2(g.v[i][p]);
+                    qw.v[i][p] = a.scale * up * q.v[i][p];
+                    kw.v[i][p] = -sm.beta[t] * up * k.v[i][p];
+                }
+                big = fmaxf(big, -gl[i]);
+            }
+            uint32_t ah[4], al[4], wh[4], wl[4];
+            split_elems(qw, ah, al);
+            split_elems(kw, wh, wl);
+            const bool strong = __any_sync(0xffffffffu, big > 96.f);
+            Elems col;
+            if (!strong) {
+                uint32_t bh[4], bl[4];
+                const float d0 = ex2(gl[0]), d1 = ex2(gl[1]);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    cd[x][0] *= d0; cd[x][1] *= d0; cd[x][2] *= d1; cd[x][3] *= d1;
+                }
+                ldsm4t(bh, tc::smem_u32(sm.g1[j]) + tt);
+                ldsm4t(bl, tc::smem_u32(sm.g1[j]) + kTile + tt);
+                mma3(cd[0], cd[1], ah, al, bh, bl);
+                ldsm4t(bh, tc::smem_u32(sm.g2[j]) + tt);
+                ldsm4t(bl, tc::smem_u32(sm.g2[j]) + kTile + tt);
+                mma3(cd[0], cd[1], wh, wl, bh, bl);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const float x = strong ? gl[i] - g.v[i][p] : -g.v[i][p];
+                    col.v[i][p] = sm.beta[j * C + token_of(p, tc2)] * ex2(x) *
+                                  cd[p >> 1][2 * i + (p & 1)];
+                }
+            if (strong) {
+                Elems x = col;
+                pairs_strong<T16>(sm, j, c0, lane, a.scale, true, x, x);
+                col = x;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int p = 0; p < 4; ++p) sm.col[j][4 * i + p][tid] = col.v[i][p];
+            decay_rows(S, ex2(gl[0]), ex2(gl[1]));
+            add_rows<kLo>(S, ah, al, so, j, lane);
+            add_rows<true>(S, wh, wl, sy, j, lane);
+        }
+        // ---- the state at the slot's start, and sum_dv S dS there
+        float carry[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            float x[4];
+            load_state(a.ckpt, j, x);
+            carry[0] += S[j][0] * x[0] + S[j][1] * x[1];
+            carry[1] += S[j][2] * x[2] + S[j][3] * x[3];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) S[j][p] = x[p];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            carry[i] += __shfl_xor_sync(0xffffffffu, carry[i], 1);
+            carry[i] += __shfl_xor_sync(0xffffffffu, carry[i], 2);
+        }
+        // ---- F, and the outputs
+#pragma unroll 1
         for (int j = 0; j < 4; ++j) {
             float cq[2][4] = {}, cy[2][4] = {};
-            const int m = lane >> 3;
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
                 uint32_t ah[4], al[4], bh[4], bl[4];
@@ -264,162 +414,125 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
                 ldsm4(bl, sy + off + kRowPlane);
                 mma_b<true>(cy[0], cy[1], ah, al, bh, bl);
             }
-            float kd[2][4], dec[2];
+            const Elems q = load_elems<T16>(&sm.q[j * C], c0, lane);
+            const Elems k = load_elems<T16>(&sm.k[j * C], c0, lane);
+            Elems kd, g;
+            float gl[2], big = 0.f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int ch = c0 + gr + 8 * i;
-                const float gl = sm.g[j * C + C - 1][ch];
-                dec[i] = ex2(gl);
+                gl[i] = sm.g[j * C + C - 1][c0 + gr + 8 * i];
+                big = fmaxf(big, -gl[i]);
+            }
+            const bool strong = __any_sync(0xffffffffu, big > 96.f);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    const int t = j * C + token(p);
-                    const float g = sm.g[t][ch], up = ex2(g), bt = sm.beta[t];
-                    kd[i][p] = bt * one<T16>(sm.k[t][ch]) * ex2(gl - g);
-                    fq[j][i][p] = a.scale * up * cq[p >> 1][2 * i + (p & 1)];
-                    fk[j][i][p] = -bt * up * cy[p >> 1][2 * i + (p & 1)];
+                    const int t = j * C + token_of(p, tc2);
+                    g.v[i][p] = sm.g[t][c0 + gr + 8 * i];
+                    kd.v[i][p] = sm.beta[t] * k.v[i][p] *
+                                 ex2((strong ? gl[i] : 0.f) - g.v[i][p]);
+                }
+            uint32_t ah[4], al[4];
+            split_elems(kd, ah, al);
+            if (!strong) {
+                uint32_t bh[4], bl[4];
+                ldsm4(bh, tc::smem_u32(sm.g1[j]) + tn);
+                ldsm4(bl, tc::smem_u32(sm.g1[j]) + kTile + tn);
+                mma3(cq[0], cq[1], ah, al, bh, bl);
+                ldsm4(bh, tc::smem_u32(sm.g2[j]) + tn);
+                ldsm4(bl, tc::smem_u32(sm.g2[j]) + kTile + tn);
+                mma3(cy[0], cy[1], ah, al, bh, bl);
+                add_rows<true>(S, ah, al, se, j, lane);
+                decay_rows(S, ex2(gl[0]), ex2(gl[1]));
+            } else {
+                decay_rows(S, ex2(gl[0]), ex2(gl[1]));
+                add_rows<true>(S, ah, al, se, j, lane);
+            }
+            Elems dq, dk;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const float up = ex2(g.v[i][p]);
+                    dq.v[i][p] = a.scale * up * cq[p >> 1][2 * i + (p & 1)];
+                    dk.v[i][p] = -sm.beta[j * C + token_of(p, tc2)] * up *
+                                 cy[p >> 1][2 * i + (p & 1)];
+                }
+            if (strong) {
+                Elems x = dq, y = dk;
+                pairs_strong<T16>(sm, j, c0, lane, a.scale, false, x, y);
+                dq = x;
+                dk = y;
+            }
+            // the gate's gradient: carry less the x of the tokens before
+            Elems dg;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float x[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    x[p] = q.v[i][p] * dq.v[i][p] +
+                           k.v[i][p] * (dk.v[i][p] - sm.col[j][4 * i + p][tid]);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const float pair = x[2 * half] + x[2 * half + 1];
+                    float incl = pair;  // over the four lanes of the channel
+                    float y = __shfl_up_sync(0xffffffffu, incl, 1, 4);
+                    if ((lane & 3) >= 1) incl += y;
+                    y = __shfl_up_sync(0xffffffffu, incl, 2, 4);
+                    if ((lane & 3) >= 2) incl += y;
+                    const float before = incl - pair;
+                    dg.v[i][2 * half] = LN2 * (carry[i] - before);
+                    dg.v[i][2 * half + 1] = LN2 * (carry[i] - before - x[2 * half]);
+                    carry[i] -= __shfl_sync(0xffffffffu, incl, 3, 4);
                 }
             }
-            uint32_t ah[4], al[4];
-            split2(kd[0][0], kd[0][1], ah[0], al[0]);
-            split2(kd[1][0], kd[1][1], ah[1], al[1]);
-            split2(kd[0][2], kd[0][3], ah[2], al[2]);
-            split2(kd[1][2], kd[1][3], ah[3], al[3]);
 #pragma unroll
-            for (int jj = 0; jj < 8; ++jj) {
+            for (int p = 0; p < 4; ++p) {
+                const int t = j * C + token_of(p, tc2);
+                const float d = a.scale * sm.beta[t] * sm.diag[t];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    S[2 * jj + i][0] *= dec[0];
-                    S[2 * jj + i][1] *= dec[0];
-                    S[2 * jj + i][2] *= dec[1];
-                    S[2 * jj + i][3] *= dec[1];
-                }
-                uint32_t bh[4], bl[4];
-                const uint32_t off = block_addr(se, 2 * j + (m & 1), 2 * jj + (m >> 1), lane);
-                ldsm4t(bh, off);
-                ldsm4t(bl, off + kRowPlane);
-                mma3(S[2 * jj], S[2 * jj + 1], ah, al, bh, bl);
-            }
-        }
-        // ---- the state's gradient at the slot's end, and sum_dv S' dS'
-        {
-            float t0s = 0.f, t1s = 0.f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                float x[4];
-                load_state(a.dckpt, j, x);
-                t0s += S[j][0] * x[0] + S[j][1] * x[1];
-                t1s += S[j][2] * x[2] + S[j][3] * x[3];
-#pragma unroll
-                for (int p = 0; p < 4; ++p) S[j][p] = x[p];
-            }
-#pragma unroll
-            for (int off = 1; off < 4; off <<= 1) {
-                t0s += __shfl_xor_sync(0xffffffffu, t0s, off);
-                t1s += __shfl_xor_sync(0xffffffffu, t1s, off);
-            }
-            if ((lane & 3) == 0) {
-                sm.tail[c0 + gr] = t0s;
-                sm.tail[c0 + gr + 8] = t1s;
-            }
-        }
-        // ---- R, and each step's triangle and outputs
-        float carry = 0.f;
-#pragma unroll
-        for (int jr = 0; jr < 4; ++jr) {
-            const int j = 3 - jr, m = lane >> 3;
-            float cd[2][4] = {};
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-                uint32_t ah[4], al[4], bh[4], bl[4];
-                split_frag(S[2 * kk], S[2 * kk + 1], ah, al);
-                const uint32_t off = block_addr(se, 2 * j + (m >> 1), 2 * kk + (m & 1), lane);
-                ldsm4(bh, off);
-                ldsm4(bl, off + kRowPlane);
-                mma_b<true>(cd[0], cd[1], ah, al, bh, bl);
-            }
-            float qw[2][4], kw[2][4], dec[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int ch = c0 + gr + 8 * i;
-                const float gl = sm.g[j * C + C - 1][ch];
-                dec[i] = ex2(gl);
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const int t = j * C + token(p);
-                    const float g = sm.g[t][ch], up = ex2(g), bt = sm.beta[t];
-                    qw[i][p] = a.scale * up * one<T16>(sm.q[t][ch]);
-                    kw[i][p] = -bt * up * one<T16>(sm.k[t][ch]);
-                    sm.x[0][token(p)][ch] = fq[j][i][p];
-                    sm.x[1][token(p)][ch] = fk[j][i][p];
-                    sm.x[2][token(p)][ch] = bt * ex2(gl - g) * cd[p >> 1][2 * i + (p & 1)];
+                    dq.v[i][p] += d * k.v[i][p];
+                    dk.v[i][p] += sm.col[j][4 * i + p][tid] + d * q.v[i][p];
                 }
             }
-            if (j > 0) {
-                uint32_t ah[4], al[4], wh[4], wl[4];
-                split2(qw[0][0], qw[0][1], ah[0], al[0]);
-                split2(qw[1][0], qw[1][1], ah[1], al[1]);
-                split2(qw[0][2], qw[0][3], ah[2], al[2]);
-                split2(qw[1][2], qw[1][3], ah[3], al[3]);
-                split2(kw[0][0], kw[0][1], wh[0], wl[0]);
-                split2(kw[1][0], kw[1][1], wh[1], wl[1]);
-                split2(kw[0][2], kw[0][3], wh[2], wl[2]);
-                split2(kw[1][2], kw[1][3], wh[3], wl[3]);
 #pragma unroll
-                for (int jj = 0; jj < 8; ++jj) {
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        S[2 * jj + i][0] *= dec[0];
-                        S[2 * jj + i][1] *= dec[0];
-                        S[2 * jj + i][2] *= dec[1];
-                        S[2 * jj + i][3] *= dec[1];
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t wg = movm_t(pack2<T16>(dg.v[i][2 * half], dg.v[i][2 * half + 1]));
+                    uint32_t wq = 0, wk = 0;
+                    if (!a.dq_hv) {
+                        wq = movm_t(pack2<T16>(dq.v[i][2 * half], dq.v[i][2 * half + 1]));
+                        wk = movm_t(pack2<T16>(dk.v[i][2 * half], dk.v[i][2 * half + 1]));
                     }
-                    uint32_t bh[4], bl[4];
-                    const uint32_t off = block_addr(0, 2 * j + (m & 1), 2 * jj + (m >> 1), lane);
-                    ldsm4t(bh, so + off);
-                    if (kLo) ldsm4t(bl, so + off + kRowPlane);
-                    mma_b<kLo>(S[2 * jj], S[2 * jj + 1], ah, al, bh, bl);
-                    ldsm4t(bh, sy + off);
-                    ldsm4t(bl, sy + off + kRowPlane);
-                    mma3(S[2 * jj], S[2 * jj + 1], wh, wl, bh, bl);
-                }
-            }
-            __syncthreads();
-            const int ch = tid & (D - 1);
-            if (warp < 4)
-                pairs<T16, 0, 11>(sm, j, ch);
-            else
-                pairs<T16, 11, 16>(sm, j, ch);
-            __syncthreads();
-            if (warp < 4) {
-                if (jr == 0) carry = sm.tail[ch];
+                    const int t = j * C + 8 * half + gr;
+                    const size_t iv =
+                        ((size_t)(row0 + t) * a.HV + hv) * D + c0 + 8 * i + tc2;
+                    if (t < rows && dbg_ok(a.dbg, iv + 1, a.rows_o * D, DBG_STORE)) {
+                        *reinterpret_cast<uint32_t *>((uint16_t *)a.dgate + iv) = wg;
+                        if (!a.dq_hv) {
+                            *reinterpret_cast<uint32_t *>((uint16_t *)a.dq + iv) = wq;
+                            *reinterpret_cast<uint32_t *>((uint16_t *)a.dk + iv) = wk;
+                        }
+                    }
+                    if (a.dq_hv) {  // summed over the head's value heads afterwards, in FP32
 #pragma unroll
-                for (int tt = C - 1; tt >= 0; --tt) {
-                    const int t = j * C + tt;
-                    const float q = one<T16>(sm.q[t][ch]), k = one<T16>(sm.k[t][ch]);
-                    float dq = sm.x[0][tt][ch], dk = sm.x[1][tt][ch];
-                    const float dkc = sm.x[2][tt][ch] + sm.col2[tt][ch];
-                    carry += q * dq + k * (dk - dkc);
-                    // the pair (t, t) has no gate: its shares of x would cancel
-                    const float diag = sm.a[j][tt][tt];
-                    dq += diag * k;
-                    dk += dkc + diag * q;
-                    if (t < rows) {
-                        const size_t tok = (size_t)(row0 + t), iv = (tok * a.HV + hv) * D + ch;
-                        if (dbg_ok(a.dbg, iv, a.rows_o * D, DBG_STORE)) {
-                            ((uint16_t *)a.dgate)[iv] = to16<T16>(LN2 * carry);
-                            if (a.dq_hv) {
-                                a.dq_hv[iv] = dq;
-                                a.dk_hv[iv] = dk;
-                            } else {
-                                ((uint16_t *)a.dq)[iv] = to16<T16>(dq);
-                                ((uint16_t *)a.dk)[iv] = to16<T16>(dk);
+                        for (int p = 2 * half; p < 2 * half + 2; ++p) {
+                            const int tp = j * C + token_of(p, tc2);
+                            const size_t ip =
+                                ((size_t)(row0 + tp) * a.HV + hv) * D + c0 + 8 * i + gr;
+                            if (tp < rows && dbg_ok(a.dbg, ip, a.rows_o * D, DBG_STORE)) {
+                                a.dq_hv[ip] = dq.v[i][p];
+                                a.dk_hv[ip] = dk.v[i][p];
                             }
                         }
                     }
                 }
-            }
-            __syncthreads();
         }
+        __syncthreads();
     }
 }
 
