@@ -1,9 +1,10 @@
-"""What the binding's modules share: checks of arguments, and the current stream."""
+"""What the binding's modules share: checks of arguments, and the call into the library."""
 
 from __future__ import annotations
 
 import ctypes
 import functools
+import sys
 
 import torch
 
@@ -13,20 +14,27 @@ DTYPES = {**DTYPES16, torch.float32: KDA_FP32}
 K = 128
 F32 = torch.float32
 
+_package = sys.modules[__package__]
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
-def check(name, t, shape, dtype, device):
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+def fits(t, shape, dtype, index):
+    """A contiguous tensor of that shape and type on CUDA device `index`."""
+    return (t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous())
+
+
+def check(name, t, shape, dtype, index):
+    if fits(t, shape, dtype, index):
+        return
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-
-
-def ptr(t):
-    return None if t is None else t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def takes_stream(fn):
@@ -46,19 +54,20 @@ def takes_stream(fn):
     return call
 
 
-def run(name, device, *args):
-    """Calls lib.<name>(*args, current stream) on the tensors' device; raises on an error."""
-    from . import KdaError, load_library
-    index = device.index
-    fn = getattr(load_library(), name)
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if torch.cuda.current_device() == index:
-        rc = fn(*args, stream)
+def library():
+    return _package._lib or _package.load_library()
+
+
+def run(name, index, *args):
+    """Calls lib.<name>(*args, current stream) on CUDA device `index`; raises on an error."""
+    fn = getattr(_package._lib or _package.load_library(), name)
+    if _current_device() == index:
+        rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            rc = fn(*args, stream)
+            rc = fn(*args, _raw_stream(index))
     if rc:
-        raise KdaError(rc, name)
+        raise _package.KdaError(rc, name)
 
 
 def declare(lib):

@@ -92,8 +92,7 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -101,19 +100,17 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
 }
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
 }
 // Transpose of an 8x8 matrix of 16-bit values held in fragment order by a warp.
 __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 __device__ __forceinline__ void bar_sync(int id, int n) {
@@ -185,6 +182,28 @@ struct __align__(16) RawStage {
     uint16_t q[C][D];
     uint16_t k[C][D];
     float gate[C][D];
+};
+
+// Which warps do what: eight prepare operands, NW consume them.  With two consumers (few heads,
+// so that the time of one step counts) these get two of the SM's four schedulers for
+// themselves, the preparing warps the other two: warps go to the schedulers in turn, and the
+// warps in between leave at once.
+template <int NW> struct Roles {
+    static constexpr bool kApart = NW == 2;
+    static constexpr int kThreads = kApart ? 512 : kPrepThreads + 32 * NW;
+    int prep, consumer;  // index, or -1
+    __device__ __forceinline__ explicit Roles(int warp) : prep(-1), consumer(-1) {
+        if (kApart) {
+            if (warp & 2)
+                prep = (warp >> 2) * 2 + (warp & 1);
+            else if (warp < 2)
+                consumer = warp;
+        } else if (warp < kPrepWarps) {
+            prep = warp;
+        } else {
+            consumer = warp - kPrepWarps;
+        }
+    }
 };
 
 template <typename T16> __device__ __forceinline__ float2 unpack2(uint32_t x);
@@ -292,28 +311,67 @@ __device__ __forceinline__ void mma3(float (&c0)[4], float (&c1)[4], const uint3
     mma16816(c1, al, bh[2], bh[3]);
 }
 
+// The same for two pairs of tiles with left operands of their own, the four accumulators in
+// turn: a product's result is needed again 32 issue cycles later, its latency being 22.
+// LO0: the first pair's B has a lo part (inputs that are exact in BF16 have none).
+template <bool LO0>
+__device__ __forceinline__ void mma3x2(float (&c0)[4], float (&c1)[4], float (&d0)[4],
+                                       float (&d1)[4], const uint32_t (&ah)[4],
+                                       const uint32_t (&al)[4], const uint32_t (&bh)[4],
+                                       const uint32_t (&bl)[4], const uint32_t (&xh)[4],
+                                       const uint32_t (&xl)[4], const uint32_t (&yh)[4],
+                                       const uint32_t (&yl)[4]) {
+    mma16816(c0, ah, bh[0], bh[1]);
+    mma16816(c1, ah, bh[2], bh[3]);
+    mma16816(d0, xh, yh[0], yh[1]);
+    mma16816(d1, xh, yh[2], yh[3]);
+    mma16816(c0, al, bh[0], bh[1]);
+    mma16816(c1, al, bh[2], bh[3]);
+    mma16816(d0, xl, yh[0], yh[1]);
+    mma16816(d1, xl, yh[2], yh[3]);
+    if (LO0) {
+        mma16816(c0, ah, bl[0], bl[1]);
+        mma16816(c1, ah, bl[2], bl[3]);
+    }
+    mma16816(d0, xh, yl[0], yl[1]);
+    mma16816(d1, xh, yl[2], yl[3]);
+}
+
+// Decay of the accumulators of S^T [16 dv, 128 dk]: columns 16 jj .. 16 jj + 15.
+__device__ __forceinline__ void decay_cols(float (&S)[16][4], const float *decay, int jj, int tc2) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const float2 d = *reinterpret_cast<const float2 *>(&decay[16 * jj + 8 * x + tc2]);
+        float(&s)[4] = S[2 * jj + x];
+        const float2 u = mul2(make_float2(s[0], s[1]), d);
+        const float2 w = mul2(make_float2(s[2], s[3]), d);
+        s[0] = u.x; s[1] = u.y; s[2] = w.x; s[3] = w.y;
+    }
+}
+
 // Per-lane byte offsets of ldmatrix.x4 in a [16][16] tile with 32-byte rows: matrices
 // (rows 0-7, cols 0-7), (rows 0-7, cols 8-15), (rows 8-15, cols 0-7), (rows 8-15, cols 8-15).
 __device__ __forceinline__ uint32_t tile_lane(int lane) {
     return (uint32_t)(((lane & 7) + ((lane >> 4) & 1) * 8) * 32 + ((lane >> 3) & 1) * 16);
 }
 
-// The accumulators of S^T [16 dv, 128 dk] as BF16 hi/lo planes in 8x8 blocks
-// [dk / 8][dv / 8][8 dk][8 dv] (128 contiguous bytes a block): rows of dk, dv contiguous, the
-// K-major operand of every product that sums over dv.
-__device__ __forceinline__ void store_checkpoint(char *base, const float (&S)[16][4], int dv0,
+// The accumulators of S^T [16 MT dv, 128 dk] as a checkpoint: 8 dk rows by 16 dv columns a
+// block, [dk / 8][dv / 16][32 lanes][16 bytes], a lane's words being (row lane / 4, columns
+// 2 (lane % 4), + 1) of the block's left half, hi and lo, and the same of its right half -- the
+// accumulator layout of S [dk, dv], whose left-operand fragments sum over dv.
+template <int MT>
+__device__ __forceinline__ void store_checkpoint(char *base, const float (&S)[MT][16][4], int tile,
                                                  int lane) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        uint32_t h0, l0, h1, l1;
-        split2(S[j][0], S[j][1], h0, l0);
-        split2(S[j][2], S[j][3], h1, l1);
-        char *p = base + ((size_t)j * 16 + dv0 / 8) * 128 + lane * 4;
-        *reinterpret_cast<uint32_t *>(p) = movm_t(h0);
-        *reinterpret_cast<uint32_t *>(p + 128) = movm_t(h1);
-        *reinterpret_cast<uint32_t *>(p + D * D * 2) = movm_t(l0);
-        *reinterpret_cast<uint32_t *>(p + D * D * 2 + 128) = movm_t(l1);
-    }
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            uint32_t h0, l0, h1, l1;
+            split2(S[t][j][0], S[t][j][1], h0, l0);
+            split2(S[t][j][2], S[t][j][3], h1, l1);
+            reinterpret_cast<uint4 *>(base)[(j * 8 + tile + t) * 32 + lane] =
+                make_uint4(movm_t(h0), movm_t(l0), movm_t(h1), movm_t(l1));
+        }
 }
 
 // A [16 dv, 16 token] accumulator pair as hi/lo planes of rows of tokens, in 8x8 blocks

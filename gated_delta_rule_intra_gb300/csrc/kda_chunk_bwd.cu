@@ -53,21 +53,6 @@ template <typename T16> struct In {
     static constexpr bool exact = std::is_same<T16, __nv_bfloat16>::value;
 };
 
-// (c0, c1) += A B^T with A hi/lo and B's blocks: hi, and lo unless B is exact.
-template <bool LO>
-__device__ __forceinline__ void mma_b(float (&c0)[4], float (&c1)[4], const uint32_t (&ah)[4],
-                                      const uint32_t (&al)[4], const uint32_t (&bh)[4],
-                                      const uint32_t (&bl)[4]) {
-    mma16816(c0, ah, bh[0], bh[1]);
-    mma16816(c1, ah, bh[2], bh[3]);
-    mma16816(c0, al, bh[0], bh[1]);
-    mma16816(c1, al, bh[2], bh[3]);
-    if (LO) {
-        mma16816(c0, ah, bl[0], bl[1]);
-        mma16816(c1, ah, bl[2], bl[3]);
-    }
-}
-
 template <typename T16> __device__ __forceinline__ float one(uint16_t x);
 template <> __device__ __forceinline__ float one<__nv_bfloat16>(uint16_t x) {
     return __uint_as_float((uint32_t)x << 16);
@@ -119,17 +104,19 @@ __device__ __forceinline__ void decay_rows(float (&S)[16][4], float d0, float d1
 }
 
 // S[16 channels, 128 dv] += A [16 channels, 16 tokens] B, B the step's rows of a block layout.
-template <bool LO>
 __device__ __forceinline__ void add_rows(float (&S)[16][4], const uint32_t (&ah)[4],
                                          const uint32_t (&al)[4], uint32_t rows, int j, int lane) {
     const int m = lane >> 3;
 #pragma unroll
-    for (int jj = 0; jj < 8; ++jj) {
-        uint32_t bh[4], bl[4];
-        const uint32_t off = block_addr(rows, 2 * j + (m & 1), 2 * jj + (m >> 1), lane);
-        ldsm4t(bh, off);
-        if (LO) ldsm4t(bl, off + kRowPlane);
-        mma_b<LO>(S[2 * jj], S[2 * jj + 1], ah, al, bh, bl);
+    for (int jj = 0; jj < 8; jj += 2) {
+        uint32_t bh[4], bl[4], ch[4], cl[4];
+        const uint32_t o0 = block_addr(rows, 2 * j + (m & 1), 2 * jj + (m >> 1), lane);
+        ldsm4t(bh, o0);
+        ldsm4t(ch, o0 + 2 * 128);
+        ldsm4t(bl, o0 + kRowPlane);
+        ldsm4t(cl, o0 + 2 * 128 + kRowPlane);
+        mma3x2<true>(S[2 * jj], S[2 * jj + 1], S[2 * jj + 2], S[2 * jj + 3], ah, al, bh, bl, ah, al,
+                     ch, cl);
     }
 }
 
@@ -248,19 +235,22 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
             tc::prefetch_l2(a.ckpt + nu * kCkptBytes, (uint32_t)kCkptBytes);
         }
         float S[16][4];  // rows dk c0 + gr, + 8; columns dv 8j + tc2, + 1
-        auto load_state = [&](const char *base, int j, float (&x)[4]) {
-            const char *p = base + su * kCkptBytes + ((size_t)(c0 / 8) * 16 + j) * 128 + lane * 4;
-            const uint32_t h0 = *reinterpret_cast<const uint32_t *>(p);
-            const uint32_t h1 = *reinterpret_cast<const uint32_t *>(p + 16 * 128);
-            const uint32_t l0 = *reinterpret_cast<const uint32_t *>(p + D * D * 2);
-            const uint32_t l1 = *reinterpret_cast<const uint32_t *>(p + D * D * 2 + 16 * 128);
-            x[0] = __uint_as_float(h0 << 16) + __uint_as_float(l0 << 16);
-            x[1] = __uint_as_float(h0 & 0xffff0000u) + __uint_as_float(l0 & 0xffff0000u);
-            x[2] = __uint_as_float(h1 << 16) + __uint_as_float(l1 << 16);
-            x[3] = __uint_as_float(h1 & 0xffff0000u) + __uint_as_float(l1 & 0xffff0000u);
+        // 16 dv columns of a checkpoint (see store_checkpoint()): tiles 2x and 2x + 1 of S
+        auto load_state = [&](const char *base, int x, float (&l)[4], float (&r)[4]) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(base + su * kCkptBytes) +
+                             ((c0 / 8) * 8 + x) * 32 + lane;
+            const uint4 u = p[0], w = p[8 * 32];
+            auto sum = [](uint32_t h, uint32_t lo, float &first, float &second) {
+                first = __uint_as_float(h << 16) + __uint_as_float(lo << 16);
+                second = __uint_as_float(h & 0xffff0000u) + __uint_as_float(lo & 0xffff0000u);
+            };
+            sum(u.x, u.y, l[0], l[1]);
+            sum(w.x, w.y, l[2], l[3]);
+            sum(u.z, u.w, r[0], r[1]);
+            sum(w.z, w.w, r[2], r[3]);
         };
 #pragma unroll
-        for (int j = 0; j < 16; ++j) load_state(a.dckpt, j, S[j]);
+        for (int x = 0; x < 8; ++x) load_state(a.dckpt, x, S[2 * x], S[2 * x + 1]);
         cp_async_wait_all();
         __syncthreads();
 
@@ -314,16 +304,25 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
         // ---- R
 #pragma unroll 1
         for (int j = 3; j >= 0; --j) {
-            float cd[2][4] = {};
+            float cd[2][4] = {}, cd2[2][4] = {}, cd3[2][4] = {};  // three chains a tile
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
                 uint32_t ah[4], al[4], bh[4], bl[4];
-                split_frag(S[2 * kk], S[2 * kk + 1], ah, al);
                 const uint32_t off = block_addr(se, 2 * j + (m >> 1), 2 * kk + (m & 1), lane);
                 ldsm4(bh, off);
                 ldsm4(bl, off + kRowPlane);
-                mma_b<true>(cd[0], cd[1], ah, al, bh, bl);
+                split_frag(S[2 * kk], S[2 * kk + 1], ah, al);
+                mma16816(cd[0], ah, bh[0], bh[1]);
+                mma16816(cd[1], ah, bh[2], bh[3]);
+                mma16816(cd2[0], ah, bl[0], bl[1]);
+                mma16816(cd2[1], ah, bl[2], bl[3]);
+                mma16816(cd3[0], al, bh[0], bh[1]);
+                mma16816(cd3[1], al, bh[2], bh[3]);
             }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int p = 0; p < 4; ++p) cd[x][p] += cd2[x][p] + cd3[x][p];
             const Elems q = load_elems<T16>(&sm.q[j * C], c0, lane);
             const Elems k = load_elems<T16>(&sm.k[j * C], c0, lane);
             Elems qw, kw, g;
@@ -379,19 +378,37 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
 #pragma unroll
                 for (int p = 0; p < 4; ++p) sm.col[j][4 * i + p][tid] = col.v[i][p];
             decay_rows(S, ex2(gl[0]), ex2(gl[1]));
-            add_rows<kLo>(S, ah, al, so, j, lane);
-            add_rows<true>(S, wh, wl, sy, j, lane);
+#pragma unroll
+            for (int jj = 0; jj < 8; ++jj) {  // + qw^T do - (beta kw)^T Y
+                uint32_t bh[4], bl[4], yh[4], yl[4];
+                float t0[4] = {}, t1[4] = {};
+                const uint32_t off = block_addr(0, 2 * j + (m & 1), 2 * jj + (m >> 1), lane);
+                ldsm4t(bh, so + off);
+                ldsm4t(yh, sy + off);
+                if (kLo) ldsm4t(bl, so + off + kRowPlane);
+                ldsm4t(yl, sy + off + kRowPlane);
+                mma3x2<kLo>(t0, t1, S[2 * jj], S[2 * jj + 1], ah, al, bh, bl, wh, wl, yh, yl);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    S[2 * jj][p] += t0[p];
+                    S[2 * jj + 1][p] += t1[p];
+                }
+            }
         }
         // ---- the state at the slot's start, and sum_dv S dS there
         float carry[2] = {0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            float x[4];
-            load_state(a.ckpt, j, x);
-            carry[0] += S[j][0] * x[0] + S[j][1] * x[1];
-            carry[1] += S[j][2] * x[2] + S[j][3] * x[3];
+        for (int i = 0; i < 8; ++i) {
+            float x[2][4];
+            load_state(a.ckpt, i, x[0], x[1]);
 #pragma unroll
-            for (int p = 0; p < 4; ++p) S[j][p] = x[p];
+            for (int y = 0; y < 2; ++y) {
+                float(&s)[4] = S[2 * i + y];
+                carry[0] += s[0] * x[y][0] + s[1] * x[y][1];
+                carry[1] += s[2] * x[y][2] + s[3] * x[y][3];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) s[p] = x[y][p];
+            }
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -405,14 +422,14 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
                 uint32_t ah[4], al[4], bh[4], bl[4];
-                split_frag(S[2 * kk], S[2 * kk + 1], ah, al);
+                uint32_t yh[4], yl[4];
                 const uint32_t off = block_addr(0, 2 * j + (m >> 1), 2 * kk + (m & 1), lane);
                 ldsm4(bh, so + off);
+                ldsm4(yh, sy + off);
                 if (kLo) ldsm4(bl, so + off + kRowPlane);
-                mma_b<kLo>(cq[0], cq[1], ah, al, bh, bl);
-                ldsm4(bh, sy + off);
-                ldsm4(bl, sy + off + kRowPlane);
-                mma_b<true>(cy[0], cy[1], ah, al, bh, bl);
+                ldsm4(yl, sy + off + kRowPlane);
+                split_frag(S[2 * kk], S[2 * kk + 1], ah, al);
+                mma3x2<kLo>(cq[0], cq[1], cy[0], cy[1], ah, al, bh, bl, ah, al, yh, yl);
             }
             const Elems q = load_elems<T16>(&sm.q[j * C], c0, lane);
             const Elems k = load_elems<T16>(&sm.k[j * C], c0, lane);
@@ -443,11 +460,11 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
                 ldsm4(bh, tc::smem_u32(sm.g2[j]) + tn);
                 ldsm4(bl, tc::smem_u32(sm.g2[j]) + kTile + tn);
                 mma3(cy[0], cy[1], ah, al, bh, bl);
-                add_rows<true>(S, ah, al, se, j, lane);
+                add_rows(S, ah, al, se, j, lane);
                 decay_rows(S, ex2(gl[0]), ex2(gl[1]));
             } else {
                 decay_rows(S, ex2(gl[0]), ex2(gl[1]));
-                add_rows<true>(S, ah, al, se, j, lane);
+                add_rows(S, ah, al, se, j, lane);
             }
             Elems dq, dk;
 #pragma unroll

@@ -55,35 +55,45 @@ __device__ __forceinline__ void load_step(Smem &sm, const ChunkBwdArgs &a, const
               true);
 }
 
-// acc += A B with A a 16-bit input fragment: exact in BF16, split in two for FP16.
-template <typename T16>
-__device__ __forceinline__ void mma_in(float (&c0)[4], float (&c1)[4], const uint32_t (&ah)[4],
+// Four tiles += A B with A of the inputs: exact in BF16 (no lo part), split in two for FP16.
+template <bool EXACT>
+__device__ __forceinline__ void mma_in(float (&c0)[4], float (&c1)[4], float (&d0)[4],
+                                       float (&d1)[4], const uint32_t (&ah)[4],
                                        const uint32_t (&al)[4], const uint32_t (&bh)[4],
-                                       const uint32_t (&bl)[4]) {
+                                       const uint32_t (&bl)[4], const uint32_t (&yh)[4],
+                                       const uint32_t (&yl)[4]) {
     mma16816(c0, ah, bh[0], bh[1]);
     mma16816(c1, ah, bh[2], bh[3]);
+    mma16816(d0, ah, yh[0], yh[1]);
+    mma16816(d1, ah, yh[2], yh[3]);
     mma16816(c0, ah, bl[0], bl[1]);
     mma16816(c1, ah, bl[2], bl[3]);
-    if (sizeof(T16) == 2 && !std::is_same<T16, __nv_bfloat16>::value) {
+    mma16816(d0, ah, yl[0], yl[1]);
+    mma16816(d1, ah, yl[2], yl[3]);
+    if (!EXACT) {
         mma16816(c0, al, bh[0], bh[1]);
         mma16816(c1, al, bh[2], bh[3]);
+        mma16816(d0, al, yh[0], yh[1]);
+        mma16816(d1, al, yh[2], yh[3]);
     }
 }
 
 template <typename T16, int NC>
-__global__ void __launch_bounds__(kPrepThreads + 32 * NC, 1)
+__global__ void __launch_bounds__(Roles<NC>::kThreads, 1)
     kda_chunk_bwd_state_kernel(const ChunkBwdArgs a) {
     extern __shared__ __align__(128) char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     constexpr int kSplit = 8 / NC;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int lane = threadIdx.x & 31;
+    const Roles<NC> role(threadIdx.x >> 5);
     const int unit = blockIdx.x / kSplit, dv0 = (blockIdx.x % kSplit) * NC * 16;
     const int n = unit / a.HV, hv = unit - n * a.HV, h = hv / (a.HV / a.H);
     const Seq sq = seq_of(n, a.T, a.cu_seqlens);
     const int steps = (sq.len + BT - 1) / BT * (BT / C);
 
-    if (warp < kPrepWarps) {
-        if (NC == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    if (role.prep >= 0) {
+        const int tid = role.prep * 32 + lane;
+        if (NC == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
         for (int i = 0; i < kRaw - 1; ++i) {
             if (i < steps) load_step<NC>(sm, a, sq, h, hv, dv0, i, steps - 1 - i, tid);
             cp_async_commit();
@@ -104,11 +114,13 @@ __global__ void __launch_bounds__(kPrepThreads + 32 * NC, 1)
         return;
     }
 
-    if (NC == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-    const int cw = warp - kPrepWarps, d0 = dv0 + cw * 16;
+    if (role.consumer < 0) return;
+    if (NC == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    const int cw = role.consumer, d0 = dv0 + cw * 16;
     const int gr = lane >> 2, tc2 = (lane & 3) * 2;
     const size_t sbase = ((size_t)n * a.HV + hv) * D * D;
-    float S[16][4];  // dS^T: rows dv d0 + gr, + 8; columns dk 8j + tc2, + 1
+    float Sm[1][16][4];
+    float(&S)[16][4] = Sm[0];  // dS^T: rows dv d0 + gr, + 8; columns dk 8j + tc2, + 1
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
         if (a.d_final_state) {
@@ -129,52 +141,109 @@ __global__ void __launch_bounds__(kPrepThreads + 32 * NC, 1)
     for (int i = 0; i < steps; ++i) {
         const int st = i & 1, step = steps - 1 - i;
         const size_t slot = (size_t)(sq.slot0 + step / 4) * a.HV + hv;
-        if (step % 4 == 3) store_checkpoint(a.dckpt + slot * kCkptBytes, S, d0, lane);
+        if (step % 4 == 3) store_checkpoint<1>(a.dckpt + slot * kCkptBytes, Sm, d0 / 16, lane);
         bar_sync(BAR_FULL + st, kPrepThreads + 32 * NC);
         const Prepared &in = sm.prep[st];
         const uint32_t pl = tc::smem_u32(in.planes);
-        uint32_t bh[4], bl[4], ah[4], al[4], oh[4], ol[4];
-        // do^T as left operand (dv rows, tokens summed)
-        ldsm4t(oh, tc::smem_u32(sm.dout[i % kRing]) +
-                       plane_off((lane & 7) + ((lane >> 4) & 1) * 8, cw * 2 + ((lane >> 3) & 1)));
-        if (!std::is_same<T16, __nv_bfloat16>::value) {
+        constexpr bool kExact = std::is_same<T16, __nv_bfloat16>::value;
+        uint32_t ah[4], al[4], oh[4], ol[4], ph[4], plo[4], th[4], tlo[4];
+        // do^T as left operand (dv rows, tokens summed): exact in BF16, split in two for FP16
+        ldsm4t(oh, tc::smem_u32(sm.dout[i % kRing]) + plane_off(lrow, cw * 2 + lcol));
+        const uint32_t tl = tc::smem_u32(sm.tiles[i % kRing]) + ttile;
+        ldsm4t(ph, tl + 2 * kTile);
+        ldsm4t(plo, tl + 3 * kTile);
+        ldsm4t(th, tl);
+        ldsm4t(tlo, tl + kTile);
+        const float2 b0 = *reinterpret_cast<const float2 *>(&sm.beta[i % kRing][tc2]);
+        const float2 b1 = *reinterpret_cast<const float2 *>(&sm.beta[i % kRing][8 + tc2]);
+        if (!kExact) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 x = unpack2<T16>(oh[j]);
                 split2(x.x, x.y, oh[j], ol[j]);
             }
         }
-        // dn^T = dS'^T kd^T + do^T P
-        float dn[2][4] = {};
+        // dn^T = do^T P + dS'^T kd^T, in three chains a tile that are added at the end
+        float dn[2][4] = {}, dn2[2][4] = {}, dn3[2][4] = {};
+        mma16816(dn[0], oh, ph[0], ph[1]);
+        mma16816(dn[1], oh, ph[2], ph[3]);
+        mma16816(dn2[0], oh, plo[0], plo[1]);
+        mma16816(dn2[1], oh, plo[2], plo[3]);
+        if (!kExact) {
+            mma16816(dn3[0], ol, ph[0], ph[1]);
+            mma16816(dn3[1], ol, ph[2], ph[3]);
+        }
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
-            split_frag(S[2 * kk], S[2 * kk + 1], ah, al);
+            uint32_t bh[4], bl[4];
             const uint32_t off = plane_off(lrow, 2 * kk + lcol);
             ldsm4(bh, pl + KD_HI * kPlane + off);
             ldsm4(bl, pl + KD_LO * kPlane + off);
-            mma3(dn[0], dn[1], ah, al, bh, bl);
+            split_frag(S[2 * kk], S[2 * kk + 1], ah, al);
+            mma16816(dn[0], ah, bh[0], bh[1]);
+            mma16816(dn[1], ah, bh[2], bh[3]);
+            mma16816(dn2[0], ah, bl[0], bl[1]);
+            mma16816(dn2[1], ah, bl[2], bl[3]);
+            mma16816(dn3[0], al, bh[0], bh[1]);
+            mma16816(dn3[1], al, bh[2], bh[3]);
         }
-        const uint32_t tl = tc::smem_u32(sm.tiles[i % kRing]) + ttile;
-        ldsm4t(bh, tl + 2 * kTile);
-        ldsm4t(bl, tl + 3 * kTile);
-        mma_in<T16>(dn[0], dn[1], oh, ol, bh, bl);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) dn[j][p] += dn2[j][p] + dn3[j][p];
         // Y^T = dn^T T
-        float y[2][4] = {};
+        float y[2][4] = {}, y2[2][4] = {}, y3[2][4] = {};
         split_frag(dn[0], dn[1], ah, al);
-        ldsm4t(bh, tl);
-        ldsm4t(bl, tl + kTile);
-        mma3(y[0], y[1], ah, al, bh, bl);
-        store_rows(a.y + slot * kRowsBytes, y, (step % 4) * C, d0, lane);
-        // dv = beta Y; -dv is the left operand of the state's update
+        mma16816(y[0], ah, th[0], th[1]);
+        mma16816(y[1], ah, th[2], th[3]);
+        mma16816(y2[0], ah, tlo[0], tlo[1]);
+        mma16816(y2[1], ah, tlo[2], tlo[3]);
+        mma16816(y3[0], al, th[0], th[1]);
+        mma16816(y3[1], al, th[2], th[3]);
+        // dS = diag(2^g_l) dS' + qw^T do - kw^T dv; what needs no Y fills Y's latency
+#pragma unroll
+        for (int jj = 0; jj < 8; jj += 2) {
+            uint32_t qh[4], ql[4], rh[4], rl[4];
+            decay_cols(S, in.decay, jj, tc2);
+            decay_cols(S, in.decay, jj + 1, tc2);
+            const uint32_t o0 = plane_off(trow, 2 * jj + tcol);
+            const uint32_t o1 = plane_off(trow, 2 * jj + 2 + tcol);
+            ldsm4t(qh, pl + QW_HI * kPlane + o0);
+            ldsm4t(rh, pl + QW_HI * kPlane + o1);
+            ldsm4t(ql, pl + QW_LO * kPlane + o0);
+            ldsm4t(rl, pl + QW_LO * kPlane + o1);
+            mma_in<kExact>(S[2 * jj], S[2 * jj + 1], S[2 * jj + 2], S[2 * jj + 3], oh, ol, qh, ql,
+                           rh, rl);
+        }
+        float dv[2][4];  // -dv = -beta Y, the left operand of the state's update
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const float2 b = *reinterpret_cast<const float2 *>(&sm.beta[i % kRing][8 * j + tc2]);
-            y[j][0] *= -b.x;
-            y[j][1] *= -b.y;
-            y[j][2] *= -b.x;
-            y[j][3] *= -b.y;
-            const uint32_t u = movm_t(pack2<T16>(-y[j][0], -y[j][1]));
-            const uint32_t w = movm_t(pack2<T16>(-y[j][2], -y[j][3]));
+            const float2 b = j ? b1 : b0;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                y[j][p] += y2[j][p] + y3[j][p];
+                dv[j][p] = -(p & 1 ? b.y : b.x) * y[j][p];
+            }
+        }
+        split_frag(dv[0], dv[1], ah, al);
+#pragma unroll
+        for (int jj = 0; jj < 8; jj += 2) {
+            uint32_t kh[4], kl[4], lh[4], ll[4];
+            const uint32_t o0 = plane_off(trow, 2 * jj + tcol);
+            const uint32_t o1 = plane_off(trow, 2 * jj + 2 + tcol);
+            ldsm4t(kh, pl + KW_HI * kPlane + o0);
+            ldsm4t(lh, pl + KW_HI * kPlane + o1);
+            ldsm4t(kl, pl + KW_LO * kPlane + o0);
+            ldsm4t(ll, pl + KW_LO * kPlane + o1);
+            mma3x2<true>(S[2 * jj], S[2 * jj + 1], S[2 * jj + 2], S[2 * jj + 3], ah, al, kh, kl, ah,
+                         al, lh, ll);
+        }
+        if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kPrepThreads + 32 * NC);
+        store_rows(a.y + slot * kRowsBytes, y, (step % 4) * C, d0, lane);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t u = movm_t(pack2<T16>(-dv[j][0], -dv[j][1]));
+            const uint32_t w = movm_t(pack2<T16>(-dv[j][2], -dv[j][3]));
             const int t = step * C + 8 * j + gr;
             if (t < sq.len) {
                 const size_t idx = ((size_t)(sq.row0 + t) * a.HV + hv) * D + d0 + tc2;
@@ -184,29 +253,6 @@ __global__ void __launch_bounds__(kPrepThreads + 32 * NC, 1)
                 }
             }
         }
-        split_frag(y[0], y[1], ah, al);
-        // dS = diag(2^g_l) dS' + qw^T do - kw^T dv
-#pragma unroll
-        for (int jj = 0; jj < 8; ++jj) {
-            const float2 u = *reinterpret_cast<const float2 *>(&in.decay[16 * jj + tc2]);
-            const float2 w = *reinterpret_cast<const float2 *>(&in.decay[16 * jj + 8 + tc2]);
-            S[2 * jj][0] *= u.x;
-            S[2 * jj][1] *= u.y;
-            S[2 * jj][2] *= u.x;
-            S[2 * jj][3] *= u.y;
-            S[2 * jj + 1][0] *= w.x;
-            S[2 * jj + 1][1] *= w.y;
-            S[2 * jj + 1][2] *= w.x;
-            S[2 * jj + 1][3] *= w.y;
-            const uint32_t off = plane_off(trow, 2 * jj + tcol);
-            ldsm4t(bh, pl + QW_HI * kPlane + off);
-            ldsm4t(bl, pl + QW_LO * kPlane + off);
-            mma_in<T16>(S[2 * jj], S[2 * jj + 1], oh, ol, bh, bl);
-            ldsm4t(bh, pl + KW_HI * kPlane + off);
-            ldsm4t(bl, pl + KW_LO * kPlane + off);
-            mma3(S[2 * jj], S[2 * jj + 1], ah, al, bh, bl);
-        }
-        if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kPrepThreads + 32 * NC);
     }
     if (a.d_initial_state) {
 #pragma unroll
@@ -227,7 +273,7 @@ cudaError_t launch(const ChunkBwdArgs &a, int dev, cudaStream_t stream) {
         smem_limit_once(kda_chunk_bwd_state_kernel<T16, NC>, (int)sizeof(Smem), dev, done);
     if (e != cudaSuccess) return e;
     kda_chunk_bwd_state_kernel<T16, NC>
-        <<<a.num_seqs * a.HV * (8 / NC), kPrepThreads + 32 * NC, sizeof(Smem), stream>>>(a);
+        <<<a.num_seqs * a.HV * (8 / NC), Roles<NC>::kThreads, sizeof(Smem), stream>>>(a);
     return cudaGetLastError();
 }
 

@@ -1,5 +1,7 @@
 // Forward of the gated delta-rule recurrence: one CTA walks one (sequence, value head) in
 // steps of 16 tokens (see kda_chunk.cuh for the mathematics).
+#include <type_traits>
+
 #include "kda_chunk.cuh"
 #include "kda_ops.h"
 
@@ -20,6 +22,7 @@ struct __align__(128) Prepared {
     char p[2 * kTile];
     float decay[D];
     int from_start;      // the key plane is k 2^-g (decay after adding), not k 2^(g_l - g)
+    int careful;         // gates too strong for that, or inputs that are not finite
 };
 
 struct __align__(128) Smem {
@@ -32,7 +35,7 @@ struct __align__(128) Smem {
     char t[2 * kTile];       // T hi, lo on the way to the saved tiles
 };
 
-template <typename T16, int NC>
+template <int SLICE>
 __device__ __forceinline__ void load_step(Smem &sm, const ChunkFwdArgs &a, const Seq &sq, int h,
                                           int hv, int dv0, int step, int tid) {
     RawStage &raw = sm.raw[step % kRaw];
@@ -47,7 +50,7 @@ __device__ __forceinline__ void load_step(Smem &sm, const ChunkFwdArgs &a, const
         cp16z(tc::smem_u32(&raw.k[row][c * 8]), (const uint16_t *)a.k + iq, ok);
         cp16z(tc::smem_u32(&raw.gate[row][c * 4]), a.gate + iv + c * 4, ok);
         cp16z(tc::smem_u32(&raw.gate[row][64 + c * 4]), a.gate + iv + 64 + c * 4, ok);
-        if (c < 2 * NC)
+        if (c < SLICE / 8)
             cp16z(tc::smem_u32(sm.v[step % kRaw]) + plane_off(row, c),
                   (const uint16_t *)a.v + iv + dv0 + c * 8, ok);
         if (c == 0)
@@ -206,21 +209,32 @@ __device__ __forceinline__ void solve(Smem &sm, Prepared &out, int buf, int lane
     }
 }
 
-// Whether any lane holds a value that is not finite.
-__device__ __forceinline__ bool any_bad(const float (&x)[2][4]) {
-    float s = 0.f;
+// Whether any value or beta of a step is not finite (128 threads, SLICE columns of values).
+template <typename T16, int SLICE>
+__device__ __forceinline__ bool not_finite(const uint16_t (*v)[D], const float *beta, int tid) {
+    float2 acc = make_float2(0.f, 0.f);
+    const float2 zero = acc;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int p = 0; p < 4; ++p) s = fmaf(x[j][p], 0.f, s);  // NaN once one is not
-    return __any_sync(0xffffffffu, s != 0.f);
+    for (int i = 0; i < C * SLICE / 8 / kHalf + (C * SLICE / 8 < kHalf); ++i) {
+        const int x = tid + i * kHalf, row = x / (SLICE / 8), c = x % (SLICE / 8);
+        if (row < C) {
+            const uint4 u =
+                *reinterpret_cast<const uint4 *>((const char *)v + plane_off(row, c));
+            acc = fma2(unpack2<T16>(u.x), zero, acc);
+            acc = fma2(unpack2<T16>(u.y), zero, acc);
+            acc = fma2(unpack2<T16>(u.z), zero, acc);
+            acc = fma2(unpack2<T16>(u.w), zero, acc);
+        }
+    }
+    if (tid < C) acc.x = fmaf(beta[tid], 0.f, acc.x);
+    return acc.x + acc.y != 0.f;  // NaN once one was not finite
 }
 
-// acc += X L^T for a lower-triangular [16][16] tile L (hi, lo) where X [16 dv, 16 tokens] has
-// values that are not finite: times the zeros above L's diagonal they would spoil tokens
+// acc += X L^T for a lower-triangular [16][16] tile L (hi, lo) where X [16 dv, 16 tokens] may
+// have values that are not finite: times the zeros above L's diagonal they would spoil tokens
 // before their own.  Each token's column is taken from the tokens up to it alone.
 __device__ __forceinline__ void mma_causal(float (&acc)[2][4], const float (&x)[2][4], uint32_t hi,
-                                        uint32_t lo, int lane) {
+                                           uint32_t lo, int lane) {
     uint32_t bh[4], bl[4];
     ldsm4(bh, hi + tile_lane(lane));
     ldsm4(bl, lo + tile_lane(lane));
@@ -243,14 +257,138 @@ __device__ __forceinline__ void mma_causal(float (&acc)[2][4], const float (&x)[
     }
 }
 
-template <typename T16, int NC, bool SAVE>
-__global__ void __launch_bounds__(kPrepThreads + 32 * NC, 1)
+// One step of a consumer warp's 16 MT columns of dv: e and o (xq) of its tokens, S updated.
+// One straight run of code, so that the chain R -> e -> n of a tile overlaps other products;
+// CAREFUL also takes steps with strong gates or inputs that are not finite.  CKPT: the state's
+// operand halves, which the first product needs anyway, are stored as the slot's checkpoint.
+template <typename T16, int MT, bool CAREFUL, bool CKPT>
+__device__ __forceinline__ void consume(float (&S)[MT][16][4], float (&xq)[MT][2][4],
+                                        float (&e)[MT][2][4], const Prepared &in,
+                                        const uint16_t (*v)[D], const float *beta, char *ckpt,
+                                        int slice_tile, int tile, int lane) {
+    const int tc2 = (lane & 3) * 2;
+    // ldmatrix lane addresses: row-major operand planes and the transposed reads of kd
+    const int lrow = (lane & 7) + ((lane >> 4) & 1) * 8, lcol = (lane >> 3) & 1;
+    const int trow = lane & 15, tcol = lane >> 4;
+    const uint32_t pl = tc::smem_u32(in.planes), tl = tile_lane(lane);
+    float xw[MT][2][4];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) xw[t][j][p] = xq[t][j][p] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+        uint32_t kh[4], kl[4], qh[4], ql[4];
+        const uint32_t off = plane_off(lrow, 2 * kk + lcol);
+        ldsm4(kh, pl + KW_HI * kPlane + off);
+        ldsm4(qh, pl + QW_HI * kPlane + off);
+        ldsm4(kl, pl + KW_LO * kPlane + off);
+        ldsm4(ql, pl + QW_LO * kPlane + off);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            uint32_t ah[4], al[4];
+            split_frag(S[t][2 * kk], S[t][2 * kk + 1], ah, al);
+            mma3x2<true>(xw[t][0], xw[t][1], xq[t][0], xq[t][1], ah, al, kh, kl, ah, al, qh, ql);
+            if (CKPT) {
+                uint4 *p = reinterpret_cast<uint4 *>(ckpt) + (2 * kk * 8 + slice_tile + tile + t) * 32 + lane;
+                p[0] = make_uint4(movm_t(ah[0]), movm_t(al[0]), movm_t(ah[1]), movm_t(al[1]));
+                p[8 * 32] = make_uint4(movm_t(ah[2]), movm_t(al[2]), movm_t(ah[3]), movm_t(al[3]));
+            }
+        }
+    }
+    uint32_t th[4], tlo[4], nh[MT][4], nl[MT][4];
+    ldsm4(th, tc::smem_u32(in.t2) + tl);
+    ldsm4(tlo, tc::smem_u32(in.t2) + kTile + tl);
+    const float2 b[2] = {*reinterpret_cast<const float2 *>(&beta[tc2]),
+                         *reinterpret_cast<const float2 *>(&beta[8 + tc2])};
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        // transposed 8x8 blocks (tokens 0-7, dv 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
+        uint32_t vr[4];
+        ldsm4t(vr, tc::smem_u32(v) + plane_off(lrow, (tile + t) * 2 + lcol));
+        float R[2][4];  // v - kw S
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float2 x = unpack2<T16>(vr[2 * j]), y = unpack2<T16>(vr[2 * j + 1]);
+            R[j][0] = x.x - xw[t][j][0];
+            R[j][1] = x.y - xw[t][j][1];
+            R[j][2] = y.x - xw[t][j][2];
+            R[j][3] = y.y - xw[t][j][3];
+            e[t][j][0] = e[t][j][1] = e[t][j][2] = e[t][j][3] = 0.f;
+        }
+        if (CAREFUL) {
+            mma_causal(e[t], R, tc::smem_u32(in.t2), tc::smem_u32(in.t2) + kTile, lane);
+        } else {
+            uint32_t ah[4], al[4];
+            float e2[2][4] = {}, e3[2][4] = {};
+            split_frag(R[0], R[1], ah, al);
+            mma16816(e[t][0], ah, th[0], th[1]);
+            mma16816(e[t][1], ah, th[2], th[3]);
+            mma16816(e2[0], ah, tlo[0], tlo[1]);
+            mma16816(e2[1], ah, tlo[2], tlo[3]);
+            mma16816(e3[0], al, th[0], th[1]);
+            mma16816(e3[1], al, th[2], th[3]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int p = 0; p < 4; ++p) e[t][j][p] += e2[j][p] + e3[j][p];
+        }
+        float nb[2][4];  // n = beta e
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) nb[j][p] = e[t][j][p] * (p & 1 ? b[j].y : b[j].x);
+        split_frag(nb[0], nb[1], nh[t], nl[t]);
+        if (CAREFUL) mma_causal(xq[t], nb, tc::smem_u32(in.p), tc::smem_u32(in.p) + kTile, lane);
+    }
+    // S' = 2^g_l (S + (k 2^-g)^T n), or with strong gates 2^g_l S + (k 2^(g_l - g))^T n
+    if (CAREFUL && !in.from_start) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int jj = 0; jj < 8; ++jj) decay_cols(S[t], in.decay, jj, tc2);
+    }
+#pragma unroll
+    for (int jj = 0; jj < 8; jj += 2) {
+        uint32_t bh[4], bl[4], ch[4], cl[4];
+        const uint32_t o0 = plane_off(trow, 2 * jj + tcol);
+        const uint32_t o1 = plane_off(trow, 2 * jj + 2 + tcol);
+        ldsm4t(bh, pl + KD_HI * kPlane + o0);
+        ldsm4t(ch, pl + KD_HI * kPlane + o1);
+        ldsm4t(bl, pl + KD_LO * kPlane + o0);
+        ldsm4t(cl, pl + KD_LO * kPlane + o1);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+            mma3x2<true>(S[t][2 * jj], S[t][2 * jj + 1], S[t][2 * jj + 2], S[t][2 * jj + 3], nh[t],
+                         nl[t], bh, bl, nh[t], nl[t], ch, cl);
+    }
+    // o = qw S + P n
+    if (!CAREFUL) {
+        ldsm4(th, tc::smem_u32(in.p) + tl);
+        ldsm4(tlo, tc::smem_u32(in.p) + kTile + tl);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) mma3(xq[t][0], xq[t][1], nh[t], nl[t], th, tlo);
+    }
+    if (!CAREFUL || in.from_start) {
+#pragma unroll
+        for (int jj = 0; jj < 8; ++jj)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) decay_cols(S[t], in.decay, jj, tc2);
+    }
+}
+
+// NW consumer warps of 16 MT dv columns each; a head takes 128 / (16 NW MT) CTAs.
+template <typename T16, int NW, int MT, bool SAVE>
+__global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
     kda_chunk_fwd_kernel(const ChunkFwdArgs a) {
+    constexpr int kSlice = 16 * NW * MT, kSplit = D / kSlice;
     extern __shared__ __align__(128) char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
-    constexpr int kSplit = 8 / NC;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int unit = blockIdx.x / kSplit, dv0 = (blockIdx.x % kSplit) * NC * 16;
+    const int lane = threadIdx.x & 31;
+    const Roles<NW> role(threadIdx.x >> 5);
+    const int unit = blockIdx.x / kSplit, dv0 = (blockIdx.x % kSplit) * kSlice;
     const int n = unit / a.HV, hv = unit - n * a.HV, h = hv / (a.HV / a.H);
     const Seq sq = seq_of(n, a.T, a.cu_seqlens);
     // whole 64-token slots where the backward's buffers are written: rows past the end are
@@ -258,15 +396,16 @@ __global__ void __launch_bounds__(kPrepThreads + 32 * NC, 1)
     const int steps = SAVE ? (sq.len + BT - 1) / BT * (BT / C) : (sq.len + C - 1) / C;
 
     // P's entries above the diagonal are never written later
-    for (int i = tid; i < kStages * 2 * kTile / 4; i += blockDim.x)
+    for (int i = threadIdx.x; i < kStages * 2 * kTile / 4; i += blockDim.x)
         reinterpret_cast<uint32_t *>(sm.prep[i / (2 * kTile / 4)].p)[i % (2 * kTile / 4)] = 0u;
     __syncthreads();
 
-    if (warp < kPrepWarps) {
-        if (NC == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    if (role.prep >= 0) {
+        const int tid = role.prep * 32 + lane;
+        if (MT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
         if (tid < kHalf) {  // raw inputs -> operand planes
             for (int i = 0; i < 2; ++i) {
-                if (i < steps) load_step<T16, NC>(sm, a, sq, h, hv, dv0, i, tid);
+                if (i < steps) load_step<kSlice>(sm, a, sq, h, hv, dv0, i, tid);
                 cp_async_commit();
             }
             for (int i = 0; i < steps; ++i) {
@@ -275,9 +414,9 @@ __global__ void __launch_bounds__(kPrepThreads + 32 * NC, 1)
                 RawStage &raw = sm.raw[i % kRaw];
                 cp_wait<1>();
                 // the consumers are done with this stage's previous step (and its values)
-                if (i >= kStages) bar_sync(BAR_EMPTY + st, kHalf + 32 * NC);
+                if (i >= kStages) bar_sync(BAR_EMPTY + st, kHalf + 32 * NW);
                 bar_sync(BAR_PREP, kHalf);
-                if (i + 2 < steps) load_step<T16, NC>(sm, a, sq, h, hv, dv0, i + 2, tid);
+                if (i + 2 < steps) load_step<kSlice>(sm, a, sq, h, hv, dv0, i + 2, tid);
                 cp_async_commit();
                 const bool big = prep_planes<T16, kHalf, true>(raw, out.planes, out.decay, a.scale,
                                                                tid);
@@ -290,7 +429,7 @@ __global__ void __launch_bounds__(kPrepThreads + 32 * NC, 1)
             return;
         }
         // planes -> scores -> T2 and T
-        const int w = warp - kHalf / 32;
+        const int w = role.prep - kHalf / 32;
         for (int i = 0; i < steps; ++i) {
             const int st = i % kStages;
             Prepared &out = sm.prep[st];
@@ -302,11 +441,13 @@ __global__ void __launch_bounds__(kPrepThreads + 32 * NC, 1)
                 scores_strong<T16>(sm, sm.raw[i % kRaw], beta, out, i & 1, a.scale, w, lane);
                 scores_strong<T16>(sm, sm.raw[i % kRaw], beta, out, i & 1, a.scale, w + 4, lane);
             }
-            bar_sync(BAR_SCORE, kHalf);
+            const bool bad = bar_or(
+                BAR_SCORE, kHalf, not_finite<T16, kSlice>(sm.v[i % kRaw], beta, tid - kHalf));
             if (w == 0) {
+                if (lane == 0) out.careful = bad || !out.from_start;
                 if (SAVE || lane < 16) solve(sm, out, i & 1, lane);
                 __syncwarp();
-                bar_arrive(BAR_FULL + st, 32 + 32 * NC);
+                bar_arrive(BAR_FULL + st, 32 + 32 * NW);
                 if (SAVE && dv0 == 0) {
                     uint4 *to = reinterpret_cast<uint4 *>(
                         a.tiles +
@@ -325,168 +466,103 @@ __global__ void __launch_bounds__(kPrepThreads + 32 * NC, 1)
     }
 
     // ------------------------------------------------------------------ consumers
-    if (NC == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
-    const int cw = warp - kPrepWarps, d0 = dv0 + cw * 16;  // this warp's dv columns
+    if (role.consumer < 0) return;
+    if (MT > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+    const int cw = role.consumer, d0 = dv0 + cw * MT * 16;  // this warp's first dv column
     const int gr = lane >> 2, tc2 = (lane & 3) * 2;
     const size_t sbase = ((size_t)n * a.HV + hv) * D * D;
-    float S[16][4];  // S^T: rows d0 + gr, d0 + gr + 8; columns dk 8j + tc2, + 1
-    if (a.initial_state) {
+    float S[MT][16][4];  // S^T: rows d0 + 16t + gr, + 8; columns dk 8j + tc2, + 1
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-            const float *p = a.initial_state + sbase + (size_t)(8 * j + tc2) * D + d0 + gr;
-            S[j][0] = p[0];
-            S[j][1] = p[D];
-            S[j][2] = p[8];
-            S[j][3] = p[D + 8];
+            S[t][j][0] = S[t][j][1] = S[t][j][2] = S[t][j][3] = 0.f;
+            if (a.initial_state) {
+                const float *p =
+                    a.initial_state + sbase + (size_t)(8 * j + tc2) * D + d0 + 16 * t + gr;
+                S[t][j][0] = p[0];
+                S[t][j][1] = p[D];
+                S[t][j][2] = p[8];
+                S[t][j][3] = p[D + 8];
+            }
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) S[j][0] = S[j][1] = S[j][2] = S[j][3] = 0.f;
-    }
-    // ldmatrix lane addresses: row-major operand planes and the transposed reads of kd
-    const int lrow = (lane & 7) + ((lane >> 4) & 1) * 8, lcol = (lane >> 3) & 1;
-    const int trow = lane & 15, tcol = lane >> 4;
 
     for (int i = 0; i < steps; ++i) {
         const int st = i % kStages;
-        if (SAVE && i % 4 == 0)
-            store_checkpoint(a.ckpt + ((size_t)(sq.slot0 + i / 4) * a.HV + hv) * kCkptBytes, S, d0,
-                             lane);
-        bar_sync(BAR_FULL + st, 32 + 32 * NC);
+        const size_t slot = (size_t)(sq.slot0 + i / 4) * a.HV + hv;
+        float xq[MT][2][4], e[MT][2][4];
+        bar_sync(BAR_FULL + st, 32 + 32 * NW);
         const Prepared &in = sm.prep[st];
-        const uint32_t pl = tc::smem_u32(in.planes);
-        float xw[2][4] = {}, xq[2][4] = {};
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-            uint32_t ah[4], al[4], bh[4], bl[4];
-            split_frag(S[2 * kk], S[2 * kk + 1], ah, al);
-            const uint32_t off = plane_off(lrow, 2 * kk + lcol);
-            ldsm4(bh, pl + KW_HI * kPlane + off);
-            ldsm4(bl, pl + KW_LO * kPlane + off);
-            mma3(xw[0], xw[1], ah, al, bh, bl);
-            ldsm4(bh, pl + QW_HI * kPlane + off);
-            ldsm4(bl, pl + QW_LO * kPlane + off);
-            mma3(xq[0], xq[1], ah, al, bh, bl);
-        }
-        // R = v - kw S
-        uint32_t vr[4];
-        {
-            // transposed 8x8 blocks (tokens 0-7, dv 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
-            const int rr = (lane & 7) + ((lane >> 4) & 1) * 8, cc = (lane >> 3) & 1;
-            ldsm4t(vr, tc::smem_u32(sm.v[i % kRaw]) + plane_off(rr, cw * 2 + cc));
-        }
-        float R[2][4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float2 x = unpack2<T16>(vr[2 * j]), y = unpack2<T16>(vr[2 * j + 1]);
-            R[j][0] = x.x - xw[j][0];
-            R[j][1] = x.y - xw[j][1];
-            R[j][2] = y.x - xw[j][2];
-            R[j][3] = y.y - xw[j][3];
-        }
-        const uint32_t tl = tile_lane(lane);
-        uint32_t ah[4], al[4], bh[4], bl[4];
-        float e[2][4] = {};
-        if (any_bad(R)) {
-            mma_causal(e, R, tc::smem_u32(in.t2), tc::smem_u32(in.t2) + kTile, lane);
-        } else {
-            split_frag(R[0], R[1], ah, al);
-            ldsm4(bh, tc::smem_u32(in.t2) + tl);
-            ldsm4(bl, tc::smem_u32(in.t2) + kTile + tl);
-            mma3(e[0], e[1], ah, al, bh, bl);
-        }
-        if (SAVE)
-            store_rows(a.e + ((size_t)(sq.slot0 + i / 4) * a.HV + hv) * kRowsBytes, e, (i % 4) * C,
-                       d0, lane);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float2 b = *reinterpret_cast<const float2 *>(&sm.beta[i % kRaw][8 * j + tc2]);
-            e[j][0] *= b.x;
-            e[j][1] *= b.y;
-            e[j][2] *= b.x;
-            e[j][3] *= b.y;
-        }
-        split_frag(e[0], e[1], ah, al);  // n = beta e
-        if (any_bad(e)) {
-            mma_causal(xq, e, tc::smem_u32(in.p), tc::smem_u32(in.p) + kTile, lane);
-        } else {
-            ldsm4(bh, tc::smem_u32(in.p) + tl);
-            ldsm4(bl, tc::smem_u32(in.p) + kTile + tl);
-            mma3(xq[0], xq[1], ah, al, bh, bl);
-        }
-        // S' = 2^g_l (S + (k 2^-g)^T n), or with strong gates 2^g_l S + (k 2^(g_l - g))^T n
-        auto decayed = [&](int jj) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const float2 d = *reinterpret_cast<const float2 *>(&in.decay[16 * jj + 8 * x + tc2]);
-                float(&s)[4] = S[2 * jj + x];
-                const float2 u = mul2(make_float2(s[0], s[1]), d);
-                const float2 w = mul2(make_float2(s[2], s[3]), d);
-                s[0] = u.x; s[1] = u.y; s[2] = w.x; s[3] = w.y;
-            }
+        const uint16_t(*v)[D] = sm.v[i % kRaw];
+        const float *beta = sm.beta[i % kRaw];
+        char *ckpt = SAVE ? a.ckpt + slot * kCkptBytes : nullptr;
+        // tiles of 16 dv columns: of the CTA's slice for v, of the head for the checkpoint
+        auto run = [&](auto careful, auto keep) {
+            consume<T16, MT, decltype(careful)::value, decltype(keep)::value>(
+                S, xq, e, in, v, beta, ckpt, dv0 / 16, cw * MT, lane);
         };
-        const bool from_start = in.from_start;
-        if (!from_start) {
-#pragma unroll
-            for (int jj = 0; jj < 8; ++jj) decayed(jj);
+        const bool keep = SAVE && i % 4 == 0;
+        if (!in.careful) {
+            if (keep)
+                run(std::false_type{}, std::integral_constant<bool, SAVE>{});
+            else
+                run(std::false_type{}, std::false_type{});
+        } else {
+            if (keep) store_checkpoint(ckpt, S, d0 / 16, lane);
+            run(std::true_type{}, std::false_type{});
         }
+        if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kHalf + 32 * NW);
 #pragma unroll
-        for (int jj = 0; jj < 8; ++jj) {
-            const uint32_t off = plane_off(trow, 2 * jj + tcol);
-            ldsm4t(bh, pl + KD_HI * kPlane + off);
-            ldsm4t(bl, pl + KD_LO * kPlane + off);
-            mma3(S[2 * jj], S[2 * jj + 1], ah, al, bh, bl);
-        }
-        if (from_start) {
+        for (int t = 0; t < MT; ++t) {
+            if (SAVE) store_rows(a.e + slot * kRowsBytes, e[t], (i % 4) * C, d0 + 16 * t, lane);
 #pragma unroll
-            for (int jj = 0; jj < 8; ++jj) decayed(jj);
-        }
-        if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kHalf + 32 * NC);
-        // o: rows of tokens after the transpose
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t x = movm_t(pack2<T16>(xq[j][0], xq[j][1]));
-            const uint32_t y = movm_t(pack2<T16>(xq[j][2], xq[j][3]));
-            const int t = i * C + 8 * j + gr;
-            if (t < sq.len) {
-                const size_t idx = ((size_t)(sq.row0 + t) * a.HV + hv) * D + d0 + tc2;
-                if (dbg_ok(a.dbg, idx + 9, a.rows_o * D, DBG_STORE)) {
-                    *reinterpret_cast<uint32_t *>((uint16_t *)a.o + idx) = x;
-                    *reinterpret_cast<uint32_t *>((uint16_t *)a.o + idx + 8) = y;
+            for (int j = 0; j < 2; ++j) {  // o: rows of tokens after the transpose
+                const uint32_t x = movm_t(pack2<T16>(xq[t][j][0], xq[t][j][1]));
+                const uint32_t y = movm_t(pack2<T16>(xq[t][j][2], xq[t][j][3]));
+                const int tok = i * C + 8 * j + gr;
+                if (tok < sq.len) {
+                    const size_t idx =
+                        ((size_t)(sq.row0 + tok) * a.HV + hv) * D + d0 + 16 * t + tc2;
+                    if (dbg_ok(a.dbg, idx + 9, a.rows_o * D, DBG_STORE)) {
+                        *reinterpret_cast<uint32_t *>((uint16_t *)a.o + idx) = x;
+                        *reinterpret_cast<uint32_t *>((uint16_t *)a.o + idx + 8) = y;
+                    }
                 }
             }
         }
     }
     if (a.final_state) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            float *p = a.final_state + sbase + (size_t)(8 * j + tc2) * D + d0 + gr;
-            p[0] = S[j][0];
-            p[D] = S[j][1];
-            p[8] = S[j][2];
-            p[D + 8] = S[j][3];
-        }
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                float *p = a.final_state + sbase + (size_t)(8 * j + tc2) * D + d0 + 16 * t + gr;
+                p[0] = S[t][j][0];
+                p[D] = S[t][j][1];
+                p[8] = S[t][j][2];
+                p[D + 8] = S[t][j][3];
+            }
     }
 }
 
-template <typename T16, int NC, bool SAVE>
+template <typename T16, int NW, int MT, bool SAVE>
 cudaError_t launch(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
     static volatile int done[kMaxDev];
     cudaError_t e =
-        smem_limit_once(kda_chunk_fwd_kernel<T16, NC, SAVE>, (int)sizeof(Smem), dev, done);
+        smem_limit_once(kda_chunk_fwd_kernel<T16, NW, MT, SAVE>, (int)sizeof(Smem), dev, done);
     if (e != cudaSuccess) return e;
-    const int grid = a.num_seqs * a.HV * (8 / NC);
-    kda_chunk_fwd_kernel<T16, NC, SAVE>
-        <<<grid, kPrepThreads + 32 * NC, sizeof(Smem), stream>>>(a);
+    const int grid = a.num_seqs * a.HV * (D / (16 * NW * MT));
+    kda_chunk_fwd_kernel<T16, NW, MT, SAVE>
+        <<<grid, Roles<NW>::kThreads, sizeof(Smem), stream>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T16, bool SAVE>
-cudaError_t launch_nc(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
+cudaError_t launch_split(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
     const long long heads = (long long)a.num_seqs * a.HV;
-    if (heads * 2 > kSMs) return launch<T16, 8, SAVE>(a, dev, stream);
-    if (heads * 4 > kSMs) return launch<T16, 4, SAVE>(a, dev, stream);
-    return launch<T16, 2, SAVE>(a, dev, stream);
+    if (heads * 2 > kSMs) return launch<T16, 4, 2, SAVE>(a, dev, stream);
+    if (heads * 4 > kSMs) return launch<T16, 4, 1, SAVE>(a, dev, stream);
+    return launch<T16, 2, 1, SAVE>(a, dev, stream);
 }
 
 }  // namespace
@@ -498,10 +574,10 @@ cudaError_t launch_chunk_fwd(const ChunkFwdArgs &a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const bool save = a.ckpt != nullptr;
     if (a.fp16)
-        return save ? chunk::launch_nc<__half, true>(a, dev, stream)
-                    : chunk::launch_nc<__half, false>(a, dev, stream);
-    return save ? chunk::launch_nc<__nv_bfloat16, true>(a, dev, stream)
-                : chunk::launch_nc<__nv_bfloat16, false>(a, dev, stream);
+        return save ? chunk::launch_split<__half, true>(a, dev, stream)
+                    : chunk::launch_split<__half, false>(a, dev, stream);
+    return save ? chunk::launch_split<__nv_bfloat16, true>(a, dev, stream)
+                : chunk::launch_split<__nv_bfloat16, false>(a, dev, stream);
 }
 
 }  // namespace kda

@@ -58,6 +58,11 @@ __device__ __forceinline__ void cp_async_wait_all() {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// All but the N newest groups of this thread's copies have landed.
+template <int N> __device__ __forceinline__ void cp_async_wait_newest() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Bounds-checked debug build (compiled with KDA_DEBUG_CHECKS): every global index a
 // kernel computes is checked against its buffer's extent before the access; an index
 // out of range sets `bit` in the caller's flag word (when one is set) and the access is

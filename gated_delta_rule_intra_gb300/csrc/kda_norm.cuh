@@ -61,6 +61,49 @@ template <typename T, bool WIDE, int TPR> struct Part {
     }
 };
 
+// Rows on their way to a thread: the 16-byte parts of its eight elements of the next DEPTH - 1
+// rows, copied asynchronously into slots of its own in shared memory, so that as many bytes
+// are in flight as the memory's latency asks for without a register or a barrier.  Rows on no
+// 16-byte boundary (WIDE false) come through registers, one row ahead.
+template <typename T, bool WIDE, int TPR, int THREADS, int DEPTH> struct Stream {
+    using P = Part<T, WIDE, TPR>;
+    static constexpr int kParts = E * (int)sizeof(T) / 16;
+    static constexpr int kBytes = WIDE ? DEPTH * kParts * THREADS * 16 : 0;
+    uint4 *slots;  // [DEPTH][kParts][THREADS], this thread's column
+    P next;
+
+    __device__ __forceinline__ Stream(char *s)
+        : slots(reinterpret_cast<uint4 *>(s) + threadIdx.x) {}
+    __device__ __forceinline__ void fetch(int stage, const T *row, int t, int width, bool ok) {
+        if (WIDE) {
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) {
+                const int c = P::col(t, i * P::kVec);
+                const bool in = ok && c < width;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 (uint32_t)__cvta_generic_to_shared(
+                                     slots + (stage * kParts + i) * THREADS)),
+                             "l"(in ? row + c : row), "r"(in ? 16 : 0)
+                             : "memory");
+            }
+        } else {
+            next.load(row, t, width, ok);
+        }
+    }
+    __device__ __forceinline__ P take(int stage) {
+        if constexpr (!WIDE) {
+            return next;
+        } else {
+            P p;
+#pragma unroll
+            for (int i = 0; i < kParts; ++i)
+                *reinterpret_cast<uint4 *>(&p.v[i * P::kVec]) =
+                    slots[(stage * kParts + i) * THREADS];
+            return p;
+        }
+    }
+};
+
 // An element of weight or bias, whose type may be x's or FP32.
 __device__ __forceinline__ float param(const void *p, int dtype, int c, float none) {
     if (!p) return none;
@@ -68,6 +111,10 @@ __device__ __forceinline__ float param(const void *p, int dtype, int c, float no
     if (dtype == NORM_BF16) return as_f32(((const __nv_bfloat16 *)p)[c]);
     return as_f32(((const __half *)p)[c]);
 }
+
+// Rows that a group takes at once: two where their sums cross warps, each covering the other's
+// exchange.
+template <bool WIDE, int TPR> constexpr int at_once() { return WIDE && TPR >= 64 ? 2 : 1; }
 
 template <int TPR> constexpr int threads() { return TPR < 256 ? 256 : TPR; }
 

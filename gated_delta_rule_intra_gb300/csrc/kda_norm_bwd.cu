@@ -12,12 +12,22 @@ namespace kda {
 namespace norm {
 namespace {
 
+// CTAs a multiprocessor, and rows on their way to a thread (the widest FP32 rows: 192 KB of
+// slots).  One row at a time: two at once, as in the forward, spill.
+template <bool WIDE, int TPR> constexpr int per_sm() { return TPR > 256 ? 1 : WIDE ? 3 : 2; }
+template <typename T, bool WIDE, int TPR> constexpr int depth() {
+    return !WIDE ? 2 : sizeof(T) == 4 && TPR == 1024 ? 3 : 4;
+}
+
 template <typename T, bool WIDE, int TPR>
-__global__ void __launch_bounds__(threads<TPR>()) kda_layer_norm_bwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(threads<TPR>(), per_sm<WIDE, TPR>()) kda_layer_norm_bwd_kernel(const NormArgs a) {
     constexpr int kThreads = threads<TPR>(), kGroups = kThreads / TPR;
     constexpr int kWarps = TPR > 32 ? TPR / 32 : 1;
     using P = Part<T, WIDE, TPR>;
+    constexpr int kDepth = depth<T, WIDE, TPR>();
+    using Rows = Stream<T, WIDE, TPR, kThreads, kDepth>;
     __shared__ float2 red[2][kGroups][kWarps];
+    extern __shared__ __align__(16) char slots[];
     __shared__ float sums[kGroups > 1 ? kGroups : 1][kGroups > 1 ? TPR * E : 1];
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR, lane = threadIdx.x & 31;
     const int w = t / 32;
@@ -30,19 +40,29 @@ __global__ void __launch_bounds__(threads<TPR>()) kda_layer_norm_bwd_kernel(cons
     const float inv_n = 1.f / (float)a.width;
     const long long step = (long long)gridDim.x * kGroups;
     long long row0 = (long long)blockIdx.x * kGroups;
-    P x, dy, nx, ndy;
-    float mean = 0.f, rstd = 0.f, nmean = 0.f, nrstd = 0.f;
-    auto fetch = [&](P &px, P &pdy, float &m, float &r, long long row) {
+    Rows xs(slots), dys(slots + Rows::kBytes);
+    auto fetch = [&](int stage, long long row) {
         const bool ok = row < a.rows;
-        px.load((const T *)a.x + row * a.x_stride, t, a.width, ok);
-        pdy.load((const T *)a.dy + row * a.dy_stride, t, a.width, ok);
-        m = ok ? a.mean[row] : 0.f;
-        r = ok ? a.rstd[row] : 0.f;
+        const long long at = ok ? row : 0;
+        xs.fetch(stage, (const T *)a.x + at * a.x_stride, t, a.width, ok);
+        dys.fetch(stage, (const T *)a.dy + at * a.dy_stride, t, a.width, ok);
+        cp_async_commit();
     };
-    fetch(x, dy, mean, rstd, row0 + grp);
-    for (int it = 0; row0 < a.rows; row0 += step, it ^= 1) {
+    auto stats = [&](long long row) {
+        return row < a.rows ? make_float2(a.mean[row], a.rstd[row]) : make_float2(0.f, 0.f);
+    };
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) fetch(i, row0 + i * step + grp);
+    float2 st = stats(row0 + grp), st1 = stats(row0 + step + grp);
+    for (int it = 0, stage = 0; row0 < a.rows;
+         row0 += step, it ^= 1, stage = stage + 1 < kDepth ? stage + 1 : 0) {
         const long long row = row0 + grp;
-        fetch(nx, ndy, nmean, nrstd, row + step);
+        cp_async_wait_newest<kDepth - 2>();
+        const P x = xs.take(stage), dy = dys.take(stage);
+        fetch(stage > 0 ? stage - 1 : kDepth - 1, row + (kDepth - 1) * step);
+        const float mean = st.x, rstd = st.y;
+        st = st1;
+        st1 = stats(row + 2 * step);
         float s1 = 0.f, s2 = 0.f, xh[E], h[E];
 #pragma unroll
         for (int i = 0; i < E; ++i) {
@@ -72,11 +92,8 @@ __global__ void __launch_bounds__(threads<TPR>()) kda_layer_norm_bwd_kernel(cons
 #pragma unroll
         for (int i = 0; i < E; ++i) out.v[i] = from_f32<T>(rstd * (h[i] - s1 - xh[i] * s2));
         out.store((T *)a.dx + row * a.dx_stride, t, a.width, row < a.rows);
-        x = nx;
-        dy = ndy;
-        mean = nmean;
-        rstd = nrstd;
     }
+    cp_async_wait_newest<0>();
     if (!a.dweight) return;
     float *to = a.partial + (size_t)blockIdx.x * 2 * a.width;
     if constexpr (kGroups == 1) {
@@ -176,7 +193,7 @@ int ctas(long long rows, int width) {
     const int tpr = group_of(width);
     if (!tpr) return (int)(rows < 64 ? rows : 64);  // slices of the column pass
     const int threads = tpr < 256 ? 256 : tpr, groups = threads / tpr;
-    const long long want = (rows + groups - 1) / groups, most = (long long)kSMs * (1024 / threads);
+    const long long want = (rows + groups - 1) / groups, most = (long long)kSMs * (tpr <= 256 ? 3 : 1024 / threads);
     return (int)(want < most ? want : most);
 }
 
@@ -189,9 +206,16 @@ cudaError_t sum_partials(const NormArgs &a, int n, cudaStream_t stream) {
 
 template <typename T, bool WIDE, int TPR>
 cudaError_t launch(const NormArgs &a, cudaStream_t stream) {
+    constexpr int kBytes = 2 * Stream<T, WIDE, TPR, threads<TPR>(), depth<T, WIDE, TPR>()>::kBytes;
+    static volatile int done[kMaxDev];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && kBytes > 40 * 1024)  // with the static part, over the default 48 KB
+        e = smem_limit_once(kda_layer_norm_bwd_kernel<T, WIDE, TPR>, kBytes, dev, done);
+    if (e != cudaSuccess) return e;
     const int n = ctas(a.rows, a.width);
-    kda_layer_norm_bwd_kernel<T, WIDE, TPR><<<n, threads<TPR>(), 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    kda_layer_norm_bwd_kernel<T, WIDE, TPR><<<n, threads<TPR>(), kBytes, stream>>>(a);
+    e = cudaGetLastError();
     return e != cudaSuccess ? e : sum_partials(a, n, stream);
 }
 

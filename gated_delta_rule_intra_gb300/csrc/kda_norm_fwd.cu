@@ -6,7 +6,7 @@
 // large sums), in FP32.  Rows of more than 32 threads: each warp finds its own mean and
 // squared differences, and one exchange through shared memory joins them,
 //   mean = sum n_w mean_w / n,   M2 = sum M2_w + sum n_w (mean_w - mean)^2.
-// The next row is fetched before the current one's reduction.
+// The next rows are on their way meanwhile (Stream).
 #include "kda_norm.cuh"
 
 namespace kda {
@@ -18,7 +18,10 @@ __global__ void __launch_bounds__(threads<TPR>()) kda_layer_norm_fwd_kernel(cons
     constexpr int kThreads = threads<TPR>(), kGroups = kThreads / TPR;
     constexpr int kWarps = TPR > 32 ? TPR / 32 : 1;
     using P = Part<T, WIDE, TPR>;
-    __shared__ float2 red[2][kGroups][kWarps];
+    constexpr int R = at_once<WIDE, TPR>(), kDepth = WIDE ? 4 / R + 1 : 2;
+    using Rows = Stream<T, WIDE, TPR, kThreads, kDepth * R>;
+    __shared__ float2 red[2][kGroups][R][kWarps];
+    extern __shared__ __align__(16) char slots[];
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR, lane = threadIdx.x & 31;
     const int w = t / 32;
     float wt[E], bs[E];
@@ -39,44 +42,77 @@ __global__ void __launch_bounds__(threads<TPR>()) kda_layer_norm_fwd_kernel(cons
     const float inv_n = 1.f / (float)a.width;
     const float inv_w = TPR > 32 ? 1.f / (float)max(held(w), 1) : inv_n;
     const float n_lane = TPR > 32 ? (lane < kWarps ? (float)held(lane) : 0.f) : 0.f;
-    const long long step = (long long)gridDim.x * kGroups;
-    long long row0 = (long long)blockIdx.x * kGroups;
-    P cur, next;
-    cur.load((const T *)a.x + (row0 + grp) * a.x_stride, t, a.width, row0 + grp < a.rows);
-    for (int it = 0; row0 < a.rows; row0 += step, it ^= 1) {
-        const long long row = row0 + grp;
-        const bool ok = row < a.rows, more = row + step < a.rows;
-        next.load((const T *)a.x + (row + step) * a.x_stride, t, a.width, more);
-        float x[E], s = 0.f;
+    const long long step = (long long)gridDim.x * kGroups * R;
+    long long row0 = (long long)blockIdx.x * kGroups * R;
+    Rows rows(slots);
+    auto fetch = [&](int stage, long long first) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) s += x[i] = as_f32(cur.v[i]);
+        for (int r = 0; r < R; ++r) {
+            const long long row = first + r * kGroups + grp;
+            const bool ok = row < a.rows;
+            rows.fetch(stage * R + r, (const T *)a.x + (ok ? row : 0) * a.x_stride, t, a.width, ok);
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) fetch(i, row0 + i * step);
+    for (int it = 0, stage = 0; row0 < a.rows;
+         row0 += step, it ^= 1, stage = stage + 1 < kDepth ? stage + 1 : 0) {
         constexpr int kLanes = TPR < 32 ? TPR : 32;
-        float mean = lanes_sum<kLanes>(s) * inv_w, m2 = 0.f;
+        cp_async_wait_newest<kDepth - 2>();
+        float x[R][E], mean[R], m2[R];
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const float d = x[i] - mean;
-            if (P::col(t, i) < a.width) m2 += d * d;
+        for (int r = 0; r < R; ++r) {
+            const P cur = rows.take(stage * R + r);
+            mean[r] = 0.f;
+#pragma unroll
+            for (int i = 0; i < E; ++i) mean[r] += x[r][i] = as_f32(cur.v[i]);
         }
-        m2 = lanes_sum<kLanes>(m2);
+        fetch(stage > 0 ? stage - 1 : kDepth - 1, row0 + (kDepth - 1) * step);
+#pragma unroll
+        for (int r = 0; r < R; ++r) mean[r] = lanes_sum<kLanes>(mean[r]) * inv_w;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m2[r] = 0.f;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const float d = x[r][i] - mean[r];
+                if (P::col(t, i) < a.width) m2[r] += d * d;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) m2[r] = lanes_sum<kLanes>(m2[r]);
         if (TPR > 32) {
-            if (lane == 0) red[it][grp][w] = make_float2(mean, m2);
-            group_sync<TPR>(grp);
-            const float2 p = lane < kWarps ? red[it][grp][lane] : make_float2(0.f, 0.f);
-            mean = lanes_sum<32>(p.x * n_lane) * inv_n;
-            const float d = p.x - mean;
-            m2 = lanes_sum<32>(p.y + n_lane * d * d);
-        }
-        const float rstd = rsqrtf(m2 * inv_n + a.eps);
-        P out;
 #pragma unroll
-        for (int i = 0; i < E; ++i) out.v[i] = from_f32<T>((x[i] - mean) * rstd * wt[i] + bs[i]);
-        out.store((T *)a.y + row * a.y_stride, t, a.width, ok);
-        if (ok && t == 0) {
-            if (a.mean) a.mean[row] = mean;
-            if (a.rstd) a.rstd[row] = rstd;
+            for (int r = 0; r < R; ++r)
+                if (lane == 0) red[it][grp][r][w] = make_float2(mean[r], m2[r]);
+            group_sync<TPR>(grp);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float2 p =
+                    lane < kWarps ? red[it][grp][r][lane] : make_float2(0.f, 0.f);
+                mean[r] = lanes_sum<32>(p.x * n_lane) * inv_n;
+                const float d = p.x - mean[r];
+                m2[r] = lanes_sum<32>(p.y + n_lane * d * d);
+            }
         }
-        cur = next;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const long long row = row0 + r * kGroups + grp;
+            const bool ok = row < a.rows;
+            const float rstd = rsqrtf(m2[r] * inv_n + a.eps);
+            P out;
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                out.v[i] = from_f32<T>((x[r][i] - mean[r]) * rstd * wt[i] + bs[i]);
+            out.store((T *)a.y + row * a.y_stride, t, a.width, ok);
+            if (ok && t == 0) {
+                if (a.mean) a.mean[row] = mean[r];
+                if (a.rstd) a.rstd[row] = rstd;
+            }
+        }
     }
+    cp_async_wait_newest<0>();
 }
 
 // Rows that no CTA's registers hold: one CTA a row, three passes over it (from L2).
@@ -114,10 +150,18 @@ template <typename T> __global__ void __launch_bounds__(1024) kda_layer_norm_fwd
 
 template <typename T, bool WIDE, int TPR>
 cudaError_t launch(const NormArgs &a, cudaStream_t stream) {
-    constexpr int kThreads = threads<TPR>(), kGroups = kThreads / TPR;
-    const long long want = (a.rows + kGroups - 1) / kGroups, most = kSMs * (2048 / kThreads);
+    constexpr int R = at_once<WIDE, TPR>();
+    constexpr int kThreads = threads<TPR>(), kGroups = kThreads / TPR * R;
+    constexpr int kBytes = Stream<T, WIDE, TPR, kThreads, (4 / R + 1) * R>::kBytes;
+    static volatile int done[kMaxDev];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && kBytes > 40 * 1024)  // with the static part, over the default 48 KB
+        e = smem_limit_once(kda_layer_norm_fwd_kernel<T, WIDE, TPR>, kBytes, dev, done);
+    if (e != cudaSuccess) return e;
+    const long long want = (a.rows + kGroups - 1) / kGroups, most = kSMs * (1024 / kThreads);
     kda_layer_norm_fwd_kernel<T, WIDE, TPR>
-        <<<(unsigned)(want < most ? want : most), kThreads, 0, stream>>>(a);
+        <<<(unsigned)(want < most ? want : most), kThreads, kBytes, stream>>>(a);
     return cudaGetLastError();
 }
 

@@ -4,13 +4,14 @@ from __future__ import annotations
 
 import torch
 
-from ._common import DTYPES, F32, check, ptr, run, takes_stream
+from ._common import DTYPES, F32, check, library, run, takes_stream
 
 
-def _rows(name, t, like):
-    """(rows, width, stride between rows) of a tensor whose leading dimensions are one run of
-    rows; the last dimension is contiguous."""
-    if t.device != like.device or t.dtype != like.dtype or t.shape != like.shape:
+def _stride(name, t, like):
+    """Elements between the rows of a tensor like `like` whose last dimension is contiguous and
+    whose leading dimensions are one evenly spaced run of rows."""
+    if t is not like and (t.dtype is not like.dtype or t.shape != like.shape
+                          or t.get_device() != like.get_device()):
         raise ValueError(f"{name} must be {like.dtype} {tuple(like.shape)} on {like.device}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     width = t.shape[-1]
@@ -34,26 +35,30 @@ def _rows(name, t, like):
     return width if step is None else step
 
 
-def _params(x, weight, bias):
-    wdtype = x.dtype
-    for t in (weight, bias):
-        if t is not None:
-            wdtype = t.dtype
-    if wdtype not in (x.dtype, F32):
-        raise ValueError(f"weight and bias must be {x.dtype} or float32, got {wdtype}")
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            check(name, t, (x.shape[-1],), wdtype, x.device)
-    return DTYPES[wdtype]
-
-
-def _input(fn, x):
-    if x.device.type != "cuda":
+def _input(fn, x, weight, bias):
+    """Checks of x and the parameters; (device index, width, rows, the parameters' type)."""
+    dev, shape = x.get_device(), x.shape
+    if dev < 0:
         raise ValueError(f"{fn} needs CUDA tensors (no CPU path exists)")
     if x.dtype not in DTYPES:
         raise ValueError(f"x must be bf16, fp16 or fp32, got {x.dtype}")
-    if x.dim() < 1 or x.shape[-1] == 0:
+    if not shape or shape[-1] == 0:
         raise ValueError("x needs a last dimension of at least 1")
+    width, wdtype = shape[-1], x.dtype
+    for t in (weight, bias):
+        if t is not None:
+            wdtype = t.dtype
+    if wdtype is not x.dtype and wdtype is not F32:
+        raise ValueError(f"weight and bias must be {x.dtype} or float32, got {wdtype}")
+    if weight is not None:
+        check("weight", weight, (width,), wdtype, dev)
+    if bias is not None:
+        check("bias", bias, (width,), wdtype, dev)
+    return dev, width, x.numel() // width, DTYPES[wdtype]
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 @takes_stream
@@ -64,16 +69,16 @@ def kda_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None):
     spaced (a column slice of a wider tensor will do).  weight and bias [width] in x's dtype or
     fp32 (None: ones, zeros).  y has x's dtype; mean and rstd [rows] are fp32.
     """
-    _input("kda_layer_norm_fwd", x)
-    wdtype = _params(x, weight, bias)
-    xs, width, dev = _rows("x", x, x), x.shape[-1], x.device
+    dev, width, rows, wdtype = _input("kda_layer_norm_fwd", x, weight, bias)
+    xs = _stride("x", x, x)
     if y is None:
-        y, ys = torch.empty(x.shape, dtype=x.dtype, device=dev), width
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        ys = width
     else:
-        ys = _rows("y", y, x)
-    rows = x.numel() // width
-    mean, rstd = torch.empty((2, rows), dtype=F32, device=dev).unbind()
-    run("kda_layer_norm_fwd", dev, x.data_ptr(), ptr(weight), ptr(bias), y.data_ptr(),
+        ys = _stride("y", y, x)
+    mean = torch.empty(rows, dtype=F32, device=x.device)
+    rstd = torch.empty(rows, dtype=F32, device=x.device)
+    run("kda_layer_norm_fwd", dev, x.data_ptr(), _ptr(weight), _ptr(bias), y.data_ptr(),
         mean.data_ptr(), rstd.data_ptr(), rows, width, eps, DTYPES[x.dtype], wdtype, xs, ys)
     return y, mean, rstd
 
@@ -83,24 +88,23 @@ def kda_layer_norm_bwd(dy, x, weight, mean, rstd, *, dx=None, param_grads=True):
     """Gradients of ``kda_layer_norm_fwd``.  Returns (dx, dweight, dbias): dx in x's dtype,
     dweight and dbias [width] fp32 summed over the rows in a fixed order (None unless
     ``param_grads``)."""
-    from . import load_library
-    _input("kda_layer_norm_bwd", x)
-    wdtype = _params(x, weight, None)
-    xs, dys, width, dev = _rows("x", x, x), _rows("dy", dy, x), x.shape[-1], x.device
-    rows = x.numel() // width
+    dev, width, rows, wdtype = _input("kda_layer_norm_bwd", x, weight, None)
+    xs, dys = _stride("x", x, x), _stride("dy", dy, x)
     check("mean", mean, (rows,), F32, dev)
     check("rstd", rstd, (rows,), F32, dev)
     if dx is None:
-        dx, dxs = torch.empty(x.shape, dtype=x.dtype, device=dev), width
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dxs = width
     else:
-        dxs = _rows("dx", dx, x)
+        dxs = _stride("dx", dx, x)
     dw = db = ws = None
     need = 0
     if param_grads:
-        dw, db = torch.empty((2, width), dtype=F32, device=dev).unbind()
-        need = load_library().kda_layer_norm_bwd_workspace_bytes(rows, width)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    run("kda_layer_norm_bwd", dev, dy.data_ptr(), x.data_ptr(), ptr(weight), mean.data_ptr(),
-        rstd.data_ptr(), dx.data_ptr(), ptr(dw), ptr(db), rows, width, DTYPES[x.dtype], wdtype,
-        dys, xs, dxs, ptr(ws), need)
+        dw = torch.empty(width, dtype=F32, device=x.device)
+        db = torch.empty(width, dtype=F32, device=x.device)
+        need = library().kda_layer_norm_bwd_workspace_bytes(rows, width)
+        ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+    run("kda_layer_norm_bwd", dev, dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(),
+        rstd.data_ptr(), dx.data_ptr(), _ptr(dw), _ptr(db), rows, width, DTYPES[x.dtype], wdtype,
+        dys, xs, dxs, _ptr(ws), need)
     return dx, dw, db

@@ -13,7 +13,7 @@ import ctypes
 
 import torch
 
-from ._common import DTYPES16, F32, K, check, ptr, run, takes_stream
+from ._common import DTYPES16, F32, K, check, fits, library, run, takes_stream
 
 
 class ChunkFwdOpts(ctypes.Structure):
@@ -39,34 +39,33 @@ class StepOpts(ctypes.Structure):
                 ("state_indices", ctypes.c_void_p), ("num_states", ctypes.c_int)]
 
 
-def _lib():
-    from . import load_library
-    return load_library()
-
-
 def _inputs(fn, q, k, v, gate, beta, lead):
-    """Checks of the five inputs; (H, HV)."""
-    if q.device.type != "cuda":
+    """Checks of the five inputs; (H, HV, device index)."""
+    shape, vshape, dt, dev = q.shape, v.shape, q.dtype, q.get_device()
+    if (len(shape) == lead + 2 == len(vshape) and shape[-1] == K and dt in DTYPES16 and dev >= 0
+            and shape[lead] and vshape[lead] % shape[lead] == 0
+            and fits(q, shape, dt, dev) and fits(k, shape, dt, dev)
+            and fits(v, (*shape[:lead], vshape[lead], K), dt, dev) and fits(gate, vshape, F32, dev)
+            and fits(beta, vshape[:-1], F32, dev)):
+        return shape[lead], vshape[lead], dev
+    if dev < 0:
         raise ValueError(f"{fn} needs CUDA tensors (no CPU path exists)")
-    if q.dtype not in DTYPES16:
-        raise ValueError(f"q/k/v dtype must be bf16 or fp16, got {q.dtype}")
-    if q.dim() != lead + 2 or q.shape[-1] != K:
-        raise ValueError(f"q must be [{'N' if lead == 1 else 'B, T'}, H, {K}], got "
-                         f"{tuple(q.shape)}")
-    if v.dim() != lead + 2:
-        raise ValueError(f"v must be [{'N' if lead == 1 else 'B, T'}, HV, {K}], got "
-                         f"{tuple(v.shape)}")
-    H, HV, dev = q.shape[lead], v.shape[lead], q.device
+    if dt not in DTYPES16:
+        raise ValueError(f"q/k/v dtype must be bf16 or fp16, got {dt}")
+    rows = "N" if lead == 1 else "B, T"
+    if len(shape) != lead + 2 or shape[-1] != K:
+        raise ValueError(f"q must be [{rows}, H, {K}], got {tuple(shape)}")
+    if len(vshape) != lead + 2:
+        raise ValueError(f"v must be [{rows}, HV, {K}], got {tuple(vshape)}")
+    H, HV = shape[lead], vshape[lead]
     if H == 0 or HV % H:
         raise ValueError(f"v's {HV} heads must be a multiple of q's {H}")
-    rows = q.shape[:lead]
-    check("k", k, q.shape, q.dtype, dev)
-    check("v", v, (*rows, HV, K), q.dtype, dev)
-    check("gate", gate, v.shape, F32, dev)
-    check("beta", beta, (*rows, HV), F32, dev)
-    if not q.is_contiguous():
-        raise ValueError("q must be contiguous")
-    return H, HV
+    check("q", q, shape, dt, dev)
+    check("k", k, shape, dt, dev)
+    check("v", v, (*shape[:lead], HV, K), dt, dev)
+    check("gate", gate, vshape, F32, dev)
+    check("beta", beta, vshape[:-1], F32, dev)
+    raise AssertionError("unreachable")
 
 
 def _scale(scale):
@@ -102,30 +101,30 @@ def kda_chunk_fwd(q, k, v, gate, beta, scale=None, initial_state=None, *,
     value head), None unless ``save``.  ``cu_seqlens`` (int32 [N + 1] on the device, B = 1)
     packs N sequences along T; it is read on the device only.
     """
-    H, HV = _inputs("kda_chunk_fwd", q, k, v, gate, beta, 2)
-    B, T, dev = q.shape[0], q.shape[1], q.device
+    H, HV, dev = _inputs("kda_chunk_fwd", q, k, v, gate, beta, 2)
+    B, T = q.shape[:2]
     N = _seqs(cu_seqlens, B, dev)
     if o is None:
         o = torch.zeros_like(v) if N else torch.empty_like(v)
     else:
         check("o", o, v.shape, v.dtype, dev)
-    states = (N or B, HV, K, K)
-    lib = _lib()
-    op = ChunkFwdOpts(HV=HV, scale=_scale(scale), num_seqs=N, cu_seqlens=ptr(cu_seqlens))
+    op = ChunkFwdOpts(HV=HV, scale=_scale(scale))
+    if N:
+        op.num_seqs, op.cu_seqlens = N, cu_seqlens.data_ptr()
     if initial_state is not None:
-        check("initial_state", initial_state, states, F32, dev)
+        check("initial_state", initial_state, (N or B, HV, K, K), F32, dev)
         op.initial_state = initial_state.data_ptr()
     final = saved = None
     if output_final_state:
-        final = torch.empty(states, dtype=F32, device=dev)
+        final = torch.empty((N or B, HV, K, K), dtype=F32, device=q.device)
         op.final_state = final.data_ptr()
     if save:
-        saved = torch.empty(lib.kda_chunk_saved_bytes(B, T, HV, N), dtype=torch.uint8, device=dev)
-        op.saved, op.saved_bytes = saved.data_ptr(), saved.numel()
-    if B == 0:
-        return o, final, saved
-    run("kda_chunk_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(),
-        beta.data_ptr(), o.data_ptr(), B, T, H, DTYPES16[q.dtype], ctypes.addressof(op))
+        size = library().kda_chunk_saved_bytes(B, T, HV, N)
+        saved = torch.empty(size, dtype=torch.uint8, device=q.device)
+        op.saved, op.saved_bytes = saved.data_ptr(), size
+    if B:
+        run("kda_chunk_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(),
+            beta.data_ptr(), o.data_ptr(), B, T, H, DTYPES16[q.dtype], ctypes.addressof(op))
     return o, final, saved
 
 
@@ -141,42 +140,39 @@ def kda_chunk_bwd(q, k, v, gate, beta, do, saved, scale=None, d_final_state=None
     final state's shape) defaults to zeros; d_initial_state (fp32) is None unless
     ``output_d_initial_state``.  Deterministic.
     """
-    H, HV = _inputs("kda_chunk_bwd", q, k, v, gate, beta, 2)
-    B, T, dev, dt = q.shape[0], q.shape[1], q.device, q.dtype
+    H, HV, dev = _inputs("kda_chunk_bwd", q, k, v, gate, beta, 2)
+    B, T, dt = q.shape[0], q.shape[1], q.dtype
     N = _seqs(cu_seqlens, B, dev)
     check("do", do, v.shape, dt, dev)
-    lib = _lib()
+    lib = library()
     saved_bytes = lib.kda_chunk_saved_bytes(B, T, HV, N)
     check("saved", saved, (saved_bytes,), torch.uint8, dev)
     new = torch.zeros_like if N else torch.empty_like
     out = []
-    for name, t, like, shape in (("dq", dq, q, q.shape), ("dk", dk, k, q.shape),
-                                 ("dv", dv, v, v.shape), ("dgate", dgate, v, v.shape),
-                                 ("dbeta", dbeta, None, beta.shape)):
-        if t is not None:
-            check(name, t, shape, dt, dev)
-        elif like is not None:
-            t = new(like)
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v), ("dgate", dgate, v),
+                          ("dbeta", dbeta, beta)):
+        if t is None:
+            t = new(like) if like is not beta else new(like, dtype=dt)
         else:
-            t = new(beta, dtype=dt)
+            check(name, t, like.shape, dt, dev)
         out.append(t)
-    states = (N or B, HV, K, K)
-    op = ChunkBwdOpts(HV=HV, scale=_scale(scale), num_seqs=N, cu_seqlens=ptr(cu_seqlens),
-                      saved=saved.data_ptr(), saved_bytes=saved_bytes)
+    op = ChunkBwdOpts(HV=HV, scale=_scale(scale), saved=saved.data_ptr(), saved_bytes=saved_bytes)
+    if N:
+        op.num_seqs, op.cu_seqlens = N, cu_seqlens.data_ptr()
     if d_final_state is not None:
-        check("d_final_state", d_final_state, states, F32, dev)
+        check("d_final_state", d_final_state, (N or B, HV, K, K), F32, dev)
         op.d_final_state = d_final_state.data_ptr()
     d_initial = None
     if output_d_initial_state:
-        d_initial = torch.empty(states, dtype=F32, device=dev)
+        d_initial = torch.empty((N or B, HV, K, K), dtype=F32, device=q.device)
         op.d_initial_state = d_initial.data_ptr()
-    if B == 0:
-        return (*out, d_initial)
-    work = lib.kda_chunk_bwd_workspace_bytes(B, T, H, HV, N)
-    ws = torch.empty(work, dtype=torch.uint8, device=dev)
-    op.workspace, op.workspace_bytes = ws.data_ptr(), work
-    run("kda_chunk_bwd", dev, q.data_ptr(), k.data_ptr(), gate.data_ptr(), beta.data_ptr(),
-        do.data_ptr(), *(t.data_ptr() for t in out), B, T, H, DTYPES16[dt], ctypes.addressof(op))
+    if B:
+        work = lib.kda_chunk_bwd_workspace_bytes(B, T, H, HV, N)
+        ws = torch.empty(work, dtype=torch.uint8, device=q.device)
+        op.workspace, op.workspace_bytes = ws.data_ptr(), work
+        run("kda_chunk_bwd", dev, q.data_ptr(), k.data_ptr(), gate.data_ptr(), beta.data_ptr(),
+            do.data_ptr(), *[t.data_ptr() for t in out], B, T, H, DTYPES16[dt],
+            ctypes.addressof(op))
     return (*out, d_initial)
 
 
@@ -189,10 +185,10 @@ def kda_step(q, k, v, gate, beta, state, scale=None, *, state_indices=None, o=No
     [N] on the device), [num_states, ...], request n's being state[state_indices[n]].  An index
     outside the states marks a padding row (its o is zero); no two rows may name one state.
     """
-    H, HV = _inputs("kda_step", q, k, v, gate, beta, 1)
-    N, dev = q.shape[0], q.device
-    check("state", state, (N if state_indices is None else state.shape[0], HV, K, K), F32, dev)
-    op = StepOpts(HV=HV, scale=_scale(scale), num_states=state.shape[0])
+    H, HV, dev = _inputs("kda_step", q, k, v, gate, beta, 1)
+    N, states = q.shape[0], state.shape[0]
+    check("state", state, (N if state_indices is None else states, HV, K, K), F32, dev)
+    op = StepOpts(HV=HV, scale=_scale(scale), num_states=states)
     if state_indices is not None:
         check("state_indices", state_indices, (N,), torch.int32, dev)
         op.state_indices = state_indices.data_ptr()
