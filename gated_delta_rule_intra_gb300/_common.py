@@ -75,9 +75,9 @@ def declare(lib):
     vp, i, ll, z, f = (ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t,
                        ctypes.c_float)
     for name, res, args in (
-            ("kda_chunk_saved_bytes", z, [i] * 4),
+            ("kda_chunk_saved_bytes", z, [i] * 6),
             ("kda_chunk_fwd", i, [vp] * 6 + [i] * 4 + [vp, vp]),
-            ("kda_chunk_bwd_workspace_bytes", z, [i] * 5),
+            ("kda_chunk_bwd_workspace_bytes", z, [i] * 6 + [z]),
             ("kda_chunk_bwd", i, [vp] * 10 + [i] * 4 + [vp, vp]),
             ("kda_step", i, [vp] * 7 + [i] * 3 + [vp, vp]),
             ("kda_layer_norm_fwd", i, [vp] * 6 + [ll, i, f, i, i, ll, ll, vp]),

@@ -150,6 +150,12 @@ __device__ __forceinline__ uint32_t plane_off(int r, int c) {
     return (uint32_t)(r * 256 + ((c ^ (r & 7)) << 4));
 }
 
+// A value that is the same in all lanes, said so that the compiler knows it too: branches on
+// it are then warp-uniform.  (Behind a branch that might diverge every ldmatrix, mma and shuffle
+// waits for the whole warp and nothing is scheduled across it: two to four times the time.)
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ int warp_index() { return uniform((int)(threadIdx.x >> 5)); }
+
 // A sequence: its rows in the [rows, heads, 128] tensors and its slots of 64 tokens.
 struct Seq {
     long long row0;  // first token
@@ -166,9 +172,9 @@ __device__ __forceinline__ Seq seq_of(int n, int T, const int *cu) {
         int a = cu[n], b = cu[n + 1];
         a = a < 0 ? 0 : a > T ? T : a;
         b = b < a ? a : b > T ? T : b;
-        s.row0 = a;
-        s.len = b - a;
-        s.slot0 = a / BT + n;
+        s.row0 = uniform(a);
+        s.len = uniform(b - a);
+        s.slot0 = uniform(a / BT + n);
     } else {
         s.row0 = (long long)n * T;
         s.len = T;

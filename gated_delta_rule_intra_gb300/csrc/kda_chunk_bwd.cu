@@ -25,6 +25,10 @@
 #include "kda_ops.h"
 
 namespace kda {
+namespace fast {
+cudaError_t launch_bwd(const ChunkBwdArgs &a, int dev, cudaStream_t stream);  // kda_fast_bwd.cu
+}  // namespace fast
+
 namespace chunk {
 
 cudaError_t launch_bwd_state(const ChunkBwdArgs &a, int dev, cudaStream_t stream);
@@ -163,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
     extern __shared__ __align__(128) char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     constexpr bool kLo = !In<T16>::exact;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const int gr = lane >> 2, tc2 = (lane & 3) * 2, m = lane >> 3;
     const int c0 = warp * 16;  // this warp's channels
     const uint32_t se = tc::smem_u32(sm.e), sy = tc::smem_u32(sm.y), so = tc::smem_u32(sm.dout);
@@ -582,17 +586,22 @@ __global__ void __launch_bounds__(256) kda_chunk_bwd_heads_kernel(const ChunkBwd
 
 template <typename T16>
 cudaError_t launch(const ChunkBwdArgs &a, int dev, cudaStream_t stream) {
-    cudaError_t e = launch_bwd_state(a, dev, stream);
-    if (e != cudaSuccess) return e;
-    const long long units = (long long)a.slots * a.HV;
-    if (units == 0) return cudaSuccess;
-    static volatile int done[kMaxDev];
-    e = smem_limit_once(kda_chunk_bwd_kernel<T16>, (int)sizeof(Smem), dev, done);
-    if (e != cudaSuccess) return e;
-    kda_chunk_bwd_kernel<T16><<<(unsigned)(units < kSMs ? units : kSMs), kThreads, sizeof(Smem),
-                                stream>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || !a.dq_hv) return e;
+    cudaError_t e;
+    if (a.fast) {
+        e = fast::launch_bwd(a, dev, stream);
+    } else {
+        e = launch_bwd_state(a, dev, stream);
+        if (e != cudaSuccess) return e;
+        const long long units = (long long)a.slots * a.HV;
+        if (units == 0) return cudaSuccess;
+        static volatile int done[kMaxDev];
+        e = smem_limit_once(kda_chunk_bwd_kernel<T16>, (int)sizeof(Smem), dev, done);
+        if (e != cudaSuccess) return e;
+        kda_chunk_bwd_kernel<T16><<<(unsigned)(units < kSMs ? units : kSMs), kThreads,
+                                    sizeof(Smem), stream>>>(a);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess || !a.dq_hv || a.slots == 0) return e;
     const size_t n = 2 * (a.rows_o / (a.HV / a.H)) * (D / 4);
     kda_chunk_bwd_heads_kernel<T16><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(a);
     return cudaGetLastError();

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(Roles<NC>::kThreads, 1)
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     constexpr int kSplit = 8 / NC;
     const int lane = threadIdx.x & 31;
-    const Roles<NC> role(threadIdx.x >> 5);
+    const Roles<NC> role(warp_index());
     const int unit = blockIdx.x / kSplit, dv0 = (blockIdx.x % kSplit) * NC * 16;
     const int n = unit / a.HV, hv = unit - n * a.HV, h = hv / (a.HV / a.H);
     const Seq sq = seq_of(n, a.T, a.cu_seqlens);

@@ -6,6 +6,10 @@
 #include "kda_ops.h"
 
 namespace kda {
+namespace fast {
+cudaError_t launch_fwd(const ChunkFwdArgs &a, int dev, cudaStream_t stream);  // kda_fast_fwd.cu
+}  // namespace fast
+
 namespace chunk {
 namespace {
 
@@ -344,7 +348,8 @@ __device__ __forceinline__ void consume(float (&S)[MT][16][4], float (&xq)[MT][2
         if (CAREFUL) mma_causal(xq[t], nb, tc::smem_u32(in.p), tc::smem_u32(in.p) + kTile, lane);
     }
     // S' = 2^g_l (S + (k 2^-g)^T n), or with strong gates 2^g_l S + (k 2^(g_l - g))^T n
-    if (CAREFUL && !in.from_start) {
+    const bool from_start = !CAREFUL || uniform(in.from_start);
+    if (CAREFUL && !from_start) {
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -371,7 +376,7 @@ __device__ __forceinline__ void consume(float (&S)[MT][16][4], float (&xq)[MT][2
 #pragma unroll
         for (int t = 0; t < MT; ++t) mma3(xq[t][0], xq[t][1], nh[t], nl[t], th, tlo);
     }
-    if (!CAREFUL || in.from_start) {
+    if (from_start) {
 #pragma unroll
         for (int jj = 0; jj < 8; ++jj)
 #pragma unroll
@@ -387,7 +392,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
     extern __shared__ __align__(128) char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int lane = threadIdx.x & 31;
-    const Roles<NW> role(threadIdx.x >> 5);
+    const Roles<NW> role(warp_index());
     const int unit = blockIdx.x / kSplit, dv0 = (blockIdx.x % kSplit) * kSlice;
     const int n = unit / a.HV, hv = unit - n * a.HV, h = hv / (a.HV / a.H);
     const Seq sq = seq_of(n, a.T, a.cu_seqlens);
@@ -435,7 +440,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
             Prepared &out = sm.prep[st];
             const float *beta = sm.beta[i % kRaw];
             bar_sync(BAR_PLANES + st, 2 * kHalf);
-            if (out.from_start) {
+            if (uniform(out.from_start)) {
                 scores(sm, out, beta, i & 1, w, lane);
             } else {
                 scores_strong<T16>(sm, sm.raw[i % kRaw], beta, out, i & 1, a.scale, w, lane);
@@ -502,7 +507,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
                 S, xq, e, in, v, beta, ckpt, dv0 / 16, cw * MT, lane);
         };
         const bool keep = SAVE && i % 4 == 0;
-        if (!in.careful) {
+        if (!uniform(in.careful)) {
             if (keep)
                 run(std::false_type{}, std::integral_constant<bool, SAVE>{});
             else
@@ -572,6 +577,7 @@ cudaError_t launch_chunk_fwd(const ChunkFwdArgs &a, cudaStream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (a.fast) return fast::launch_fwd(a, dev, stream);
     const bool save = a.ckpt != nullptr;
     if (a.fp16)
         return save ? chunk::launch_split<__half, true>(a, dev, stream)

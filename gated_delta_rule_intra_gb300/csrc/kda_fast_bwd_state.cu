@@ -1,0 +1,317 @@
+// Backward of the gated delta-rule recurrence for BF16 training, first pass (see kda_fast.cuh,
+// and kda_chunk_bwd_state.cu for what it computes): the state's gradient walks each
+// (sequence, value head) backwards in steps of 16 tokens.
+#include "kda_fast.cuh"
+#include "kda_ops.h"
+
+namespace kda {
+namespace fast {
+namespace {
+
+using chunk::bar_arrive;
+using chunk::bar_sync;
+using chunk::cp16z;
+using chunk::ldsm4;
+using chunk::ldsm4t;
+using chunk::plane_off;
+using chunk::Roles;
+using chunk::Seq;
+using tc::smem_u32;
+
+constexpr int kStages = 3, kRaw = kStages + 2;
+
+enum { BAR_PREP = 1, BAR_FULL = 3, BAR_EMPTY = 6 };  // PREP + group; FULL, EMPTY + stage
+
+struct __align__(128) Smem {
+    Planes stage[kStages];
+    RawStage raw[kRaw];
+    uint16_t dout[kRaw][C][D];  // rows of the CTA's dv slice, swizzled chunks
+    char tiles[kRaw][2 * kTall];
+    float beta[kRaw][C];
+};
+
+// Step i of the walk (the last step of the sequence first), tokens 16 * step on.
+template <int SLICE>
+__device__ __forceinline__ void load_step(Smem &sm, const ChunkBwdArgs &a, const Seq &sq, int h,
+                                          int hv, int dv0, int i, int step, int tid) {
+    const int slot = i % kRaw, c = tid & 15;
+    RawStage &raw = sm.raw[slot];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int r = (tid >> 4) + 8 * x, t = step * C + r;
+        const bool ok = t < sq.len;
+        const size_t tok = (size_t)sq.row0 + (ok ? t : 0);
+        const size_t iq = (tok * a.H + h) * D + c * 8, iv = (tok * a.HV + hv) * D;
+        cp16z(smem_u32(&raw.q[r][c * 8]), (const uint16_t *)a.q + iq, ok);
+        cp16z(smem_u32(&raw.k[r][c * 8]), (const uint16_t *)a.k + iq, ok);
+        cp16z(smem_u32(&raw.gate[r][c * 4]), a.gate + iv + c * 4, ok);
+        cp16z(smem_u32(&raw.gate[r][64 + c * 4]), a.gate + iv + 64 + c * 4, ok);
+        if (c < SLICE / 8)
+            cp16z(smem_u32(sm.dout[slot]) + plane_off(r, c),
+                  (const uint16_t *)a.dout + iv + dv0 + c * 8, ok);
+        if (c == 0) chunk::cp4z(smem_u32(&sm.beta[slot][r]), a.beta + tok * a.HV + hv, ok);
+    }
+    cp16z(smem_u32(sm.tiles[slot]) + tid * 16,
+          a.tiles + ((size_t)(sq.slot0 + step / 4) * a.HV + hv) * kTilesBytes +
+              (step % 4) * 2 * kTall + tid * 16,
+          true);
+}
+
+template <int NW, int MT>
+__global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
+    kda_fast_bwd_state_kernel(const ChunkBwdArgs a) {
+    constexpr int kSlice = 16 * NW * MT, kSplit = D / kSlice;
+    extern __shared__ __align__(128) char smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
+    const int lane = threadIdx.x & 31;
+    const Roles<NW> role(chunk::warp_index());
+    const int unit = blockIdx.x / kSplit, dv0 = (blockIdx.x % kSplit) * kSlice;
+    const int n = unit / a.HV, hv = unit - n * a.HV, h = hv / (a.HV / a.H);
+    const Seq sq = chunk::seq_of(n, a.T, a.cu_seqlens);
+    const int steps = (sq.len + BT - 1) / BT * (BT / C);
+
+    if (role.prep >= 0) {
+        if (MT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+        // two groups of four warps take the steps in turn
+        const int group = role.prep >> 2, tid = (role.prep & 3) * 32 + lane;
+        if (group < steps) load_step<kSlice>(sm, a, sq, h, hv, dv0, group, steps - 1 - group, tid);
+        cp_async_commit();
+        for (int i = group; i < steps; i += 2) {
+            const int st = i % kStages;
+            Planes &out = sm.stage[st];
+            // the consumers are done with this stage's previous step and its inputs, whose
+            // place the step after next takes
+            if (i >= kStages) bar_sync(BAR_EMPTY + st, kHalf + 32 * NW);
+            if (i + 2 < steps)
+                load_step<kSlice>(sm, a, sq, h, hv, dv0, i + 2, steps - 3 - i, tid);
+            cp_async_commit();
+            cp_async_wait_newest<1>();
+            bar_sync(BAR_PREP + group, kHalf);
+            prepare<false>(sm.raw[i % kRaw], out, nullptr, a.scale, tid);
+            if (tid < 32) {
+                const float bm =
+                    warp_max(lane < C ? fabsf(sm.beta[i % kRaw][lane]) : 0.f);
+                if (lane == 0) {
+                    out.bmax = bm;
+                    out.careful = !finite(bm);
+                }
+            }
+            bar_arrive(BAR_FULL + st, kHalf + 32 * NW);
+        }
+        cp_async_wait_all();
+        return;
+    }
+
+    if (role.consumer < 0) return;
+    if (MT > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+    const int tile0 = dv0 / 16 + role.consumer * MT;
+    const int gr = lane >> 2, tc2 = (lane & 3) * 2;
+    const int lrow = (lane & 7) + ((lane >> 4) & 1) * 8, lcol = (lane >> 3) & 1;
+    const int trow = lane & 15, tcol = lane >> 4;
+    Tile S[MT];
+    const size_t sbase = ((size_t)n * a.HV + hv) * D * D + (size_t)tc2 * D + tile0 * 16 + gr;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        S[t].clear();
+        if (a.d_final_state) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float *p = a.d_final_state + sbase + (size_t)8 * j * D + 16 * t;
+                S[t].s[j][0] = p[0];
+                S[t].s[j][1] = p[D];
+                S[t].s[j][2] = p[8];
+                S[t].s[j][3] = p[D + 8];
+            }
+            S[t].bound = 2.f * kLimit;
+        }
+    }
+    const size_t vrow = (size_t)a.HV * D;
+    uint16_t *dv_at = (uint16_t *)a.dv + (size_t)sq.row0 * vrow + (size_t)hv * D + tile0 * 16 + tc2;
+
+    for (int i = 0; i < steps; ++i) {
+        const int st = i % kStages, slot = i % kRaw, step = steps - 1 - i;
+        const size_t unit_at = (size_t)(sq.slot0 + step / 4) * a.HV + hv;
+        const bool keep = step % 4 == 3;
+        bar_sync(BAR_FULL + st, kHalf + 32 * NW);
+        const Planes &in = sm.stage[st];
+        const uint32_t kw = smem_u32(in.kw), qw = smem_u32(in.qw), kd = smem_u32(in.kd);
+        const float kmax = largest(in.kmax), qmax = a.scale * largest(in.qmax), bm = in.bmax;
+        bool careful = in.careful || !(kmax <= 16384.f) || !(qmax <= 16384.f);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+            if (chunk::uniform(S[t].bound > kLimit)) S[t].renew();
+        uint32_t th[4], tl[4], ph[4], pl[4];
+        load_tall(smem_u32(sm.tiles[slot]), lane, tl, th);
+        load_tall(smem_u32(sm.tiles[slot]) + kTall, lane, pl, ph);
+        const float2 b[2] = {*reinterpret_cast<const float2 *>(&sm.beta[slot][tc2]),
+                             *reinterpret_cast<const float2 *>(&sm.beta[slot][8 + tc2])};
+        uint32_t dor[MT][4];  // do^T, BF16 pairs of tokens
+        float om[MT], ds[MT][2][4] = {};
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            ldsm4t(dor[t], smem_u32(sm.dout[slot]) +
+                               plane_off(lrow, (role.consumer * MT + t) * 2 + lcol));
+            uint32_t m = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m = __vmaxu2(m, dor[t][j] & 0x7fff7fffu);
+            om[t] = __uint_as_float(
+                __reduce_max_sync(0xffffffffu, max(m << 16, m & 0xffff0000u)));
+        }
+        // dS' kd
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+            uint32_t kf[4];
+            ldsm4(kf, kd + plane_off(lrow, 2 * kk + lcol));
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const float(&x)[4] = S[t].s[2 * kk], (&y)[4] = S[t].s[2 * kk + 1];
+                const uint32_t af[4] = {pack_f16(x[0], x[1]), pack_f16(x[2], x[3]),
+                                        pack_f16(y[0], y[1]), pack_f16(y[2], y[3])};
+                mma_f16(ds[t][0], af, kf[0], kf[1]);
+                mma_f16(ds[t][1], af, kf[2], kf[3]);
+                if (keep)  // the operand is the checkpoint
+                    reinterpret_cast<uint4 *>(a.dckpt + unit_at * kCkptBytes)
+                        [((tile0 + t) * 8 + kk) * 32 + lane] =
+                            make_uint4(af[0], af[1], af[2], af[3]);
+            }
+        }
+        float y[MT][2][4] = {}, ym[MT], ckpt_scale[MT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            ckpt_scale[t] = S[t].saved_scale();
+            // dn^T = do^T P + dS'^T kd^T (do is exact in TF32), Y^T = dn^T T
+            float dn[2][4] = {};
+            const uint32_t o0[4] = {dor[t][0] << 16, dor[t][1] << 16, dor[t][0] & 0xffff0000u,
+                                    dor[t][1] & 0xffff0000u};
+            const uint32_t o1[4] = {dor[t][2] << 16, dor[t][3] << 16, dor[t][2] & 0xffff0000u,
+                                    dor[t][3] & 0xffff0000u};
+            mma_tall(dn[0], dn[1], o0, o1, pl, ph);
+            uint32_t x0[4], x1[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int p = 0; p < 4; ++p) dn[j][p] = fmaf(ds[t][j][p], S[t].inv, dn[j][p]);
+            tf_frag(dn[0], x0);
+            tf_frag(dn[1], x1);
+            mma_tall(y[t][0], y[t][1], x0, x1, tl, th);
+            ym[t] = warp_max(abs_max(y[t]));
+            careful = careful || !finite(ym[t]) || !finite(om[t]);
+        }
+        if (!chunk::uniform(careful)) {
+            uint32_t of[MT][4], nf[MT][4];
+            float ratio[MT];
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                ratio[t] = join_scale(S[t], fmaxf(om[t], ym[t] * bm), C * (kmax + qmax));
+                const float c = S[t].c;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 o = bf2(dor[t][j]);
+                    of[t][j] = pack_f16(o.x * c, o.y * c);
+                }
+                const float nx[2] = {-b[0].x * c, -b[1].x * c}, ny[2] = {-b[0].y * c, -b[1].y * c};
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    nf[t][2 * j] = pack_f16(y[t][j][0] * nx[j], y[t][j][1] * ny[j]);
+                    nf[t][2 * j + 1] = pack_f16(y[t][j][2] * nx[j], y[t][j][3] * ny[j]);
+                }
+                S[t].inv = inverse_of(c);
+            }
+            // dS = diag(2^g_l) dS' + qw^T do - kw^T dv
+#pragma unroll
+            for (int jj = 0; jj < 8; ++jj) {
+                uint32_t kf[4], qf[4];
+                ldsm4t(qf, qw + plane_off(trow, 2 * jj + tcol));
+                ldsm4t(kf, kw + plane_off(trow, 2 * jj + tcol));
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float2 d =
+                        *reinterpret_cast<const float2 *>(&in.decay[16 * jj + 8 * x + tc2]);
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        float(&s)[4] = S[t].s[2 * jj + x];
+                        const float2 dr = chunk::mul2(d, make_float2(ratio[t], ratio[t]));
+                        const float2 u = chunk::mul2(make_float2(s[0], s[1]), dr);
+                        const float2 w = chunk::mul2(make_float2(s[2], s[3]), dr);
+                        s[0] = u.x; s[1] = u.y; s[2] = w.x; s[3] = w.y;
+                        mma_f16(s, of[t], qf[2 * x], qf[2 * x + 1]);
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+                        mma_f16(S[t].s[2 * jj + x], nf[t], kf[2 * x], kf[2 * x + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                walk_tokens_back(S[t], y[t], sm.raw[slot], sm.beta[slot], sm.dout[slot],
+                                 (role.consumer * MT + t) * 16, a.scale, lane);
+                ym[t] = warp_max(abs_max(y[t]));
+            }
+        }
+        if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kHalf + 32 * NW);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            const float s = store_block(a.y + unit_at * kRowsBytes, y[t], ym[t],
+                                        (step % 4) * 8 + tile0 + t, lane);
+            if (lane == 0) {
+                float *scales = a.dscales + unit_at * kScales;
+                scales[8 + (step % 4) * 8 + tile0 + t] = s;
+                if (keep) scales[tile0 + t] = ckpt_scale[t];
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {  // dv = beta Y
+                const uint32_t u =
+                    chunk::movm_t(chunk::pack_bf16(b[j].x * y[t][j][0], b[j].y * y[t][j][1]));
+                const uint32_t w =
+                    chunk::movm_t(chunk::pack_bf16(b[j].x * y[t][j][2], b[j].y * y[t][j][3]));
+                const int tok = step * C + 8 * j + gr;
+                if (tok < sq.len) {
+                    uint16_t *at = dv_at + (size_t)tok * vrow + 16 * t;
+                    if (dbg_ok(a.dbg, (size_t)(at - (uint16_t *)a.dv) + 9, a.rows_o * D,
+                               DBG_STORE)) {
+                        *reinterpret_cast<uint32_t *>(at) = u;
+                        *reinterpret_cast<uint32_t *>(at + 8) = w;
+                    }
+                }
+            }
+        }
+    }
+    if (a.d_initial_state) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                float *p = a.d_initial_state + sbase + (size_t)8 * j * D + 16 * t;
+                p[0] = S[t].s[j][0] * S[t].inv;
+                p[D] = S[t].s[j][1] * S[t].inv;
+                p[8] = S[t].s[j][2] * S[t].inv;
+                p[D + 8] = S[t].s[j][3] * S[t].inv;
+            }
+    }
+}
+
+template <int NW, int MT>
+cudaError_t launch(const ChunkBwdArgs &a, int dev, cudaStream_t stream) {
+    static volatile int done[kMaxDev];
+    cudaError_t e =
+        smem_limit_once(kda_fast_bwd_state_kernel<NW, MT>, (int)sizeof(Smem), dev, done);
+    if (e != cudaSuccess) return e;
+    kda_fast_bwd_state_kernel<NW, MT><<<a.num_seqs * a.HV * (D / (16 * NW * MT)),
+                                        Roles<NW>::kThreads, sizeof(Smem), stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_bwd_state(const ChunkBwdArgs &a, int dev, cudaStream_t stream) {
+    const long long heads = (long long)a.num_seqs * a.HV;
+    if (heads * 2 > kSMs) return launch<4, 2>(a, dev, stream);
+    if (heads * 4 > kSMs) return launch<4, 1>(a, dev, stream);
+    return launch<2, 1>(a, dev, stream);
+}
+
+}  // namespace fast
+}  // namespace kda

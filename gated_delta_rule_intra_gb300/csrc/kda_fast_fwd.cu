@@ -1,0 +1,499 @@
+// Forward of the gated delta-rule recurrence for BF16 training (see kda_fast.cuh): one CTA
+// walks one (sequence, value head), or a part of its dv columns, in steps of 16 tokens.
+#include "kda_fast.cuh"
+#include "kda_ops.h"
+
+namespace kda {
+namespace fast {
+namespace {
+
+using chunk::bar_arrive;
+using chunk::bar_or;
+using chunk::bar_sync;
+using chunk::cp16z;
+using chunk::ldsm4;
+using chunk::ldsm4t;
+using chunk::plane_off;
+using chunk::Roles;
+using chunk::Seq;
+using tc::smem_u32;
+
+constexpr int kStages = 3;         // prepared stages
+constexpr int kRaw = kStages + 2;  // raw input stages: two ahead, and as far back as a stage lives
+
+// Named barriers; PLANES, FULL, EMPTY + stage.
+enum { BAR_PREP = 1, BAR_SCORE = 2, BAR_PLANES = 3, BAR_FULL = 6, BAR_EMPTY = 9 };
+
+struct __align__(128) Stage {
+    Planes pl;
+    char t2[kTall];  // T2, FP32 for TF32 products
+    char p[kTile];   // P, FP16
+    float g[C][kRowPad];
+    int strong;
+};
+
+struct __align__(128) Smem {
+    Stage stage[kStages];
+    RawStage raw[kRaw];
+    uint16_t v[kRaw][C][D];  // rows of the CTA's dv slice, swizzled chunks
+    float beta[kRaw][C];
+    float4 part[4][4][32];   // scores of a quarter of the channels
+    float a2[2][C][C + 4];   // (M diag(beta))^T, two steps' worth
+    float a1[2][C][C + 4];   // (diag(beta) M)^T
+    char pt[2][kTall];       // P^T on its way to the saved tiles
+};
+
+// A preparing thread's pointers to the raw inputs; step s is `s` steps further on.
+template <int SLICE> struct Loader {
+    const char *q, *k, *v, *gate, *beta;
+    size_t hrow, vrow;  // bytes of a token's row of q or k, and of v (gate: twice)
+    int row, c, len;
+
+    __device__ __forceinline__ Loader(const ChunkFwdArgs &a, const Seq &sq, int h, int hv, int dv0,
+                                      int tid)
+        : row(tid >> 4), c(tid & 15), len(sq.len) {
+        hrow = (size_t)a.H * D * 2;
+        vrow = (size_t)a.HV * D * 2;
+        const size_t r0 = (size_t)sq.row0;
+        q = (const char *)a.q + r0 * hrow + h * D * 2 + c * 16;
+        k = (const char *)a.k + r0 * hrow + h * D * 2 + c * 16;
+        v = (const char *)a.v + r0 * vrow + (hv * D + dv0) * 2 + c * 16;
+        gate = (const char *)a.gate + r0 * vrow * 2 + hv * D * 4 + c * 16;
+        beta = (const char *)(a.beta + r0 * a.HV + hv);
+    }
+    __device__ __forceinline__ void load(Smem &sm, const ChunkFwdArgs &a, int step) const {
+        const int slot = step % kRaw;
+        RawStage &raw = sm.raw[slot];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = row + 8 * i, t = step * C + r;
+            const bool ok = t < len;
+            const size_t at = ok ? (size_t)t : 0;
+            cp16z(smem_u32(&raw.q[r][c * 8]), q + at * hrow, ok);
+            cp16z(smem_u32(&raw.k[r][c * 8]), k + at * hrow, ok);
+            cp16z(smem_u32(&raw.gate[r][c * 4]), gate + at * vrow * 2, ok);
+            cp16z(smem_u32(&raw.gate[r][64 + c * 4]), gate + at * vrow * 2 + 256, ok);
+            if (c < SLICE / 8)
+                cp16z(smem_u32(sm.v[slot]) + plane_off(r, c), v + at * vrow, ok);
+            if (c == 0)
+                chunk::cp4z(smem_u32(&sm.beta[slot][r]), beta + at * a.HV * 4, ok);
+        }
+    }
+};
+
+// An entry of P (zero above the diagonal).
+__device__ __forceinline__ void put_p(Stage &out, char *pt, int r, int s, float x) {
+    const uint32_t b = pack_f16(x, 0.f);
+    reinterpret_cast<uint16_t *>(out.p)[r * C + s] = (uint16_t)b;
+    *reinterpret_cast<uint32_t *>(pt + tall_at(s, r)) = to_tf32(x);
+}
+
+// M and P of a step, M = (k 2^g) (k 2^-g)^T and P = (scale q 2^g) (k 2^-g)^T: the exponents
+// cancel in each term, and no term is above |q_r k_s|.  Each warp sums a quarter of the
+// channels, straight from the raw inputs, then one of the four 16x8 tiles over the quarters.
+// Entries above the diagonal may be of any size and are dropped.  Returns whether an entry of
+// P is out of FP16's reach.
+__device__ __forceinline__ bool scores(Smem &sm, Stage &out, const RawStage &raw,
+                                       const float *beta, int buf, float scale, int w, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    float acc[4][4] = {};  // M, tokens s 0-7 and 8-15; P, the same
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int ch = 32 * w + 8 * i + 2 * t;
+        uint32_t ak[4], aq[4], b[4];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int r = g + 8 * x;
+            const float2 k = bf2(*reinterpret_cast<const uint32_t *>(&raw.k[r][ch]));
+            const float2 q = bf2(*reinterpret_cast<const uint32_t *>(&raw.q[r][ch]));
+            const float2 gg = *reinterpret_cast<const float2 *>(&out.g[r][ch]);
+            const float2 up = make_float2(ex2(gg.x), ex2(gg.y));
+            ak[x] = to_tf32(k.x * up.x);
+            ak[2 + x] = to_tf32(k.y * up.y);
+            aq[x] = to_tf32(scale * q.x * up.x);
+            aq[2 + x] = to_tf32(scale * q.y * up.y);
+            b[2 * x] = to_tf32(k.x * ex2(-gg.x));
+            b[2 * x + 1] = to_tf32(k.y * ex2(-gg.y));
+        }
+        mma_tf32(acc[0], ak, b[0], b[1]);
+        mma_tf32(acc[1], ak, b[2], b[3]);
+        mma_tf32(acc[2], aq, b[0], b[1]);
+        mma_tf32(acc[3], aq, b[2], b[3]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        sm.part[w][i][lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    bar_sync(BAR_SCORE, kHalf);
+    float x[4] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 y = sm.part[i][w][lane];
+        x[0] += y.x; x[1] += y.y; x[2] += y.z; x[3] += y.w;
+    }
+    bool big = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = g + (i >> 1) * 8, s = 8 * (w & 1) + 2 * t + (i & 1);
+        if (w >= 2) {
+            const float p = s <= r ? x[i] : 0.f;
+            put_p(out, sm.pt[buf], r, s, p);
+            big = big || !(fabsf(p) <= 16384.f);
+        } else if (s < r) {
+            sm.a2[buf][s][r] = x[i] * beta[s];
+            sm.a1[buf][s][r] = x[i] * beta[r];
+        }
+    }
+    return big;
+}
+
+// The same where 2^-g would leave FP32's range: pair by pair, one exp2 per (r, s, channel),
+// every exponent <= 0.  17 pairs of the rows w and 15 - w a call; lane l holds channels 4l on.
+__device__ __noinline__ bool scores_strong(Smem &sm, Stage &out, const RawStage &raw,
+                                           const float *beta, int buf, float scale, int w,
+                                           int lane) {
+    auto row4 = [&](const uint16_t *p, float (&x)[4]) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p + 4 * lane);
+        const float2 lo = bf2(u.x), hi = bf2(u.y);
+        x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
+    };
+    bool big = false;
+    const int r1 = w, r2 = C - 1 - w;
+    for (int j = 0; j < 17; ++j) {
+        const int r = j <= w ? r1 : r2, s = j <= w ? j : j - w - 1;
+        float q[4], k[4], ks[4];
+        row4(raw.q[r], q);
+        row4(raw.k[r], k);
+        row4(raw.k[s], ks);
+        const float4 gr = *reinterpret_cast<const float4 *>(&out.g[r][4 * lane]);
+        const float4 gs = *reinterpret_cast<const float4 *>(&out.g[s][4 * lane]);
+        const float e[4] = {ex2(gr.x - gs.x) * ks[0], ex2(gr.y - gs.y) * ks[1],
+                            ex2(gr.z - gs.z) * ks[2], ex2(gr.w - gs.w) * ks[3]};
+        float p = 0.f, m = 0.f;
+        for (int i = 0; i < 4; ++i) {
+            p += q[i] * e[i];
+            m += k[i] * e[i];
+        }
+        for (int off = 16; off > 0; off >>= 1) {
+            p += __shfl_xor_sync(0xffffffffu, p, off);
+            m += __shfl_xor_sync(0xffffffffu, m, off);
+        }
+        p *= scale;
+        big = big || !(fabsf(p) <= 16384.f);
+        if (lane == 0) {
+            put_p(out, sm.pt[buf], r, s, p);
+            if (s < r) {
+                put_p(out, sm.pt[buf], s, r, 0.f);
+                sm.a2[buf][s][r] = m * beta[s];
+                sm.a1[buf][s][r] = m * beta[r];
+            }
+        }
+    }
+    return big;
+}
+
+// T2 = (I + M diag(beta))^-1 (lanes 0-15, one column each) and T = (I + diag(beta) M)^-1
+// (lanes 16-31) by forward substitution in FP32, column by column of the matrix: a found entry
+// is taken out of all later rows at once.  T goes to `tiles` as rows of T^T.
+__device__ __forceinline__ void solve(Smem &sm, Stage &out, int buf, char *tiles, int lane) {
+    const int c = lane & 15;
+    const bool second = lane >= 16;
+    const float(*A)[C + 4] = second ? sm.a1[buf] : sm.a2[buf];  // A[j][r], r > j
+    float x[C];
+#pragma unroll
+    for (int r = 0; r < C; ++r) x[r] = r == c ? 1.f : 0.f;
+#pragma unroll
+    for (int j = 0; j < C - 1; ++j)
+#pragma unroll
+        for (int r = (j + 1) & ~3; r < C; r += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(&A[j][r]);
+            if (r > j) x[r] -= a.x * x[j];
+            if (r + 1 > j) x[r + 1] -= a.y * x[j];
+            if (r + 2 > j) x[r + 2] -= a.z * x[j];
+            x[r + 3] -= a.w * x[j];
+        }
+    if (!second) {
+#pragma unroll
+        for (int r = 0; r < C; ++r)
+            *reinterpret_cast<uint32_t *>(out.t2 + tall_at(r, c)) = to_tf32(x[r]);
+    } else if (tiles) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int b = (i >> 1) * 8 + (i & 1);
+            *reinterpret_cast<uint4 *>(tiles + tall_off(c, i)) = make_uint4(
+                to_tf32(x[b]), to_tf32(x[b + 2]), to_tf32(x[b + 4]), to_tf32(x[b + 6]));
+        }
+    }
+}
+
+// NW consumer warps of 16 MT dv columns each; a head takes 128 / (16 NW MT) CTAs.
+template <int NW, int MT, bool SAVE>
+__global__ void __launch_bounds__(Roles<NW>::kThreads, 1) kda_fast_fwd_kernel(const ChunkFwdArgs a) {
+    constexpr int kSlice = 16 * NW * MT, kSplit = D / kSlice;
+    extern __shared__ __align__(128) char smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
+    const int lane = threadIdx.x & 31;
+    const Roles<NW> role(chunk::warp_index());
+    const int unit = blockIdx.x / kSplit, dv0 = (blockIdx.x % kSplit) * kSlice;
+    const int n = unit / a.HV, hv = unit - n * a.HV, h = hv / (a.HV / a.H);
+    const Seq sq = chunk::seq_of(n, a.T, a.cu_seqlens);
+    // whole 64-token slots where the backward's buffers are written: rows past the end are
+    // computed as zeros, so every row of a slot is defined
+    const int steps = SAVE ? (sq.len + BT - 1) / BT * (BT / C) : (sq.len + C - 1) / C;
+
+    if (role.prep >= 0) {
+        const int tid = role.prep * 32 + lane;
+        if (MT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+        if (tid < kHalf) {  // raw inputs -> operand planes
+            const Loader<kSlice> in(a, sq, h, hv, dv0, tid);
+            for (int i = 0; i < 2; ++i) {
+                if (i < steps) in.load(sm, a, i);
+                cp_async_commit();
+            }
+            for (int i = 0; i < steps; ++i) {
+                const int st = i % kStages;
+                Stage &out = sm.stage[st];
+                cp_async_wait_newest<1>();
+                // the consumers are done with this stage's previous step (and its inputs)
+                if (i >= kStages) bar_sync(BAR_EMPTY + st, kHalf + 32 * NW);
+                bar_sync(BAR_PREP, kHalf);
+                if (i + 2 < steps) in.load(sm, a, i + 2);
+                cp_async_commit();
+                const bool strong =
+                    prepare<true>(sm.raw[i % kRaw], out.pl, out.g, a.scale, tid);
+                const bool any = bar_or(BAR_PREP, kHalf, strong);
+                if (tid == 0) out.strong = any;
+                bar_arrive(BAR_PLANES + st, 2 * kHalf);
+            }
+            cp_async_wait_all();
+            return;
+        }
+        // planes -> scores -> T2 and T
+        const int w = role.prep - kHalf / 32;
+        for (int i = 0; i < steps; ++i) {
+            const int st = i % kStages;
+            Stage &out = sm.stage[st];
+            const float *beta = sm.beta[i % kRaw];
+            const RawStage &raw = sm.raw[i % kRaw];
+            bar_sync(BAR_PLANES + st, 2 * kHalf);
+            bool big;
+            if (!chunk::uniform(out.strong)) {
+                big = scores(sm, out, raw, beta, i & 1, a.scale, w, lane);
+            } else {
+                big = scores_strong(sm, out, raw, beta, i & 1, a.scale, w, lane);
+                big = scores_strong(sm, out, raw, beta, i & 1, a.scale, w + 4, lane) || big;
+            }
+            big = bar_or(BAR_SCORE, kHalf, big);
+            if (w == 0) {
+                char *tiles = nullptr;
+                if (SAVE && dv0 == 0)
+                    tiles = a.tiles + ((size_t)(sq.slot0 + i / 4) * a.HV + hv) * kTilesBytes +
+                            (i % 4) * 2 * kTall;
+                if (SAVE || lane < 16) solve(sm, out, i & 1, tiles, lane);
+                const float bm =
+                    warp_max(lane < C ? fabsf(beta[lane]) : 0.f);
+                if (lane == 0) out.pl.bmax = bm;
+                if (lane == 0)
+                    out.pl.careful = big || !finite(bm) || !(largest(out.pl.kmax) <= 16384.f) ||
+                                     !(a.scale * largest(out.pl.qmax) <= 16384.f);
+                __syncwarp();
+                bar_arrive(BAR_FULL + st, 32 + 32 * NW);
+                if (tiles) {
+                    uint4 *to = reinterpret_cast<uint4 *>(tiles + kTall);
+                    const uint4 *p = reinterpret_cast<const uint4 *>(sm.pt[i & 1]);
+                    to[lane] = p[lane];
+                    to[32 + lane] = p[32 + lane];
+                    __syncwarp();
+                }
+            }
+        }
+        return;
+    }
+
+    // ------------------------------------------------------------------ consumers
+    if (role.consumer < 0) return;
+    if (MT > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+    const int tile0 = dv0 / 16 + role.consumer * MT;  // the head's tile of 16 dv columns
+    const int gr = lane >> 2, tc2 = (lane & 3) * 2;
+    const int lrow = (lane & 7) + ((lane >> 4) & 1) * 8, lcol = (lane >> 3) & 1;
+    const int trow = lane & 15, tcol = lane >> 4;
+    Tile S[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) S[t].clear();
+    const size_t orow = (size_t)a.HV * D;
+    uint16_t *o_at = (uint16_t *)a.o + (size_t)sq.row0 * orow + (size_t)hv * D + tile0 * 16 + tc2;
+
+    for (int i = 0; i < steps; ++i) {
+        const int st = i % kStages, slot = i % kRaw;
+        const size_t unit_at = (size_t)(sq.slot0 + i / 4) * a.HV + hv;
+        bar_sync(BAR_FULL + st, 32 + 32 * NW);
+        const Stage &in = sm.stage[st];
+        const float *beta = sm.beta[slot];
+        const uint32_t kw = smem_u32(in.pl.kw), qw = smem_u32(in.pl.qw), kd = smem_u32(in.pl.kd);
+        const float kmax = largest(in.pl.kmax);
+        const bool keep = SAVE && i % 4 == 0;
+        bool careful = chunk::uniform(in.pl.careful);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+            if (chunk::uniform(S[t].bound > kLimit)) S[t].renew();
+        uint32_t th[4], tl[4], pf[4];
+        load_tall(smem_u32(in.t2), lane, tl, th);
+        ldsm4(pf, smem_u32(in.p) + chunk::tile_lane(lane));
+        const float2 b[2] = {*reinterpret_cast<const float2 *>(&beta[tc2]),
+                             *reinterpret_cast<const float2 *>(&beta[8 + tc2])};
+        float xw[MT][2][4] = {}, xq[MT][2][4] = {}, e[MT][2][4] = {};
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+            uint32_t kf[4], qf[4];
+            const uint32_t off = plane_off(lrow, 2 * kk + lcol);
+            ldsm4(kf, kw + off);
+            ldsm4(qf, qw + off);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const float(&x)[4] = S[t].s[2 * kk], (&y)[4] = S[t].s[2 * kk + 1];
+                const uint32_t af[4] = {pack_f16(x[0], x[1]), pack_f16(x[2], x[3]),
+                                        pack_f16(y[0], y[1]), pack_f16(y[2], y[3])};
+                mma_f16(xw[t][0], af, kf[0], kf[1]);
+                mma_f16(xw[t][1], af, kf[2], kf[3]);
+                mma_f16(xq[t][0], af, qf[0], qf[1]);
+                mma_f16(xq[t][1], af, qf[2], qf[3]);
+                if (keep)  // the operand is the checkpoint
+                    reinterpret_cast<uint4 *>(a.ckpt + unit_at * kCkptBytes)
+                        [((tile0 + t) * 8 + kk) * 32 + lane] =
+                            make_uint4(af[0], af[1], af[2], af[3]);
+            }
+        }
+        float em[MT], ckpt_scale[MT], inv[MT];  // of the state as it was an operand
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            ckpt_scale[t] = S[t].saved_scale();
+            inv[t] = S[t].inv;
+            // R = v - kw S and e = T2 R; blocks (tokens 0-7, dv 0-7), (0-7, 8-15), (8-15, ..)
+            uint32_t vr[4], x0[4], x1[4];
+            ldsm4t(vr, smem_u32(sm.v[slot]) +
+                           plane_off(lrow, (role.consumer * MT + t) * 2 + lcol));
+            float R[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float2 x = bf2(vr[2 * j]), y = bf2(vr[2 * j + 1]);
+                R[j][0] = fmaf(xw[t][j][0], -inv[t], x.x);
+                R[j][1] = fmaf(xw[t][j][1], -inv[t], x.y);
+                R[j][2] = fmaf(xw[t][j][2], -inv[t], y.x);
+                R[j][3] = fmaf(xw[t][j][3], -inv[t], y.y);
+            }
+            tf_frag(R[0], x0);
+            tf_frag(R[1], x1);
+            mma_tall(e[t][0], e[t][1], x0, x1, tl, th);
+            em[t] = warp_max(abs_max(e[t]));
+            careful = careful || !finite(em[t]);
+        }
+        const float bm = in.pl.bmax;
+        if (!chunk::uniform(careful)) {
+            // n = beta e
+            uint32_t nf[MT][4];
+            float ratio[MT];
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                ratio[t] = join_scale(S[t], em[t] * bm, C * kmax);
+                const float c = S[t].c;
+                nf[t][0] = pack_f16(e[t][0][0] * (b[0].x * c), e[t][0][1] * (b[0].y * c));
+                nf[t][1] = pack_f16(e[t][0][2] * (b[0].x * c), e[t][0][3] * (b[0].y * c));
+                nf[t][2] = pack_f16(e[t][1][0] * (b[1].x * c), e[t][1][1] * (b[1].y * c));
+                nf[t][3] = pack_f16(e[t][1][2] * (b[1].x * c), e[t][1][3] * (b[1].y * c));
+                S[t].inv = inverse_of(c);
+            }
+            // S' = diag(2^g_l) S + kd^T n
+#pragma unroll
+            for (int jj = 0; jj < 8; ++jj) {
+                uint32_t kf[4];
+                ldsm4t(kf, kd + plane_off(trow, 2 * jj + tcol));
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float2 d =
+                        *reinterpret_cast<const float2 *>(&in.pl.decay[16 * jj + 8 * x + tc2]);
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        float(&s)[4] = S[t].s[2 * jj + x];
+                        const float2 dr = chunk::mul2(d, make_float2(ratio[t], ratio[t]));
+                        const float2 u = chunk::mul2(make_float2(s[0], s[1]), dr);
+                        const float2 w = chunk::mul2(make_float2(s[2], s[3]), dr);
+                        s[0] = u.x; s[1] = u.y; s[2] = w.x; s[3] = w.y;
+                        mma_f16(s, nf[t], kf[2 * x], kf[2 * x + 1]);
+                    }
+                }
+            }
+            // o = qw S + P n
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                float po[2][4] = {};
+                mma_f16(po[0], nf[t], pf[0], pf[1]);
+                mma_f16(po[1], nf[t], pf[2], pf[3]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        xq[t][j][p] = fmaf(po[j][p], S[t].inv, xq[t][j][p] * inv[t]);
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                walk_tokens(S[t], xq[t], e[t], sm.raw[slot], beta, sm.v[slot],
+                            (role.consumer * MT + t) * 16, a.scale, lane);
+                em[t] = warp_max(abs_max(e[t]));
+            }
+        }
+        if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kHalf + 32 * NW);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            if (SAVE) {
+                const float s = store_block(a.e + unit_at * kRowsBytes, e[t], em[t],
+                                            (i % 4) * 8 + tile0 + t, lane);
+                if (lane == 0) {
+                    float *scales = a.scales + unit_at * kScales;
+                    scales[8 + (i % 4) * 8 + tile0 + t] = s;
+                    if (keep) scales[tile0 + t] = ckpt_scale[t];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {  // o: rows of tokens after the transpose
+                const uint32_t x = chunk::movm_t(chunk::pack_bf16(xq[t][j][0], xq[t][j][1]));
+                const uint32_t y = chunk::movm_t(chunk::pack_bf16(xq[t][j][2], xq[t][j][3]));
+                const int tok = i * C + 8 * j + gr;
+                if (tok < sq.len) {
+                    uint16_t *at = o_at + (size_t)tok * orow + 16 * t;
+                    if (dbg_ok(a.dbg, (size_t)(at - (uint16_t *)a.o) + 9, a.rows_o * D,
+                               DBG_STORE)) {
+                        *reinterpret_cast<uint32_t *>(at) = x;
+                        *reinterpret_cast<uint32_t *>(at + 8) = y;
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <int NW, int MT, bool SAVE>
+cudaError_t launch(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
+    static volatile int done[kMaxDev];
+    cudaError_t e =
+        smem_limit_once(kda_fast_fwd_kernel<NW, MT, SAVE>, (int)sizeof(Smem), dev, done);
+    if (e != cudaSuccess) return e;
+    const int grid = a.num_seqs * a.HV * (D / (16 * NW * MT));
+    kda_fast_fwd_kernel<NW, MT, SAVE><<<grid, Roles<NW>::kThreads, sizeof(Smem), stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <bool SAVE> cudaError_t launch_split(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
+    const long long heads = (long long)a.num_seqs * a.HV;
+    if (heads * 2 > kSMs) return launch<4, 2, SAVE>(a, dev, stream);
+    if (heads * 4 > kSMs) return launch<4, 1, SAVE>(a, dev, stream);
+    return launch<2, 1, SAVE>(a, dev, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_fwd(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
+    return a.ckpt ? launch_split<true>(a, dev, stream) : launch_split<false>(a, dev, stream);
+}
+
+}  // namespace fast
+}  // namespace kda

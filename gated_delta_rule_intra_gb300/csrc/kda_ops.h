@@ -15,10 +15,12 @@ struct ChunkFwdArgs {
     const float *initial_state;  // [num_seqs, HV, 128 dk, 128 dv] or null
     float *final_state;          // the same, or null
     char *ckpt, *e, *tiles;      // the backward's buffers, all or none
+    float *scales;               // with them in BF16 training (kda_fast.cuh)
     int T, H, HV, num_seqs;      // T = tokens of a sequence, or of the packed row
     const int *cu_seqlens;       // [num_seqs + 1] or null
     float scale;
     bool fp16;
+    bool fast;                   // BF16 training (kda_fast.cuh)
     size_t rows_o;               // rows of o (tokens * HV), for the debug build's checks
     unsigned *dbg;
 };
@@ -32,7 +34,10 @@ struct ChunkBwdArgs {
     const float *d_final_state;          // [num_seqs, HV, 128 dk, 128 dv] or null
     float *d_initial_state;              // the same, or null
     const char *ckpt, *e, *tiles;        // what the forward saved
+    const float *scales;
     char *dckpt, *y;                     // workspace: state gradients at slot ends, Y
+    float *dscales;
+    bool fast;                           // BF16 training (kda_fast.cuh)
     float *dq_hv, *dk_hv;                // workspace [rows, HV, 128], only when HV > H
     int B, T, H, HV, num_seqs, slots;
     const int *cu_seqlens;

@@ -44,7 +44,17 @@ template <size_t N> bool misaligned(const void *const (&ps)[N], unsigned to) {
 
 kda_status_t finish(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
-constexpr size_t kSavedPerSlot = 65536 + 32768 + 8192;  // checkpoint, e, tiles of 64 tokens
+// What the forward saves, and the backward's workspace, for 64 tokens of a head: the state (or
+// its gradient), e (or Y), the steps' tiles; FP16 with scales in BF16 training (kda_fast.cuh),
+// BF16 hi and lo otherwise.
+struct SlotBytes {
+    size_t state, rows, tiles, scales;
+    size_t saved() const { return state + rows + tiles + scales; }
+    size_t work() const { return state + rows + scales; }
+};
+constexpr SlotBytes kFull = {65536, 32768, 8192, 0}, kFast = {32768, 16384, 8192, 160};
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // 64-token slots of a call (see seq_of() in kda_chunk.cuh).
 long long chunk_slots(int B, int T, int num_seqs) {
@@ -68,9 +78,11 @@ kda_status_t check_chunk_shape(int B, int T, int H, int HV, bool varlen, int num
 
 extern "C" {
 
-size_t kda_chunk_saved_bytes(int B, int T, int HV, int num_seqs) {
+size_t kda_chunk_saved_bytes(int B, int T, int HV, int num_seqs, kda_dtype_t dtype,
+                             int with_state) {
     if (check_chunk_shape(B, T, 1, HV, num_seqs > 0, num_seqs) != KDA_OK) return 0;
-    return (size_t)chunk_slots(B, T, num_seqs) * HV * kSavedPerSlot;
+    const SlotBytes &s = dtype == KDA_BF16 && !with_state ? kFast : kFull;
+    return up256((size_t)chunk_slots(B, T, num_seqs) * HV * s.saved());
 }
 
 kda_status_t kda_chunk_fwd(const void *q, const void *k, const void *v, const float *gate,
@@ -89,8 +101,10 @@ kda_status_t kda_chunk_fwd(const void *q, const void *k, const void *v, const fl
     const void *a4[] = {beta, op.cu_seqlens};
     const void *a256[] = {op.saved};
     if (misaligned(a16, 16) || misaligned(a4, 4) || misaligned(a256, 256)) return KDA_ERR_ALIGN;
-    const size_t saved = kda_chunk_saved_bytes(B, T, HV, op.num_seqs);
-    if (op.saved && op.saved_bytes < saved) return KDA_ERR_WORKSPACE;
+    const bool with_state = op.initial_state || op.final_state;
+    const bool fast = dtype == KDA_BF16 && !with_state;
+    const size_t saved = kda_chunk_saved_bytes(B, T, HV, op.num_seqs, dtype, with_state);
+    if (op.saved && op.saved_bytes != saved) return KDA_ERR_WORKSPACE;
     const size_t rq = (size_t)B * T * H, rv = (size_t)B * T * HV;
     const int seqs = varlen ? op.num_seqs : B;
     const size_t states = (size_t)seqs * HV * KDA_K * KDA_K * 4;
@@ -108,10 +122,13 @@ kda_status_t kda_chunk_fwd(const void *q, const void *k, const void *v, const fl
     a.final_state = op.final_state;
     if (op.saved) {
         const size_t n = (size_t)chunk_slots(B, T, op.num_seqs) * HV;
+        const SlotBytes &s = fast ? kFast : kFull;
         a.ckpt = (char *)op.saved;
-        a.e = a.ckpt + n * 65536;
-        a.tiles = a.e + n * 32768;
+        a.e = a.ckpt + n * s.state;
+        a.tiles = a.e + n * s.rows;
+        a.scales = (float *)(a.tiles + n * s.tiles);
     }
+    a.fast = fast;
     a.T = T; a.H = H; a.HV = HV; a.num_seqs = seqs;
     a.cu_seqlens = op.cu_seqlens;
     a.scale = op.scale != 0.f ? op.scale : 0.08838834764831845f;
@@ -121,11 +138,22 @@ kda_status_t kda_chunk_fwd(const void *q, const void *k, const void *v, const fl
     return finish(kda::launch_chunk_fwd(a, (cudaStream_t)stream));
 }
 
-size_t kda_chunk_bwd_workspace_bytes(int B, int T, int H, int HV, int num_seqs) {
+// The mode that wrote `saved_bytes`: 0 with states or FP16, 1 BF16 training, -1 neither.
+static int saved_mode(int B, int T, int HV, int num_seqs, kda_dtype_t dtype, size_t saved_bytes) {
+    if (saved_bytes && dtype == KDA_BF16 &&
+        saved_bytes == kda_chunk_saved_bytes(B, T, HV, num_seqs, dtype, 0))
+        return 1;
+    return saved_bytes == kda_chunk_saved_bytes(B, T, HV, num_seqs, dtype, 1) ? 0 : -1;
+}
+
+size_t kda_chunk_bwd_workspace_bytes(int B, int T, int H, int HV, int num_seqs,
+                                     kda_dtype_t dtype, size_t saved_bytes) {
     if (check_chunk_shape(B, T, H, HV, num_seqs > 0, num_seqs) != KDA_OK) return 0;
+    const int mode = saved_mode(B, T, HV, num_seqs, dtype, saved_bytes);
+    if (mode < 0) return 0;
     const size_t units = (size_t)chunk_slots(B, T, num_seqs) * HV;
     const size_t heads = HV > H ? (size_t)B * T * HV * KDA_K * 4 * 2 : 0;
-    return units * (65536 + 32768) + heads;
+    return up256(units * (mode ? kFast : kFull).work()) + heads;
 }
 
 kda_status_t kda_chunk_bwd(const void *q, const void *k, const float *gate, const float *beta,
@@ -147,9 +175,12 @@ kda_status_t kda_chunk_bwd(const void *q, const void *k, const float *gate, cons
     const void *a256[] = {op.saved, op.workspace};
     if (misaligned(a16, 16) || misaligned(a4, 4) || misaligned(a2, 2) || misaligned(a256, 256))
         return KDA_ERR_ALIGN;
-    const size_t saved = kda_chunk_saved_bytes(B, T, HV, op.num_seqs);
-    const size_t work = kda_chunk_bwd_workspace_bytes(B, T, H, HV, op.num_seqs);
-    if ((saved && (!op.saved || op.saved_bytes < saved)) ||
+    const int mode = saved_mode(B, T, HV, op.num_seqs, dtype, op.saved_bytes);
+    if (mode < 0) return KDA_ERR_WORKSPACE;
+    const size_t saved = op.saved_bytes;
+    const size_t work =
+        kda_chunk_bwd_workspace_bytes(B, T, H, HV, op.num_seqs, dtype, op.saved_bytes);
+    if ((saved && !op.saved) ||
         (work && (!op.workspace || op.workspace_bytes < work)))
         return KDA_ERR_WORKSPACE;
     const size_t rq = (size_t)B * T * H, rv = (size_t)B * T * HV;
@@ -172,13 +203,17 @@ kda_status_t kda_chunk_bwd(const void *q, const void *k, const float *gate, cons
     a.d_initial_state = op.d_initial_state;
     const long long slots = chunk_slots(B, T, op.num_seqs);
     const size_t n = (size_t)slots * HV;
+    a.fast = mode == 1;
+    const SlotBytes &s = a.fast ? kFast : kFull;
     a.ckpt = (const char *)op.saved;
-    a.e = a.ckpt + n * 65536;
-    a.tiles = a.e + n * 32768;
+    a.e = a.ckpt + n * s.state;
+    a.tiles = a.e + n * s.rows;
+    a.scales = (const float *)(a.tiles + n * s.tiles);
     a.dckpt = (char *)op.workspace;
-    a.y = a.dckpt + n * 65536;
+    a.y = a.dckpt + n * s.state;
+    a.dscales = (float *)(a.y + n * s.rows);
     if (HV > H) {
-        a.dq_hv = (float *)(a.y + n * 32768);
+        a.dq_hv = (float *)((char *)op.workspace + up256(n * s.work()));
         a.dk_hv = a.dq_hv + rv * KDA_K;
     }
     a.B = B; a.T = T; a.H = H; a.HV = HV; a.num_seqs = seqs;

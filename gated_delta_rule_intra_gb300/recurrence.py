@@ -97,8 +97,8 @@ def kda_chunk_fwd(q, k, v, gate, beta, scale=None, initial_state=None, *,
     beta [B, T, HV] fp32; any T.  ``scale`` defaults to 128 ** -0.5.  ``initial_state``
     [sequences, HV, 128 dk, 128 dv] fp32 defaults to zeros.  o is in q's dtype, with zeros at
     tokens in no sequence when it is allocated here.  final_state (fp32) is None unless
-    ``output_final_state``.  saved is what ``kda_chunk_bwd`` needs (about 1.7 KB a token and
-    value head), None unless ``save``.  ``cu_seqlens`` (int32 [N + 1] on the device, B = 1)
+    ``output_final_state``.  saved is what ``kda_chunk_bwd`` needs (0.9 KB a token and
+    value head in bf16 without a state, 1.7 KB otherwise), None unless ``save``.  ``cu_seqlens`` (int32 [N + 1] on the device, B = 1)
     packs N sequences along T; it is read on the device only.
     """
     H, HV, dev = _inputs("kda_chunk_fwd", q, k, v, gate, beta, 2)
@@ -119,7 +119,8 @@ def kda_chunk_fwd(q, k, v, gate, beta, scale=None, initial_state=None, *,
         final = torch.empty((N or B, HV, K, K), dtype=F32, device=q.device)
         op.final_state = final.data_ptr()
     if save:
-        size = library().kda_chunk_saved_bytes(B, T, HV, N)
+        size = library().kda_chunk_saved_bytes(B, T, HV, N, DTYPES16[q.dtype],
+                                               initial_state is not None or output_final_state)
         saved = torch.empty(size, dtype=torch.uint8, device=q.device)
         op.saved, op.saved_bytes = saved.data_ptr(), size
     if B:
@@ -145,7 +146,10 @@ def kda_chunk_bwd(q, k, v, gate, beta, do, saved, scale=None, d_final_state=None
     N = _seqs(cu_seqlens, B, dev)
     check("do", do, v.shape, dt, dev)
     lib = library()
-    saved_bytes = lib.kda_chunk_saved_bytes(B, T, HV, N)
+    saved_bytes = saved.numel()
+    if saved_bytes not in (lib.kda_chunk_saved_bytes(B, T, HV, N, DTYPES16[dt], 0),
+                           lib.kda_chunk_saved_bytes(B, T, HV, N, DTYPES16[dt], 1)):
+        raise ValueError(f"saved has {saved_bytes} bytes: not from a forward of these inputs")
     check("saved", saved, (saved_bytes,), torch.uint8, dev)
     new = torch.zeros_like if N else torch.empty_like
     out = []
@@ -167,7 +171,7 @@ def kda_chunk_bwd(q, k, v, gate, beta, do, saved, scale=None, d_final_state=None
         d_initial = torch.empty((N or B, HV, K, K), dtype=F32, device=q.device)
         op.d_initial_state = d_initial.data_ptr()
     if B:
-        work = lib.kda_chunk_bwd_workspace_bytes(B, T, H, HV, N)
+        work = lib.kda_chunk_bwd_workspace_bytes(B, T, H, HV, N, DTYPES16[dt], saved_bytes)
         ws = torch.empty(work, dtype=torch.uint8, device=q.device)
         op.workspace, op.workspace_bytes = ws.data_ptr(), work
         run("kda_chunk_bwd", dev, q.data_ptr(), k.data_ptr(), gate.data_ptr(), beta.data_ptr(),

@@ -346,9 +346,11 @@ kda_status_t kda_intra_fwd_ex(const void *q, const void *k, const float *g,
  *   beta        [B, T, HV]       fp32
  * HV is a multiple of H; value head hv reads q/k head hv / (HV / H).  Any T >= 0.
  *
- * Accuracy: o within a rounding to dtype plus 1e-5, the final state within 1e-5 (2-norm of
- * the error over 2-norm of the result): states, sums and the solve are FP32 and every product
- * of FP32 values is taken in three BF16 tensor-core products.
+ * Accuracy (2-norm of the error over 2-norm of the result): states, sums and the solve are
+ * FP32.  Calls that take or return a state, and FP16 ones, take every product of FP32 values
+ * in three BF16 tensor-core products: o within a rounding to dtype plus 1e-5, the final state
+ * within 1e-5.  BF16 calls without a state (training) take one FP16 product with operands of
+ * 11 bits, each with a power of two of its own: o within a rounding to BF16 plus 1e-3.
  *
  * Options (zero-initialise; NULL = none):
  *   HV             0 means HV = H
@@ -356,8 +358,9 @@ kda_status_t kda_intra_fwd_ex(const void *q, const void *k, const float *g,
  *   initial_state  [sequences, HV, 128 dk, 128 dv] fp32, NULL = zeros
  *   final_state    the same shape, written (a sequence of no tokens: a copy of its initial
  *                  state); must not overlap initial_state
- *   saved          what kda_chunk_bwd needs, kda_chunk_saved_bytes() bytes, 256-byte aligned;
- *   saved_bytes    NULL when no backward follows.  About 1.7 KB a token and value head.
+ *   saved          what kda_chunk_bwd needs, exactly kda_chunk_saved_bytes() bytes, 256-byte
+ *   saved_bytes    aligned; NULL when no backward follows.  0.9 KB a token and value head in
+ *                  BF16 without a state, 1.7 KB otherwise.
  *   cu_seqlens     variable-length sequences packed along T (B == 1): device int32
  *   num_seqs       [num_seqs + 1], sequence n is tokens [cu_seqlens[n], cu_seqlens[n+1]).
  *                  Values are read on the device only and clamped to [0, T]; tokens in no
@@ -374,8 +377,10 @@ typedef struct {
     int num_seqs;
 } kda_chunk_fwd_opts_t;
 
-/* Bytes of `saved` (num_seqs: 0 for fixed-length calls); 0 for sizes that no call accepts. */
-size_t kda_chunk_saved_bytes(int B, int T, int HV, int num_seqs);
+/* Bytes of `saved` (num_seqs: 0 for fixed-length calls; with_state: whether the call has an
+ * initial_state or a final_state); 0 for sizes that no call accepts. */
+size_t kda_chunk_saved_bytes(int B, int T, int HV, int num_seqs, kda_dtype_t dtype,
+                             int with_state);
 
 kda_status_t kda_chunk_fwd(const void *q, const void *k, const void *v, const float *gate,
                            const float *beta, void *o, int B, int T, int H, kda_dtype_t dtype,
@@ -388,9 +393,11 @@ kda_status_t kda_chunk_fwd(const void *q, const void *k, const void *v, const fl
  * and cu_seqlens as given to the forward.  No atomics: the same inputs give the same bits.
  *   d_final_state    gradient of the final state, [sequences, HV, 128, 128] fp32, NULL = zeros
  *   d_initial_state  gradient of the initial state, the same shape, written; NULL = not wanted
- *   saved            the forward's, read only (a backward may run again from it)
+ *   saved            the forward's, read only (a backward may run again from it); saved_bytes
+ *                    is the forward's too, and tells how it was written
  *   workspace        kda_chunk_bwd_workspace_bytes() bytes, 256-byte aligned
- * Accuracy: within a rounding to dtype plus 1e-4; the initial state's gradient within 1e-5.
+ * Accuracy: within a rounding to dtype plus 1e-4, the initial state's gradient within 1e-5;
+ * after a BF16 forward without a state a rounding plus 1e-3 (and 1e-3).
  */
 typedef struct {
     int HV;
@@ -405,7 +412,8 @@ typedef struct {
     size_t workspace_bytes;
 } kda_chunk_bwd_opts_t;
 
-size_t kda_chunk_bwd_workspace_bytes(int B, int T, int H, int HV, int num_seqs);
+size_t kda_chunk_bwd_workspace_bytes(int B, int T, int H, int HV, int num_seqs,
+                                     kda_dtype_t dtype, size_t saved_bytes);
 
 kda_status_t kda_chunk_bwd(const void *q, const void *k, const float *gate, const float *beta,
                            const void *dout, void *dq, void *dk, void *dv, void *dgate,
