@@ -190,27 +190,61 @@ struct __align__(16) RawStage {
     float gate[C][D];
 };
 
-// Which warps do what: eight prepare operands, NW consume them.  With two consumers (few heads,
-// so that the time of one step counts) these get two of the SM's four schedulers for
-// themselves, the preparing warps the other two: warps go to the schedulers in turn, and the
-// warps in between leave at once.
-template <int NW> struct Roles {
+// Which warps do what: eight prepare operands, SOLVERS solve the steps' triangular systems, NW
+// consume all that.  With two consumers (few heads, so that the time of one step counts) these
+// get two of the SM's four schedulers with the solvers, the preparing warps the other two: warps
+// go to the schedulers in turn, and the warps in between leave at once.
+//
+// Registers move from the feeding warps to the consumers, by groups of four warps: both shares
+// add up to no more than the kernel is launched with (65,536 over its threads, in eights), which
+// ready_once() checks, because a consumer would wait for the rest forever.
+template <int NW, int SOLVERS = 0> struct Roles {
     static constexpr bool kApart = NW == 2;
-    static constexpr int kThreads = kApart ? 512 : kPrepThreads + 32 * NW;
-    int prep, consumer;  // index, or -1
-    __device__ __forceinline__ explicit Roles(int warp) : prep(-1), consumer(-1) {
-        if (kApart) {
+    static constexpr int kGroup = kApart ? 4 : NW;  // warps that take registers
+    static constexpr int kThreads = kApart ? 640 : kPrepThreads + 32 * (SOLVERS + NW);
+    static constexpr int kGive = kApart ? 80 : NW == 8 ? 112 : SOLVERS ? 88 : 112;
+    static constexpr int kTake = kApart ? 160 : NW == 8 ? 144 : 248;
+    static constexpr int kLaunch = 65536 / kThreads / 8 * 8;
+    static_assert(kGroup % 4 == 0 && SOLVERS % 4 == 0 && SOLVERS <= 8, "");
+    static_assert(kGroup * 32 * kTake + (kThreads - kGroup * 32) * kGive <= kLaunch * kThreads, "");
+
+    int prep, solver, consumer;  // index, or -1
+    bool feeds;                  // prepares or solves (or idles next to those)
+    __device__ __forceinline__ explicit Roles(int warp) : prep(-1), solver(-1), consumer(-1) {
+        feeds = warp >= kGroup;
+        if (!feeds) {
+            if (warp < NW) consumer = warp;
+        } else if (kApart) {
+            const int x = (warp - kGroup) / 4 * 2 + (warp & 1);
             if (warp & 2)
-                prep = (warp >> 2) * 2 + (warp & 1);
-            else if (warp < 2)
-                consumer = warp;
-        } else if (warp < kPrepWarps) {
-            prep = warp;
+                prep = x;
+            else if (x < SOLVERS)
+                solver = x;
+        } else if (warp < kGroup + kPrepWarps) {
+            prep = warp - kGroup;
         } else {
-            consumer = warp - kPrepWarps;
+            solver = warp - kGroup - kPrepWarps;
         }
     }
+    static __device__ __forceinline__ void give() {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGive));
+    }
+    static __device__ __forceinline__ void take() {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTake));
+    }
 };
+
+// A kernel of these roles may be launched: its shared memory is allowed, and it starts with the
+// registers that its warps are going to share out.
+template <class R, class Kernel>
+cudaError_t ready_once(Kernel *kernel, int smem, int dev, volatile int *done) {
+    if (dev >= 0 && dev < kMaxDev && done[dev]) return cudaSuccess;
+    cudaFuncAttributes at;
+    const cudaError_t e = cudaFuncGetAttributes(&at, kernel);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs != R::kLaunch) return cudaErrorLaunchOutOfResources;
+    return smem_limit_once(kernel, smem, dev, done);
+}
 
 template <typename T16> __device__ __forceinline__ float2 unpack2(uint32_t x);
 template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t x) {
@@ -280,20 +314,6 @@ __device__ __forceinline__ bool prep_planes(const RawStage &raw, char *planes, f
         if (FROM_START) big = fmaxf(big, fmaxf(fabsf(kd.x), fabsf(kd.y)));
     }
     return big > 0x1p96f;
-}
-
-// Sums of 32 values over the 32 lanes; lane i returns the sum of v[i].
-__device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        const bool up = lane & off;
-#pragma unroll
-        for (int i = 0; i < off; ++i) {
-            const float keep = up ? v[i + off] : v[i], send = up ? v[i] : v[i + off];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
-        }
-    }
-    return v[0];
 }
 
 // hi and lo A-fragments of a 16x16 FP32 block held as two adjacent 16x8 accumulators.
@@ -378,6 +398,38 @@ __device__ __forceinline__ void store_checkpoint(char *base, const float (&S)[MT
             reinterpret_cast<uint4 *>(base)[(j * 8 + tile + t) * 32 + lane] =
                 make_uint4(movm_t(h0), movm_t(l0), movm_t(h1), movm_t(l1));
         }
+}
+
+__device__ __forceinline__ void stsm4t(uint32_t addr, const uint32_t (&w)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                 : "memory");
+}
+// A warp's 16 tokens of MT tiles of 16 columns, given transposed (words: tokens 0-7 of columns
+// 0-7 and 8-15, tokens 8-15), to rows `row` bytes apart from `at` on, in 16-byte pieces through
+// 512 MT bytes of shared memory: 32 MT bytes of a row leave together (4-byte stores straight
+// from the transposed words cost the walk 200 cycles a step more).  Only `tokens` rows exist;
+// `end` is the size of what lies behind `base`.
+template <int MT>
+__device__ __forceinline__ void store_out(char *stage, const uint32_t (&w)[MT][4], char *at,
+                                          size_t row, int tokens, const char *base, size_t end,
+                                          unsigned *dbg, int lane) {
+    constexpr int kPer = 2 * MT;  // pieces of a row
+    auto off = [](int r, int c) { return (uint32_t)(r * kPer + (c ^ (r / (8 / kPer) % kPer))) * 16; };
+    const uint32_t sm = tc::smem_u32(stage);
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+        stsm4t(sm + off((lane & 7) + (lane >> 4) * 8, 2 * t + ((lane >> 3) & 1)), w[t]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int x = lane + 32 * i, r = x / kPer, c = x % kPer;
+        const uint4 u = *reinterpret_cast<const uint4 *>(stage + off(r, c));
+        char *to = at + r * row + c * 16;
+        if (r < tokens && dbg_ok(dbg, (size_t)(to - base) + 15, end, DBG_STORE))
+            *reinterpret_cast<uint4 *>(to) = u;
+    }
+    __syncwarp();
 }
 
 // A [16 dv, 16 token] accumulator pair as hi/lo planes of rows of tokens, in 8x8 blocks

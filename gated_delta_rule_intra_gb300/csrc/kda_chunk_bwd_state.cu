@@ -91,31 +91,34 @@ __global__ void __launch_bounds__(Roles<NC>::kThreads, 1)
     const Seq sq = seq_of(n, a.T, a.cu_seqlens);
     const int steps = (sq.len + BT - 1) / BT * (BT / C);
 
-    if (role.prep >= 0) {
-        const int tid = role.prep * 32 + lane;
-        if (NC == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
-        for (int i = 0; i < kRaw - 1; ++i) {
-            if (i < steps) load_step<NC>(sm, a, sq, h, hv, dv0, i, steps - 1 - i, tid);
-            cp_async_commit();
+    if (role.feeds) {
+        role.give();
+        if (role.prep >= 0) {
+            const int tid = role.prep * 32 + lane;
+            for (int i = 0; i < kRaw - 1; ++i) {
+                if (i < steps) load_step<NC>(sm, a, sq, h, hv, dv0, i, steps - 1 - i, tid);
+                cp_async_commit();
+            }
+            for (int i = 0; i < steps; ++i) {
+                const int st = i & 1;
+                cp_wait<kRaw - 2>();
+                if (i >= kStages) bar_sync(BAR_EMPTY + st, kPrepThreads + 32 * NC);
+                bar_sync(BAR_PREP, kPrepThreads);
+                if (i + kRaw - 1 < steps)
+                    load_step<NC>(sm, a, sq, h, hv, dv0, i + kRaw - 1, steps - kRaw - i, tid);
+                cp_async_commit();
+                prep_planes<T16, kPrepThreads, false>(sm.raw[i % kRaw], sm.prep[st].planes,
+                                                      sm.prep[st].decay, a.scale, tid);
+                bar_arrive(BAR_FULL + st, kPrepThreads + 32 * NC);
+            }
+            cp_async_wait_all();
+            return;
         }
-        for (int i = 0; i < steps; ++i) {
-            const int st = i & 1;
-            cp_wait<kRaw - 2>();
-            if (i >= kStages) bar_sync(BAR_EMPTY + st, kPrepThreads + 32 * NC);
-            bar_sync(BAR_PREP, kPrepThreads);
-            if (i + kRaw - 1 < steps)
-                load_step<NC>(sm, a, sq, h, hv, dv0, i + kRaw - 1, steps - kRaw - i, tid);
-            cp_async_commit();
-            prep_planes<T16, kPrepThreads, false>(sm.raw[i % kRaw], sm.prep[st].planes,
-                                                  sm.prep[st].decay, a.scale, tid);
-            bar_arrive(BAR_FULL + st, kPrepThreads + 32 * NC);
-        }
-        cp_async_wait_all();
         return;
     }
 
+    role.take();
     if (role.consumer < 0) return;
-    if (NC == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     const int cw = role.consumer, d0 = dv0 + cw * 16;
     const int gr = lane >> 2, tc2 = (lane & 3) * 2;
     const size_t sbase = ((size_t)n * a.HV + hv) * D * D;
@@ -140,7 +143,7 @@ __global__ void __launch_bounds__(Roles<NC>::kThreads, 1)
 
     for (int i = 0; i < steps; ++i) {
         const int st = i & 1, step = steps - 1 - i;
-        const size_t slot = (size_t)(sq.slot0 + step / 4) * a.HV + hv;
+        const unsigned slot = (unsigned)(sq.slot0 + step / 4) * a.HV + hv;
         if (step % 4 == 3) store_checkpoint<1>(a.dckpt + slot * kCkptBytes, Sm, d0 / 16, lane);
         bar_sync(BAR_FULL + st, kPrepThreads + 32 * NC);
         const Prepared &in = sm.prep[st];
@@ -269,8 +272,8 @@ __global__ void __launch_bounds__(Roles<NC>::kThreads, 1)
 template <typename T16, int NC>
 cudaError_t launch(const ChunkBwdArgs &a, int dev, cudaStream_t stream) {
     static volatile int done[kMaxDev];
-    cudaError_t e =
-        smem_limit_once(kda_chunk_bwd_state_kernel<T16, NC>, (int)sizeof(Smem), dev, done);
+    cudaError_t e = ready_once<Roles<NC>>(kda_chunk_bwd_state_kernel<T16, NC>,
+                                            (int)sizeof(Smem), dev, done);
     if (e != cudaSuccess) return e;
     kda_chunk_bwd_state_kernel<T16, NC>
         <<<a.num_seqs * a.HV * (8 / NC), Roles<NC>::kThreads, sizeof(Smem), stream>>>(a);

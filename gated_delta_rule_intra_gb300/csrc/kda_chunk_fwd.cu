@@ -17,8 +17,10 @@ constexpr int kStages = 3;         // prepared stages
 constexpr int kRaw = kStages + 2;  // raw input stages: two ahead, and as far back as a stage lives
 constexpr int kHalf = 128;         // threads of each half of the preparing warps
 
-// Named barriers; PLANES, FULL, EMPTY + stage.
-enum { BAR_PREP = 1, BAR_SCORE = 2, BAR_PLANES = 3, BAR_FULL = 6, BAR_EMPTY = 9 };
+// Named barriers; PLANES, FULL, EMPTY + stage, SOLVE + solver.
+enum { BAR_PREP = 1, BAR_PLANES = 3, BAR_FULL = 6, BAR_EMPTY = 9, BAR_SOLVE = 12 };
+
+constexpr int kSolvers = 4;  // warps that take the steps' systems in turn
 
 struct __align__(128) Prepared {
     char planes[kPlanes * kPlane];
@@ -34,9 +36,11 @@ struct __align__(128) Smem {
     RawStage raw[kRaw];
     uint16_t v[kRaw][C][D];  // rows of the CTA's dv slice, swizzled chunks
     float beta[kRaw][C];
-    float a2[2][C][C + 4];   // M diag(beta), two steps' worth
-    float a1[2][C][C + 4];   // diag(beta) M
-    char t[2 * kTile];       // T hi, lo on the way to the saved tiles
+    float a2[kSolvers][C][C + 4];  // M diag(beta)
+    float a1[kSolvers][C][C + 4];  // diag(beta) M
+    char t[kSolvers][2 * kTile];   // T hi, lo on the way to the saved tiles
+    int bad[kSolvers][4];          // whether a warp has seen an input that is not finite
+    char out[4][2 * 512];          // a consumer's o on its way out
 };
 
 template <int SLICE>
@@ -112,7 +116,7 @@ __device__ __forceinline__ void scores(Smem &sm, Prepared &out, const float *bet
 // Gates so strong that k 2^-g leaves FP32's range inside a step (a channel loses more than
 // 2^-96 in 16 tokens): the key plane in its bounded form, the gate replaced by its cumsum ...
 template <typename T16>
-__device__ __noinline__ void prep_strong(RawStage &raw, Prepared &out, float scale, int tid) {
+__device__ __forceinline__ void prep_strong(RawStage &raw, Prepared &out, float scale, int tid) {
     prep_planes<T16, kHalf, false>(raw, out.planes, out.decay, scale, tid);
     bar_sync(BAR_PREP, kHalf);
     float acc = 0.f;
@@ -122,64 +126,47 @@ __device__ __noinline__ void prep_strong(RawStage &raw, Prepared &out, float sca
 // ... and M and P pair by pair, one exp2 per (r, s, channel), every exponent <= 0: 17 pairs of
 // the rows w and 15 - w a call.  Lane l holds channels 4l .. 4l + 3.
 template <typename T16>
-__device__ __noinline__ void scores_strong(Smem &sm, const RawStage &raw, const float *beta,
-                                           Prepared &out, int buf, float scale, int w, int lane) {
+__device__ __forceinline__ void scores_strong(Smem &sm, const RawStage &raw, const float *beta,
+                                              Prepared &out, int buf, float scale, int w,
+                                              int lane) {
     auto row4 = [&](const uint16_t *p, float (&x)[4]) {
         const uint2 u = *reinterpret_cast<const uint2 *>(p + 4 * lane);
         const float2 lo = unpack2<T16>(u.x), hi = unpack2<T16>(u.y);
         x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
     };
-    float q1[4], k1[4], q2[4], k2[4];
-    const int r1 = w, r2 = C - 1 - w;
-    row4(raw.q[r1], q1);
-    row4(raw.k[r1], k1);
-    row4(raw.q[r2], q2);
-    row4(raw.k[r2], k2);
-    const float4 g1 = *reinterpret_cast<const float4 *>(&raw.gate[r1][4 * lane]);
-    const float4 g2 = *reinterpret_cast<const float4 *>(&raw.gate[r2][4 * lane]);
-    float v[32], lastp = 0.f;
-#pragma unroll
+#pragma unroll 1
     for (int j = 0; j < 17; ++j) {
-        const bool first = j <= w;
-        const int s = first ? j : j - w - 1;
-        float ks[4];
+        const int r = j <= w ? w : C - 1 - w, s = j <= w ? j : j - w - 1;
+        float q[4], k[4], ks[4];
+        row4(raw.q[r], q);
+        row4(raw.k[r], k);
         row4(raw.k[s], ks);
+        const float4 gr = *reinterpret_cast<const float4 *>(&raw.gate[r][4 * lane]);
         const float4 gs = *reinterpret_cast<const float4 *>(&raw.gate[s][4 * lane]);
-        const float4 gr = first ? g1 : g2;
         const float e[4] = {ex2(gr.x - gs.x) * ks[0], ex2(gr.y - gs.y) * ks[1],
                             ex2(gr.z - gs.z) * ks[2], ex2(gr.w - gs.w) * ks[3]};
         float p = 0.f, m = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            p += (first ? q1[i] : q2[i]) * e[i];
-            m += (first ? k1[i] : k2[i]) * e[i];
+            p += q[i] * e[i];
+            m += k[i] * e[i];
         }
-        if (j < 16) {
-            v[2 * j] = p;
-            v[2 * j + 1] = m;
-        } else {
-            lastp = p;  // the pair (r2, r2): only P has a diagonal
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            p += __shfl_xor_sync(0xffffffffu, p, off);
+            m += __shfl_xor_sync(0xffffffffu, m, off);
+        }
+        if (lane == 0) {  // P's entries above the diagonal are zero from the start or scores()
+            uint32_t hi, lo;
+            split2(p * scale, 0.f, hi, lo);
+            reinterpret_cast<uint16_t *>(out.p)[r * C + s] = (uint16_t)hi;
+            reinterpret_cast<uint16_t *>(out.p + kTile)[r * C + s] = (uint16_t)lo;
+            if (s < r) {
+                sm.a2[buf][r][s] = m * beta[s];
+                sm.a1[buf][r][s] = m * beta[r];
+            }
         }
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) lastp += __shfl_xor_sync(0xffffffffu, lastp, off);
-    const float sum = transpose_sum(v, lane);
-    auto put = [&](int r, int s, float x, bool is_p) {
-        if (is_p) {  // the entries above the diagonal are zero from the start or from scores()
-            const uint32_t b = pack_bf16(x * scale, 0.f) & 0xffffu;
-            const float rest = x * scale - __uint_as_float(b << 16);
-            reinterpret_cast<uint16_t *>(out.p)[r * C + s] = (uint16_t)b;
-            reinterpret_cast<uint16_t *>(out.p + kTile)[r * C + s] =
-                (uint16_t)(pack_bf16(rest, 0.f) & 0xffffu);
-        } else if (s < r) {
-            sm.a2[buf][r][s] = x * beta[s];
-            sm.a1[buf][r][s] = x * beta[r];
-        }
-    };
-    const int j = lane >> 1;
-    const bool first = j <= w;
-    put(first ? r1 : r2, first ? j : j - w - 1, sum, !(lane & 1));
-    if (lane == 0) put(r2, r2, lastp, true);
 }
 
 // T2 = (I + M diag(beta))^-1 (lanes 0-15, one column each) and T = (I + diag(beta) M)^-1
@@ -202,7 +189,7 @@ __device__ __forceinline__ void solve(Smem &sm, Prepared &out, int buf, int lane
         }
         x[r] = s;
     }
-    uint16_t *hi = reinterpret_cast<uint16_t *>(second ? sm.t : out.t2);
+    uint16_t *hi = reinterpret_cast<uint16_t *>(second ? sm.t[buf] : out.t2);
     uint16_t *lo = hi + C * C;
 #pragma unroll
     for (int r = 0; r < C; ++r) {
@@ -296,7 +283,8 @@ __device__ __forceinline__ void consume(float (&S)[MT][16][4], float (&xq)[MT][2
             split_frag(S[t][2 * kk], S[t][2 * kk + 1], ah, al);
             mma3x2<true>(xw[t][0], xw[t][1], xq[t][0], xq[t][1], ah, al, kh, kl, ah, al, qh, ql);
             if (CKPT) {
-                uint4 *p = reinterpret_cast<uint4 *>(ckpt) + (2 * kk * 8 + slice_tile + tile + t) * 32 + lane;
+                uint4 *p = reinterpret_cast<uint4 *>(ckpt) +
+                           (2 * kk * 8 + slice_tile + tile + t) * 32 + lane;
                 p[0] = make_uint4(movm_t(ah[0]), movm_t(al[0]), movm_t(ah[1]), movm_t(al[1]));
                 p[8 * 32] = make_uint4(movm_t(ah[2]), movm_t(al[2]), movm_t(ah[3]), movm_t(al[3]));
             }
@@ -386,13 +374,13 @@ __device__ __forceinline__ void consume(float (&S)[MT][16][4], float (&xq)[MT][2
 
 // NW consumer warps of 16 MT dv columns each; a head takes 128 / (16 NW MT) CTAs.
 template <typename T16, int NW, int MT, bool SAVE>
-__global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
+__global__ void __launch_bounds__(Roles<NW, kSolvers>::kThreads, 1)
     kda_chunk_fwd_kernel(const ChunkFwdArgs a) {
     constexpr int kSlice = 16 * NW * MT, kSplit = D / kSlice;
     extern __shared__ __align__(128) char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int lane = threadIdx.x & 31;
-    const Roles<NW> role(warp_index());
+    const Roles<NW, kSolvers> role(warp_index());
     const int unit = blockIdx.x / kSplit, dv0 = (blockIdx.x % kSplit) * kSlice;
     const int n = unit / a.HV, hv = unit - n * a.HV, h = hv / (a.HV / a.H);
     const Seq sq = seq_of(n, a.T, a.cu_seqlens);
@@ -405,74 +393,91 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         reinterpret_cast<uint32_t *>(sm.prep[i / (2 * kTile / 4)].p)[i % (2 * kTile / 4)] = 0u;
     __syncthreads();
 
-    if (role.prep >= 0) {
-        const int tid = role.prep * 32 + lane;
-        if (MT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-        if (tid < kHalf) {  // raw inputs -> operand planes
-            for (int i = 0; i < 2; ++i) {
-                if (i < steps) load_step<kSlice>(sm, a, sq, h, hv, dv0, i, tid);
-                cp_async_commit();
+    if (role.feeds) {
+        role.give();
+        if (role.prep >= 0) {
+            const int tid = role.prep * 32 + lane;
+            if (tid < kHalf) {  // raw inputs -> operand planes
+                for (int i = 0; i < 2; ++i) {
+                    if (i < steps) load_step<kSlice>(sm, a, sq, h, hv, dv0, i, tid);
+                    cp_async_commit();
+                }
+                for (int i = 0; i < steps; ++i) {
+                    const int st = i % kStages;
+                    Prepared &out = sm.prep[st];
+                    RawStage &raw = sm.raw[i % kRaw];
+                    cp_wait<1>();
+                    // the consumers are done with this stage's previous step (and its values)
+                    if (i >= kStages) bar_sync(BAR_EMPTY + st, kHalf + 32 * NW);
+                    bar_sync(BAR_PREP, kHalf);
+                    if (i + 2 < steps) load_step<kSlice>(sm, a, sq, h, hv, dv0, i + 2, tid);
+                    cp_async_commit();
+                    const bool big =
+                        prep_planes<T16, kHalf, true>(raw, out.planes, out.decay, a.scale, tid);
+                    const bool strong = bar_or(BAR_PREP, kHalf, big);
+                    if (strong) prep_strong<T16>(raw, out, a.scale, tid);
+                    if (tid == 0) out.from_start = !strong;
+                    bar_arrive(BAR_PLANES + st, 2 * kHalf);
+                }
+                cp_async_wait_all();
+                return;
             }
+            // planes -> scores
+            const int w = role.prep - kHalf / 32;
             for (int i = 0; i < steps; ++i) {
                 const int st = i % kStages;
                 Prepared &out = sm.prep[st];
-                RawStage &raw = sm.raw[i % kRaw];
-                cp_wait<1>();
-                // the consumers are done with this stage's previous step (and its values)
-                if (i >= kStages) bar_sync(BAR_EMPTY + st, kHalf + 32 * NW);
-                bar_sync(BAR_PREP, kHalf);
-                if (i + 2 < steps) load_step<kSlice>(sm, a, sq, h, hv, dv0, i + 2, tid);
-                cp_async_commit();
-                const bool big = prep_planes<T16, kHalf, true>(raw, out.planes, out.decay, a.scale,
-                                                               tid);
-                const bool strong = bar_or(BAR_PREP, kHalf, big);
-                if (strong) prep_strong<T16>(raw, out, a.scale, tid);
-                if (tid == 0) out.from_start = !strong;
-                bar_arrive(BAR_PLANES + st, 2 * kHalf);
+                const int buf = i % kSolvers;
+                const float *beta = sm.beta[i % kRaw];
+                bar_sync(BAR_PLANES + st, 2 * kHalf);
+                if (uniform(out.from_start)) {
+                    scores(sm, out, beta, buf, w, lane);
+                } else {
+                    scores_strong<T16>(sm, sm.raw[i % kRaw], beta, out, buf, a.scale, w, lane);
+                    scores_strong<T16>(sm, sm.raw[i % kRaw], beta, out, buf, a.scale, w + 4, lane);
+                }
+                const bool bad = __any_sync(
+                    0xffffffffu, not_finite<T16, kSlice>(sm.v[i % kRaw], beta, tid - kHalf));
+                if (lane == 0) sm.bad[buf][w] = bad;
+                bar_arrive(BAR_SOLVE + buf, kHalf + 32);
             }
-            cp_async_wait_all();
             return;
         }
-        // planes -> scores -> T2 and T
-        const int w = role.prep - kHalf / 32;
-        for (int i = 0; i < steps; ++i) {
-            const int st = i % kStages;
-            Prepared &out = sm.prep[st];
-            const float *beta = sm.beta[i % kRaw];
-            bar_sync(BAR_PLANES + st, 2 * kHalf);
-            if (uniform(out.from_start)) {
-                scores(sm, out, beta, i & 1, w, lane);
-            } else {
-                scores_strong<T16>(sm, sm.raw[i % kRaw], beta, out, i & 1, a.scale, w, lane);
-                scores_strong<T16>(sm, sm.raw[i % kRaw], beta, out, i & 1, a.scale, w + 4, lane);
-            }
-            const bool bad = bar_or(
-                BAR_SCORE, kHalf, not_finite<T16, kSlice>(sm.v[i % kRaw], beta, tid - kHalf));
-            if (w == 0) {
-                if (lane == 0) out.careful = bad || !out.from_start;
-                if (SAVE || lane < 16) solve(sm, out, i & 1, lane);
+        if (role.solver >= 0) {  // scores -> T2 and T
+            const int w = role.solver;
+            for (int i = w; i < steps; i += kSolvers) {
+                const int st = i % kStages;
+                Prepared &out = sm.prep[st];
+                bar_sync(BAR_SOLVE + w, kHalf + 32);
+                const uint4 *p = reinterpret_cast<const uint4 *>(out.p);
+                const uint4 p0 = p[lane], p1 = p[32 + lane];
+                if (lane == 0) {
+                    const int *bad = sm.bad[w];
+                    out.careful = bad[0] || bad[1] || bad[2] || bad[3] || !out.from_start;
+                }
+                if (SAVE || lane < 16) solve(sm, out, w, lane);
                 __syncwarp();
                 bar_arrive(BAR_FULL + st, 32 + 32 * NW);
                 if (SAVE && dv0 == 0) {
                     uint4 *to = reinterpret_cast<uint4 *>(
                         a.tiles +
                         (((size_t)(sq.slot0 + i / 4) * a.HV + hv) * 4 + i % 4) * kTilesBytes);
-                    const uint4 *t = reinterpret_cast<const uint4 *>(sm.t);
-                    const uint4 *p = reinterpret_cast<const uint4 *>(out.p);
+                    const uint4 *t = reinterpret_cast<const uint4 *>(sm.t[w]);
                     to[lane] = t[lane];
                     to[32 + lane] = t[32 + lane];
-                    to[64 + lane] = p[lane];
-                    to[96 + lane] = p[32 + lane];
+                    to[64 + lane] = p0;
+                    to[96 + lane] = p1;
                     __syncwarp();
                 }
             }
+            return;
         }
         return;
     }
 
     // ------------------------------------------------------------------ consumers
+    role.take();
     if (role.consumer < 0) return;
-    if (MT > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
     const int cw = role.consumer, d0 = dv0 + cw * MT * 16;  // this warp's first dv column
     const int gr = lane >> 2, tc2 = (lane & 3) * 2;
     const size_t sbase = ((size_t)n * a.HV + hv) * D * D;
@@ -492,9 +497,12 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
             }
         }
 
+    const size_t orow = (size_t)a.HV * D;
+    uint16_t *o_at = (uint16_t *)a.o + (size_t)sq.row0 * orow + (size_t)hv * D + d0;
+
     for (int i = 0; i < steps; ++i) {
         const int st = i % kStages;
-        const size_t slot = (size_t)(sq.slot0 + i / 4) * a.HV + hv;
+        const unsigned slot = (unsigned)(sq.slot0 + i / 4) * a.HV + hv;
         float xq[MT][2][4], e[MT][2][4];
         bar_sync(BAR_FULL + st, 32 + 32 * NW);
         const Prepared &in = sm.prep[st];
@@ -517,24 +525,20 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
             run(std::true_type{}, std::false_type{});
         }
         if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kHalf + 32 * NW);
+        if (SAVE)
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            if (SAVE) store_rows(a.e + slot * kRowsBytes, e[t], (i % 4) * C, d0 + 16 * t, lane);
+            for (int t = 0; t < MT; ++t)
+                store_rows(a.e + slot * kRowsBytes, e[t], (i % 4) * C, d0 + 16 * t, lane);
+        uint32_t ow[MT][4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {  // o: rows of tokens after the transpose
-                const uint32_t x = movm_t(pack2<T16>(xq[t][j][0], xq[t][j][1]));
-                const uint32_t y = movm_t(pack2<T16>(xq[t][j][2], xq[t][j][3]));
-                const int tok = i * C + 8 * j + gr;
-                if (tok < sq.len) {
-                    const size_t idx =
-                        ((size_t)(sq.row0 + tok) * a.HV + hv) * D + d0 + 16 * t + tc2;
-                    if (dbg_ok(a.dbg, idx + 9, a.rows_o * D, DBG_STORE)) {
-                        *reinterpret_cast<uint32_t *>((uint16_t *)a.o + idx) = x;
-                        *reinterpret_cast<uint32_t *>((uint16_t *)a.o + idx + 8) = y;
-                    }
-                }
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                ow[t][2 * j] = pack2<T16>(xq[t][j][0], xq[t][j][1]);
+                ow[t][2 * j + 1] = pack2<T16>(xq[t][j][2], xq[t][j][3]);
             }
-        }
+        store_out<MT>(sm.out[cw], ow, (char *)(o_at + (size_t)i * C * orow), orow * 2,
+                      sq.len - i * C, (char *)a.o, a.rows_o * D * 2, a.dbg, lane);
     }
     if (a.final_state) {
 #pragma unroll
@@ -553,12 +557,12 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
 template <typename T16, int NW, int MT, bool SAVE>
 cudaError_t launch(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
     static volatile int done[kMaxDev];
-    cudaError_t e =
-        smem_limit_once(kda_chunk_fwd_kernel<T16, NW, MT, SAVE>, (int)sizeof(Smem), dev, done);
+    cudaError_t e = ready_once<Roles<NW, kSolvers>>(kda_chunk_fwd_kernel<T16, NW, MT, SAVE>,
+                                            (int)sizeof(Smem), dev, done);
     if (e != cudaSuccess) return e;
     const int grid = a.num_seqs * a.HV * (D / (16 * NW * MT));
     kda_chunk_fwd_kernel<T16, NW, MT, SAVE>
-        <<<grid, Roles<NW>::kThreads, sizeof(Smem), stream>>>(a);
+        <<<grid, Roles<NW, kSolvers>::kThreads, sizeof(Smem), stream>>>(a);
     return cudaGetLastError();
 }
 

@@ -352,6 +352,17 @@ __device__ __forceinline__ float join_scale(Tile &t, float nmax, float sum) {
     return ratio;
 }
 
+// The tile as an operand, kept as the state at the slot's start.
+__device__ __forceinline__ void store_tile(char *ckpt, const Tile &t, int tile, int lane) {
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+        const float(&x)[4] = t.s[2 * kk], (&y)[4] = t.s[2 * kk + 1];
+        reinterpret_cast<uint4 *>(ckpt)[(tile * 8 + kk) * 32 + lane] =
+            make_uint4(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]), pack_f16(y[0], y[1]),
+                       pack_f16(y[2], y[3]));
+    }
+}
+
 // A [16 dv, 16 token] accumulator pair as the slot's FP16 block of a step and tile: a lane's
 // words are (row lane / 4, tokens 2 (lane % 4), + 1), the row 8 below, and the same of tokens
 // 8 - 15.  Returns the scale.

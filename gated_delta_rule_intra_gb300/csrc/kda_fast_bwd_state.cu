@@ -28,6 +28,7 @@ struct __align__(128) Smem {
     uint16_t dout[kRaw][C][D];  // rows of the CTA's dv slice, swizzled chunks
     char tiles[kRaw][2 * kTall];
     float beta[kRaw][C];
+    char out[4][2 * 512];  // a consumer's dv on its way out
 };
 
 // Step i of the walk (the last step of the sequence first), tokens 16 * step on.
@@ -70,40 +71,44 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
     const Seq sq = chunk::seq_of(n, a.T, a.cu_seqlens);
     const int steps = (sq.len + BT - 1) / BT * (BT / C);
 
-    if (role.prep >= 0) {
-        if (MT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-        // two groups of four warps take the steps in turn
-        const int group = role.prep >> 2, tid = (role.prep & 3) * 32 + lane;
-        if (group < steps) load_step<kSlice>(sm, a, sq, h, hv, dv0, group, steps - 1 - group, tid);
-        cp_async_commit();
-        for (int i = group; i < steps; i += 2) {
-            const int st = i % kStages;
-            Planes &out = sm.stage[st];
-            // the consumers are done with this stage's previous step and its inputs, whose
-            // place the step after next takes
-            if (i >= kStages) bar_sync(BAR_EMPTY + st, kHalf + 32 * NW);
-            if (i + 2 < steps)
-                load_step<kSlice>(sm, a, sq, h, hv, dv0, i + 2, steps - 3 - i, tid);
+    if (role.feeds) {
+        role.give();
+        if (role.prep >= 0) {
+            // two groups of four warps take the steps in turn
+            const int group = role.prep >> 2, tid = (role.prep & 3) * 32 + lane;
+            if (group < steps)
+                load_step<kSlice>(sm, a, sq, h, hv, dv0, group, steps - 1 - group, tid);
             cp_async_commit();
-            cp_async_wait_newest<1>();
-            bar_sync(BAR_PREP + group, kHalf);
-            prepare<false>(sm.raw[i % kRaw], out, nullptr, a.scale, tid);
-            if (tid < 32) {
-                const float bm =
-                    warp_max(lane < C ? fabsf(sm.beta[i % kRaw][lane]) : 0.f);
-                if (lane == 0) {
-                    out.bmax = bm;
-                    out.careful = !finite(bm);
+            for (int i = group; i < steps; i += 2) {
+                const int st = i % kStages;
+                Planes &out = sm.stage[st];
+                // the consumers are done with this stage's previous step and its inputs, whose
+                // place the step after next takes
+                if (i >= kStages) bar_sync(BAR_EMPTY + st, kHalf + 32 * NW);
+                if (i + 2 < steps)
+                    load_step<kSlice>(sm, a, sq, h, hv, dv0, i + 2, steps - 3 - i, tid);
+                cp_async_commit();
+                cp_async_wait_newest<1>();
+                bar_sync(BAR_PREP + group, kHalf);
+                prepare<false>(sm.raw[i % kRaw], out, nullptr, a.scale, tid);
+                if (tid < 32) {
+                    const float bm =
+                        warp_max(lane < C ? fabsf(sm.beta[i % kRaw][lane]) : 0.f);
+                    if (lane == 0) {
+                        out.bmax = bm;
+                        out.careful = !finite(bm);
+                    }
                 }
+                bar_arrive(BAR_FULL + st, kHalf + 32 * NW);
             }
-            bar_arrive(BAR_FULL + st, kHalf + 32 * NW);
+            cp_async_wait_all();
+            return;
         }
-        cp_async_wait_all();
         return;
     }
 
+    role.take();
     if (role.consumer < 0) return;
-    if (MT > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
     const int tile0 = dv0 / 16 + role.consumer * MT;
     const int gr = lane >> 2, tc2 = (lane & 3) * 2;
     const int lrow = (lane & 7) + ((lane >> 4) & 1) * 8, lcol = (lane >> 3) & 1;
@@ -126,11 +131,11 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         }
     }
     const size_t vrow = (size_t)a.HV * D;
-    uint16_t *dv_at = (uint16_t *)a.dv + (size_t)sq.row0 * vrow + (size_t)hv * D + tile0 * 16 + tc2;
+    uint16_t *dv_at = (uint16_t *)a.dv + (size_t)sq.row0 * vrow + (size_t)hv * D + tile0 * 16;
 
     for (int i = 0; i < steps; ++i) {
         const int st = i % kStages, slot = i % kRaw, step = steps - 1 - i;
-        const size_t unit_at = (size_t)(sq.slot0 + step / 4) * a.HV + hv;
+        const unsigned unit_at = (unsigned)(sq.slot0 + step / 4) * a.HV + hv;
         const bool keep = step % 4 == 3;
         bar_sync(BAR_FULL + st, kHalf + 32 * NW);
         const Planes &in = sm.stage[st];
@@ -169,12 +174,12 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
                                         pack_f16(y[0], y[1]), pack_f16(y[2], y[3])};
                 mma_f16(ds[t][0], af, kf[0], kf[1]);
                 mma_f16(ds[t][1], af, kf[2], kf[3]);
-                if (keep)  // the operand is the checkpoint
-                    reinterpret_cast<uint4 *>(a.dckpt + unit_at * kCkptBytes)
-                        [((tile0 + t) * 8 + kk) * 32 + lane] =
-                            make_uint4(af[0], af[1], af[2], af[3]);
             }
         }
+        if (keep)  // outside the loop above, which a branch would cut into pieces
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+                store_tile(a.dckpt + unit_at * kCkptBytes, S[t], tile0 + t, lane);
         float y[MT][2][4] = {}, ym[MT], ckpt_scale[MT];
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
@@ -252,32 +257,26 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
             }
         }
         if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kHalf + 32 * NW);
+        float s[MT];
+        uint32_t dw[MT][4];  // dv = beta Y
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            const float s = store_block(a.y + unit_at * kRowsBytes, y[t], ym[t],
-                                        (step % 4) * 8 + tile0 + t, lane);
-            if (lane == 0) {
-                float *scales = a.dscales + unit_at * kScales;
-                scales[8 + (step % 4) * 8 + tile0 + t] = s;
-                if (keep) scales[tile0 + t] = ckpt_scale[t];
-            }
+            s[t] = store_block(a.y + unit_at * kRowsBytes, y[t], ym[t],
+                               (step % 4) * 8 + tile0 + t, lane);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {  // dv = beta Y
-                const uint32_t u =
-                    chunk::movm_t(chunk::pack_bf16(b[j].x * y[t][j][0], b[j].y * y[t][j][1]));
-                const uint32_t w =
-                    chunk::movm_t(chunk::pack_bf16(b[j].x * y[t][j][2], b[j].y * y[t][j][3]));
-                const int tok = step * C + 8 * j + gr;
-                if (tok < sq.len) {
-                    uint16_t *at = dv_at + (size_t)tok * vrow + 16 * t;
-                    if (dbg_ok(a.dbg, (size_t)(at - (uint16_t *)a.dv) + 9, a.rows_o * D,
-                               DBG_STORE)) {
-                        *reinterpret_cast<uint32_t *>(at) = u;
-                        *reinterpret_cast<uint32_t *>(at + 8) = w;
-                    }
-                }
+            for (int j = 0; j < 2; ++j) {
+                dw[t][2 * j] = chunk::pack_bf16(b[j].x * y[t][j][0], b[j].y * y[t][j][1]);
+                dw[t][2 * j + 1] = chunk::pack_bf16(b[j].x * y[t][j][2], b[j].y * y[t][j][3]);
             }
         }
+        if (lane < MT) {
+            float *scales = a.dscales + unit_at * kScales + tile0 + lane;
+            scales[8 + (step % 4) * 8] = lane ? s[MT - 1] : s[0];
+            if (keep) scales[0] = lane ? ckpt_scale[MT - 1] : ckpt_scale[0];
+        }
+        chunk::store_out<MT>(sm.out[role.consumer], dw, (char *)(dv_at + (size_t)step * C * vrow),
+                             vrow * 2, sq.len - step * C, (char *)a.dv, a.rows_o * D * 2, a.dbg,
+                             lane);
     }
     if (a.d_initial_state) {
 #pragma unroll
@@ -296,8 +295,8 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
 template <int NW, int MT>
 cudaError_t launch(const ChunkBwdArgs &a, int dev, cudaStream_t stream) {
     static volatile int done[kMaxDev];
-    cudaError_t e =
-        smem_limit_once(kda_fast_bwd_state_kernel<NW, MT>, (int)sizeof(Smem), dev, done);
+    cudaError_t e = chunk::ready_once<Roles<NW>>(kda_fast_bwd_state_kernel<NW, MT>,
+                                            (int)sizeof(Smem), dev, done);
     if (e != cudaSuccess) return e;
     kda_fast_bwd_state_kernel<NW, MT><<<a.num_seqs * a.HV * (D / (16 * NW * MT)),
                                         Roles<NW>::kThreads, sizeof(Smem), stream>>>(a);

@@ -14,15 +14,17 @@ using chunk::cp16z;
 using chunk::ldsm4;
 using chunk::ldsm4t;
 using chunk::plane_off;
-using chunk::Roles;
 using chunk::Seq;
 using tc::smem_u32;
 
 constexpr int kStages = 3;         // prepared stages
 constexpr int kRaw = kStages + 2;  // raw input stages: two ahead, and as far back as a stage lives
 
-// Named barriers; PLANES, FULL, EMPTY + stage.
-enum { BAR_PREP = 1, BAR_SCORE = 2, BAR_PLANES = 3, BAR_FULL = 6, BAR_EMPTY = 9 };
+// Named barriers; PLANES, FULL, EMPTY + stage, SOLVE + solver.
+enum { BAR_PREP = 1, BAR_SCORE = 2, BAR_PLANES = 3, BAR_FULL = 6, BAR_EMPTY = 9, BAR_SOLVE = 12 };
+
+constexpr int kSolvers = 4;  // warps that take the steps' systems in turn
+template <int NW> using Roles = chunk::Roles<NW, kSolvers>;
 
 struct __align__(128) Stage {
     Planes pl;
@@ -37,10 +39,12 @@ struct __align__(128) Smem {
     RawStage raw[kRaw];
     uint16_t v[kRaw][C][D];  // rows of the CTA's dv slice, swizzled chunks
     float beta[kRaw][C];
-    float4 part[4][4][32];   // scores of a quarter of the channels
-    float a2[2][C][C + 4];   // (M diag(beta))^T, two steps' worth
-    float a1[2][C][C + 4];   // (diag(beta) M)^T
-    char pt[2][kTall];       // P^T on its way to the saved tiles
+    float4 part[2][4][4][32];      // scores of a quarter of the channels, two steps' worth
+    float a2[kSolvers][C][C + 4];  // (M diag(beta))^T
+    float a1[kSolvers][C][C + 4];  // (diag(beta) M)^T
+    char pt[kSolvers][kTall];      // P^T on its way to the saved tiles
+    int big[kSolvers][4];          // whether a warp's entries of P are out of FP16's reach
+    char out[4][2 * 512];          // a consumer's o on its way out
 };
 
 // A preparing thread's pointers to the raw inputs; step s is `s` steps further on.
@@ -122,12 +126,12 @@ __device__ __forceinline__ bool scores(Smem &sm, Stage &out, const RawStage &raw
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        sm.part[w][i][lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        sm.part[buf & 1][w][i][lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
     bar_sync(BAR_SCORE, kHalf);
     float x[4] = {};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float4 y = sm.part[i][w][lane];
+        const float4 y = sm.part[buf & 1][i][w][lane];
         x[0] += y.x; x[1] += y.y; x[2] += y.z; x[3] += y.w;
     }
     bool big = false;
@@ -148,18 +152,18 @@ __device__ __forceinline__ bool scores(Smem &sm, Stage &out, const RawStage &raw
 
 // The same where 2^-g would leave FP32's range: pair by pair, one exp2 per (r, s, channel),
 // every exponent <= 0.  17 pairs of the rows w and 15 - w a call; lane l holds channels 4l on.
-__device__ __noinline__ bool scores_strong(Smem &sm, Stage &out, const RawStage &raw,
-                                           const float *beta, int buf, float scale, int w,
-                                           int lane) {
+__device__ __forceinline__ bool scores_strong(Smem &sm, Stage &out, const RawStage &raw,
+                                              const float *beta, int buf, float scale, int w,
+                                              int lane) {
     auto row4 = [&](const uint16_t *p, float (&x)[4]) {
         const uint2 u = *reinterpret_cast<const uint2 *>(p + 4 * lane);
         const float2 lo = bf2(u.x), hi = bf2(u.y);
         x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
     };
     bool big = false;
-    const int r1 = w, r2 = C - 1 - w;
+#pragma unroll 1
     for (int j = 0; j < 17; ++j) {
-        const int r = j <= w ? r1 : r2, s = j <= w ? j : j - w - 1;
+        const int r = j <= w ? w : C - 1 - w, s = j <= w ? j : j - w - 1;
         float q[4], k[4], ks[4];
         row4(raw.q[r], q);
         row4(raw.k[r], k);
@@ -227,7 +231,8 @@ __device__ __forceinline__ void solve(Smem &sm, Stage &out, int buf, char *tiles
 
 // NW consumer warps of 16 MT dv columns each; a head takes 128 / (16 NW MT) CTAs.
 template <int NW, int MT, bool SAVE>
-__global__ void __launch_bounds__(Roles<NW>::kThreads, 1) kda_fast_fwd_kernel(const ChunkFwdArgs a) {
+__global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
+    kda_fast_fwd_kernel(const ChunkFwdArgs a) {
     constexpr int kSlice = 16 * NW * MT, kSplit = D / kSlice;
     extern __shared__ __align__(128) char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
@@ -240,91 +245,107 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1) kda_fast_fwd_kernel(co
     // computed as zeros, so every row of a slot is defined
     const int steps = SAVE ? (sq.len + BT - 1) / BT * (BT / C) : (sq.len + C - 1) / C;
 
-    if (role.prep >= 0) {
-        const int tid = role.prep * 32 + lane;
-        if (MT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-        if (tid < kHalf) {  // raw inputs -> operand planes
-            const Loader<kSlice> in(a, sq, h, hv, dv0, tid);
-            for (int i = 0; i < 2; ++i) {
-                if (i < steps) in.load(sm, a, i);
-                cp_async_commit();
+    if (role.feeds) {
+        role.give();
+        if (role.prep >= 0) {
+            const int tid = role.prep * 32 + lane;
+            if (tid < kHalf) {  // raw inputs -> operand planes
+                const Loader<kSlice> in(a, sq, h, hv, dv0, tid);
+                for (int i = 0; i < 2; ++i) {
+                    if (i < steps) in.load(sm, a, i);
+                    cp_async_commit();
+                }
+                for (int i = 0; i < steps; ++i) {
+                    const int st = i % kStages;
+                    Stage &out = sm.stage[st];
+                    cp_async_wait_newest<1>();
+                    // the consumers are done with this stage's previous step (and its inputs)
+                    if (i >= kStages) bar_sync(BAR_EMPTY + st, kHalf + 32 * NW);
+                    bar_sync(BAR_PREP, kHalf);
+                    if (i + 2 < steps) in.load(sm, a, i + 2);
+                    cp_async_commit();
+                    const bool strong =
+                        prepare<true>(sm.raw[i % kRaw], out.pl, out.g, a.scale, tid);
+                    const bool any = bar_or(BAR_PREP, kHalf, strong);
+                    if (tid == 0) out.strong = any;
+                    bar_arrive(BAR_PLANES + st, 2 * kHalf);
+                }
+                cp_async_wait_all();
+                return;
             }
+            // planes -> scores
+            const int w = role.prep - kHalf / 32;
             for (int i = 0; i < steps; ++i) {
                 const int st = i % kStages;
                 Stage &out = sm.stage[st];
-                cp_async_wait_newest<1>();
-                // the consumers are done with this stage's previous step (and its inputs)
-                if (i >= kStages) bar_sync(BAR_EMPTY + st, kHalf + 32 * NW);
-                bar_sync(BAR_PREP, kHalf);
-                if (i + 2 < steps) in.load(sm, a, i + 2);
-                cp_async_commit();
-                const bool strong =
-                    prepare<true>(sm.raw[i % kRaw], out.pl, out.g, a.scale, tid);
-                const bool any = bar_or(BAR_PREP, kHalf, strong);
-                if (tid == 0) out.strong = any;
-                bar_arrive(BAR_PLANES + st, 2 * kHalf);
+                const int buf = i % kSolvers;
+                const float *beta = sm.beta[i % kRaw];
+                const RawStage &raw = sm.raw[i % kRaw];
+                bar_sync(BAR_PLANES + st, 2 * kHalf);
+                bool big;
+                if (!chunk::uniform(out.strong)) {
+                    big = scores(sm, out, raw, beta, buf, a.scale, w, lane);
+                } else {
+                    big = scores_strong(sm, out, raw, beta, buf, a.scale, w, lane);
+                    big = scores_strong(sm, out, raw, beta, buf, a.scale, w + 4, lane) || big;
+                }
+                big = __any_sync(0xffffffffu, big);
+                if (lane == 0) sm.big[buf][w] = big;
+                bar_arrive(BAR_SOLVE + buf, kHalf + 32);
             }
-            cp_async_wait_all();
             return;
         }
-        // planes -> scores -> T2 and T
-        const int w = role.prep - kHalf / 32;
-        for (int i = 0; i < steps; ++i) {
-            const int st = i % kStages;
-            Stage &out = sm.stage[st];
-            const float *beta = sm.beta[i % kRaw];
-            const RawStage &raw = sm.raw[i % kRaw];
-            bar_sync(BAR_PLANES + st, 2 * kHalf);
-            bool big;
-            if (!chunk::uniform(out.strong)) {
-                big = scores(sm, out, raw, beta, i & 1, a.scale, w, lane);
-            } else {
-                big = scores_strong(sm, out, raw, beta, i & 1, a.scale, w, lane);
-                big = scores_strong(sm, out, raw, beta, i & 1, a.scale, w + 4, lane) || big;
-            }
-            big = bar_or(BAR_SCORE, kHalf, big);
-            if (w == 0) {
+        if (role.solver >= 0) {  // scores -> T2 and T
+            const int w = role.solver;
+            for (int i = w; i < steps; i += kSolvers) {
+                const int st = i % kStages;
+                Stage &out = sm.stage[st];
+                const float *beta = sm.beta[i % kRaw];
                 char *tiles = nullptr;
                 if (SAVE && dv0 == 0)
                     tiles = a.tiles + ((size_t)(sq.slot0 + i / 4) * a.HV + hv) * kTilesBytes +
                             (i % 4) * 2 * kTall;
-                if (SAVE || lane < 16) solve(sm, out, i & 1, tiles, lane);
-                const float bm =
-                    warp_max(lane < C ? fabsf(beta[lane]) : 0.f);
-                if (lane == 0) out.pl.bmax = bm;
-                if (lane == 0)
-                    out.pl.careful = big || !finite(bm) || !(largest(out.pl.kmax) <= 16384.f) ||
+                bar_sync(BAR_SOLVE + w, kHalf + 32);
+                const uint4 *p = reinterpret_cast<const uint4 *>(sm.pt[w]);
+                const uint4 p0 = p[lane], p1 = p[32 + lane];
+                const float bm = warp_max(lane < C ? fabsf(beta[lane]) : 0.f);
+                if (lane == 0) {
+                    const int *big = sm.big[w];
+                    out.pl.bmax = bm;
+                    out.pl.careful = big[0] || big[1] || big[2] || big[3] || !finite(bm) ||
+                                     !(largest(out.pl.kmax) <= 16384.f) ||
                                      !(a.scale * largest(out.pl.qmax) <= 16384.f);
+                }
+                if (SAVE || lane < 16) solve(sm, out, w, tiles, lane);
                 __syncwarp();
                 bar_arrive(BAR_FULL + st, 32 + 32 * NW);
                 if (tiles) {
                     uint4 *to = reinterpret_cast<uint4 *>(tiles + kTall);
-                    const uint4 *p = reinterpret_cast<const uint4 *>(sm.pt[i & 1]);
-                    to[lane] = p[lane];
-                    to[32 + lane] = p[32 + lane];
-                    __syncwarp();
+                    to[lane] = p0;
+                    to[32 + lane] = p1;
                 }
             }
+            return;
         }
         return;
     }
 
     // ------------------------------------------------------------------ consumers
+    role.take();
     if (role.consumer < 0) return;
-    if (MT > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
     const int tile0 = dv0 / 16 + role.consumer * MT;  // the head's tile of 16 dv columns
-    const int gr = lane >> 2, tc2 = (lane & 3) * 2;
+    const int tc2 = (lane & 3) * 2;
     const int lrow = (lane & 7) + ((lane >> 4) & 1) * 8, lcol = (lane >> 3) & 1;
     const int trow = lane & 15, tcol = lane >> 4;
     Tile S[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) S[t].clear();
     const size_t orow = (size_t)a.HV * D;
-    uint16_t *o_at = (uint16_t *)a.o + (size_t)sq.row0 * orow + (size_t)hv * D + tile0 * 16 + tc2;
+    uint16_t *o_at = (uint16_t *)a.o + (size_t)sq.row0 * orow + (size_t)hv * D + tile0 * 16;
 
     for (int i = 0; i < steps; ++i) {
         const int st = i % kStages, slot = i % kRaw;
-        const size_t unit_at = (size_t)(sq.slot0 + i / 4) * a.HV + hv;
+        const unsigned unit_at = (unsigned)(sq.slot0 + i / 4) * a.HV + hv;
         bar_sync(BAR_FULL + st, 32 + 32 * NW);
         const Stage &in = sm.stage[st];
         const float *beta = sm.beta[slot];
@@ -356,12 +377,12 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1) kda_fast_fwd_kernel(co
                 mma_f16(xw[t][1], af, kf[2], kf[3]);
                 mma_f16(xq[t][0], af, qf[0], qf[1]);
                 mma_f16(xq[t][1], af, qf[2], qf[3]);
-                if (keep)  // the operand is the checkpoint
-                    reinterpret_cast<uint4 *>(a.ckpt + unit_at * kCkptBytes)
-                        [((tile0 + t) * 8 + kk) * 32 + lane] =
-                            make_uint4(af[0], af[1], af[2], af[3]);
             }
         }
+        if (keep)  // outside the loop above, which a branch would cut into pieces
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+                store_tile(a.ckpt + unit_at * kCkptBytes, S[t], tile0 + t, lane);
         float em[MT], ckpt_scale[MT], inv[MT];  // of the state as it was an operand
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
@@ -442,40 +463,36 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1) kda_fast_fwd_kernel(co
             }
         }
         if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kHalf + 32 * NW);
+        if (SAVE) {
+            float s[MT];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            if (SAVE) {
-                const float s = store_block(a.e + unit_at * kRowsBytes, e[t], em[t],
-                                            (i % 4) * 8 + tile0 + t, lane);
-                if (lane == 0) {
-                    float *scales = a.scales + unit_at * kScales;
-                    scales[8 + (i % 4) * 8 + tile0 + t] = s;
-                    if (keep) scales[tile0 + t] = ckpt_scale[t];
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {  // o: rows of tokens after the transpose
-                const uint32_t x = chunk::movm_t(chunk::pack_bf16(xq[t][j][0], xq[t][j][1]));
-                const uint32_t y = chunk::movm_t(chunk::pack_bf16(xq[t][j][2], xq[t][j][3]));
-                const int tok = i * C + 8 * j + gr;
-                if (tok < sq.len) {
-                    uint16_t *at = o_at + (size_t)tok * orow + 16 * t;
-                    if (dbg_ok(a.dbg, (size_t)(at - (uint16_t *)a.o) + 9, a.rows_o * D,
-                               DBG_STORE)) {
-                        *reinterpret_cast<uint32_t *>(at) = x;
-                        *reinterpret_cast<uint32_t *>(at + 8) = y;
-                    }
-                }
+            for (int t = 0; t < MT; ++t)
+                s[t] = store_block(a.e + unit_at * kRowsBytes, e[t], em[t],
+                                   (i % 4) * 8 + tile0 + t, lane);
+            if (lane < MT) {
+                float *scales = a.scales + unit_at * kScales + tile0 + lane;
+                scales[8 + (i % 4) * 8] = lane ? s[MT - 1] : s[0];
+                if (keep) scales[0] = lane ? ckpt_scale[MT - 1] : ckpt_scale[0];
             }
         }
+        uint32_t ow[MT][4];
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                ow[t][2 * j] = chunk::pack_bf16(xq[t][j][0], xq[t][j][1]);
+                ow[t][2 * j + 1] = chunk::pack_bf16(xq[t][j][2], xq[t][j][3]);
+            }
+        chunk::store_out<MT>(sm.out[role.consumer], ow, (char *)(o_at + (size_t)i * C * orow),
+                             orow * 2, sq.len - i * C, (char *)a.o, a.rows_o * D * 2, a.dbg, lane);
     }
 }
 
 template <int NW, int MT, bool SAVE>
 cudaError_t launch(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
     static volatile int done[kMaxDev];
-    cudaError_t e =
-        smem_limit_once(kda_fast_fwd_kernel<NW, MT, SAVE>, (int)sizeof(Smem), dev, done);
+    cudaError_t e = chunk::ready_once<Roles<NW>>(kda_fast_fwd_kernel<NW, MT, SAVE>,
+                                            (int)sizeof(Smem), dev, done);
     if (e != cudaSuccess) return e;
     const int grid = a.num_seqs * a.HV * (D / (16 * NW * MT));
     kda_fast_fwd_kernel<NW, MT, SAVE><<<grid, Roles<NW>::kThreads, sizeof(Smem), stream>>>(a);
