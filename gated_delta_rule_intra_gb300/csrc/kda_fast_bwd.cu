@@ -37,6 +37,8 @@ struct __align__(128) Smem {
     float beta[BT], diag[BT];           // diag: do_t.e_t
     char g1[4][2 * kTile], g2[4][2 * kTile];  // BF16 hi, lo of each step, zero from the diagonal on
     float col[4][8][kThreads];          // dk_col from R to F, each thread's own
+    uint4 state[8][kThreads];           // a saved state on its way, each thread's own part
+    char out[3][kThreads / 32][512];    // a warp's dq, dk, dgate of a step on their way out
     uint32_t omax[4];                   // largest |do| of a step
 };
 
@@ -129,6 +131,38 @@ __device__ __noinline__ void pairs_strong(Smem &sm, int j, int c0, int lane, flo
     }
 }
 
+__device__ __forceinline__ void prefetch_line(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
+// The tokens of unit u (a slot of a value head); rows <= 0 where there are none.
+struct Where {
+    long long row0;
+    int rows, h, hv;
+};
+__device__ __forceinline__ Where locate(const ChunkBwdArgs &a, unsigned u) {
+    Where w;
+    const int slot = (int)(u / (unsigned)a.HV);
+    w.hv = (int)u - slot * a.HV;
+    w.h = w.hv / (a.HV / a.H);
+    int n;  // the slot's sequence
+    if (a.cu_seqlens) {
+        int lo = 0, hi = a.num_seqs - 1;
+        while (lo < hi) {  // the last sequence whose slots begin at or before this one
+            const int mid = (lo + hi + 1) / 2;
+            if (chunk::seq_of(mid, a.T, a.cu_seqlens).slot0 <= slot) lo = mid; else hi = mid - 1;
+        }
+        n = lo;
+    } else {
+        n = slot / ((a.T + BT - 1) / BT);
+    }
+    const Seq sq = chunk::seq_of(n, a.T, a.cu_seqlens);
+    const int t0 = (slot - sq.slot0) * BT;
+    w.row0 = sq.row0 + t0;
+    w.rows = t0 < 0 ? 0 : min(BT, sq.len - t0);
+    return w;
+}
+
 __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBwdArgs a) {
     extern __shared__ __align__(128) char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
@@ -139,32 +173,48 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
     // lanes' offsets of a [16][16] tile as right operand: rows as columns, or rows summed over
     const uint32_t tn = chunk::tile_lane(lane);
     const uint32_t tt = (uint32_t)(((lane & 7) + ((lane >> 3) & 1) * 8) * 32 + (lane >> 4) * 16);
-    const long long units = (long long)a.slots * a.HV;
+    // a unit's saved blocks take 57 KB, so that their number is far below 2^31
+    const unsigned units = (unsigned)a.slots * a.HV;
 
-    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-        const int slot = (int)(u / a.HV), hv = (int)(u - (long long)slot * a.HV);
-        const int h = hv / (a.HV / a.H);
-        int n;  // the slot's sequence
-        if (a.cu_seqlens) {
-            int lo = 0, hi = a.num_seqs - 1;
-            while (lo < hi) {  // the last sequence whose slots begin at or before this one
-                const int mid = (lo + hi + 1) / 2;
-                if (chunk::seq_of(mid, a.T, a.cu_seqlens).slot0 <= slot) lo = mid; else hi = mid - 1;
+    // a thread's words of a saved state, asked for long before they are used
+    auto fetch_state = [&](const char *base, unsigned u) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            cp_async16(&sm.state[t][tid], base + (size_t)u * kCkptBytes + (t * kThreads + tid) * 16);
+        cp_async_commit();
+    };
+
+    Where next = locate(a, blockIdx.x);
+    fetch_state(a.dckpt, blockIdx.x);
+    for (unsigned u = blockIdx.x; u < units; u += gridDim.x) {
+        const long long row0 = next.row0;
+        const unsigned after = u + gridDim.x;
+        const int rows = next.rows, h = next.h, hv = next.hv;
+        if (rows <= 0) {  // no tokens here (the same for every thread)
+            cp_async_wait_all();
+            if (after < units) {
+                next = locate(a, after);
+                fetch_state(a.dckpt, after);
             }
-            n = lo;
-        } else {
-            n = slot / ((a.T + BT - 1) / BT);
+            continue;
         }
-        const Seq sq = chunk::seq_of(n, a.T, a.cu_seqlens);
-        const int t0 = (slot - sq.slot0) * BT;
-        const long long row0 = sq.row0 + t0;
-        if (t0 < 0 || t0 >= sq.len) continue;  // no tokens here (the same for every thread)
-        const int rows = min(BT, sq.len - t0);
         const size_t su = (size_t)u;
 
-        // ---- loads; the next unit's large blocks are asked into L2 meanwhile
+        // ---- loads
         if (tid < 4) sm.omax[tid] = 0u;
+        // do: eight rows at a time, so that a lane's piece of its FP16 block falls into banks of
+        // its own
+        const int o_row = (lane & 7) + (warp >> 2) * 8, o_col = (warp & 3) * 4 + (lane >> 3);
         uint4 dor[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int r = 16 * x + o_row;
+            dor[x] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows)
+                dor[x] = *reinterpret_cast<const uint4 *>(
+                    (const uint16_t *)a.dout + ((size_t)(row0 + r) * a.HV + hv) * D + o_col * 8);
+        }
+#pragma unroll
         for (int x = 0; x < 4; ++x) {
             const int r = (tid >> 4) + 16 * x, c = tid & 15;
             const bool ok = r < rows;
@@ -174,8 +224,6 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
             const size_t iv = (tok * a.HV + hv) * D;
             cp16z(smem_u32(&sm.g[r][c * 4]), a.gate + iv + c * 4, ok);
             cp16z(smem_u32(&sm.g[r][64 + c * 4]), a.gate + iv + 64 + c * 4, ok);
-            dor[x] = make_uint4(0u, 0u, 0u, 0u);
-            if (ok) dor[x] = *reinterpret_cast<const uint4 *>((const uint16_t *)a.dout + iv + c * 8);
         }
         cp_async_commit();
         // e and Y: a warp has tile `warp` of the four steps; lane 8j + t knows the scale of
@@ -190,20 +238,11 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
         const float cs = a.scales[su * kScales + (lane & 7)];
         const float ds = a.dscales[su * kScales + (lane & 7)];
         if (tid < BT) sm.beta[tid] = tid < rows ? a.beta[(size_t)(row0 + tid) * a.HV + hv] : 0.f;
-        if (tid == 0 && u + gridDim.x < units) {
-            const size_t nu = su + gridDim.x;
-            tc::prefetch_l2(a.dckpt + nu * kCkptBytes, (uint32_t)kCkptBytes);
-            tc::prefetch_l2(a.e + nu * kRowsBytes, (uint32_t)kRowsBytes);
-            tc::prefetch_l2(a.y + nu * kRowsBytes, (uint32_t)kRowsBytes);
-            tc::prefetch_l2(a.ckpt + nu * kCkptBytes, (uint32_t)kCkptBytes);
-        }
         // a warp's 16 rows of a saved state: tile t of 16 dv columns is the word pair w of its
         // blocks; brought to the common scale `c` of the eight tiles
         float S[16][4];  // rows dk c0 + gr, + 8; columns dv 8j + tc2, + 1
-        auto load_state = [&](const char *base, float scales, float c, int t, float (&l)[4],
-                              float (&r)[4]) {
-            const uint4 w = reinterpret_cast<const uint4 *>(base + su * kCkptBytes)
-                [(t * 8 + warp) * 32 + lane];
+        auto load_state = [&](float scales, float c, int t, float (&l)[4], float (&r)[4]) {
+            const uint4 w = sm.state[t][tid];
             const float f = c * inverse_of(__shfl_sync(0xffffffffu, scales, t));
             auto put = [&](uint32_t x, float &first, float &second) {
                 const uint32_t y = movm_t(x);
@@ -258,12 +297,12 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
             co[x] = scale_for(fmaxf(__uint_as_float(sm.omax[x]), 1e-30f), kTop);
-            const int r = (tid >> 4) + 16 * x, c = tid & 15;
             auto one = [&](uint32_t v) {
                 const float2 f = bf2(v);
                 return pack_f16(f.x * co[x], f.y * co[x]);
             };
-            *reinterpret_cast<uint4 *>(sm.dout + ((r >> 3) * 16 + c) * 128 + (r & 7) * 16) =
+            *reinterpret_cast<uint4 *>(
+                sm.dout + ((2 * x + (warp >> 2)) * 16 + o_col) * 128 + (lane & 7) * 16) =
                 make_uint4(one(dor[x].x), one(dor[x].y), one(dor[x].z), one(dor[x].w));
         }
         // ---- cumulative gate inside each step
@@ -281,21 +320,26 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
         // ---- scales of the warp's rows of S and dS: room for what the four steps add to them
         float cS, cD;
         {
-            float qm = 0.f, km = 0.f;
+            uint32_t qb = 0u, kb = 0u;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const Elems q = load_elems(&sm.q[j * C], c0, lane);
-                const Elems k = load_elems(&sm.k[j * C], c0, lane);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        qm = fmaxf(qm, fabsf(q.v[i][p]));
-                        km = fmaxf(km, fabsf(sm.beta[j * C + token_of(p, tc2)] * k.v[i][p]));
-                    }
+            for (int x = 0; x < 4; ++x) {  // 16 tokens a time, two pieces of a row
+                const int r = 16 * x + (lane >> 1), c = c0 + (lane & 1) * 8;
+                const uint4 q = *reinterpret_cast<const uint4 *>(&sm.q[r][c]);
+                const uint4 k = *reinterpret_cast<const uint4 *>(&sm.k[r][c]);
+                auto most = [](uint32_t m, const uint4 &v) {
+                    m = __vmaxu2(__vmaxu2(m, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
+                    return __vmaxu2(__vmaxu2(m, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
+                };
+                qb = most(qb, q);
+                kb = most(kb, k);
             }
-            qm = a.scale * warp_max(qm);
-            km = warp_max(km);
+            auto over_warp = [](uint32_t m) {
+                return __uint_as_float(
+                    __reduce_max_sync(0xffffffffu, max(m << 16, m & 0xffff0000u)));
+            };
+            const float qm = a.scale * over_warp(qb);
+            const float km = over_warp(kb) *
+                             warp_max(fmaxf(fabsf(sm.beta[lane]), fabsf(sm.beta[32 + lane])));
             float e_sum = 0.f, d_sum = 0.f;  // 2^14 of the operands' own scales
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -311,7 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
             cD = room(d_state, d_sum);
         }
 #pragma unroll
-        for (int t = 0; t < 8; ++t) load_state(a.dckpt, ds, cD, t, S[2 * t], S[2 * t + 1]);
+        for (int t = 0; t < 8; ++t) load_state(ds, cD, t, S[2 * t], S[2 * t + 1]);
+        fetch_state(a.ckpt, u);
         __syncthreads();
         // ---- the pairs' products
         {
@@ -354,6 +399,28 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
         }
         __syncthreads();
 
+        // the next unit's inputs are asked into L2 while the loads' queue is empty
+        if (after < units) {
+            next = locate(a, after);
+            const size_t nu = (size_t)after;
+            if (tid == 0) {
+                tc::prefetch_l2(a.e + nu * kRowsBytes, (uint32_t)kRowsBytes);
+                tc::prefetch_l2(a.y + nu * kRowsBytes, (uint32_t)kRowsBytes);
+                tc::prefetch_l2(a.ckpt + nu * kCkptBytes, (uint32_t)kCkptBytes);
+            }
+            // rows of q, k and do: two lines each, of the gate four
+            for (int x = tid; x < 10 * BT; x += kThreads) {
+                const int r = x / 10, l = x - 10 * r;
+                if (r >= next.rows) break;
+                const size_t tok = (size_t)(next.row0 + r);
+                const size_t iq = (tok * a.H + next.h) * D, iv = (tok * a.HV + next.hv) * D;
+                const char *p = l < 2   ? (const char *)((const uint16_t *)a.q + iq)
+                                : l < 4 ? (const char *)((const uint16_t *)a.k + iq)
+                                : l < 6 ? (const char *)((const uint16_t *)a.dout + iv)
+                                        : (const char *)(a.gate + iv);
+                prefetch_line(p + (l < 6 ? l & 1 : l - 6) * 128);
+            }
+        }
         // ---- R
 #pragma unroll 1
         for (int j = 3; j >= 0; --j) {
@@ -444,10 +511,11 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
         }
         // ---- the state at the slot's start, and sum_dv S dS there
         float carry[2] = {0.f, 0.f};
+        cp_async_wait_all();
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
             float x[2][4];
-            load_state(a.ckpt, cs, cS, t, x[0], x[1]);
+            load_state(cs, cS, t, x[0], x[1]);
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 float(&s)[4] = S[2 * t + y];
@@ -463,7 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
             carry[i] += __shfl_xor_sync(0xffffffffu, carry[i], 1);
             carry[i] += __shfl_xor_sync(0xffffffffu, carry[i], 2);
         }
+        if (after < units) fetch_state(a.dckpt, after);
         // ---- F, and the outputs
+        const size_t orow = (size_t)a.HV * D;
+        const size_t out_at = (size_t)row0 * orow + (size_t)hv * D + c0;
 #pragma unroll 1
         for (int j = 0; j < 4; ++j) {
             const float cj = j == 0 ? co[0] : j == 1 ? co[1] : j == 2 ? co[2] : co[3];
@@ -578,38 +649,33 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
                     dk.v[i][p] += sm.col[j][4 * i + p][tid] + d * q.v[i][p];
                 }
             }
+            auto put = [&](void *out, int which, const Elems &x) {
+                uint32_t w[1][4];
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+                for (int y = 0; y < 4; ++y)
+                    w[0][y] = pack_bf16(x.v[y & 1][y & 2], x.v[y & 1][(y & 2) + 1]);
+                chunk::store_out<1>(sm.out[which][warp], w,
+                                    (char *)((uint16_t *)out + out_at + (size_t)j * C * orow),
+                                    orow * 2, rows - j * C, (char *)out, a.rows_o * D * 2, a.dbg,
+                                    lane);
+            };
+            put(a.dgate, 0, dg);
+            if (!a.dq_hv) {
+                put(a.dq, 1, dq);
+                put(a.dk, 2, dk);
+            } else {  // summed over the head's value heads afterwards, in FP32
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t wg = movm_t(pack_bf16(dg.v[i][2 * half], dg.v[i][2 * half + 1]));
-                    uint32_t wq = 0, wk = 0;
-                    if (!a.dq_hv) {
-                        wq = movm_t(pack_bf16(dq.v[i][2 * half], dq.v[i][2 * half + 1]));
-                        wk = movm_t(pack_bf16(dk.v[i][2 * half], dk.v[i][2 * half + 1]));
-                    }
-                    const int t = j * C + 8 * half + gr;
-                    const size_t iv = ((size_t)(row0 + t) * a.HV + hv) * D + c0 + 8 * i + tc2;
-                    if (t < rows && dbg_ok(a.dbg, iv + 1, a.rows_o * D, DBG_STORE)) {
-                        *reinterpret_cast<uint32_t *>((uint16_t *)a.dgate + iv) = wg;
-                        if (!a.dq_hv) {
-                            *reinterpret_cast<uint32_t *>((uint16_t *)a.dq + iv) = wq;
-                            *reinterpret_cast<uint32_t *>((uint16_t *)a.dk + iv) = wk;
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const int t = j * C + token_of(p, tc2);
+                        const size_t at = out_at + (size_t)t * orow + 8 * i + gr;
+                        if (t < rows && dbg_ok(a.dbg, at, a.rows_o * D, DBG_STORE)) {
+                            a.dq_hv[at] = dq.v[i][p];
+                            a.dk_hv[at] = dk.v[i][p];
                         }
                     }
-                    if (a.dq_hv) {  // summed over the head's value heads afterwards, in FP32
-#pragma unroll
-                        for (int p = 2 * half; p < 2 * half + 2; ++p) {
-                            const int tp = j * C + token_of(p, tc2);
-                            const size_t ip =
-                                ((size_t)(row0 + tp) * a.HV + hv) * D + c0 + 8 * i + gr;
-                            if (tp < rows && dbg_ok(a.dbg, ip, a.rows_o * D, DBG_STORE)) {
-                                a.dq_hv[ip] = dq.v[i][p];
-                                a.dk_hv[ip] = dk.v[i][p];
-                            }
-                        }
-                    }
-                }
+            }
         }
         __syncthreads();
     }
