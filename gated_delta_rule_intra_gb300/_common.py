@@ -55,6 +55,7 @@ def takes_stream(fn):
 
 
 def library():
+    """The library in use; lib.quick_<name> is the short way into its functions."""
     return _package._lib or _package.load_library()
 
 
@@ -85,3 +86,27 @@ def declare(lib):
             ("kda_layer_norm_bwd", i, [vp] * 8 + [ll, i, i, i, ll, ll, ll, vp, z, vp])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
+    _declare_quick(lib)
+
+
+def _declare_quick(lib):
+    """The short way in (csrc/binding.cpp) as lib.quick_<name>: functions that return None for
+    arguments that need the checks here."""
+    try:
+        from . import _native
+    except ImportError as e:
+        raise RuntimeError("_native.so is missing or of another torch: build it with "
+                           "gated_delta_rule_intra_gb300.build.build_library()") from e
+
+    def address(name):
+        return ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+
+    for name, fns in (
+            ("step", ("kda_step",)),
+            ("chunk_fwd", ("kda_chunk_fwd", "kda_chunk_saved_bytes")),
+            ("chunk_bwd", ("kda_chunk_bwd", "kda_chunk_saved_bytes",
+                           "kda_chunk_bwd_workspace_bytes")),
+            ("layer_norm_fwd", ("kda_layer_norm_fwd",)),
+            ("layer_norm_bwd", ("kda_layer_norm_bwd", "kda_layer_norm_bwd_workspace_bytes"))):
+        setattr(lib, "quick_" + name,
+                functools.partial(getattr(_native, name), *[address(f) for f in fns]))

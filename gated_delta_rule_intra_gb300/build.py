@@ -1,8 +1,9 @@
-"""Build libkda.so in-tree with nvcc for sm_103a.
+"""Build libkda.so in-tree with nvcc for sm_103a, and the binding's C++ half with g++.
 
 Each .cu under csrc/ is compiled to an object in parallel, then linked into
 ``gated_delta_rule_intra_gb300/libkda.so`` (git-ignored).  No CMake, no torch
-extension machinery: the library is a plain C-ABI shared object.
+extension machinery: the library is a plain C-ABI shared object.  csrc/binding.cpp becomes
+``_native.so``, compiled against the installed torch's headers next to it.
 ``build_debug_library()`` builds the same sources with ``-DKDA_DEBUG_CHECKS`` into
 ``libkda_debug.so``: every global index the kernels compute is checked against its
 buffer's extent and reported through ``kda_debug_set_flags`` (tests only).
@@ -15,11 +16,13 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libkda.so")
+NATIVE = os.path.join(PKG, "_native.so")
 DEBUG_LIB = os.path.join(PKG, "libkda_debug.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 DEBUG_BUILD_DIR = os.path.join(PKG, "_build_debug")
@@ -53,13 +56,40 @@ def _compile(src: str, extra, build_dir: str) -> str:
     return obj
 
 
+def build_native() -> str:
+    """Compile csrc/binding.cpp into _native.so; returns its path."""
+    import torch
+
+    home = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    headers = [os.path.join(home, "include"),
+               os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = NATIVE + ".tmp"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), *[x for h in headers for x in ("-isystem", h)],
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", os.path.join(home, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           "-Wl,-rpath," + os.path.join(home, "lib")]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, NATIVE)
+    return NATIVE
+
+
 def build_library(out: str = LIB, extra_flags=(), verbose: bool = False,
                   build_dir: str = BUILD_DIR) -> str:
-    """Compile every csrc/*.cu for sm_103a and link libkda.so; returns its path."""
+    """Compile every csrc/*.cu for sm_103a and link libkda.so; returns its path.  Together with
+    libkda.so itself _native.so is built."""
     os.makedirs(build_dir, exist_ok=True)
     srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        native = ex.submit(build_native) if out == LIB else None
         objs = list(ex.map(lambda s: _compile(s, list(extra_flags), build_dir), srcs))
+        if native:
+            native.result()
     tmp = out + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)

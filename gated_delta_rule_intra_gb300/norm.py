@@ -61,14 +61,22 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-@takes_stream
-def kda_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None):
+def kda_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None, stream=None):
     """y = (x - mean) * rstd * weight + bias over the last dimension.  Returns (y, mean, rstd).
 
     x [..., width] bf16/fp16/fp32; its last dimension is contiguous and its rows are evenly
     spaced (a column slice of a wider tensor will do).  weight and bias [width] in x's dtype or
     fp32 (None: ones, zeros).  y has x's dtype; mean and rstd [rows] are fp32.
     """
+    if stream is None and y is None:
+        out = library().quick_layer_norm_fwd(x, weight, bias, eps)
+        if out is not None:
+            return out
+    return _layer_norm_fwd(x, weight, bias, eps, y, stream=stream)
+
+
+@takes_stream
+def _layer_norm_fwd(x, weight, bias, eps, y):
     dev, width, rows, wdtype = _input("kda_layer_norm_fwd", x, weight, bias)
     xs = _stride("x", x, x)
     if y is None:
@@ -83,11 +91,19 @@ def kda_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None):
     return y, mean, rstd
 
 
-@takes_stream
-def kda_layer_norm_bwd(dy, x, weight, mean, rstd, *, dx=None, param_grads=True):
+def kda_layer_norm_bwd(dy, x, weight, mean, rstd, *, dx=None, param_grads=True, stream=None):
     """Gradients of ``kda_layer_norm_fwd``.  Returns (dx, dweight, dbias): dx in x's dtype,
     dweight and dbias [width] fp32 summed over the rows in a fixed order (None unless
     ``param_grads``)."""
+    if stream is None and dx is None and param_grads:
+        out = library().quick_layer_norm_bwd(dy, x, weight, mean, rstd)
+        if out is not None:
+            return out
+    return _layer_norm_bwd(dy, x, weight, mean, rstd, dx, param_grads, stream=stream)
+
+
+@takes_stream
+def _layer_norm_bwd(dy, x, weight, mean, rstd, dx, param_grads):
     dev, width, rows, wdtype = _input("kda_layer_norm_bwd", x, weight, None)
     xs, dys = _stride("x", x, x), _stride("dy", dy, x)
     check("mean", mean, (rows,), F32, dev)

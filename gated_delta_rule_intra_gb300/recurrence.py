@@ -1,5 +1,6 @@
 """The gated delta-rule recurrence over whole sequences (``kda_chunk_fwd``,
-``kda_chunk_bwd``) and its single-token form (``kda_step``).
+``kda_chunk_bwd``) and its single-token form (``kda_step``).  ``stream=`` (a torch stream or a
+raw handle) runs a call on another stream than the current one.
 
 Per value head the state S is [128 dk, 128 dv] in fp32; a token decays it per channel and
 corrects it towards its value::
@@ -87,9 +88,8 @@ def _seqs(cu_seqlens, B, dev):
     return cu_seqlens.numel() - 1
 
 
-@takes_stream
 def kda_chunk_fwd(q, k, v, gate, beta, scale=None, initial_state=None, *,
-                  output_final_state=False, save=False, cu_seqlens=None, o=None):
+                  output_final_state=False, save=False, cu_seqlens=None, o=None, stream=None):
     """The recurrence over whole sequences.  Returns (o, final_state, saved).
 
     q, k [B, T, H, 128] and v [B, T, HV, 128] bf16/fp16 (value head hv reads q/k head
@@ -98,9 +98,21 @@ def kda_chunk_fwd(q, k, v, gate, beta, scale=None, initial_state=None, *,
     [sequences, HV, 128 dk, 128 dv] fp32 defaults to zeros.  o is in q's dtype, with zeros at
     tokens in no sequence when it is allocated here.  final_state (fp32) is None unless
     ``output_final_state``.  saved is what ``kda_chunk_bwd`` needs (0.9 KB a token and
-    value head in bf16 without a state, 1.7 KB otherwise), None unless ``save``.  ``cu_seqlens`` (int32 [N + 1] on the device, B = 1)
-    packs N sequences along T; it is read on the device only.
+    value head in bf16 without a state, 1.7 KB otherwise), None unless ``save``.
+    ``cu_seqlens`` (int32 [N + 1] on the device, B = 1) packs N sequences along T; it is read on
+    the device only.
     """
+    if stream is None and cu_seqlens is None and o is None:
+        out = library().quick_chunk_fwd(q, k, v, gate, beta, scale, initial_state,
+                                        output_final_state, save)
+        if out is not None:
+            return out
+    return _chunk_fwd(q, k, v, gate, beta, scale, initial_state, output_final_state, save,
+                      cu_seqlens, o, stream=stream)
+
+
+@takes_stream
+def _chunk_fwd(q, k, v, gate, beta, scale, initial_state, output_final_state, save, cu_seqlens, o):
     H, HV, dev = _inputs("kda_chunk_fwd", q, k, v, gate, beta, 2)
     B, T = q.shape[:2]
     N = _seqs(cu_seqlens, B, dev)
@@ -129,10 +141,9 @@ def kda_chunk_fwd(q, k, v, gate, beta, scale=None, initial_state=None, *,
     return o, final, saved
 
 
-@takes_stream
 def kda_chunk_bwd(q, k, v, gate, beta, do, saved, scale=None, d_final_state=None, *,
                   output_d_initial_state=False, cu_seqlens=None, dq=None, dk=None, dv=None,
-                  dgate=None, dbeta=None):
+                  dgate=None, dbeta=None, stream=None):
     """Gradients of ``kda_chunk_fwd``.  Returns (dq, dk, dv, dgate, dbeta, d_initial_state).
 
     The five inputs, ``scale`` and ``cu_seqlens`` as given to the forward, do like its o,
@@ -141,6 +152,20 @@ def kda_chunk_bwd(q, k, v, gate, beta, do, saved, scale=None, d_final_state=None
     final state's shape) defaults to zeros; d_initial_state (fp32) is None unless
     ``output_d_initial_state``.  Deterministic.
     """
+    if (stream is None and cu_seqlens is None and d_final_state is None
+            and not output_d_initial_state and dq is None and dk is None and dv is None
+            and dgate is None and dbeta is None):
+        out = library().quick_chunk_bwd(q, k, v, gate, beta, do, saved, scale)
+        if out is not None:
+            return out
+    return _chunk_bwd(q, k, v, gate, beta, do, saved, scale, d_final_state,
+                      output_d_initial_state, cu_seqlens, (dq, dk, dv, dgate, dbeta),
+                      stream=stream)
+
+
+@takes_stream
+def _chunk_bwd(q, k, v, gate, beta, do, saved, scale, d_final_state, output_d_initial_state,
+               cu_seqlens, given):
     H, HV, dev = _inputs("kda_chunk_bwd", q, k, v, gate, beta, 2)
     B, T, dt = q.shape[0], q.shape[1], q.dtype
     N = _seqs(cu_seqlens, B, dev)
@@ -153,8 +178,7 @@ def kda_chunk_bwd(q, k, v, gate, beta, do, saved, scale=None, d_final_state=None
     check("saved", saved, (saved_bytes,), torch.uint8, dev)
     new = torch.zeros_like if N else torch.empty_like
     out = []
-    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v), ("dgate", dgate, v),
-                          ("dbeta", dbeta, beta)):
+    for name, t, like in zip(("dq", "dk", "dv", "dgate", "dbeta"), given, (q, k, v, v, beta)):
         if t is None:
             t = new(like) if like is not beta else new(like, dtype=dt)
         else:
@@ -180,8 +204,7 @@ def kda_chunk_bwd(q, k, v, gate, beta, do, saved, scale=None, d_final_state=None
     return (*out, d_initial)
 
 
-@takes_stream
-def kda_step(q, k, v, gate, beta, state, scale=None, *, state_indices=None, o=None):
+def kda_step(q, k, v, gate, beta, state, scale=None, *, state_indices=None, o=None, stream=None):
     """One token for each of N requests, the states updated in place.  Returns o [N, HV, 128].
 
     q, k [N, H, 128], v [N, HV, 128] bf16/fp16, gate [N, HV, 128] and beta [N, HV] fp32 as in
@@ -189,6 +212,15 @@ def kda_step(q, k, v, gate, beta, state, scale=None, *, state_indices=None, o=No
     [N] on the device), [num_states, ...], request n's being state[state_indices[n]].  An index
     outside the states marks a padding row (its o is zero); no two rows may name one state.
     """
+    if stream is None:
+        out = library().quick_step(q, k, v, gate, beta, state, scale, state_indices, o)
+        if out is not None:
+            return out
+    return _step(q, k, v, gate, beta, state, scale, state_indices, o, stream=stream)
+
+
+@takes_stream
+def _step(q, k, v, gate, beta, state, scale, state_indices, o):
     H, HV, dev = _inputs("kda_step", q, k, v, gate, beta, 1)
     N, states = q.shape[0], state.shape[0]
     check("state", state, (N if state_indices is None else states, HV, K, K), F32, dev)
