@@ -27,6 +27,7 @@
 #pragma once
 
 #include "kda_common.cuh"
+#include "kda_ops.h"
 #include "tc_ptx.cuh"
 
 namespace kda {
@@ -34,8 +35,7 @@ namespace chunk {
 
 constexpr int C = 16;            // tokens a step
 constexpr int D = KD;            // channels of q and k, and of v
-constexpr int kPrepWarps = 8;
-constexpr int kPrepThreads = 32 * kPrepWarps;
+constexpr int kPrepThreads = 256;
 constexpr int kPlane = C * D * 2;      // bytes of a BF16 [16][128] operand plane
 constexpr int kTile = C * C * 2;       // bytes of a BF16 [16][16] tile
 constexpr size_t kCkptBytes = 2 * D * D * 2;  // a state checkpoint: hi and lo planes
@@ -166,21 +166,71 @@ struct Seq {
 // Sequence n of the launch.  Fixed length: n = batch index.  Variable length: the tokens
 // [cu[n], cu[n+1]) clamped to the packed length, slots from cu[n] / 64 + n on (no two
 // sequences' slots meet, and T / 64 + num_seqs + 1 slots cover every input).
+__device__ __forceinline__ int2 range_of(int n, int T, const int *cu) {
+    int a = cu[n], b = cu[n + 1];
+    a = a < 0 ? 0 : a > T ? T : a;
+    b = b < a ? a : b > T ? T : b;
+    return make_int2(a, b);
+}
+// The same n in all lanes of the warp.
 __device__ __forceinline__ Seq seq_of(int n, int T, const int *cu) {
     Seq s;
     if (cu) {
-        int a = cu[n], b = cu[n + 1];
-        a = a < 0 ? 0 : a > T ? T : a;
-        b = b < a ? a : b > T ? T : b;
-        s.row0 = uniform(a);
-        s.len = uniform(b - a);
-        s.slot0 = uniform(a / BT + n);
+        const int2 x = range_of(n, T, cu);
+        s.row0 = uniform(x.x);
+        s.len = uniform(x.y - x.x);
+        s.slot0 = uniform(x.x / BT + n);
     } else {
         s.row0 = (long long)n * T;
         s.len = T;
         s.slot0 = n * ((T + BT - 1) / BT);
     }
     return s;
+}
+
+// The sequence that is `rank`-th in length, the longest first: a batch of ragged sequences has
+// its longest walks begun at once and the short ones fill in behind them.  Sequences of one
+// length, and batches too large to be worth ranking, keep their order.  All threads call it.
+constexpr int kRanked = 128;
+__device__ __forceinline__ int by_length(int rank, int num_seqs, int T, const int *cu) {
+    if (!cu || num_seqs > kRanked) return rank;
+    __shared__ int len[kRanked], found;
+    const int i = threadIdx.x;
+    if (i < num_seqs) {
+        const int2 x = range_of(i, T, cu);
+        len[i] = x.y - x.x;
+    }
+    __syncthreads();
+    if (i < num_seqs) {
+        int before = 0;
+        for (int j = 0; j < num_seqs; ++j) before += len[j] > len[i] || (len[j] == len[i] && j < i);
+        if (before == rank) found = i;
+    }
+    __syncthreads();
+    return uniform(found);
+}
+
+// CTAs that a head's 128 dv columns are divided between: the fewest rounds over the SMs.  A
+// finer split repeats the preparation, but its step is shorter: one, two and four CTAs take some
+// 5.0, 3.7 and 2.7 thousand cycles for a step (B=1 T=32768 H=32: 2.63 ms in four CTAs a head, 3.7
+// in two).  Of sequences of unknown lengths the longest is taken to be four times the average, and
+// the others to fill in behind it (ten prompts of 1 to 2609 tokens, 16 heads: 404 us in one CTA
+// a head, 257 in four).
+inline int best_split(int num_seqs, int HV, const int *cu) {
+    constexpr int kSplit[3] = {1, 2, 4}, kStep[3] = {50, 37, 27};
+    const long long heads = (long long)num_seqs * HV;
+    int best = 4;
+    double least = 1e300;
+    for (int i = 2; i >= 0; --i) {
+        const double share = (double)heads * kSplit[i] / kSMs;
+        const double cost =
+            kStep[i] * (cu ? 4.0 + share : (double)((heads * kSplit[i] + kSMs - 1) / kSMs));
+        if (cost < least) {
+            least = cost;
+            best = kSplit[i];
+        }
+    }
+    return best;
 }
 
 // Raw inputs of a step in shared memory.
@@ -190,22 +240,23 @@ struct __align__(16) RawStage {
     float gate[C][D];
 };
 
-// Which warps do what: eight prepare operands, SOLVERS solve the steps' triangular systems, NW
-// consume all that.  With two consumers (few heads, so that the time of one step counts) these
-// get two of the SM's four schedulers with the solvers, the preparing warps the other two: warps
-// go to the schedulers in turn, and the warps in between leave at once.
+// Which warps do what: NW consume, PREP prepare operands, SOLVERS solve the steps' triangular
+// systems.  Two consumers get two of the SM's four schedulers with the solvers, the preparing
+// warps the other two: warps go to the schedulers in turn, and the warps in between leave at
+// once.
 //
 // Registers move from the feeding warps to the consumers, by groups of four warps: both shares
 // add up to no more than the kernel is launched with (65,536 over its threads, in eights), which
 // ready_once() checks, because a consumer would wait for the rest forever.
-template <int NW, int SOLVERS = 0> struct Roles {
+template <int NW, int PREP, int SOLVERS> struct Roles {
     static constexpr bool kApart = NW == 2;
     static constexpr int kGroup = kApart ? 4 : NW;  // warps that take registers
-    static constexpr int kThreads = kApart ? 640 : kPrepThreads + 32 * (SOLVERS + NW);
-    static constexpr int kGive = kApart ? 80 : NW == 8 ? 112 : SOLVERS ? 88 : 112;
-    static constexpr int kTake = kApart ? 160 : NW == 8 ? 144 : 248;
+    static constexpr int kThreads = kApart ? 640 : 32 * (NW + PREP + SOLVERS);
+    static constexpr int kGive = kThreads > 512 ? 80 : kThreads == 512 && NW == 4 ? 88 : 112;
+    static constexpr int kTake = kThreads > 512 ? 160 : NW == 8 ? 144 : 248;
     static constexpr int kLaunch = 65536 / kThreads / 8 * 8;
-    static_assert(kGroup % 4 == 0 && SOLVERS % 4 == 0 && SOLVERS <= 8, "");
+    static_assert(kGroup % 4 == 0 && PREP % 4 == 0 && SOLVERS % 4 == 0, "");
+    static_assert(!kApart || (PREP == 8 && SOLVERS <= 8), "");
     static_assert(kGroup * 32 * kTake + (kThreads - kGroup * 32) * kGive <= kLaunch * kThreads, "");
 
     int prep, solver, consumer;  // index, or -1
@@ -220,10 +271,10 @@ template <int NW, int SOLVERS = 0> struct Roles {
                 prep = x;
             else if (x < SOLVERS)
                 solver = x;
-        } else if (warp < kGroup + kPrepWarps) {
+        } else if (warp < kGroup + PREP) {
             prep = warp - kGroup;
         } else {
-            solver = warp - kGroup - kPrepWarps;
+            solver = warp - kGroup - PREP;
         }
     }
     static __device__ __forceinline__ void give() {
@@ -364,7 +415,8 @@ __device__ __forceinline__ void mma3x2(float (&c0)[4], float (&c1)[4], float (&d
 }
 
 // Decay of the accumulators of S^T [16 dv, 128 dk]: columns 16 jj .. 16 jj + 15.
-__device__ __forceinline__ void decay_cols(float (&S)[16][4], const float *decay, int jj, int tc2) {
+template <int NJ>
+__device__ __forceinline__ void decay_cols(float (&S)[NJ][4], const float *decay, int jj, int tc2) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const float2 d = *reinterpret_cast<const float2 *>(&decay[16 * jj + 8 * x + tc2]);
@@ -385,17 +437,17 @@ __device__ __forceinline__ uint32_t tile_lane(int lane) {
 // block, [dk / 8][dv / 16][32 lanes][16 bytes], a lane's words being (row lane / 4, columns
 // 2 (lane % 4), + 1) of the block's left half, hi and lo, and the same of its right half -- the
 // accumulator layout of S [dk, dv], whose left-operand fragments sum over dv.
-template <int MT>
-__device__ __forceinline__ void store_checkpoint(char *base, const float (&S)[MT][16][4], int tile,
-                                                 int lane) {
+template <int MT, int NJ>
+__device__ __forceinline__ void store_checkpoint(char *base, const float (&S)[MT][NJ][4], int tile,
+                                                 int j0, int lane) {
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < NJ; ++j) {
             uint32_t h0, l0, h1, l1;
             split2(S[t][j][0], S[t][j][1], h0, l0);
             split2(S[t][j][2], S[t][j][3], h1, l1);
-            reinterpret_cast<uint4 *>(base)[(j * 8 + tile + t) * 32 + lane] =
+            reinterpret_cast<uint4 *>(base)[((j0 + j) * 8 + tile + t) * 32 + lane] =
                 make_uint4(movm_t(h0), movm_t(l0), movm_t(h1), movm_t(l1));
         }
 }
@@ -432,21 +484,48 @@ __device__ __forceinline__ void store_out(char *stage, const uint32_t (&w)[MT][4
     __syncwarp();
 }
 
+// Moves an accumulator pair's sum away, and adds it again.
+__device__ __forceinline__ void take_sum(float (&x)[2][4], float (&kept)[2][4]) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            kept[j][p] = x[j][p];
+            x[j][p] = 0.f;
+        }
+}
+__device__ __forceinline__ void add_sum(float (&x)[2][4], const float (&kept)[2][4]) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int p = 0; p < 4; ++p) x[j][p] += kept[j][p];
+}
+
+// The half `second` of an accumulator pair: warps choose without a branch, which would make all
+// that follows wait for its lanes to meet again.
+__device__ __forceinline__ void half_of(const float (&x)[2][4], bool second, float (&y)[4]) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) y[p] = second ? x[1][p] : x[0][p];
+}
+
 // A [16 dv, 16 token] accumulator pair as hi/lo planes of rows of tokens, in 8x8 blocks
-// [token / 8][dv / 8][8 token][8 dv]; t0 is the step's first token in its 64-token slot.
+// [token / 8][dv / 8][8 token][8 dv] of a 64-token slot: eight tokens of it ...
+__device__ __forceinline__ void store_row_block(char *base, const float (&x)[4], int block, int dv0,
+                                                int lane) {
+    uint32_t h0, l0, h1, l1;
+    split2(x[0], x[1], h0, l0);
+    split2(x[2], x[3], h1, l1);
+    char *p = base + ((size_t)block * 16 + dv0 / 8) * 128 + lane * 4;
+    *reinterpret_cast<uint32_t *>(p) = movm_t(h0);
+    *reinterpret_cast<uint32_t *>(p + 128) = movm_t(h1);
+    *reinterpret_cast<uint32_t *>(p + kRowPlane) = movm_t(l0);
+    *reinterpret_cast<uint32_t *>(p + kRowPlane + 128) = movm_t(l1);
+}
+// ... and both eights; t0 is the step's first token in its slot.
 __device__ __forceinline__ void store_rows(char *base, const float (&x)[2][4], int t0, int dv0,
                                            int lane) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        uint32_t h0, l0, h1, l1;
-        split2(x[j][0], x[j][1], h0, l0);
-        split2(x[j][2], x[j][3], h1, l1);
-        char *p = base + ((size_t)(t0 / 8 + j) * 16 + dv0 / 8) * 128 + lane * 4;
-        *reinterpret_cast<uint32_t *>(p) = movm_t(h0);
-        *reinterpret_cast<uint32_t *>(p + 128) = movm_t(h1);
-        *reinterpret_cast<uint32_t *>(p + kRowPlane) = movm_t(l0);
-        *reinterpret_cast<uint32_t *>(p + kRowPlane + 128) = movm_t(l1);
-    }
+    store_row_block(base, x[0], t0 / 8, dv0, lane);
+    store_row_block(base, x[1], t0 / 8 + 1, dv0, lane);
 }
 
 }  // namespace chunk

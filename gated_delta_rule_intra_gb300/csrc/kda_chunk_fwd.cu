@@ -15,12 +15,17 @@ namespace {
 
 constexpr int kStages = 3;         // prepared stages
 constexpr int kRaw = kStages + 2;  // raw input stages: two ahead, and as far back as a stage lives
-constexpr int kHalf = 128;         // threads of each half of the preparing warps
+constexpr int kHalf = 128;         // threads that take the scores
 
-// Named barriers; PLANES, FULL, EMPTY + stage, SOLVE + solver.
-enum { BAR_PREP = 1, BAR_PLANES = 3, BAR_FULL = 6, BAR_EMPTY = 9, BAR_SOLVE = 12 };
-
-constexpr int kSolvers = 4;  // warps that take the steps' systems in turn
+// Named barriers; JOIN + pair of consumers that share a tile; PLANES, FULL, EMPTY, SOLVE + stage.
+enum {
+    BAR_PREP = 0,
+    BAR_JOIN = 1,
+    BAR_PLANES = 3,
+    BAR_FULL = 6,
+    BAR_EMPTY = 9,
+    BAR_SOLVE = 12
+};
 
 struct __align__(128) Prepared {
     char planes[kPlanes * kPlane];
@@ -36,21 +41,22 @@ struct __align__(128) Smem {
     RawStage raw[kRaw];
     uint16_t v[kRaw][C][D];  // rows of the CTA's dv slice, swizzled chunks
     float beta[kRaw][C];
-    float a2[kSolvers][C][C + 4];  // M diag(beta)
-    float a1[kSolvers][C][C + 4];  // diag(beta) M
-    char t[kSolvers][2 * kTile];   // T hi, lo on the way to the saved tiles
-    int bad[kSolvers][4];          // whether a warp has seen an input that is not finite
-    char out[4][2 * 512];          // a consumer's o on its way out
+    float a2[kStages][C][C + 4];  // (M diag(beta))^T
+    float a1[kStages][C][C + 4];  // (diag(beta) M)^T
+    char t[kStages][2 * kTile];   // T hi, lo on the way to the saved tiles
+    int bad[kStages][4];          // whether a warp has seen an input that is not finite
+    char out[4][2 * 512];         // a consumer's o on its way out
+    float4 join[2][4][3][32];     // partial sums of consumers that share a tile, two steps' worth
 };
 
-template <int SLICE>
+template <int SLICE, int NT>
 __device__ __forceinline__ void load_step(Smem &sm, const ChunkFwdArgs &a, const Seq &sq, int h,
                                           int hv, int dv0, int step, int tid) {
     RawStage &raw = sm.raw[step % kRaw];
     const int c = tid & 15;
 #pragma unroll
-    for (int i = 0; i < C * 16 / kHalf; ++i) {
-        const int row = (tid >> 4) + i * (kHalf / 16), t = step * C + row;
+    for (int i = 0; i < C * 16 / NT; ++i) {
+        const int row = (tid >> 4) + i * (NT / 16), t = step * C + row;
         const bool ok = t < sq.len;
         const size_t tok = (size_t)sq.row0 + (ok ? t : 0);
         const size_t iq = (tok * a.H + h) * D + c * 8, iv = (tok * a.HV + hv) * D;
@@ -102,12 +108,12 @@ __device__ __forceinline__ void scores(Smem &sm, Prepared &out, const float *bet
             *reinterpret_cast<uint32_t *>(out.p + kTile + (r * C + s) * 2) = lo;
         } else {
             if (s < r) {
-                sm.a2[buf][r][s] = x * beta[s];
-                sm.a1[buf][r][s] = x * beta[r];
+                sm.a2[buf][s][r] = x * beta[s];
+                sm.a1[buf][s][r] = x * beta[r];
             }
             if (s + 1 < r) {
-                sm.a2[buf][r][s + 1] = y * beta[s + 1];
-                sm.a1[buf][r][s + 1] = y * beta[r];
+                sm.a2[buf][s + 1][r] = y * beta[s + 1];
+                sm.a1[buf][s + 1][r] = y * beta[r];
             }
         }
     }
@@ -115,12 +121,12 @@ __device__ __forceinline__ void scores(Smem &sm, Prepared &out, const float *bet
 
 // Gates so strong that k 2^-g leaves FP32's range inside a step (a channel loses more than
 // 2^-96 in 16 tokens): the key plane in its bounded form, the gate replaced by its cumsum ...
-template <typename T16>
+template <typename T16, int NT>
 __device__ __forceinline__ void prep_strong(RawStage &raw, Prepared &out, float scale, int tid) {
-    prep_planes<T16, kHalf, false>(raw, out.planes, out.decay, scale, tid);
-    bar_sync(BAR_PREP, kHalf);
+    prep_planes<T16, NT, false>(raw, out.planes, out.decay, scale, tid);
+    bar_sync(BAR_PREP, NT);
     float acc = 0.f;
-    for (int r = 0; r < C; ++r) raw.gate[r][tid] = acc += floor_gate(raw.gate[r][tid]);
+    for (int r = tid < D ? 0 : C; r < C; ++r) raw.gate[r][tid] = acc += floor_gate(raw.gate[r][tid]);
 }
 
 // ... and M and P pair by pair, one exp2 per (r, s, channel), every exponent <= 0: 17 pairs of
@@ -162,33 +168,33 @@ __device__ __forceinline__ void scores_strong(Smem &sm, const RawStage &raw, con
             reinterpret_cast<uint16_t *>(out.p)[r * C + s] = (uint16_t)hi;
             reinterpret_cast<uint16_t *>(out.p + kTile)[r * C + s] = (uint16_t)lo;
             if (s < r) {
-                sm.a2[buf][r][s] = m * beta[s];
-                sm.a1[buf][r][s] = m * beta[r];
+                sm.a2[buf][s][r] = m * beta[s];
+                sm.a1[buf][s][r] = m * beta[r];
             }
         }
     }
 }
 
 // T2 = (I + M diag(beta))^-1 (lanes 0-15, one column each) and T = (I + diag(beta) M)^-1
-// (lanes 16-31) by forward substitution in FP32.
+// (lanes 16-31) by forward substitution in FP32, column by column of the matrix: a found entry
+// is taken out of all later rows at once.
 __device__ __forceinline__ void solve(Smem &sm, Prepared &out, int buf, int lane) {
     const int c = lane & 15;
     const bool second = lane >= 16;
-    const float(*A)[C + 4] = second ? sm.a1[buf] : sm.a2[buf];
+    const float(*A)[C + 4] = second ? sm.a1[buf] : sm.a2[buf];  // A[j][r], r > j
     float x[C];
 #pragma unroll
-    for (int r = 0; r < C; ++r) {
-        float s = r == c ? 1.f : 0.f;
+    for (int r = 0; r < C; ++r) x[r] = r == c ? 1.f : 0.f;
 #pragma unroll
-        for (int j = 0; j < r; j += 4) {
-            const float4 a = *reinterpret_cast<const float4 *>(&A[r][j]);
-            s -= a.x * x[j];
-            if (j + 1 < r) s -= a.y * x[j + 1];
-            if (j + 2 < r) s -= a.z * x[j + 2];
-            if (j + 3 < r) s -= a.w * x[j + 3];
+    for (int j = 0; j < C - 1; ++j)
+#pragma unroll
+        for (int r = (j + 1) & ~3; r < C; r += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(&A[j][r]);
+            if (r > j) x[r] -= a.x * x[j];
+            if (r + 1 > j) x[r + 1] -= a.y * x[j];
+            if (r + 2 > j) x[r + 2] -= a.z * x[j];
+            x[r + 3] -= a.w * x[j];
         }
-        x[r] = s;
-    }
     uint16_t *hi = reinterpret_cast<uint16_t *>(second ? sm.t[buf] : out.t2);
     uint16_t *lo = hi + C * C;
 #pragma unroll
@@ -249,20 +255,25 @@ __device__ __forceinline__ void mma_causal(float (&acc)[2][4], const float (&x)[
 }
 
 // One step of a consumer warp's 16 MT columns of dv: e and o (xq) of its tokens, S updated.
+// With KS = 2 the warp has the half `kh` of dk: sums over dk are joined with the partner's in
+// shared memory, both warps have e, and o is finished for the tokens 8 kh .. 8 kh + 7.
 // One straight run of code, so that the chain R -> e -> n of a tile overlaps other products;
 // CAREFUL also takes steps with strong gates or inputs that are not finite.  CKPT: the state's
 // operand halves, which the first product needs anyway, are stored as the slot's checkpoint.
-template <typename T16, int MT, bool CAREFUL, bool CKPT>
-__device__ __forceinline__ void consume(float (&S)[MT][16][4], float (&xq)[MT][2][4],
+template <typename T16, int MT, int KS, bool CAREFUL, bool CKPT>
+__device__ __forceinline__ void consume(float (&S)[MT][16 / KS][4], float (&xq)[MT][2][4],
                                         float (&e)[MT][2][4], const Prepared &in,
                                         const uint16_t (*v)[D], const float *beta, char *ckpt,
-                                        int slice_tile, int tile, int lane) {
+                                        int slice_tile, int tile, int kh,
+                                        float4 (*join)[3][32], int warp, int lane) {
+    static_assert(KS == 1 || MT == 1, "");
+    const int k0 = kh * (8 / KS);  // first 16 channels of dk
     const int tc2 = (lane & 3) * 2;
     // ldmatrix lane addresses: row-major operand planes and the transposed reads of kd
     const int lrow = (lane & 7) + ((lane >> 4) & 1) * 8, lcol = (lane >> 3) & 1;
     const int trow = lane & 15, tcol = lane >> 4;
     const uint32_t pl = tc::smem_u32(in.planes), tl = tile_lane(lane);
-    float xw[MT][2][4];
+    float xw[MT][2][4], lw[MT][2][4], lq[MT][2][4];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -270,10 +281,17 @@ __device__ __forceinline__ void consume(float (&S)[MT][16][4], float (&xq)[MT][2
 #pragma unroll
             for (int p = 0; p < 4; ++p) xw[t][j][p] = xq[t][j][p] = 0.f;
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {
-        uint32_t kh[4], kl[4], qh[4], ql[4];
-        const uint32_t off = plane_off(lrow, 2 * kk + lcol);
-        ldsm4(kh, pl + KW_HI * kPlane + off);
+    for (int kk = 0; kk < 8 / KS; ++kk) {
+        if (KS == 1 && kk == 4) {  // the halves of dk apart, as where two warps have them
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                take_sum(xw[t], lw[t]);
+                take_sum(xq[t], lq[t]);
+            }
+        }
+        uint32_t kf[4], kl[4], qh[4], ql[4];
+        const uint32_t off = plane_off(lrow, 2 * (k0 + kk) + lcol);
+        ldsm4(kf, pl + KW_HI * kPlane + off);
         ldsm4(qh, pl + QW_HI * kPlane + off);
         ldsm4(kl, pl + KW_LO * kPlane + off);
         ldsm4(ql, pl + QW_LO * kPlane + off);
@@ -281,14 +299,41 @@ __device__ __forceinline__ void consume(float (&S)[MT][16][4], float (&xq)[MT][2
         for (int t = 0; t < MT; ++t) {
             uint32_t ah[4], al[4];
             split_frag(S[t][2 * kk], S[t][2 * kk + 1], ah, al);
-            mma3x2<true>(xw[t][0], xw[t][1], xq[t][0], xq[t][1], ah, al, kh, kl, ah, al, qh, ql);
+            mma3x2<true>(xw[t][0], xw[t][1], xq[t][0], xq[t][1], ah, al, kf, kl, ah, al, qh, ql);
             if (CKPT) {
                 uint4 *p = reinterpret_cast<uint4 *>(ckpt) +
-                           (2 * kk * 8 + slice_tile + tile + t) * 32 + lane;
+                           (2 * (k0 + kk) * 8 + slice_tile + tile + t) * 32 + lane;
                 p[0] = make_uint4(movm_t(ah[0]), movm_t(al[0]), movm_t(ah[1]), movm_t(al[1]));
                 p[8 * 32] = make_uint4(movm_t(ah[2]), movm_t(al[2]), movm_t(ah[3]), movm_t(al[3]));
             }
         }
+    }
+    if (KS == 1) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            add_sum(xw[t], lw[t]);
+            add_sum(xq[t], lq[t]);
+        }
+    } else {
+        auto put = [&](int i, const float (&x)[4]) {
+            join[warp][i][lane] = make_float4(x[0], x[1], x[2], x[3]);
+        };
+        auto add = [&](int i, float (&x)[4]) {
+            const float4 y = join[warp ^ 1][i][lane];
+            x[0] += y.x; x[1] += y.y; x[2] += y.z; x[3] += y.w;
+        };
+        put(0, xw[0][0]);
+        put(1, xw[0][1]);
+        float own[4], other[4];
+        half_of(xq[0], kh, own);
+        half_of(xq[0], !kh, other);
+        put(2, other);
+        bar_sync(BAR_JOIN + (warp >> 1), 64);
+        add(0, xw[0][0]);
+        add(1, xw[0][1]);
+        add(2, own);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) xq[0][0][p] = xq[0][1][p] = own[p];
     }
     uint32_t th[4], tlo[4], nh[MT][4], nl[MT][4];
     ldsm4(th, tc::smem_u32(in.t2) + tl);
@@ -341,13 +386,13 @@ __device__ __forceinline__ void consume(float (&S)[MT][16][4], float (&xq)[MT][2
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int jj = 0; jj < 8; ++jj) decay_cols(S[t], in.decay, jj, tc2);
+            for (int jj = 0; jj < 8 / KS; ++jj) decay_cols(S[t], in.decay + 16 * k0, jj, tc2);
     }
 #pragma unroll
-    for (int jj = 0; jj < 8; jj += 2) {
+    for (int jj = 0; jj < 8 / KS; jj += 2) {
         uint32_t bh[4], bl[4], ch[4], cl[4];
-        const uint32_t o0 = plane_off(trow, 2 * jj + tcol);
-        const uint32_t o1 = plane_off(trow, 2 * jj + 2 + tcol);
+        const uint32_t o0 = plane_off(trow, 2 * (k0 + jj) + tcol);
+        const uint32_t o1 = plane_off(trow, 2 * (k0 + jj) + 2 + tcol);
         ldsm4t(bh, pl + KD_HI * kPlane + o0);
         ldsm4t(ch, pl + KD_HI * kPlane + o1);
         ldsm4t(bl, pl + KD_LO * kPlane + o0);
@@ -362,27 +407,56 @@ __device__ __forceinline__ void consume(float (&S)[MT][16][4], float (&xq)[MT][2
         ldsm4(th, tc::smem_u32(in.p) + tl);
         ldsm4(tlo, tc::smem_u32(in.p) + kTile + tl);
 #pragma unroll
-        for (int t = 0; t < MT; ++t) mma3(xq[t][0], xq[t][1], nh[t], nl[t], th, tlo);
+        for (int t = 0; t < MT; ++t) {
+            if (KS == 1) {
+                mma3(xq[t][0], xq[t][1], nh[t], nl[t], th, tlo);
+            } else {
+                const uint32_t h0 = kh ? th[2] : th[0], h1 = kh ? th[3] : th[1];
+                const uint32_t l0 = kh ? tlo[2] : tlo[0], l1 = kh ? tlo[3] : tlo[1];
+                mma16816(xq[t][0], nh[t], h0, h1);
+                mma16816(xq[t][0], nh[t], l0, l1);
+                mma16816(xq[t][0], nl[t], h0, h1);
+            }
+        }
     }
     if (from_start) {
 #pragma unroll
-        for (int jj = 0; jj < 8; ++jj)
+        for (int jj = 0; jj < 8 / KS; ++jj)
 #pragma unroll
-            for (int t = 0; t < MT; ++t) decay_cols(S[t], in.decay, jj, tc2);
+            for (int t = 0; t < MT; ++t) decay_cols(S[t], in.decay + 16 * k0, jj, tc2);
     }
 }
 
-// NW consumer warps of 16 MT dv columns each; a head takes 128 / (16 NW MT) CTAs.
-template <typename T16, int NW, int MT, bool SAVE>
-__global__ void __launch_bounds__(Roles<NW, kSolvers>::kThreads, 1)
+// Four consumer warps, KS for each 16 MT columns of dv: a head takes 2 KS / MT CTAs.
+template <int KS> using Roles = chunk::Roles<4, 4 * KS + 4, 4>;
+
+// Eight tokens of o and, for the backward, of e on their way out.
+template <typename T16, bool SAVE>
+__device__ __forceinline__ void finish(const ChunkFwdArgs &a, const float (&o)[4],
+                                       const float (&e)[4], unsigned slot, int step, int j,
+                                       uint16_t *o_at, size_t orow, int len, int d0, int lane) {
+    if (SAVE) store_row_block(a.e + slot * kRowsBytes, e, (step % 4) * C / 8 + j, d0, lane);
+    const uint32_t x = movm_t(pack2<T16>(o[0], o[1])), y = movm_t(pack2<T16>(o[2], o[3]));
+    const int tok = step * C + 8 * j + (lane >> 2);
+    uint16_t *at = o_at + (size_t)tok * orow + (lane & 3) * 2;
+    if (tok < len && dbg_ok(a.dbg, (size_t)(at - (uint16_t *)a.o) + 9, a.rows_o * D, DBG_STORE)) {
+        *reinterpret_cast<uint32_t *>(at) = x;
+        *reinterpret_cast<uint32_t *>(at + 8) = y;
+    }
+}
+
+template <typename T16, int MT, int KS, bool SAVE>
+__global__ void __launch_bounds__(Roles<KS>::kThreads, 1)
     kda_chunk_fwd_kernel(const ChunkFwdArgs a) {
-    constexpr int kSlice = 16 * NW * MT, kSplit = D / kSlice;
+    constexpr int NW = 4, kSlice = 16 * NW * MT / KS, kSplit = D / kSlice, kJ = 16 / KS;
+    constexpr int kPrep = 128 * KS;  // threads that prepare operands
     extern __shared__ __align__(128) char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int lane = threadIdx.x & 31;
-    const Roles<NW, kSolvers> role(warp_index());
+    const Roles<KS> role(warp_index());
     const int unit = blockIdx.x / kSplit, dv0 = (blockIdx.x % kSplit) * kSlice;
-    const int n = unit / a.HV, hv = unit - n * a.HV, h = hv / (a.HV / a.H);
+    const int n = by_length(unit / a.HV, a.num_seqs, a.T, a.cu_seqlens);
+    const int hv = unit % a.HV, h = hv / (a.HV / a.H);
     const Seq sq = seq_of(n, a.T, a.cu_seqlens);
     // whole 64-token slots where the backward's buffers are written: rows past the end are
     // computed as zeros, so every row of a slot is defined
@@ -393,43 +467,43 @@ __global__ void __launch_bounds__(Roles<NW, kSolvers>::kThreads, 1)
         reinterpret_cast<uint32_t *>(sm.prep[i / (2 * kTile / 4)].p)[i % (2 * kTile / 4)] = 0u;
     __syncthreads();
 
-    if (role.feeds) {
+    if (role.consumer < 0) {
         role.give();
-        if (role.prep >= 0) {
+        if (role.prep >= 0 && role.prep < 4 * KS) {  // raw inputs -> operand planes
             const int tid = role.prep * 32 + lane;
-            if (tid < kHalf) {  // raw inputs -> operand planes
-                for (int i = 0; i < 2; ++i) {
-                    if (i < steps) load_step<kSlice>(sm, a, sq, h, hv, dv0, i, tid);
-                    cp_async_commit();
-                }
-                for (int i = 0; i < steps; ++i) {
-                    const int st = i % kStages;
-                    Prepared &out = sm.prep[st];
-                    RawStage &raw = sm.raw[i % kRaw];
-                    cp_wait<1>();
-                    // the consumers are done with this stage's previous step (and its values)
-                    if (i >= kStages) bar_sync(BAR_EMPTY + st, kHalf + 32 * NW);
-                    bar_sync(BAR_PREP, kHalf);
-                    if (i + 2 < steps) load_step<kSlice>(sm, a, sq, h, hv, dv0, i + 2, tid);
-                    cp_async_commit();
-                    const bool big =
-                        prep_planes<T16, kHalf, true>(raw, out.planes, out.decay, a.scale, tid);
-                    const bool strong = bar_or(BAR_PREP, kHalf, big);
-                    if (strong) prep_strong<T16>(raw, out, a.scale, tid);
-                    if (tid == 0) out.from_start = !strong;
-                    bar_arrive(BAR_PLANES + st, 2 * kHalf);
-                }
-                cp_async_wait_all();
-                return;
+            for (int i = 0; i < 2; ++i) {
+                if (i < steps) load_step<kSlice, kPrep>(sm, a, sq, h, hv, dv0, i, tid);
+                cp_async_commit();
             }
-            // planes -> scores
-            const int w = role.prep - kHalf / 32;
             for (int i = 0; i < steps; ++i) {
                 const int st = i % kStages;
                 Prepared &out = sm.prep[st];
-                const int buf = i % kSolvers;
+                RawStage &raw = sm.raw[i % kRaw];
+                cp_wait<1>();
+                // the consumers are done with this stage's previous step (and its values)
+                if (i >= kStages) bar_sync(BAR_EMPTY + st, kPrep + 32 * NW);
+                bar_sync(BAR_PREP, kPrep);
+                const bool big =
+                    prep_planes<T16, kPrep, true>(raw, out.planes, out.decay, a.scale, tid);
+                const bool strong = bar_or(BAR_PREP, kPrep, big);
+                if (strong) prep_strong<T16, kPrep>(raw, out, a.scale, tid);
+                if (tid == 0) out.from_start = !strong;
+                bar_arrive(BAR_PLANES + st, kPrep + kHalf);
+                if (i + 2 < steps) load_step<kSlice, kPrep>(sm, a, sq, h, hv, dv0, i + 2, tid);
+                cp_async_commit();
+            }
+            cp_async_wait_all();
+            return;
+        }
+        if (role.prep >= 0) {
+            // planes -> scores
+            const int w = role.prep - 4 * KS, tid = w * 32 + lane;
+            for (int i = 0; i < steps; ++i) {
+                const int st = i % kStages;
+                Prepared &out = sm.prep[st];
+                const int buf = st;
                 const float *beta = sm.beta[i % kRaw];
-                bar_sync(BAR_PLANES + st, 2 * kHalf);
+                bar_sync(BAR_PLANES + st, kPrep + kHalf);
                 if (uniform(out.from_start)) {
                     scores(sm, out, beta, buf, w, lane);
                 } else {
@@ -437,32 +511,31 @@ __global__ void __launch_bounds__(Roles<NW, kSolvers>::kThreads, 1)
                     scores_strong<T16>(sm, sm.raw[i % kRaw], beta, out, buf, a.scale, w + 4, lane);
                 }
                 const bool bad = __any_sync(
-                    0xffffffffu, not_finite<T16, kSlice>(sm.v[i % kRaw], beta, tid - kHalf));
+                    0xffffffffu, not_finite<T16, kSlice>(sm.v[i % kRaw], beta, tid));
                 if (lane == 0) sm.bad[buf][w] = bad;
                 bar_arrive(BAR_SOLVE + buf, kHalf + 32);
             }
             return;
         }
         if (role.solver >= 0) {  // scores -> T2 and T
-            const int w = role.solver;
-            for (int i = w; i < steps; i += kSolvers) {
-                const int st = i % kStages;
-                Prepared &out = sm.prep[st];
-                bar_sync(BAR_SOLVE + w, kHalf + 32);
+            const int st = role.solver;  // a stage each
+            Prepared &out = sm.prep[st];
+            for (int i = st; st < kStages && i < steps; i += kStages) {
+                bar_sync(BAR_SOLVE + st, kHalf + 32);
                 const uint4 *p = reinterpret_cast<const uint4 *>(out.p);
                 const uint4 p0 = p[lane], p1 = p[32 + lane];
                 if (lane == 0) {
-                    const int *bad = sm.bad[w];
+                    const int *bad = sm.bad[st];
                     out.careful = bad[0] || bad[1] || bad[2] || bad[3] || !out.from_start;
                 }
-                if (SAVE || lane < 16) solve(sm, out, w, lane);
+                if (SAVE || lane < 16) solve(sm, out, st, lane);
                 __syncwarp();
                 bar_arrive(BAR_FULL + st, 32 + 32 * NW);
                 if (SAVE && dv0 == 0) {
                     uint4 *to = reinterpret_cast<uint4 *>(
                         a.tiles +
                         (((size_t)(sq.slot0 + i / 4) * a.HV + hv) * 4 + i % 4) * kTilesBytes);
-                    const uint4 *t = reinterpret_cast<const uint4 *>(sm.t[w]);
+                    const uint4 *t = reinterpret_cast<const uint4 *>(sm.t[st]);
                     to[lane] = t[lane];
                     to[32 + lane] = t[32 + lane];
                     to[64 + lane] = p0;
@@ -477,15 +550,15 @@ __global__ void __launch_bounds__(Roles<NW, kSolvers>::kThreads, 1)
 
     // ------------------------------------------------------------------ consumers
     role.take();
-    if (role.consumer < 0) return;
-    const int cw = role.consumer, d0 = dv0 + cw * MT * 16;  // this warp's first dv column
+    // this warp's tiles of the slice, its first dv column, its part of dk
+    const int cw = role.consumer, tile = cw / KS * MT, d0 = dv0 + tile * 16, kh = cw % KS;
     const int gr = lane >> 2, tc2 = (lane & 3) * 2;
-    const size_t sbase = ((size_t)n * a.HV + hv) * D * D;
-    float S[MT][16][4];  // S^T: rows d0 + 16t + gr, + 8; columns dk 8j + tc2, + 1
+    const size_t sbase = ((size_t)n * a.HV + hv) * D * D + (size_t)kh * (D / KS) * D;
+    float S[MT][kJ][4];  // S^T: rows d0 + 16t + gr, + 8; columns dk 8j + tc2, + 1 of its part
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < kJ; ++j) {
             S[t][j][0] = S[t][j][1] = S[t][j][2] = S[t][j][3] = 0.f;
             if (a.initial_state) {
                 const float *p =
@@ -510,21 +583,29 @@ __global__ void __launch_bounds__(Roles<NW, kSolvers>::kThreads, 1)
         const float *beta = sm.beta[i % kRaw];
         char *ckpt = SAVE ? a.ckpt + slot * kCkptBytes : nullptr;
         // tiles of 16 dv columns: of the CTA's slice for v, of the head for the checkpoint
-        auto run = [&](auto careful, auto keep) {
-            consume<T16, MT, decltype(careful)::value, decltype(keep)::value>(
-                S, xq, e, in, v, beta, ckpt, dv0 / 16, cw * MT, lane);
+        auto run = [&](auto with_care, auto keep) {
+            consume<T16, MT, KS, decltype(with_care)::value, decltype(keep)::value>(
+                S, xq, e, in, v, beta, ckpt, dv0 / 16, tile, kh, sm.join[i & 1], cw, lane);
         };
         const bool keep = SAVE && i % 4 == 0;
-        if (!uniform(in.careful)) {
+        const bool careful = uniform(in.careful);
+        if (!careful) {
             if (keep)
                 run(std::false_type{}, std::integral_constant<bool, SAVE>{});
             else
                 run(std::false_type{}, std::false_type{});
         } else {
-            if (keep) store_checkpoint(ckpt, S, d0 / 16, lane);
+            if (keep) store_checkpoint(ckpt, S, d0 / 16, kh * kJ, lane);
             run(std::true_type{}, std::false_type{});
         }
-        if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kHalf + 32 * NW);
+        if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kPrep + 32 * NW);
+        if (KS == 2) {  // the tokens that this warp has finished
+            float eh[4], oh[4];
+            half_of(e[0], kh, eh);
+            half_of(xq[0], kh && careful, oh);
+            finish<T16, SAVE>(a, oh, eh, slot, i, kh, o_at, orow, sq.len, d0, lane);
+            continue;
+        }
         if (SAVE)
 #pragma unroll
             for (int t = 0; t < MT; ++t)
@@ -544,7 +625,7 @@ __global__ void __launch_bounds__(Roles<NW, kSolvers>::kThreads, 1)
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
+            for (int j = 0; j < kJ; ++j) {
                 float *p = a.final_state + sbase + (size_t)(8 * j + tc2) * D + d0 + 16 * t + gr;
                 p[0] = S[t][j][0];
                 p[D] = S[t][j][1];
@@ -554,24 +635,24 @@ __global__ void __launch_bounds__(Roles<NW, kSolvers>::kThreads, 1)
     }
 }
 
-template <typename T16, int NW, int MT, bool SAVE>
+template <typename T16, int MT, int KS, bool SAVE>
 cudaError_t launch(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
     static volatile int done[kMaxDev];
-    cudaError_t e = ready_once<Roles<NW, kSolvers>>(kda_chunk_fwd_kernel<T16, NW, MT, SAVE>,
-                                            (int)sizeof(Smem), dev, done);
+    const auto kernel = kda_chunk_fwd_kernel<T16, MT, KS, SAVE>;
+    const cudaError_t e = ready_once<Roles<KS>>(kernel, (int)sizeof(Smem), dev, done);
     if (e != cudaSuccess) return e;
-    const int grid = a.num_seqs * a.HV * (D / (16 * NW * MT));
-    kda_chunk_fwd_kernel<T16, NW, MT, SAVE>
-        <<<grid, Roles<NW, kSolvers>::kThreads, sizeof(Smem), stream>>>(a);
+    const int grid = a.num_seqs * a.HV * (2 * KS / MT);
+    kernel<<<grid, Roles<KS>::kThreads, sizeof(Smem), stream>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T16, bool SAVE>
 cudaError_t launch_split(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
-    const long long heads = (long long)a.num_seqs * a.HV;
-    if (heads * 2 > kSMs) return launch<T16, 4, 2, SAVE>(a, dev, stream);
-    if (heads * 4 > kSMs) return launch<T16, 4, 1, SAVE>(a, dev, stream);
-    return launch<T16, 2, 1, SAVE>(a, dev, stream);
+    switch (best_split(a.num_seqs, a.HV, a.cu_seqlens)) {
+        case 1: return launch<T16, 2, 1, SAVE>(a, dev, stream);
+        case 2: return launch<T16, 1, 1, SAVE>(a, dev, stream);
+        default: return launch<T16, 1, 2, SAVE>(a, dev, stream);
+    }
 }
 
 }  // namespace

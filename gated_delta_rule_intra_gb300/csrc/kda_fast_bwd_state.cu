@@ -14,7 +14,8 @@ using chunk::cp16z;
 using chunk::ldsm4;
 using chunk::ldsm4t;
 using chunk::plane_off;
-using chunk::Roles;
+
+template <int NW> using Roles = chunk::Roles<NW, 8, 0>;
 using chunk::Seq;
 using tc::smem_u32;
 
@@ -67,7 +68,8 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
     const int lane = threadIdx.x & 31;
     const Roles<NW> role(chunk::warp_index());
     const int unit = blockIdx.x / kSplit, dv0 = (blockIdx.x % kSplit) * kSlice;
-    const int n = unit / a.HV, hv = unit - n * a.HV, h = hv / (a.HV / a.H);
+    const int n = chunk::by_length(unit / a.HV, a.num_seqs, a.T, a.cu_seqlens);
+    const int hv = unit % a.HV, h = hv / (a.HV / a.H);
     const Seq sq = chunk::seq_of(n, a.T, a.cu_seqlens);
     const int steps = (sq.len + BT - 1) / BT * (BT / C);
 
@@ -306,10 +308,11 @@ cudaError_t launch(const ChunkBwdArgs &a, int dev, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_bwd_state(const ChunkBwdArgs &a, int dev, cudaStream_t stream) {
-    const long long heads = (long long)a.num_seqs * a.HV;
-    if (heads * 2 > kSMs) return launch<4, 2>(a, dev, stream);
-    if (heads * 4 > kSMs) return launch<4, 1>(a, dev, stream);
-    return launch<2, 1>(a, dev, stream);
+    switch (chunk::best_split(a.num_seqs, a.HV, a.cu_seqlens)) {
+        case 1: return launch<4, 2>(a, dev, stream);
+        case 2: return launch<4, 1>(a, dev, stream);
+        default: return launch<2, 1>(a, dev, stream);
+    }
 }
 
 }  // namespace fast

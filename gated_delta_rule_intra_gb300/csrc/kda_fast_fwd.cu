@@ -24,7 +24,7 @@ constexpr int kRaw = kStages + 2;  // raw input stages: two ahead, and as far ba
 enum { BAR_PREP = 1, BAR_SCORE = 2, BAR_PLANES = 3, BAR_FULL = 6, BAR_EMPTY = 9, BAR_SOLVE = 12 };
 
 constexpr int kSolvers = 4;  // warps that take the steps' systems in turn
-template <int NW> using Roles = chunk::Roles<NW, kSolvers>;
+template <int NW> using Roles = chunk::Roles<NW, 8, kSolvers>;
 
 struct __align__(128) Stage {
     Planes pl;
@@ -239,7 +239,8 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
     const int lane = threadIdx.x & 31;
     const Roles<NW> role(chunk::warp_index());
     const int unit = blockIdx.x / kSplit, dv0 = (blockIdx.x % kSplit) * kSlice;
-    const int n = unit / a.HV, hv = unit - n * a.HV, h = hv / (a.HV / a.H);
+    const int n = chunk::by_length(unit / a.HV, a.num_seqs, a.T, a.cu_seqlens);
+    const int hv = unit - unit / a.HV * a.HV, h = hv / (a.HV / a.H);
     const Seq sq = chunk::seq_of(n, a.T, a.cu_seqlens);
     // whole 64-token slots where the backward's buffers are written: rows past the end are
     // computed as zeros, so every row of a slot is defined
@@ -500,10 +501,11 @@ cudaError_t launch(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
 }
 
 template <bool SAVE> cudaError_t launch_split(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
-    const long long heads = (long long)a.num_seqs * a.HV;
-    if (heads * 2 > kSMs) return launch<4, 2, SAVE>(a, dev, stream);
-    if (heads * 4 > kSMs) return launch<4, 1, SAVE>(a, dev, stream);
-    return launch<2, 1, SAVE>(a, dev, stream);
+    switch (chunk::best_split(a.num_seqs, a.HV, a.cu_seqlens)) {
+        case 1: return launch<4, 2, SAVE>(a, dev, stream);
+        case 2: return launch<4, 1, SAVE>(a, dev, stream);
+        default: return launch<2, 1, SAVE>(a, dev, stream);
+    }
 }
 
 }  // namespace
