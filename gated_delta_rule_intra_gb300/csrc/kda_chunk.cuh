@@ -252,8 +252,8 @@ template <int NW, int PREP, int SOLVERS> struct Roles {
     static constexpr bool kApart = NW == 2;
     static constexpr int kGroup = kApart ? 4 : NW;  // warps that take registers
     static constexpr int kThreads = kApart ? 640 : 32 * (NW + PREP + SOLVERS);
-    static constexpr int kGive = kThreads > 512 ? 80 : kThreads == 512 && NW == 4 ? 88 : 112;
-    static constexpr int kTake = kThreads > 512 ? 160 : NW == 8 ? 144 : 248;
+    static constexpr int kGive = kThreads > 512 ? (NW == 8 ? 64 : 80) : kThreads == 512 && NW == 4 ? 88 : 112;
+    static constexpr int kTake = kThreads > 512 && NW != 8 ? 160 : NW == 8 ? 144 : 248;
     static constexpr int kLaunch = 65536 / kThreads / 8 * 8;
     static_assert(kGroup % 4 == 0 && PREP % 4 == 0 && SOLVERS % 4 == 0, "");
     static_assert(!kApart || (PREP == 8 && SOLVERS <= 8), "");
@@ -433,23 +433,21 @@ __device__ __forceinline__ uint32_t tile_lane(int lane) {
     return (uint32_t)(((lane & 7) + ((lane >> 4) & 1) * 8) * 32 + ((lane >> 3) & 1) * 16);
 }
 
-// The accumulators of S^T [16 MT dv, 128 dk] as a checkpoint: 8 dk rows by 16 dv columns a
+// The accumulators of S^T [16 dv, 8 NJ dk] as a checkpoint: 8 dk rows by 16 dv columns a
 // block, [dk / 8][dv / 16][32 lanes][16 bytes], a lane's words being (row lane / 4, columns
 // 2 (lane % 4), + 1) of the block's left half, hi and lo, and the same of its right half -- the
 // accumulator layout of S [dk, dv], whose left-operand fragments sum over dv.
-template <int MT, int NJ>
-__device__ __forceinline__ void store_checkpoint(char *base, const float (&S)[MT][NJ][4], int tile,
+template <int NJ>
+__device__ __forceinline__ void store_checkpoint(char *base, const float (&S)[NJ][4], int tile,
                                                  int j0, int lane) {
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            uint32_t h0, l0, h1, l1;
-            split2(S[t][j][0], S[t][j][1], h0, l0);
-            split2(S[t][j][2], S[t][j][3], h1, l1);
-            reinterpret_cast<uint4 *>(base)[((j0 + j) * 8 + tile + t) * 32 + lane] =
-                make_uint4(movm_t(h0), movm_t(l0), movm_t(h1), movm_t(l1));
-        }
+    for (int j = 0; j < NJ; ++j) {
+        uint32_t h0, l0, h1, l1;
+        split2(S[j][0], S[j][1], h0, l0);
+        split2(S[j][2], S[j][3], h1, l1);
+        reinterpret_cast<uint4 *>(base)[((j0 + j) * 8 + tile) * 32 + lane] =
+            make_uint4(movm_t(h0), movm_t(l0), movm_t(h1), movm_t(l1));
+    }
 }
 
 __device__ __forceinline__ void stsm4t(uint32_t addr, const uint32_t (&w)[4]) {
@@ -457,30 +455,22 @@ __device__ __forceinline__ void stsm4t(uint32_t addr, const uint32_t (&w)[4]) {
                  "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                  : "memory");
 }
-// A warp's 16 tokens of MT tiles of 16 columns, given transposed (words: tokens 0-7 of columns
-// 0-7 and 8-15, tokens 8-15), to rows `row` bytes apart from `at` on, in 16-byte pieces through
-// 512 MT bytes of shared memory: 32 MT bytes of a row leave together (4-byte stores straight
-// from the transposed words cost the walk 200 cycles a step more).  Only `tokens` rows exist;
-// `end` is the size of what lies behind `base`.
-template <int MT>
-__device__ __forceinline__ void store_out(char *stage, const uint32_t (&w)[MT][4], char *at,
-                                          size_t row, int tokens, const char *base, size_t end,
-                                          unsigned *dbg, int lane) {
-    constexpr int kPer = 2 * MT;  // pieces of a row
-    auto off = [](int r, int c) { return (uint32_t)(r * kPer + (c ^ (r / (8 / kPer) % kPer))) * 16; };
-    const uint32_t sm = tc::smem_u32(stage);
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-        stsm4t(sm + off((lane & 7) + (lane >> 4) * 8, 2 * t + ((lane >> 3) & 1)), w[t]);
+// A warp's 16 tokens of 16 columns, given transposed (words: tokens 0-7 of columns 0-7 and 8-15,
+// tokens 8-15), to rows `row` bytes apart from `at` on, in 16-byte pieces through 512 bytes of
+// shared memory: a row's 32 bytes leave together (4-byte stores straight from the transposed
+// words cost the walk 200 cycles a step more).  Only `tokens` rows exist; `end` is the size of
+// what lies behind `base`.
+__device__ __forceinline__ void store_out(char *stage, const uint32_t (&w)[4], char *at, size_t row,
+                                          int tokens, const char *base, size_t end, unsigned *dbg,
+                                          int lane) {
+    auto off = [](int r, int c) { return (uint32_t)(r * 32 + ((c ^ (r >> 2 & 1)) << 4)); };
+    stsm4t(tc::smem_u32(stage) + off((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1), w);
     __syncwarp();
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int x = lane + 32 * i, r = x / kPer, c = x % kPer;
-        const uint4 u = *reinterpret_cast<const uint4 *>(stage + off(r, c));
-        char *to = at + r * row + c * 16;
-        if (r < tokens && dbg_ok(dbg, (size_t)(to - base) + 15, end, DBG_STORE))
-            *reinterpret_cast<uint4 *>(to) = u;
-    }
+    const int r = lane >> 1, c = lane & 1;
+    const uint4 u = *reinterpret_cast<const uint4 *>(stage + off(r, c));
+    char *to = at + r * row + c * 16;
+    if (r < tokens && dbg_ok(dbg, (size_t)(to - base) + 15, end, DBG_STORE))
+        *reinterpret_cast<uint4 *>(to) = u;
     __syncwarp();
 }
 

@@ -127,8 +127,7 @@ __global__ void __launch_bounds__(Roles<NC, 8, 0>::kThreads, 1)
     const int k0 = kh * (8 / KS);  // first 16 channels of dk
     const int gr = lane >> 2, tc2 = (lane & 3) * 2;
     const size_t sbase = ((size_t)n * a.HV + hv) * D * D + (size_t)k0 * 16 * D;
-    float Sm[1][kJ][4];
-    float(&S)[kJ][4] = Sm[0];  // dS^T: rows dv d0 + gr, + 8; columns dk 8j + tc2, + 1 of its part
+    float S[kJ][4];  // dS^T: rows dv d0 + gr, + 8; columns dk 8j + tc2, + 1 of its part
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
         if (a.d_final_state) {
@@ -151,7 +150,7 @@ __global__ void __launch_bounds__(Roles<NC, 8, 0>::kThreads, 1)
     for (int i = 0; i < steps; ++i) {
         const int st = i & 1, step = steps - 1 - i;
         const unsigned slot = (unsigned)(sq.slot0 + step / 4) * a.HV + hv;
-        if (step % 4 == 3) store_checkpoint(a.dckpt + slot * kCkptBytes, Sm, d0 / 16, kh * kJ, lane);
+        if (step % 4 == 3) store_checkpoint(a.dckpt + slot * kCkptBytes, S, d0 / 16, kh * kJ, lane);
         bar_sync(BAR_FULL + st, kPrepThreads + 32 * NC);
         const Prepared &in = sm.prep[st];
         const uint32_t pl = tc::smem_u32(in.planes);

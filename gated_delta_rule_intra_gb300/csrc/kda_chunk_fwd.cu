@@ -45,7 +45,7 @@ struct __align__(128) Smem {
     float a1[kStages][C][C + 4];  // (diag(beta) M)^T
     char t[kStages][2 * kTile];   // T hi, lo on the way to the saved tiles
     int bad[kStages][4];          // whether a warp has seen an input that is not finite
-    char out[4][2 * 512];         // a consumer's o on its way out
+    char out[8][512];             // a consumer's o on its way out
     float4 join[2][4][3][32];     // partial sums of consumers that share a tile, two steps' worth
 };
 
@@ -254,40 +254,34 @@ __device__ __forceinline__ void mma_causal(float (&acc)[2][4], const float (&x)[
     }
 }
 
-// One step of a consumer warp's 16 MT columns of dv: e and o (xq) of its tokens, S updated.
+// One step of a consumer warp's 16 columns of dv: e and o (xq) of its tokens, S updated.
 // With KS = 2 the warp has the half `kh` of dk: sums over dk are joined with the partner's in
 // shared memory, both warps have e, and o is finished for the tokens 8 kh .. 8 kh + 7.
 // One straight run of code, so that the chain R -> e -> n of a tile overlaps other products;
 // CAREFUL also takes steps with strong gates or inputs that are not finite.  CKPT: the state's
 // operand halves, which the first product needs anyway, are stored as the slot's checkpoint.
-template <typename T16, int MT, int KS, bool CAREFUL, bool CKPT>
-__device__ __forceinline__ void consume(float (&S)[MT][16 / KS][4], float (&xq)[MT][2][4],
-                                        float (&e)[MT][2][4], const Prepared &in,
+template <typename T16, int KS, bool CAREFUL, bool CKPT>
+__device__ __forceinline__ void consume(float (&S)[16 / KS][4], float (&xq)[2][4],
+                                        float (&e)[2][4], const Prepared &in,
                                         const uint16_t (*v)[D], const float *beta, char *ckpt,
                                         int slice_tile, int tile, int kh,
                                         float4 (*join)[3][32], int warp, int lane) {
-    static_assert(KS == 1 || MT == 1, "");
     const int k0 = kh * (8 / KS);  // first 16 channels of dk
     const int tc2 = (lane & 3) * 2;
     // ldmatrix lane addresses: row-major operand planes and the transposed reads of kd
     const int lrow = (lane & 7) + ((lane >> 4) & 1) * 8, lcol = (lane >> 3) & 1;
     const int trow = lane & 15, tcol = lane >> 4;
     const uint32_t pl = tc::smem_u32(in.planes), tl = tile_lane(lane);
-    float xw[MT][2][4], lw[MT][2][4], lq[MT][2][4];
+    float xw[2][4], lw[2][4], lq[2][4];
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int p = 0; p < 4; ++p) xw[t][j][p] = xq[t][j][p] = 0.f;
+        for (int p = 0; p < 4; ++p) xw[j][p] = xq[j][p] = 0.f;
 #pragma unroll
     for (int kk = 0; kk < 8 / KS; ++kk) {
         if (KS == 1 && kk == 4) {  // the halves of dk apart, as where two warps have them
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                take_sum(xw[t], lw[t]);
-                take_sum(xq[t], lq[t]);
-            }
+            take_sum(xw, lw);
+            take_sum(xq, lq);
         }
         uint32_t kf[4], kl[4], qh[4], ql[4];
         const uint32_t off = plane_off(lrow, 2 * (k0 + kk) + lcol);
@@ -295,25 +289,19 @@ __device__ __forceinline__ void consume(float (&S)[MT][16 / KS][4], float (&xq)[
         ldsm4(qh, pl + QW_HI * kPlane + off);
         ldsm4(kl, pl + KW_LO * kPlane + off);
         ldsm4(ql, pl + QW_LO * kPlane + off);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            uint32_t ah[4], al[4];
-            split_frag(S[t][2 * kk], S[t][2 * kk + 1], ah, al);
-            mma3x2<true>(xw[t][0], xw[t][1], xq[t][0], xq[t][1], ah, al, kf, kl, ah, al, qh, ql);
-            if (CKPT) {
-                uint4 *p = reinterpret_cast<uint4 *>(ckpt) +
-                           (2 * (k0 + kk) * 8 + slice_tile + tile + t) * 32 + lane;
-                p[0] = make_uint4(movm_t(ah[0]), movm_t(al[0]), movm_t(ah[1]), movm_t(al[1]));
-                p[8 * 32] = make_uint4(movm_t(ah[2]), movm_t(al[2]), movm_t(ah[3]), movm_t(al[3]));
-            }
+        uint32_t ah[4], al[4];
+        split_frag(S[2 * kk], S[2 * kk + 1], ah, al);
+        mma3x2<true>(xw[0], xw[1], xq[0], xq[1], ah, al, kf, kl, ah, al, qh, ql);
+        if (CKPT) {
+            uint4 *p = reinterpret_cast<uint4 *>(ckpt) +
+                       (2 * (k0 + kk) * 8 + slice_tile + tile) * 32 + lane;
+            p[0] = make_uint4(movm_t(ah[0]), movm_t(al[0]), movm_t(ah[1]), movm_t(al[1]));
+            p[8 * 32] = make_uint4(movm_t(ah[2]), movm_t(al[2]), movm_t(ah[3]), movm_t(al[3]));
         }
     }
     if (KS == 1) {
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            add_sum(xw[t], lw[t]);
-            add_sum(xq[t], lq[t]);
-        }
+        add_sum(xw, lw);
+        add_sum(xq, lq);
     } else {
         auto put = [&](int i, const float (&x)[4]) {
             join[warp][i][lane] = make_float4(x[0], x[1], x[2], x[3]);
@@ -322,71 +310,66 @@ __device__ __forceinline__ void consume(float (&S)[MT][16 / KS][4], float (&xq)[
             const float4 y = join[warp ^ 1][i][lane];
             x[0] += y.x; x[1] += y.y; x[2] += y.z; x[3] += y.w;
         };
-        put(0, xw[0][0]);
-        put(1, xw[0][1]);
+        put(0, xw[0]);
+        put(1, xw[1]);
         float own[4], other[4];
-        half_of(xq[0], kh, own);
-        half_of(xq[0], !kh, other);
+        half_of(xq, kh, own);
+        half_of(xq, !kh, other);
         put(2, other);
         bar_sync(BAR_JOIN + (warp >> 1), 64);
-        add(0, xw[0][0]);
-        add(1, xw[0][1]);
+        add(0, xw[0]);
+        add(1, xw[1]);
         add(2, own);
 #pragma unroll
-        for (int p = 0; p < 4; ++p) xq[0][0][p] = xq[0][1][p] = own[p];
+        for (int p = 0; p < 4; ++p) xq[0][p] = xq[1][p] = own[p];
     }
-    uint32_t th[4], tlo[4], nh[MT][4], nl[MT][4];
+    uint32_t th[4], tlo[4], nh[4], nl[4];
     ldsm4(th, tc::smem_u32(in.t2) + tl);
     ldsm4(tlo, tc::smem_u32(in.t2) + kTile + tl);
     const float2 b[2] = {*reinterpret_cast<const float2 *>(&beta[tc2]),
                          *reinterpret_cast<const float2 *>(&beta[8 + tc2])};
+    // transposed 8x8 blocks (tokens 0-7, dv 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
+    uint32_t vr[4];
+    ldsm4t(vr, tc::smem_u32(v) + plane_off(lrow, tile * 2 + lcol));
+    float R[2][4];  // v - kw S
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        // transposed 8x8 blocks (tokens 0-7, dv 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
-        uint32_t vr[4];
-        ldsm4t(vr, tc::smem_u32(v) + plane_off(lrow, (tile + t) * 2 + lcol));
-        float R[2][4];  // v - kw S
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float2 x = unpack2<T16>(vr[2 * j]), y = unpack2<T16>(vr[2 * j + 1]);
-            R[j][0] = x.x - xw[t][j][0];
-            R[j][1] = x.y - xw[t][j][1];
-            R[j][2] = y.x - xw[t][j][2];
-            R[j][3] = y.y - xw[t][j][3];
-            e[t][j][0] = e[t][j][1] = e[t][j][2] = e[t][j][3] = 0.f;
-        }
-        if (CAREFUL) {
-            mma_causal(e[t], R, tc::smem_u32(in.t2), tc::smem_u32(in.t2) + kTile, lane);
-        } else {
-            uint32_t ah[4], al[4];
-            float e2[2][4] = {}, e3[2][4] = {};
-            split_frag(R[0], R[1], ah, al);
-            mma16816(e[t][0], ah, th[0], th[1]);
-            mma16816(e[t][1], ah, th[2], th[3]);
-            mma16816(e2[0], ah, tlo[0], tlo[1]);
-            mma16816(e2[1], ah, tlo[2], tlo[3]);
-            mma16816(e3[0], al, th[0], th[1]);
-            mma16816(e3[1], al, th[2], th[3]);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int p = 0; p < 4; ++p) e[t][j][p] += e2[j][p] + e3[j][p];
-        }
-        float nb[2][4];  // n = beta e
+    for (int j = 0; j < 2; ++j) {
+        const float2 x = unpack2<T16>(vr[2 * j]), y = unpack2<T16>(vr[2 * j + 1]);
+        R[j][0] = x.x - xw[j][0];
+        R[j][1] = x.y - xw[j][1];
+        R[j][2] = y.x - xw[j][2];
+        R[j][3] = y.y - xw[j][3];
+        e[j][0] = e[j][1] = e[j][2] = e[j][3] = 0.f;
+    }
+    if (CAREFUL) {
+        mma_causal(e, R, tc::smem_u32(in.t2), tc::smem_u32(in.t2) + kTile, lane);
+    } else {
+        uint32_t ah[4], al[4];
+        float e2[2][4] = {}, e3[2][4] = {};
+        split_frag(R[0], R[1], ah, al);
+        mma16816(e[0], ah, th[0], th[1]);
+        mma16816(e[1], ah, th[2], th[3]);
+        mma16816(e2[0], ah, tlo[0], tlo[1]);
+        mma16816(e2[1], ah, tlo[2], tlo[3]);
+        mma16816(e3[0], al, th[0], th[1]);
+        mma16816(e3[1], al, th[2], th[3]);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int p = 0; p < 4; ++p) nb[j][p] = e[t][j][p] * (p & 1 ? b[j].y : b[j].x);
-        split_frag(nb[0], nb[1], nh[t], nl[t]);
-        if (CAREFUL) mma_causal(xq[t], nb, tc::smem_u32(in.p), tc::smem_u32(in.p) + kTile, lane);
+            for (int p = 0; p < 4; ++p) e[j][p] += e2[j][p] + e3[j][p];
     }
+    float nb[2][4];  // n = beta e
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int p = 0; p < 4; ++p) nb[j][p] = e[j][p] * (p & 1 ? b[j].y : b[j].x);
+    split_frag(nb[0], nb[1], nh, nl);
+    if (CAREFUL) mma_causal(xq, nb, tc::smem_u32(in.p), tc::smem_u32(in.p) + kTile, lane);
     // S' = 2^g_l (S + (k 2^-g)^T n), or with strong gates 2^g_l S + (k 2^(g_l - g))^T n
     const bool from_start = !CAREFUL || uniform(in.from_start);
     if (CAREFUL && !from_start) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int jj = 0; jj < 8 / KS; ++jj) decay_cols(S[t], in.decay + 16 * k0, jj, tc2);
+        for (int jj = 0; jj < 8 / KS; ++jj) decay_cols(S, in.decay + 16 * k0, jj, tc2);
     }
 #pragma unroll
     for (int jj = 0; jj < 8 / KS; jj += 2) {
@@ -397,38 +380,32 @@ __device__ __forceinline__ void consume(float (&S)[MT][16 / KS][4], float (&xq)[
         ldsm4t(ch, pl + KD_HI * kPlane + o1);
         ldsm4t(bl, pl + KD_LO * kPlane + o0);
         ldsm4t(cl, pl + KD_LO * kPlane + o1);
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-            mma3x2<true>(S[t][2 * jj], S[t][2 * jj + 1], S[t][2 * jj + 2], S[t][2 * jj + 3], nh[t],
-                         nl[t], bh, bl, nh[t], nl[t], ch, cl);
+        mma3x2<true>(S[2 * jj], S[2 * jj + 1], S[2 * jj + 2], S[2 * jj + 3], nh,
+                     nl, bh, bl, nh, nl, ch, cl);
     }
     // o = qw S + P n
     if (!CAREFUL) {
         ldsm4(th, tc::smem_u32(in.p) + tl);
         ldsm4(tlo, tc::smem_u32(in.p) + kTile + tl);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            if (KS == 1) {
-                mma3(xq[t][0], xq[t][1], nh[t], nl[t], th, tlo);
-            } else {
-                const uint32_t h0 = kh ? th[2] : th[0], h1 = kh ? th[3] : th[1];
-                const uint32_t l0 = kh ? tlo[2] : tlo[0], l1 = kh ? tlo[3] : tlo[1];
-                mma16816(xq[t][0], nh[t], h0, h1);
-                mma16816(xq[t][0], nh[t], l0, l1);
-                mma16816(xq[t][0], nl[t], h0, h1);
-            }
+        if (KS == 1) {
+            mma3(xq[0], xq[1], nh, nl, th, tlo);
+        } else {
+            const uint32_t h0 = kh ? th[2] : th[0], h1 = kh ? th[3] : th[1];
+            const uint32_t l0 = kh ? tlo[2] : tlo[0], l1 = kh ? tlo[3] : tlo[1];
+            mma16816(xq[0], nh, h0, h1);
+            mma16816(xq[0], nh, l0, l1);
+            mma16816(xq[0], nl, h0, h1);
         }
     }
     if (from_start) {
 #pragma unroll
-        for (int jj = 0; jj < 8 / KS; ++jj)
-#pragma unroll
-            for (int t = 0; t < MT; ++t) decay_cols(S[t], in.decay + 16 * k0, jj, tc2);
+        for (int jj = 0; jj < 8 / KS; ++jj) decay_cols(S, in.decay + 16 * k0, jj, tc2);
     }
 }
 
-// Four consumer warps, KS for each 16 MT columns of dv: a head takes 2 KS / MT CTAs.
-template <int KS> using Roles = chunk::Roles<4, 4 * KS + 4, 4>;
+// NW consumer warps, KS for each 16 columns of dv: a head takes 8 KS / NW CTAs.  Four of these
+// are bound by the preparation, which then has eight warps instead of four.
+template <int NW, int KS> using Roles = chunk::Roles<NW, 4 * KS + 4, 4>;
 
 // Eight tokens of o and, for the backward, of e on their way out.
 template <typename T16, bool SAVE>
@@ -445,15 +422,15 @@ __device__ __forceinline__ void finish(const ChunkFwdArgs &a, const float (&o)[4
     }
 }
 
-template <typename T16, int MT, int KS, bool SAVE>
-__global__ void __launch_bounds__(Roles<KS>::kThreads, 1)
+template <typename T16, int NW, int KS, bool SAVE>
+__global__ void __launch_bounds__(Roles<NW, KS>::kThreads, 1)
     kda_chunk_fwd_kernel(const ChunkFwdArgs a) {
-    constexpr int NW = 4, kSlice = 16 * NW * MT / KS, kSplit = D / kSlice, kJ = 16 / KS;
+    constexpr int kSlice = 16 * NW / KS, kSplit = D / kSlice, kJ = 16 / KS;
     constexpr int kPrep = 128 * KS;  // threads that prepare operands
     extern __shared__ __align__(128) char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int lane = threadIdx.x & 31;
-    const Roles<KS> role(warp_index());
+    const Roles<NW, KS> role(warp_index());
     const int unit = blockIdx.x / kSplit, dv0 = (blockIdx.x % kSplit) * kSlice;
     const int n = by_length(unit / a.HV, a.num_seqs, a.T, a.cu_seqlens);
     const int hv = unit % a.HV, h = hv / (a.HV / a.H);
@@ -551,24 +528,22 @@ __global__ void __launch_bounds__(Roles<KS>::kThreads, 1)
     // ------------------------------------------------------------------ consumers
     role.take();
     // this warp's tiles of the slice, its first dv column, its part of dk
-    const int cw = role.consumer, tile = cw / KS * MT, d0 = dv0 + tile * 16, kh = cw % KS;
+    const int cw = role.consumer, tile = cw / KS, d0 = dv0 + tile * 16, kh = cw % KS;
     const int gr = lane >> 2, tc2 = (lane & 3) * 2;
     const size_t sbase = ((size_t)n * a.HV + hv) * D * D + (size_t)kh * (D / KS) * D;
-    float S[MT][kJ][4];  // S^T: rows d0 + 16t + gr, + 8; columns dk 8j + tc2, + 1 of its part
+    float S[kJ][4];  // S^T: rows d0 + gr, + 8; columns dk 8j + tc2, + 1 of its part
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-            S[t][j][0] = S[t][j][1] = S[t][j][2] = S[t][j][3] = 0.f;
-            if (a.initial_state) {
-                const float *p =
-                    a.initial_state + sbase + (size_t)(8 * j + tc2) * D + d0 + 16 * t + gr;
-                S[t][j][0] = p[0];
-                S[t][j][1] = p[D];
-                S[t][j][2] = p[8];
-                S[t][j][3] = p[D + 8];
-            }
+    for (int j = 0; j < kJ; ++j) {
+        S[j][0] = S[j][1] = S[j][2] = S[j][3] = 0.f;
+        if (a.initial_state) {
+            const float *p =
+                a.initial_state + sbase + (size_t)(8 * j + tc2) * D + d0 + gr;
+            S[j][0] = p[0];
+            S[j][1] = p[D];
+            S[j][2] = p[8];
+            S[j][3] = p[D + 8];
         }
+    }
 
     const size_t orow = (size_t)a.HV * D;
     uint16_t *o_at = (uint16_t *)a.o + (size_t)sq.row0 * orow + (size_t)hv * D + d0;
@@ -576,7 +551,7 @@ __global__ void __launch_bounds__(Roles<KS>::kThreads, 1)
     for (int i = 0; i < steps; ++i) {
         const int st = i % kStages;
         const unsigned slot = (unsigned)(sq.slot0 + i / 4) * a.HV + hv;
-        float xq[MT][2][4], e[MT][2][4];
+        float xq[2][4], e[2][4];
         bar_sync(BAR_FULL + st, 32 + 32 * NW);
         const Prepared &in = sm.prep[st];
         const uint16_t(*v)[D] = sm.v[i % kRaw];
@@ -584,7 +559,7 @@ __global__ void __launch_bounds__(Roles<KS>::kThreads, 1)
         char *ckpt = SAVE ? a.ckpt + slot * kCkptBytes : nullptr;
         // tiles of 16 dv columns: of the CTA's slice for v, of the head for the checkpoint
         auto run = [&](auto with_care, auto keep) {
-            consume<T16, MT, KS, decltype(with_care)::value, decltype(keep)::value>(
+            consume<T16, KS, decltype(with_care)::value, decltype(keep)::value>(
                 S, xq, e, in, v, beta, ckpt, dv0 / 16, tile, kh, sm.join[i & 1], cw, lane);
         };
         const bool keep = SAVE && i % 4 == 0;
@@ -601,57 +576,51 @@ __global__ void __launch_bounds__(Roles<KS>::kThreads, 1)
         if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kPrep + 32 * NW);
         if (KS == 2) {  // the tokens that this warp has finished
             float eh[4], oh[4];
-            half_of(e[0], kh, eh);
-            half_of(xq[0], kh && careful, oh);
+            half_of(e, kh, eh);
+            half_of(xq, kh && careful, oh);
             finish<T16, SAVE>(a, oh, eh, slot, i, kh, o_at, orow, sq.len, d0, lane);
             continue;
         }
         if (SAVE)
+            store_rows(a.e + slot * kRowsBytes, e, (i % 4) * C, d0, lane);
+        uint32_t ow[4];
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-                store_rows(a.e + slot * kRowsBytes, e[t], (i % 4) * C, d0 + 16 * t, lane);
-        uint32_t ow[MT][4];
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                ow[t][2 * j] = pack2<T16>(xq[t][j][0], xq[t][j][1]);
-                ow[t][2 * j + 1] = pack2<T16>(xq[t][j][2], xq[t][j][3]);
-            }
-        store_out<MT>(sm.out[cw], ow, (char *)(o_at + (size_t)i * C * orow), orow * 2,
+        for (int j = 0; j < 2; ++j) {
+            ow[2 * j] = pack2<T16>(xq[j][0], xq[j][1]);
+            ow[2 * j + 1] = pack2<T16>(xq[j][2], xq[j][3]);
+        }
+        store_out(sm.out[cw], ow, (char *)(o_at + (size_t)i * C * orow), orow * 2,
                       sq.len - i * C, (char *)a.o, a.rows_o * D * 2, a.dbg, lane);
     }
     if (a.final_state) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int j = 0; j < kJ; ++j) {
-                float *p = a.final_state + sbase + (size_t)(8 * j + tc2) * D + d0 + 16 * t + gr;
-                p[0] = S[t][j][0];
-                p[D] = S[t][j][1];
-                p[8] = S[t][j][2];
-                p[D + 8] = S[t][j][3];
-            }
+        for (int j = 0; j < kJ; ++j) {
+            float *p = a.final_state + sbase + (size_t)(8 * j + tc2) * D + d0 + gr;
+            p[0] = S[j][0];
+            p[D] = S[j][1];
+            p[8] = S[j][2];
+            p[D + 8] = S[j][3];
+        }
     }
 }
 
-template <typename T16, int MT, int KS, bool SAVE>
+template <typename T16, int NW, int KS, bool SAVE>
 cudaError_t launch(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
     static volatile int done[kMaxDev];
-    const auto kernel = kda_chunk_fwd_kernel<T16, MT, KS, SAVE>;
-    const cudaError_t e = ready_once<Roles<KS>>(kernel, (int)sizeof(Smem), dev, done);
+    const auto kernel = kda_chunk_fwd_kernel<T16, NW, KS, SAVE>;
+    const cudaError_t e = ready_once<Roles<NW, KS>>(kernel, (int)sizeof(Smem), dev, done);
     if (e != cudaSuccess) return e;
-    const int grid = a.num_seqs * a.HV * (2 * KS / MT);
-    kernel<<<grid, Roles<KS>::kThreads, sizeof(Smem), stream>>>(a);
+    const int grid = a.num_seqs * a.HV * (8 * KS / NW);
+    kernel<<<grid, Roles<NW, KS>::kThreads, sizeof(Smem), stream>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T16, bool SAVE>
 cudaError_t launch_split(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
     switch (best_split(a.num_seqs, a.HV, a.cu_seqlens)) {
-        case 1: return launch<T16, 2, 1, SAVE>(a, dev, stream);
-        case 2: return launch<T16, 1, 1, SAVE>(a, dev, stream);
-        default: return launch<T16, 1, 2, SAVE>(a, dev, stream);
+        case 1: return launch<T16, 8, 1, SAVE>(a, dev, stream);
+        case 2: return launch<T16, 4, 1, SAVE>(a, dev, stream);
+        default: return launch<T16, 4, 2, SAVE>(a, dev, stream);
     }
 }
 

@@ -650,11 +650,11 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
                 }
             }
             auto put = [&](void *out, int which, const Elems &x) {
-                uint32_t w[1][4];
+                uint32_t w[4];
 #pragma unroll
                 for (int y = 0; y < 4; ++y)
-                    w[0][y] = pack_bf16(x.v[y & 1][y & 2], x.v[y & 1][(y & 2) + 1]);
-                chunk::store_out<1>(sm.out[which][warp], w,
+                    w[y] = pack_bf16(x.v[y & 1][y & 2], x.v[y & 1][(y & 2) + 1]);
+                chunk::store_out(sm.out[which][warp], w,
                                     (char *)((uint16_t *)out + out_at + (size_t)j * C * orow),
                                     orow * 2, rows - j * C, (char *)out, a.rows_o * D * 2, a.dbg,
                                     lane);

@@ -29,7 +29,7 @@ struct __align__(128) Smem {
     uint16_t dout[kRaw][C][D];  // rows of the CTA's dv slice, swizzled chunks
     char tiles[kRaw][2 * kTall];
     float beta[kRaw][C];
-    char out[4][2 * 512];  // a consumer's dv on its way out
+    char out[8][512];  // a consumer's dv on its way out
 };
 
 // Step i of the walk (the last step of the sequence first), tokens 16 * step on.
@@ -59,10 +59,10 @@ __device__ __forceinline__ void load_step(Smem &sm, const ChunkBwdArgs &a, const
           true);
 }
 
-template <int NW, int MT>
+template <int NW>
 __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
     kda_fast_bwd_state_kernel(const ChunkBwdArgs a) {
-    constexpr int kSlice = 16 * NW * MT, kSplit = D / kSlice;
+    constexpr int kSlice = 16 * NW, kSplit = D / kSlice;
     extern __shared__ __align__(128) char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int lane = threadIdx.x & 31;
@@ -111,26 +111,23 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
 
     role.take();
     if (role.consumer < 0) return;
-    const int tile0 = dv0 / 16 + role.consumer * MT;
+    const int tile0 = dv0 / 16 + role.consumer;
     const int gr = lane >> 2, tc2 = (lane & 3) * 2;
     const int lrow = (lane & 7) + ((lane >> 4) & 1) * 8, lcol = (lane >> 3) & 1;
     const int trow = lane & 15, tcol = lane >> 4;
-    Tile S[MT];
+    Tile S;
     const size_t sbase = ((size_t)n * a.HV + hv) * D * D + (size_t)tc2 * D + tile0 * 16 + gr;
+    S.clear();
+    if (a.d_final_state) {
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        S[t].clear();
-        if (a.d_final_state) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const float *p = a.d_final_state + sbase + (size_t)8 * j * D + 16 * t;
-                S[t].s[j][0] = p[0];
-                S[t].s[j][1] = p[D];
-                S[t].s[j][2] = p[8];
-                S[t].s[j][3] = p[D + 8];
-            }
-            S[t].bound = 2.f * kLimit;
+        for (int j = 0; j < 16; ++j) {
+            const float *p = a.d_final_state + sbase + (size_t)8 * j * D;
+            S.s[j][0] = p[0];
+            S.s[j][1] = p[D];
+            S.s[j][2] = p[8];
+            S.s[j][3] = p[D + 8];
         }
+        S.bound = 2.f * kLimit;
     }
     const size_t vrow = (size_t)a.HV * D;
     uint16_t *dv_at = (uint16_t *)a.dv + (size_t)sq.row0 * vrow + (size_t)hv * D + tile0 * 16;
@@ -144,86 +141,68 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         const uint32_t kw = smem_u32(in.kw), qw = smem_u32(in.qw), kd = smem_u32(in.kd);
         const float kmax = largest(in.kmax), qmax = a.scale * largest(in.qmax), bm = in.bmax;
         bool careful = in.careful || !(kmax <= 16384.f) || !(qmax <= 16384.f);
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-            if (chunk::uniform(S[t].bound > kLimit)) S[t].renew();
+        if (chunk::uniform(S.bound > kLimit)) S.renew();
         uint32_t th[4], tl[4], ph[4], pl[4];
         load_tall(smem_u32(sm.tiles[slot]), lane, tl, th);
         load_tall(smem_u32(sm.tiles[slot]) + kTall, lane, pl, ph);
         const float2 b[2] = {*reinterpret_cast<const float2 *>(&sm.beta[slot][tc2]),
                              *reinterpret_cast<const float2 *>(&sm.beta[slot][8 + tc2])};
-        uint32_t dor[MT][4];  // do^T, BF16 pairs of tokens
-        float om[MT], ds[MT][2][4] = {};
+        uint32_t dor[4];  // do^T, BF16 pairs of tokens
+        float ds[2][4] = {};
+        ldsm4t(dor, smem_u32(sm.dout[slot]) + plane_off(lrow, role.consumer * 2 + lcol));
+        uint32_t m = 0;
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            ldsm4t(dor[t], smem_u32(sm.dout[slot]) +
-                               plane_off(lrow, (role.consumer * MT + t) * 2 + lcol));
-            uint32_t m = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) m = __vmaxu2(m, dor[t][j] & 0x7fff7fffu);
-            om[t] = __uint_as_float(
-                __reduce_max_sync(0xffffffffu, max(m << 16, m & 0xffff0000u)));
-        }
+        for (int j = 0; j < 4; ++j) m = __vmaxu2(m, dor[j] & 0x7fff7fffu);
+        const float om = __uint_as_float(
+            __reduce_max_sync(0xffffffffu, max(m << 16, m & 0xffff0000u)));
         // dS' kd
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
             uint32_t kf[4];
             ldsm4(kf, kd + plane_off(lrow, 2 * kk + lcol));
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                const float(&x)[4] = S[t].s[2 * kk], (&y)[4] = S[t].s[2 * kk + 1];
-                const uint32_t af[4] = {pack_f16(x[0], x[1]), pack_f16(x[2], x[3]),
-                                        pack_f16(y[0], y[1]), pack_f16(y[2], y[3])};
-                mma_f16(ds[t][0], af, kf[0], kf[1]);
-                mma_f16(ds[t][1], af, kf[2], kf[3]);
-            }
+            const float(&x)[4] = S.s[2 * kk], (&y)[4] = S.s[2 * kk + 1];
+            const uint32_t af[4] = {pack_f16(x[0], x[1]), pack_f16(x[2], x[3]),
+                                    pack_f16(y[0], y[1]), pack_f16(y[2], y[3])};
+            mma_f16(ds[0], af, kf[0], kf[1]);
+            mma_f16(ds[1], af, kf[2], kf[3]);
         }
         if (keep)  // outside the loop above, which a branch would cut into pieces
+            store_tile(a.dckpt + unit_at * kCkptBytes, S, tile0, lane);
+        const float ckpt_scale = S.saved_scale();
+        float y[2][4] = {};
+        // dn^T = do^T P + dS'^T kd^T (do is exact in TF32), Y^T = dn^T T
+        float dn[2][4] = {};
+        const uint32_t o0[4] = {dor[0] << 16, dor[1] << 16, dor[0] & 0xffff0000u,
+                                dor[1] & 0xffff0000u};
+        const uint32_t o1[4] = {dor[2] << 16, dor[3] << 16, dor[2] & 0xffff0000u,
+                                dor[3] & 0xffff0000u};
+        mma_tall(dn[0], dn[1], o0, o1, pl, ph);
+        uint32_t x0[4], x1[4];
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-                store_tile(a.dckpt + unit_at * kCkptBytes, S[t], tile0 + t, lane);
-        float y[MT][2][4] = {}, ym[MT], ckpt_scale[MT];
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            ckpt_scale[t] = S[t].saved_scale();
-            // dn^T = do^T P + dS'^T kd^T (do is exact in TF32), Y^T = dn^T T
-            float dn[2][4] = {};
-            const uint32_t o0[4] = {dor[t][0] << 16, dor[t][1] << 16, dor[t][0] & 0xffff0000u,
-                                    dor[t][1] & 0xffff0000u};
-            const uint32_t o1[4] = {dor[t][2] << 16, dor[t][3] << 16, dor[t][2] & 0xffff0000u,
-                                    dor[t][3] & 0xffff0000u};
-            mma_tall(dn[0], dn[1], o0, o1, pl, ph);
-            uint32_t x0[4], x1[4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int p = 0; p < 4; ++p) dn[j][p] = fmaf(ds[t][j][p], S[t].inv, dn[j][p]);
-            tf_frag(dn[0], x0);
-            tf_frag(dn[1], x1);
-            mma_tall(y[t][0], y[t][1], x0, x1, tl, th);
-            ym[t] = warp_max(abs_max(y[t]));
-            careful = careful || !finite(ym[t]) || !finite(om[t]);
-        }
+            for (int p = 0; p < 4; ++p) dn[j][p] = fmaf(ds[j][p], S.inv, dn[j][p]);
+        tf_frag(dn[0], x0);
+        tf_frag(dn[1], x1);
+        mma_tall(y[0], y[1], x0, x1, tl, th);
+        float ym = warp_max(abs_max(y));
+        careful = careful || !finite(ym) || !finite(om);
         if (!chunk::uniform(careful)) {
-            uint32_t of[MT][4], nf[MT][4];
-            float ratio[MT];
+            uint32_t of[4], nf[4];
+            const float ratio = join_scale(S, fmaxf(om, ym * bm), C * (kmax + qmax));
+            const float c = S.c;
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                ratio[t] = join_scale(S[t], fmaxf(om[t], ym[t] * bm), C * (kmax + qmax));
-                const float c = S[t].c;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 o = bf2(dor[t][j]);
-                    of[t][j] = pack_f16(o.x * c, o.y * c);
-                }
-                const float nx[2] = {-b[0].x * c, -b[1].x * c}, ny[2] = {-b[0].y * c, -b[1].y * c};
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    nf[t][2 * j] = pack_f16(y[t][j][0] * nx[j], y[t][j][1] * ny[j]);
-                    nf[t][2 * j + 1] = pack_f16(y[t][j][2] * nx[j], y[t][j][3] * ny[j]);
-                }
-                S[t].inv = inverse_of(c);
+            for (int j = 0; j < 4; ++j) {
+                const float2 o = bf2(dor[j]);
+                of[j] = pack_f16(o.x * c, o.y * c);
             }
+            const float nx[2] = {-b[0].x * c, -b[1].x * c}, ny[2] = {-b[0].y * c, -b[1].y * c};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                nf[2 * j] = pack_f16(y[j][0] * nx[j], y[j][1] * ny[j]);
+                nf[2 * j + 1] = pack_f16(y[j][2] * nx[j], y[j][3] * ny[j]);
+            }
+            S.inv = inverse_of(c);
             // dS = diag(2^g_l) dS' + qw^T do - kw^T dv
 #pragma unroll
             for (int jj = 0; jj < 8; ++jj) {
@@ -234,73 +213,58 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
                 for (int x = 0; x < 2; ++x) {
                     const float2 d =
                         *reinterpret_cast<const float2 *>(&in.decay[16 * jj + 8 * x + tc2]);
-#pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        float(&s)[4] = S[t].s[2 * jj + x];
-                        const float2 dr = chunk::mul2(d, make_float2(ratio[t], ratio[t]));
-                        const float2 u = chunk::mul2(make_float2(s[0], s[1]), dr);
-                        const float2 w = chunk::mul2(make_float2(s[2], s[3]), dr);
-                        s[0] = u.x; s[1] = u.y; s[2] = w.x; s[3] = w.y;
-                        mma_f16(s, of[t], qf[2 * x], qf[2 * x + 1]);
-                    }
+                    float(&s)[4] = S.s[2 * jj + x];
+                    const float2 dr = chunk::mul2(d, make_float2(ratio, ratio));
+                    const float2 u = chunk::mul2(make_float2(s[0], s[1]), dr);
+                    const float2 w = chunk::mul2(make_float2(s[2], s[3]), dr);
+                    s[0] = u.x; s[1] = u.y; s[2] = w.x; s[3] = w.y;
+                    mma_f16(s, of, qf[2 * x], qf[2 * x + 1]);
                 }
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int t = 0; t < MT; ++t)
-                        mma_f16(S[t].s[2 * jj + x], nf[t], kf[2 * x], kf[2 * x + 1]);
+                    mma_f16(S.s[2 * jj + x], nf, kf[2 * x], kf[2 * x + 1]);
             }
         } else {
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                walk_tokens_back(S[t], y[t], sm.raw[slot], sm.beta[slot], sm.dout[slot],
-                                 (role.consumer * MT + t) * 16, a.scale, lane);
-                ym[t] = warp_max(abs_max(y[t]));
-            }
+            walk_tokens_back(S, y, sm.raw[slot], sm.beta[slot], sm.dout[slot],
+                             role.consumer * 16, a.scale, lane);
+            ym = warp_max(abs_max(y));
         }
         if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kHalf + 32 * NW);
-        float s[MT];
-        uint32_t dw[MT][4];  // dv = beta Y
+        uint32_t dw[4];  // dv = beta Y
+        const float s =
+            store_block(a.y + unit_at * kRowsBytes, y, ym, (step % 4) * 8 + tile0, lane);
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            s[t] = store_block(a.y + unit_at * kRowsBytes, y[t], ym[t],
-                               (step % 4) * 8 + tile0 + t, lane);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                dw[t][2 * j] = chunk::pack_bf16(b[j].x * y[t][j][0], b[j].y * y[t][j][1]);
-                dw[t][2 * j + 1] = chunk::pack_bf16(b[j].x * y[t][j][2], b[j].y * y[t][j][3]);
-            }
+        for (int j = 0; j < 2; ++j) {
+            dw[2 * j] = chunk::pack_bf16(b[j].x * y[j][0], b[j].y * y[j][1]);
+            dw[2 * j + 1] = chunk::pack_bf16(b[j].x * y[j][2], b[j].y * y[j][3]);
         }
-        if (lane < MT) {
-            float *scales = a.dscales + unit_at * kScales + tile0 + lane;
-            scales[8 + (step % 4) * 8] = lane ? s[MT - 1] : s[0];
-            if (keep) scales[0] = lane ? ckpt_scale[MT - 1] : ckpt_scale[0];
+        if (lane == 0) {
+            float *scales = a.dscales + unit_at * kScales + tile0;
+            scales[8 + (step % 4) * 8] = s;
+            if (keep) scales[0] = ckpt_scale;
         }
-        chunk::store_out<MT>(sm.out[role.consumer], dw, (char *)(dv_at + (size_t)step * C * vrow),
-                             vrow * 2, sq.len - step * C, (char *)a.dv, a.rows_o * D * 2, a.dbg,
-                             lane);
+        chunk::store_out(sm.out[role.consumer], dw, (char *)(dv_at + (size_t)step * C * vrow),
+                         vrow * 2, sq.len - step * C, (char *)a.dv, a.rows_o * D * 2, a.dbg, lane);
     }
     if (a.d_initial_state) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                float *p = a.d_initial_state + sbase + (size_t)8 * j * D + 16 * t;
-                p[0] = S[t].s[j][0] * S[t].inv;
-                p[D] = S[t].s[j][1] * S[t].inv;
-                p[8] = S[t].s[j][2] * S[t].inv;
-                p[D + 8] = S[t].s[j][3] * S[t].inv;
-            }
+        for (int j = 0; j < 16; ++j) {
+            float *p = a.d_initial_state + sbase + (size_t)8 * j * D;
+            p[0] = S.s[j][0] * S.inv;
+            p[D] = S.s[j][1] * S.inv;
+            p[8] = S.s[j][2] * S.inv;
+            p[D + 8] = S.s[j][3] * S.inv;
+        }
     }
 }
 
-template <int NW, int MT>
+template <int NW>
 cudaError_t launch(const ChunkBwdArgs &a, int dev, cudaStream_t stream) {
     static volatile int done[kMaxDev];
-    cudaError_t e = chunk::ready_once<Roles<NW>>(kda_fast_bwd_state_kernel<NW, MT>,
+    cudaError_t e = chunk::ready_once<Roles<NW>>(kda_fast_bwd_state_kernel<NW>,
                                             (int)sizeof(Smem), dev, done);
     if (e != cudaSuccess) return e;
-    kda_fast_bwd_state_kernel<NW, MT><<<a.num_seqs * a.HV * (D / (16 * NW * MT)),
+    kda_fast_bwd_state_kernel<NW><<<a.num_seqs * a.HV * (8 / NW),
                                         Roles<NW>::kThreads, sizeof(Smem), stream>>>(a);
     return cudaGetLastError();
 }
@@ -309,9 +273,9 @@ cudaError_t launch(const ChunkBwdArgs &a, int dev, cudaStream_t stream) {
 
 cudaError_t launch_bwd_state(const ChunkBwdArgs &a, int dev, cudaStream_t stream) {
     switch (chunk::best_split(a.num_seqs, a.HV, a.cu_seqlens)) {
-        case 1: return launch<4, 2>(a, dev, stream);
-        case 2: return launch<4, 1>(a, dev, stream);
-        default: return launch<2, 1>(a, dev, stream);
+        case 1: return launch<8>(a, dev, stream);
+        case 2: return launch<4>(a, dev, stream);
+        default: return launch<2>(a, dev, stream);
     }
 }
 

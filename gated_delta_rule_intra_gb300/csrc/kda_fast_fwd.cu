@@ -44,7 +44,7 @@ struct __align__(128) Smem {
     float a1[kSolvers][C][C + 4];  // (diag(beta) M)^T
     char pt[kSolvers][kTall];      // P^T on its way to the saved tiles
     int big[kSolvers][4];          // whether a warp's entries of P are out of FP16's reach
-    char out[4][2 * 512];          // a consumer's o on its way out
+    char out[8][512];          // a consumer's o on its way out
 };
 
 // A preparing thread's pointers to the raw inputs; step s is `s` steps further on.
@@ -229,11 +229,11 @@ __device__ __forceinline__ void solve(Smem &sm, Stage &out, int buf, char *tiles
     }
 }
 
-// NW consumer warps of 16 MT dv columns each; a head takes 128 / (16 NW MT) CTAs.
-template <int NW, int MT, bool SAVE>
+// NW consumer warps of 16 dv columns each; a head takes 8 / NW CTAs.
+template <int NW, bool SAVE>
 __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
     kda_fast_fwd_kernel(const ChunkFwdArgs a) {
-    constexpr int kSlice = 16 * NW * MT, kSplit = D / kSlice;
+    constexpr int kSlice = 16 * NW, kSplit = D / kSlice;
     extern __shared__ __align__(128) char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int lane = threadIdx.x & 31;
@@ -334,13 +334,12 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
     // ------------------------------------------------------------------ consumers
     role.take();
     if (role.consumer < 0) return;
-    const int tile0 = dv0 / 16 + role.consumer * MT;  // the head's tile of 16 dv columns
+    const int tile0 = dv0 / 16 + role.consumer;  // the head's tile of 16 dv columns
     const int tc2 = (lane & 3) * 2;
     const int lrow = (lane & 7) + ((lane >> 4) & 1) * 8, lcol = (lane >> 3) & 1;
     const int trow = lane & 15, tcol = lane >> 4;
-    Tile S[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) S[t].clear();
+    Tile S;
+    S.clear();
     const size_t orow = (size_t)a.HV * D;
     uint16_t *o_at = (uint16_t *)a.o + (size_t)sq.row0 * orow + (size_t)hv * D + tile0 * 16;
 
@@ -354,75 +353,58 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         const float kmax = largest(in.pl.kmax);
         const bool keep = SAVE && i % 4 == 0;
         bool careful = chunk::uniform(in.pl.careful);
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-            if (chunk::uniform(S[t].bound > kLimit)) S[t].renew();
+        if (chunk::uniform(S.bound > kLimit)) S.renew();
         uint32_t th[4], tl[4], pf[4];
         load_tall(smem_u32(in.t2), lane, tl, th);
         ldsm4(pf, smem_u32(in.p) + chunk::tile_lane(lane));
         const float2 b[2] = {*reinterpret_cast<const float2 *>(&beta[tc2]),
                              *reinterpret_cast<const float2 *>(&beta[8 + tc2])};
-        float xw[MT][2][4] = {}, xq[MT][2][4] = {}, e[MT][2][4] = {};
+        float xw[2][4] = {}, xq[2][4] = {}, e[2][4] = {};
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
             uint32_t kf[4], qf[4];
             const uint32_t off = plane_off(lrow, 2 * kk + lcol);
             ldsm4(kf, kw + off);
             ldsm4(qf, qw + off);
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                const float(&x)[4] = S[t].s[2 * kk], (&y)[4] = S[t].s[2 * kk + 1];
-                const uint32_t af[4] = {pack_f16(x[0], x[1]), pack_f16(x[2], x[3]),
-                                        pack_f16(y[0], y[1]), pack_f16(y[2], y[3])};
-                mma_f16(xw[t][0], af, kf[0], kf[1]);
-                mma_f16(xw[t][1], af, kf[2], kf[3]);
-                mma_f16(xq[t][0], af, qf[0], qf[1]);
-                mma_f16(xq[t][1], af, qf[2], qf[3]);
-            }
+            const float(&x)[4] = S.s[2 * kk], (&y)[4] = S.s[2 * kk + 1];
+            const uint32_t af[4] = {pack_f16(x[0], x[1]), pack_f16(x[2], x[3]),
+                                    pack_f16(y[0], y[1]), pack_f16(y[2], y[3])};
+            mma_f16(xw[0], af, kf[0], kf[1]);
+            mma_f16(xw[1], af, kf[2], kf[3]);
+            mma_f16(xq[0], af, qf[0], qf[1]);
+            mma_f16(xq[1], af, qf[2], qf[3]);
         }
         if (keep)  // outside the loop above, which a branch would cut into pieces
+            store_tile(a.ckpt + unit_at * kCkptBytes, S, tile0, lane);
+        const float ckpt_scale = S.saved_scale(), inv = S.inv;  // of the state as an operand
+        // R = v - kw S and e = T2 R; blocks (tokens 0-7, dv 0-7), (0-7, 8-15), (8-15, ..)
+        uint32_t vr[4], x0[4], x1[4];
+        ldsm4t(vr, smem_u32(sm.v[slot]) + plane_off(lrow, role.consumer * 2 + lcol));
+        float R[2][4];
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-                store_tile(a.ckpt + unit_at * kCkptBytes, S[t], tile0 + t, lane);
-        float em[MT], ckpt_scale[MT], inv[MT];  // of the state as it was an operand
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            ckpt_scale[t] = S[t].saved_scale();
-            inv[t] = S[t].inv;
-            // R = v - kw S and e = T2 R; blocks (tokens 0-7, dv 0-7), (0-7, 8-15), (8-15, ..)
-            uint32_t vr[4], x0[4], x1[4];
-            ldsm4t(vr, smem_u32(sm.v[slot]) +
-                           plane_off(lrow, (role.consumer * MT + t) * 2 + lcol));
-            float R[2][4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float2 x = bf2(vr[2 * j]), y = bf2(vr[2 * j + 1]);
-                R[j][0] = fmaf(xw[t][j][0], -inv[t], x.x);
-                R[j][1] = fmaf(xw[t][j][1], -inv[t], x.y);
-                R[j][2] = fmaf(xw[t][j][2], -inv[t], y.x);
-                R[j][3] = fmaf(xw[t][j][3], -inv[t], y.y);
-            }
-            tf_frag(R[0], x0);
-            tf_frag(R[1], x1);
-            mma_tall(e[t][0], e[t][1], x0, x1, tl, th);
-            em[t] = warp_max(abs_max(e[t]));
-            careful = careful || !finite(em[t]);
+        for (int j = 0; j < 2; ++j) {
+            const float2 x = bf2(vr[2 * j]), y = bf2(vr[2 * j + 1]);
+            R[j][0] = fmaf(xw[j][0], -inv, x.x);
+            R[j][1] = fmaf(xw[j][1], -inv, x.y);
+            R[j][2] = fmaf(xw[j][2], -inv, y.x);
+            R[j][3] = fmaf(xw[j][3], -inv, y.y);
         }
+        tf_frag(R[0], x0);
+        tf_frag(R[1], x1);
+        mma_tall(e[0], e[1], x0, x1, tl, th);
+        float em = warp_max(abs_max(e));
+        careful = careful || !finite(em);
         const float bm = in.pl.bmax;
         if (!chunk::uniform(careful)) {
             // n = beta e
-            uint32_t nf[MT][4];
-            float ratio[MT];
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                ratio[t] = join_scale(S[t], em[t] * bm, C * kmax);
-                const float c = S[t].c;
-                nf[t][0] = pack_f16(e[t][0][0] * (b[0].x * c), e[t][0][1] * (b[0].y * c));
-                nf[t][1] = pack_f16(e[t][0][2] * (b[0].x * c), e[t][0][3] * (b[0].y * c));
-                nf[t][2] = pack_f16(e[t][1][0] * (b[1].x * c), e[t][1][1] * (b[1].y * c));
-                nf[t][3] = pack_f16(e[t][1][2] * (b[1].x * c), e[t][1][3] * (b[1].y * c));
-                S[t].inv = inverse_of(c);
-            }
+            uint32_t nf[4];
+            const float ratio = join_scale(S, em * bm, C * kmax);
+            const float c = S.c;
+            nf[0] = pack_f16(e[0][0] * (b[0].x * c), e[0][1] * (b[0].y * c));
+            nf[1] = pack_f16(e[0][2] * (b[0].x * c), e[0][3] * (b[0].y * c));
+            nf[2] = pack_f16(e[1][0] * (b[1].x * c), e[1][1] * (b[1].y * c));
+            nf[3] = pack_f16(e[1][2] * (b[1].x * c), e[1][3] * (b[1].y * c));
+            S.inv = inverse_of(c);
             // S' = diag(2^g_l) S + kd^T n
 #pragma unroll
             for (int jj = 0; jj < 8; ++jj) {
@@ -432,79 +414,64 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
                 for (int x = 0; x < 2; ++x) {
                     const float2 d =
                         *reinterpret_cast<const float2 *>(&in.pl.decay[16 * jj + 8 * x + tc2]);
-#pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        float(&s)[4] = S[t].s[2 * jj + x];
-                        const float2 dr = chunk::mul2(d, make_float2(ratio[t], ratio[t]));
-                        const float2 u = chunk::mul2(make_float2(s[0], s[1]), dr);
-                        const float2 w = chunk::mul2(make_float2(s[2], s[3]), dr);
-                        s[0] = u.x; s[1] = u.y; s[2] = w.x; s[3] = w.y;
-                        mma_f16(s, nf[t], kf[2 * x], kf[2 * x + 1]);
-                    }
+                    float(&s)[4] = S.s[2 * jj + x];
+                    const float2 dr = chunk::mul2(d, make_float2(ratio, ratio));
+                    const float2 u = chunk::mul2(make_float2(s[0], s[1]), dr);
+                    const float2 w = chunk::mul2(make_float2(s[2], s[3]), dr);
+                    s[0] = u.x; s[1] = u.y; s[2] = w.x; s[3] = w.y;
+                    mma_f16(s, nf, kf[2 * x], kf[2 * x + 1]);
                 }
             }
             // o = qw S + P n
+            float po[2][4] = {};
+            mma_f16(po[0], nf, pf[0], pf[1]);
+            mma_f16(po[1], nf, pf[2], pf[3]);
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                float po[2][4] = {};
-                mma_f16(po[0], nf[t], pf[0], pf[1]);
-                mma_f16(po[1], nf[t], pf[2], pf[3]);
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int p = 0; p < 4; ++p)
-                        xq[t][j][p] = fmaf(po[j][p], S[t].inv, xq[t][j][p] * inv[t]);
-            }
+                for (int p = 0; p < 4; ++p) xq[j][p] = fmaf(po[j][p], S.inv, xq[j][p] * inv);
         } else {
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                walk_tokens(S[t], xq[t], e[t], sm.raw[slot], beta, sm.v[slot],
-                            (role.consumer * MT + t) * 16, a.scale, lane);
-                em[t] = warp_max(abs_max(e[t]));
-            }
+            walk_tokens(S, xq, e, sm.raw[slot], beta, sm.v[slot], role.consumer * 16, a.scale,
+                        lane);
+            em = warp_max(abs_max(e));
         }
         if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kHalf + 32 * NW);
         if (SAVE) {
-            float s[MT];
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-                s[t] = store_block(a.e + unit_at * kRowsBytes, e[t], em[t],
-                                   (i % 4) * 8 + tile0 + t, lane);
-            if (lane < MT) {
-                float *scales = a.scales + unit_at * kScales + tile0 + lane;
-                scales[8 + (i % 4) * 8] = lane ? s[MT - 1] : s[0];
-                if (keep) scales[0] = lane ? ckpt_scale[MT - 1] : ckpt_scale[0];
+            const float s =
+                store_block(a.e + unit_at * kRowsBytes, e, em, (i % 4) * 8 + tile0, lane);
+            if (lane == 0) {
+                float *scales = a.scales + unit_at * kScales + tile0;
+                scales[8 + (i % 4) * 8] = s;
+                if (keep) scales[0] = ckpt_scale;
             }
         }
-        uint32_t ow[MT][4];
+        uint32_t ow[4];
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                ow[t][2 * j] = chunk::pack_bf16(xq[t][j][0], xq[t][j][1]);
-                ow[t][2 * j + 1] = chunk::pack_bf16(xq[t][j][2], xq[t][j][3]);
-            }
-        chunk::store_out<MT>(sm.out[role.consumer], ow, (char *)(o_at + (size_t)i * C * orow),
-                             orow * 2, sq.len - i * C, (char *)a.o, a.rows_o * D * 2, a.dbg, lane);
+        for (int j = 0; j < 2; ++j) {
+            ow[2 * j] = chunk::pack_bf16(xq[j][0], xq[j][1]);
+            ow[2 * j + 1] = chunk::pack_bf16(xq[j][2], xq[j][3]);
+        }
+        chunk::store_out(sm.out[role.consumer], ow, (char *)(o_at + (size_t)i * C * orow),
+                         orow * 2, sq.len - i * C, (char *)a.o, a.rows_o * D * 2, a.dbg, lane);
     }
 }
 
-template <int NW, int MT, bool SAVE>
+template <int NW, bool SAVE>
 cudaError_t launch(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
     static volatile int done[kMaxDev];
-    cudaError_t e = chunk::ready_once<Roles<NW>>(kda_fast_fwd_kernel<NW, MT, SAVE>,
+    cudaError_t e = chunk::ready_once<Roles<NW>>(kda_fast_fwd_kernel<NW, SAVE>,
                                             (int)sizeof(Smem), dev, done);
     if (e != cudaSuccess) return e;
-    const int grid = a.num_seqs * a.HV * (D / (16 * NW * MT));
-    kda_fast_fwd_kernel<NW, MT, SAVE><<<grid, Roles<NW>::kThreads, sizeof(Smem), stream>>>(a);
+    const int grid = a.num_seqs * a.HV * (8 / NW);
+    kda_fast_fwd_kernel<NW, SAVE><<<grid, Roles<NW>::kThreads, sizeof(Smem), stream>>>(a);
     return cudaGetLastError();
 }
 
 template <bool SAVE> cudaError_t launch_split(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
     switch (chunk::best_split(a.num_seqs, a.HV, a.cu_seqlens)) {
-        case 1: return launch<4, 2, SAVE>(a, dev, stream);
-        case 2: return launch<4, 1, SAVE>(a, dev, stream);
-        default: return launch<2, 1, SAVE>(a, dev, stream);
+        case 1: return launch<8, SAVE>(a, dev, stream);
+        case 2: return launch<4, SAVE>(a, dev, stream);
+        default: return launch<2, SAVE>(a, dev, stream);
     }
 }
 
