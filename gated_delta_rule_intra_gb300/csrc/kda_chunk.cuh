@@ -211,13 +211,13 @@ __device__ __forceinline__ int by_length(int rank, int num_seqs, int T, const in
 }
 
 // CTAs that a head's 128 dv columns are divided between: the fewest rounds over the SMs.  A
-// finer split repeats the preparation, but its step is shorter: one, two and four CTAs take some
-// 5.0, 3.7 and 2.7 thousand cycles for a step (B=1 T=32768 H=32: 2.63 ms in four CTAs a head, 3.7
-// in two).  Of sequences of unknown lengths the longest is taken to be four times the average, and
-// the others to fill in behind it (ten prompts of 1 to 2609 tokens, 16 heads: 404 us in one CTA
-// a head, 257 in four).
+// finer split repeats the preparation, but its step is shorter: a step of the precise forward
+// takes 4.7, 3.3 and 2.7 thousand cycles in one, two and four CTAs a head (prefill of T=2048: 298
+// us for 128 heads, 204 for 64, 169 for 32).  Of sequences of unknown lengths the longest is
+// taken to be four times the average, and the others to fill in behind it (ten prompts of 1 to
+// 2609 tokens, 16 heads: 404 us in one CTA a head, 259 in two, 257 in four).
 inline int best_split(int num_seqs, int HV, const int *cu) {
-    constexpr int kSplit[3] = {1, 2, 4}, kStep[3] = {50, 37, 27};
+    constexpr int kSplit[3] = {1, 2, 4}, kStep[3] = {47, 33, 27};
     const long long heads = (long long)num_seqs * HV;
     int best = 4;
     double least = 1e300;
