@@ -1,5 +1,8 @@
-// Shared parts of the layer-norm kernels: a row is held in registers, eight elements a
-// thread, by a group of TPR threads (16 to 1024, the smallest power of two that holds it).
+// Shared parts of the layer-norm kernels: a row is held in registers by a group of TPR threads
+// (the smallest power of two that holds it).  A thread has 32 bytes of it: with 16, BF16 rows are
+// bound by instructions, most of them in the sums over lanes (32768 x 2048: forward 54.5 us with
+// 76% of the issue slots taken).  Rows on no 16-byte boundary take eight elements a thread, which
+// need more registers each.
 #pragma once
 
 #include "kda_common.cuh"
@@ -8,8 +11,10 @@
 namespace kda {
 namespace norm {
 
-constexpr int E = 8;                 // elements of a row held by one thread
-constexpr int kMaxWidth = 1024 * E;  // widest row that one CTA holds in registers
+constexpr int kMaxWidth = 8192;  // widest row that one CTA holds in registers
+template <typename T, bool WIDE> constexpr int elements() {  // of a thread
+    return WIDE ? 32 / (int)sizeof(T) : 8;
+}
 
 __device__ __forceinline__ float as_f32(float x) { return x; }
 __device__ __forceinline__ float as_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -23,13 +28,15 @@ template <> __device__ __forceinline__ __half from_f32<__half>(float x) {
     return __float2half_rn(x);
 }
 
-// Eight elements of a row.  WIDE: 16-byte accesses to consecutive columns; otherwise single
-// elements TPR columns apart (rows that start at no 16-byte boundary).
+// A thread's elements of a row.  WIDE: 16-byte accesses, a group's next to each other; otherwise
+// single elements TPR columns apart (rows that start at no 16-byte boundary).
 template <typename T, bool WIDE, int TPR> struct Part {
+    static constexpr int E = elements<T, WIDE>(), kVec = 16 / (int)sizeof(T);
     T v[E];
-    static constexpr int kVec = 16 / (int)sizeof(T);
 
-    static __device__ __forceinline__ int col(int t, int i) { return WIDE ? t * E + i : t + i * TPR; }
+    static __device__ __forceinline__ int col(int t, int i) {
+        return WIDE ? (i / kVec * TPR + t) * kVec + i % kVec : t + i * TPR;
+    }
 
     __device__ __forceinline__ void load(const T *row, int t, int width, bool ok) {
         if (WIDE) {
@@ -61,13 +68,12 @@ template <typename T, bool WIDE, int TPR> struct Part {
     }
 };
 
-// Rows on their way to a thread: the 16-byte parts of its eight elements of the next DEPTH - 1
-// rows, copied asynchronously into slots of its own in shared memory, so that as many bytes
+// Rows on their way to a thread: its two 16-byte parts of each of the next DEPTH - 1 rows, copied asynchronously into slots of its own in shared memory, so that as many bytes
 // are in flight as the memory's latency asks for without a register or a barrier.  Rows on no
 // 16-byte boundary (WIDE false) come through registers, one row ahead.
 template <typename T, bool WIDE, int TPR, int THREADS, int DEPTH> struct Stream {
     using P = Part<T, WIDE, TPR>;
-    static constexpr int kParts = E * (int)sizeof(T) / 16;
+    static constexpr int kParts = 2;
     static constexpr int kBytes = WIDE ? DEPTH * kParts * THREADS * 16 : 0;
     uint4 *slots;  // [DEPTH][kParts][THREADS], this thread's column
     P next;
@@ -133,14 +139,15 @@ template <int N> __device__ __forceinline__ float lanes_sum(float x) {
 }
 
 // Threads of a row for a width, 0 when one CTA's registers do not hold it.
-inline int group_of(int width) {
+inline int esize(int dtype) { return dtype == NORM_FP32 ? 4 : 2; }
+
+// Threads of a row, e elements each; 0 when one CTA's registers do not hold it.
+inline int group_of(int width, int e) {
     if (width > kMaxWidth) return 0;
-    int t = 16;
-    while (t * E < width) t *= 2;
+    int t = 128 / e;
+    while (t * e < width) t *= 2;
     return t;
 }
-
-inline int esize(int dtype) { return dtype == NORM_FP32 ? 4 : 2; }
 
 inline bool wide_ok(int dtype, int width, const void *p, long long stride, bool with = true) {
     const int vec = 16 / esize(dtype);

@@ -14,17 +14,18 @@ namespace {
 
 // CTAs a multiprocessor, and rows on their way to a thread (the widest FP32 rows: 192 KB of
 // slots).  One row at a time: two at once, as in the forward, spill.
-template <bool WIDE, int TPR> constexpr int per_sm() { return TPR > 256 ? 1 : WIDE ? 3 : 2; }
-template <typename T, bool WIDE, int TPR> constexpr int depth() {
-    return !WIDE ? 2 : sizeof(T) == 4 && TPR == 1024 ? 3 : 4;
+template <int E, bool WIDE, int TPR> constexpr int per_sm() {
+    return TPR > 256 ? 1 : WIDE && E == 8 ? 3 : 2;
 }
+template <bool WIDE, int TPR> constexpr int depth() { return !WIDE ? 2 : TPR == 1024 ? 3 : 4; }
 
 template <typename T, bool WIDE, int TPR>
-__global__ void __launch_bounds__(threads<TPR>(), per_sm<WIDE, TPR>()) kda_layer_norm_bwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(threads<TPR>(), per_sm<elements<T, WIDE>(), WIDE, TPR>())
+    kda_layer_norm_bwd_kernel(const NormArgs a) {
     constexpr int kThreads = threads<TPR>(), kGroups = kThreads / TPR;
     constexpr int kWarps = TPR > 32 ? TPR / 32 : 1;
     using P = Part<T, WIDE, TPR>;
-    constexpr int kDepth = depth<T, WIDE, TPR>();
+    constexpr int E = P::E, kDepth = depth<WIDE, TPR>();
     using Rows = Stream<T, WIDE, TPR, kThreads, kDepth>;
     __shared__ float2 red[2][kGroups][kWarps];
     extern __shared__ __align__(16) char slots[];
@@ -189,11 +190,13 @@ template <typename T> __global__ void __launch_bounds__(256) kda_layer_norm_bwd_
     to[a.width + c] = db;
 }
 
-int ctas(long long rows, int width) {
-    const int tpr = group_of(width);
+// CTAs, each with a row of `partial`.
+int ctas(long long rows, int width, int e, bool wide) {
+    const int tpr = group_of(width, e);
     if (!tpr) return (int)(rows < 64 ? rows : 64);  // slices of the column pass
-    const int threads = tpr < 256 ? 256 : tpr, groups = threads / tpr;
-    const long long want = (rows + groups - 1) / groups, most = (long long)kSMs * (tpr <= 256 ? 3 : 1024 / threads);
+    const int groups = tpr < 256 ? 256 / tpr : 1;
+    const int a_sm = tpr > 256 ? 1024 / tpr : wide && e == 8 ? 3 : 2;
+    const long long want = (rows + groups - 1) / groups, most = (long long)kSMs * a_sm;
     return (int)(want < most ? want : most);
 }
 
@@ -206,35 +209,36 @@ cudaError_t sum_partials(const NormArgs &a, int n, cudaStream_t stream) {
 
 template <typename T, bool WIDE, int TPR>
 cudaError_t launch(const NormArgs &a, cudaStream_t stream) {
-    constexpr int kBytes = 2 * Stream<T, WIDE, TPR, threads<TPR>(), depth<T, WIDE, TPR>()>::kBytes;
+    constexpr int kBytes = 2 * Stream<T, WIDE, TPR, threads<TPR>(), depth<WIDE, TPR>()>::kBytes;
     static volatile int done[kMaxDev];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && kBytes > 40 * 1024)  // with the static part, over the default 48 KB
         e = smem_limit_once(kda_layer_norm_bwd_kernel<T, WIDE, TPR>, kBytes, dev, done);
     if (e != cudaSuccess) return e;
-    const int n = ctas(a.rows, a.width);
+    const int n = ctas(a.rows, a.width, elements<T, WIDE>(), WIDE);
     kda_layer_norm_bwd_kernel<T, WIDE, TPR><<<n, threads<TPR>(), kBytes, stream>>>(a);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : sum_partials(a, n, stream);
 }
 
 template <typename T, bool WIDE> cudaError_t pick(const NormArgs &a, cudaStream_t stream) {
-    switch (group_of(a.width)) {
-        case 16: return launch<T, WIDE, 16>(a, stream);
-        case 32: return launch<T, WIDE, 32>(a, stream);
-        case 64: return launch<T, WIDE, 64>(a, stream);
-        case 128: return launch<T, WIDE, 128>(a, stream);
-        case 256: return launch<T, WIDE, 256>(a, stream);
-        case 512: return launch<T, WIDE, 512>(a, stream);
-        case 1024: return launch<T, WIDE, 1024>(a, stream);
+    constexpr int E = elements<T, WIDE>();
+    switch (group_of(a.width, E)) {
+        case 128 / E: return launch<T, WIDE, 128 / E>(a, stream);
+        case 256 / E: return launch<T, WIDE, 256 / E>(a, stream);
+        case 512 / E: return launch<T, WIDE, 512 / E>(a, stream);
+        case 1024 / E: return launch<T, WIDE, 1024 / E>(a, stream);
+        case 2048 / E: return launch<T, WIDE, 2048 / E>(a, stream);
+        case 4096 / E: return launch<T, WIDE, 4096 / E>(a, stream);
+        case 8192 / E: return launch<T, WIDE, 8192 / E>(a, stream);
     }
     const long long most = 2 * kSMs;
     kda_layer_norm_bwd_long_kernel<T>
         <<<(unsigned)(a.rows < most ? a.rows : most), 1024, 0, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.dweight) return e;
-    const int n = ctas(a.rows, a.width);
+    const int n = ctas(a.rows, a.width, elements<T, WIDE>(), WIDE);
     kda_layer_norm_bwd_cols_kernel<T>
         <<<dim3((unsigned)((a.width + 255) / 256), (unsigned)n), 256, 0, stream>>>(a);
     e = cudaGetLastError();
@@ -251,7 +255,16 @@ template <typename T> cudaError_t pick_wide(const NormArgs &a, cudaStream_t stre
 }  // namespace
 }  // namespace norm
 
-int norm_bwd_ctas(long long rows, int width) { return norm::ctas(rows, width); }
+// Enough for rows of any type and alignment.
+int norm_bwd_ctas(long long rows, int width) {
+    int most = 0;
+    for (int e = 8; e <= 16; e *= 2)
+        for (int wide = 0; wide < 2; ++wide) {
+            const int n = norm::ctas(rows, width, e, wide);
+            most = n > most ? n : most;
+        }
+    return most;
+}
 
 cudaError_t launch_norm_bwd(const NormArgs &a, cudaStream_t stream) {
     if (a.rows == 0) return norm::sum_partials(a, 0, stream);  // sums of nothing: zeros

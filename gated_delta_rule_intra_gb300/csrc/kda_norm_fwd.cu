@@ -18,6 +18,7 @@ __global__ void __launch_bounds__(threads<TPR>()) kda_layer_norm_fwd_kernel(cons
     constexpr int kThreads = threads<TPR>(), kGroups = kThreads / TPR;
     constexpr int kWarps = TPR > 32 ? TPR / 32 : 1;
     using P = Part<T, WIDE, TPR>;
+    constexpr int E = P::E;
     constexpr int R = at_once<WIDE, TPR>(), kDepth = WIDE ? 4 / R + 1 : 2;
     using Rows = Stream<T, WIDE, TPR, kThreads, kDepth * R>;
     __shared__ float2 red[2][kGroups][R][kWarps];
@@ -33,10 +34,11 @@ __global__ void __launch_bounds__(threads<TPR>()) kda_layer_norm_fwd_kernel(cons
     }
     // elements of the row that warp j of the group holds
     auto held = [&](int j) {
-        if (WIDE) return min(max(a.width - j * 32 * E, 0), 32 * E);
+        constexpr int kRun = WIDE ? P::kVec : 1;  // neighbouring columns of a thread
         int n = 0;
 #pragma unroll
-        for (int i = 0; i < E; ++i) n += min(max(a.width - i * TPR - j * 32, 0), 32);
+        for (int i = 0; i < E / kRun; ++i)
+            n += min(max(a.width - (i * TPR + j * 32) * kRun, 0), 32 * kRun);
         return n;
     };
     const float inv_n = 1.f / (float)a.width;
@@ -166,14 +168,15 @@ cudaError_t launch(const NormArgs &a, cudaStream_t stream) {
 }
 
 template <typename T, bool WIDE> cudaError_t pick(const NormArgs &a, cudaStream_t stream) {
-    switch (group_of(a.width)) {
-        case 16: return launch<T, WIDE, 16>(a, stream);
-        case 32: return launch<T, WIDE, 32>(a, stream);
-        case 64: return launch<T, WIDE, 64>(a, stream);
-        case 128: return launch<T, WIDE, 128>(a, stream);
-        case 256: return launch<T, WIDE, 256>(a, stream);
-        case 512: return launch<T, WIDE, 512>(a, stream);
-        case 1024: return launch<T, WIDE, 1024>(a, stream);
+    constexpr int E = elements<T, WIDE>();
+    switch (group_of(a.width, E)) {
+        case 128 / E: return launch<T, WIDE, 128 / E>(a, stream);
+        case 256 / E: return launch<T, WIDE, 256 / E>(a, stream);
+        case 512 / E: return launch<T, WIDE, 512 / E>(a, stream);
+        case 1024 / E: return launch<T, WIDE, 1024 / E>(a, stream);
+        case 2048 / E: return launch<T, WIDE, 2048 / E>(a, stream);
+        case 4096 / E: return launch<T, WIDE, 4096 / E>(a, stream);
+        case 8192 / E: return launch<T, WIDE, 8192 / E>(a, stream);
     }
     const long long most = 2 * kSMs;
     kda_layer_norm_fwd_long_kernel<T>
