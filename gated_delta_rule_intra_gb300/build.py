@@ -70,7 +70,7 @@ def build_native() -> str:
            "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", os.path.join(ROOT, "include"), *[x for h in headers for x in ("-isystem", h)],
            os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", os.path.join(home, "lib"),
-           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
            "-Wl,-rpath," + os.path.join(home, "lib")]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:

@@ -10,8 +10,7 @@
 // be sent through another build of it.
 #include <Python.h>
 
-#include <ATen/core/LegacyTypeDispatch.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -56,7 +55,7 @@ int type_of(ScalarType t) {
 }
 
 Tensor empty(at::IntArrayRef shape, ScalarType type, const Tensor &like) {
-    return at::empty(shape, like.options().dtype(type));
+    return Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 Tensor bytes(size_t n, const Tensor &like) { return empty({(int64_t)n}, at::kByte, like); }
 
@@ -298,7 +297,6 @@ PyObject *method(PyObject *, PyObject *const *args, Py_ssize_t n) {
         return nullptr;
     }
     try {
-        const at::AutoDispatchBelowADInplaceOrView guard;
         return F(args);
     } catch (const std::exception &) {
         PyErr_Clear();
