@@ -188,6 +188,54 @@ __device__ __forceinline__ Seq seq_of(int n, int T, const int *cu) {
     return s;
 }
 
+__device__ __forceinline__ void prefetch_line(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
+// The tokens of unit u (a slot of a value head); rows <= 0 where there are none.
+struct Where {
+    long long row0;
+    int rows, h, hv;
+};
+__device__ __forceinline__ Where locate(const ChunkBwdArgs &a, unsigned u) {
+    Where w;
+    const int slot = (int)(u / (unsigned)a.HV);
+    w.hv = (int)u - slot * a.HV;
+    w.h = w.hv / (a.HV / a.H);
+    int n;  // the slot's sequence
+    if (a.cu_seqlens) {
+        int lo = 0, hi = a.num_seqs - 1;
+        while (lo < hi) {  // the last sequence whose slots begin at or before this one
+            const int mid = (lo + hi + 1) / 2;
+            if (seq_of(mid, a.T, a.cu_seqlens).slot0 <= slot) lo = mid; else hi = mid - 1;
+        }
+        n = lo;
+    } else {
+        n = slot / ((a.T + BT - 1) / BT);
+    }
+    const Seq sq = seq_of(n, a.T, a.cu_seqlens);
+    const int t0 = (slot - sq.slot0) * BT;
+    w.row0 = sq.row0 + t0;
+    w.rows = t0 < 0 ? 0 : min(BT, sq.len - t0);
+    return w;
+}
+
+// Asks a unit's rows of q, k and do (two lines each) and of the gate (four) into L2.
+__device__ __forceinline__ void prefetch_rows(const ChunkBwdArgs &a, const Where &w, int tid,
+                                              int threads) {
+    for (int x = tid; x < 10 * BT; x += threads) {
+        const int r = x / 10, l = x - 10 * r;
+        if (r >= w.rows) break;
+        const size_t tok = (size_t)(w.row0 + r);
+        const size_t iq = (tok * a.H + w.h) * D, iv = (tok * a.HV + w.hv) * D;
+        const char *p = l < 2   ? (const char *)((const uint16_t *)a.q + iq)
+                        : l < 4 ? (const char *)((const uint16_t *)a.k + iq)
+                        : l < 6 ? (const char *)((const uint16_t *)a.dout + iv)
+                                : (const char *)(a.gate + iv);
+        prefetch_line(p + (l < 6 ? l & 1 : l - 6) * 128);
+    }
+}
+
 // The sequence that is `rank`-th in length, the longest first: a batch of ragged sequences has
 // its longest walks begun at once and the short ones fill in behind them.  Sequences of one
 // length, and batches too large to be worth ranking, keep their order.  All threads call it.

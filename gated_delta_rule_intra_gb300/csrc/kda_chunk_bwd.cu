@@ -47,6 +47,7 @@ struct __align__(128) Smem {
     float beta[BT], diag[BT];           // diag: do_t.e_t
     char g1[4][2 * kTile], g2[4][2 * kTile];  // hi, lo of each step, zero from the diagonal on
     float col[4][8][kThreads];          // dk_col from R to F, each thread's own
+    char out[3][kThreads / 32][512];    // a warp's dq, dk, dgate of a step on their way out
 };
 
 __device__ __forceinline__ uint32_t block_addr(uint32_t base, int rb, int cb, int lane) {
@@ -174,30 +175,20 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
     // lanes' offsets of a [16][16] tile as right operand: rows as columns, or rows summed over
     const uint32_t tn = tile_lane(lane);
     const uint32_t tt = (uint32_t)(((lane & 7) + ((lane >> 3) & 1) * 8) * 32 + (lane >> 4) * 16);
-    const long long units = (long long)a.slots * a.HV;
+    // a unit's saved blocks take 104 KB, so that their number is far below 2^31
+    const unsigned units = (unsigned)a.slots * a.HV;
+    const size_t orow = (size_t)a.HV * D;
 
-    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-        const int slot = (int)(u / a.HV), hv = (int)(u - (long long)slot * a.HV);
-        const int h = hv / (a.HV / a.H);
-        int n;  // the slot's sequence
-        if (a.cu_seqlens) {
-            int lo = 0, hi = a.num_seqs - 1;
-            while (lo < hi) {  // the last sequence whose slots begin at or before this one
-                const int mid = (lo + hi + 1) / 2;
-                if (seq_of(mid, a.T, a.cu_seqlens).slot0 <= slot) lo = mid; else hi = mid - 1;
-            }
-            n = lo;
-        } else {
-            n = slot / ((a.T + BT - 1) / BT);
-        }
-        const Seq sq = seq_of(n, a.T, a.cu_seqlens);
-        const int t0 = (slot - sq.slot0) * BT;
-        const long long row0 = sq.row0 + t0;
-        if (t0 < 0 || t0 >= sq.len) continue;  // no tokens here (the same for every thread)
-        const int rows = min(BT, sq.len - t0);
+    Where next = locate(a, blockIdx.x);
+    for (unsigned u = blockIdx.x; u < units; u += gridDim.x) {
+        const long long row0 = next.row0;
+        const unsigned after = u + gridDim.x;
+        const int rows = next.rows, h = next.h, hv = next.hv;
+        if (after < units) next = locate(a, after);
+        if (rows <= 0) continue;  // no tokens here (the same for every thread)
         const size_t su = (size_t)u;
 
-        // ---- loads; the next unit's large blocks are asked into L2 meanwhile
+        // ---- loads
         for (int i = tid; i < (int)kRowsBytes / 16; i += kThreads) {
             cp16z(se + i * 16, a.e + su * kRowsBytes + i * 16, true);
             cp16z(sy + i * 16, a.y + su * kRowsBytes + i * 16, true);
@@ -213,31 +204,30 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
             const size_t iv = (tok * a.HV + hv) * D;
             cp16z(tc::smem_u32(&sm.g[r][c * 4]), a.gate + iv + c * 4, ok);
             cp16z(tc::smem_u32(&sm.g[r][64 + c * 4]), a.gate + iv + 64 + c * 4, ok);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {  // do: eight rows at a time, whose pieces share no banks
+            const int r = 16 * x + (warp >> 2) * 8 + (lane & 7), c = (warp & 3) * 4 + (lane >> 3);
+            const bool ok = r < rows;
             char *to = sm.dout + ((r >> 3) * 16 + c) * 128 + (r & 7) * 16;
-            const uint16_t *from = (const uint16_t *)a.dout + iv + c * 8;
+            const uint16_t *from = (const uint16_t *)a.dout +
+                                   ((size_t)(row0 + (ok ? r : 0)) * a.HV + hv) * D + c * 8;
             if (!kLo) {
                 cp16z(tc::smem_u32(to), from, ok);
             } else {
-                uint4 x = make_uint4(0u, 0u, 0u, 0u), hi, lo;
-                if (ok) x = *reinterpret_cast<const uint4 *>(from);
+                uint4 v = make_uint4(0u, 0u, 0u, 0u), hi, lo;
+                if (ok) v = *reinterpret_cast<const uint4 *>(from);
                 float2 f;
-                f = unpack2<T16>(x.x); split2(f.x, f.y, hi.x, lo.x);
-                f = unpack2<T16>(x.y); split2(f.x, f.y, hi.y, lo.y);
-                f = unpack2<T16>(x.z); split2(f.x, f.y, hi.z, lo.z);
-                f = unpack2<T16>(x.w); split2(f.x, f.y, hi.w, lo.w);
+                f = unpack2<T16>(v.x); split2(f.x, f.y, hi.x, lo.x);
+                f = unpack2<T16>(v.y); split2(f.x, f.y, hi.y, lo.y);
+                f = unpack2<T16>(v.z); split2(f.x, f.y, hi.z, lo.z);
+                f = unpack2<T16>(v.w); split2(f.x, f.y, hi.w, lo.w);
                 *reinterpret_cast<uint4 *>(to) = hi;
                 *reinterpret_cast<uint4 *>(to + kRowPlane) = lo;
             }
         }
         if (tid < BT) sm.beta[tid] = tid < rows ? a.beta[(size_t)(row0 + tid) * a.HV + hv] : 0.f;
         cp_async_commit();
-        if (tid == 0 && u + gridDim.x < units) {
-            const size_t nu = su + gridDim.x;
-            tc::prefetch_l2(a.dckpt + nu * kCkptBytes, (uint32_t)kCkptBytes);
-            tc::prefetch_l2(a.e + nu * kRowsBytes, (uint32_t)kRowsBytes);
-            tc::prefetch_l2(a.y + nu * kRowsBytes, (uint32_t)kRowsBytes);
-            tc::prefetch_l2(a.ckpt + nu * kCkptBytes, (uint32_t)kCkptBytes);
-        }
         float S[16][4];  // rows dk c0 + gr, + 8; columns dv 8j + tc2, + 1
         // 16 dv columns of a checkpoint (see store_checkpoint()): tiles 2x and 2x + 1 of S
         auto load_state = [&](const char *base, int x, float (&l)[4], float (&r)[4]) {
@@ -305,6 +295,17 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
         }
         __syncthreads();
 
+        // the next unit's inputs are asked into L2 while the loads' queue is empty
+        if (after < units) {
+            const size_t nu = (size_t)after;
+            if (tid == 0) {
+                tc::prefetch_l2(a.dckpt + nu * kCkptBytes, (uint32_t)kCkptBytes);
+                tc::prefetch_l2(a.e + nu * kRowsBytes, (uint32_t)kRowsBytes);
+                tc::prefetch_l2(a.y + nu * kRowsBytes, (uint32_t)kRowsBytes);
+                tc::prefetch_l2(a.ckpt + nu * kCkptBytes, (uint32_t)kCkptBytes);
+            }
+            prefetch_rows(a, next, tid, kThreads);
+        }
         // ---- R
 #pragma unroll 1
         for (int j = 3; j >= 0; --j) {
@@ -420,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
             carry[i] += __shfl_xor_sync(0xffffffffu, carry[i], 2);
         }
         // ---- F, and the outputs
+        const size_t out_at = (size_t)row0 * orow + (size_t)hv * D + c0;
 #pragma unroll 1
         for (int j = 0; j < 4; ++j) {
             float cq[2][4] = {}, cy[2][4] = {};
@@ -519,39 +521,32 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
                     dk.v[i][p] += sm.col[j][4 * i + p][tid] + d * q.v[i][p];
                 }
             }
+            auto put = [&](void *out, int which, const Elems &x) {
+                uint32_t w[4];
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+                for (int y = 0; y < 4; ++y)
+                    w[y] = pack2<T16>(x.v[y & 1][y & 2], x.v[y & 1][(y & 2) + 1]);
+                store_out(sm.out[which][warp], w,
+                          (char *)((uint16_t *)out + out_at + (size_t)j * C * orow), orow * 2,
+                          rows - j * C, (char *)out, a.rows_o * D * 2, a.dbg, lane);
+            };
+            put(a.dgate, 0, dg);
+            if (!a.dq_hv) {
+                put(a.dq, 1, dq);
+                put(a.dk, 2, dk);
+            } else {  // summed over the head's value heads afterwards, in FP32
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t wg = movm_t(pack2<T16>(dg.v[i][2 * half], dg.v[i][2 * half + 1]));
-                    uint32_t wq = 0, wk = 0;
-                    if (!a.dq_hv) {
-                        wq = movm_t(pack2<T16>(dq.v[i][2 * half], dq.v[i][2 * half + 1]));
-                        wk = movm_t(pack2<T16>(dk.v[i][2 * half], dk.v[i][2 * half + 1]));
-                    }
-                    const int t = j * C + 8 * half + gr;
-                    const size_t iv =
-                        ((size_t)(row0 + t) * a.HV + hv) * D + c0 + 8 * i + tc2;
-                    if (t < rows && dbg_ok(a.dbg, iv + 1, a.rows_o * D, DBG_STORE)) {
-                        *reinterpret_cast<uint32_t *>((uint16_t *)a.dgate + iv) = wg;
-                        if (!a.dq_hv) {
-                            *reinterpret_cast<uint32_t *>((uint16_t *)a.dq + iv) = wq;
-                            *reinterpret_cast<uint32_t *>((uint16_t *)a.dk + iv) = wk;
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const int t = j * C + token_of(p, tc2);
+                        const size_t at = out_at + (size_t)t * orow + 8 * i + gr;
+                        if (t < rows && dbg_ok(a.dbg, at, a.rows_o * D, DBG_STORE)) {
+                            a.dq_hv[at] = dq.v[i][p];
+                            a.dk_hv[at] = dk.v[i][p];
                         }
                     }
-                    if (a.dq_hv) {  // summed over the head's value heads afterwards, in FP32
-#pragma unroll
-                        for (int p = 2 * half; p < 2 * half + 2; ++p) {
-                            const int tp = j * C + token_of(p, tc2);
-                            const size_t ip =
-                                ((size_t)(row0 + tp) * a.HV + hv) * D + c0 + 8 * i + gr;
-                            if (tp < rows && dbg_ok(a.dbg, ip, a.rows_o * D, DBG_STORE)) {
-                                a.dq_hv[ip] = dq.v[i][p];
-                                a.dk_hv[ip] = dk.v[i][p];
-                            }
-                        }
-                    }
-                }
+            }
         }
         __syncthreads();
     }

@@ -131,38 +131,6 @@ __device__ __noinline__ void pairs_strong(Smem &sm, int j, int c0, int lane, flo
     }
 }
 
-__device__ __forceinline__ void prefetch_line(const void *p) {
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
-
-// The tokens of unit u (a slot of a value head); rows <= 0 where there are none.
-struct Where {
-    long long row0;
-    int rows, h, hv;
-};
-__device__ __forceinline__ Where locate(const ChunkBwdArgs &a, unsigned u) {
-    Where w;
-    const int slot = (int)(u / (unsigned)a.HV);
-    w.hv = (int)u - slot * a.HV;
-    w.h = w.hv / (a.HV / a.H);
-    int n;  // the slot's sequence
-    if (a.cu_seqlens) {
-        int lo = 0, hi = a.num_seqs - 1;
-        while (lo < hi) {  // the last sequence whose slots begin at or before this one
-            const int mid = (lo + hi + 1) / 2;
-            if (chunk::seq_of(mid, a.T, a.cu_seqlens).slot0 <= slot) lo = mid; else hi = mid - 1;
-        }
-        n = lo;
-    } else {
-        n = slot / ((a.T + BT - 1) / BT);
-    }
-    const Seq sq = chunk::seq_of(n, a.T, a.cu_seqlens);
-    const int t0 = (slot - sq.slot0) * BT;
-    w.row0 = sq.row0 + t0;
-    w.rows = t0 < 0 ? 0 : min(BT, sq.len - t0);
-    return w;
-}
-
 __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBwdArgs a) {
     extern __shared__ __align__(128) char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
@@ -184,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
         cp_async_commit();
     };
 
-    Where next = locate(a, blockIdx.x);
+    chunk::Where next = chunk::locate(a, blockIdx.x);
     fetch_state(a.dckpt, blockIdx.x);
     for (unsigned u = blockIdx.x; u < units; u += gridDim.x) {
         const long long row0 = next.row0;
@@ -193,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
         if (rows <= 0) {  // no tokens here (the same for every thread)
             cp_async_wait_all();
             if (after < units) {
-                next = locate(a, after);
+                next = chunk::locate(a, after);
                 fetch_state(a.dckpt, after);
             }
             continue;
@@ -401,25 +369,14 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
 
         // the next unit's inputs are asked into L2 while the loads' queue is empty
         if (after < units) {
-            next = locate(a, after);
+            next = chunk::locate(a, after);
             const size_t nu = (size_t)after;
             if (tid == 0) {
                 tc::prefetch_l2(a.e + nu * kRowsBytes, (uint32_t)kRowsBytes);
                 tc::prefetch_l2(a.y + nu * kRowsBytes, (uint32_t)kRowsBytes);
                 tc::prefetch_l2(a.ckpt + nu * kCkptBytes, (uint32_t)kCkptBytes);
             }
-            // rows of q, k and do: two lines each, of the gate four
-            for (int x = tid; x < 10 * BT; x += kThreads) {
-                const int r = x / 10, l = x - 10 * r;
-                if (r >= next.rows) break;
-                const size_t tok = (size_t)(next.row0 + r);
-                const size_t iq = (tok * a.H + next.h) * D, iv = (tok * a.HV + next.hv) * D;
-                const char *p = l < 2   ? (const char *)((const uint16_t *)a.q + iq)
-                                : l < 4 ? (const char *)((const uint16_t *)a.k + iq)
-                                : l < 6 ? (const char *)((const uint16_t *)a.dout + iv)
-                                        : (const char *)(a.gate + iv);
-                prefetch_line(p + (l < 6 ? l & 1 : l - 6) * 128);
-            }
+            chunk::prefetch_rows(a, next, tid, kThreads);
         }
         // ---- R
 #pragma unroll 1
