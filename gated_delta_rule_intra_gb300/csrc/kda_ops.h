@@ -49,6 +49,16 @@ struct ChunkBwdArgs {
 
 cudaError_t launch_chunk_bwd(const ChunkBwdArgs &a, cudaStream_t stream);
 
+// Outputs [T, row bytes] of a packed call, whose tokens in no sequence get zeros.
+struct ZeroArgs {
+    void *out[5];
+    size_t row[5];
+    int count, T, num_seqs;
+    const int *cu_seqlens;
+};
+
+cudaError_t launch_zero_rest(const ZeroArgs &a, cudaStream_t stream);
+
 struct StepArgs {
     const void *q, *k, *v;  // 16-bit, [N, H, 128] and [N, HV, 128]
     const float *gate, *beta;

@@ -116,6 +116,11 @@ kda_status_t kda_chunk_fwd(const void *q, const void *k, const void *v, const fl
     if ((st = kda::require_device()) != KDA_OK) return st;
     (void)cudaGetLastError();
     if (T == 0 && !op.final_state) return KDA_OK;
+    if (varlen && op.zero_rest) {
+        const kda::ZeroArgs z = {{o}, {(size_t)HV * KDA_K * 2}, 1, T, seqs, op.cu_seqlens};
+        const cudaError_t e = kda::launch_zero_rest(z, (cudaStream_t)stream);
+        if (e != cudaSuccess) return finish(e);
+    }
     kda::ChunkFwdArgs a = {};
     a.q = q; a.k = k; a.v = v; a.gate = gate; a.beta = beta; a.o = o;
     a.initial_state = op.initial_state;
@@ -196,6 +201,14 @@ kda_status_t kda_chunk_bwd(const void *q, const void *k, const float *gate, cons
     if ((st = kda::require_device()) != KDA_OK) return st;
     (void)cudaGetLastError();
     if (T == 0 && !op.d_initial_state) return KDA_OK;
+    if (varlen && op.zero_rest) {
+        const size_t head = KDA_K * 2;
+        const kda::ZeroArgs z = {{dq, dk, dv, dgate, dbeta},
+                                 {H * head, H * head, HV * head, HV * head, (size_t)HV * 2},
+                                 5, T, seqs, op.cu_seqlens};
+        const cudaError_t e = kda::launch_zero_rest(z, (cudaStream_t)stream);
+        if (e != cudaSuccess) return finish(e);
+    }
     kda::ChunkBwdArgs a = {};
     a.q = q; a.k = k; a.dout = dout; a.gate = gate; a.beta = beta;
     a.dq = dq; a.dk = dk; a.dv = dv; a.dgate = dgate; a.dbeta = dbeta;

@@ -22,7 +22,8 @@ class ChunkFwdOpts(ctypes.Structure):
     _fields_ = [("HV", ctypes.c_int), ("scale", ctypes.c_float),
                 ("initial_state", ctypes.c_void_p), ("final_state", ctypes.c_void_p),
                 ("saved", ctypes.c_void_p), ("saved_bytes", ctypes.c_size_t),
-                ("cu_seqlens", ctypes.c_void_p), ("num_seqs", ctypes.c_int)]
+                ("cu_seqlens", ctypes.c_void_p), ("num_seqs", ctypes.c_int),
+                ("zero_rest", ctypes.c_int)]
 
 
 class ChunkBwdOpts(ctypes.Structure):
@@ -30,8 +31,9 @@ class ChunkBwdOpts(ctypes.Structure):
     _fields_ = [("HV", ctypes.c_int), ("scale", ctypes.c_float),
                 ("d_final_state", ctypes.c_void_p), ("d_initial_state", ctypes.c_void_p),
                 ("cu_seqlens", ctypes.c_void_p), ("num_seqs", ctypes.c_int),
-                ("saved", ctypes.c_void_p), ("saved_bytes", ctypes.c_size_t),
-                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+                ("zero_rest", ctypes.c_int), ("saved", ctypes.c_void_p),
+                ("saved_bytes", ctypes.c_size_t), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
 
 
 class StepOpts(ctypes.Structure):
@@ -116,11 +118,12 @@ def _chunk_fwd(q, k, v, gate, beta, scale, initial_state, output_final_state, sa
     H, HV, dev = _inputs("kda_chunk_fwd", q, k, v, gate, beta, 2)
     B, T = q.shape[:2]
     N = _seqs(cu_seqlens, B, dev)
+    op = ChunkFwdOpts(HV=HV, scale=_scale(scale))
     if o is None:
-        o = torch.zeros_like(v) if N else torch.empty_like(v)
+        o = torch.empty_like(v)
+        op.zero_rest = 1
     else:
         check("o", o, v.shape, v.dtype, dev)
-    op = ChunkFwdOpts(HV=HV, scale=_scale(scale))
     if N:
         op.num_seqs, op.cu_seqlens = N, cu_seqlens.data_ptr()
     if initial_state is not None:
@@ -176,7 +179,8 @@ def _chunk_bwd(q, k, v, gate, beta, do, saved, scale, d_final_state, output_d_in
                            lib.kda_chunk_saved_bytes(B, T, HV, N, DTYPES16[dt], 1)):
         raise ValueError(f"saved has {saved_bytes} bytes: not from a forward of these inputs")
     check("saved", saved, (saved_bytes,), torch.uint8, dev)
-    new = torch.zeros_like if N else torch.empty_like
+    zero_rest = all(t is None for t in given)
+    new = torch.zeros_like if N and not zero_rest else torch.empty_like
     out = []
     for name, t, like in zip(("dq", "dk", "dv", "dgate", "dbeta"), given, (q, k, v, v, beta)):
         if t is None:
@@ -184,7 +188,8 @@ def _chunk_bwd(q, k, v, gate, beta, do, saved, scale, d_final_state, output_d_in
         else:
             check(name, t, like.shape, dt, dev)
         out.append(t)
-    op = ChunkBwdOpts(HV=HV, scale=_scale(scale), saved=saved.data_ptr(), saved_bytes=saved_bytes)
+    op = ChunkBwdOpts(HV=HV, scale=_scale(scale), saved=saved.data_ptr(), saved_bytes=saved_bytes,
+                      zero_rest=zero_rest)
     if N:
         op.num_seqs, op.cu_seqlens = N, cu_seqlens.data_ptr()
     if d_final_state is not None:

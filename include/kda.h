@@ -364,7 +364,8 @@ kda_status_t kda_intra_fwd_ex(const void *q, const void *k, const float *g,
  *   cu_seqlens     variable-length sequences packed along T (B == 1): device int32
  *   num_seqs       [num_seqs + 1], sequence n is tokens [cu_seqlens[n], cu_seqlens[n+1]).
  *                  Values are read on the device only and clamped to [0, T]; tokens in no
- *                  sequence are left untouched.
+ *                  sequence are left untouched, or with
+ *   zero_rest      get zeros.
  */
 typedef struct {
     int HV;
@@ -375,6 +376,7 @@ typedef struct {
     size_t saved_bytes;
     const int *cu_seqlens;
     int num_seqs;
+    int zero_rest;
 } kda_chunk_fwd_opts_t;
 
 /* Bytes of `saved` (num_seqs: 0 for fixed-length calls; with_state: whether the call has an
@@ -390,7 +392,7 @@ kda_status_t kda_chunk_fwd(const void *q, const void *k, const void *v, const fl
  * Gradients of kda_chunk_fwd from dout [B, T, HV, 128] (dtype) and what it saved: dq, dk
  * [B, T, H, 128] (summed over the value heads of a q/k head), dv, dgate [B, T, HV, 128] and
  * dbeta [B, T, HV], all in dtype, rounded once from FP32 sums.  q, k, gate, beta, scale, HV
- * and cu_seqlens as given to the forward.  No atomics: the same inputs give the same bits.
+ * and cu_seqlens as given to the forward (zero_rest as there, for all five).  No atomics: the same inputs give the same bits.
  *   d_final_state    gradient of the final state, [sequences, HV, 128, 128] fp32, NULL = zeros
  *   d_initial_state  gradient of the initial state, the same shape, written; NULL = not wanted
  *   saved            the forward's, read only (a backward may run again from it); saved_bytes
@@ -406,6 +408,7 @@ typedef struct {
     float *d_initial_state;
     const int *cu_seqlens;
     int num_seqs;
+    int zero_rest;
     const void *saved;
     size_t saved_bytes;
     void *workspace;

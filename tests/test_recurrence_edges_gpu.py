@@ -192,3 +192,26 @@ def test_the_short_way_leaves_the_rest_to_the_checks():
     assert lib.quick_layer_norm_fwd(h, None, None, 1e-5) is not None
     o, _, _ = kda.kda_chunk_fwd(*a, 1)  # the checked way takes an integer
     assert torch.equal(o, kda.kda_chunk_fwd(*a, 1.0)[0])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("H,HV", [(1, 3), (2, 2)])
+def test_zeros_where_no_sequence_is(H, HV, dtype):
+    """Outputs that the call allocates have zeros before the first and behind the last sequence,
+    whatever was in their memory."""
+    x = cuda(make(50, H, HV, dtype=dtype, seed=42))
+    c = cu([20, 0, 13], start=5)
+    junk = [torch.full((50 * HV * 128,), float("nan"), device="cuda", dtype=dtype)
+            for _ in range(8)]
+    torch.cuda.synchronize()
+    del junk  # the allocator hands this memory out again
+    got = train(x, x["v"], cu_seqlens=c)
+    for name, t in zip(("o", *GRADS), got):
+        assert (t[:, :5] == 0).all() and (t[:, 38:] == 0).all(), name
+        assert torch.isfinite(t).all() and (t[:, 5:38] != 0).any(), name
+    mine = torch.full_like(x["q"], 7.0)  # an output that the caller gives keeps what it had
+    _, _, saved = kda.kda_chunk_fwd(*args(x), save=True, cu_seqlens=c)
+    rest = kda.kda_chunk_bwd(*args(x), x["v"], saved, cu_seqlens=c, dq=mine)
+    assert (mine[:, :5] == 7).all() and (mine[:, 38:] == 7).all()
+    for name, t in zip(GRADS[1:], rest[1:5]):
+        assert (t[:, :5] == 0).all() and (t[:, 38:] == 0).all(), name
