@@ -51,31 +51,9 @@ __device__ __forceinline__ float floor_gate(float x) {
     return y;
 }
 
-// Two FP32 operations in one instruction (the pair in a 64-bit register).
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\n"
-        "mul.rn.f32x2 z, x, y;\nmov.b64 {%0, %1}, z;\n}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\n"
-        "add.rn.f32x2 z, x, y;\nmov.b64 {%0, %1}, z;\n}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\n"
-        "mov.b64 z, {%6, %7};\nfma.rn.f32x2 z, x, y, z;\nmov.b64 {%0, %1}, z;\n}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
+using kda::add2;
+using kda::fma2;
+using kda::mul2;
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
@@ -300,7 +278,8 @@ template <int NW, int PREP, int SOLVERS> struct Roles {
     static constexpr bool kApart = NW == 2;
     static constexpr int kGroup = kApart ? 4 : NW;  // warps that take registers
     static constexpr int kThreads = kApart ? 640 : 32 * (NW + PREP + SOLVERS);
-    static constexpr int kGive = kThreads > 512 ? (NW == 8 ? 64 : 80) : kThreads == 512 && NW == 4 ? 88 : 112;
+    static constexpr int kGive = kThreads > 512   ? (NW == 8 ? 64 : 80)
+                                 : kThreads == 512 && NW == 4 ? 88 : 112;
     static constexpr int kTake = kThreads > 512 && NW != 8 ? 160 : NW == 8 ? 144 : 248;
     static constexpr int kLaunch = 65536 / kThreads / 8 * 8;
     static_assert(kGroup % 4 == 0 && PREP % 4 == 0 && SOLVERS % 4 == 0, "");

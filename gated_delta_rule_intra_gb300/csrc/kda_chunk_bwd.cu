@@ -19,6 +19,9 @@
 // Every term carries 2^(G_r - G_s) of the whole-sequence cumulative gate, so with
 // x_t = q dq_t + k (dk_row - dk_col)_t the gate's gradient falls by ln2 x_t from a token to the
 // next; at a slot's first token it is ln2 sum_dv S dS.
+//
+// B=8 T=2048 H=16 FP16: 600 us for 4096 slots, 45 thousand cycles each on one SM: three products
+// for each of kda_fast_bwd.cu's, whose comment tells what bounds them.
 #include <type_traits>
 
 #include "kda_chunk.cuh"

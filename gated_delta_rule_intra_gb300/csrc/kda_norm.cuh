@@ -28,11 +28,32 @@ template <> __device__ __forceinline__ __half from_f32<__half>(float x) {
     return __float2half_rn(x);
 }
 
+// Neighbouring elements as FP32.
+__device__ __forceinline__ float2 two(const float *p) { return make_float2(p[0], p[1]); }
+__device__ __forceinline__ float2 two(const __nv_bfloat16 *p) {
+    const uint32_t u = *reinterpret_cast<const uint32_t *>(p);
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ float2 two(const __half *p) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(p));
+}
+__device__ __forceinline__ void put_two(float *p, float2 x) {
+    p[0] = x.x;
+    p[1] = x.y;
+}
+__device__ __forceinline__ void put_two(__nv_bfloat16 *p, float2 x) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __float22bfloat162_rn(x);
+}
+__device__ __forceinline__ void put_two(__half *p, float2 x) {
+    *reinterpret_cast<__half2 *>(p) = __float22half2_rn(x);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // A thread's elements of a row.  WIDE: 16-byte accesses, a group's next to each other; otherwise
 // single elements TPR columns apart (rows that start at no 16-byte boundary).
 template <typename T, bool WIDE, int TPR> struct Part {
     static constexpr int E = elements<T, WIDE>(), kVec = 16 / (int)sizeof(T);
-    T v[E];
+    alignas(16) T v[E];
 
     static __device__ __forceinline__ int col(int t, int i) {
         return WIDE ? (i / kVec * TPR + t) * kVec + i % kVec : t + i * TPR;

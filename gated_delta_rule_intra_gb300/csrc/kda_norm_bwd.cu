@@ -5,7 +5,8 @@
 // Bound by memory: x and dy are read once, dx is written once.  A resident CTA walks rows
 // grid-stride and keeps its columns' sums of dy xhat and dy in registers; at the end it writes
 // them to its own row of `partial`, and a second kernel adds the rows up in a fixed order, so
-// the result does not depend on which CTA finished first.
+// the result does not depend on which CTA finished first.  32768 x 2048 BF16: 68.3 + 3.4 us, of
+// which the first is 5.9 TB/s.
 #include "kda_norm.cuh"
 
 namespace kda {
@@ -32,11 +33,12 @@ __global__ void __launch_bounds__(threads<TPR>(), per_sm<elements<T, WIDE>(), WI
     __shared__ float sums[kGroups > 1 ? kGroups : 1][kGroups > 1 ? TPR * E : 1];
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR, lane = threadIdx.x & 31;
     const int w = t / 32;
-    float wt[E], dw[E] = {}, db[E] = {};
+    float2 wt[E / 2], dw[E / 2] = {}, db[E / 2] = {};
 #pragma unroll
     for (int i = 0; i < E; ++i) {
         const int c = P::col(t, i);
-        wt[i] = c < a.width ? param(a.weight, a.wdtype, c, 1.f) : 0.f;
+        (i & 1 ? wt[i / 2].y : wt[i / 2].x) =
+            c < a.width ? param(a.weight, a.wdtype, c, 1.f) : 0.f;
     }
     const float inv_n = 1.f / (float)a.width;
     const long long step = (long long)gridDim.x * kGroups;
@@ -64,19 +66,19 @@ __global__ void __launch_bounds__(threads<TPR>(), per_sm<elements<T, WIDE>(), WI
         const float mean = st.x, rstd = st.y;
         st = st1;
         st1 = stats(row + 2 * step);
-        float s1 = 0.f, s2 = 0.f, xh[E], h[E];
+        // past the row's end weight and dy are zero, so that nothing of xhat there counts
+        float2 sum1 = both(0.f), sum2 = both(0.f), xh[E / 2], h[E / 2];
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const float d = as_f32(dy.v[i]);
-            xh[i] = (as_f32(x.v[i]) - mean) * rstd;
-            h[i] = d * wt[i];
-            s1 += h[i];
-            s2 += h[i] * xh[i];
-            if (WIDE || P::col(t, i) < a.width) {
-                dw[i] += d * xh[i];
-                db[i] += d;
-            }
+        for (int i = 0; i < E / 2; ++i) {
+            const float2 d = two(&dy.v[2 * i]);
+            xh[i] = mul2(add2(two(&x.v[2 * i]), both(-mean)), both(rstd));
+            h[i] = mul2(d, wt[i]);
+            sum1 = add2(sum1, h[i]);
+            sum2 = fma2(h[i], xh[i], sum2);
+            dw[i] = fma2(d, xh[i], dw[i]);
+            db[i] = add2(db[i], d);
         }
+        float s1 = sum1.x + sum1.y, s2 = sum2.x + sum2.y;
         constexpr int kLanes = TPR < 32 ? TPR : 32;
         s1 = lanes_sum<kLanes>(s1);
         s2 = lanes_sum<kLanes>(s2);
@@ -91,7 +93,8 @@ __global__ void __launch_bounds__(threads<TPR>(), per_sm<elements<T, WIDE>(), WI
         s2 *= inv_n;
         P out;
 #pragma unroll
-        for (int i = 0; i < E; ++i) out.v[i] = from_f32<T>(rstd * (h[i] - s1 - xh[i] * s2));
+        for (int i = 0; i < E / 2; ++i)
+            put_two(&out.v[2 * i], mul2(both(rstd), fma2(xh[i], both(-s2), add2(h[i], both(-s1)))));
         out.store((T *)a.dx + row * a.dx_stride, t, a.width, row < a.rows);
     }
     cp_async_wait_newest<0>();
@@ -102,8 +105,8 @@ __global__ void __launch_bounds__(threads<TPR>(), per_sm<elements<T, WIDE>(), WI
         for (int i = 0; i < E; ++i) {
             const int c = P::col(t, i);
             if (c < a.width) {
-                to[c] = dw[i];
-                to[a.width + c] = db[i];
+                to[c] = i & 1 ? dw[i / 2].y : dw[i / 2].x;
+                to[a.width + c] = i & 1 ? db[i / 2].y : db[i / 2].x;
             }
         }
     } else {
@@ -111,7 +114,10 @@ __global__ void __launch_bounds__(threads<TPR>(), per_sm<elements<T, WIDE>(), WI
         for (int pass = 0; pass < 2; ++pass) {
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < E; ++i) sums[grp][P::col(t, i)] = pass ? db[i] : dw[i];
+            for (int i = 0; i < E; ++i) {
+                const float2 x = pass ? db[i / 2] : dw[i / 2];
+                sums[grp][P::col(t, i)] = i & 1 ? x.y : x.x;
+            }
             __syncthreads();
             for (int c = threadIdx.x; c < a.width; c += kThreads) {
                 float s = 0.f;

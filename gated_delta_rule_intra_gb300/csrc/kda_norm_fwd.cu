@@ -6,7 +6,8 @@
 // large sums), in FP32.  Rows of more than 32 threads: each warp finds its own mean and
 // squared differences, and one exchange through shared memory joins them,
 //   mean = sum n_w mean_w / n,   M2 = sum M2_w + sum n_w (mean_w - mean)^2.
-// The next rows are on their way meanwhile (Stream).
+// The next rows are on their way meanwhile (Stream).  32768 x 2048 BF16: 44.4 us, 6.05 TB/s (49.3
+// with the sums' operations in pairs, as the backward has them: more registers).
 #include "kda_norm.cuh"
 
 namespace kda {
