@@ -26,8 +26,7 @@
 // that a user may scale freely needs.  A TF32 operand would keep 11 bits at half the rate.
 #pragma once
 
-#include "kda_common.cuh"
-#include "kda_ops.h"
+#include "kda_ops.cuh"
 #include "tc_ptx.cuh"
 
 namespace kda {

@@ -5,8 +5,7 @@
 // need more registers each.
 #pragma once
 
-#include "kda_common.cuh"
-#include "kda_ops.h"
+#include "kda_ops.cuh"
 
 namespace kda {
 namespace norm {
