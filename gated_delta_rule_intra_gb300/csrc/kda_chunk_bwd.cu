@@ -558,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
 // dq and dk of a q/k head: the sum over its value heads, in head order.
 template <typename T16>
 __global__ void __launch_bounds__(256) kda_chunk_bwd_heads_kernel(const ChunkBwdArgs a) {
+    wait_for_previous();
     const int G = a.HV / a.H;
     const size_t n = a.rows_o / G * (D / 4);
     const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
@@ -595,14 +596,14 @@ cudaError_t launch(const ChunkBwdArgs &a, int dev, cudaStream_t stream) {
         static volatile int done[kMaxDev];
         e = smem_limit_once(kda_chunk_bwd_kernel<T16>, (int)sizeof(Smem), dev, done);
         if (e != cudaSuccess) return e;
-        kda_chunk_bwd_kernel<T16><<<(unsigned)(units < kSMs ? units : kSMs), kThreads,
-                                    sizeof(Smem), stream>>>(a);
+        kda_chunk_bwd_kernel<T16><<<units < kSMs ? (unsigned)units : kSMs, kThreads, sizeof(Smem),
+                                    stream>>>(a);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess || !a.dq_hv || a.slots == 0) return e;
     const size_t n = 2 * (a.rows_o / (a.HV / a.H)) * (D / 4);
-    kda_chunk_bwd_heads_kernel<T16><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_early(kda_chunk_bwd_heads_kernel<T16>, (unsigned)((n + 255) / 256), 256, 0, stream,
+                        a);
 }
 
 }  // namespace

@@ -432,6 +432,7 @@ __device__ __forceinline__ void finish(const ChunkFwdArgs &a, const float (&o)[4
 template <typename T16, int NW, int KS, bool SAVE>
 __global__ void __launch_bounds__(Roles<NW, KS>::kThreads, 1)
     kda_chunk_fwd_kernel(const ChunkFwdArgs a) {
+    wait_for_previous();
     constexpr int kSlice = 16 * NW / KS, kSplit = D / kSlice, kJ = 16 / KS;
     constexpr int kPrep = 128 * KS;  // threads that prepare operands
     extern __shared__ __align__(128) char smem_raw[];
@@ -618,8 +619,7 @@ cudaError_t launch(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
     const cudaError_t e = ready_once<Roles<NW, KS>>(kernel, (int)sizeof(Smem), dev, done);
     if (e != cudaSuccess) return e;
     const int grid = a.num_seqs * a.HV * (8 * KS / NW);
-    kernel<<<grid, Roles<NW, KS>::kThreads, sizeof(Smem), stream>>>(a);
-    return cudaGetLastError();
+    return launch_early(kernel, grid, Roles<NW, KS>::kThreads, sizeof(Smem), stream, a);
 }
 
 template <typename T16, bool SAVE>

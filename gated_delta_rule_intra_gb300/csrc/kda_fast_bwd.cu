@@ -654,7 +654,7 @@ cudaError_t launch_bwd(const ChunkBwdArgs &a, int dev, cudaStream_t stream) {
     static volatile int done[kMaxDev];
     e = smem_limit_once(kda_fast_bwd_kernel, (int)sizeof(Smem), dev, done);
     if (e != cudaSuccess) return e;
-    kda_fast_bwd_kernel<<<(unsigned)(units < kSMs ? units : kSMs), kThreads, sizeof(Smem), stream>>>(
+    kda_fast_bwd_kernel<<<units < kSMs ? (unsigned)units : kSMs, kThreads, sizeof(Smem), stream>>>(
         a);
     return cudaGetLastError();
 }

@@ -269,8 +269,8 @@ cudaError_t launch(const ChunkBwdArgs &a, int dev, cudaStream_t stream) {
     cudaError_t e = chunk::ready_once<Roles<NW>>(kda_fast_bwd_state_kernel<NW>,
                                             (int)sizeof(Smem), dev, done);
     if (e != cudaSuccess) return e;
-    kda_fast_bwd_state_kernel<NW><<<a.num_seqs * a.HV * (8 / NW),
-                                        Roles<NW>::kThreads, sizeof(Smem), stream>>>(a);
+    kda_fast_bwd_state_kernel<NW><<<a.num_seqs * a.HV * (8 / NW), Roles<NW>::kThreads,
+                                    sizeof(Smem), stream>>>(a);
     return cudaGetLastError();
 }
 

@@ -241,6 +241,7 @@ __device__ __forceinline__ void solve(Smem &sm, Stage &out, int buf, char *tiles
 template <int NW, bool SAVE>
 __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
     kda_fast_fwd_kernel(const ChunkFwdArgs a) {
+    wait_for_previous();
     constexpr int kSlice = 16 * NW, kSplit = D / kSlice;
     extern __shared__ __align__(128) char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
@@ -471,8 +472,8 @@ cudaError_t launch(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
                                             (int)sizeof(Smem), dev, done);
     if (e != cudaSuccess) return e;
     const int grid = a.num_seqs * a.HV * (8 / NW);
-    kda_fast_fwd_kernel<NW, SAVE><<<grid, Roles<NW>::kThreads, sizeof(Smem), stream>>>(a);
-    return cudaGetLastError();
+    return launch_early(kda_fast_fwd_kernel<NW, SAVE>, grid, Roles<NW>::kThreads, sizeof(Smem),
+                        stream, a);
 }
 
 template <bool SAVE> cudaError_t launch_split(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {

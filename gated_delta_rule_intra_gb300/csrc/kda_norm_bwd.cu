@@ -23,6 +23,7 @@ template <bool WIDE, int TPR> constexpr int depth() { return !WIDE ? 2 : TPR == 
 template <typename T, bool WIDE, int TPR>
 __global__ void __launch_bounds__(threads<TPR>(), per_sm<elements<T, WIDE>(), WIDE, TPR>())
     kda_layer_norm_bwd_kernel(const NormArgs a) {
+    wait_for_previous();
     constexpr int kThreads = threads<TPR>(), kGroups = kThreads / TPR;
     constexpr int kWarps = TPR > 32 ? TPR / 32 : 1;
     using P = Part<T, WIDE, TPR>;
@@ -132,6 +133,7 @@ __global__ void __launch_bounds__(threads<TPR>(), per_sm<elements<T, WIDE>(), WI
 // Column sums of `partial` [n][cols]: 32 columns a CTA, 32 slices of rows side by side.
 __global__ void __launch_bounds__(1024)
     kda_layer_norm_sum_kernel(const float *partial, int n, int width, float *dweight, float *dbias) {
+    wait_for_previous();
     __shared__ float red[32][33];
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const long long cols = 2LL * width, c = (long long)blockIdx.x * 32 + lane;
@@ -154,6 +156,7 @@ __global__ void __launch_bounds__(1024)
 
 // Rows that no CTA's registers hold: dx by one CTA a row ...
 template <typename T> __global__ void __launch_bounds__(1024) kda_layer_norm_bwd_long_kernel(const NormArgs a) {
+    wait_for_previous();
     __shared__ float2 red[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -183,6 +186,7 @@ template <typename T> __global__ void __launch_bounds__(1024) kda_layer_norm_bwd
 
 // ... and the column sums by a pass of their own: 256 columns a CTA, one slice of the rows.
 template <typename T> __global__ void __launch_bounds__(256) kda_layer_norm_bwd_cols_kernel(const NormArgs a) {
+    wait_for_previous();
     const int c = blockIdx.x * 256 + threadIdx.x;
     if (c >= a.width) return;
     float dw = 0.f, db = 0.f;
@@ -208,9 +212,8 @@ int ctas(long long rows, int width, int e, bool wide) {
 
 cudaError_t sum_partials(const NormArgs &a, int n, cudaStream_t stream) {
     if (!a.dweight) return cudaSuccess;
-    kda_layer_norm_sum_kernel<<<(unsigned)((2LL * a.width + 31) / 32), 1024, 0, stream>>>(
-        a.partial, n, a.width, a.dweight, a.dbias);
-    return cudaGetLastError();
+    return launch_early(kda_layer_norm_sum_kernel, (unsigned)((2LL * a.width + 31) / 32), 1024, 0,
+                        stream, a.partial, n, a.width, a.dweight, a.dbias);
 }
 
 template <typename T, bool WIDE, int TPR>
@@ -223,8 +226,7 @@ cudaError_t launch(const NormArgs &a, cudaStream_t stream) {
         e = smem_limit_once(kda_layer_norm_bwd_kernel<T, WIDE, TPR>, kBytes, dev, done);
     if (e != cudaSuccess) return e;
     const int n = ctas(a.rows, a.width, elements<T, WIDE>(), WIDE);
-    kda_layer_norm_bwd_kernel<T, WIDE, TPR><<<n, threads<TPR>(), kBytes, stream>>>(a);
-    e = cudaGetLastError();
+    e = launch_early(kda_layer_norm_bwd_kernel<T, WIDE, TPR>, n, threads<TPR>(), kBytes, stream, a);
     return e != cudaSuccess ? e : sum_partials(a, n, stream);
 }
 
@@ -240,14 +242,12 @@ template <typename T, bool WIDE> cudaError_t pick(const NormArgs &a, cudaStream_
         case 8192 / E: return launch<T, WIDE, 8192 / E>(a, stream);
     }
     const long long most = 2 * kSMs;
-    kda_layer_norm_bwd_long_kernel<T>
-        <<<(unsigned)(a.rows < most ? a.rows : most), 1024, 0, stream>>>(a);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_early(kda_layer_norm_bwd_long_kernel<T>,
+                                 (unsigned)(a.rows < most ? a.rows : most), 1024, 0, stream, a);
     if (e != cudaSuccess || !a.dweight) return e;
     const int n = ctas(a.rows, a.width, elements<T, WIDE>(), WIDE);
-    kda_layer_norm_bwd_cols_kernel<T>
-        <<<dim3((unsigned)((a.width + 255) / 256), (unsigned)n), 256, 0, stream>>>(a);
-    e = cudaGetLastError();
+    e = launch_early(kda_layer_norm_bwd_cols_kernel<T>,
+                     dim3((unsigned)((a.width + 255) / 256), (unsigned)n), 256, 0, stream, a);
     return e != cudaSuccess ? e : sum_partials(a, n, stream);
 }
 

@@ -16,6 +16,7 @@ namespace {
 
 template <typename T, bool WIDE, int TPR>
 __global__ void __launch_bounds__(threads<TPR>()) kda_layer_norm_fwd_kernel(const NormArgs a) {
+    wait_for_previous();
     constexpr int kThreads = threads<TPR>(), kGroups = kThreads / TPR;
     constexpr int kWarps = TPR > 32 ? TPR / 32 : 1;
     using P = Part<T, WIDE, TPR>;
@@ -120,6 +121,7 @@ __global__ void __launch_bounds__(threads<TPR>()) kda_layer_norm_fwd_kernel(cons
 
 // Rows that no CTA's registers hold: one CTA a row, three passes over it (from L2).
 template <typename T> __global__ void __launch_bounds__(1024) kda_layer_norm_fwd_long_kernel(const NormArgs a) {
+    wait_for_previous();
     __shared__ float red[2][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -163,9 +165,8 @@ cudaError_t launch(const NormArgs &a, cudaStream_t stream) {
         e = smem_limit_once(kda_layer_norm_fwd_kernel<T, WIDE, TPR>, kBytes, dev, done);
     if (e != cudaSuccess) return e;
     const long long want = (a.rows + kGroups - 1) / kGroups, most = kSMs * (1024 / kThreads);
-    kda_layer_norm_fwd_kernel<T, WIDE, TPR>
-        <<<(unsigned)(want < most ? want : most), kThreads, kBytes, stream>>>(a);
-    return cudaGetLastError();
+    return launch_early(kda_layer_norm_fwd_kernel<T, WIDE, TPR>,
+                        (unsigned)(want < most ? want : most), kThreads, kBytes, stream, a);
 }
 
 template <typename T, bool WIDE> cudaError_t pick(const NormArgs &a, cudaStream_t stream) {
@@ -180,9 +181,8 @@ template <typename T, bool WIDE> cudaError_t pick(const NormArgs &a, cudaStream_
         case 8192 / E: return launch<T, WIDE, 8192 / E>(a, stream);
     }
     const long long most = 2 * kSMs;
-    kda_layer_norm_fwd_long_kernel<T>
-        <<<(unsigned)(a.rows < most ? a.rows : most), 1024, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_early(kda_layer_norm_fwd_long_kernel<T>,
+                        (unsigned)(a.rows < most ? a.rows : most), 1024, 0, stream, a);
 }
 
 template <typename T> cudaError_t pick_wide(const NormArgs &a, cudaStream_t stream) {

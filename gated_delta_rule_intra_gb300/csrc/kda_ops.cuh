@@ -6,6 +6,33 @@
 
 namespace kda {
 
+// Kernels launched with launch_early() may start before the one in front of them on the stream has
+// ended, so that the launch itself overlaps its tail (a prefill of 37 tokens 10.2 -> 7.3 us, the
+// three launches of a 2021 x 1111 layer norm 22.9 -> 16.9).  Each thread's first act there is
+// wait_for_previous(): everything in front is complete and its writes are visible behind it.  No
+// CTA may leave this out, one with nothing to do included: the next kernel's wait covers what is
+// in front of this one only through this one.  The backward's long kernels are launched as usual:
+// early, their CTAs land on other SMs than the ones that wrote what they read (1655 -> 1678 us
+// for a training step).
+__device__ __forceinline__ void wait_for_previous() {
+    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+}
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem,
+                         cudaStream_t stream, Args... args) {
+    cudaLaunchAttribute early = {};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
 // Two FP32 operations in one instruction (the pair in a 64-bit register).
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 r;

@@ -5,8 +5,8 @@
 //
 // The state (64 KB a head in FP32) is read once and written once; everything else is 1.5 KB.
 // A CTA holds its part of one head's state in registers between the column sums and the
-// update, every load issued before the first use.  Bound by memory: 8192 heads take 158 us,
-// 6.8 TB/s; one request's 16 heads take 2.5 us, the latency of a launch and one round trip.
+// update, every load issued before the first use.  Bound by memory: 8192 heads take 156 us,
+// 6.9 TB/s; one request's 16 heads take 2.5 us, the latency of a launch and one round trip.
 #include "kda_chunk.cuh"
 #include "kda_ops.h"
 
@@ -19,6 +19,7 @@ constexpr int D = KD;
 // VQ: groups of four dv columns of a CTA (32 = the whole head).
 template <typename T16, int VQ>
 __global__ void __launch_bounds__(kThreads) kda_step_kernel(const StepArgs a) {
+    wait_for_previous();
     constexpr int kRowGroups = kThreads / VQ;  // dk rows in flight side by side
     constexpr int kRows = D / kRowGroups;      // rows of a thread
     __shared__ float coef[3][D];               // 2^gate, k, q
@@ -120,10 +121,8 @@ template <typename T16> cudaError_t launch(const StepArgs &a, cudaStream_t strea
     // one CTA each and 4.4 in four, 64 heads 3.6 and 3.1.
     const long long heads = (long long)a.N * a.HV;
     if (heads * 2 > kSMs)
-        kda_step_kernel<T16, 32><<<(unsigned)heads, kThreads, 0, stream>>>(a);
-    else
-        kda_step_kernel<T16, 8><<<(unsigned)(4 * heads), kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+        return launch_early(kda_step_kernel<T16, 32>, (unsigned)heads, kThreads, 0, stream, a);
+    return launch_early(kda_step_kernel<T16, 8>, (unsigned)(4 * heads), kThreads, 0, stream, a);
 }
 
 }  // namespace

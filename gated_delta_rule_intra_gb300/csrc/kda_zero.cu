@@ -1,8 +1,7 @@
 // Zeros for the tokens of a packed row that are in no sequence, in all outputs of a call at once:
 // one launch of 2.5 us instead of a fill of every output from end to end before the call (six of
 // 4.5 us for the 9467 tokens of a training step with 8 value heads).
-#include "kda_common.cuh"
-#include "kda_ops.h"
+#include "kda_ops.cuh"
 
 namespace kda {
 namespace {
@@ -19,6 +18,7 @@ __device__ __forceinline__ void clear(char *p, size_t row, long long lead, long 
 }
 
 __global__ void __launch_bounds__(256) kda_zero_rest_kernel(const ZeroArgs a) {
+    wait_for_previous();
     auto token = [&](int x) { return (long long)(x < 0 ? 0 : x > a.T ? a.T : x); };
     const long long lead = token(a.cu_seqlens[0]);  // the sequences are [lead, tail)
     long long tail = token(a.cu_seqlens[a.num_seqs]);
@@ -35,8 +35,7 @@ __global__ void __launch_bounds__(256) kda_zero_rest_kernel(const ZeroArgs a) {
 
 cudaError_t launch_zero_rest(const ZeroArgs &a, cudaStream_t stream) {
     if (a.T == 0) return cudaSuccess;
-    kda_zero_rest_kernel<<<kSMs, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_early(kda_zero_rest_kernel, kSMs, 256, 0, stream, a);
 }
 
 }  // namespace kda
