@@ -7,7 +7,7 @@
 // warp is held in FP32 as S c with |S c| <= 2^15 (c follows from a running bound, made exact
 // again whenever it runs out), e and the gradients a power of two per tile and step found
 // with a warp reduction.  q 2^g, k 2^g and k 2^(g_l - g) are no larger than q and k and need
-// none; steps whose inputs pass 2^14, or anything not finite, take the definition token by
+// none of their own; steps whose inputs pass 2^14, or anything not finite, take the definition token by
 // token in FP32 instead.  Sums, the state, the solve and the pairs' scores stay FP32 (the small
 // [16][16] products and the scores take TF32 operands, which need no range).
 #pragma once
@@ -180,11 +180,62 @@ struct __align__(128) Planes {
     int careful;        // take the definition
 };
 
+// Steps whose channels lose no more than 2^-19 and whose inputs are of ordinary size (the mild
+// ones): q 2^g, k 2^g and k 2^-g all fit FP16's normal range when the first two are taken 2^11
+// times and the last 2^-8 times as large.  The scores are then products of these planes, and the
+// key plane is that from the step's start, as in the precise kernels.
+constexpr float kMildGate = -19.f, kMildK = 8.f, kMildQ = 16.f;
+constexpr int kMildUp = 11, kMildDown = 8;
+
+// These planes from the raw inputs (128 threads, two channels of eight rows each).  Returns
+// whether the step is mild as far as the thread's warp has seen.
+__device__ __forceinline__ bool prepare_mild(const RawStage &raw, Planes &out, float scale,
+                                             int tid) {
+    const int c2 = tid & 63, r0 = (tid >> 6) * 8;
+    auto gate = [&](int r) {
+        const float2 x = *reinterpret_cast<const float2 *>(&raw.gate[r][2 * c2]);
+        return make_float2(chunk::floor_gate(x.x), chunk::floor_gate(x.y));
+    };
+    float2 g = make_float2(0.f, 0.f);
+    if (r0) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) g = chunk::add2(g, gate(r));
+    }
+    uint32_t km = 0, qm = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = r0 + i;
+        g = chunk::add2(g, gate(r));
+        const uint32_t qr = *reinterpret_cast<const uint32_t *>(&raw.q[r][2 * c2]);
+        const uint32_t kr = *reinterpret_cast<const uint32_t *>(&raw.k[r][2 * c2]);
+        km = __vmaxu2(km, kr & 0x7fff7fffu);
+        qm = __vmaxu2(qm, qr & 0x7fff7fffu);
+        const float2 k = bf2(kr), q = chunk::mul2(bf2(qr), make_float2(scale, scale));
+        const float2 up = make_float2(ex2(g.x + kMildUp), ex2(g.y + kMildUp));
+        const float2 dn = make_float2(ex2(-kMildDown - g.x), ex2(-kMildDown - g.y));
+        const float2 kw = chunk::mul2(k, up), qw = chunk::mul2(q, up), kd = chunk::mul2(k, dn);
+        const uint32_t off = chunk::plane_off(r, c2 >> 2) + (c2 & 3) * 4;
+        *reinterpret_cast<uint32_t *>(out.kw + off) = pack_f16(kw.x, kw.y);
+        *reinterpret_cast<uint32_t *>(out.qw + off) = pack_f16(qw.x, qw.y);
+        *reinterpret_cast<uint32_t *>(out.kd + off) = pack_f16(kd.x, kd.y);
+    }
+    if (r0) *reinterpret_cast<float2 *>(&out.decay[2 * c2]) = make_float2(ex2(g.x), ex2(g.y));
+    const uint32_t kb = __reduce_max_sync(0xffffffffu, max(km << 16, km & 0xffff0000u));
+    const uint32_t qb = __reduce_max_sync(0xffffffffu, max(qm << 16, qm & 0xffff0000u));
+    if ((tid & 31) == 0) {
+        out.kmax[tid >> 5] = kb;
+        out.qmax[tid >> 5] = qb;
+    }
+    return g.x >= kMildGate && g.y >= kMildGate && __uint_as_float(kb) <= kMildK &&
+           scale * __uint_as_float(qb) <= kMildQ;
+}
+
 // The operand planes from the raw inputs (128 threads, two channels of eight rows each) and,
-// where wanted, the cumulative gate.  Returns whether a channel loses more than 2^-96.
+// where wanted, the cumulative gate.  Returns whether a channel loses more than 2^-96; `mild`,
+// whether prepare_mild() would have done.
 template <bool KEEP_G>
 __device__ __forceinline__ bool prepare(const RawStage &raw, Planes &out, float (*gcum)[kRowPad],
-                                        float scale, int tid) {
+                                        float scale, int tid, bool *mild = nullptr) {
     const int c2 = tid & 63, r0 = (tid >> 6) * 8;
     auto gate = [&](int r) {
         const float2 x = *reinterpret_cast<const float2 *>(&raw.gate[r][2 * c2]);
@@ -223,6 +274,9 @@ __device__ __forceinline__ bool prepare(const RawStage &raw, Planes &out, float 
         out.kmax[tid >> 5] = kb;
         out.qmax[tid >> 5] = qb;
     }
+    if (mild)
+        *mild = total.x >= kMildGate && total.y >= kMildGate && __uint_as_float(kb) <= kMildK &&
+                scale * __uint_as_float(qb) <= kMildQ;
     return total.x < -96.f || total.y < -96.f;
 }
 __device__ __forceinline__ float largest(const uint32_t (&m)[4]) {

@@ -5,9 +5,13 @@
 // operand planes, four take the scores M and P, four solve the steps' triangular systems in
 // turn, and eight (or four) consumers with 16 dv columns of the state each take the products.
 // The walk is a chain, R -> e -> n -> S', so what bounds it is the time of one step on one SM:
-// 3.9 thousand cycles with eight consumers, 3.0 with four.  A consumer's own 58 products are 0.5
-// of these; the rest is shared by the issue slots (55% taken), the shared-memory pipe (57%) and
-// the chain's latencies.  B=8 T=4096 H=16: 480 us for 256 steps, B=2 T=1024 H=4: 94 us for 64.
+// 3.6 thousand cycles with eight consumers, 2.7 with four.  A consumer's own 58 products are 0.5
+// of these; the rest is shared by the issue slots and the shared-memory pipe (both 55% taken) and
+// the chain's latencies.  With nothing but the consumers a step would take half as long.
+// B=8 T=4096 H=16: 447 us for 256 steps, B=2 T=1024 H=4: 86 us for 64; with gates too strong for
+// the mild form 498 and 98.
+#include <type_traits>
+
 #include "kda_fast.cuh"
 #include "kda_ops.h"
 
@@ -32,15 +36,20 @@ constexpr int kRaw = kStages + 2;  // raw input stages: two ahead, and as far ba
 enum { BAR_PREP = 1, BAR_SCORE = 2, BAR_PLANES = 3, BAR_FULL = 6, BAR_EMPTY = 9, BAR_SOLVE = 12 };
 
 constexpr int kSolvers = 4;  // warps that take the steps' systems in turn
+// Mild steps are tried after as many that would have been: a step that turns out not to be is
+// prepared twice.
+constexpr int kCalm = 4;
 // NW consumer warps of 16 dv columns each; a head takes 8 / NW CTAs.
 template <int NW> using Roles = chunk::Roles<NW, 8, kSolvers>;
+
+enum { MILD = 0, GENERAL, STRONG };  // how a step's scores are taken
 
 struct __align__(128) Stage {
     Planes pl;
     char t2[kTall];  // T2, FP32 for TF32 products
     char p[kTile];   // P, FP16
-    float g[C][kRowPad];
-    int strong;
+    float g[C][kRowPad];  // cumulative gate, unless the step is mild
+    int form;
 };
 
 struct __align__(128) Smem {
@@ -101,11 +110,53 @@ __device__ __forceinline__ void put_p(Stage &out, char *pt, int r, int s, float 
     *reinterpret_cast<uint32_t *>(pt + tall_at(s, r)) = to_tf32(x);
 }
 
-// M and P of a step, M = (k 2^g) (k 2^-g)^T and P = (scale q 2^g) (k 2^-g)^T: the exponents
-// cancel in each term, and no term is above |q_r k_s|.  Each warp sums a quarter of the
-// channels, straight from the raw inputs, then one of the four 16x8 tiles over the quarters.
-// Entries above the diagonal may be of any size and are dropped.  Returns whether an entry of
-// P is out of FP16's reach.
+// A warp's tile of the scores: M (w < 2) or P, the tokens s 8 (w % 2) on.  Entries above the
+// diagonal may be of any size and are dropped.  Returns whether an entry of P is out of FP16's
+// reach.
+__device__ __forceinline__ bool put_scores(Smem &sm, Stage &out, const float *beta, int buf,
+                                           const float (&x)[4], int w, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    bool big = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = g + (i >> 1) * 8, s = 8 * (w & 1) + 2 * t + (i & 1);
+        if (w >= 2) {
+            const float p = s <= r ? x[i] : 0.f;
+            put_p(out, sm.pt[buf], r, s, p);
+            big = big || !(fabsf(p) <= 16384.f);
+        } else if (s < r) {
+            sm.a2[buf][s][r] = x[i] * beta[s];
+            sm.a1[buf][s][r] = x[i] * beta[r];
+        }
+    }
+    return big;
+}
+
+// M and P of a mild step, M = kw (k 2^-g)^T and P = qw (k 2^-g)^T, from its planes.
+__device__ __forceinline__ bool scores_mild(Smem &sm, Stage &out, const float *beta, int buf,
+                                            int w, int lane) {
+    const uint32_t left = smem_u32(w >= 2 ? out.pl.qw : out.pl.kw), right = smem_u32(out.pl.kd);
+    const int m = lane >> 3, arow = (lane & 7) + (m & 1) * 8, brow = 8 * (w & 1) + (lane & 7);
+    float c[2][4] = {};
+#pragma unroll
+    for (int kk = 0; kk < 8; kk += 2) {
+        uint32_t a0[4], a1[4], b[4];
+        ldsm4(a0, left + plane_off(arow, 2 * kk + (m >> 1)));
+        ldsm4(a1, left + plane_off(arow, 2 * kk + 2 + (m >> 1)));
+        ldsm4(b, right + plane_off(brow, 2 * kk + m));
+        mma_f16(c[0], a0, b[0], b[1]);
+        mma_f16(c[1], a1, b[2], b[3]);
+    }
+    constexpr float kBack = 1.f / (1 << (kMildUp - kMildDown));
+    float x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = (c[0][i] + c[1][i]) * kBack;
+    return put_scores(sm, out, beta, buf, x, w, lane);
+}
+
+// The same in general, in TF32: the exponents cancel in each term, and no term is above
+// |q_r k_s|.  Each warp sums a quarter of the channels, straight from the raw inputs, then one of
+// the four tiles over the quarters.
 __device__ __forceinline__ bool scores(Smem &sm, Stage &out, const RawStage &raw,
                                        const float *beta, int buf, float scale, int w, int lane) {
     const int g = lane >> 2, t = lane & 3;
@@ -143,20 +194,7 @@ __device__ __forceinline__ bool scores(Smem &sm, Stage &out, const RawStage &raw
         const float4 y = sm.part[buf & 1][i][w][lane];
         x[0] += y.x; x[1] += y.y; x[2] += y.z; x[3] += y.w;
     }
-    bool big = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = g + (i >> 1) * 8, s = 8 * (w & 1) + 2 * t + (i & 1);
-        if (w >= 2) {
-            const float p = s <= r ? x[i] : 0.f;
-            put_p(out, sm.pt[buf], r, s, p);
-            big = big || !(fabsf(p) <= 16384.f);
-        } else if (s < r) {
-            sm.a2[buf][s][r] = x[i] * beta[s];
-            sm.a1[buf][s][r] = x[i] * beta[r];
-        }
-    }
-    return big;
+    return put_scores(sm, out, beta, buf, x, w, lane);
 }
 
 // The same where 2^-g would leave FP32's range: pair by pair, one exp2 per (r, s, channel),
@@ -265,6 +303,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
                     if (i < steps) in.load(sm, a, i);
                     cp_async_commit();
                 }
+                int calm = kCalm;  // steps in a row that were mild
                 for (int i = 0; i < steps; ++i) {
                     const int st = i % kStages;
                     Stage &out = sm.stage[st];
@@ -272,10 +311,18 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
                     // the consumers are done with this stage's previous step (and its inputs)
                     if (i >= kStages) bar_sync(BAR_EMPTY + st, kHalf + 32 * NW);
                     bar_sync(BAR_PREP, kHalf);
-                    const bool strong =
-                        prepare<true>(sm.raw[i % kRaw], out.pl, out.g, a.scale, tid);
-                    const bool any = bar_or(BAR_PREP, kHalf, strong);
-                    if (tid == 0) out.strong = any;
+                    const RawStage &raw = sm.raw[i % kRaw];
+                    int form = GENERAL;
+                    if (calm >= kCalm &&
+                        !bar_or(BAR_PREP, kHalf, !prepare_mild(raw, out.pl, a.scale, tid)))
+                        form = MILD;
+                    if (form != MILD) {
+                        bool mild;
+                        const bool strong = prepare<true>(raw, out.pl, out.g, a.scale, tid, &mild);
+                        if (bar_or(BAR_PREP, kHalf, strong)) form = STRONG;
+                        calm = bar_or(BAR_PREP, kHalf, !mild) ? 0 : calm + 1;
+                    }
+                    if (tid == 0) out.form = form;
                     bar_arrive(BAR_PLANES + st, 2 * kHalf);
                     if (i + 2 < steps) in.load(sm, a, i + 2);
                     cp_async_commit();
@@ -293,7 +340,10 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
                 const RawStage &raw = sm.raw[i % kRaw];
                 bar_sync(BAR_PLANES + st, 2 * kHalf);
                 bool big;
-                if (!chunk::uniform(out.strong)) {
+                const int form = chunk::uniform(out.form);
+                if (form == MILD) {
+                    big = scores_mild(sm, out, beta, buf, w, lane);
+                } else if (form == GENERAL) {
                     big = scores(sm, out, raw, beta, buf, a.scale, w, lane);
                 } else {
                     big = scores_strong(sm, out, raw, beta, buf, a.scale, w, lane);
@@ -385,7 +435,9 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         }
         if (keep)  // outside the loop above, which a branch would cut into pieces
             store_tile(a.ckpt + unit_at * kCkptBytes, S, tile0, lane);
-        const float ckpt_scale = S.saved_scale(), inv = S.inv;  // of the state as an operand
+        const bool mild = chunk::uniform(in.form == MILD);
+        const float ckpt_scale = S.saved_scale();  // of the state as an operand
+        const float inv = mild ? S.inv * (1.f / (1 << kMildUp)) : S.inv;  // with that of kw and qw
         // R = v - kw S and e = T2 R; blocks (tokens 0-7, dv 0-7), (0-7, 8-15), (8-15, ..)
         uint32_t vr[4], x0[4], x1[4];
         ldsm4t(vr, smem_u32(sm.v[slot]) + plane_off(lrow, role.consumer * 2 + lcol));
@@ -405,40 +457,57 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         careful = careful || !finite(em);
         const float bm = in.pl.bmax;
         if (!chunk::uniform(careful)) {
-            // n = beta e
+            // n = beta e, 2^4 times as large where the key plane is 2^-4 times
+            const float more = mild ? (float)(1 << kMildDown) : 1.f;
+            const float less = mild ? 1.f / (1 << kMildDown) : 1.f;
             uint32_t nf[4];
-            const float ratio = join_scale(S, em * bm, C * kmax);
-            const float c = S.c;
+            const float ratio = join_scale(S, em * bm * more, C * kmax * less);
+            const float c = S.c * more;
             nf[0] = pack_f16(e[0][0] * (b[0].x * c), e[0][1] * (b[0].y * c));
             nf[1] = pack_f16(e[0][2] * (b[0].x * c), e[0][3] * (b[0].y * c));
             nf[2] = pack_f16(e[1][0] * (b[1].x * c), e[1][1] * (b[1].y * c));
             nf[3] = pack_f16(e[1][2] * (b[1].x * c), e[1][3] * (b[1].y * c));
-            S.inv = inverse_of(c);
-            // S' = diag(2^g_l) S + kd^T n
+            S.inv = inverse_of(S.c);
+            // S' = diag(2^g_l) (S + (k 2^-g)^T n), or diag(2^g_l) S + kd^T n
+            if (mild && chunk::uniform(ratio != 1.f)) {
 #pragma unroll
-            for (int jj = 0; jj < 8; ++jj) {
-                uint32_t kf[4];
-                ldsm4t(kf, kd + plane_off(trow, 2 * jj + tcol));
+                for (int j = 0; j < 16; ++j)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float2 d =
-                        *reinterpret_cast<const float2 *>(&in.pl.decay[16 * jj + 8 * x + tc2]);
-                    float(&s)[4] = S.s[2 * jj + x];
-                    const float2 dr = chunk::mul2(d, make_float2(ratio, ratio));
-                    const float2 u = chunk::mul2(make_float2(s[0], s[1]), dr);
-                    const float2 w = chunk::mul2(make_float2(s[2], s[3]), dr);
-                    s[0] = u.x; s[1] = u.y; s[2] = w.x; s[3] = w.y;
-                    mma_f16(s, nf, kf[2 * x], kf[2 * x + 1]);
-                }
+                    for (int p = 0; p < 4; ++p) S.s[j][p] *= ratio;
             }
+            auto update = [&](auto decay_last) {
+#pragma unroll
+                for (int jj = 0; jj < 8; ++jj) {
+                    uint32_t kf[4];
+                    ldsm4t(kf, kd + plane_off(trow, 2 * jj + tcol));
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float2 d =
+                            *reinterpret_cast<const float2 *>(&in.pl.decay[16 * jj + 8 * x + tc2]);
+                        float(&s)[4] = S.s[2 * jj + x];
+                        const float2 dr =
+                            decay_last ? d : chunk::mul2(d, make_float2(ratio, ratio));
+                        if (decay_last) mma_f16(s, nf, kf[2 * x], kf[2 * x + 1]);
+                        const float2 u = chunk::mul2(make_float2(s[0], s[1]), dr);
+                        const float2 w = chunk::mul2(make_float2(s[2], s[3]), dr);
+                        s[0] = u.x; s[1] = u.y; s[2] = w.x; s[3] = w.y;
+                        if (!decay_last) mma_f16(s, nf, kf[2 * x], kf[2 * x + 1]);
+                    }
+                }
+            };
+            if (mild)
+                update(std::true_type{});
+            else
+                update(std::false_type{});
             // o = qw S + P n
             float po[2][4] = {};
             mma_f16(po[0], nf, pf[0], pf[1]);
             mma_f16(po[1], nf, pf[2], pf[3]);
+            const float p_inv = S.inv * less;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int p = 0; p < 4; ++p) xq[j][p] = fmaf(po[j][p], S.inv, xq[j][p] * inv);
+                for (int p = 0; p < 4; ++p) xq[j][p] = fmaf(po[j][p], p_inv, xq[j][p] * inv);
         } else {
             walk_tokens(S, xq, e, sm.raw[slot], beta, sm.v[slot], role.consumer * 16, a.scale,
                         lane);
@@ -477,7 +546,7 @@ cudaError_t launch(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
 }
 
 template <bool SAVE> cudaError_t launch_split(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
-    // A step takes 3.9 thousand cycles in one CTA a head and 3.0 in two.  In four it takes
+    // A step takes 3.6 thousand cycles in one CTA a head and 2.7 in two.  In four it takes
     // as long: the preparation bounds it from two on.
     return chunk::best_split(a.num_seqs, a.HV, a.cu_seqlens) == 1
                ? launch<8, SAVE>(a, dev, stream)

@@ -215,3 +215,23 @@ def test_zeros_where_no_sequence_is(H, HV, dtype):
     assert (mine[:, :5] == 7).all() and (mine[:, 38:] == 7).all()
     for name, t in zip(GRADS[1:], rest[1:5]):
         assert (t[:, :5] == 0).all() and (t[:, 38:] == 0).all(), name
+
+
+@pytest.mark.parametrize("every", [1, 2, 3, 7])
+def test_mild_and_other_steps_in_turn(every):
+    """BF16 training prepares steps with mild gates and ordinary inputs in a form of their own: the
+    forms follow one another, also where a step looks mild and turns out not to be."""
+    x = make(16 * 23 + 5, 1, 2, seed=43)
+    for step in range(0, 24, every):
+        a = slice(16 * step, 16 * step + 16)
+        kind = step // every % 4
+        if kind == 0:
+            x["gate"][:, a, 0, 7] -= 1.9  # a channel loses 2^-30 and more
+        elif kind == 1:
+            x["k"][:, a] *= 16.0
+            x["beta"][:, a] /= 256.0
+        elif kind == 2:
+            x["q"][:, a] *= 512.0
+        else:
+            x["gate"][:, a] -= 8.0
+    check(x)
