@@ -265,10 +265,10 @@ struct __align__(16) RawStage {
     float gate[C][D];
 };
 
-// Which warps do what: NW consume, PREP prepare operands, SOLVERS solve the steps' triangular
-// systems.  Two consumers get two of the SM's four schedulers with the solvers, the preparing
-// warps the other two: warps go to the schedulers in turn, and the warps in between leave at
-// once.
+// Which warps do what: NW consume, PREP prepare operands (and take the scores), SOLVERS solve the
+// steps' triangular systems.  Two consumers have two of the SM's four schedulers to themselves and
+// leave the other two to the preparing warps: warps go to the schedulers in turn, and the warps in
+// between leave at once.
 //
 // Registers move from the feeding warps to the consumers, by groups of four warps: both shares
 // add up to no more than the kernel is launched with (65,536 over its threads, in eights), which
@@ -282,7 +282,7 @@ template <int NW, int PREP, int SOLVERS> struct Roles {
     static constexpr int kTake = kThreads > 512 && NW != 8 ? 160 : NW == 8 ? 144 : 248;
     static constexpr int kLaunch = 65536 / kThreads / 8 * 8;
     static_assert(kGroup % 4 == 0 && PREP % 4 == 0 && SOLVERS % 4 == 0, "");
-    static_assert(!kApart || (PREP == 8 && SOLVERS <= 8), "");
+    static_assert(!kApart || (PREP == 8 && SOLVERS == 0), "");
     static_assert(kGroup * 32 * kTake + (kThreads - kGroup * 32) * kGive <= kLaunch * kThreads, "");
 
     int prep, solver, consumer;  // index, or -1
@@ -292,11 +292,7 @@ template <int NW, int PREP, int SOLVERS> struct Roles {
         if (!feeds) {
             if (warp < NW) consumer = warp;
         } else if (kApart) {
-            const int x = (warp - kGroup) / 4 * 2 + (warp & 1);
-            if (warp & 2)
-                prep = x;
-            else if (x < SOLVERS)
-                solver = x;
+            if (warp & 2) prep = (warp - kGroup) / 4 * 2 + (warp & 1);
         } else if (warp < kGroup + PREP) {
             prep = warp - kGroup;
         } else {
