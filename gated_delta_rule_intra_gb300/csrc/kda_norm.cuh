@@ -138,8 +138,9 @@ __device__ __forceinline__ float param(const void *p, int dtype, int c, float no
     return as_f32(((const __half *)p)[c]);
 }
 
-// Rows that a group takes at once: two where their sums cross warps, each covering the other's
-// exchange.
+// Rows that a group takes at once in the forward: two where their sums cross warps, each covering
+// the other's exchange (32768 x 2048 BF16 45 us, one at a time 59; inside a warp there is no
+// difference: 524288 x 128 takes 45 us either way).
 template <bool WIDE, int TPR> constexpr int at_once() { return WIDE && TPR >= 64 ? 2 : 1; }
 
 template <int TPR> constexpr int threads() { return TPR < 256 ? 256 : TPR; }
