@@ -345,9 +345,18 @@ __device__ __forceinline__ void put_split(char *hi_plane, uint32_t off, float x,
     *reinterpret_cast<uint32_t *>(hi_plane + kPlane + off) = lo;
 }
 
+// The larger one; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // Operand planes of a step from its raw inputs: NT threads, each two channels of C * 64 / NT
 // rows.  Writes kw, qw, 2^g_l and the key plane: k 2^(g_l - g), or with FROM_START k 2^-g,
-// which may grow without bound.  Returns whether one of these grew past 2^96.
+// which may grow without bound.  Returns whether the latter will not do: a key grew past 2^96 or is
+// NaN, or a channel lost more than 2^-100 (2^-g leaves FP32's range soon after, and a key of
+// zero times infinity would be NaN).
 template <typename T16, int NT, bool FROM_START>
 __device__ __forceinline__ bool prep_planes(const RawStage &raw, char *planes, float *decay,
                                             float scale, int tid) {
@@ -384,9 +393,9 @@ __device__ __forceinline__ bool prep_planes(const RawStage &raw, char *planes, f
         put_split(planes + QW_HI * kPlane, off, qw.x, qw.y);
         put_split(planes + KD_HI * kPlane, off, kd.x, kd.y);
         if (r == C - 1) *reinterpret_cast<float2 *>(&decay[2 * c2]) = up;
-        if (FROM_START) big = fmaxf(big, fmaxf(fabsf(kd.x), fabsf(kd.y)));
+        if (FROM_START) big = max_nan(big, max_nan(fabsf(kd.x), fabsf(kd.y)));
     }
-    return big > 0x1p96f;
+    return !(big <= 0x1p96f && g.x >= -100.f && g.y >= -100.f);
 }
 
 // hi and lo A-fragments of a 16x16 FP32 block held as two adjacent 16x8 accumulators.

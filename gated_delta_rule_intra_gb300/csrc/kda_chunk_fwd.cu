@@ -127,7 +127,7 @@ __device__ __forceinline__ void scores(Smem &sm, Prepared &out, const float *bet
 }
 
 // Gates so strong that k 2^-g leaves FP32's range inside a step (a channel loses more than
-// 2^-96 in 16 tokens): the key plane in its bounded form, the gate replaced by its cumsum ...
+// 2^-96 or so in 16 tokens), or keys and gates that are not finite: the key plane in its bounded form, the gate replaced by its cumsum ...
 template <typename T16, int NT>
 __device__ __forceinline__ void prep_strong(RawStage &raw, Prepared &out, float scale, int tid) {
     prep_planes<T16, NT, false>(raw, out.planes, out.decay, scale, tid);

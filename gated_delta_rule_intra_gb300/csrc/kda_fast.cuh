@@ -91,11 +91,7 @@ __device__ __forceinline__ void mma_tall(float (&c0)[4], float (&c1)[4], const u
     mma_tf32(c1, x1, hi[2], hi[3]);
 }
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
+using chunk::max_nan;
 // The warp's largest of non-negative values (or of their bits); NaN counts as largest.
 __device__ __forceinline__ float warp_max(float x) {
     return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));

@@ -1,0 +1,125 @@
+"""The recurrence over the whole range of its inputs: scales of either sign, keys and queries of any
+size, keys of zero under gates that clear their channel, keys and gates that are not finite, values
+near the type's limits under strong gates -- against the definition in 64 bits."""
+
+import pytest
+import torch
+
+import gated_delta_rule_intra_gb300 as kda
+from tests._recurrence import (EXTRA, F64, GRADS, NAMES, STATE_TOL, cu, cuda, forward64,
+                               gradients64, make, rel, states)
+
+pytestmark = pytest.mark.gpu
+
+BF, HF = torch.bfloat16, torch.float16
+
+# What the header promises beside the rounding of the outputs: 1e-3 for BF16 calls without a
+# state, 1e-5 for o and 1e-4 for the gradients otherwise (EXTRA covers both).
+TRAIN = 1e-3
+
+
+def args(x):
+    return [x[n] for n in NAMES]
+
+
+def rounding(ref, dtype):
+    """The error of the exact result rounded to `dtype`; 2% for the spread of another sample."""
+    ref = ref.detach()
+    return 1.02 * float((ref.to(dtype).to(F64) - ref).norm() / ref.norm().clamp(min=1e-30))
+
+
+def close(name, got, ref, extra):
+    bound = rounding(ref, got.dtype) + extra
+    assert rel(got, ref) <= bound, (name, rel(got, ref), bound)
+
+
+def gradient_of(x, seed=9):
+    return torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(seed)).to(
+        x["v"].dtype)
+
+
+def check_train(x, scale=None, do=None, lens=None, extra=None, ref=None):
+    """Forward and backward without a state; `ref` are the inputs of the definition."""
+    dt = x["q"].dtype
+    do = gradient_of(x) if do is None else do
+    extra = extra or (TRAIN if dt == BF else EXTRA)
+    d, c = cuda(x), None if lens is None else cu(lens)
+    o, _, saved = kda.kda_chunk_fwd(*args(d), scale=scale, cu_seqlens=c, save=True)
+    got = kda.kda_chunk_bwd(*args(d), do.cuda(), saved, scale=scale, cu_seqlens=c)
+    s = scale or 128 ** -0.5
+    ref = x if ref is None else ref
+    close("o", o, forward64(ref, s, None, lens)[0], extra)
+    for name, g, r in zip(GRADS, got, gradients64(ref, do, s, None, None, lens)[0]):
+        close(name, g, r, extra)
+
+
+def check_states(x, scale=None, do=None, ref=None, state_tol=STATE_TOL):
+    """Forward and backward with the states and their gradients."""
+    B, HV = x["v"].shape[0], x["v"].shape[2]
+    S0, dS = states(B, HV), states(B, HV, seed=4)
+    do = gradient_of(x) if do is None else do
+    d = cuda(x)
+    o, final, saved = kda.kda_chunk_fwd(*args(d), scale=scale, initial_state=S0.cuda(),
+                                        output_final_state=True, save=True)
+    got = kda.kda_chunk_bwd(*args(d), do.cuda(), saved, scale=scale, d_final_state=dS.cuda(),
+                            output_d_initial_state=True)
+    s = scale or 128 ** -0.5
+    ref = x if ref is None else ref
+    ro, rf = forward64(ref, s, S0)
+    close("o", o, ro, EXTRA)
+    assert rel(final, rf) <= state_tol, rel(final, rf)
+    grads, dS0 = gradients64(ref, do, s, S0, dS)
+    for name, g, r in zip(GRADS, got, grads):
+        close(name, g, r, EXTRA)
+    assert rel(got[5], dS0) <= state_tol, rel(got[5], dS0)
+
+
+# ------------------------------------------------------------------------ cleared channels
+def cleared(x, mask, gate):
+    """(inputs with that gate at `mask`, those of the definition, where 2^gate is zero)"""
+    return (dict(x, gate=x["gate"].masked_fill(mask, gate)),
+            dict(x, gate=x["gate"].masked_fill(mask, -5000.0)))
+
+
+def zero_keys(case, dtype):
+    x = make(40, 1, 2, dtype=dtype, seed=61)
+    drop = torch.zeros(x["gate"].shape, dtype=torch.bool)
+    if case == "padding":      # tokens behind the end of a prompt
+        drop[:, 25:] = True
+        x["k"][:, 25:] = 0
+        x["v"][:, 25:] = 0
+    elif case == "reset":      # a token that only clears, last in a step of 16
+        drop[:, 15] = True
+        x["k"][:, 15] = 0
+    elif case == "first":      # the same, first in a step
+        drop[:, 16] = True
+        x["k"][:, 16] = 0
+    else:                      # a channel no key uses, forgotten fast
+        x["k"][..., 7] = 0
+        x["gate"][..., 7] = -10.0
+    return cleared(x, drop, float("-inf"))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("case", ["padding", "reset", "first", "channel"])
+def test_keys_of_zero_where_a_channel_is_cleared(case, dtype):
+    x, ref = zero_keys(case, dtype)
+    check_states(x, ref=ref)
+    check_train(x, ref=ref)
+
+
+# ------------------------------------------------------------------------ not finite
+@pytest.mark.parametrize("dtype,state", [(BF, False), (BF, True), (HF, False)])
+@pytest.mark.parametrize("what", ["q", "k", "v", "gate", "beta"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_what_is_not_finite_reaches_no_earlier_token(value, what, dtype, state):
+    if what == "gate" and value > 0:
+        pytest.skip("a gate is not above zero")
+    x = make(40, 2, 2, 2, dtype, seed=62)
+    ref = forward64(x)[0]
+    clean = kda.kda_chunk_fwd(*args(cuda(x)), output_final_state=state)[0]
+    x[what][0, 21, 1] = value
+    o = kda.kda_chunk_fwd(*args(cuda(x)), output_final_state=state)[0]
+    assert torch.equal(o[1], clean[1]) and torch.equal(o[0, :, 0], clean[0, :, 0])
+    assert rel(o[0, :21, 1], ref[0, :21, 1]) <= 2.0 ** -8 + EXTRA
+    assert not torch.isfinite(o[0, 21, 1]).all()
