@@ -223,7 +223,7 @@ __device__ __forceinline__ bool prepare_mild(const RawStage &raw, Planes &out, f
         out.qmax[tid >> 5] = qb;
     }
     return g.x >= kMildGate && g.y >= kMildGate && __uint_as_float(kb) <= kMildK &&
-           scale * __uint_as_float(qb) <= kMildQ;
+           fabsf(scale) * __uint_as_float(qb) <= kMildQ;
 }
 
 // The operand planes from the raw inputs (128 threads, two channels of eight rows each) and,
@@ -272,7 +272,7 @@ __device__ __forceinline__ bool prepare(const RawStage &raw, Planes &out, float 
     }
     if (mild)
         *mild = total.x >= kMildGate && total.y >= kMildGate && __uint_as_float(kb) <= kMildK &&
-                scale * __uint_as_float(qb) <= kMildQ;
+                fabsf(scale) * __uint_as_float(qb) <= kMildQ;
     return total.x < -96.f || total.y < -96.f;
 }
 __device__ __forceinline__ float largest(const uint32_t (&m)[4]) {

@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
                 return __uint_as_float(
                     __reduce_max_sync(0xffffffffu, max(m << 16, m & 0xffff0000u)));
             };
-            const float qm = a.scale * over_warp(qb);
+            const float qm = fabsf(a.scale) * over_warp(qb);
             const float km = over_warp(kb) *
                              warp_max(fmaxf(fabsf(sm.beta[lane]), fabsf(sm.beta[32 + lane])));
             float e_sum = 0.f, d_sum = 0.f;  // 2^14 of the operands' own scales

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         bar_sync(BAR_FULL + st, kHalf + 32 * NW);
         const Planes &in = sm.stage[st];
         const uint32_t kw = smem_u32(in.kw), qw = smem_u32(in.qw), kd = smem_u32(in.kd);
-        const float kmax = largest(in.kmax), qmax = a.scale * largest(in.qmax), bm = in.bmax;
+        const float kmax = largest(in.kmax), qmax = fabsf(a.scale) * largest(in.qmax), bm = in.bmax;
         bool careful = in.careful || !(kmax <= 16384.f) || !(qmax <= 16384.f);
         if (chunk::uniform(S.bound > kLimit)) S.renew();
         uint32_t th[4], tl[4], ph[4], pl[4];

@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
                     out.pl.bmax = bm;
                     out.pl.careful = big[0] || big[1] || big[2] || big[3] || !finite(bm) ||
                                      !(largest(out.pl.kmax) <= 16384.f) ||
-                                     !(a.scale * largest(out.pl.qmax) <= 16384.f);
+                                     !(fabsf(a.scale) * largest(out.pl.qmax) <= 16384.f);
                 }
                 if (SAVE || lane < 16) solve(sm, out, w, tiles, lane);
                 __syncwarp();

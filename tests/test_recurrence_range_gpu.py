@@ -74,6 +74,24 @@ def check_states(x, scale=None, do=None, ref=None, state_tol=STATE_TOL):
     assert rel(got[5], dS0) <= state_tol, rel(got[5], dS0)
 
 
+# ------------------------------------------------------------------------ scales
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("lo", [-0.5, -3.0, -40.0])
+@pytest.mark.parametrize("scale", [-128 ** -0.5, -2.0])
+def test_negative_scales(scale, lo, dtype):
+    check_train(make(100, 1, 2, dtype=dtype, lo=lo, seed=52), scale)
+
+
+def test_a_negative_scale_in_packed_sequences():
+    lens = [70, 1, 0, 33]
+    check_train(make(sum(lens), 2, 2, seed=53), -0.25, lens=lens)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_a_negative_scale_with_states(dtype):
+    check_states(make(70, 1, 2, dtype=dtype, seed=54), -0.25)
+
+
 # ------------------------------------------------------------------------ cleared channels
 def cleared(x, mask, gate):
     """(inputs with that gate at `mask`, those of the definition, where 2^gate is zero)"""
