@@ -6,10 +6,11 @@
 // operands that a user may scale freely carry a power of two of their own: the state tile of a
 // warp is held in FP32 as S c with |S c| <= 2^15 (c follows from a running bound, made exact
 // again whenever it runs out), e and the gradients a power of two per tile and step found
-// with a warp reduction.  q 2^g, k 2^g and k 2^(g_l - g) are no larger than q and k and need
-// none of their own; steps whose inputs pass 2^14, or anything not finite, take the definition token by
-// token in FP32 instead.  Sums, the state, the solve and the pairs' scores stay FP32 (the small
-// [16][16] products and the scores take TF32 operands, which need no range).
+// with a warp reduction, and the planes of q and k one each that follows a step's largest |q| and
+// |k|: an input keeps its 11 bits down to 2^-6 of that where the gates are mild, 2^-11 otherwise.
+// Steps whose inputs pass 2^14, or anything not finite, take the definition token by token in FP32
+// instead.  Sums, the state, the solve and the pairs' scores stay FP32 (the small [16][16]
+// products and the scores take TF32 operands, which need no range).
 #pragma once
 
 #include "kda_chunk.cuh"
@@ -172,20 +173,110 @@ struct __align__(128) Planes {
     float decay[D];     // 2^g_l
     uint32_t kmax[4];   // |k|, |q| of each preparing warp's rows: BF16 bits shifted up
     uint32_t qmax[4];
+    float kinv, qinv;   // the planes' powers of two, inverse
+    float ktop, qtop;   // backward: the step's largest |k| and |scale q|
     float bmax;         // largest |beta|
     int careful;        // take the definition
 };
+__device__ __forceinline__ float largest(const uint32_t (&m)[4]) {
+    return __uint_as_float(max(max(m[0], m[1]), max(m[2], m[3])));
+}
 
-// Steps whose channels lose no more than 2^-19 and whose inputs are of ordinary size (the mild
-// ones): q 2^g, k 2^g and k 2^-g all fit FP16's normal range when the first two are taken 2^11
-// times and the last 2^-8 times as large.  The scores are then products of these planes, and the
+// The power of two that brings a step's largest |k| (or |scale q|) to 1 .. 2, so that the planes
+// have FP16's bits for inputs of any size; 1 where there are only zeros.  Outside 2^-60 .. 2^14 it
+// stays what it is at the end: what is smaller has no bits beside a value of ordinary size, and
+// larger inputs take the definition.
+__device__ __forceinline__ float plane_scale(float largest) {
+    return largest == 0.f ? 1.f : scale_for(fminf(fmaxf(largest, 0x1p-60f), 0x1p14f), 0);
+}
+// Where the largest |k| and |scale q| have to be with the planes' powers of two, so that the
+// forward may go on with the step before's: finding the maximum in front of the planes costs its
+// preparing warps, whose chain is the longer one, 3% of a step.
+constexpr float kLeast = 0.125f, kMost = 3.5f;
+
+// The planes' powers of two: kw and kd are taken `k` times as large, qw `q` times (`scale` included;
+// qabs is its size).
+struct Scales {
+    float k, q, kinv, qinv, qabs;
+
+    __device__ __forceinline__ explicit Scales(float scale) { set(1.f, 1.f, scale); }
+    __device__ __forceinline__ void set(float kpower, float qpower, float scale) {
+        k = kpower;
+        q = scale * qpower;
+        kinv = inverse_of(kpower);
+        qinv = inverse_of(qpower);
+        qabs = fabsf(q);
+    }
+    __device__ __forceinline__ void follow(const Planes &p, float scale) {
+        set(plane_scale(largest(p.kmax)), plane_scale(fabsf(scale) * largest(p.qmax)), scale);
+    }
+    __device__ __forceinline__ bool in_range(float kmax, float qmax) const {
+        const float x = k * kmax, y = qabs * qmax;
+        return x >= kLeast && x <= kMost && y >= kLeast && y <= kMost;
+    }
+    // For the step; zeros fit any power.
+    __device__ __forceinline__ bool fit(const Planes &p) const {
+        const float km = largest(p.kmax), qm = largest(p.qmax);
+        return in_range(km == 0.f ? kinv : km, qm == 0.f ? 1.f / qabs : qm);
+    }
+    // The same for each preparing warp's part of it, as its barrier sees it.
+    __device__ __forceinline__ bool fit_all(const Planes &p) const {
+        bool ok = true;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            ok = ok && in_range(__uint_as_float(p.kmax[i]), __uint_as_float(p.qmax[i]));
+        return ok;
+    }
+};
+// A preparing warp's largest |k| and |q| from its threads'; returns whether they are in range.
+__device__ __forceinline__ bool put_largest(Planes &out, uint32_t km, uint32_t qm, const Scales &sc,
+                                            int tid) {
+    const uint32_t kb = __reduce_max_sync(0xffffffffu, max(km << 16, km & 0xffff0000u));
+    const uint32_t qb = __reduce_max_sync(0xffffffffu, max(qm << 16, qm & 0xffff0000u));
+    if ((tid & 31) == 0) {
+        out.kmax[tid >> 5] = kb;
+        out.qmax[tid >> 5] = qb;
+    }
+    return sc.in_range(__uint_as_float(kb), __uint_as_float(qb));
+}
+
+// The largest |q| and |k| among what a preparing thread has copied itself (eight channels of the
+// rows tid / 16 and 8 more), which it may read before the others' copies are visible to it: the
+// maxima then cost no barrier of their own.
+__device__ __forceinline__ void find_largest(const RawStage &raw, Planes &out, int tid) {
+    auto most = [&](const uint16_t (*rows)[kRowPad]) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 x =
+                *reinterpret_cast<const uint4 *>(&rows[(tid >> 4) + 8 * i][(tid & 15) * 8]);
+            m = __vmaxu2(__vmaxu2(m, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
+            m = __vmaxu2(__vmaxu2(m, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
+        }
+        return __reduce_max_sync(0xffffffffu, max(m << 16, m & 0xffff0000u));
+    };
+    const uint32_t q = most(raw.q), k = most(raw.k);
+    if ((tid & 31) == 0) {
+        out.qmax[tid >> 5] = q;
+        out.kmax[tid >> 5] = k;
+    }
+}
+
+// Inputs that FP16 planes take; the others go the definition's way.
+__device__ __forceinline__ bool in_reach(const Planes &p, float scale) {
+    return largest(p.kmax) <= 16384.f && fabsf(scale) * largest(p.qmax) <= 16384.f;
+}
+
+// Steps whose channels lose no more than 2^-19 (the mild ones): q 2^g, k 2^g and k 2^-g of inputs
+// with a largest element of 1 .. 2 all fit FP16's normal range when the first two are taken 2^14
+// times and the last 2^-5 times as large.  The scores are then products of these planes, and the
 // key plane is that from the step's start, as in the precise kernels.
-constexpr float kMildGate = -19.f, kMildK = 8.f, kMildQ = 16.f;
-constexpr int kMildUp = 11, kMildDown = 8;
+constexpr float kMildGate = -19.f;
+constexpr int kUp = 14, kMildDown = 5;
 
-// These planes from the raw inputs (128 threads, two channels of eight rows each).  Returns
-// whether the step is mild as far as the thread's warp has seen.
-__device__ __forceinline__ bool prepare_mild(const RawStage &raw, Planes &out, float scale,
+// These planes (128 threads, two channels of eight rows each).  Returns whether the step is mild,
+// with inputs in range of the planes' powers of two, as far as the thread and its warp have seen.
+__device__ __forceinline__ bool prepare_mild(const RawStage &raw, Planes &out, const Scales &sc,
                                              int tid) {
     const int c2 = tid & 63, r0 = (tid >> 6) * 8;
     auto gate = [&](int r) {
@@ -197,6 +288,7 @@ __device__ __forceinline__ bool prepare_mild(const RawStage &raw, Planes &out, f
 #pragma unroll
         for (int r = 0; r < 8; ++r) g = chunk::add2(g, gate(r));
     }
+    const float2 ks = make_float2(sc.k, sc.k), qs = make_float2(sc.q, sc.q);
     uint32_t km = 0, qm = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -206,8 +298,8 @@ __device__ __forceinline__ bool prepare_mild(const RawStage &raw, Planes &out, f
         const uint32_t kr = *reinterpret_cast<const uint32_t *>(&raw.k[r][2 * c2]);
         km = __vmaxu2(km, kr & 0x7fff7fffu);
         qm = __vmaxu2(qm, qr & 0x7fff7fffu);
-        const float2 k = bf2(kr), q = chunk::mul2(bf2(qr), make_float2(scale, scale));
-        const float2 up = make_float2(ex2(g.x + kMildUp), ex2(g.y + kMildUp));
+        const float2 k = chunk::mul2(bf2(kr), ks), q = chunk::mul2(bf2(qr), qs);
+        const float2 up = make_float2(ex2(g.x + kUp), ex2(g.y + kUp));
         const float2 dn = make_float2(ex2(-kMildDown - g.x), ex2(-kMildDown - g.y));
         const float2 kw = chunk::mul2(k, up), qw = chunk::mul2(q, up), kd = chunk::mul2(k, dn);
         const uint32_t off = chunk::plane_off(r, c2 >> 2) + (c2 & 3) * 4;
@@ -216,22 +308,18 @@ __device__ __forceinline__ bool prepare_mild(const RawStage &raw, Planes &out, f
         *reinterpret_cast<uint32_t *>(out.kd + off) = pack_f16(kd.x, kd.y);
     }
     if (r0) *reinterpret_cast<float2 *>(&out.decay[2 * c2]) = make_float2(ex2(g.x), ex2(g.y));
-    const uint32_t kb = __reduce_max_sync(0xffffffffu, max(km << 16, km & 0xffff0000u));
-    const uint32_t qb = __reduce_max_sync(0xffffffffu, max(qm << 16, qm & 0xffff0000u));
-    if ((tid & 31) == 0) {
-        out.kmax[tid >> 5] = kb;
-        out.qmax[tid >> 5] = qb;
-    }
-    return g.x >= kMildGate && g.y >= kMildGate && __uint_as_float(kb) <= kMildK &&
-           fabsf(scale) * __uint_as_float(qb) <= kMildQ;
+    return put_largest(out, km, qm, sc, tid) && g.x >= kMildGate && g.y >= kMildGate;
 }
 
-// The operand planes from the raw inputs (128 threads, two channels of eight rows each) and,
-// where wanted, the cumulative gate.  Returns whether a channel loses more than 2^-96; `mild`,
-// whether prepare_mild() would have done.
-template <bool KEEP_G>
-__device__ __forceinline__ bool prepare(const RawStage &raw, Planes &out, float (*gcum)[kRowPad],
-                                        float scale, int tid, bool *mild = nullptr) {
+// What a thread of prepare() has seen: a channel loses more than 2^-96; none more than a mild step's.
+struct Seen {
+    bool strong, mild;
+};
+// The operand planes in general (128 threads), kw and qw 2^UP and kd 2^DOWN times as large, and
+// where wanted the cumulative gate (plus UP, which its differences do not see).
+template <int UP, int DOWN>
+__device__ __forceinline__ Seen prepare(const RawStage &raw, Planes &out, float (*gcum)[kRowPad],
+                                        const Scales &sc, int tid) {
     const int c2 = tid & 63, r0 = (tid >> 6) * 8;
     auto gate = [&](int r) {
         const float2 x = *reinterpret_cast<const float2 *>(&raw.gate[r][2 * c2]);
@@ -243,40 +331,29 @@ __device__ __forceinline__ bool prepare(const RawStage &raw, Planes &out, float 
         if (r == r0) g = total;
         total = chunk::add2(total, gate(r));
     }
-    uint32_t km = 0, qm = 0;
+    g = chunk::add2(g, make_float2(UP, UP));
+    const float2 last = chunk::add2(total, make_float2(UP + DOWN, UP + DOWN));
+    const float2 ks = make_float2(sc.k, sc.k), qs = make_float2(sc.q, sc.q);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int r = r0 + i;
         g = chunk::add2(g, gate(r));
-        if (KEEP_G) *reinterpret_cast<float2 *>(&gcum[r][2 * c2]) = g;
-        const uint32_t qr = *reinterpret_cast<const uint32_t *>(&raw.q[r][2 * c2]);
-        const uint32_t kr = *reinterpret_cast<const uint32_t *>(&raw.k[r][2 * c2]);
-        km = __vmaxu2(km, kr & 0x7fff7fffu);
-        qm = __vmaxu2(qm, qr & 0x7fff7fffu);
-        const float2 q = bf2(qr), k = bf2(kr);
+        if (gcum) *reinterpret_cast<float2 *>(&gcum[r][2 * c2]) = g;
+        const float2 q = chunk::mul2(
+            bf2(*reinterpret_cast<const uint32_t *>(&raw.q[r][2 * c2])), qs);
+        const float2 k = chunk::mul2(
+            bf2(*reinterpret_cast<const uint32_t *>(&raw.k[r][2 * c2])), ks);
         const float2 up = make_float2(ex2(g.x), ex2(g.y));
-        const float2 dn = make_float2(ex2(total.x - g.x), ex2(total.y - g.y));
+        const float2 dn = make_float2(ex2(last.x - g.x), ex2(last.y - g.y));
+        const float2 kw = chunk::mul2(k, up), qw = chunk::mul2(q, up), kd = chunk::mul2(k, dn);
         const uint32_t off = chunk::plane_off(r, c2 >> 2) + (c2 & 3) * 4;
-        *reinterpret_cast<uint32_t *>(out.kw + off) = pack_f16(k.x * up.x, k.y * up.y);
-        *reinterpret_cast<uint32_t *>(out.qw + off) =
-            pack_f16(scale * q.x * up.x, scale * q.y * up.y);
-        *reinterpret_cast<uint32_t *>(out.kd + off) = pack_f16(k.x * dn.x, k.y * dn.y);
+        *reinterpret_cast<uint32_t *>(out.kw + off) = pack_f16(kw.x, kw.y);
+        *reinterpret_cast<uint32_t *>(out.qw + off) = pack_f16(qw.x, qw.y);
+        *reinterpret_cast<uint32_t *>(out.kd + off) = pack_f16(kd.x, kd.y);
     }
     if (r0 == 8)
         *reinterpret_cast<float2 *>(&out.decay[2 * c2]) = make_float2(ex2(total.x), ex2(total.y));
-    const uint32_t kb = __reduce_max_sync(0xffffffffu, max(km << 16, km & 0xffff0000u));
-    const uint32_t qb = __reduce_max_sync(0xffffffffu, max(qm << 16, qm & 0xffff0000u));
-    if ((tid & 31) == 0) {
-        out.kmax[tid >> 5] = kb;
-        out.qmax[tid >> 5] = qb;
-    }
-    if (mild)
-        *mild = total.x >= kMildGate && total.y >= kMildGate && __uint_as_float(kb) <= kMildK &&
-                fabsf(scale) * __uint_as_float(qb) <= kMildQ;
-    return total.x < -96.f || total.y < -96.f;
-}
-__device__ __forceinline__ float largest(const uint32_t (&m)[4]) {
-    return __uint_as_float(max(max(m[0], m[1]), max(m[2], m[3])));
+    return {total.x < -96.f || total.y < -96.f, total.x >= kMildGate && total.y >= kMildGate};
 }
 
 // A step token by token from the definition, forwards: e and o (before its rounding) of a tile
@@ -388,17 +465,19 @@ __device__ __forceinline__ void walk_tokens_back(Tile &t, float (&y)[2][4], cons
 
 // Scale of a step's right-hand factors of largest element `nmax` that are added to the tile:
 // the tile's own, or the tile comes down to theirs.  `ratio` is what its elements still have
-// to be multiplied by; `sum` bounds the added rows' other factors.
-__device__ __forceinline__ float join_scale(Tile &t, float nmax, float sum) {
-    nmax = fmaxf(nmax, 1e-20f);
-    if (chunk::uniform(nmax * t.c < 0.0625f)) t.renew();  // the tile has faded, or its bound is stale
+// to be multiplied by; `grow` bounds what is added, without the scale.
+__device__ __forceinline__ float join_scale(Tile &t, float nmax, float grow) {
+    nmax = fmaxf(nmax, 0x1p-80f);
+    // the tile has faded, or its bound is stale: 2^-8 leaves the largest factor its 11 bits, and six
+    // octaves below it theirs
+    if (chunk::uniform(nmax * t.c < 0x1p-8f)) t.renew();
     const float cn = scale_for(nmax, kTop);
     float ratio = 1.f;
     if (cn < t.c || t.bound == 0.f) {
         ratio = cn * t.inv;
         t.c = cn;
     }
-    t.bound = t.bound * ratio + nmax * t.c * sum;
+    t.bound = t.bound * ratio + grow * t.c;
     return ratio;
 }
 

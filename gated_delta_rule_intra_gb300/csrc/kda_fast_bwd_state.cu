@@ -96,14 +96,24 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
                     load_step<kSlice>(sm, a, sq, h, hv, dv0, i + 2, steps - 3 - i, tid);
                 cp_async_commit();
                 cp_async_wait_newest<1>();
+                find_largest(sm.raw[i % kRaw], out, tid);
                 bar_sync(BAR_PREP + group, kHalf);
-                prepare<false>(sm.raw[i % kRaw], out, nullptr, a.scale, tid);
+                Scales sc(a.scale);
+                sc.follow(out, a.scale);
+                // kw and qw are added to the state's gradient, kd is only multiplied by it
+                prepare<0, kUp>(sm.raw[i % kRaw], out, nullptr, sc, tid);
+                if (tid == 32) {
+                    out.kinv = sc.kinv;
+                    out.qinv = sc.qinv;
+                    out.ktop = largest(out.kmax);
+                    out.qtop = fabsf(a.scale) * largest(out.qmax);
+                }
                 if (tid < 32) {
                     const float bm =
                         warp_max(lane < C ? fabsf(sm.beta[i % kRaw][lane]) : 0.f);
                     if (lane == 0) {
                         out.bmax = bm;
-                        out.careful = !finite(bm);
+                        out.careful = !finite(bm) || !in_reach(out, a.scale);
                     }
                 }
                 bar_arrive(BAR_FULL + st, kHalf + 32 * NW);
@@ -144,8 +154,8 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         bar_sync(BAR_FULL + st, kHalf + 32 * NW);
         const Planes &in = sm.stage[st];
         const uint32_t kw = smem_u32(in.kw), qw = smem_u32(in.qw), kd = smem_u32(in.kd);
-        const float kmax = largest(in.kmax), qmax = fabsf(a.scale) * largest(in.qmax), bm = in.bmax;
-        bool careful = in.careful || !(kmax <= 16384.f) || !(qmax <= 16384.f);
+        const float kinv = in.kinv, qinv = in.qinv, ktop = in.ktop, qtop = in.qtop, bm = in.bmax;
+        bool careful = in.careful;
         if (chunk::uniform(S.bound > kLimit)) S.renew();
         uint32_t th[4], tl[4], ph[4], pl[4];
         load_tall(smem_u32(sm.tiles[slot]), lane, tl, th);
@@ -183,10 +193,11 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
                                 dor[3] & 0xffff0000u};
         mma_tall(dn[0], dn[1], o0, o1, pl, ph);
         uint32_t x0[4], x1[4];
+        const float ds_inv = S.inv * (1.f / (1 << kUp)) * kinv;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int p = 0; p < 4; ++p) dn[j][p] = fmaf(ds[j][p], S.inv, dn[j][p]);
+            for (int p = 0; p < 4; ++p) dn[j][p] = fmaf(ds[j][p], ds_inv, dn[j][p]);
         tf_frag(dn[0], x0);
         tf_frag(dn[1], x1);
         mma_tall(y[0], y[1], x0, x1, tl, th);
@@ -194,14 +205,15 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         careful = careful || !finite(ym) || !finite(om);
         if (!chunk::uniform(careful)) {
             uint32_t of[4], nf[4];
-            const float ratio = join_scale(S, fmaxf(om, ym * bm), C * (kmax + qmax));
-            const float c = S.c;
+            const float ratio = join_scale(S, fmaxf(om * qinv, ym * bm * kinv),
+                                           C * (om * qtop + ym * bm * ktop));
+            const float c = S.c, co = c * qinv, cy = c * kinv;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 o = bf2(dor[j]);
-                of[j] = pack_f16(o.x * c, o.y * c);
+                of[j] = pack_f16(o.x * co, o.y * co);
             }
-            const float nx[2] = {-b[0].x * c, -b[1].x * c}, ny[2] = {-b[0].y * c, -b[1].y * c};
+            const float nx[2] = {-b[0].x * cy, -b[1].x * cy}, ny[2] = {-b[0].y * cy, -b[1].y * cy};
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 nf[2 * j] = pack_f16(y[j][0] * nx[j], y[j][1] * ny[j]);

@@ -37,7 +37,7 @@ enum { BAR_PREP = 1, BAR_SCORE = 2, BAR_PLANES = 3, BAR_FULL = 6, BAR_EMPTY = 9,
 
 constexpr int kSolvers = 4;  // warps that take the steps' systems in turn
 // Mild steps are tried after as many that would have been: a step that turns out not to be is
-// prepared twice.
+// prepared twice (the first of a walk is, to find the planes' powers of two).
 constexpr int kCalm = 4;
 // NW consumer warps of 16 dv columns each; a head takes 8 / NW CTAs.
 template <int NW> using Roles = chunk::Roles<NW, 8, kSolvers>;
@@ -103,9 +103,12 @@ template <int SLICE> struct Loader {
     }
 };
 
-// An entry of P (zero above the diagonal).
-__device__ __forceinline__ void put_p(Stage &out, char *pt, int r, int s, float x) {
-    const uint32_t b = pack_f16(x, 0.f);
+// P's power of two: no entry is above 128 times the planes' largest elements, 2^13 with this.
+__device__ __forceinline__ float p_scale(const Planes &p) { return 4.f * inverse_of(p.kinv * p.qinv); }
+
+// An entry of P (zero above the diagonal), `f` times as large in FP16.
+__device__ __forceinline__ void put_p(Stage &out, char *pt, int r, int s, float x, float f) {
+    const uint32_t b = pack_f16(x * f, 0.f);
     reinterpret_cast<uint16_t *>(out.p)[r * C + s] = (uint16_t)b;
     *reinterpret_cast<uint32_t *>(pt + tall_at(s, r)) = to_tf32(x);
 }
@@ -117,13 +120,14 @@ __device__ __forceinline__ bool put_scores(Smem &sm, Stage &out, const float *be
                                            const float (&x)[4], int w, int lane) {
     const int g = lane >> 2, t = lane & 3;
     bool big = false;
+    const float f = p_scale(out.pl);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = g + (i >> 1) * 8, s = 8 * (w & 1) + 2 * t + (i & 1);
         if (w >= 2) {
             const float p = s <= r ? x[i] : 0.f;
-            put_p(out, sm.pt[buf], r, s, p);
-            big = big || !(fabsf(p) <= 16384.f);
+            put_p(out, sm.pt[buf], r, s, p, f);
+            big = big || !(fabsf(p) * f <= 16384.f);
         } else if (s < r) {
             sm.a2[buf][s][r] = x[i] * beta[s];
             sm.a1[buf][s][r] = x[i] * beta[r];
@@ -147,10 +151,11 @@ __device__ __forceinline__ bool scores_mild(Smem &sm, Stage &out, const float *b
         mma_f16(c[0], a0, b[0], b[1]);
         mma_f16(c[1], a1, b[2], b[3]);
     }
-    constexpr float kBack = 1.f / (1 << (kMildUp - kMildDown));
+    const float back =
+        out.pl.kinv * (w >= 2 ? out.pl.qinv : out.pl.kinv) * (1.f / (1 << (kUp - kMildDown)));
     float x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = (c[0][i] + c[1][i]) * kBack;
+    for (int i = 0; i < 4; ++i) x[i] = (c[0][i] + c[1][i]) * back;
     return put_scores(sm, out, beta, buf, x, w, lane);
 }
 
@@ -208,6 +213,7 @@ __device__ __forceinline__ bool scores_strong(Smem &sm, Stage &out, const RawSta
         x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
     };
     bool big = false;
+    const float f = p_scale(out.pl);
 #pragma unroll 1
     for (int j = 0; j < 17; ++j) {
         const int r = j <= w ? w : C - 1 - w, s = j <= w ? j : j - w - 1;
@@ -229,11 +235,11 @@ __device__ __forceinline__ bool scores_strong(Smem &sm, Stage &out, const RawSta
             m += __shfl_xor_sync(0xffffffffu, m, off);
         }
         p *= scale;
-        big = big || !(fabsf(p) <= 16384.f);
+        big = big || !(fabsf(p) * f <= 16384.f);
         if (lane == 0) {
-            put_p(out, sm.pt[buf], r, s, p);
+            put_p(out, sm.pt[buf], r, s, p, f);
             if (s < r) {
-                put_p(out, sm.pt[buf], s, r, 0.f);
+                put_p(out, sm.pt[buf], s, r, 0.f, f);
                 sm.a2[buf][s][r] = m * beta[s];
                 sm.a1[buf][s][r] = m * beta[r];
             }
@@ -304,25 +310,33 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
                     cp_async_commit();
                 }
                 int calm = kCalm;  // steps in a row that were mild
+                Scales sc(a.scale);
                 for (int i = 0; i < steps; ++i) {
                     const int st = i % kStages;
                     Stage &out = sm.stage[st];
                     cp_async_wait_newest<1>();
                     // the consumers are done with this stage's previous step (and its inputs)
                     if (i >= kStages) bar_sync(BAR_EMPTY + st, kHalf + 32 * NW);
-                    bar_sync(BAR_PREP, kHalf);
                     const RawStage &raw = sm.raw[i % kRaw];
+                    const bool try_mild = calm >= kCalm;
+                    if (!try_mild) find_largest(raw, out.pl, tid);
+                    bar_sync(BAR_PREP, kHalf);
                     int form = GENERAL;
-                    if (calm >= kCalm &&
-                        !bar_or(BAR_PREP, kHalf, !prepare_mild(raw, out.pl, a.scale, tid)))
+                    if (try_mild &&
+                        !bar_or(BAR_PREP, kHalf, !prepare_mild(raw, out.pl, sc, tid)))
                         form = MILD;
                     if (form != MILD) {
-                        bool mild;
-                        const bool strong = prepare<true>(raw, out.pl, out.g, a.scale, tid, &mild);
-                        if (bar_or(BAR_PREP, kHalf, strong)) form = STRONG;
-                        calm = bar_or(BAR_PREP, kHalf, !mild) ? 0 : calm + 1;
+                        if (!sc.fit(out.pl)) sc.follow(out.pl, a.scale);
+                        const Seen f = prepare<kUp, 0>(raw, out.pl, out.g, sc, tid);
+                        if (bar_or(BAR_PREP, kHalf, f.strong)) form = STRONG;
+                        const bool calm_now = f.mild && sc.fit_all(out.pl);
+                        calm = bar_or(BAR_PREP, kHalf, !calm_now) ? 0 : calm + 1;
                     }
-                    if (tid == 0) out.form = form;
+                    if (tid == 0) {
+                        out.pl.kinv = sc.kinv;
+                        out.pl.qinv = sc.qinv;
+                        out.form = form;
+                    }
                     bar_arrive(BAR_PLANES + st, 2 * kHalf);
                     if (i + 2 < steps) in.load(sm, a, i + 2);
                     cp_async_commit();
@@ -373,8 +387,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
                     const int *big = sm.big[w];
                     out.pl.bmax = bm;
                     out.pl.careful = big[0] || big[1] || big[2] || big[3] || !finite(bm) ||
-                                     !(largest(out.pl.kmax) <= 16384.f) ||
-                                     !(fabsf(a.scale) * largest(out.pl.qmax) <= 16384.f);
+                                     !in_reach(out.pl, a.scale);
                 }
                 if (SAVE || lane < 16) solve(sm, out, w, tiles, lane);
                 __syncwarp();
@@ -409,7 +422,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         const Stage &in = sm.stage[st];
         const float *beta = sm.beta[slot];
         const uint32_t kw = smem_u32(in.pl.kw), qw = smem_u32(in.pl.qw), kd = smem_u32(in.pl.kd);
-        const float kmax = largest(in.pl.kmax);
+        const float kinv = in.pl.kinv, qinv = in.pl.qinv, ktop = largest(in.pl.kmax);
         const bool keep = SAVE && i % 4 == 0;
         bool careful = chunk::uniform(in.pl.careful);
         if (chunk::uniform(S.bound > kLimit)) S.renew();
@@ -437,7 +450,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
             store_tile(a.ckpt + unit_at * kCkptBytes, S, tile0, lane);
         const bool mild = chunk::uniform(in.form == MILD);
         const float ckpt_scale = S.saved_scale();  // of the state as an operand
-        const float inv = mild ? S.inv * (1.f / (1 << kMildUp)) : S.inv;  // with that of kw and qw
+        const float inv = S.inv * (1.f / (1 << kUp));
         // R = v - kw S and e = T2 R; blocks (tokens 0-7, dv 0-7), (0-7, 8-15), (8-15, ..)
         uint32_t vr[4], x0[4], x1[4];
         ldsm4t(vr, smem_u32(sm.v[slot]) + plane_off(lrow, role.consumer * 2 + lcol));
@@ -445,10 +458,11 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const float2 x = bf2(vr[2 * j]), y = bf2(vr[2 * j + 1]);
-            R[j][0] = fmaf(xw[j][0], -inv, x.x);
-            R[j][1] = fmaf(xw[j][1], -inv, x.y);
-            R[j][2] = fmaf(xw[j][2], -inv, y.x);
-            R[j][3] = fmaf(xw[j][3], -inv, y.y);
+            const float back = -inv * kinv;
+            R[j][0] = fmaf(xw[j][0], back, x.x);
+            R[j][1] = fmaf(xw[j][1], back, x.y);
+            R[j][2] = fmaf(xw[j][2], back, y.x);
+            R[j][3] = fmaf(xw[j][3], back, y.y);
         }
         tf_frag(R[0], x0);
         tf_frag(R[1], x1);
@@ -457,11 +471,11 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         careful = careful || !finite(em);
         const float bm = in.pl.bmax;
         if (!chunk::uniform(careful)) {
-            // n = beta e, 2^4 times as large where the key plane is 2^-4 times
-            const float more = mild ? (float)(1 << kMildDown) : 1.f;
+            // n = beta e with the inverse of the key plane's power of two
             const float less = mild ? 1.f / (1 << kMildDown) : 1.f;
+            const float more = (mild ? (float)(1 << kMildDown) : 1.f) * kinv;
             uint32_t nf[4];
-            const float ratio = join_scale(S, em * bm * more, C * kmax * less);
+            const float ratio = join_scale(S, em * bm * more, em * bm * (C * ktop));
             const float c = S.c * more;
             nf[0] = pack_f16(e[0][0] * (b[0].x * c), e[0][1] * (b[0].y * c));
             nf[1] = pack_f16(e[0][2] * (b[0].x * c), e[0][3] * (b[0].y * c));
@@ -503,11 +517,11 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
             float po[2][4] = {};
             mma_f16(po[0], nf, pf[0], pf[1]);
             mma_f16(po[1], nf, pf[2], pf[3]);
-            const float p_inv = S.inv * less;
+            const float p_inv = S.inv * less * (qinv / 4.f), q_inv = inv * qinv;  // see p_scale()
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int p = 0; p < 4; ++p) xq[j][p] = fmaf(po[j][p], p_inv, xq[j][p] * inv);
+                for (int p = 0; p < 4; ++p) xq[j][p] = fmaf(po[j][p], p_inv, xq[j][p] * q_inv);
         } else {
             walk_tokens(S, xq, e, sm.raw[slot], beta, sm.v[slot], role.consumer * 16, a.scale,
                         lane);

@@ -74,6 +74,14 @@ def check_states(x, scale=None, do=None, ref=None, state_tol=STATE_TOL):
     assert rel(got[5], dS0) <= state_tol, rel(got[5], dS0)
 
 
+# ------------------------------------------------------------------------ ordinary inputs
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("lo", [-0.02, -0.5, -3.0, -8.0])
+@pytest.mark.parametrize("T", [40, 131])
+def test_errors_beside_the_rounding(T, lo, dtype):
+    check_train(make(T, 1, 2, dtype=dtype, lo=lo, seed=51))
+
+
 # ------------------------------------------------------------------------ scales
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("lo", [-0.5, -3.0, -40.0])
@@ -90,6 +98,55 @@ def test_a_negative_scale_in_packed_sequences():
 @pytest.mark.parametrize("dtype", [BF, HF])
 def test_a_negative_scale_with_states(dtype):
     check_states(make(70, 1, 2, dtype=dtype, seed=54), -0.25)
+
+
+# ------------------------------------------------------------------------ small inputs
+@pytest.mark.parametrize("lo", [-0.5, -3.0, -40.0])
+@pytest.mark.parametrize("scale", [1e-3, -1e-6, 1e-9])
+def test_small_scales(scale, lo):
+    x = make(100, 1, 2, lo=lo, seed=66)
+    check_train(x, scale)
+    check_states(x, scale)
+
+
+@pytest.mark.parametrize("lo", [-0.02, -3.0, -40.0])
+@pytest.mark.parametrize("power", [-5, -9, -13, -16, -30])
+@pytest.mark.parametrize("what", ["k", "q", "qk", "v"])
+def test_small_inputs(what, power, lo):
+    """BF16 training takes FP16 operands: their power of two follows the inputs."""
+    x = make(70, 1, 2, lo=lo, seed=55)
+    for n in what:
+        x[n] = x[n] * 2.0 ** power
+    check_train(x)
+
+
+@pytest.mark.parametrize("power", [-9, -16, -30])
+def test_small_gradients(power):
+    x = make(70, 1, 2, seed=56)
+    check_train(x, do=gradient_of(x) * 2.0 ** power)
+
+
+@pytest.mark.parametrize("what", ["k", "q"])
+def test_sizes_that_change_from_step_to_step(what):
+    """Each step's o is within the bound of its own size."""
+    x = make(16 * 7, 1, 2, lo=-0.1, seed=57)
+    for step, power in enumerate((0, -12, 3, -25, -7, 5, 0)):
+        x[what][:, 16 * step:16 * step + 16] *= 2.0 ** power
+    if what == "k":  # the correction of a large key stays a contraction
+        x["beta"] = x["beta"] * 2.0 ** -10
+    d = cuda(x)
+    o = kda.kda_chunk_fwd(*args(d), save=True)[0].cpu()
+    ref = forward64(x)[0]
+    for a in range(0, 16 * 7, 16):
+        close(a, o[:, a:a + 16], ref[:, a:a + 16], TRAIN)
+
+
+@pytest.mark.parametrize("lo", [-0.5, -40.0])
+def test_keys_and_queries_of_zero_in_whole_steps(lo):
+    x = make(80, 1, 2, lo=lo, seed=58)
+    x["k"][:, 16:32] = 0
+    x["q"][:, 48:64] = 0
+    check_train(x)
 
 
 # ------------------------------------------------------------------------ cleared channels
