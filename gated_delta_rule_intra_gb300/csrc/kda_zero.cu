@@ -24,7 +24,8 @@ __global__ void __launch_bounds__(256) kda_zero_rest_kernel(const ZeroArgs a) {
     long long tail = token(a.cu_seqlens[a.num_seqs]);
     tail = tail < lead ? lead : tail;
     for (int k = 0; k < a.count; ++k) {
-        if (a.row[k] % 16 == 0)
+        // 16 bytes at a time where rows begin on such boundaries (dbeta need not)
+        if (a.row[k] % 16 == 0 && (uintptr_t)a.out[k] % 16 == 0)
             clear<uint4>((char *)a.out[k], a.row[k], lead, tail, a.T);
         else
             clear<uint16_t>((char *)a.out[k], a.row[k], lead, tail, a.T);

@@ -391,8 +391,9 @@ kda_status_t kda_chunk_fwd(const void *q, const void *k, const void *v, const fl
 /*
  * Gradients of kda_chunk_fwd from dout [B, T, HV, 128] (dtype) and what it saved: dq, dk
  * [B, T, H, 128] (summed over the value heads of a q/k head), dv, dgate [B, T, HV, 128] and
- * dbeta [B, T, HV], all in dtype, rounded once from FP32 sums.  q, k, gate, beta, scale, HV
- * and cu_seqlens as given to the forward (zero_rest as there, for all five).  No atomics: the same inputs give the same bits.
+ * dbeta [B, T, HV], all in dtype, rounded once from FP32 sums; all 16-byte aligned but beta (4)
+ * and dbeta (2).  q, k, gate, beta, scale, HV and cu_seqlens as given to the forward (zero_rest
+ * as there, for all five).  No atomics: the same inputs give the same bits.
  *   d_final_state    gradient of the final state, [sequences, HV, 128, 128] fp32, NULL = zeros
  *   d_initial_state  gradient of the initial state, the same shape, written; NULL = not wanted
  *   saved            the forward's, read only (a backward may run again from it); saved_bytes

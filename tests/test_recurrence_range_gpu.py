@@ -2,10 +2,13 @@
 size, keys of zero under gates that clear their channel, keys and gates that are not finite, values
 near the type's limits under strong gates -- against the definition in 64 bits."""
 
+import ctypes
+
 import pytest
 import torch
 
 import gated_delta_rule_intra_gb300 as kda
+from gated_delta_rule_intra_gb300 import recurrence
 from tests._recurrence import (EXTRA, F64, GRADS, NAMES, STATE_TOL, cu, cuda, forward64,
                                gradients64, make, rel, states)
 
@@ -198,3 +201,31 @@ def test_what_is_not_finite_reaches_no_earlier_token(value, what, dtype, state):
     assert torch.equal(o[1], clean[1]) and torch.equal(o[0, :, 0], clean[0, :, 0])
     assert rel(o[0, :21, 1], ref[0, :21, 1]) <= 2.0 ** -8 + EXTRA
     assert not torch.isfinite(o[0, 21, 1]).all()
+
+
+# ------------------------------------------------------------------------ zeros
+@pytest.mark.parametrize("HV", [8, 3])
+def test_zeros_in_a_dbeta_on_any_two_byte_boundary(HV):
+    """The C entry takes dbeta on a 2-byte boundary; rows of 8 heads are 16 bytes long."""
+    x = cuda(make(50, 1, HV, seed=67))
+    c = cu([20, 13], start=5)
+    _, _, saved = kda.kda_chunk_fwd(*args(x), cu_seqlens=c, save=True)
+    want = kda.kda_chunk_bwd(*args(x), x["v"], saved, cu_seqlens=c)[:5]
+    q, k, v, gate, beta = args(x)
+    out = [torch.full_like(t, 7.0) for t in want]
+    room = torch.full((50 * HV + 3,), 7.0, dtype=BF, device="cuda")
+    dbeta = room[1:-2]
+    assert dbeta.data_ptr() % 16 == 2
+    lib = kda.load_library()
+    size = lib.kda_chunk_bwd_workspace_bytes(1, 50, 1, HV, 2, 0, saved.numel())
+    work = torch.empty(size, dtype=torch.uint8, device="cuda")
+    op = recurrence.ChunkBwdOpts(HV=HV, cu_seqlens=c.data_ptr(), num_seqs=2, zero_rest=1,
+                                 saved=saved.data_ptr(), saved_bytes=saved.numel(),
+                                 workspace=work.data_ptr(), workspace_bytes=size)
+    rc = lib.kda_chunk_bwd(q.data_ptr(), k.data_ptr(), gate.data_ptr(), beta.data_ptr(),
+                           v.data_ptr(), *[t.data_ptr() for t in out[:4]], dbeta.data_ptr(), 1, 50,
+                           1, 0, ctypes.addressof(op), torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    for a, b in zip((*out[:4], dbeta.view_as(want[4])), want):
+        assert torch.equal(a, b)
+    assert room[0] == 7 and (room[-2:] == 7).all()
