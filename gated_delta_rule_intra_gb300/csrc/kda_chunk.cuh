@@ -366,15 +366,18 @@ __device__ __forceinline__ bool prep_planes(const RawStage &raw, char *planes, f
         const float2 x = *reinterpret_cast<const float2 *>(&raw.gate[r][2 * c2]);
         return make_float2(floor_gate(x.x), floor_gate(x.y));
     };
-    float2 g = make_float2(0.f, 0.f), ref = g;
-    if (FROM_START) {
+    // g, and g_l - g as a sum of its own: gates of -160 add up to -2560, where FP32 has steps of 2^-12
+    float2 g = make_float2(0.f, 0.f), tail[kRows];
 #pragma unroll 8
-        for (int r = 0; r < r0; ++r) g = add2(g, gate(r));
-    } else {
+    for (int r = 0; r < r0; ++r) g = add2(g, gate(r));
+    if (!FROM_START) {
+        float2 after = make_float2(0.f, 0.f);
+#pragma unroll 8
+        for (int r = C - 1; r >= r0 + kRows; --r) after = add2(after, gate(r));
 #pragma unroll
-        for (int r = 0; r < C; ++r) {
-            if (r == r0) g = ref;
-            ref = add2(ref, gate(r));
+        for (int i = kRows - 1; i >= 0; --i) {
+            tail[i] = after;
+            after = add2(after, gate(r0 + i));
         }
     }
     float big = 0.f;
@@ -382,10 +385,11 @@ __device__ __forceinline__ bool prep_planes(const RawStage &raw, char *planes, f
     for (int i = 0; i < kRows; ++i) {
         const int r = r0 + i;
         g = add2(g, gate(r));
+        if (FROM_START) tail[i] = make_float2(-g.x, -g.y);
         const float2 q = unpack2<T16>(*reinterpret_cast<const uint32_t *>(&raw.q[r][2 * c2]));
         const float2 k = unpack2<T16>(*reinterpret_cast<const uint32_t *>(&raw.k[r][2 * c2]));
         const float2 up = make_float2(ex2(g.x), ex2(g.y));
-        const float2 dn = make_float2(ex2(ref.x - g.x), ex2(ref.y - g.y));
+        const float2 dn = make_float2(ex2(tail[i].x), ex2(tail[i].y));
         const uint32_t off = plane_off(r, c2 >> 2) + (c2 & 3) * 4;
         const float2 kw = mul2(k, up), kd = mul2(k, dn);
         const float2 qw = mul2(mul2(q, make_float2(scale, scale)), up);

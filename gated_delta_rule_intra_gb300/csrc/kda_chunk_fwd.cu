@@ -127,17 +127,10 @@ __device__ __forceinline__ void scores(Smem &sm, Prepared &out, const float *bet
 }
 
 // Gates so strong that k 2^-g leaves FP32's range inside a step (a channel loses more than
-// 2^-96 or so in 16 tokens), or keys and gates that are not finite: the key plane in its bounded form, the gate replaced by its cumsum ...
-template <typename T16, int NT>
-__device__ __forceinline__ void prep_strong(RawStage &raw, Prepared &out, float scale, int tid) {
-    prep_planes<T16, NT, false>(raw, out.planes, out.decay, scale, tid);
-    bar_sync(BAR_PREP, NT);
-    float acc = 0.f;
-    for (int r = tid < D ? 0 : C; r < C; ++r) raw.gate[r][tid] = acc += floor_gate(raw.gate[r][tid]);
-}
-
-// ... and M and P pair by pair, one exp2 per (r, s, channel), every exponent <= 0: 17 pairs of
-// the rows w and 15 - w a call.  Lane l holds channels 4l .. 4l + 3.
+// 2^-96 or so in 16 tokens), or keys and gates that are not finite: the key plane is taken
+// in its bounded form, and M and P pair by pair, one exp2 per (r, s, channel), every exponent <= 0
+// and summed from the pair's own gates.  17 pairs of the rows w and 15 - w a call, each row's from its diagonal on.  Lane l holds
+// channels 4l .. 4l + 3.
 template <typename T16>
 __device__ __forceinline__ void scores_strong(Smem &sm, const RawStage &raw, const float *beta,
                                               Prepared &out, int buf, float scale, int w,
@@ -147,17 +140,20 @@ __device__ __forceinline__ void scores_strong(Smem &sm, const RawStage &raw, con
         const float2 lo = unpack2<T16>(u.x), hi = unpack2<T16>(u.y);
         x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
     };
+    float4 d = make_float4(0.f, 0.f, 0.f, 0.f);  // the gates behind s up to r
 #pragma unroll 1
     for (int j = 0; j < 17; ++j) {
-        const int r = j <= w ? w : C - 1 - w, s = j <= w ? j : j - w - 1;
+        const int r = j <= w ? w : C - 1 - w, s = j <= w ? w - j : C - j;
         float q[4], k[4], ks[4];
         row4(raw.q[r], q);
         row4(raw.k[r], k);
         row4(raw.k[s], ks);
-        const float4 gr = *reinterpret_cast<const float4 *>(&raw.gate[r][4 * lane]);
-        const float4 gs = *reinterpret_cast<const float4 *>(&raw.gate[s][4 * lane]);
-        const float e[4] = {ex2(gr.x - gs.x) * ks[0], ex2(gr.y - gs.y) * ks[1],
-                            ex2(gr.z - gs.z) * ks[2], ex2(gr.w - gs.w) * ks[3]};
+        if (s == r) d = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float e[4] = {ex2(d.x) * ks[0], ex2(d.y) * ks[1], ex2(d.z) * ks[2],
+                            ex2(d.w) * ks[3]};
+        const float4 g = *reinterpret_cast<const float4 *>(&raw.gate[s][4 * lane]);
+        d.x += floor_gate(g.x); d.y += floor_gate(g.y);
+        d.z += floor_gate(g.z); d.w += floor_gate(g.w);
         float p = 0.f, m = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -463,7 +459,7 @@ __global__ void __launch_bounds__(Roles<NW, KS>::kThreads, 1)
             for (int i = 0; i < steps; ++i) {
                 const int st = i % kStages;
                 Prepared &out = sm.prep[st];
-                RawStage &raw = sm.raw[i % kRaw];
+                const RawStage &raw = sm.raw[i % kRaw];
                 cp_wait<1>();
                 // the consumers are done with this stage's previous step (and its values)
                 if (i >= kStages) bar_sync(BAR_EMPTY + st, kPrep + 32 * NW);
@@ -471,7 +467,8 @@ __global__ void __launch_bounds__(Roles<NW, KS>::kThreads, 1)
                 const bool big =
                     prep_planes<T16, kPrep, true>(raw, out.planes, out.decay, a.scale, tid);
                 const bool strong = bar_or(BAR_PREP, kPrep, big);
-                if (strong) prep_strong<T16, kPrep>(raw, out, a.scale, tid);
+                if (strong)
+                    prep_planes<T16, kPrep, false>(raw, out.planes, out.decay, a.scale, tid);
                 if (tid == 0) out.from_start = !strong;
                 bar_arrive(BAR_PLANES + st, kPrep + kHalf);
                 if (i + 2 < steps) load_step<kSlice, kPrep>(sm, a, sq, h, hv, dv0, i + 2, tid);

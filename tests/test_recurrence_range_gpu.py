@@ -159,6 +159,32 @@ def cleared(x, mask, gate):
             dict(x, gate=x["gate"].masked_fill(mask, -5000.0)))
 
 
+LOWEST = [float("-inf"), torch.finfo(torch.float32).min, -1e4, -200.0]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("gate", LOWEST)
+@pytest.mark.parametrize("share", [0.2, 0.75])
+def test_cleared_channels(share, gate, dtype):
+    """That share of all gates clears its channel, and one token every channel."""
+    x = make(40, 1, 2, dtype=dtype, seed=59)
+    drop = torch.rand(x["gate"].shape, generator=torch.Generator().manual_seed(8)) < share
+    drop[:, 20] = True
+    low, ref = cleared(x, drop, gate)
+    check_states(low, ref=ref)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("gate", LOWEST)
+@pytest.mark.parametrize("share", [0.2, 0.75])
+def test_cleared_channels_in_training(share, gate, dtype):
+    x = make(40, 1, 2, dtype=dtype, seed=60)
+    drop = torch.rand(x["gate"].shape, generator=torch.Generator().manual_seed(8)) < share
+    drop[:, 20] = True
+    low, ref = cleared(x, drop, gate)
+    check_train(low, ref=ref)
+
+
 def zero_keys(case, dtype):
     x = make(40, 1, 2, dtype=dtype, seed=61)
     drop = torch.zeros(x["gate"].shape, dtype=torch.bool)
@@ -184,6 +210,20 @@ def test_keys_of_zero_where_a_channel_is_cleared(case, dtype):
     x, ref = zero_keys(case, dtype)
     check_states(x, ref=ref)
     check_train(x, ref=ref)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("T,at,n", [(16, 0, 12), (16, 0, 10), (32, 18, 11), (40, 5, 12)])
+def test_ordinary_gates_behind_a_run_of_cleared_tokens(T, at, n, dtype):
+    """Tokens in a row that clear every channel, or lose 2^-100 each, and a few ordinary ones to the
+    end of the step."""
+    x = make(T, 1, 2, dtype=dtype, lo=-0.3, seed=65)
+    drop = torch.zeros(x["gate"].shape, dtype=torch.bool)
+    drop[:, at:at + n] = True
+    low, ref = cleared(x, drop, float("-inf"))
+    check_states(low, ref=ref)
+    x["gate"][:, at:at + n] -= 100.0
+    check_states(x)
 
 
 # ------------------------------------------------------------------------ not finite
