@@ -450,6 +450,10 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
                 big = fmaxf(big, -gl[i]);
             }
             const bool strong = __any_sync(0xffffffffu, big > 96.f);
+            // the keys' factors from the middle of the step's decay on: 2^-g itself reaches 2^96,
+            // beside which large values would leave FP32's range
+            const float mid[2] = {strong ? 0.f : 0.5f * gl[0], strong ? 0.f : 0.5f * gl[1]};
+            const float m0 = ex2(mid[0]), m1 = ex2(mid[1]);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -457,12 +461,20 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
                     const int t = j * C + token_of(p, tc2);
                     g.v[i][p] = sm.g[t][c0 + gr + 8 * i];
                     kd.v[i][p] = sm.beta[t] * k.v[i][p] *
-                                 ex2((strong ? gl[i] : 0.f) - g.v[i][p]);
+                                 ex2((strong ? gl[i] : mid[i]) - g.v[i][p]);
                 }
             uint32_t ah[4], al[4];
             split_elems(kd, ah, al);
             if (!strong) {
                 uint32_t bh[4], bl[4];
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        cq[x][p] *= p < 2 ? m0 : m1;
+                        cy[x][p] *= p < 2 ? m0 : m1;
+                    }
+                decay_rows(S, m0, m1);
                 ldsm4(bh, tc::smem_u32(sm.g1[j]) + tn);
                 ldsm4(bl, tc::smem_u32(sm.g1[j]) + kTile + tn);
                 mma3(cq[0], cq[1], ah, al, bh, bl);
@@ -470,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
                 ldsm4(bl, tc::smem_u32(sm.g2[j]) + kTile + tn);
                 mma3(cy[0], cy[1], ah, al, bh, bl);
                 add_rows(S, ah, al, se, j, lane);
-                decay_rows(S, ex2(gl[0]), ex2(gl[1]));
+                decay_rows(S, ex2(gl[0] - mid[0]), ex2(gl[1] - mid[1]));
             } else {
                 decay_rows(S, ex2(gl[0]), ex2(gl[1]));
                 add_rows(S, ah, al, se, j, lane);
@@ -480,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    const float up = ex2(g.v[i][p]);
+                    const float up = ex2(g.v[i][p] - mid[i]);
                     dq.v[i][p] = a.scale * up * cq[p >> 1][2 * i + (p & 1)];
                     dk.v[i][p] = -sm.beta[j * C + token_of(p, tc2)] * up *
                                  cy[p >> 1][2 * i + (p & 1)];

@@ -257,6 +257,22 @@ __device__ __forceinline__ void mma_causal(float (&acc)[2][4], const float (&x)[
     }
 }
 
+template <int NJ>
+__device__ __forceinline__ void scale_all(float (&S)[NJ][4], float (&n)[2][4], float (&o)[2][4],
+                                          float f) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int p = 0; p < 4; ++p) S[j][p] *= f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            n[j][p] *= f;
+            o[j][p] *= f;
+        }
+}
+
 // One step of a consumer warp's 16 columns of dv: e and o (xq) of its tokens, S updated.
 // With KS = 2 the warp has the half `kh` of dk: sums over dk are joined with the partner's in
 // shared memory, both warps have e, and o is finished for the tokens 8 kh .. 8 kh + 7.
@@ -361,11 +377,17 @@ __device__ __forceinline__ void consume(float (&S)[16 / KS][4], float (&xq)[2][4
 #pragma unroll
             for (int p = 0; p < 4; ++p) e[j][p] += e2[j][p] + e3[j][p];
     }
-    float nb[2][4];  // n = beta e
+    float nb[2][4], most = 0.f;  // n = beta e
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int p = 0; p < 4; ++p) nb[j][p] = e[j][p] * (p & 1 ? b[j].y : b[j].x);
+        for (int p = 0; p < 4; ++p) {
+            nb[j][p] = e[j][p] * (p & 1 ? b[j].y : b[j].x);
+            most = fmaxf(most, fabsf(nb[j][p]));
+        }
+    // the key plane reaches 2^96: beside n of this size the sums would leave FP32's range
+    const bool large = __any_sync(0xffffffffu, most > 0x1p24f);
+    if (large) scale_all(S, nb, xq, 0x1p-72f);
     split_frag(nb[0], nb[1], nh, nl);
     if (CAREFUL) mma_causal(xq, nb, tc::smem_u32(in.p), tc::smem_u32(in.p) + kTile, lane);
     // S' = 2^g_l (S + (k 2^-g)^T n), or with strong gates 2^g_l S + (k 2^(g_l - g))^T n
@@ -404,6 +426,7 @@ __device__ __forceinline__ void consume(float (&S)[16 / KS][4], float (&xq)[2][4
 #pragma unroll
         for (int jj = 0; jj < 8 / KS; ++jj) decay_cols(S, in.decay + 16 * k0, jj, tc2);
     }
+    if (large) scale_all(S, nb, xq, 0x1p72f);
 }
 
 // NW consumer warps, KS for each 16 columns of dv: a head takes 8 KS / NW CTAs.  Four of these

@@ -523,6 +523,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
                 big = fmaxf(big, -gl[i]);
             }
             const bool strong = __any_sync(0xffffffffu, big > 96.f);
+            // the pairs' factors from the middle of the step's decay on: 2^-g itself reaches 2^96,
+            // beside which large values would leave FP32's range
+            const float mid[2] = {strong ? 0.f : 0.5f * gl[0], strong ? 0.f : 0.5f * gl[1]};
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -530,16 +533,17 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
                     const int t = j * C + token_of(p, tc2);
                     g.v[i][p] = sm.g[t][c0 + gr + 8 * i];
                     const float x = sm.beta[t] * k.v[i][p];
-                    kb.v[i][p] = x * ex2(-g.v[i][p]);
+                    kb.v[i][p] = x * ex2(mid[i] - g.v[i][p]);
                     kd.v[i][p] = x * ex2(gl[i] - g.v[i][p]);
                 }
+            const float m0 = ex2(mid[0]), m1 = ex2(mid[1]);
             const float fq = inverse_of(cS) * inverse_of(cj), fy = inverse_of(cS) * inverse_of(yj);
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    cq[x][p] *= fq;
-                    cyy[x][p] *= fy;
+                    cq[x][p] *= fq * (p < 2 ? m0 : m1);
+                    cyy[x][p] *= fy * (p < 2 ? m0 : m1);
                 }
             if (!strong) {
                 uint32_t ah[4], al[4], bh[4], bl[4], ch[4], cl[4];
@@ -567,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    const float up = ex2(g.v[i][p]);
+                    const float up = ex2(g.v[i][p] - mid[i]);
                     dq.v[i][p] = a.scale * up * cq[p >> 1][2 * i + (p & 1)];
                     dk.v[i][p] = -sm.beta[j * C + token_of(p, tc2)] * up *
                                  cyy[p >> 1][2 * i + (p & 1)];

@@ -243,6 +243,17 @@ def test_what_is_not_finite_reaches_no_earlier_token(value, what, dtype, state):
     assert not torch.isfinite(o[0, 21, 1]).all()
 
 
+# ------------------------------------------------------------------------ large values
+@pytest.mark.parametrize("power", [20, 40, 60])
+def test_large_values_under_strong_gates(power):
+    """A channel loses 2^-90 in a step, 2^90 times the values is out of FP32's range."""
+    x = make(70, 1, 2, seed=63)
+    x["gate"] = -5.6 - 0.05 * x["gate"].abs()
+    x["v"] = x["v"] * 2.0 ** power
+    check_train(x)
+    check_states(x)
+
+
 # ------------------------------------------------------------------------ zeros
 @pytest.mark.parametrize("HV", [8, 3])
 def test_zeros_in_a_dbeta_on_any_two_byte_boundary(HV):
