@@ -5,6 +5,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import sys
+import warnings
 
 import torch
 
@@ -91,15 +92,20 @@ def declare(lib):
 
 def _declare_quick(lib):
     """The short way in (csrc/binding.cpp) as lib.quick_<name>: functions that return None for
-    arguments that need the checks here."""
-    try:
-        from . import _native
-    except ImportError as e:
-        raise RuntimeError("_native.so is missing or of another torch: build it with "
-                           "gated_delta_rule_intra_gb300.build.build_library()") from e
+    arguments that need the checks here.  Without _native.so every call goes that way: it takes
+    longer (10 us of a small call), and the intra-chunk calls need nothing of it."""
 
     def address(name):
         return ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+
+    try:
+        from . import _native
+    except ImportError as e:
+        def quick(name, fns, why=str(e)):
+            return lambda *args: _without_native(why)
+    else:
+        def quick(name, fns):
+            return functools.partial(getattr(_native, name), *[address(f) for f in fns])
 
     for name, fns in (
             ("step", ("kda_step",)),
@@ -108,5 +114,11 @@ def _declare_quick(lib):
                            "kda_chunk_bwd_workspace_bytes")),
             ("layer_norm_fwd", ("kda_layer_norm_fwd",)),
             ("layer_norm_bwd", ("kda_layer_norm_bwd", "kda_layer_norm_bwd_workspace_bytes"))):
-        setattr(lib, "quick_" + name,
-                functools.partial(getattr(_native, name), *[address(f) for f in fns]))
+        setattr(lib, "quick_" + name, quick(name, fns))
+
+
+@functools.cache
+def _without_native(why):
+    warnings.warn("_native.so is missing or of another torch: small calls of the recurrence, the "
+                  "single-token form and layer norm take longer on the host; build it with "
+                  f"gated_delta_rule_intra_gb300.build.build_native() ({why})", RuntimeWarning)
