@@ -18,12 +18,26 @@ unsigned *debug_flags();
 
 namespace {
 
+// Bytes that a call reads or writes: one run, or rows of `row` bytes `step` apart.
 struct Range {
-    uintptr_t lo, hi;
-    Range(const void *p, size_t bytes) : lo((uintptr_t)p), hi(p ? (uintptr_t)p + bytes : 0) {}
+    uintptr_t lo, hi, row, step;
+    Range(const void *p, size_t bytes)
+        : lo((uintptr_t)p), hi(p ? (uintptr_t)p + bytes : 0), row(bytes), step(bytes) {}
+    Range(const void *p, long long rows, int width, long long stride, int es)
+        : Range(p, rows ? ((size_t)(rows - 1) * stride + width) * es : 0) {
+        row = (size_t)width * es;
+        step = (size_t)stride * es;
+    }
 };
 
-bool meet(const Range &a, const Range &b) { return a.lo < b.hi && b.lo < a.hi; }
+bool meet(const Range &a, const Range &b) {
+    if (!(a.lo < b.hi && b.lo < a.hi)) return false;
+    if (a.step != b.step) return true;
+    // rows equally far apart may lie between each other's (column slices of one buffer)
+    const uintptr_t off = b.lo >= a.lo ? (b.lo - a.lo) % a.step
+                                       : (a.step - (a.lo - b.lo) % a.step) % a.step;
+    return !(off >= a.row && off + b.row <= a.step);
+}
 
 // Every output against every input and every other output.
 template <size_t NO, size_t NI> bool overlap(const Range (&out)[NO], const Range (&in)[NI]) {
@@ -283,11 +297,6 @@ static kda_status_t check_norm(long long rows, int width, int dtype, int wdtype)
     return KDA_OK;
 }
 
-// Bytes from a [rows, width] tensor's first element to behind its last.
-static size_t span(long long rows, int width, long long stride, int es) {
-    return rows ? ((size_t)(rows - 1) * stride + width) * es : 0;
-}
-
 kda_status_t kda_layer_norm_fwd(const void *x, const void *weight, const void *bias, void *y,
                                 float *mean, float *rstd, long long rows, int width, float eps,
                                 int dtype, int wdtype, long long x_stride, long long y_stride,
@@ -301,9 +310,9 @@ kda_status_t kda_layer_norm_fwd(const void *x, const void *weight, const void *b
     const int es = dtype == KDA_FP32 ? 4 : 2, ws = wdtype == KDA_FP32 ? 4 : 2;
     const void *ae[] = {x, y}, *aw[] = {weight, bias}, *a4[] = {mean, rstd};
     if (misaligned(ae, es) || misaligned(aw, ws) || misaligned(a4, 4)) return KDA_ERR_ALIGN;
-    const Range in[] = {{x, span(rows, width, x_stride, es)}, {weight, (size_t)width * ws},
+    const Range in[] = {{x, rows, width, x_stride, es}, {weight, (size_t)width * ws},
                         {bias, (size_t)width * ws}};
-    const Range out[] = {{y, span(rows, width, y_stride, es)}, {mean, (size_t)rows * 4},
+    const Range out[] = {{y, rows, width, y_stride, es}, {mean, (size_t)rows * 4},
                          {rstd, (size_t)rows * 4}};
     if (overlap(out, in)) return KDA_ERR_OVERLAP;
     if ((st = kda::require_device()) != KDA_OK) return st;
@@ -342,10 +351,10 @@ kda_status_t kda_layer_norm_bwd(const void *dy, const void *x, const void *weigh
         return KDA_ERR_ALIGN;
     const size_t need = dweight ? kda_layer_norm_bwd_workspace_bytes(rows, width) : 0;
     if (need && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
-    const Range in[] = {{dy, span(rows, width, dy_stride, es)},
-                        {x, span(rows, width, x_stride, es)}, {weight, (size_t)width * ws},
+    const Range in[] = {{dy, rows, width, dy_stride, es}, {x, rows, width, x_stride, es},
+                        {weight, (size_t)width * ws},
                         {mean, (size_t)rows * 4}, {rstd, (size_t)rows * 4}};
-    const Range out[] = {{dx, span(rows, width, dx_stride, es)}, {dweight, (size_t)width * 4},
+    const Range out[] = {{dx, rows, width, dx_stride, es}, {dweight, (size_t)width * 4},
                          {dbias, (size_t)width * 4}, {need ? workspace : nullptr, need}};
     if (overlap(out, in)) return KDA_ERR_OVERLAP;
     if ((st = kda::require_device()) != KDA_OK) return st;

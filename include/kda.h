@@ -449,7 +449,8 @@ kda_status_t kda_step(const void *q, const void *k, const void *v, const float *
  * x, y, dy and dx have one type (KDA_BF16, KDA_FP16 or KDA_FP32) and a row stride each, in
  * elements (0 = width); weight and bias have `wdtype`, which is the same type or KDA_FP32, and
  * may be NULL (ones, zeros).  mean and rstd [rows] fp32 are what the backward needs (NULL =
- * not wanted).  Statistics, sums and gradients of weight and bias are FP32.  Pointers need
+ * not wanted).  y and dx must not overlap the inputs; column slices of one buffer may lie side by
+ * side.  Statistics, sums and gradients of weight and bias are FP32.  Pointers need
  * their element's alignment; rows on 16-byte boundaries are read and written 16 bytes at a
  * time, others element by element.
  *
