@@ -197,6 +197,16 @@ __device__ __forceinline__ Where locate(const ChunkBwdArgs &a, unsigned u) {
     return w;
 }
 
+// The debug build's checks: a token of the inputs, and a head's state from element `at` on (its last
+// 16 rows lie behind that in any split).
+template <class Args> __device__ __forceinline__ bool token_ok(const Args &a, long long token) {
+    return dbg_ok(a.dbg, (size_t)token, a.rows_o / a.HV, DBG_LOAD);
+}
+template <class Args>
+__device__ __forceinline__ bool state_ok(const Args &a, const void *p, size_t at, unsigned bit) {
+    return !p || dbg_ok(a.dbg, at / (D * D) * (D * D) + D * D - 1, a.states, bit);
+}
+
 // Asks a unit's rows of q, k and do (two lines each) and of the gate (four) into L2.
 __device__ __forceinline__ void prefetch_rows(const ChunkBwdArgs &a, const Where &w, int tid,
                                               int threads) {

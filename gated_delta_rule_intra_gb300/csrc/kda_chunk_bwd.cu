@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
         }
         for (int i = tid; i < BT * 16; i += kThreads) {
             const int r = i >> 4, c = i & 15;
-            const bool ok = r < rows;
+            const bool ok = r < rows && token_ok(a, row0 + r);
             const size_t tok = (size_t)(row0 + (ok ? r : 0));
             cp16z(tc::smem_u32(&sm.q[r][c * 8]), (const uint16_t *)a.q + (tok * a.H + h) * D + c * 8,
                   ok);
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
 #pragma unroll
         for (int x = 0; x < 4; ++x) {  // do: eight rows at a time, whose pieces share no banks
             const int r = 16 * x + (warp >> 2) * 8 + (lane & 7), c = (warp & 3) * 4 + (lane >> 3);
-            const bool ok = r < rows;
+            const bool ok = r < rows && token_ok(a, row0 + r);
             char *to = sm.dout + ((r >> 3) * 16 + c) * 128 + (r & 7) * 16;
             const uint16_t *from = (const uint16_t *)a.dout +
                                    ((size_t)(row0 + (ok ? r : 0)) * a.HV + hv) * D + c * 8;
@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
                 *reinterpret_cast<uint4 *>(to + kRowPlane) = lo;
             }
         }
-        if (tid < BT) sm.beta[tid] = tid < rows ? a.beta[(size_t)(row0 + tid) * a.HV + hv] : 0.f;
+        if (tid < BT)
+            sm.beta[tid] = tid < rows && token_ok(a, row0 + tid) ? a.beta[(size_t)(row0 + tid) * a.HV + hv] : 0.f;
         cp_async_commit();
         float S[16][4];  // rows dk c0 + gr, + 8; columns dv 8j + tc2, + 1
         // 16 dv columns of a checkpoint (see store_checkpoint()): tiles 2x and 2x + 1 of S
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
                         const float d = r == s ? c[i][p] : c[i][p + 1];
                         if (warp < 4)
                             sm.diag[t] = d;
-                        else if (t < rows)
+                        else if (t < rows && token_ok(a, row0 + t))
                             ((uint16_t *)a.dbeta)[(size_t)(row0 + t) * a.HV + hv] = to16<T16>(d);
                     }
                 }
@@ -582,6 +583,8 @@ __global__ void __launch_bounds__(256) kda_chunk_bwd_heads_kernel(const ChunkBwd
         const long long t = (long long)tok;
         if (t < a.cu_seqlens[0] || t >= a.cu_seqlens[a.num_seqs]) return;
     }
+    const size_t last = (tok * a.HV + h * G + G - 1) * (D / 4) + c;
+    if (!dbg_ok(a.dbg, last, a.rows_o * (D / 4), DBG_LOAD) || !dbg_ok(a.dbg, e, n, DBG_STORE)) return;
     const float4 *from = reinterpret_cast<const float4 *>(second ? a.dk_hv : a.dq_hv) +
                          (tok * a.HV + h * G) * (D / 4) + c;
     float4 s = from[0];

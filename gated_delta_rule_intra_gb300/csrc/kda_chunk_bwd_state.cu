@@ -41,7 +41,7 @@ __device__ __forceinline__ void load_step(Smem &sm, const ChunkBwdArgs &a, const
                                           int hv, int dv0, int i, int step, int tid) {
     const int row = tid >> 4, c = tid & 15;
     const int t = step * C + row;
-    const bool ok = t < sq.len;
+    const bool ok = t < sq.len && token_ok(a, sq.row0 + t);
     const size_t tok = (size_t)sq.row0 + (ok ? t : 0);
     RawStage &raw = sm.raw[i % kRaw];
     const size_t iq = (tok * a.H + h) * D + c * 8, iv = (tok * a.HV + hv) * D;
@@ -53,12 +53,10 @@ __device__ __forceinline__ void load_step(Smem &sm, const ChunkBwdArgs &a, const
         cp16z(tc::smem_u32(sm.dout[i % kRing]) + plane_off(row, c),
               (const uint16_t *)a.dout + iv + dv0 + c * 8, ok);
     if (c == 0) cp4z(tc::smem_u32(&sm.beta[i % kRing][row]), a.beta + tok * a.HV + hv, ok);
-    if (tid < (int)kTilesBytes / 16)
+    const size_t unit_at = (size_t)(sq.slot0 + step / 4) * a.HV + hv;
+    if (tid < (int)kTilesBytes / 16 && dbg_ok(a.dbg, unit_at, a.units, DBG_LOAD))
         cp16z(tc::smem_u32(sm.tiles[i % kRing]) + tid * 16,
-              a.tiles +
-                  (((size_t)(sq.slot0 + step / 4) * a.HV + hv) * 4 + step % 4) * kTilesBytes +
-                  tid * 16,
-              true);
+              a.tiles + (unit_at * 4 + step % 4) * kTilesBytes + tid * 16, true);
 }
 
 // Four tiles += A B with A of the inputs: exact in BF16 (no lo part), split in two for FP16.
@@ -131,10 +129,12 @@ __global__ void __launch_bounds__(Roles<NC, 8, 0>::kThreads, 1)
     const int k0 = kh * (8 / KS);  // first 16 channels of dk
     const int gr = lane >> 2, tc2 = (lane & 3) * 2;
     const size_t sbase = ((size_t)n * a.HV + hv) * D * D + (size_t)k0 * 16 * D;
+    const bool states_in = state_ok(a, a.d_final_state, sbase, DBG_LOAD) &&
+                           state_ok(a, a.d_initial_state, sbase, DBG_STORE);
     float S[kJ][4];  // dS^T: rows dv d0 + gr, + 8; columns dk 8j + tc2, + 1 of its part
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
-        if (a.d_final_state) {
+        if (a.d_final_state && states_in) {
             const float *p = a.d_final_state + sbase + (size_t)(8 * j + tc2) * D + d0 + gr;
             S[j][0] = p[0];
             S[j][1] = p[D];
@@ -154,7 +154,9 @@ __global__ void __launch_bounds__(Roles<NC, 8, 0>::kThreads, 1)
     for (int i = 0; i < steps; ++i) {
         const int st = i & 1, step = steps - 1 - i;
         const unsigned slot = (unsigned)(sq.slot0 + step / 4) * a.HV + hv;
-        if (step % 4 == 3) store_checkpoint(a.dckpt + slot * kCkptBytes, S, d0 / 16, kh * kJ, lane);
+        const bool save = dbg_ok(a.dbg, slot, a.units, DBG_STORE);
+        if (save && step % 4 == 3)
+            store_checkpoint(a.dckpt + slot * kCkptBytes, S, d0 / 16, kh * kJ, lane);
         bar_sync(BAR_FULL + st, kPrepThreads + 32 * NC);
         const Prepared &in = sm.prep[st];
         const uint32_t pl = tc::smem_u32(in.planes);
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(Roles<NC, 8, 0>::kThreads, 1)
         if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kPrepThreads + 32 * NC);
         // Y and dv, eight tokens at a time
         auto put = [&](const float (&yj)[4], const float (&x)[4], int j) {
-            store_row_block(a.y + slot * kRowsBytes, yj, (step % 4) * C / 8 + j, d0, lane);
+            if (save) store_row_block(a.y + slot * kRowsBytes, yj, (step % 4) * C / 8 + j, d0, lane);
             const uint32_t u = movm_t(pack2<T16>(-x[0], -x[1]));
             const uint32_t w = movm_t(pack2<T16>(-x[2], -x[3]));
             const int t = step * C + 8 * j + gr;
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(Roles<NC, 8, 0>::kThreads, 1)
             put(yh, dh, kh);
         }
     }
-    if (a.d_initial_state) {
+    if (a.d_initial_state && states_in) {
 #pragma unroll
         for (int j = 0; j < kJ; ++j) {
             float *p = a.d_initial_state + sbase + (size_t)(8 * j + tc2) * D + d0 + gr;

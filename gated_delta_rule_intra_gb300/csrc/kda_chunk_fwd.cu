@@ -64,7 +64,7 @@ __device__ __forceinline__ void load_step(Smem &sm, const ChunkFwdArgs &a, const
 #pragma unroll
     for (int i = 0; i < C * 16 / NT; ++i) {
         const int row = (tid >> 4) + i * (NT / 16), t = step * C + row;
-        const bool ok = t < sq.len;
+        const bool ok = t < sq.len && token_ok(a, sq.row0 + t);
         const size_t tok = (size_t)sq.row0 + (ok ? t : 0);
         const size_t iq = (tok * a.H + h) * D + c * 8, iv = (tok * a.HV + hv) * D;
         cp16z(tc::smem_u32(&raw.q[row][c * 8]), (const uint16_t *)a.q + iq, ok);
@@ -129,8 +129,8 @@ __device__ __forceinline__ void scores(Smem &sm, Prepared &out, const float *bet
 // Gates so strong that k 2^-g leaves FP32's range inside a step (a channel loses more than
 // 2^-96 or so in 16 tokens), or keys and gates that are not finite: the key plane is taken
 // in its bounded form, and M and P pair by pair, one exp2 per (r, s, channel), every exponent <= 0
-// and summed from the pair's own gates.  17 pairs of the rows w and 15 - w a call, each row's from its diagonal on.  Lane l holds
-// channels 4l .. 4l + 3.
+// and summed from the pair's own gates.  17 pairs of the rows w and 15 - w a call, each row's from
+// its diagonal on.  Lane l holds channels 4l .. 4l + 3.
 template <typename T16>
 __device__ __forceinline__ void scores_strong(Smem &sm, const RawStage &raw, const float *beta,
                                               Prepared &out, int buf, float scale, int w,
@@ -434,11 +434,12 @@ __device__ __forceinline__ void consume(float (&S)[16 / KS][4], float (&xq)[2][4
 template <int NW, int KS> using Roles = chunk::Roles<NW, 4 * KS + 4, 4>;
 
 // Eight tokens of o and, for the backward, of e on their way out.
-template <typename T16, bool SAVE>
+template <typename T16>
 __device__ __forceinline__ void finish(const ChunkFwdArgs &a, const float (&o)[4],
-                                       const float (&e)[4], unsigned slot, int step, int j,
-                                       uint16_t *o_at, size_t orow, int len, int d0, int lane) {
-    if (SAVE) store_row_block(a.e + slot * kRowsBytes, e, (step % 4) * C / 8 + j, d0, lane);
+                                       const float (&e)[4], bool save, unsigned slot, int step,
+                                       int j, uint16_t *o_at, size_t orow, int len, int d0,
+                                       int lane) {
+    if (save) store_row_block(a.e + slot * kRowsBytes, e, (step % 4) * C / 8 + j, d0, lane);
     const uint32_t x = movm_t(pack2<T16>(o[0], o[1])), y = movm_t(pack2<T16>(o[2], o[3]));
     const int tok = step * C + 8 * j + (lane >> 2);
     uint16_t *at = o_at + (size_t)tok * orow + (lane & 3) * 2;
@@ -536,10 +537,10 @@ __global__ void __launch_bounds__(Roles<NW, KS>::kThreads, 1)
                 if (SAVE || lane < 16) solve(sm, out, st, lane);
                 __syncwarp();
                 bar_arrive(BAR_FULL + st, 32 + 32 * NW);
-                if (SAVE && dv0 == 0) {
-                    uint4 *to = reinterpret_cast<uint4 *>(
-                        a.tiles +
-                        (((size_t)(sq.slot0 + i / 4) * a.HV + hv) * 4 + i % 4) * kTilesBytes);
+                const size_t unit_at = (size_t)(sq.slot0 + i / 4) * a.HV + hv;
+                if (SAVE && dv0 == 0 && dbg_ok(a.dbg, unit_at, a.units, DBG_STORE)) {
+                    uint4 *to =
+                        reinterpret_cast<uint4 *>(a.tiles + (unit_at * 4 + i % 4) * kTilesBytes);
                     const uint4 *t = reinterpret_cast<const uint4 *>(sm.t[st]);
                     to[lane] = t[lane];
                     to[32 + lane] = t[32 + lane];
@@ -559,11 +560,13 @@ __global__ void __launch_bounds__(Roles<NW, KS>::kThreads, 1)
     const int cw = role.consumer, tile = cw / KS, d0 = dv0 + tile * 16, kh = cw % KS;
     const int gr = lane >> 2, tc2 = (lane & 3) * 2;
     const size_t sbase = ((size_t)n * a.HV + hv) * D * D + (size_t)kh * (D / KS) * D;
+    const bool states_in = state_ok(a, a.initial_state, sbase, DBG_LOAD) &&
+                           state_ok(a, a.final_state, sbase, DBG_STORE);
     float S[kJ][4];  // S^T: rows d0 + gr, + 8; columns dk 8j + tc2, + 1 of its part
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
         S[j][0] = S[j][1] = S[j][2] = S[j][3] = 0.f;
-        if (a.initial_state) {
+        if (a.initial_state && states_in) {
             const float *p =
                 a.initial_state + sbase + (size_t)(8 * j + tc2) * D + d0 + gr;
             S[j][0] = p[0];
@@ -590,7 +593,8 @@ __global__ void __launch_bounds__(Roles<NW, KS>::kThreads, 1)
             consume<T16, KS, decltype(with_care)::value, decltype(keep)::value>(
                 S, xq, e, in, v, beta, ckpt, dv0 / 16, tile, kh, sm.join[i & 1], cw, lane);
         };
-        const bool keep = SAVE && i % 4 == 0;
+        const bool save = SAVE && dbg_ok(a.dbg, slot, a.units, DBG_STORE);
+        const bool keep = save && i % 4 == 0;
         const bool careful = uniform(in.careful);
         if (!careful) {
             if (keep)
@@ -606,10 +610,10 @@ __global__ void __launch_bounds__(Roles<NW, KS>::kThreads, 1)
             float eh[4], oh[4];
             half_of(e, kh, eh);
             half_of(xq, kh && careful, oh);
-            finish<T16, SAVE>(a, oh, eh, slot, i, kh, o_at, orow, sq.len, d0, lane);
+            finish<T16>(a, oh, eh, save, slot, i, kh, o_at, orow, sq.len, d0, lane);
             continue;
         }
-        if (SAVE)
+        if (save)
             store_rows(a.e + slot * kRowsBytes, e, (i % 4) * C, d0, lane);
         uint32_t ow[4];
 #pragma unroll
@@ -620,7 +624,7 @@ __global__ void __launch_bounds__(Roles<NW, KS>::kThreads, 1)
         store_out(sm.out[cw], ow, (char *)(o_at + (size_t)i * C * orow), orow * 2,
                       sq.len - i * C, (char *)a.o, a.rows_o * D * 2, a.dbg, lane);
     }
-    if (a.final_state) {
+    if (a.final_state && states_in) {
 #pragma unroll
         for (int j = 0; j < kJ; ++j) {
             float *p = a.final_state + sbase + (size_t)(8 * j + tc2) * D + d0 + gr;

@@ -183,14 +183,14 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
         for (int x = 0; x < 4; ++x) {
             const int r = 16 * x + o_row;
             dor[x] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < rows)
+            if (r < rows && chunk::token_ok(a, row0 + r))
                 dor[x] = *reinterpret_cast<const uint4 *>(
                     (const uint16_t *)a.dout + ((size_t)(row0 + r) * a.HV + hv) * D + o_col * 8);
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
             const int r = (tid >> 4) + 16 * x, c = tid & 15;
-            const bool ok = r < rows;
+            const bool ok = r < rows && chunk::token_ok(a, row0 + r);
             const size_t tok = (size_t)(row0 + (ok ? r : 0));
             cp16z(smem_u32(&sm.q[r][c * 8]), (const uint16_t *)a.q + (tok * a.H + h) * D + c * 8, ok);
             cp16z(smem_u32(&sm.k[r][c * 8]), (const uint16_t *)a.k + (tok * a.H + h) * D + c * 8, ok);
@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
         const float es = a.scales[su * kScales + 8 + lane], ys = a.dscales[su * kScales + 8 + lane];
         const float cs = a.scales[su * kScales + (lane & 7)];
         const float ds = a.dscales[su * kScales + (lane & 7)];
-        if (tid < BT) sm.beta[tid] = tid < rows ? a.beta[(size_t)(row0 + tid) * a.HV + hv] : 0.f;
+        if (tid < BT)
+            sm.beta[tid] = tid < rows && chunk::token_ok(a, row0 + tid) ? a.beta[(size_t)(row0 + tid) * a.HV + hv] : 0.f;
         // a warp's 16 rows of a saved state: tile t of 16 dv columns is the word pair w of its
         // blocks; brought to the common scale `c` of the eight tiles
         float S[16][4];  // rows dk c0 + gr, + 8; columns dv 8j + tc2, + 1
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
                         const float d = r == s ? x : y;
                         if (warp < 4)
                             sm.diag[t] = d;
-                        else if (t < rows)
+                        else if (t < rows && chunk::token_ok(a, row0 + t))
                             ((uint16_t *)a.dbeta)[(size_t)(row0 + t) * a.HV + hv] =
                                 (uint16_t)(pack_bf16(d, 0.f) & 0xffffu);
                     }

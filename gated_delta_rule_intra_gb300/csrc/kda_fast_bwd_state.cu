@@ -46,7 +46,7 @@ __device__ __forceinline__ void load_step(Smem &sm, const ChunkBwdArgs &a, const
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int r = (tid >> 4) + 8 * x, t = step * C + r;
-        const bool ok = t < sq.len;
+        const bool ok = t < sq.len && chunk::token_ok(a, sq.row0 + t);
         const size_t tok = (size_t)sq.row0 + (ok ? t : 0);
         const size_t iq = (tok * a.H + h) * D + c * 8, iv = (tok * a.HV + hv) * D;
         cp16z(smem_u32(&raw.q[r][c * 8]), (const uint16_t *)a.q + iq, ok);
@@ -58,10 +58,10 @@ __device__ __forceinline__ void load_step(Smem &sm, const ChunkBwdArgs &a, const
                   (const uint16_t *)a.dout + iv + dv0 + c * 8, ok);
         if (c == 0) chunk::cp4z(smem_u32(&sm.beta[slot][r]), a.beta + tok * a.HV + hv, ok);
     }
-    cp16z(smem_u32(sm.tiles[slot]) + tid * 16,
-          a.tiles + ((size_t)(sq.slot0 + step / 4) * a.HV + hv) * kTilesBytes +
-              (step % 4) * 2 * kTall + tid * 16,
-          true);
+    const size_t unit_at = (size_t)(sq.slot0 + step / 4) * a.HV + hv;
+    if (dbg_ok(a.dbg, unit_at, a.units, DBG_LOAD))
+        cp16z(smem_u32(sm.tiles[slot]) + tid * 16,
+              a.tiles + unit_at * kTilesBytes + (step % 4) * 2 * kTall + tid * 16, true);
 }
 
 template <int NW>
@@ -133,7 +133,9 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
     Tile S;
     const size_t sbase = ((size_t)n * a.HV + hv) * D * D + (size_t)tc2 * D + tile0 * 16 + gr;
     S.clear();
-    if (a.d_final_state) {
+    const bool states_in = chunk::state_ok(a, a.d_final_state, sbase, DBG_LOAD) &&
+                           chunk::state_ok(a, a.d_initial_state, sbase, DBG_STORE);
+    if (a.d_final_state && states_in) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
             const float *p = a.d_final_state + sbase + (size_t)8 * j * D;
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
     for (int i = 0; i < steps; ++i) {
         const int st = i % kStages, slot = i % kRaw, step = steps - 1 - i;
         const unsigned unit_at = (unsigned)(sq.slot0 + step / 4) * a.HV + hv;
-        const bool keep = step % 4 == 3;
+        const bool save = dbg_ok(a.dbg, unit_at, a.units, DBG_STORE), keep = save && step % 4 == 3;
         bar_sync(BAR_FULL + st, kHalf + 32 * NW);
         const Planes &in = sm.stage[st];
         const uint32_t kw = smem_u32(in.kw), qw = smem_u32(in.qw), kd = smem_u32(in.kd);
@@ -248,14 +250,14 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         }
         if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kHalf + 32 * NW);
         uint32_t dw[4];  // dv = beta Y
-        const float s =
-            store_block(a.y + unit_at * kRowsBytes, y, ym, (step % 4) * 8 + tile0, lane);
+        float s = 1.f;
+        if (save) s = store_block(a.y + unit_at * kRowsBytes, y, ym, (step % 4) * 8 + tile0, lane);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             dw[2 * j] = chunk::pack_bf16(b[j].x * y[j][0], b[j].y * y[j][1]);
             dw[2 * j + 1] = chunk::pack_bf16(b[j].x * y[j][2], b[j].y * y[j][3]);
         }
-        if (lane == 0) {
+        if (save && lane == 0) {
             float *scales = a.dscales + unit_at * kScales + tile0;
             scales[8 + (step % 4) * 8] = s;
             if (keep) scales[0] = ckpt_scale;
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         chunk::store_out(sm.out[role.consumer], dw, (char *)(dv_at + (size_t)step * C * vrow),
                          vrow * 2, sq.len - step * C, (char *)a.dv, a.rows_o * D * 2, a.dbg, lane);
     }
-    if (a.d_initial_state) {
+    if (a.d_initial_state && states_in) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
             float *p = a.d_initial_state + sbase + (size_t)8 * j * D;

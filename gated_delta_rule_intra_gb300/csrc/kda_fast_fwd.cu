@@ -68,12 +68,13 @@ struct __align__(128) Smem {
 // A preparing thread's pointers to the raw inputs; step s is `s` steps further on.
 template <int SLICE> struct Loader {
     const char *q, *k, *v, *gate, *beta;
+    long long row0;
     size_t hrow, vrow;  // bytes of a token's row of q or k, and of v (gate: twice)
     int row, c, len;
 
     __device__ __forceinline__ Loader(const ChunkFwdArgs &a, const Seq &sq, int h, int hv, int dv0,
                                       int tid)
-        : row(tid >> 4), c(tid & 15), len(sq.len) {
+        : row0(sq.row0), row(tid >> 4), c(tid & 15), len(sq.len) {
         hrow = (size_t)a.H * D * 2;
         vrow = (size_t)a.HV * D * 2;
         const size_t r0 = (size_t)sq.row0;
@@ -89,7 +90,7 @@ template <int SLICE> struct Loader {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = row + 8 * i, t = step * C + r;
-            const bool ok = t < len;
+            const bool ok = t < len && chunk::token_ok(a, row0 + t);
             const size_t at = ok ? (size_t)t : 0;
             cp16z(smem_u32(&raw.q[r][c * 8]), q + at * hrow, ok);
             cp16z(smem_u32(&raw.k[r][c * 8]), k + at * hrow, ok);
@@ -376,9 +377,9 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
                 Stage &out = sm.stage[st];
                 const float *beta = sm.beta[i % kRaw];
                 char *tiles = nullptr;
-                if (SAVE && dv0 == 0)
-                    tiles = a.tiles + ((size_t)(sq.slot0 + i / 4) * a.HV + hv) * kTilesBytes +
-                            (i % 4) * 2 * kTall;
+                const size_t unit_at = (size_t)(sq.slot0 + i / 4) * a.HV + hv;
+                if (SAVE && dv0 == 0 && dbg_ok(a.dbg, unit_at, a.units, DBG_STORE))
+                    tiles = a.tiles + unit_at * kTilesBytes + (i % 4) * 2 * kTall;
                 bar_sync(BAR_SOLVE + w, kHalf + 32);
                 const uint4 *p = reinterpret_cast<const uint4 *>(sm.pt[w]);
                 const uint4 p0 = p[lane], p1 = p[32 + lane];
@@ -423,7 +424,8 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         const float *beta = sm.beta[slot];
         const uint32_t kw = smem_u32(in.pl.kw), qw = smem_u32(in.pl.qw), kd = smem_u32(in.pl.kd);
         const float kinv = in.pl.kinv, qinv = in.pl.qinv, ktop = largest(in.pl.kmax);
-        const bool keep = SAVE && i % 4 == 0;
+        const bool save = SAVE && dbg_ok(a.dbg, unit_at, a.units, DBG_STORE);
+        const bool keep = save && i % 4 == 0;
         bool careful = chunk::uniform(in.pl.careful);
         if (chunk::uniform(S.bound > kLimit)) S.renew();
         uint32_t th[4], tl[4], pf[4];
@@ -528,7 +530,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
             em = warp_max(abs_max(e));
         }
         if (i + kStages < steps) bar_arrive(BAR_EMPTY + st, kHalf + 32 * NW);
-        if (SAVE) {
+        if (save) {
             const float s =
                 store_block(a.e + unit_at * kRowsBytes, e, em, (i % 4) * 8 + tile0, lane);
             if (lane == 0) {

@@ -48,6 +48,18 @@ __device__ __forceinline__ void put_two(__half *p, float2 x) {
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
+// Where a row is in its tensor of `end` elements, from the first to behind the last, for the debug
+// build's checks.
+struct Place {
+    unsigned *dbg;
+    size_t at, end;
+    __device__ __forceinline__ Place(const NormArgs &a, long long row, long long stride)
+        : dbg(a.dbg), at((size_t)row * stride), end((size_t)(a.rows - 1) * stride + a.width) {}
+    __device__ __forceinline__ bool ok(int last, unsigned bit) const {
+        return dbg_ok(dbg, at + last, end, bit);
+    }
+};
+
 // A thread's elements of a row.  WIDE: 16-byte accesses, a group's next to each other; otherwise
 // single elements TPR columns apart (rows that start at no 16-byte boundary).
 template <typename T, bool WIDE, int TPR> struct Part {
@@ -58,38 +70,34 @@ template <typename T, bool WIDE, int TPR> struct Part {
         return WIDE ? (i / kVec * TPR + t) * kVec + i % kVec : t + i * TPR;
     }
 
-    __device__ __forceinline__ void load(const T *row, int t, int width, bool ok) {
-        if (WIDE) {
+    // (rows on 16-byte boundaries come through Stream)
+    __device__ __forceinline__ void load(const T *row, int t, int width, bool ok,
+                                         const Place &where) {
 #pragma unroll
-            for (int i = 0; i < E; i += kVec) {
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (ok && col(t, i) < width)
-                    x = __ldcs(reinterpret_cast<const uint4 *>(row + col(t, i)));
-                *reinterpret_cast<uint4 *>(&v[i]) = x;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < E; ++i)
-                v[i] = ok && col(t, i) < width ? row[col(t, i)] : from_f32<T>(0.f);
-        }
+        for (int i = 0; i < E; ++i)
+            v[i] = ok && col(t, i) < width && where.ok(col(t, i), DBG_LOAD) ? row[col(t, i)]
+                                                                           : from_f32<T>(0.f);
     }
-    __device__ __forceinline__ void store(T *row, int t, int width, bool ok) const {
+    __device__ __forceinline__ void store(T *row, int t, int width, bool ok,
+                                          const Place &where) const {
         if (WIDE) {
 #pragma unroll
             for (int i = 0; i < E; i += kVec)
-                if (ok && col(t, i) < width)
+                if (ok && col(t, i) < width && where.ok(col(t, i) + kVec - 1, DBG_STORE))
                     *reinterpret_cast<uint4 *>(row + col(t, i)) =
                         *reinterpret_cast<const uint4 *>(&v[i]);
         } else {
 #pragma unroll
             for (int i = 0; i < E; ++i)
-                if (ok && col(t, i) < width) row[col(t, i)] = v[i];
+                if (ok && col(t, i) < width && where.ok(col(t, i), DBG_STORE))
+                    row[col(t, i)] = v[i];
         }
     }
 };
 
-// Rows on their way to a thread: its two 16-byte parts of each of the next DEPTH - 1 rows, copied asynchronously into slots of its own in shared memory, so that as many bytes
-// are in flight as the memory's latency asks for without a register or a barrier.  Rows on no
+// Rows on their way to a thread: its two 16-byte parts of each of the next DEPTH - 1 rows, copied
+// asynchronously into slots of its own in shared memory, so that as many bytes are in flight as
+// the memory's latency asks for without a register or a barrier.  Rows on no
 // 16-byte boundary (WIDE false) come through registers, one row ahead.
 template <typename T, bool WIDE, int TPR, int THREADS, int DEPTH> struct Stream {
     using P = Part<T, WIDE, TPR>;
@@ -100,12 +108,13 @@ template <typename T, bool WIDE, int TPR, int THREADS, int DEPTH> struct Stream 
 
     __device__ __forceinline__ Stream(char *s)
         : slots(reinterpret_cast<uint4 *>(s) + threadIdx.x) {}
-    __device__ __forceinline__ void fetch(int stage, const T *row, int t, int width, bool ok) {
+    __device__ __forceinline__ void fetch(int stage, const T *row, int t, int width, bool ok,
+                                          const Place &where) {
         if (WIDE) {
 #pragma unroll
             for (int i = 0; i < kParts; ++i) {
                 const int c = P::col(t, i * P::kVec);
-                const bool in = ok && c < width;
+                const bool in = ok && c < width && where.ok(c + P::kVec - 1, DBG_LOAD);
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                                  (uint32_t)__cvta_generic_to_shared(
                                      slots + (stage * kParts + i) * THREADS)),
@@ -113,7 +122,7 @@ template <typename T, bool WIDE, int TPR, int THREADS, int DEPTH> struct Stream 
                              : "memory");
             }
         } else {
-            next.load(row, t, width, ok);
+            next.load(row, t, width, ok, where);
         }
     }
     __device__ __forceinline__ P take(int stage) {

@@ -48,12 +48,14 @@ __global__ void __launch_bounds__(threads<TPR>(), per_sm<elements<T, WIDE>(), WI
     auto fetch = [&](int stage, long long row) {
         const bool ok = row < a.rows;
         const long long at = ok ? row : 0;
-        xs.fetch(stage, (const T *)a.x + at * a.x_stride, t, a.width, ok);
-        dys.fetch(stage, (const T *)a.dy + at * a.dy_stride, t, a.width, ok);
+        xs.fetch(stage, (const T *)a.x + at * a.x_stride, t, a.width, ok, Place(a, row, a.x_stride));
+        dys.fetch(stage, (const T *)a.dy + at * a.dy_stride, t, a.width, ok,
+                  Place(a, row, a.dy_stride));
         cp_async_commit();
     };
     auto stats = [&](long long row) {
-        return row < a.rows ? make_float2(a.mean[row], a.rstd[row]) : make_float2(0.f, 0.f);
+        return row < a.rows && dbg_ok(a.dbg, (size_t)row, (size_t)a.rows, DBG_LOAD)
+                   ? make_float2(a.mean[row], a.rstd[row]) : make_float2(0.f, 0.f);
     };
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) fetch(i, row0 + i * step + grp);
@@ -96,10 +98,11 @@ __global__ void __launch_bounds__(threads<TPR>(), per_sm<elements<T, WIDE>(), WI
 #pragma unroll
         for (int i = 0; i < E / 2; ++i)
             put_two(&out.v[2 * i], mul2(both(rstd), fma2(xh[i], both(-s2), add2(h[i], both(-s1)))));
-        out.store((T *)a.dx + row * a.dx_stride, t, a.width, row < a.rows);
+        out.store((T *)a.dx + row * a.dx_stride, t, a.width, row < a.rows,
+                  Place(a, row, a.dx_stride));
     }
     cp_async_wait_newest<0>();
-    if (!a.dweight) return;
+    if (!a.dweight || !dbg_ok(a.dbg, blockIdx.x, (size_t)a.partials, DBG_STORE)) return;
     float *to = a.partial + (size_t)blockIdx.x * 2 * a.width;
     if constexpr (kGroups == 1) {
 #pragma unroll
@@ -132,13 +135,14 @@ __global__ void __launch_bounds__(threads<TPR>(), per_sm<elements<T, WIDE>(), WI
 
 // Column sums of `partial` [n][cols]: 32 columns a CTA, 32 slices of rows side by side.
 __global__ void __launch_bounds__(1024)
-    kda_layer_norm_sum_kernel(const float *partial, int n, int width, float *dweight, float *dbias) {
+    kda_layer_norm_sum_kernel(const float *partial, int n, int width, float *dweight, float *dbias,
+                              int partials, unsigned *dbg) {
     wait_for_previous();
     __shared__ float red[32][33];
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const long long cols = 2LL * width, c = (long long)blockIdx.x * 32 + lane;
     float s = 0.f;
-    if (c < cols) {
+    if (c < cols && dbg_ok(dbg, (size_t)n, (size_t)partials + 1, DBG_LOAD)) {
 #pragma unroll 4
         for (int i = slice; i < n; i += 32) s += partial[(size_t)i * cols + c];
     }
@@ -161,6 +165,10 @@ template <typename T> __global__ void __launch_bounds__(1024) kda_layer_norm_bwd
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T *x = (const T *)a.x + row * a.x_stride, *dy = (const T *)a.dy + row * a.dy_stride;
+        if (!Place(a, row, a.x_stride).ok(a.width - 1, DBG_LOAD) ||
+            !Place(a, row, a.dy_stride).ok(a.width - 1, DBG_LOAD) ||
+            !Place(a, row, a.dx_stride).ok(a.width - 1, DBG_STORE))
+            return;
         const float mean = a.mean[row], rstd = a.rstd[row];
         float s1 = 0.f, s2 = 0.f;
         for (int c = tid; c < a.width; c += 1024) {
@@ -188,9 +196,11 @@ template <typename T> __global__ void __launch_bounds__(1024) kda_layer_norm_bwd
 template <typename T> __global__ void __launch_bounds__(256) kda_layer_norm_bwd_cols_kernel(const NormArgs a) {
     wait_for_previous();
     const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= a.width) return;
+    if (c >= a.width || !dbg_ok(a.dbg, blockIdx.y, (size_t)a.partials, DBG_STORE)) return;
     float dw = 0.f, db = 0.f;
     for (long long row = blockIdx.y; row < a.rows; row += gridDim.y) {
+        if (!Place(a, row, a.dy_stride).ok(c, DBG_LOAD) || !Place(a, row, a.x_stride).ok(c, DBG_LOAD))
+            return;
         const float d = as_f32(((const T *)a.dy)[row * a.dy_stride + c]);
         dw += d * (as_f32(((const T *)a.x)[row * a.x_stride + c]) - a.mean[row]) * a.rstd[row];
         db += d;
@@ -213,7 +223,7 @@ int ctas(long long rows, int width, int e, bool wide) {
 cudaError_t sum_partials(const NormArgs &a, int n, cudaStream_t stream) {
     if (!a.dweight) return cudaSuccess;
     return launch_early(kda_layer_norm_sum_kernel, (unsigned)((2LL * a.width + 31) / 32), 1024, 0,
-                        stream, a.partial, n, a.width, a.dweight, a.dbias);
+                        stream, a.partial, n, a.width, a.dweight, a.dbias, a.partials, a.dbg);
 }
 
 template <typename T, bool WIDE, int TPR>

@@ -54,7 +54,8 @@ __global__ void __launch_bounds__(threads<TPR>()) kda_layer_norm_fwd_kernel(cons
         for (int r = 0; r < R; ++r) {
             const long long row = first + r * kGroups + grp;
             const bool ok = row < a.rows;
-            rows.fetch(stage * R + r, (const T *)a.x + (ok ? row : 0) * a.x_stride, t, a.width, ok);
+            rows.fetch(stage * R + r, (const T *)a.x + (ok ? row : 0) * a.x_stride, t, a.width, ok,
+                       Place(a, row, a.x_stride));
         }
         cp_async_commit();
     };
@@ -109,8 +110,8 @@ __global__ void __launch_bounds__(threads<TPR>()) kda_layer_norm_fwd_kernel(cons
 #pragma unroll
             for (int i = 0; i < E; ++i)
                 out.v[i] = from_f32<T>((x[r][i] - mean[r]) * rstd * wt[i] + bs[i]);
-            out.store((T *)a.y + row * a.y_stride, t, a.width, ok);
-            if (ok && t == 0) {
+            out.store((T *)a.y + row * a.y_stride, t, a.width, ok, Place(a, row, a.y_stride));
+            if (ok && t == 0 && dbg_ok(a.dbg, (size_t)row, (size_t)a.rows, DBG_STORE)) {
                 if (a.mean) a.mean[row] = mean[r];
                 if (a.rstd) a.rstd[row] = rstd;
             }
@@ -126,6 +127,9 @@ template <typename T> __global__ void __launch_bounds__(1024) kda_layer_norm_fwd
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T *x = (const T *)a.x + row * a.x_stride;
+        if (!Place(a, row, a.x_stride).ok(a.width - 1, DBG_LOAD) ||
+            !Place(a, row, a.y_stride).ok(a.width - 1, DBG_STORE))
+            return;
         float s = 0.f;
         for (int c = tid; c < a.width; c += 1024) s += as_f32(x[c]);
         s = lanes_sum<32>(s);

@@ -21,7 +21,9 @@ struct ChunkFwdArgs {
     float scale;
     bool fp16;
     bool fast;                   // BF16 training (kda_fast.cuh)
-    size_t rows_o;               // rows of o (tokens * HV), for the debug build's checks
+    // For the debug build's checks: rows of o (tokens * HV), slots of value heads that are saved,
+    // elements of a state's tensor.
+    size_t rows_o, units, states;
     unsigned *dbg;
 };
 
@@ -43,7 +45,7 @@ struct ChunkBwdArgs {
     const int *cu_seqlens;
     float scale;
     bool fp16;
-    size_t rows_o;
+    size_t rows_o, units, states;  // as above
     unsigned *dbg;
 };
 
@@ -55,6 +57,7 @@ struct ZeroArgs {
     size_t row[5];
     int count, T, num_seqs;
     const int *cu_seqlens;
+    unsigned *dbg;
 };
 
 cudaError_t launch_zero_rest(const ZeroArgs &a, cudaStream_t stream);
@@ -85,7 +88,8 @@ struct NormArgs {
     const void *dy;
     void *dx;
     float *dweight, *dbias;         // [width], both or none
-    float *partial;                 // [norm_bwd_ctas(rows, width)][2][width]
+    float *partial;                 // [partials = norm_bwd_ctas(rows, width)][2][width]
+    int partials;
     long long rows;
     int width, dtype, wdtype;
     long long x_stride, y_stride, dy_stride, dx_stride;  // elements between rows

@@ -131,7 +131,7 @@ kda_status_t kda_chunk_fwd(const void *q, const void *k, const void *v, const fl
     (void)cudaGetLastError();
     if (T == 0 && !op.final_state) return KDA_OK;
     if (varlen && op.zero_rest) {
-        const kda::ZeroArgs z = {{o}, {(size_t)HV * KDA_K * 2}, 1, T, seqs, op.cu_seqlens};
+        const kda::ZeroArgs z = {{o}, {(size_t)HV * KDA_K * 2}, 1, T, seqs, op.cu_seqlens, kda::debug_flags()};
         const cudaError_t e = kda::launch_zero_rest(z, (cudaStream_t)stream);
         if (e != cudaSuccess) return finish(e);
     }
@@ -153,6 +153,8 @@ kda_status_t kda_chunk_fwd(const void *q, const void *k, const void *v, const fl
     a.scale = op.scale != 0.f ? op.scale : 0.08838834764831845f;
     a.fp16 = dtype == KDA_FP16;
     a.rows_o = rv;
+    a.units = (size_t)chunk_slots(B, T, op.num_seqs) * HV;
+    a.states = states / 4;
     a.dbg = kda::debug_flags();
     return finish(kda::launch_chunk_fwd(a, (cudaStream_t)stream));
 }
@@ -219,7 +221,7 @@ kda_status_t kda_chunk_bwd(const void *q, const void *k, const float *gate, cons
         const size_t head = KDA_K * 2;
         const kda::ZeroArgs z = {{dq, dk, dv, dgate, dbeta},
                                  {H * head, H * head, HV * head, HV * head, (size_t)HV * 2},
-                                 5, T, seqs, op.cu_seqlens};
+                                 5, T, seqs, op.cu_seqlens, kda::debug_flags()};
         const cudaError_t e = kda::launch_zero_rest(z, (cudaStream_t)stream);
         if (e != cudaSuccess) return finish(e);
     }
@@ -249,6 +251,8 @@ kda_status_t kda_chunk_bwd(const void *q, const void *k, const float *gate, cons
     a.scale = op.scale != 0.f ? op.scale : 0.08838834764831845f;
     a.fp16 = dtype == KDA_FP16;
     a.rows_o = rv;
+    a.units = n;
+    a.states = states / 4;
     a.dbg = kda::debug_flags();
     return finish(kda::launch_chunk_bwd(a, (cudaStream_t)stream));
 }
@@ -323,6 +327,7 @@ kda_status_t kda_layer_norm_fwd(const void *x, const void *weight, const void *b
     a.rows = rows; a.width = width; a.dtype = dtype; a.wdtype = wdtype;
     a.x_stride = x_stride; a.y_stride = y_stride;
     a.eps = eps;
+    a.dbg = kda::debug_flags();
     return finish(kda::launch_norm_fwd(a, (cudaStream_t)stream));
 }
 
@@ -367,6 +372,8 @@ kda_status_t kda_layer_norm_bwd(const void *dy, const void *x, const void *weigh
     a.dweight = dweight; a.dbias = dbias; a.partial = (float *)workspace;
     a.rows = rows; a.width = width; a.dtype = dtype; a.wdtype = wdtype;
     a.x_stride = x_stride; a.dy_stride = dy_stride; a.dx_stride = dx_stride;
+    a.partials = kda::norm_bwd_ctas(rows, width);
+    a.dbg = kda::debug_flags();
     return finish(kda::launch_norm_bwd(a, (cudaStream_t)stream));
 }
 

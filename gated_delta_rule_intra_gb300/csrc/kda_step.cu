@@ -34,12 +34,15 @@ __global__ void __launch_bounds__(kThreads) kda_step_kernel(const StepArgs a) {
     if (a.state_indices) {
         slot = a.state_indices[n];
         if (slot < 0 || slot >= a.num_states) {  // no request here: o is zero
-            if (rg == 0)
-                *reinterpret_cast<uint2 *>((uint16_t *)a.o + row * D + 4 * (c0 + quad)) =
-                    make_uint2(0u, 0u);
+            const size_t idx = row * D + 4 * (c0 + quad);
+            if (rg == 0 && dbg_ok(a.dbg, idx + 3, (size_t)a.N * a.HV * D, DBG_STORE))
+                *reinterpret_cast<uint2 *>((uint16_t *)a.o + idx) = make_uint2(0u, 0u);
             return;
         }
     }
+    if (!dbg_ok(a.dbg, (size_t)slot * a.HV + hv, (size_t)a.num_states * a.HV, DBG_STORE) ||
+        !dbg_ok(a.dbg, row, (size_t)a.N * a.HV, DBG_LOAD))
+        return;
     float4 *st = reinterpret_cast<float4 *>(a.state) + ((size_t)slot * a.HV + hv) * (D * D / 4) +
                  c0 + quad;
     float4 s[kRows];

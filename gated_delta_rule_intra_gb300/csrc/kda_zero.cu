@@ -7,13 +7,15 @@ namespace kda {
 namespace {
 
 template <typename U>
-__device__ __forceinline__ void clear(char *p, size_t row, long long lead, long long tail, int T) {
+__device__ __forceinline__ void clear(char *p, size_t row, long long lead, long long tail, int T,
+                                      unsigned *dbg) {
     const size_t per = row / sizeof(U);
     const size_t n = (size_t)(lead + T - tail) * per, step = (size_t)gridDim.x * blockDim.x;
     for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
         const long long r = (long long)(i / per);
         const size_t at = (size_t)(r < lead ? r : r - lead + tail) * row + i % per * sizeof(U);
-        *reinterpret_cast<U *>(p + at) = U{};
+        if (dbg_ok(dbg, at + sizeof(U) - 1, (size_t)T * row, DBG_STORE))
+            *reinterpret_cast<U *>(p + at) = U{};
     }
 }
 
@@ -26,9 +28,9 @@ __global__ void __launch_bounds__(256) kda_zero_rest_kernel(const ZeroArgs a) {
     for (int k = 0; k < a.count; ++k) {
         // 16 bytes at a time where rows begin on such boundaries (dbeta need not)
         if (a.row[k] % 16 == 0 && (uintptr_t)a.out[k] % 16 == 0)
-            clear<uint4>((char *)a.out[k], a.row[k], lead, tail, a.T);
+            clear<uint4>((char *)a.out[k], a.row[k], lead, tail, a.T, a.dbg);
         else
-            clear<uint16_t>((char *)a.out[k], a.row[k], lead, tail, a.T);
+            clear<uint16_t>((char *)a.out[k], a.row[k], lead, tail, a.T, a.dbg);
     }
 }
 
