@@ -116,8 +116,12 @@ kda_status_t kda_chunk_fwd(const void *q, const void *k, const void *v, const fl
     const void *a256[] = {op.saved};
     if (misaligned(a16, 16) || misaligned(a4, 4) || misaligned(a256, 256)) return KDA_ERR_ALIGN;
     const bool with_state = op.initial_state || op.final_state;
-    const bool fast = dtype == KDA_BF16 && !with_state;
-    const size_t saved = kda_chunk_saved_bytes(B, T, HV, op.num_seqs, dtype, with_state);
+    bool fast = dtype == KDA_BF16 && !with_state;
+    size_t saved = kda_chunk_saved_bytes(B, T, HV, op.num_seqs, dtype, with_state);
+    if (op.saved && op.saved_bytes != saved && fast) {  // the caller's choice of the other kernels
+        fast = false;
+        saved = kda_chunk_saved_bytes(B, T, HV, op.num_seqs, dtype, 1);
+    }
     if (op.saved && op.saved_bytes != saved) return KDA_ERR_WORKSPACE;
     const size_t rq = (size_t)B * T * H, rv = (size_t)B * T * HV;
     const int seqs = varlen ? op.num_seqs : B;

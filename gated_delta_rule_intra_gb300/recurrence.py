@@ -91,7 +91,8 @@ def _seqs(cu_seqlens, B, dev):
 
 
 def kda_chunk_fwd(q, k, v, gate, beta, scale=None, initial_state=None, *,
-                  output_final_state=False, save=False, cu_seqlens=None, o=None, stream=None):
+                  output_final_state=False, save=False, cu_seqlens=None, o=None, precise=False,
+                  stream=None):
     """The recurrence over whole sequences.  Returns (o, final_state, saved).
 
     q, k [B, T, H, 128] and v [B, T, HV, 128] bf16/fp16 (value head hv reads q/k head
@@ -100,21 +101,24 @@ def kda_chunk_fwd(q, k, v, gate, beta, scale=None, initial_state=None, *,
     [sequences, HV, 128 dk, 128 dv] fp32 defaults to zeros.  o is in q's dtype, with zeros at
     tokens in no sequence when it is allocated here.  final_state (fp32) is None unless
     ``output_final_state``.  saved is what ``kda_chunk_bwd`` needs (0.9 KB a token and
-    value head in bf16 without a state, 1.7 KB otherwise), None unless ``save``.
+    value head in bf16 without a state, 1.7 KB otherwise), None unless ``save``.  bf16 calls
+    without a state take fp16 operands of 11 bits (o within 1e-3 beside its rounding) unless
+    ``precise``; all others keep 16 bits and more (1e-5).
     ``cu_seqlens`` (int32 [N + 1] on the device, B = 1) packs N sequences along T; it is read on
     the device only.
     """
-    if stream is None and cu_seqlens is None and o is None:
+    if stream is None and cu_seqlens is None and o is None and not precise:
         out = library().quick_chunk_fwd(q, k, v, gate, beta, scale, initial_state,
                                         output_final_state, save)
         if out is not None:
             return out
     return _chunk_fwd(q, k, v, gate, beta, scale, initial_state, output_final_state, save,
-                      cu_seqlens, o, stream=stream)
+                      cu_seqlens, o, precise, stream=stream)
 
 
 @takes_stream
-def _chunk_fwd(q, k, v, gate, beta, scale, initial_state, output_final_state, save, cu_seqlens, o):
+def _chunk_fwd(q, k, v, gate, beta, scale, initial_state, output_final_state, save, cu_seqlens, o,
+               precise=False):
     H, HV, dev = _inputs("kda_chunk_fwd", q, k, v, gate, beta, 2)
     B, T = q.shape[:2]
     N = _seqs(cu_seqlens, B, dev)
@@ -130,18 +134,19 @@ def _chunk_fwd(q, k, v, gate, beta, scale, initial_state, output_final_state, sa
         check("initial_state", initial_state, (N or B, HV, K, K), F32, dev)
         op.initial_state = initial_state.data_ptr()
     final = saved = None
-    if output_final_state:
+    if output_final_state or (precise and not save):  # taking a state is what asks for it there
         final = torch.empty((N or B, HV, K, K), dtype=F32, device=q.device)
         op.final_state = final.data_ptr()
     if save:
         size = library().kda_chunk_saved_bytes(B, T, HV, N, DTYPES16[q.dtype],
-                                               initial_state is not None or output_final_state)
+                                               initial_state is not None or output_final_state
+                                               or precise)
         saved = torch.empty(size, dtype=torch.uint8, device=q.device)
         op.saved, op.saved_bytes = saved.data_ptr(), size
     if B:
         run("kda_chunk_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(),
             beta.data_ptr(), o.data_ptr(), B, T, H, DTYPES16[q.dtype], ctypes.addressof(op))
-    return o, final, saved
+    return o, final if output_final_state else None, saved
 
 
 def kda_chunk_bwd(q, k, v, gate, beta, do, saved, scale=None, d_final_state=None, *,

@@ -350,7 +350,9 @@ kda_status_t kda_intra_fwd_ex(const void *q, const void *k, const float *g,
  * FP32.  Calls that take or return a state, and FP16 ones, take every product of FP32 values
  * in three BF16 tensor-core products: o within a rounding to dtype plus 1e-5, the final state
  * within 1e-5.  BF16 calls without a state (training) take one FP16 product with operands of
- * 11 bits, each with a power of two of its own: o within a rounding to BF16 plus 1e-3.
+ * 11 bits, each with a power of two of its own (q and k one a step of 16 tokens): o within a
+ * rounding to BF16 plus 1e-3, for values between 2^-80 and 2^100.  A caller who wants the former
+ * there passes `saved` of a call with a state (or takes the final state): the size chooses.
  *
  * Options (zero-initialise; NULL = none):
  *   HV             0 means HV = H
@@ -360,7 +362,8 @@ kda_status_t kda_intra_fwd_ex(const void *q, const void *k, const float *g,
  *                  state); must not overlap initial_state
  *   saved          what kda_chunk_bwd needs, exactly kda_chunk_saved_bytes() bytes, 256-byte
  *   saved_bytes    aligned; NULL when no backward follows.  0.9 KB a token and value head in
- *                  BF16 without a state, 1.7 KB otherwise.
+ *                  BF16 without a state, 1.7 KB otherwise (with_state = 1, which a BF16 call
+ *                  without a state may have too).
  *   cu_seqlens     variable-length sequences packed along T (B == 1): device int32
  *   num_seqs       [num_seqs + 1], sequence n is tokens [cu_seqlens[n], cu_seqlens[n+1]).
  *                  Values are read on the device only and clamped to [0, T]; tokens in no

@@ -280,3 +280,25 @@ def test_zeros_in_a_dbeta_on_any_two_byte_boundary(HV):
     for a, b in zip((*out[:4], dbeta.view_as(want[4])), want):
         assert torch.equal(a, b)
     assert room[0] == 7 and (room[-2:] == 7).all()
+
+
+# ------------------------------------------------------------------------ the caller's choice
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("lens", [None, [40, 0, 61]])
+def test_precise_calls_without_a_state(lens, dtype):
+    """``precise``: the kernels of the calls with a state, the same bits forwards and backwards."""
+    x = cuda(make(101, 1, 2, dtype=dtype, seed=68))
+    c = None if lens is None else cu(lens)
+    do = gradient_of(x).cuda()
+    want, _, saved = kda.kda_chunk_fwd(*args(x), cu_seqlens=c, save=True, output_final_state=True)
+    grads = kda.kda_chunk_bwd(*args(x), do, saved, cu_seqlens=c)[:5]
+    o, final, mine = kda.kda_chunk_fwd(*args(x), cu_seqlens=c, save=True, precise=True)
+    assert final is None and mine.numel() == saved.numel() and torch.equal(o, want)
+    for a, b in zip(kda.kda_chunk_bwd(*args(x), do, mine, cu_seqlens=c)[:5], grads):
+        assert torch.equal(a, b)
+    o, final, mine = kda.kda_chunk_fwd(*args(x), cu_seqlens=c, precise=True)
+    assert final is None and mine is None and torch.equal(o, want)
+    ref = {n: t.cpu() for n, t in x.items()}
+    close("o", o, forward64(ref, lens=lens)[0], 1e-5)
+    for name, g, r in zip(GRADS, grads, gradients64(ref, do.cpu(), lens=lens)[0]):
+        close(name, g, r, EXTRA)
