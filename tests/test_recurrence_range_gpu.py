@@ -254,6 +254,31 @@ def test_large_values_under_strong_gates(power):
     check_states(x)
 
 
+# ------------------------------------------------------------------------ heads
+@pytest.mark.parametrize("heads", [1, 40, 100, 160])
+@pytest.mark.parametrize("dtype,state", [(BF, True), (HF, False), (HF, True)])
+def test_number_of_heads_does_not_change_a_head(heads, dtype, state):
+    """Heads run in one, two or four CTAs, by how many there are: the same bits."""
+    x = cuda(make(40, heads, heads, dtype=dtype, seed=64))
+    S0 = states(1, heads).cuda() if state else None
+    dS = states(1, heads, seed=4).cuda() if state else None
+
+    def run(x, S0, dS):
+        o, final, saved = kda.kda_chunk_fwd(*args(x), initial_state=S0, save=True,
+                                            output_final_state=state)
+        return (o, *kda.kda_chunk_bwd(*args(x), x["v"], saved, d_final_state=dS,
+                                      output_d_initial_state=state), final)
+
+    many = run(x, S0, dS)
+    one = run({n: t[:, :, :1].contiguous() for n, t in x.items()},
+              *(t if t is None else t[:, :1].contiguous() for t in (S0, dS)))
+    for a, b in zip(one[:6], many[:6]):
+        assert torch.equal(a, b[:, :, :1])
+    if state:
+        for a, b in zip(one[6:], many[6:]):
+            assert torch.equal(a, b[:, :1])
+
+
 # ------------------------------------------------------------------------ zeros
 @pytest.mark.parametrize("HV", [8, 3])
 def test_zeros_in_a_dbeta_on_any_two_byte_boundary(HV):
@@ -302,3 +327,17 @@ def test_precise_calls_without_a_state(lens, dtype):
     close("o", o, forward64(ref, lens=lens)[0], 1e-5)
     for name, g, r in zip(GRADS, grads, gradients64(ref, do.cpu(), lens=lens)[0]):
         close(name, g, r, EXTRA)
+
+
+@pytest.mark.parametrize("what", ["v", "do"])
+@pytest.mark.parametrize("power", [-60, 60, 90])
+@pytest.mark.parametrize("lo", [-0.5, -3.0, -40.0])
+def test_values_and_gradients_of_any_size(lo, power, what):
+    """As far as the header goes: 2^-80 to 2^100, a little room for sums left."""
+    x = make(70, 1, 2, lo=lo, seed=69)
+    do = gradient_of(x)
+    if what == "v":
+        x["v"] = x["v"] * 2.0 ** power
+    else:
+        do = do * 2.0 ** power
+    check_train(x, do=do)
