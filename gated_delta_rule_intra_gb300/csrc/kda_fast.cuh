@@ -210,16 +210,15 @@ struct Scales {
     __device__ __forceinline__ void follow(const Planes &p, float scale) {
         set(plane_scale(largest(p.kmax)), plane_scale(fabsf(scale) * largest(p.qmax)), scale);
     }
+    // Zeros fit any power (unused channels, tokens behind the end).
     __device__ __forceinline__ bool in_range(float kmax, float qmax) const {
         const float x = k * kmax, y = qabs * qmax;
-        return x >= kLeast && x <= kMost && y >= kLeast && y <= kMost;
+        return (x >= kLeast || x == 0.f) && x <= kMost && (y >= kLeast || y == 0.f) && y <= kMost;
     }
-    // For the step; zeros fit any power.
     __device__ __forceinline__ bool fit(const Planes &p) const {
-        const float km = largest(p.kmax), qm = largest(p.qmax);
-        return in_range(km == 0.f ? kinv : km, qm == 0.f ? 1.f / qabs : qm);
+        return in_range(largest(p.kmax), largest(p.qmax));
     }
-    // The same for each preparing warp's part of it, as its barrier sees it.
+    // The same for each preparing warp's part of the step, as its barrier sees it.
     __device__ __forceinline__ bool fit_all(const Planes &p) const {
         bool ok = true;
 #pragma unroll

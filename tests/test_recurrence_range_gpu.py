@@ -341,3 +341,11 @@ def test_values_and_gradients_of_any_size(lo, power, what):
     else:
         do = do * 2.0 ** power
     check_train(x, do=do)
+
+
+@pytest.mark.parametrize("lo", [-0.1, -3.0])
+def test_channels_that_no_key_or_query_uses(lo):
+    x = make(70, 1, 2, lo=lo, seed=70)
+    x["k"][..., 64:] = 0
+    x["q"][..., :32] = 0
+    check_train(x)
