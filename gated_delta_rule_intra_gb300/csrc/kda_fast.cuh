@@ -190,53 +190,41 @@ __device__ __forceinline__ float plane_scale(float largest) {
     return largest == 0.f ? 1.f : scale_for(fminf(fmaxf(largest, 0x1p-60f), 0x1p14f), 0);
 }
 // Where the largest |k| and |scale q| have to be with the planes' powers of two, so that the
-// forward may go on with the step before's: finding the maximum in front of the planes costs its
-// preparing warps, whose chain is the longer one, 3% of a step.
+// forward may go on with the step before's: finding the maximum in front of the planes would cost
+// its preparing warps, whose chain is the longer one, 3% of a mild step and 10% of another.
 constexpr float kLeast = 0.125f, kMost = 3.5f;
 
-// The planes' powers of two: kw and kd are taken `k` times as large, qw `q` times (`scale` included;
-// qabs is its size).
+// The planes' powers of two: kw and kd are taken `k` times as large, qw `q` times.
 struct Scales {
-    float k, q, kinv, qinv, qabs;
+    float k = 1.f, q = 1.f;
 
-    __device__ __forceinline__ explicit Scales(float scale) { set(1.f, 1.f, scale); }
-    __device__ __forceinline__ void set(float kpower, float qpower, float scale) {
-        k = kpower;
-        q = scale * qpower;
-        kinv = inverse_of(kpower);
-        qinv = inverse_of(qpower);
-        qabs = fabsf(q);
-    }
     __device__ __forceinline__ void follow(const Planes &p, float scale) {
-        set(plane_scale(largest(p.kmax)), plane_scale(fabsf(scale) * largest(p.qmax)), scale);
+        k = plane_scale(largest(p.kmax));
+        q = plane_scale(fabsf(scale) * largest(p.qmax));
     }
     // Zeros fit any power (unused channels, tokens behind the end).
-    __device__ __forceinline__ bool in_range(float kmax, float qmax) const {
-        const float x = k * kmax, y = qabs * qmax;
+    __device__ __forceinline__ bool in_range(float kmax, float qmax, float scale) const {
+        const float x = k * kmax, y = fabsf(scale * q) * qmax;
         return (x >= kLeast || x == 0.f) && x <= kMost && (y >= kLeast || y == 0.f) && y <= kMost;
     }
-    __device__ __forceinline__ bool fit(const Planes &p) const {
-        return in_range(largest(p.kmax), largest(p.qmax));
+    __device__ __forceinline__ bool fit(const Planes &p, float scale) const {
+        return in_range(largest(p.kmax), largest(p.qmax), scale);
     }
-    // The same for each preparing warp's part of the step, as its barrier sees it.
-    __device__ __forceinline__ bool fit_all(const Planes &p) const {
-        bool ok = true;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            ok = ok && in_range(__uint_as_float(p.kmax[i]), __uint_as_float(p.qmax[i]));
-        return ok;
+    __device__ __forceinline__ void put(Planes &p) const {
+        p.kinv = inverse_of(k);
+        p.qinv = inverse_of(q);
     }
 };
 // A preparing warp's largest |k| and |q| from its threads'; returns whether they are in range.
 __device__ __forceinline__ bool put_largest(Planes &out, uint32_t km, uint32_t qm, const Scales &sc,
-                                            int tid) {
+                                            float scale, int tid) {
     const uint32_t kb = __reduce_max_sync(0xffffffffu, max(km << 16, km & 0xffff0000u));
     const uint32_t qb = __reduce_max_sync(0xffffffffu, max(qm << 16, qm & 0xffff0000u));
     if ((tid & 31) == 0) {
         out.kmax[tid >> 5] = kb;
         out.qmax[tid >> 5] = qb;
     }
-    return sc.in_range(__uint_as_float(kb), __uint_as_float(qb));
+    return sc.in_range(__uint_as_float(kb), __uint_as_float(qb), scale);
 }
 
 // The largest |q| and |k| among what a preparing thread has copied itself (eight channels of the
@@ -276,7 +264,7 @@ constexpr int kUp = 14, kMildDown = 5;
 // These planes (128 threads, two channels of eight rows each).  Returns whether the step is mild,
 // with inputs in range of the planes' powers of two, as far as the thread and its warp have seen.
 __device__ __forceinline__ bool prepare_mild(const RawStage &raw, Planes &out, const Scales &sc,
-                                             int tid) {
+                                             float scale, int tid) {
     const int c2 = tid & 63, r0 = (tid >> 6) * 8;
     auto gate = [&](int r) {
         const float2 x = *reinterpret_cast<const float2 *>(&raw.gate[r][2 * c2]);
@@ -287,7 +275,8 @@ __device__ __forceinline__ bool prepare_mild(const RawStage &raw, Planes &out, c
 #pragma unroll
         for (int r = 0; r < 8; ++r) g = chunk::add2(g, gate(r));
     }
-    const float2 ks = make_float2(sc.k, sc.k), qs = make_float2(sc.q, sc.q);
+    const float2 ks = make_float2(sc.k, sc.k);
+    const float2 qs = make_float2(scale * sc.q, scale * sc.q);
     uint32_t km = 0, qm = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -307,18 +296,20 @@ __device__ __forceinline__ bool prepare_mild(const RawStage &raw, Planes &out, c
         *reinterpret_cast<uint32_t *>(out.kd + off) = pack_f16(kd.x, kd.y);
     }
     if (r0) *reinterpret_cast<float2 *>(&out.decay[2 * c2]) = make_float2(ex2(g.x), ex2(g.y));
-    return put_largest(out, km, qm, sc, tid) && g.x >= kMildGate && g.y >= kMildGate;
+    return put_largest(out, km, qm, sc, scale, tid) && g.x >= kMildGate && g.y >= kMildGate;
 }
 
-// What a thread of prepare() has seen: a channel loses more than 2^-96; none more than a mild step's.
+// What a thread of prepare() has seen: a channel loses more than 2^-96; none more than a mild step's;
+// its warp's inputs are in range of the planes' powers of two.
 struct Seen {
-    bool strong, mild;
+    bool strong, mild, in_range;
 };
-// The operand planes in general (128 threads), kw and qw 2^UP and kd 2^DOWN times as large, and
-// where wanted the cumulative gate (plus UP, which its differences do not see).
-template <int UP, int DOWN>
+// The operand planes in general (128 threads), kw and qw 2^UP and kd 2^DOWN times as large.
+// FORWARD: the cumulative gate too (plus UP, which its differences do not see), and the largest
+// inputs, which have been found before otherwise.
+template <bool FORWARD, int UP, int DOWN>
 __device__ __forceinline__ Seen prepare(const RawStage &raw, Planes &out, float (*gcum)[kRowPad],
-                                        const Scales &sc, int tid) {
+                                        const Scales &sc, float scale, int tid) {
     const int c2 = tid & 63, r0 = (tid >> 6) * 8;
     auto gate = [&](int r) {
         const float2 x = *reinterpret_cast<const float2 *>(&raw.gate[r][2 * c2]);
@@ -332,16 +323,21 @@ __device__ __forceinline__ Seen prepare(const RawStage &raw, Planes &out, float 
     }
     g = chunk::add2(g, make_float2(UP, UP));
     const float2 last = chunk::add2(total, make_float2(UP + DOWN, UP + DOWN));
-    const float2 ks = make_float2(sc.k, sc.k), qs = make_float2(sc.q, sc.q);
+    const float2 ks = make_float2(sc.k, sc.k);
+    const float2 qs = make_float2(scale * sc.q, scale * sc.q);
+    uint32_t km = 0, qm = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int r = r0 + i;
         g = chunk::add2(g, gate(r));
-        if (gcum) *reinterpret_cast<float2 *>(&gcum[r][2 * c2]) = g;
-        const float2 q = chunk::mul2(
-            bf2(*reinterpret_cast<const uint32_t *>(&raw.q[r][2 * c2])), qs);
-        const float2 k = chunk::mul2(
-            bf2(*reinterpret_cast<const uint32_t *>(&raw.k[r][2 * c2])), ks);
+        if (FORWARD) *reinterpret_cast<float2 *>(&gcum[r][2 * c2]) = g;
+        const uint32_t qr = *reinterpret_cast<const uint32_t *>(&raw.q[r][2 * c2]);
+        const uint32_t kr = *reinterpret_cast<const uint32_t *>(&raw.k[r][2 * c2]);
+        if (FORWARD) {
+            km = __vmaxu2(km, kr & 0x7fff7fffu);
+            qm = __vmaxu2(qm, qr & 0x7fff7fffu);
+        }
+        const float2 q = chunk::mul2(bf2(qr), qs), k = chunk::mul2(bf2(kr), ks);
         const float2 up = make_float2(ex2(g.x), ex2(g.y));
         const float2 dn = make_float2(ex2(last.x - g.x), ex2(last.y - g.y));
         const float2 kw = chunk::mul2(k, up), qw = chunk::mul2(q, up), kd = chunk::mul2(k, dn);
@@ -352,7 +348,8 @@ __device__ __forceinline__ Seen prepare(const RawStage &raw, Planes &out, float 
     }
     if (r0 == 8)
         *reinterpret_cast<float2 *>(&out.decay[2 * c2]) = make_float2(ex2(total.x), ex2(total.y));
-    return {total.x < -96.f || total.y < -96.f, total.x >= kMildGate && total.y >= kMildGate};
+    return {total.x < -96.f || total.y < -96.f, total.x >= kMildGate && total.y >= kMildGate,
+            !FORWARD || put_largest(out, km, qm, sc, scale, tid)};
 }
 
 // A step token by token from the definition, forwards: e and o (before its rounding) of a tile

@@ -98,16 +98,15 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
                 cp_async_wait_newest<1>();
                 find_largest(sm.raw[i % kRaw], out, tid);
                 bar_sync(BAR_PREP + group, kHalf);
-                Scales sc(a.scale);
+                Scales sc;
                 sc.follow(out, a.scale);
-                // kw and qw are added to the state's gradient, kd is only multiplied by it
-                prepare<0, kUp>(sm.raw[i % kRaw], out, nullptr, sc, tid);
                 if (tid == 32) {
-                    out.kinv = sc.kinv;
-                    out.qinv = sc.qinv;
+                    sc.put(out);
                     out.ktop = largest(out.kmax);
                     out.qtop = fabsf(a.scale) * largest(out.qmax);
                 }
+                // kw and qw are added to the state's gradient, kd is only multiplied by it
+                prepare<false, 0, kUp>(sm.raw[i % kRaw], out, nullptr, sc, a.scale, tid);
                 if (tid < 32) {
                     const float bm =
                         warp_max(lane < C ? fabsf(sm.beta[i % kRaw][lane]) : 0.f);

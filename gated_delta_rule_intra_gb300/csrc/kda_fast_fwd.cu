@@ -61,25 +61,25 @@ struct __align__(128) Smem {
     float a2[kSolvers][C][C + 4];  // (M diag(beta))^T
     float a1[kSolvers][C][C + 4];  // (diag(beta) M)^T
     char pt[kSolvers][kTall];      // P^T on its way to the saved tiles
+    alignas(16) int mild[4];       // whether a preparing warp's part of a step would do for mild
     int big[kSolvers][4];          // whether a warp's entries of P are out of FP16's reach
     char out[8][512];          // a consumer's o on its way out
 };
 
 // A preparing thread's pointers to the raw inputs; step s is `s` steps further on.
 template <int SLICE> struct Loader {
-    const char *q, *k, *v, *gate, *beta;
+    const char *q, *v, *gate, *beta;  // (k lies as far from its start as q)
     long long row0;
-    size_t hrow, vrow;  // bytes of a token's row of q or k, and of v (gate: twice)
+    unsigned hrow, vrow;  // bytes of a token's row of q or k, and of v (gate: twice)
     int row, c, len;
 
     __device__ __forceinline__ Loader(const ChunkFwdArgs &a, const Seq &sq, int h, int hv, int dv0,
                                       int tid)
         : row0(sq.row0), row(tid >> 4), c(tid & 15), len(sq.len) {
-        hrow = (size_t)a.H * D * 2;
-        vrow = (size_t)a.HV * D * 2;
+        hrow = (unsigned)a.H * D * 2;
+        vrow = (unsigned)a.HV * D * 2;
         const size_t r0 = (size_t)sq.row0;
         q = (const char *)a.q + r0 * hrow + h * D * 2 + c * 16;
-        k = (const char *)a.k + r0 * hrow + h * D * 2 + c * 16;
         v = (const char *)a.v + r0 * vrow + (hv * D + dv0) * 2 + c * 16;
         gate = (const char *)a.gate + r0 * vrow * 2 + hv * D * 4 + c * 16;
         beta = (const char *)(a.beta + r0 * a.HV + hv);
@@ -93,7 +93,7 @@ template <int SLICE> struct Loader {
             const bool ok = t < len && chunk::token_ok(a, row0 + t);
             const size_t at = ok ? (size_t)t : 0;
             cp16z(smem_u32(&raw.q[r][c * 8]), q + at * hrow, ok);
-            cp16z(smem_u32(&raw.k[r][c * 8]), k + at * hrow, ok);
+            cp16z(smem_u32(&raw.k[r][c * 8]), q + ((const char *)a.k - (const char *)a.q) + at * hrow, ok);
             cp16z(smem_u32(&raw.gate[r][c * 4]), gate + at * vrow * 2, ok);
             cp16z(smem_u32(&raw.gate[r][64 + c * 4]), gate + at * vrow * 2 + 256, ok);
             if (c < SLICE / 8)
@@ -311,36 +311,43 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
                     cp_async_commit();
                 }
                 int calm = kCalm;  // steps in a row that were mild
-                Scales sc(a.scale);
-                for (int i = 0; i < steps; ++i) {
+                Scales sc;
+                bool again = false;  // a step a second time, as the planes' powers did not fit
+                for (int i = 0; i < steps;) {
                     const int st = i % kStages;
                     Stage &out = sm.stage[st];
                     cp_async_wait_newest<1>();
                     // the consumers are done with this stage's previous step (and its inputs)
-                    if (i >= kStages) bar_sync(BAR_EMPTY + st, kHalf + 32 * NW);
+                    if (i >= kStages && !again) bar_sync(BAR_EMPTY + st, kHalf + 32 * NW);
                     const RawStage &raw = sm.raw[i % kRaw];
-                    const bool try_mild = calm >= kCalm;
-                    if (!try_mild) find_largest(raw, out.pl, tid);
                     bar_sync(BAR_PREP, kHalf);
                     int form = GENERAL;
-                    if (try_mild &&
-                        !bar_or(BAR_PREP, kHalf, !prepare_mild(raw, out.pl, sc, tid)))
+                    if (calm >= kCalm && !again &&
+                        !bar_or(BAR_PREP, kHalf, !prepare_mild(raw, out.pl, sc, a.scale, tid))) {
                         form = MILD;
-                    if (form != MILD) {
-                        if (!sc.fit(out.pl)) sc.follow(out.pl, a.scale);
-                        const Seen f = prepare<kUp, 0>(raw, out.pl, out.g, sc, tid);
+                    } else {
+                        const Seen f =
+                            prepare<true, kUp, 0>(raw, out.pl, out.g, sc, a.scale, tid);
+                        const bool mild = __all_sync(0xffffffffu, f.mild && f.in_range);
+                        if (lane == 0) sm.mild[role.prep] = mild;
                         if (bar_or(BAR_PREP, kHalf, f.strong)) form = STRONG;
-                        const bool calm_now = f.mild && sc.fit_all(out.pl);
-                        calm = bar_or(BAR_PREP, kHalf, !calm_now) ? 0 : calm + 1;
+                        const bool off = bar_or(BAR_PREP, kHalf, !f.in_range);
+                        const int4 m = *reinterpret_cast<const int4 *>(sm.mild);
+                        calm = m.x && m.y && m.z && m.w ? calm + 1 : 0;
+                        again = off && !again && !sc.fit(out.pl, a.scale);
+                        if (again) {
+                            sc.follow(out.pl, a.scale);
+                            continue;
+                        }
                     }
                     if (tid == 0) {
-                        out.pl.kinv = sc.kinv;
-                        out.pl.qinv = sc.qinv;
+                        sc.put(out.pl);
                         out.form = form;
                     }
                     bar_arrive(BAR_PLANES + st, 2 * kHalf);
                     if (i + 2 < steps) in.load(sm, a, i + 2);
                     cp_async_commit();
+                    ++i;
                 }
                 cp_async_wait_all();
                 return;
