@@ -4,6 +4,7 @@ Each .cu under csrc/ is compiled to an object in parallel, then linked into
 ``gated_delta_rule_intra_gb300/libkda.so`` (git-ignored).  No CMake, no torch
 extension machinery: the library is a plain C-ABI shared object.  csrc/binding.cpp becomes
 ``_native.so``, compiled against the installed torch's headers next to it.
+(Only the short way into the recurrence, the single-token form and layer norm is in it.)
 ``build_debug_library()`` builds the same sources with ``-DKDA_DEBUG_CHECKS`` into
 ``libkda_debug.so``: every global index the kernels compute is checked against its
 buffer's extent and reported through ``kda_debug_set_flags`` (tests only).

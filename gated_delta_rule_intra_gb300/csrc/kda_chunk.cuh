@@ -247,8 +247,8 @@ __device__ __forceinline__ int by_length(int rank, int num_seqs, int T, const in
 
 // CTAs that a head's 128 dv columns are divided between: the fewest rounds over the SMs.  A
 // finer split repeats the preparation, but its step is shorter: a step of the precise forward
-// takes 4.7, 3.3 and 2.7 thousand cycles in one, two and four CTAs a head (prefill of T=2048: 298
-// us for 128 heads, 204 for 64, 169 for 32).  Of sequences of unknown lengths the longest is
+// takes 4.8, 3.3 and 2.8 thousand cycles in one, two and four CTAs a head (prefill of T=2048: 304
+// us for 128 heads, 204 for 64, 175 for 32).  Of sequences of unknown lengths the longest is
 // taken to be four times the average, and the others to fill in behind it (ten prompts of 1 to
 // 2609 tokens, 16 heads: 404 us in one CTA a head, 259 in two, 257 in four).
 inline int best_split(int num_seqs, int HV, const int *cu) {
@@ -376,7 +376,8 @@ __device__ __forceinline__ bool prep_planes(const RawStage &raw, char *planes, f
         const float2 x = *reinterpret_cast<const float2 *>(&raw.gate[r][2 * c2]);
         return make_float2(floor_gate(x.x), floor_gate(x.y));
     };
-    // g, and g_l - g as a sum of its own: gates of -160 add up to -2560, where FP32 has steps of 2^-12
+    // g, and g_l - g as a sum of its own: gates of -160 add up to -2560, where FP32 has steps of
+    // 2^-12
     float2 g = make_float2(0.f, 0.f), tail[kRows];
 #pragma unroll 8
     for (int r = 0; r < r0; ++r) g = add2(g, gate(r));

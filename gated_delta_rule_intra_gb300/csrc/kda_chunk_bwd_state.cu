@@ -5,8 +5,8 @@
 // other gradients of all slots at once.
 //
 // Bound by the time of a step on one SM, as the forward: B=8 T=2048 H=16 FP16 in one CTA a head
-// 340 us for 128 steps (5.4 thousand cycles); 9 packed sequences of up to 4096 tokens, 8 value
-// heads, in four CTAs a head 297 us for the longest's 256 (2.4).
+// 330 us for 128 steps (5.3 thousand cycles); 9 packed sequences of up to 4096 tokens, 8 value
+// heads, in four CTAs a head 302 us for the longest's 256 (2.4).
 #include <type_traits>
 
 #include "kda_chunk.cuh"

@@ -2,11 +2,11 @@
 // of its dv columns, in steps of 16 tokens (see kda_chunk.cuh for the mathematics).
 //
 // Warps have the same four parts as in kda_fast_fwd.cu; three BF16 products take the place of one
-// FP16 product.  Bound by the time of a step on one SM: 4.7, 3.3 and 2.6 thousand cycles with
+// FP16 product.  Bound by the time of a step on one SM: 4.8, 3.3 and 2.7 thousand cycles with
 // one, two and four CTAs a head.  In four, two consumer warps share 16 dv columns and have half of
-// dk each: their 48 + 24 products a step take a third of the 2.6, the rest is the preparation's
-// share of the issue slots (53% taken) and of the shared-memory pipe (62%), which every CTA of a
-// head repeats.  B=1 T=32768 H=32: 2.63 ms for 2048 steps; 37 tokens: 7.5 us.
+// dk each: their 48 + 24 products a step take a third of the 2.7, the rest is the preparation's
+// share of the issue slots (52% taken) and of the shared-memory pipe (61%), which every CTA of a
+// head repeats.  B=1 T=32768 H=32: 2.70 ms for 2048 steps; 37 tokens: 7.4 us.
 #include <type_traits>
 
 #include "kda_chunk.cuh"

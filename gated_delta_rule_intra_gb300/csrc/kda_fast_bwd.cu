@@ -9,7 +9,7 @@
 // memory).  Of a slot's 28 thousand cycles R takes 7, F 9, loads 5, preparing operands 3.5 and the
 // pairs' products 1; no unit is saturated: shared-memory pipe 63%, issue slots 40%, tensor cores
 // 26%.  Each warp's 16 rows read all of e, Y and do from shared memory.  Sixteen warps, R and F on
-// eight each, took longer (860 us).  B=8 T=4096 H=16: 763 us for 8192 slots, 2.4 TB/s.
+// eight each, took longer (860 us).  B=8 T=4096 H=16: 768 us for 8192 slots, 2.4 TB/s.
 #include "kda_fast.cuh"
 #include "kda_ops.h"
 

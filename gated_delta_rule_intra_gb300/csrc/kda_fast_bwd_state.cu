@@ -2,8 +2,8 @@
 // and kda_chunk_bwd_state.cu for what it computes): the state's gradient walks each
 // (sequence, value head) backwards in steps of 16 tokens.
 //
-// Bound as the forward is, by the time of a step on one SM: 3.2 thousand cycles with eight
-// consumers (B=8 T=4096 H=16: 403 us), 2.1 with four, 1.7 with two (B=2 T=1024 H=4: 54 us).
+// Bound as the forward is, by the time of a step on one SM: 3.1 thousand cycles with eight
+// consumers (B=8 T=4096 H=16: 388 us), 2.2 with four, 1.8 with two (B=2 T=1024 H=4: 57 us).
 // Nothing is solved here (T comes from the forward), so that two groups of four preparing warps,
 // each with every second step, keep ahead of the consumers.
 #include "kda_fast.cuh"

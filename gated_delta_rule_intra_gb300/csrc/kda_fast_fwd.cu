@@ -5,11 +5,11 @@
 // operand planes, four take the scores M and P, four solve the steps' triangular systems in
 // turn, and eight (or four) consumers with 16 dv columns of the state each take the products.
 // The walk is a chain, R -> e -> n -> S', so what bounds it is the time of one step on one SM:
-// 3.6 thousand cycles with eight consumers, 2.7 with four.  A consumer's own 58 products are 0.5
-// of these; the rest is shared by the issue slots and the shared-memory pipe (both 55% taken) and
+// 3.7 thousand cycles with eight consumers, 2.9 with four.  A consumer's own 58 products are 0.5
+// of these; the rest is shared by the issue slots and the shared-memory pipe (52% and 57% taken) and
 // the chain's latencies.  With nothing but the consumers a step would take half as long.
-// B=8 T=4096 H=16: 447 us for 256 steps, B=2 T=1024 H=4: 86 us for 64; with gates too strong for
-// the mild form 498 and 98.
+// B=8 T=4096 H=16: 453 us for 256 steps, B=2 T=1024 H=4: 89 us for 64; with gates too strong for
+// the mild form 504 and 101.
 #include <type_traits>
 
 #include "kda_fast.cuh"
@@ -105,7 +105,9 @@ template <int SLICE> struct Loader {
 };
 
 // P's power of two: no entry is above 128 times the planes' largest elements, 2^13 with this.
-__device__ __forceinline__ float p_scale(const Planes &p) { return 4.f * inverse_of(p.kinv * p.qinv); }
+__device__ __forceinline__ float p_scale(const Planes &p) {
+    return 4.f * inverse_of(p.kinv * p.qinv);
+}
 
 // An entry of P (zero above the diagonal), `f` times as large in FP16.
 __device__ __forceinline__ void put_p(Stage &out, char *pt, int r, int s, float x, float f) {
@@ -569,7 +571,7 @@ cudaError_t launch(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
 }
 
 template <bool SAVE> cudaError_t launch_split(const ChunkFwdArgs &a, int dev, cudaStream_t stream) {
-    // A step takes 3.6 thousand cycles in one CTA a head and 2.7 in two.  In four it takes
+    // A step takes 3.7 thousand cycles in one CTA a head and 2.9 in two.  In four it takes
     // as long: the preparation bounds it from two on.
     return chunk::best_split(a.num_seqs, a.HV, a.cu_seqlens) == 1
                ? launch<8, SAVE>(a, dev, stream)

@@ -168,7 +168,6 @@ template <int N> __device__ __forceinline__ float lanes_sum(float x) {
     return x;
 }
 
-// Threads of a row for a width, 0 when one CTA's registers do not hold it.
 inline int esize(int dtype) { return dtype == NORM_FP32 ? 4 : 2; }
 
 // Threads of a row, e elements each; 0 when one CTA's registers do not hold it.

@@ -403,7 +403,9 @@ kda_status_t kda_chunk_fwd(const void *q, const void *k, const void *v, const fl
  *                    is the forward's too, and tells how it was written
  *   workspace        kda_chunk_bwd_workspace_bytes() bytes, 256-byte aligned
  * Accuracy: within a rounding to dtype plus 1e-4, the initial state's gradient within 1e-5;
- * after a BF16 forward without a state a rounding plus 1e-3 (and 1e-3).
+ * after a BF16 forward that took the 11-bit operands a rounding plus 1e-3 (and 1e-3).  dgate and
+ * dbeta are sums that may cancel: what they are within is then that share of their terms (of
+ * |q dq| + |k dk|, and of |dv / beta| |v - S~^T k|).
  */
 typedef struct {
     int HV;
