@@ -44,8 +44,7 @@ class Recurrence(torch.autograd.Function):
     @staticmethod
     def backward(ctx, do):
         *inputs, saved = ctx.saved_tensors
-        dq, dk, dv, dgate, dbeta, _ = kda.kda_chunk_bwd(*inputs, do.contiguous(), saved)
-        return dq, dk, dv, dgate.float(), dbeta.float()
+        return kda.kda_chunk_bwd(*inputs, do.contiguous(), saved, gate_grads_fp32=True)[:5]
 
 
 class Layer(torch.nn.Module):

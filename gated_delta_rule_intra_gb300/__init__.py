@@ -46,7 +46,7 @@ DEBUG_LIB_PATH = os.path.join(_HERE, "libkda_debug.so")
 
 # KDA_ABI_VERSION of the include/kda.h these ctypes mirrors follow (option structs,
 # signatures); a library of any other version is refused at load.
-ABI_VERSION = 10
+ABI_VERSION = 11
 KDA_OK = 0
 KDA_BF16 = 0
 KDA_FP16 = 1

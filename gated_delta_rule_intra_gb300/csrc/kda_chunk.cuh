@@ -207,6 +207,14 @@ __device__ __forceinline__ bool state_ok(const Args &a, const void *p, size_t at
     return !p || dbg_ok(a.dbg, at / (D * D) * (D * D) + D * D - 1, a.states, bit);
 }
 
+// An element of dbeta: FP32, or what it is in 16 bits.
+__device__ __forceinline__ void put_dbeta(const ChunkBwdArgs &a, size_t at, float x, uint16_t x16) {
+    if (a.gates32)
+        ((float *)a.dbeta)[at] = x;
+    else
+        ((uint16_t *)a.dbeta)[at] = x16;
+}
+
 // Asks a unit's rows of q, k and do (two lines each) and of the gate (four) into L2.
 __device__ __forceinline__ void prefetch_rows(const ChunkBwdArgs &a, const Where &w, int tid,
                                               int threads) {

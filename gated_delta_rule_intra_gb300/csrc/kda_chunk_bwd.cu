@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
                         if (warp < 4)
                             sm.diag[t] = d;
                         else if (t < rows && token_ok(a, row0 + t))
-                            ((uint16_t *)a.dbeta)[(size_t)(row0 + t) * a.HV + hv] = to16<T16>(d);
+                            put_dbeta(a, (size_t)(row0 + t) * a.HV + hv, d, to16<T16>(d));
                     }
                 }
         }
@@ -546,7 +546,19 @@ __global__ void __launch_bounds__(kThreads, 1) kda_chunk_bwd_kernel(const ChunkB
                           (char *)((uint16_t *)out + out_at + (size_t)j * C * orow), orow * 2,
                           rows - j * C, (char *)out, a.rows_o * D * 2, a.dbg, lane);
             };
-            put(a.dgate, 0, dg);
+            if (!a.gates32) {
+                put(a.dgate, 0, dg);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const int t = j * C + token_of(p, tc2);
+                        const size_t at = out_at + (size_t)t * orow + 8 * i + gr;
+                        if (t < rows && dbg_ok(a.dbg, at, a.rows_o * D, DBG_STORE))
+                            ((float *)a.dgate)[at] = dg.v[i][p];
+                    }
+            }
             if (!a.dq_hv) {
                 put(a.dq, 1, dq);
                 put(a.dk, 2, dk);

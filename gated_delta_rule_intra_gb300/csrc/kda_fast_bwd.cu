@@ -9,7 +9,7 @@
 // memory).  Of a slot's 28 thousand cycles R takes 7, F 9, loads 5, preparing operands 3.5 and the
 // pairs' products 1; no unit is saturated: shared-memory pipe 63%, issue slots 40%, tensor cores
 // 26%.  Each warp's 16 rows read all of e, Y and do from shared memory.  Sixteen warps, R and F on
-// eight each, took longer (860 us).  B=8 T=4096 H=16: 768 us for 8192 slots, 2.4 TB/s.
+// eight each, took longer (860 us).  B=8 T=4096 H=16: 775 us for 8192 slots, 2.4 TB/s.
 #include "kda_fast.cuh"
 #include "kda_ops.h"
 
@@ -366,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
                         if (warp < 4)
                             sm.diag[t] = d;
                         else if (t < rows && chunk::token_ok(a, row0 + t))
-                            ((uint16_t *)a.dbeta)[(size_t)(row0 + t) * a.HV + hv] =
-                                (uint16_t)(pack_bf16(d, 0.f) & 0xffffu);
+                            chunk::put_dbeta(a, (size_t)(row0 + t) * a.HV + hv, d,
+                                      (uint16_t)(pack_bf16(d, 0.f) & 0xffffu));
                     }
                 }
         }
@@ -626,7 +626,19 @@ __global__ void __launch_bounds__(kThreads, 1) kda_fast_bwd_kernel(const ChunkBw
                                     orow * 2, rows - j * C, (char *)out, a.rows_o * D * 2, a.dbg,
                                     lane);
             };
-            put(a.dgate, 0, dg);
+            if (!a.gates32) {
+                put(a.dgate, 0, dg);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const int t = j * C + token_of(p, tc2);
+                        const size_t at = out_at + (size_t)t * orow + 8 * i + gr;
+                        if (t < rows && dbg_ok(a.dbg, at, a.rows_o * D, DBG_STORE))
+                            ((float *)a.dgate)[at] = dg.v[i][p];
+                    }
+            }
             if (!a.dq_hv) {
                 put(a.dq, 1, dq);
                 put(a.dk, 2, dk);

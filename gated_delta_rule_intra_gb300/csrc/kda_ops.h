@@ -41,6 +41,7 @@ struct ChunkBwdArgs {
     float *dscales;
     bool fast;                           // BF16 training (kda_fast.cuh)
     float *dq_hv, *dk_hv;                // workspace [rows, HV, 128], only when HV > H
+    bool gates32;                        // dgate and dbeta are FP32
     int B, T, H, HV, num_seqs, slots;
     const int *cu_seqlens;
     float scale;

@@ -196,9 +196,12 @@ kda_status_t kda_chunk_bwd(const void *q, const void *k, const float *gate, cons
     if (dtype != KDA_BF16 && dtype != KDA_FP16) return KDA_ERR_DTYPE;
     const void *a16[] = {q, k, gate, dout, dq, dk, dv, dgate, op.d_final_state,
                          op.d_initial_state};
-    const void *a4[] = {beta, op.cu_seqlens}, *a2[] = {dbeta};
+    const bool zero_rest = op.zero_rest & 1, gates32 = op.zero_rest & KDA_GATE_GRADS_FP32;
+    const size_t gs = gates32 ? 4 : 2;  // bytes of an element of dgate and dbeta
+    const void *a4[] = {beta, op.cu_seqlens}, *ab[] = {dbeta};
     const void *a256[] = {op.saved, op.workspace};
-    if (misaligned(a16, 16) || misaligned(a4, 4) || misaligned(a2, 2) || misaligned(a256, 256))
+    if (misaligned(a16, 16) || misaligned(a4, 4) || misaligned(ab, (unsigned)gs) ||
+        misaligned(a256, 256))
         return KDA_ERR_ALIGN;
     const int mode = saved_mode(B, T, HV, op.num_seqs, dtype, op.saved_bytes);
     if (mode < 0) return KDA_ERR_WORKSPACE;
@@ -215,16 +218,16 @@ kda_status_t kda_chunk_bwd(const void *q, const void *k, const float *gate, cons
                         {gate, rv * KDA_K * 4}, {beta, rv * 4}, {op.d_final_state, states},
                         {op.cu_seqlens, varlen ? ((size_t)seqs + 1) * 4 : 0}, {op.saved, saved}};
     const Range out[] = {{dq, rq * KDA_K * 2}, {dk, rq * KDA_K * 2}, {dv, rv * KDA_K * 2},
-                         {dgate, rv * KDA_K * 2}, {dbeta, rv * 2}, {op.d_initial_state, states},
+                         {dgate, rv * KDA_K * gs}, {dbeta, rv * gs}, {op.d_initial_state, states},
                          {op.workspace, work}};
     if (overlap(out, in)) return KDA_ERR_OVERLAP;
     if ((st = kda::require_device()) != KDA_OK) return st;
     (void)cudaGetLastError();
     if (T == 0 && !op.d_initial_state) return KDA_OK;
-    if (varlen && op.zero_rest) {
+    if (varlen && zero_rest) {
         const size_t head = KDA_K * 2;
         const kda::ZeroArgs z = {{dq, dk, dv, dgate, dbeta},
-                                 {H * head, H * head, HV * head, HV * head, (size_t)HV * 2},
+                                 {H * head, H * head, HV * head, HV * KDA_K * gs, HV * gs},
                                  5, T, seqs, op.cu_seqlens, kda::debug_flags()};
         const cudaError_t e = kda::launch_zero_rest(z, (cudaStream_t)stream);
         if (e != cudaSuccess) return finish(e);
@@ -249,6 +252,7 @@ kda_status_t kda_chunk_bwd(const void *q, const void *k, const float *gate, cons
         a.dq_hv = (float *)((char *)op.workspace + up256(n * s.work()));
         a.dk_hv = a.dq_hv + rv * KDA_K;
     }
+    a.gates32 = gates32;
     a.B = B; a.T = T; a.H = H; a.HV = HV; a.num_seqs = seqs;
     a.slots = (int)slots;
     a.cu_seqlens = op.cu_seqlens;

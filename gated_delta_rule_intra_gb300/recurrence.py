@@ -151,29 +151,29 @@ def _chunk_fwd(q, k, v, gate, beta, scale, initial_state, output_final_state, sa
 
 def kda_chunk_bwd(q, k, v, gate, beta, do, saved, scale=None, d_final_state=None, *,
                   output_d_initial_state=False, cu_seqlens=None, dq=None, dk=None, dv=None,
-                  dgate=None, dbeta=None, stream=None):
+                  dgate=None, dbeta=None, gate_grads_fp32=False, stream=None):
     """Gradients of ``kda_chunk_fwd``.  Returns (dq, dk, dv, dgate, dbeta, d_initial_state).
 
     The five inputs, ``scale`` and ``cu_seqlens`` as given to the forward, do like its o,
-    ``saved`` what it returned with ``save=True`` (read only).  The gradients are in q's dtype;
-    dq and dk are summed over the value heads of their head.  ``d_final_state`` (fp32, the
+    ``saved`` what it returned with ``save=True`` (read only).  The gradients are in q's dtype,
+    dgate and dbeta in fp32 with ``gate_grads_fp32`` (as gate and beta themselves are); dq and dk are summed over the value heads of their head.  ``d_final_state`` (fp32, the
     final state's shape) defaults to zeros; d_initial_state (fp32) is None unless
     ``output_d_initial_state``.  Deterministic.
     """
     if (stream is None and cu_seqlens is None and d_final_state is None
             and not output_d_initial_state and dq is None and dk is None and dv is None
-            and dgate is None and dbeta is None):
+            and dgate is None and dbeta is None and not gate_grads_fp32):
         out = library().quick_chunk_bwd(q, k, v, gate, beta, do, saved, scale)
         if out is not None:
             return out
     return _chunk_bwd(q, k, v, gate, beta, do, saved, scale, d_final_state,
                       output_d_initial_state, cu_seqlens, (dq, dk, dv, dgate, dbeta),
-                      stream=stream)
+                      gate_grads_fp32, stream=stream)
 
 
 @takes_stream
 def _chunk_bwd(q, k, v, gate, beta, do, saved, scale, d_final_state, output_d_initial_state,
-               cu_seqlens, given):
+               cu_seqlens, given, gate_grads_fp32=False):
     H, HV, dev = _inputs("kda_chunk_bwd", q, k, v, gate, beta, 2)
     B, T, dt = q.shape[0], q.shape[1], q.dtype
     N = _seqs(cu_seqlens, B, dev)
@@ -187,14 +187,16 @@ def _chunk_bwd(q, k, v, gate, beta, do, saved, scale, d_final_state, output_d_in
     zero_rest = all(t is None for t in given)
     new = torch.zeros_like if N and not zero_rest else torch.empty_like
     out = []
-    for name, t, like in zip(("dq", "dk", "dv", "dgate", "dbeta"), given, (q, k, v, v, beta)):
+    gdt = F32 if gate_grads_fp32 else dt
+    for name, t, like, ty in zip(("dq", "dk", "dv", "dgate", "dbeta"), given,
+                                 (q, k, v, gate, beta), (dt, dt, dt, gdt, gdt)):
         if t is None:
-            t = new(like) if like is not beta else new(like, dtype=dt)
+            t = new(like, dtype=ty)
         else:
-            check(name, t, like.shape, dt, dev)
+            check(name, t, like.shape, ty, dev)
         out.append(t)
     op = ChunkBwdOpts(HV=HV, scale=_scale(scale), saved=saved.data_ptr(), saved_bytes=saved_bytes,
-                      zero_rest=zero_rest)
+                      zero_rest=zero_rest + (2 if gate_grads_fp32 else 0))
     if N:
         op.num_seqs, op.cu_seqlens = N, cu_seqlens.data_ptr()
     if d_final_state is not None:

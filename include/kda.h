@@ -69,6 +69,8 @@ extern "C" {
 
 /*
  * ABI versions (kda_abi_version() returns the loaded library's):
+ *   11 kda_chunk_bwd's zero_rest also takes KDA_GATE_GRADS_FP32, kda_chunk_fwd's saved either
+ *      of its sizes in BF16 calls without a state
  *   10 kda_chunk_fwd, kda_chunk_bwd, kda_step, kda_layer_norm_fwd, kda_layer_norm_bwd
  *      and their option structs and size queries
  *   9  kda_intra_bwd_opts_t gains split_tf32 (appended; the struct grew)
@@ -86,7 +88,7 @@ extern "C" {
  * must check at start-up that kda_abi_version() equals the KDA_ABI_VERSION it was
  * compiled with (the Python binding refuses to load any other version).
  */
-#define KDA_ABI_VERSION 10
+#define KDA_ABI_VERSION 11
 #define KDA_BT 64  /* chunk length */
 #define KDA_BC 16  /* sub-block length inside a chunk */
 #define KDA_K 128  /* head dimension */
@@ -397,6 +399,8 @@ kda_status_t kda_chunk_fwd(const void *q, const void *k, const void *v, const fl
  * dbeta [B, T, HV], all in dtype, rounded once from FP32 sums; all 16-byte aligned but beta (4)
  * and dbeta (2).  q, k, gate, beta, scale, HV and cu_seqlens as given to the forward (zero_rest
  * as there, for all five).  No atomics: the same inputs give the same bits.
+ *   zero_rest        1 and, or alone, KDA_GATE_GRADS_FP32: dgate and dbeta are fp32 (dbeta then
+ *                    4-byte aligned), not rounded to dtype
  *   d_final_state    gradient of the final state, [sequences, HV, 128, 128] fp32, NULL = zeros
  *   d_initial_state  gradient of the initial state, the same shape, written; NULL = not wanted
  *   saved            the forward's, read only (a backward may run again from it); saved_bytes
@@ -407,6 +411,8 @@ kda_status_t kda_chunk_fwd(const void *q, const void *k, const void *v, const fl
  * dbeta are sums that may cancel: what they are within is then that share of their terms (of
  * |q dq| + |k dk|, and of |dv / beta| |v - S~^T k|).
  */
+#define KDA_GATE_GRADS_FP32 2
+
 typedef struct {
     int HV;
     float scale;
