@@ -348,13 +348,16 @@ kda_status_t kda_intra_fwd_ex(const void *q, const void *k, const float *g,
  *   beta        [B, T, HV]       fp32
  * HV is a multiple of H; value head hv reads q/k head hv / (HV / H).  Any T >= 0.
  *
- * Accuracy (2-norm of the error over 2-norm of the result): states, sums and the solve are
+ * Accuracy (2-norm of the error over 2-norm of the result, of some dozen tokens; of a few whose
+ * q.k or S^T q cancels, that share of |q| |k| |v| and |S| |q|): states, sums and the solve are
  * FP32.  Calls that take or return a state, and FP16 ones, take every product of FP32 values
  * in three BF16 tensor-core products: o within a rounding to dtype plus 1e-5, the final state
- * within 1e-5.  BF16 calls without a state (training) take one FP16 product with operands of
- * 11 bits, each with a power of two of its own (q and k one a step of 16 tokens): o within a
- * rounding to BF16 plus 1e-3, for values between 2^-80 and 2^100.  A caller who wants the former
- * there passes `saved` of a call with a state (or takes the final state): the size chooses.
+ * within 1e-5 (up to twice that when it holds a few tokens only).  BF16 calls without a state
+ * (training) take one FP16 product with operands of 11 bits, each with a power of two of its
+ * own: o within a rounding to BF16 plus 1e-3, for values between 2^-80 and 2^100.  q and k have
+ * one power each a step of 16 tokens: of a token below 2^-6 of the step's largest bits are lost.
+ * A caller who wants the former there passes `saved` of a call with a state (or takes the final
+ * state): the size chooses.
  *
  * Options (zero-initialise; NULL = none):
  *   HV             0 means HV = H
