@@ -156,8 +156,9 @@ def kda_chunk_bwd(q, k, v, gate, beta, do, saved, scale=None, d_final_state=None
 
     The five inputs, ``scale`` and ``cu_seqlens`` as given to the forward, do like its o,
     ``saved`` what it returned with ``save=True`` (read only).  The gradients are in q's dtype,
-    dgate and dbeta in fp32 with ``gate_grads_fp32`` (as gate and beta themselves are); dq and dk are summed over the value heads of their head.  ``d_final_state`` (fp32, the
-    final state's shape) defaults to zeros; d_initial_state (fp32) is None unless
+    dgate and dbeta in fp32 with ``gate_grads_fp32`` (as gate and beta themselves are); dq and
+    dk are summed over the value heads of their head.  ``d_final_state`` (fp32, the final
+    state's shape) defaults to zeros; d_initial_state (fp32) is None unless
     ``output_d_initial_state``.  Deterministic.
     """
     if (stream is None and cu_seqlens is None and d_final_state is None

@@ -495,10 +495,10 @@ const char *kda_status_str(kda_status_t status);
  * build script's libkda_debug.so) check every global index their kernels compute
  * (output stores, incoming-gradient and beta reads, chunk-table reads; of the recurrence
  * and layer norm the tokens and rows that are read, states, and the slots of saved and
- * workspace buffers too) against the extent of its buffer.  An index out of range sets KDA_DBG_STORE or KDA_DBG_LOAD in a
- * caller-owned device word and the access is skipped; a bounded wait that gives up sets
- * KDA_DBG_WAIT.  Nothing traps or asserts.  TMA tiles need no check: the tensor maps
- * clip them.
+ * workspace buffers too) against the extent of its buffer.  An index out of range sets
+ * KDA_DBG_STORE or KDA_DBG_LOAD in a caller-owned device word and the access is skipped;
+ * a bounded wait that gives up sets KDA_DBG_WAIT.  Nothing traps or asserts.  TMA tiles
+ * need no check: the tensor maps clip them.
  *
  * kda_debug_checks() is 1 in such a build, 0 otherwise.  kda_debug_set_flags(word)
  * makes every later launch of this library report into `word` (device memory, 4 bytes,
