@@ -23,6 +23,12 @@ The functions carry the C names of ``include/kda.h``:
   sequences, forward and backward (``recurrence.py``)
 * ``kda_step``            -- its single-token form, states updated in place
 * ``kda_layer_norm_fwd``, ``kda_layer_norm_bwd`` -- layer norm (``norm.py``)
+* ``kda_conv_fwd``, ``kda_conv_bwd``, ``kda_conv_step`` -- the short causal convolution
+  (``conv.py``)
+* ``kda_scan_fwd``, ``kda_scan_bwd``, ``kda_scan_step`` -- the selective state-space scan
+  (``scan.py``)
+* ``kda_linear_fwd``, ``kda_linear_bwd`` -- matrix product with bias, activation and residual
+  in its epilogue (``linear.py``)
 * ``kda_status_str``, ``kda_abi_version``
 * ``use_library``, ``kda_debug_checks``, ``kda_debug_set_flags`` -- run the same calls
   through the bounds-checked debug build ``libkda_debug.so`` (tests)
@@ -37,8 +43,11 @@ import os
 import torch
 
 from . import _common
+from .conv import kda_conv_bwd, kda_conv_fwd, kda_conv_step
+from .linear import kda_linear_bwd, kda_linear_fwd
 from .norm import kda_layer_norm_bwd, kda_layer_norm_fwd
 from .recurrence import kda_chunk_bwd, kda_chunk_fwd, kda_step
+from .scan import kda_scan_bwd, kda_scan_fwd, kda_scan_step
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkda.so")
@@ -46,7 +55,7 @@ DEBUG_LIB_PATH = os.path.join(_HERE, "libkda_debug.so")
 
 # KDA_ABI_VERSION of the include/kda.h these ctypes mirrors follow (option structs,
 # signatures); a library of any other version is refused at load.
-ABI_VERSION = 11
+ABI_VERSION = 12
 KDA_OK = 0
 KDA_BF16 = 0
 KDA_FP16 = 1

@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import sys
 import warnings
 
@@ -12,6 +13,7 @@ import torch
 KDA_BF16, KDA_FP16, KDA_FP32 = 0, 1, 2
 DTYPES16 = {torch.bfloat16: KDA_BF16, torch.float16: KDA_FP16}
 DTYPES = {**DTYPES16, torch.float32: KDA_FP32}
+ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2, "relu": 3}
 K = 128
 F32 = torch.float32
 
@@ -36,6 +38,59 @@ def check(name, t, shape, dtype, index):
     if t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     raise ValueError(f"{name} must be contiguous")
+
+
+def row_stride(name, t, shape, dtype, index, tail=1):
+    """Elements between the rows of a tensor of that shape and type on CUDA device `index`, whose
+    last `tail` dimensions are one contiguous row and whose leading ones are one evenly spaced run
+    of rows (a column slice of a wider tensor will do)."""
+    if fits(t, shape, dtype, index):
+        return math.prod(shape[len(shape) - tail:])
+    if t.get_device() != index or t.shape != shape or t.dtype is not dtype:
+        check(name, t, shape, dtype, index)
+    width = 1
+    for n, s in zip(reversed(t.shape[-tail:]), reversed(t.stride()[-tail:])):
+        if n > 1 and s != width:
+            raise ValueError(f"{name}'s last dimension must be contiguous")
+        width *= n
+    step = None  # every leading dimension has to continue the one behind it
+    for n, s in zip(reversed(t.shape[:-tail]), reversed(t.stride()[:-tail])):
+        if n == 1:
+            continue
+        if step is None:
+            step, run = s, n * s
+        elif s == run:
+            run = n * s
+        else:
+            raise ValueError(f"{name}'s rows must be evenly spaced")
+    if step is None or t.numel() == 0:
+        return width
+    if step < width:
+        raise ValueError(f"{name}'s rows must not overlap")
+    return step
+
+
+def sequences(cu_seqlens, B, index):
+    """Sequences that are packed along T (0 without cu_seqlens)."""
+    if cu_seqlens is None:
+        return 0
+    if B != 1:
+        raise ValueError("cu_seqlens packs sequences along T: B must be 1")
+    if cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must have at least two entries")
+    check("cu_seqlens", cu_seqlens, (cu_seqlens.numel(),), torch.int32, index)
+    return cu_seqlens.numel() - 1
+
+
+def ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def activation_code(activation, allowed):
+    if activation not in allowed:
+        names = ", ".join("None" if a is None else repr(a) for a in allowed)
+        raise ValueError(f"activation must be one of {names}, got {activation!r}")
+    return ACTIVATIONS[activation]
 
 
 def takes_stream(fn):
@@ -73,7 +128,7 @@ def run(name, index, *args):
 
 
 def declare(lib):
-    """ctypes signatures of the recurrence, single-token and layer-norm entry points."""
+    """ctypes signatures of the entry points around the intra-chunk calls."""
     vp, i, ll, z, f = (ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t,
                        ctypes.c_float)
     for name, res, args in (
@@ -84,7 +139,22 @@ def declare(lib):
             ("kda_step", i, [vp] * 7 + [i] * 3 + [vp, vp]),
             ("kda_layer_norm_fwd", i, [vp] * 6 + [ll, i, f, i, i, ll, ll, vp]),
             ("kda_layer_norm_bwd_workspace_bytes", z, [ll, i]),
-            ("kda_layer_norm_bwd", i, [vp] * 8 + [ll, i, i, i, ll, ll, ll, vp, z, vp])):
+            ("kda_layer_norm_bwd", i, [vp] * 8 + [ll, i, i, i, ll, ll, ll, vp, z, vp]),
+            ("kda_conv_fwd", i, [vp] * 4 + [i] * 7 + [vp, vp]),
+            ("kda_conv_bwd_workspace_bytes", z, [i] * 5),
+            ("kda_conv_bwd", i, [vp] * 7 + [i] * 7 + [vp, vp]),
+            ("kda_conv_step", i, [vp] * 5 + [i] * 6 + [vp, vp]),
+            ("kda_scan_saved_bytes", z, [i] * 5),
+            ("kda_scan_fwd_workspace_bytes", z, [i] * 6),
+            ("kda_scan_fwd", i, [vp] * 6 + [i] * 6 + [vp, vp]),
+            ("kda_scan_bwd_workspace_bytes", z, [i] * 6),
+            ("kda_scan_bwd", i, [vp] * 11 + [i] * 6 + [vp, vp]),
+            ("kda_scan_step", i, [vp] * 7 + [i] * 5 + [vp, vp]),
+            ("kda_linear_copies", i, [vp, ll, vp, ll, vp, ll]),
+            ("kda_linear_fwd_workspace_bytes", z, [i] * 4),
+            ("kda_linear_fwd", i, [vp] * 3 + [i] * 4 + [vp, vp]),
+            ("kda_linear_bwd_workspace_bytes", z, [i] * 6),
+            ("kda_linear_bwd", i, [vp] * 6 + [i] * 4 + [vp, vp])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
     _declare_quick(lib)
@@ -115,6 +185,8 @@ def _declare_quick(lib):
             ("layer_norm_fwd", ("kda_layer_norm_fwd",)),
             ("layer_norm_bwd", ("kda_layer_norm_bwd", "kda_layer_norm_bwd_workspace_bytes"))):
         setattr(lib, "quick_" + name, quick(name, fns))
+    for name in ("conv_fwd", "conv_bwd", "conv_step", "scan_fwd", "scan_step", "linear_fwd"):
+        setattr(lib, "quick_" + name, lambda *a: None)
 
 
 @functools.cache

@@ -1,0 +1,505 @@
+// Matrix product with its epilogue on the tensor cores: C = A B^T, y = act(C + bias) + residual.
+//
+// Persistent, one CTA an SM, by role: one warp asks for the operands' tiles (TMA, 128-byte swizzle,
+// [128 x 64] of A and [BN x 64] of B a stage), one issues the products (tcgen05.mma, M = 128, N =
+// BN, accumulators in tensor memory), four take the accumulators out and finish them.  There are
+// two accumulators, so that a tile's products run while the one before it is finished.  Operands
+// may lie either way round: contracted along their rows' direction (K-major, boxes of 64 k) or
+// across it (MN-major, boxes of 64 columns x 64 k), which is what the gradients need of the
+// same tensors.  Where the tiles of C are too few for the card, the contraction is cut into parts
+// whose sums a second kernel joins, always in the same order.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <type_traits>
+
+#include "kda_linear.cuh"
+#include "tc_ptx.cuh"
+
+namespace kda {
+namespace linear {
+namespace {
+
+constexpr int BM = 128, BK = 64;
+constexpr int kThreads = 192;              // warps: copies, products, 4 of the epilogue
+constexpr uint32_t kWaitPolls = 1u << 22;  // then the kernel gives up (and writes NaN)
+
+template <int BN> struct Cfg {
+    static constexpr int kA = BM * BK * 2, kB = BN * BK * 2, kStage = kA + kB;
+    static constexpr int kStages = BN == 256 ? 4 : 6;
+    static constexpr int kOut = 4 * 4096;  // a [32 rows x 64 columns] box of each epilogue warp
+    static constexpr int kBias = 4 * BN * 4;
+    static constexpr int kBytes = 1024 + kStages * kStage + kOut + kBias + 256;
+    static constexpr int kColumns = 2 * BN;  // of tensor memory
+};
+
+struct Maps {
+    CUtensorMap a, b, y, pre;
+};
+
+struct Params {
+    int M, N, K, nt, tiles, splits, per;  // tiles across N; of C; parts of K, blocks of 64 of each
+    const void *bias, *residual;
+    void *y, *pre;
+    long long ldr, ldy, ldp;
+    int act, split_n;
+    float *partial;  // [splits][M][ldw], or null
+    int ldw;
+    bool tma_out, wide_r;  // y and pre leave by TMA; residual's rows are on 16-byte boundaries
+    unsigned *dbg;
+};
+
+// Shared-memory descriptor, 128-byte swizzle: K-major sbo = 1024 (eight rows); MN-major sbo = 1024
+// (eight k), lbo = from 64 columns to the next.
+__device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return tc::smem_desc(addr, lbo, sbo) | (uint64_t)2 << 61;
+}
+// FP32 sums of 16-bit operands.
+constexpr uint32_t idesc16(bool fp16, bool a_mn, bool b_mn, int n) {
+    return 1u << 4 | (fp16 ? 0u : 1u) << 7 | (fp16 ? 0u : 1u) << 10 | (uint32_t)a_mn << 15 |
+           (uint32_t)b_mn << 16 | (uint32_t)(n >> 3) << 17 | (uint32_t)(BM >> 4) << 24;
+}
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(tc::smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void store_2d(const CUtensorMap *map, uint32_t src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+          "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+          "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]),
+          "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
+          "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+struct Tile {
+    int m, n, kb, ke;  // first row and column, blocks of K
+};
+// Tiles go down 16 rows of tiles before the next column, so that those at work at one time share
+// both operands' tiles in L2.
+__device__ __forceinline__ Tile tile_of(const Params &p, int i, int BN) {
+    Tile t;
+    const int s = i / p.tiles, j = i - s * p.tiles, mt = p.tiles / p.nt;
+    const int group = j / (16 * p.nt), rows = min(16, mt - group * 16), r = j - group * 16 * p.nt;
+    t.m = (group * 16 + r % rows) * BM;
+    t.n = r / rows * BN;
+    t.kb = s * p.per;
+    t.ke = min(t.kb + p.per, (p.K + BK - 1) / BK);
+    return t;
+}
+
+template <int V> __device__ __forceinline__ void activate_all(float (&v)[V], int act) {
+    if (act == ACT_SILU) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = activate(v[j], ACT_SILU);
+    } else if (act == ACT_GELU) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = activate(v[j], ACT_GELU);
+    } else if (act == ACT_RELU) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = activate(v[j], ACT_RELU);
+    }
+}
+
+// Elements of a row to (or from) a swizzled [32][64] box, where the row is not on a 16-byte boundary:
+// `pair` if it is on a 4-byte one.
+template <typename T>
+__device__ __forceinline__ void box_out(const char *box, void *base, long long ld, int m, int n, int M,
+                                        int N, int lane, bool pair) {
+    const int rows = min(32, M - m);
+    for (int r = 0; r < rows; ++r) {
+        const uint32_t x = *(const uint32_t *)(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+        uint16_t *to = (uint16_t *)base + (size_t)(m + r) * ld + n + 2 * lane;
+        if (pair && n + 2 * lane + 1 < N) {
+            *(uint32_t *)to = x;
+        } else {
+            if (n + 2 * lane < N) to[0] = (uint16_t)x;
+            if (n + 2 * lane + 1 < N) to[1] = (uint16_t)(x >> 16);
+        }
+    }
+}
+__device__ __forceinline__ void box_in(char *box, const void *base, long long ld, int m, int n, int M,
+                                       int N, int lane, bool wide) {
+    const int rows = min(32, M - m);
+    if (wide) {  // eight lanes a row, 16 bytes each
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3), c = lane & 7;
+            if (r < rows && n + c * 8 < N)
+                *(uint4 *)(box + r * 128 + ((c ^ (r & 7)) << 4)) =
+                    *(const uint4 *)((const uint16_t *)base + (size_t)(m + r) * ld + n + c * 8);
+        }
+        return;
+    }
+    for (int r = 0; r < rows; ++r) {
+        const uint16_t *at = (const uint16_t *)base + (size_t)(m + r) * ld + n + 2 * lane;
+        uint32_t x = 0;
+        if (n + 2 * lane < N) x = at[0];
+        if (n + 2 * lane + 1 < N) x |= (uint32_t)at[1] << 16;
+        *(uint32_t *)(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) = x;
+    }
+}
+
+template <typename T, bool A_MN, bool B_MN, int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    kda_linear_kernel(const __grid_constant__ Maps maps, const Params p) {
+    wait_for_previous();
+    using C = Cfg<BN>;
+    extern __shared__ char raw[];
+    char *base = (char *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    char *out = base + C::kStages * C::kStage;
+    float *bias = (float *)(out + C::kOut);
+    uint64_t *full = (uint64_t *)((char *)bias + C::kBias), *empty = full + C::kStages;
+    uint64_t *done = empty + C::kStages, *taken = done + 2;
+    uint32_t *slot = (uint32_t *)(taken + 2);
+    volatile uint32_t *broken = slot + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int work = p.tiles * p.splits;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            tc::mbar_init(full + i, 1);
+            tc::mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(done + i, 1);
+            tc::mbar_init(taken + i, 4);
+        }
+        *broken = 0;
+    }
+    if (warp == 1) tc::tmem_alloc(slot, C::kColumns);
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *slot;
+    // A wait that gives up ends this CTA's work; the other warps learn of it here.
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (*broken) return false;
+        if (tc::mbar_wait(bar, parity, kWaitPolls)) return true;
+        *broken = 1;
+        dbg_flag(p.dbg, true, DBG_WAIT);
+        return false;
+    };
+    if (warp == 0) {
+        if (lane == 0) {
+            int n = 0;  // stages filled so far
+            for (int i = blockIdx.x; i < work; i += gridDim.x) {
+                const Tile t = tile_of(p, i, BN);
+                bool ok = true;
+                for (int kb = t.kb; kb < t.ke && ok; ++kb, ++n) {
+                    const int st = n % C::kStages;
+                    if (n >= C::kStages && !(ok = wait(empty + st, (n / C::kStages - 1) & 1))) break;
+                    const uint32_t a = tc::smem_u32(base + st * C::kStage), b = a + C::kA;
+                    tc::mbar_arrive_expect_tx(full + st, C::kStage);
+                    if (A_MN) {
+#pragma unroll
+                        for (int x = 0; x < BM / 64; ++x)
+                            load_2d(a + x * 8192, &maps.a, t.m + 64 * x, kb * BK, full + st);
+                    } else {
+                        load_2d(a, &maps.a, kb * BK, t.m, full + st);
+                    }
+                    if (B_MN) {
+#pragma unroll
+                        for (int x = 0; x < BN / 64; ++x)
+                            load_2d(b + x * 8192, &maps.b, t.n + 64 * x, kb * BK, full + st);
+                    } else {
+                        load_2d(b, &maps.b, kb * BK, t.n, full + st);
+                    }
+                }
+                if (!ok) break;
+            }
+            // every copy has landed before the CTA ends
+            for (int s = max(0, n - C::kStages); s < n; ++s)
+                tc::mbar_wait(full + s % C::kStages, (s / C::kStages) & 1, kWaitPolls);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc16(std::is_same<T, __half>::value, A_MN, B_MN, BN);
+            constexpr uint32_t kStepA = A_MN ? 2048 : 32, kStepB = B_MN ? 2048 : 32;  // 16 of K
+            int n = 0, c = 0;
+            for (int i = blockIdx.x; i < work; i += gridDim.x, ++c) {
+                const Tile t = tile_of(p, i, BN);
+                bool ok = true;
+                if (c >= 2 && !wait(taken + (c & 1), (c / 2 - 1) & 1)) break;
+                tc::fence_after_sync();
+                const uint32_t d = tmem + (c & 1) * BN;
+                for (int kb = t.kb; kb < t.ke; ++kb, ++n) {
+                    const int st = n % C::kStages;
+                    if (!(ok = wait(full + st, (n / C::kStages) & 1))) break;
+                    tc::fence_after_sync();
+                    const uint32_t a = tc::smem_u32(base + st * C::kStage), b = a + C::kA;
+#pragma unroll
+                    for (int k = 0; k < BK / 16; ++k)
+                        mma_f16(d, desc128(a + k * kStepA, A_MN ? 8192 : 16, 1024),
+                                desc128(b + k * kStepB, B_MN ? 8192 : 16, 1024), idesc, kb > t.kb || k > 0);
+                    tc::mma_commit(empty + st);
+                }
+                if (!ok) break;
+                tc::mma_commit(done + (c & 1));
+            }
+            // the last products are done with the stages before the CTA ends
+            if (n > 0) tc::mbar_wait(empty + (n - 1) % C::kStages, ((n - 1) / C::kStages) & 1, kWaitPolls);
+        }
+    } else {
+        const int e = warp - 2, quarter = warp & 3;  // a warp reads its own 32 lanes of tensor memory
+        char *box = out + e * 4096;
+        float *bs = bias + e * BN;
+        const bool pair = ((uintptr_t)p.y | (uintptr_t)p.pre) % 4 == 0 && (p.ldy | p.ldp) % 2 == 0;
+        int c = 0;
+        for (int i = blockIdx.x; i < work; i += gridDim.x, ++c) {
+            const Tile t = tile_of(p, i, BN);
+            const int m0 = t.m + 32 * quarter, n1 = min(p.N - t.n, BN);
+            if (!p.partial) {
+                __syncwarp();
+                for (int j = lane; j < BN; j += 32)
+                    bs[j] = p.bias && t.n + j < p.N ? as_f32(((const T *)p.bias)[t.n + j]) : 0.f;
+                __syncwarp();
+            }
+            const bool ok = wait(done + (c & 1), (c / 2) & 1);
+            tc::fence_after_sync();
+            const uint32_t d = tmem + (c & 1) * BN + ((uint32_t)quarter << 21);
+            for (int n = 0; n < n1; n += 64) {
+                float v[64];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x[32];
+                    tmem_ld32(d + n + 32 * h, x);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[32 * h + j] = ok ? x[j] : __int_as_float(0x7fc00000);
+                }
+                if (n + 64 >= n1) {  // the accumulator may be written again
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(taken + (c & 1));
+                }
+                if (p.partial) {
+                    const int m = m0 + lane;
+                    if (m < p.M) {
+                        float *to = p.partial + ((size_t)(i / p.tiles) * p.M + m) * p.ldw + t.n + n;
+#pragma unroll
+                        for (int j = 0; j < 64; j += 4)
+                            if (t.n + n + j < p.ldw)
+                                *(float4 *)(to + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    }
+                    continue;
+                }
+#pragma unroll
+                for (int j = 0; j < 64; j += 4) {
+                    const float4 b = *(const float4 *)(bs + n + j);
+                    v[j] += b.x; v[j + 1] += b.y; v[j + 2] += b.z; v[j + 3] += b.w;
+                }
+                // a box of 32 rows x 64 columns at a time: pre, then y
+                auto begin = [&] {  // the box may be written
+                    if (p.tma_out) {
+                        if (lane == 0) tc::bulk_wait_read_all();
+                        __syncwarp();
+                    }
+                };
+                auto put = [&](bool add) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        uint4 *at = (uint4 *)(box + lane * 128 + ((q ^ (lane & 7)) << 4));
+                        if (add) {
+                            const uint4 r = *at;
+                            const uint32_t rr[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const float2 f = unpack<T>(rr[x]);
+                                v[8 * q + 2 * x] += f.x;
+                                v[8 * q + 2 * x + 1] += f.y;
+                            }
+                        }
+                        *at = make_uint4(pack<T>(v[8 * q], v[8 * q + 1]), pack<T>(v[8 * q + 2], v[8 * q + 3]),
+                                         pack<T>(v[8 * q + 4], v[8 * q + 5]), pack<T>(v[8 * q + 6], v[8 * q + 7]));
+                    }
+                };
+                auto leave = [&](const CUtensorMap *map, void *to, long long ld) {
+                    if (p.tma_out) {
+                        tc::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && m0 < p.M) {
+                            store_2d(map, tc::smem_u32(box), t.n + n, m0);
+                            tc::bulk_commit_group();
+                        }
+                    } else {
+                        __syncwarp();
+                        box_out<T>(box, to, ld, m0, t.n + n, p.M, p.N, lane, pair);
+                        __syncwarp();
+                    }
+                };
+                if (p.pre) {
+                    begin();
+                    put(false);
+                    leave(&maps.pre, p.pre, p.ldp);
+                }
+                activate_all(v, p.act);
+                begin();
+                if (p.residual) {
+                    box_in(box, p.residual, p.ldr, m0, t.n + n, p.M, p.N, lane, p.wide_r);
+                    __syncwarp();
+                }
+                put(p.residual);
+                leave(&maps.y, p.y, p.ldy);
+            }
+            if (!ok) break;
+        }
+        if (lane == 0) tc::bulk_wait_all();
+    }
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 1) tc::tmem_dealloc(tmem, C::kColumns);
+}
+
+// The parts of the contraction joined, with the epilogue: a thread has four columns of a row.
+template <typename T>
+__global__ void __launch_bounds__(256) kda_linear_join_kernel(const Params p) {
+    wait_for_previous();
+    const int quads = p.ldw / 4;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long m = i / quads;
+    const int n = (int)(i - m * quads) * 4;
+    if (m >= p.M) return;
+    const float *at = p.partial + m * p.ldw + n;
+    float v[4] = {};
+    for (int s = 0; s < p.splits; ++s) {
+        const float4 x = *(const float4 *)(at + (size_t)s * p.M * p.ldw);
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (n + j >= p.N) break;
+        const float x = v[j] + (p.bias ? as_f32(((const T *)p.bias)[n + j]) : 0.f);
+        if (p.pre) ((T *)p.pre)[m * p.ldp + n + j] = from_f32<T>(x);
+        float y = activate(x, p.act);
+        if (p.residual) y += as_f32(((const T *)p.residual)[m * p.ldr + n + j]);
+        ((T *)p.y)[m * p.ldy + n + j] = from_f32<T>(y);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+cudaError_t encode(CUtensorMap *m, bool fp16, const void *base, long long cols, long long rows,
+                   long long ld, int box_cols, int box_rows) {
+    if (!g_encode) {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                               cudaEnableDefault, &q);
+        if (e != cudaSuccess) return e;
+        if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+        g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, one[2] = {1, 1};
+    const CUresult r = g_encode(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                                const_cast<void *>(base), dims, strides, box, one,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Columns of a tile, and parts of the contraction.
+struct Plan {
+    int bn, tiles, splits, per, ldw;
+};
+Plan plan_of(int M, int N, int K) {
+    Plan q;
+    const long long mt = (M + BM - 1) / BM;
+    auto tiles = [&](int bn) { return mt * ((N + bn - 1) / bn); };
+    q.bn = tiles(256) >= kSMs ? 256 : tiles(128) >= kSMs / 2 || N > 64 ? 128 : 64;
+    q.tiles = (int)tiles(q.bn);
+    const int blocks = (K + BK - 1) / BK;
+    int splits = q.tiles * 2 <= kSMs ? kSMs / q.tiles : 1;
+    if (splits > blocks / 4) splits = blocks / 4;  // four blocks of 64 at least
+    if (splits > 16) splits = 16;
+    if (splits < 1) splits = 1;
+    q.per = (blocks + splits - 1) / splits;
+    q.splits = blocks ? (blocks + q.per - 1) / q.per : 1;
+    q.ldw = (N + 3) / 4 * 4;
+    return q;
+}
+
+template <typename T, bool A_MN, bool B_MN, int BN>
+cudaError_t launch(const Maps &maps, const Params &p, cudaStream_t stream) {
+    static volatile int done[kMaxDev];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = smem_limit_once(kda_linear_kernel<T, A_MN, B_MN, BN>, Cfg<BN>::kBytes, dev, done);
+    if (e != cudaSuccess) return e;
+    const int work = p.tiles * p.splits;
+    return launch_early(kda_linear_kernel<T, A_MN, B_MN, BN>, (unsigned)(work < kSMs ? work : kSMs), kThreads,
+                        Cfg<BN>::kBytes, stream, maps, p);
+}
+template <typename T, bool A_MN, bool B_MN>
+cudaError_t pick(int bn, const Maps &maps, const Params &p, cudaStream_t stream) {
+    return bn == 256 ? launch<T, A_MN, B_MN, 256>(maps, p, stream)
+           : bn == 128 ? launch<T, A_MN, B_MN, 128>(maps, p, stream)
+                       : launch<T, A_MN, B_MN, 64>(maps, p, stream);
+}
+template <typename T> cudaError_t run(const GemmArgs &a, cudaStream_t stream) {
+    const Plan q = plan_of(a.M, a.N, a.K);
+    Maps maps;
+    cudaError_t e = a.a_mn ? encode(&maps.a, a.fp16, a.A, a.M, a.K, a.lda, 64, BK)
+                           : encode(&maps.a, a.fp16, a.A, a.K, a.M, a.lda, BK, BM);
+    if (e == cudaSuccess)
+        e = a.b_mn ? encode(&maps.b, a.fp16, a.B, a.N, a.K, a.ldb, 64, BK)
+                   : encode(&maps.b, a.fp16, a.B, a.K, a.N, a.ldb, BK, q.bn);
+    if (e != cudaSuccess) return e;
+    Params p = {};
+    p.M = a.M; p.N = a.N; p.K = a.K;
+    p.nt = (a.N + q.bn - 1) / q.bn;
+    p.tiles = q.tiles; p.splits = q.splits; p.per = q.per;
+    p.bias = a.bias; p.residual = a.residual; p.y = a.y; p.pre = a.pre;
+    p.ldr = a.ldr; p.ldy = a.ldy; p.ldp = a.ldp;
+    p.act = a.act;
+    p.ldw = q.ldw;
+    p.partial = q.splits > 1 ? a.partial : nullptr;
+    p.dbg = a.dbg;
+    p.wide_r = aligned(a.residual, 16) && a.ldr % 8 == 0 && a.N % 8 == 0;
+    p.tma_out = !p.partial && aligned(a.y, 16) && a.ldy % 8 == 0 && (!a.pre || (aligned(a.pre, 16) && a.ldp % 8 == 0));
+    if (p.tma_out) {
+        e = encode(&maps.y, a.fp16, a.y, a.N, a.M, a.ldy, 64, 32);
+        if (e == cudaSuccess && a.pre) e = encode(&maps.pre, a.fp16, a.pre, a.N, a.M, a.ldp, 64, 32);
+        if (e != cudaSuccess) return e;
+    }
+    e = a.a_mn ? pick<T, true, true>(q.bn, maps, p, stream)
+        : a.b_mn ? pick<T, false, true>(q.bn, maps, p, stream) : pick<T, false, false>(q.bn, maps, p, stream);
+    if (e != cudaSuccess || !p.partial) return e;
+    const long long quads = (long long)a.M * (q.ldw / 4);
+    return launch_early(kda_linear_join_kernel<T>, (unsigned)((quads + 255) / 256), 256, 0, stream, p);
+}
+
+}  // namespace
+}  // namespace linear
+
+size_t gemm_partial_bytes(int M, int N, int K) {
+    const linear::Plan q = linear::plan_of(M, N, K);
+    return q.splits > 1 ? (size_t)q.splits * M * q.ldw * 4 : 0;
+}
+
+cudaError_t launch_gemm(const GemmArgs &a, cudaStream_t stream) {
+    return a.fp16 ? linear::run<__half>(a, stream) : linear::run<__nv_bfloat16>(a, stream);
+}
+
+}  // namespace kda

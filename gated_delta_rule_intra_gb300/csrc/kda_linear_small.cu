@@ -1,0 +1,194 @@
+// Matrix product with its epilogue for a few rows (decoding), the copy of rows onto 16-byte
+// boundaries, and the first step of the backward pass.
+#include <type_traits>
+
+#include "kda_linear.cuh"
+
+namespace kda {
+namespace linear {
+namespace {
+
+// y [M, N], M <= 8 MT.  Bound by memory: every weight is read once, straight from memory into the
+// left operands of mma.sync (16 rows of the weight a CTA, the contraction cut over its eight warps);
+// the few rows of x are the right operands.  Which k an operand's places stand for does not matter
+// as long as both agree, so a lane takes 16 consecutive bytes of its row: four of them are two
+// products' operands.  The tensor-memory path would move 128 rows of x for these few.
+constexpr int kWarps = 8, kAhead = 4;
+
+template <typename T>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1) {
+    if (std::is_same<T, __half>::value)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <typename T, int MT>
+__global__ void __launch_bounds__(32 * kWarps) kda_linear_small_kernel(const GemmArgs a) {
+    wait_for_previous();
+    __shared__ float red[kWarps][MT][32][4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 2, quad = lane & 3;
+    const int n0 = blockIdx.x * 16;
+    const T *W = (const T *)a.B, *x = (const T *)a.A;
+    float acc[MT][4] = {};
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    // chunks of 32 k: chunk warp, warp + 8, ...
+    const int chunks = (a.K + 31) / 32;
+    for (int c0 = warp; c0 < chunks; c0 += kWarps * kAhead) {
+        uint4 w[kAhead][2], b[kAhead][MT];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int k = (c0 + i * kWarps) * 32 + quad * 8;
+            const bool in = k < a.K;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int n = n0 + row + 8 * h;
+                w[i][h] = in && n < a.N ? *(const uint4 *)(W + (size_t)n * a.ldb + k) : none;
+            }
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const int m = row + 8 * t;
+                b[i][t] = in && m < a.M ? *(const uint4 *)(x + (size_t)m * a.lda + k) : none;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                mma<T>(acc[t], w[i][0].x, w[i][1].x, w[i][0].y, w[i][1].y, b[i][t].x, b[i][t].y);
+                mma<T>(acc[t], w[i][0].z, w[i][1].z, w[i][0].w, w[i][1].w, b[i][t].z, b[i][t].w);
+            }
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) *(float4 *)red[warp][t][lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+    __syncthreads();
+    // thread: one of 16 weight rows, one of 8 MT rows of x
+    for (int e = threadIdx.x; e < 128 * MT; e += 32 * kWarps) {
+        const int r = e & 15, m = e >> 4, t = m >> 3, n = n0 + r;
+        // row r, column m % 8 of the 16 x 8 block: lane and register of the fragment
+        const int l = (r & 7) * 4 + ((m & 7) >> 1), i = (r >> 3) * 2 + (m & 1);
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += red[w][t][l][i];
+        if (m >= a.M || n >= a.N || !dbg_ok(a.dbg, (size_t)m * a.N + n, (size_t)a.M * a.N, DBG_STORE)) continue;
+        if (a.bias) v += as_f32(((const T *)a.bias)[n]);
+        if (a.pre) ((T *)a.pre)[m * a.ldp + n] = from_f32<T>(v);
+        v = activate(v, a.act);
+        if (a.residual) v += as_f32(((const T *)a.residual)[m * a.ldr + n]);
+        ((T *)a.y)[m * a.ldy + n] = from_f32<T>(v);
+    }
+}
+
+__global__ void __launch_bounds__(256) kda_linear_copy_kernel(const CopyArgs a, int per) {
+    wait_for_previous();
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x, r = i / per;
+    const int c = (int)(i - r * per) * 8;
+    if (r >= a.rows) return;
+    const uint16_t *at = (const uint16_t *)a.src + r * a.lds + c;
+    alignas(16) uint16_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < a.width ? at[j] : (uint16_t)0;
+    *(uint4 *)((uint16_t *)a.dst + r * a.ldd + c) = *(const uint4 *)v;
+}
+
+// dpre and the sums of its columns.  A warp has 32 V neighbouring columns of every eighth row of its
+// CTA's part; the CTAs' sums are joined in order by a second kernel.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) kda_linear_dact_kernel(const DActArgs a, int rows_each) {
+    wait_for_previous();
+    __shared__ float red[8][32 * V];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = blockIdx.x * 32 * V + lane * V;
+    const long long m0 = (long long)blockIdx.y * rows_each, m1 = min((long long)a.M, m0 + rows_each);
+    float sum[V] = {};
+    if (n < a.N) {
+#pragma unroll 4
+        for (long long m = m0 + warp; m < m1; m += 8) {
+            if (!dbg_ok(a.dbg, (size_t)m, (size_t)a.M, DBG_LOAD)) break;
+            const auto dy = *(const Vec<T, V> *)((const T *)a.dy + m * a.lddy + n);
+            Vec<T, V> p, d;
+            if (a.act != ACT_NONE) p = *(const Vec<T, V> *)((const T *)a.pre + m * a.ldp + n);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float g = a.act != ACT_NONE ? dy[i] * slope(p[i], a.act) : dy[i];
+                sum[i] += g;
+                d.v[i] = from_f32<T>(g);
+            }
+            if (a.dpre) *(Vec<T, V> *)((T *)a.dpre + m * a.ldd + n) = d;
+        }
+    }
+    if (!a.dbias) return;
+#pragma unroll
+    for (int i = 0; i < V; ++i) red[warp][lane * V + i] = sum[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * V; i += 256) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) s += red[w][i];
+        if (blockIdx.x * 32 * V + i < a.N) a.partial[(size_t)blockIdx.y * a.N + blockIdx.x * 32 * V + i] = s;
+    }
+}
+template <typename T>
+__global__ void __launch_bounds__(256) kda_linear_dbias_kernel(const DActArgs a, int n) {
+    wait_for_previous();
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= a.N) return;
+    float s = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) s += a.partial[(size_t)i * a.N + c];
+    ((T *)a.dbias)[c] = from_f32<T>(s);
+}
+
+template <typename T, int V> cudaError_t dact(const DActArgs &a, cudaStream_t stream) {
+    const int parts = dact_partials(a.M, a.N), each = (a.M + parts - 1) / parts;
+    cudaError_t e = launch_early(kda_linear_dact_kernel<T, V>,
+                                 dim3((unsigned)((a.N + 32 * V - 1) / (32 * V)), (unsigned)parts), 256, 0,
+                                 stream, a, each);
+    if (e != cudaSuccess || !a.dbias) return e;
+    return launch_early(kda_linear_dbias_kernel<T>, (unsigned)((a.N + 255) / 256), 256, 0, stream, a, parts);
+}
+template <typename T> cudaError_t dact(const DActArgs &a, cudaStream_t stream) {
+    auto ok = [](const void *p, long long ld) { return !p || (aligned(p, 16) && ld % 8 == 0); };
+    return a.N % 8 == 0 && ok(a.dy, a.lddy) && ok(a.pre, a.ldp) && ok(a.dpre, a.ldd) ? dact<T, 8>(a, stream)
+                                                                                     : dact<T, 1>(a, stream);
+}
+
+template <typename T> cudaError_t small(const GemmArgs &a, cudaStream_t stream) {
+    const unsigned grid = (unsigned)((a.N + 15) / 16);
+    return a.M <= 8 ? launch_early(kda_linear_small_kernel<T, 1>, grid, 32 * kWarps, 0, stream, a)
+                    : launch_early(kda_linear_small_kernel<T, 2>, grid, 32 * kWarps, 0, stream, a);
+}
+
+}  // namespace
+}  // namespace linear
+
+// Parts of the rows, each with a row of column sums: enough CTAs for the card at 256 columns each.
+int dact_partials(int M, int N) {
+    const long long blocks = (N + 255) / 256, want = (4 * kSMs + blocks - 1) / blocks;
+    const long long most = (M + 31) / 32;
+    const long long n = want < most ? want : most;
+    return (int)(n < 1 ? 1 : n);
+}
+
+cudaError_t launch_dact(const DActArgs &a, cudaStream_t stream) {
+    return a.fp16 ? linear::dact<__half>(a, stream) : linear::dact<__nv_bfloat16>(a, stream);
+}
+
+cudaError_t launch_copy_rows(const CopyArgs &a, cudaStream_t stream) {
+    const int per = (a.width + 7) / 8;
+    return launch_early(linear::kda_linear_copy_kernel, (unsigned)((a.rows * per + 255) / 256), 256, 0, stream, a, per);
+}
+
+bool small_gemm_ok(const GemmArgs &a) { return a.M <= kSmallM && !a.a_mn && !a.b_mn && a.K % 8 == 0; }
+
+cudaError_t launch_small_gemm(const GemmArgs &a, cudaStream_t stream) {
+    return a.fp16 ? linear::small<__half>(a, stream) : linear::small<__nv_bfloat16>(a, stream);
+}
+
+}  // namespace kda

@@ -1,0 +1,94 @@
+// Rows of tokens with the channels last: neighbouring channels of a row in registers, and the
+// pieces that sequences are cut into.
+#pragma once
+
+#include "kda_layer.h"
+#include "kda_ops.cuh"
+
+namespace kda {
+namespace rows {
+
+__device__ __forceinline__ float as_f32(float x) { return x; }
+__device__ __forceinline__ float as_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float as_f32(__half x) { return __half2float(x); }
+template <typename T> __device__ __forceinline__ T from_f32(float x);
+template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
+    return __float2bfloat16_rn(x);
+}
+template <> __device__ __forceinline__ __half from_f32<__half>(float x) {
+    return __float2half_rn(x);
+}
+
+// V neighbouring channels of a row.
+template <typename T, int V> struct alignas(sizeof(T) * V) Vec {
+    T v[V];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = from_f32<T>(0.f);
+    }
+    __device__ __forceinline__ float operator[](int i) const { return as_f32(v[i]); }
+    __device__ __forceinline__ float2 two(int i) const {
+        return make_float2(as_f32(v[i]), as_f32(v[i + 1]));
+    }
+};
+
+// An element of a parameter, whose type may be x's or FP32.
+__device__ __forceinline__ float param(const void *p, int dtype, size_t i, float none) {
+    if (!p) return none;
+    if (dtype == TYPE_FP32) return ((const float *)p)[i];
+    if (dtype == TYPE_BF16) return as_f32(((const __nv_bfloat16 *)p)[i]);
+    return as_f32(((const __half *)p)[i]);
+}
+
+// 1 / (1 + e^-x), from the exponential and reciprocal units (2^-22 each); 0 and 1 at the far ends.
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
+// d silu / dx, with s = sigmoid(x)
+__device__ __forceinline__ float silu_slope(float x, float s) { return s * fmaf(x, 1.f - s, 1.f); }
+
+// A piece of a sequence: its tokens [begin, begin + len) of the sequence's [0, total).
+struct Piece {
+    long long row0;  // the sequence's first row
+    int seq, index, begin, len, total;
+};
+
+// Piece p of the pieces of `size` tokens.  Packed sequences take theirs from cu[n] / size + n on, so
+// that no two meet and T / size + num_seqs cover every input; each has one at least, an empty
+// sequence too.  len < 0: there is none.
+__device__ __forceinline__ Piece find_piece(const Tokens &t, long long p, int size) {
+    Piece x;
+    if (!t.cu_seqlens) {
+        const int per = t.T > size ? (t.T + size - 1) / size : 1;
+        x.seq = (int)(p / per);
+        x.index = (int)(p - (long long)x.seq * per);
+        x.row0 = (long long)x.seq * t.T;
+        x.total = t.T;
+    } else {
+        auto token = [&](int v) { return v < 0 ? 0 : v > t.T ? t.T : v; };
+        int lo = 0, hi = t.num_seqs - 1;
+        while (lo < hi) {  // the last sequence whose pieces begin at or before this one
+            const int mid = (lo + hi + 1) >> 1;
+            if (token(t.cu_seqlens[mid]) / size + mid <= p) lo = mid; else hi = mid - 1;
+        }
+        const int a = token(t.cu_seqlens[lo]), b = token(t.cu_seqlens[lo + 1]);
+        x.seq = lo;
+        x.row0 = a;
+        x.total = b > a ? b - a : 0;
+        x.index = (int)(p - (a / size + lo));
+    }
+    x.begin = x.index * size;
+    const int left = x.total - x.begin;
+    x.len = x.index < 0 || (left <= 0 && x.index > 0) ? -1 : left < size ? left : size;
+    return x;
+}
+
+inline bool aligned(const void *p, size_t to) { return (uintptr_t)p % to == 0; }
+
+}  // namespace rows
+}  // namespace kda

@@ -69,6 +69,8 @@ extern "C" {
 
 /*
  * ABI versions (kda_abi_version() returns the loaded library's):
+ *   12 kda_conv_fwd, kda_conv_bwd, kda_conv_step, kda_scan_fwd, kda_scan_bwd, kda_scan_step,
+ *      kda_linear_fwd, kda_linear_bwd and their option structs and size queries
  *   11 kda_chunk_bwd's zero_rest also takes KDA_GATE_GRADS_FP32, kda_chunk_fwd's saved either
  *      of its sizes in BF16 calls without a state
  *   10 kda_chunk_fwd, kda_chunk_bwd, kda_step, kda_layer_norm_fwd, kda_layer_norm_bwd
@@ -88,7 +90,7 @@ extern "C" {
  * must check at start-up that kda_abi_version() equals the KDA_ABI_VERSION it was
  * compiled with (the Python binding refuses to load any other version).
  */
-#define KDA_ABI_VERSION 11
+#define KDA_ABI_VERSION 12
 #define KDA_BT 64  /* chunk length */
 #define KDA_BC 16  /* sub-block length inside a chunk */
 #define KDA_K 128  /* head dimension */
@@ -472,7 +474,7 @@ kda_status_t kda_step(const void *q, const void *k, const void *v, const float *
  * fixed order.  `workspace` holds kda_layer_norm_bwd_workspace_bytes() bytes of partial sums
  * (16-byte aligned; not needed without dweight).
  */
-#define KDA_FP32 2 /* layer norm only */
+#define KDA_FP32 2 /* layer norm, convolution and scan */
 
 kda_status_t kda_layer_norm_fwd(const void *x, const void *weight, const void *bias, void *y,
                                 float *mean, float *rstd, long long rows, int width, float eps,
@@ -486,6 +488,211 @@ kda_status_t kda_layer_norm_bwd(const void *dy, const void *x, const void *weigh
                                 float *dbias, long long rows, int width, int dtype, int wdtype,
                                 long long dy_stride, long long x_stride, long long dx_stride,
                                 void *workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * Short causal convolution of each channel (the one in front of q, k and v, or of the scan below):
+ *   pre[t, d] = bias[d] + sum_j weight[d, j] x[t - W + 1 + j, d],  y = act(pre)
+ * over the tokens of a sequence, x, y [B, T, D] with a row stride each, in elements (0 = D), W 2 to
+ * 4.  x, y, dy, dx and the states have one type (KDA_BF16, KDA_FP16 or KDA_FP32); weight [D, W] and
+ * bias [D] (NULL = 0) have `wdtype`, which is the same type or KDA_FP32.  The inputs in front of a
+ * sequence come from initial_state [sequences, W - 1, D], oldest first (NULL = zeros); final_state
+ * gets the last W - 1 of state and sequence (a sequence of no tokens: a copy).  Sums are FP32.
+ * cu_seqlens, num_seqs and zero_rest as in kda_chunk_fwd (zero_rest: rows of outputs D apart).
+ * Pointers need their element's alignment; channels on 16-byte boundaries are read 16 bytes at a
+ * time.
+ *
+ * Backward: dx, and dweight [D, W], dbias [D] fp32 (both or neither), summed over the tokens in a
+ * fixed order; d_final_state (NULL = zeros) and d_initial_state (written, NULL = not wanted, at most
+ * 65535 sequences) are like the states.  `workspace` holds kda_conv_bwd_workspace_bytes() bytes,
+ * 16-byte aligned (not needed without dweight).
+ *
+ * kda_conv_step: one token for each of N <= 65535 requests, x, y [N, D], `state` [num_states, W - 1,
+ * D] updated in place; state_indices as in kda_step.
+ */
+#define KDA_ACT_NONE 0
+#define KDA_ACT_SILU 1
+#define KDA_ACT_GELU 2 /* x Phi(x), of the matrix product only */
+#define KDA_ACT_RELU 3 /* of the matrix product only */
+
+typedef struct {
+    const void *initial_state;
+    void *final_state;
+    const int *cu_seqlens;
+    int num_seqs;
+    int zero_rest;
+    long long x_stride, y_stride;
+} kda_conv_fwd_opts_t;
+
+kda_status_t kda_conv_fwd(const void *x, const void *weight, const void *bias, void *y, int B, int T,
+                          int D, int W, int dtype, int wdtype, int activation,
+                          const kda_conv_fwd_opts_t *opts, kda_stream_t stream);
+
+typedef struct {
+    const void *initial_state, *d_final_state;
+    void *d_initial_state;
+    const int *cu_seqlens;
+    int num_seqs;
+    int zero_rest;
+    long long dy_stride, x_stride, dx_stride;
+    void *workspace;
+    size_t workspace_bytes;
+} kda_conv_bwd_opts_t;
+
+size_t kda_conv_bwd_workspace_bytes(int B, int T, int D, int W, int num_seqs);
+
+kda_status_t kda_conv_bwd(const void *dy, const void *x, const void *weight, const void *bias, void *dx,
+                          float *dweight, float *dbias, int B, int T, int D, int W, int dtype,
+                          int wdtype, int activation, const kda_conv_bwd_opts_t *opts,
+                          kda_stream_t stream);
+
+typedef struct {
+    const int *state_indices;
+    int num_states; /* 0 means N */
+    long long x_stride, y_stride;
+} kda_conv_step_opts_t;
+
+kda_status_t kda_conv_step(const void *x, const void *weight, const void *bias, void *state, void *y,
+                           int N, int D, int W, int dtype, int wdtype, int activation,
+                           const kda_conv_step_opts_t *opts, kda_stream_t stream);
+
+/*
+ * Selective state-space scan.  Per channel d of D a state h of N <= 64 numbers:
+ *   s_t = softplus(delta_t + delta_bias)              (plain_delta: without the softplus)
+ *   h_t[n] = exp(s_t A[d, n]) h_{t-1}[n] + s_t u_t B_t[n],
+ *   y_t = (sum_n C_t[n] h_t[n] + skip[d] u_t) silu(z_t)
+ * u, delta, z, y [B, T, D], Bm, Cm [B, T, G, N] (channel d reads group d / (D / G)), all of one type
+ * (KDA_BF16, KDA_FP16 or KDA_FP32) with a row stride each, in elements (0 = D, G N); A [D, N], skip,
+ * delta_bias [D] fp32.  skip, z, delta_bias: NULL = none.  A is finite, <= 0 for states that fade.
+ * Pointers need their element's alignment (rows on boundaries of four elements are read
+ * four channels at a time), saved and workspace 256 bytes.  States, sums and exponentials are FP32.
+ *   initial_state, final_state   [sequences, D, N] fp32 as in kda_chunk_fwd
+ *   saved, saved_bytes           what kda_scan_bwd needs: kda_scan_saved_bytes(), N / 4 bytes a token
+ *                                and channel; NULL when no backward follows
+ *   cu_seqlens, num_seqs,        as in kda_chunk_fwd (zero_rest: rows of y D apart)
+ *   zero_rest
+ *   workspace                    kda_scan_fwd_workspace_bytes() bytes (0 where the card is full of
+ *                                channels)
+ *
+ * kda_scan_bwd: du, ddelta, dz [B, T, D], dB, dC [B, T, G, N] of the type, contiguous, rounded once;
+ * dA [D, N], dskip, ddelta_bias [D] fp32.  dz, dskip and ddelta_bias come with z, skip and
+ * delta_bias.  No atomics: the same inputs give the same bits.  zero_rest: for all five outputs
+ * with rows of tokens.
+ *
+ * kda_scan_step: one token for each of `requests` <= 65535: u, delta, z, y [requests, D], Bm, Cm
+ * [requests, G, N]; `state` [num_states, D, N] fp32 (16-byte aligned) updated in place;
+ * state_indices as in kda_step.
+ */
+typedef struct {
+    const float *skip, *delta_bias;
+    const void *z;
+    const float *initial_state;
+    float *final_state;
+    void *saved;
+    size_t saved_bytes;
+    const int *cu_seqlens;
+    int num_seqs;
+    int zero_rest;
+    int plain_delta;
+    long long u_stride, delta_stride, z_stride, B_stride, C_stride, y_stride;
+    void *workspace;
+    size_t workspace_bytes;
+} kda_scan_fwd_opts_t;
+
+size_t kda_scan_saved_bytes(int B, int T, int D, int N, int num_seqs);
+size_t kda_scan_fwd_workspace_bytes(int B, int T, int D, int N, int G, int num_seqs);
+
+kda_status_t kda_scan_fwd(const void *u, const void *delta, const float *A, const void *Bm,
+                          const void *Cm, void *y, int B, int T, int D, int N, int G, int dtype,
+                          const kda_scan_fwd_opts_t *opts, kda_stream_t stream);
+
+typedef struct {
+    const float *skip, *delta_bias;
+    const void *z;
+    float *dskip, *ddelta_bias;
+    void *dz;
+    const float *d_final_state;
+    float *d_initial_state;
+    const void *saved;
+    size_t saved_bytes;
+    const int *cu_seqlens;
+    int num_seqs;
+    int zero_rest;
+    int plain_delta;
+    long long dy_stride, u_stride, delta_stride, z_stride, B_stride, C_stride;
+    void *workspace;
+    size_t workspace_bytes;
+} kda_scan_bwd_opts_t;
+
+size_t kda_scan_bwd_workspace_bytes(int B, int T, int D, int N, int G, int num_seqs);
+
+kda_status_t kda_scan_bwd(const void *dy, const void *u, const void *delta, const float *A,
+                          const void *Bm, const void *Cm, void *du, void *ddelta, float *dA, void *dB,
+                          void *dC, int B, int T, int D, int N, int G, int dtype,
+                          const kda_scan_bwd_opts_t *opts, kda_stream_t stream);
+
+typedef struct {
+    const float *skip, *delta_bias;
+    const void *z;
+    const int *state_indices;
+    int num_states; /* 0 means requests */
+    int plain_delta;
+    long long u_stride, delta_stride, z_stride, B_stride, C_stride, y_stride;
+} kda_scan_step_opts_t;
+
+kda_status_t kda_scan_step(const void *u, const void *delta, const float *A, const void *Bm,
+                           const void *Cm, float *state, void *y, int requests, int D, int N, int G,
+                           int dtype, const kda_scan_step_opts_t *opts, kda_stream_t stream);
+
+/*
+ * Matrix product with its epilogue: y = act(x weight^T + bias) + residual, x [M, K], weight [N, K], y,
+ * residual [M, N], bias [N], all KDA_BF16 or all KDA_FP16, with a row stride each (0 = width); bias
+ * and residual may be NULL.  Sums are FP32 and rounded once, behind the residual.  `saved` [M, N]
+ * (contiguous, of the type; NULL when no backward follows or without an activation) gets x weight^T +
+ * bias, rounded.  Rows on 16-byte boundaries are taken as they are; of x and weight others are
+ * copied to such boundaries first: kda_linear_copies() tells which, and `workspace`
+ * (256-byte aligned) holds kda_linear_fwd_workspace_bytes() of that.
+ *
+ * Backward: dpre = dy act'(saved), rounded to the type as the operand of two products; dx = dpre
+ * weight, dweight = dpre^T x [N, K], dbias = dpre's column sums (before the rounding), each rounded once
+ * from FP32 sums in a fixed order; NULL = not wanted.  residual's gradient is dy itself.  `wanted` says
+ * which (KDA_GRAD_*), as the pointers do.
+ */
+#define KDA_COPY_X 1
+#define KDA_COPY_WEIGHT 2
+#define KDA_COPY_DY 4
+#define KDA_GRAD_X 1
+#define KDA_GRAD_WEIGHT 2
+#define KDA_GRAD_BIAS 4
+
+typedef struct {
+    const void *bias, *residual;
+    void *saved;
+    int activation;
+    long long x_stride, weight_stride, residual_stride, y_stride;
+    void *workspace;
+    size_t workspace_bytes;
+} kda_linear_fwd_opts_t;
+
+int kda_linear_copies(const void *x, long long x_stride, const void *weight, long long weight_stride,
+                      const void *dy, long long dy_stride);
+size_t kda_linear_fwd_workspace_bytes(int M, int K, int N, int copies);
+
+kda_status_t kda_linear_fwd(const void *x, const void *weight, void *y, int M, int K, int N, int dtype,
+                            const kda_linear_fwd_opts_t *opts, kda_stream_t stream);
+
+typedef struct {
+    const void *saved;
+    int activation;
+    long long dy_stride, x_stride, weight_stride, dx_stride;
+    void *workspace;
+    size_t workspace_bytes;
+} kda_linear_bwd_opts_t;
+
+size_t kda_linear_bwd_workspace_bytes(int M, int K, int N, int activation, int copies, int wanted);
+
+kda_status_t kda_linear_bwd(const void *dy, const void *x, const void *weight, void *dx, void *dweight,
+                            void *dbias, int M, int K, int N, int dtype,
+                            const kda_linear_bwd_opts_t *opts, kda_stream_t stream);
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *kda_status_str(kda_status_t status);
