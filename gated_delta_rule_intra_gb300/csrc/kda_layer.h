@@ -90,11 +90,11 @@ struct ScanArgs {
 
 constexpr int kScanTile = 16, kScanMaxN = 64;
 inline int scan_padded(int N) {  // NP: states of a channel, padded
-    int np = 4;
+    int np = 8;
     while (np < N) np *= 2;
     return np;
 }
-inline int scan_channels(int N) { return 512 / scan_padded(N); }  // of a CTA
+inline int scan_channels(int N) { return 1024 / scan_padded(N); }  // of a CTA
 inline long long scan_blocks(int D, int N, int G) {               // CTAs side by side
     const int ch = scan_channels(N);
     return (long long)G * ((D / G + ch - 1) / ch);

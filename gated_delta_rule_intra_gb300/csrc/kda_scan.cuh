@@ -2,12 +2,17 @@
 //   D_t = softplus(delta_t + delta_bias),  h_t[n] = exp(D_t A[n]) h_{t-1}[n] + D_t u_t B_t[n],
 //   y_t = (sum_n C_t[n] h_t[n] + skip u_t) silu(z_t).
 //
-// A thread holds four states of a channel (N is padded to a power of two, NP; padded ones stay
-// zero), NP / 4 neighbouring lanes a channel.  A CTA of 128 threads walks 512 / NP channels through
-// its tokens in tiles of 16: the tile's step sizes and inputs are prepared by threads that each
-// take four neighbouring channels of one token (8-byte loads), and come to the lanes that need them
-// through shared memory, as do B and C; sums over a channel's states are taken for four
-// tokens at once, each lane ending with one token's.
+// A thread holds four states of each of two channels (N is padded to a power of two, NP; padded ones
+// stay zero), NP / 4 neighbouring lanes a channel; half of a CTA's 256 threads walk 1024 / NP channels
+// through their tokens in tiles of 16.  What does not depend on the state -- step sizes, inputs,
+// the gate -- is prepared and finished by the other half, one tile ahead and one behind, with one
+// barrier a tile: each takes eight neighbouring channels of a token.  They
+// leave it in shared memory with the tokens last, as they leave B and C: a lane then reads four
+// tokens of a number at once, and products of neighbouring tokens are one instruction (f32x2).
+// Two channels a thread, because every byte that a lane reads from shared memory costs the same
+// whether or not its neighbours read it too: with one channel a thread, B and C alone are 2.5 of the
+// 4 cycles that the exponentials leave (scan_train's forward took 475 us).  Sums over a channel's
+// states are taken for four tokens at once, each lane ending with one token's.
 //
 // A sequence is one chain; where there are too few channels to fill the card it is cut into
 // segments.  A first pass walks them all from zero and leaves each one's end (and the sum of its
@@ -26,25 +31,36 @@ constexpr int kThreads = 128, kTile = kScanTile;
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int NP_> struct Shape {
-    static constexpr int NP = NP_, L = NP / 4, CH = kThreads / L;  // lanes of a channel, channels
-    static constexpr int kQuads = CH / 4;                          // of four channels
-    static constexpr int kPer = (kTile * kQuads + kThreads - 1) / kThreads;  // quads of a thread
+    static constexpr int NP = NP_, L = NP / 4;           // lanes of a channel
+    static constexpr int HC = kThreads / L, CH = 2 * HC;  // a thread has channels c and c + HC of CH
+    static constexpr int kChunks = CH / 8;                // of eight channels
+    static constexpr int kPer = kTile * kChunks / kThreads > 0 ? kTile * kChunks / kThreads : 1;  // of a thread
     static constexpr int kRow = CH + 8;  // of a [kTile][..] array that lanes write four tokens of
     static constexpr int kBC = (kTile * NP + kThreads - 1) / kThreads;  // elements of B, of C
+    static constexpr int kVec = kTile * 4 + 4;  // of an [L][..] array of four states' tokens: parts in other banks
 };
+
+// Where four tokens (4 q ..) of channel c are in a [CH][kTile] array.  The groups of four change
+// places with c / 8, so that threads which write one token of channels eight apart meet different
+// banks.
+__device__ __forceinline__ int place(int c, int q) { return c * kTile + 4 * (q ^ (c >> 3 & 3)); }
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // log(1 + e^x): with t = e^-|x| and s = t / (2 + t), log(1 + t) = 2 artanh(s) as its series, whose
 // s^2 is at most 1/9.  Small t keep their accuracy, which log(1 + t) would lose.
-__device__ __forceinline__ float softplus(float x) {
-    const float t = ex2(-kLog2e * fabsf(x)), s = t * rcp(2.f + t), q = s * s;
-    float r = fmaf(q, 1.f / 13.f, 1.f / 11.f);
-    r = fmaf(q, r, 1.f / 9.f);
-    r = fmaf(q, r, 1.f / 7.f);
-    r = fmaf(q, r, 1.f / 5.f);
-    r = fmaf(q, r, 1.f / 3.f);
-    r = fmaf(q, r, 1.f);
-    return fmaf(2.f * s, r, x > 0.f ? x : 0.f);
+__device__ __forceinline__ float2 softplus(float2 x) {
+    const float2 t = make_float2(ex2(-kLog2e * fabsf(x.x)), ex2(-kLog2e * fabsf(x.y)));
+    const float2 s = mul2(t, make_float2(rcp(2.f + t.x), rcp(2.f + t.y))), q = mul2(s, s);
+    float2 r = fma2(q, both(1.f / 13.f), both(1.f / 11.f));
+    r = fma2(q, r, both(1.f / 9.f));
+    r = fma2(q, r, both(1.f / 7.f));
+    r = fma2(q, r, both(1.f / 5.f));
+    r = fma2(q, r, both(1.f / 3.f));
+    r = fma2(q, r, both(1.f));
+    return fma2(add2(s, s), r, make_float2(x.x > 0.f ? x.x : 0.f, x.y > 0.f ? x.y : 0.f));
 }
+__device__ __forceinline__ float softplus(float x) { return softplus(both(x)).x; }
 
 // v[V] summed over LANES lanes STRIDE apart: every lane ends with V / LANES of the sums (one where
 // there are more lanes), the part of them that its place among the lanes says.
@@ -90,54 +106,89 @@ template <int NP> struct Block {
     }
 };
 
-// Four neighbouring channels of a token; zeros where there are none.  `vec`: rows begin on
-// boundaries of four elements and blocks hold whole quads.
+// Eight neighbouring channels of a token on their way to the thread that takes them, which copies
+// them into a slot of its own in shared memory: nobody else's copies have to be waited for.  `unit`
+// bytes at a time (16, 8 or 4 by asynchronous copies, or an element): rows and blocks of channels
+// begin on such boundaries.  Zeros where there are none.
 template <typename T>
-__device__ __forceinline__ Vec<T, 4> load_quad(const void *base, long long stride, long long row,
-                                               int c, int left, bool ok, bool vec) {
-    Vec<T, 4> x;
-    x.clear();
-    const T *at = (const T *)base + row * stride + c;
-    if (vec) {
-        if (ok && left > 0) x = *reinterpret_cast<const Vec<T, 4> *>(at);
-    } else {
+__device__ __forceinline__ void fetch_chunk(Vec<T, 8> *slot, const void *base, long long stride,
+                                            long long row, int c, int left, bool ok, int unit) {
+    const char *at = (const char *)((const T *)base + row * stride + c);
+    constexpr int E = sizeof(T);
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot);
+    if (unit == 16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (ok && i < left) x.v[i] = at[i];
+        for (int i = 0; i < 8 * E; i += 16) {
+            const bool in = ok && i < left * E;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i), "l"(in ? at + i : base),
+                         "r"(in ? 16 : 0) : "memory");
+        }
+    } else if (unit == 8) {
+#pragma unroll
+        for (int i = 0; i < 8 * E; i += 8) {
+            const bool in = ok && i < left * E;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + i), "l"(in ? at + i : base),
+                         "r"(in ? 8 : 0) : "memory");
+        }
+    } else if (unit == 4) {
+#pragma unroll
+        for (int i = 0; i < 8 * E; i += 4) {
+            const bool in = ok && i < left * E;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + i), "l"(in ? at + i : base),
+                         "r"(in ? 4 : 0) : "memory");
+        }
+    } else {
+        T v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = ok && i < left ? ((const T *)at)[i] : from_f32<T>(0.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) slot->v[i] = v[i];
     }
-    return x;
 }
 template <typename T>
-__device__ __forceinline__ void store_quad(void *base, long long stride, long long row, int c,
-                                           int left, const Vec<T, 4> &x, bool vec) {
+__device__ __forceinline__ void store_chunk(void *base, long long stride, long long row, int c,
+                                            int left, const Vec<T, 8> &x, int unit) {
     T *at = (T *)base + row * stride + c;
-    if (vec) {
-        if (left > 0) *reinterpret_cast<Vec<T, 4> *>(at) = x;
+    constexpr int E = sizeof(T);
+    if (unit == 16) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 16 / E)
+            if (i < left) *(uint4 *)(at + i) = *(const uint4 *)(x.v + i);
+    } else if (unit == 8) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 8 / E)
+            if (i < left) *(uint2 *)(at + i) = *(const uint2 *)(x.v + i);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i)
             if (i < left) at[i] = x.v[i];
     }
 }
+template <typename T> __device__ __forceinline__ float2 pair(const Vec<T, 8> &x, int i) { return x.two(2 * i); }
+template <typename T> __device__ __forceinline__ void put_pair(Vec<T, 8> &x, int i, float2 v) {
+    x.v[2 * i] = from_f32<T>(v.x);
+    x.v[2 * i + 1] = from_f32<T>(v.y);
+}
+__device__ __forceinline__ float2 sigmoid2(float2 x) { return make_float2(sigmoid(x.x), sigmoid(x.y)); }
 
 // A tile's elements of B or C in the registers of all threads, and from there to shared memory.
 template <typename T, int NP> struct Vectors {
     using S = Shape<NP>;
     T v[S::kBC];
-    __device__ __forceinline__ void load(const void *base, long long stride, long long row0, int rows,
-                                         int group, int N) {
+    __device__ __forceinline__ void load(int tid, const void *base, long long stride, long long row0,
+                                         int rows, int group, int N) {
 #pragma unroll
         for (int i = 0; i < S::kBC; ++i) {
-            const int e = threadIdx.x + i * kThreads, t = e / NP, n = e % NP;
+            const int e = tid + i * kThreads, t = e / NP, n = e % NP;
             v[i] = t < rows && n < N ? ((const T *)base)[(row0 + t) * stride + (long long)group * N + n]
                                      : from_f32<T>(0.f);
         }
     }
-    __device__ __forceinline__ void put(float (*to)[NP]) const {
+    __device__ __forceinline__ void put(int tid, float (*to)[S::kVec]) const {  // [L][state][token]
 #pragma unroll
         for (int i = 0; i < S::kBC; ++i) {
-            const int e = threadIdx.x + i * kThreads;
-            if (S::kBC * kThreads == kTile * NP || e < kTile * NP) to[e / NP][e % NP] = as_f32(v[i]);
+            const int e = tid + i * kThreads;
+            if (S::kBC * kThreads == kTile * NP || e < kTile * NP) to[e % NP / 4][e % 4 * kTile + e / NP] = as_f32(v[i]);
         }
     }
 };
@@ -163,7 +214,6 @@ __device__ __forceinline__ void store_states(float *base, size_t channel, int n,
     for (int i = 0; i < 4; ++i)
         if (n + i < N) base[channel * N + n + i] = x.get(i);
 }
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ Four scaled(Four a, float x) { return {mul2(a.lo, both(x)), mul2(a.hi, both(x))}; }
 // 2^(d a)
 __device__ __forceinline__ Four decay(float2 dd, Four a2) {
@@ -179,6 +229,27 @@ __device__ __forceinline__ float dot(Four a, Four b) {
     return s.x + s.y;
 }
 
+// Shared memory that the phase behind a barrier only reads: the loads are plain functions of their
+// address, so that no store of the phase holds them back (it is not known that the arrays are
+// apart); `phase`, which is new behind every barrier, keeps them from moving across it.
+struct Phase {
+    uint32_t base;
+    __device__ __forceinline__ Phase(const void *smem) : base((uint32_t)__cvta_generic_to_shared(smem)) {}
+    __device__ __forceinline__ void next() { asm volatile("" : "+r"(base)::"memory"); }
+    __device__ __forceinline__ void load4(uint32_t off, float2 (&to)[2]) const {
+        asm("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+            : "=f"(to[0].x), "=f"(to[0].y), "=f"(to[1].x), "=f"(to[1].y) : "r"(base + off));
+    }
+    __device__ __forceinline__ float2 load2(uint32_t off) const {
+        float2 x;
+        asm("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(base + off));
+        return x;
+    }
+};
+// All 2 kThreads of a CTA, and the kThreads of its second half.
+__device__ __forceinline__ void sync_all() { asm volatile("bar.sync 0, %0;" ::"n"(2 * kThreads) : "memory"); }
+__device__ __forceinline__ void sync_half() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+
 // How the four sums that scatter_sum<L, 1> leaves are spread: a lane's first token, and how many.
 template <int L> struct Share {
     static constexpr int kCount = L < 4 ? 4 / L : 1;
@@ -186,9 +257,16 @@ template <int L> struct Share {
     static __device__ __forceinline__ bool mine(int part) { return L <= 4 || part % (L / 4 > 0 ? L / 4 : 1) == 0; }
 };
 
-inline bool vec_ok(const ScanArgs &a, const void *p, long long stride) {
-    return !p || (aligned(p, 4 * (size_t)esize(a.dtype)) && stride % 4 == 0);
-}
+// The widest of 16, 8, 4 bytes and an element on whose boundaries all rows and blocks begin.
+struct Unit {
+    int es, unit;
+    Unit(const ScanArgs &a) : es(esize(a.dtype)), unit(16) {
+        while (unit > es && (a.D / a.G) * es % unit) unit /= 2;
+    }
+    void add(const void *p, long long stride) {
+        while (p && unit > es && !(aligned(p, unit) && stride * es % unit == 0)) unit /= 2;
+    }
+};
 
 }  // namespace scan
 }  // namespace kda

@@ -8,295 +8,445 @@
 // The states come again from the ones that the forward left in front of every 16 tokens: half a
 // tile at a time, so that eight tokens' p stay in registers (h is p + D u B, without a difference
 // that would lose small p).  Sums over a channel's states as in the forward; dB and dC are summed
-// over a warp's channels by lanes that each end with one of their 2 NP values, over the CTA's warps
-// in shared memory and over the CTAs by a second kernel, always in the same order.
+// over a thread's two channels, over a warp's by lanes that each end with one of the 8 values of
+// four states, over the CTA's warps in shared memory and over the CTAs by a second kernel,
+// always in the same order.
 #include "kda_scan.cuh"
 
 namespace kda {
 namespace scan {
 namespace {
 
-constexpr int kHalf = 8;
+constexpr int kHalf = 8, kWarps = kThreads / 32;
 
-template <int NP> struct Smem {
+// Registers: as many as a launch of two CTAs a multiprocessor has, moved to the half that walks.
+constexpr int kLaunchRegs = 128, kWalkRegs = 168, kOtherRegs = 88;
+static_assert(kWalkRegs + kOtherRegs == 2 * kLaunchRegs, "");
+
+template <typename T, int NP, bool ENDS> struct Smem {
     using S = Shape<NP>;
-    float4 dx[kTile][S::CH];       // step size twice, step size times input twice
-    float g[kTile][S::CH];         // dy'
-    float B[kTile][NP], C[kTile][NP];
-    float sum[3][kTile][S::kRow];  // over a channel's states: g B, g p A, C h
-    float bc[kThreads / 32][kHalf][2 * NP];
+    static constexpr int kStages = sizeof(T) * S::kPer > 4 ? 3 : 4;
+    static constexpr int kSum = kTile * S::kRow + 16;
+    float d[2][S::CH * kTile], x[2][S::CH * kTile], g[2][S::CH * kTile];  // D, D u, dy': place()
+    float B[2][S::L][S::kVec], C[2][S::L][S::kVec];
+    float sum[ENDS ? 1 : 2][3][kSum];  // over a channel's states: g B, g p A, C h, [kTile][kRow] each
+    float bc[ENDS ? 1 : 2][kWarps][kTile][2 * NP];
+    float4 h[ENDS ? 1 : 2][2][kThreads];           // the states in front of a tile: each thread's own
+    Vec<T, 8> raw[kStages][4][S::kPer][kThreads];  // u, delta, dy, z: a slot of each thread
 };
 
-// The first pass over segments: what each one's tokens leave of g in front of it.
-template <typename T, int NP>
-__global__ void __launch_bounds__(kThreads) kda_scan_bwd_ends_kernel(const ScanArgs a, int nb, bool vec) {
+// ENDS: the first pass over segments, which leaves what each one's tokens make of g in front of it.
+template <typename T, int NP, bool ENDS>
+__global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const ScanArgs a, int nb, int unit) {
     wait_for_previous();
     using S = Shape<NP>;
-    __shared__ float2 sdg[kTile][S::CH];
-    __shared__ __align__(16) float sC[kTile][NP], st[kTile][S::kRow];
-    const int tid = threadIdx.x, c = tid / S::L, n0 = 4 * (tid % S::L);
+    using M = Smem<T, NP, ENDS>;
+    extern __shared__ __align__(16) char smem[];
+    M &s = *reinterpret_cast<M *>(smem);
+    constexpr int kStages = M::kStages;
     const Block<NP> k(a, nb);
     const Piece &p = k.p;
-    if (p.len < 0 || p.begin == 0) return;
-    const bool in = c < k.channels;
-    const size_t ch = (size_t)k.c0 + c;
-    const Four A2 = scaled(load_states(a.A, ch, n0, a.N, in), kLog2e);
-    Four g = {both(0.f), both(0.f)};
-    const int q = tid % S::kQuads, qt = tid / S::kQuads, qc = k.c0 + 4 * q, left = k.channels - 4 * q;
-    constexpr int kStep = kThreads / S::kQuads;
-    float total[4] = {};
-    Vec<T, 4> dl[S::kPer], dy[S::kPer], z[S::kPer];
-    Vectors<T, NP> vc;
-    auto fetch = [&](int t0) {
-        const int rows = t0 < 0 ? 0 : p.len - t0;
-        const long long row0 = p.row0 + p.begin + t0;
-        const bool fine = rows <= 0 || dbg_ok(a.dbg, (size_t)(row0 + min(rows, kTile) - 1), (size_t)a.tok.rows(), DBG_LOAD);
+    if (ENDS && (p.len < 0 || p.begin == 0)) return;
+    // tiles are taken from the last to the first: step i is tile tiles - 1 - i
+    const int tiles = p.len > 0 ? (p.len + kTile - 1) / kTile : 0;
+    const long long first = p.row0 + p.begin;
+    const size_t seg = (size_t)k.slot * a.D;
+    auto rows_of = [&](int i) { return i < tiles ? min(kTile, p.len - (tiles - 1 - i) * kTile) : 0; };
+    if (threadIdx.x < kThreads) {  // the walk
+        if (!ENDS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWalkRegs));
+        const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, part = tid % S::L, n0 = 4 * part;
+        const int c[2] = {tid / S::L, tid / S::L + S::HC};
+        float A2[2][4], carry[2][4];
+        float2 dA[2][4] = {};
 #pragma unroll
-        for (int i = 0; i < S::kPer; ++i) {
-            const int t = qt + i * kStep;
-            const bool ok = t < kTile && t < rows && fine;
-            dl[i] = load_quad<T>(a.delta, a.delta_stride, row0 + t, qc, left, ok, vec);
-            dy[i] = load_quad<T>(a.dy, a.dy_stride, row0 + t, qc, left, ok, vec);
-            if (a.z) z[i] = load_quad<T>(a.z, a.z_stride, row0 + t, qc, left, ok, vec);
-        }
-        vc.load(a.C, a.C_stride, row0, fine ? rows : 0, k.group, a.N);
-    };
-    const int last = (p.len - 1) / kTile * kTile;
-    fetch(last);
-    for (int t0 = last; t0 >= 0; t0 -= kTile) {
-#pragma unroll
-        for (int i = 0; i < S::kPer; ++i) {
-            const int t = qt + i * kStep;
-            if (t >= kTile) continue;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float d = dl[i][e] + (a.delta_bias && e < left ? a.delta_bias[qc + e] : 0.f);
-                if (a.softplus) d = softplus(d);
-                if (t >= p.len - t0) d = 0.f;
-                float y = dy[i][e];
-                if (a.z) y *= z[i][e] * sigmoid(z[i][e]);
-                total[e] += d;
-                sdg[t][4 * q + e] = make_float2(d, y);
-            }
-        }
-        vc.put(sC);
-        fetch(t0 - kTile);
-        __syncthreads();
-#pragma unroll
-        for (int t = kTile - 1; t >= 0; --t) {
-            const float2 x = sdg[t][c];
-            g = mul(fma(both(x.y), four(*(const float4 *)&sC[t][n0]), g), decay(both(x.x), A2));
-        }
-        __syncthreads();
-    }
-    const size_t at = (size_t)k.slot * a.D;
-    if (in && dbg_ok(a.dbg, (at + ch) * NP + NP - 1, a.segment_floats, DBG_STORE))
-        *(float4 *)(a.ends + (at + ch) * NP + n0) = one(g);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (qt < kTile) st[qt][4 * q + e] = total[e];
-    __syncthreads();
-    if (tid < k.channels) {
-        float s = 0.f;
-        for (int t = 0; t < min(kTile, kStep); ++t) s += st[t][tid];
-        a.sums[at + k.c0 + tid] = s;
-    }
-}
-
-template <typename T, int NP>
-__global__ void __launch_bounds__(kThreads, 4) kda_scan_bwd_kernel(const ScanArgs a, int nb, bool vec) {
-    wait_for_previous();
-    using S = Shape<NP>;
-    extern __shared__ __align__(16) char raw[];
-    Smem<NP> &s = *reinterpret_cast<Smem<NP> *>(raw);
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
-    const int c = tid / S::L, part = tid % S::L, n0 = 4 * part;
-    const Block<NP> k(a, nb);
-    const Piece &p = k.p;
-    const bool in = c < k.channels;
-    const size_t ch = (size_t)k.c0 + c;
-    const Four A2 = scaled(load_states(a.A, ch, n0, a.N, in), kLog2e);
-    Four carry = {both(0.f), both(0.f)}, dA = carry;
-    if (p.len >= 0 && in) {  // from the segments behind this one
-        carry = load_states(a.d_final, (size_t)p.seq * a.D + ch, n0, a.N, a.d_final);
-        const int behind = (p.total + a.segment - 1) / a.segment - 1 - p.index;
-        for (int j = k.slot + behind; j > k.slot; --j) {
-            const size_t at = (size_t)j * a.D + ch;
-            if (!dbg_ok(a.dbg, at * NP + NP - 1, a.segment_floats, DBG_LOAD)) break;
-            carry = fma(decay(both(a.sums[at]), A2), carry, four(*(const float4 *)(a.ends + at * NP + n0)));
-        }
-    }
-    const int q = tid % S::kQuads, qt = tid / S::kQuads, qc = k.c0 + 4 * q, left = k.channels - 4 * q;
-    constexpr int kStep = kThreads / S::kQuads;
-    float bias[4], skip[4], dskip[4] = {}, dbias[4] = {};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        bias[i] = a.delta_bias && i < left ? a.delta_bias[qc + i] : 0.f;
-        skip[i] = a.skip && i < left ? a.skip[qc + i] : 0.f;
-    }
-    const long long tile0 = k.tiles0(a) + p.begin / kTile;
-    const int first = p.len > 0 ? (p.len - 1) / kTile * kTile : -1;
-    for (int t0 = first; t0 >= 0; t0 -= kTile) {
-        const int rows = min(kTile, p.len - t0);
-        const long long row0 = p.row0 + p.begin + t0;
-        const bool fine = dbg_ok(a.dbg, (size_t)(row0 + rows - 1), (size_t)a.tok.rows(), DBG_LOAD | DBG_STORE);
-        Vec<T, 4> u[S::kPer], dl[S::kPer], z[S::kPer], dy[S::kPer];
-        Vectors<T, NP> vb, vc;
-#pragma unroll
-        for (int i = 0; i < S::kPer; ++i) {
-            const int t = qt + i * kStep;
-            const bool ok = t < rows && fine;
-            u[i] = load_quad<T>(a.u, a.u_stride, row0 + t, qc, left, ok, vec);
-            dl[i] = load_quad<T>(a.delta, a.delta_stride, row0 + t, qc, left, ok, vec);
-            dy[i] = load_quad<T>(a.dy, a.dy_stride, row0 + t, qc, left, ok, vec);
-            if (a.z) z[i] = load_quad<T>(a.z, a.z_stride, row0 + t, qc, left, ok, vec);
-        }
-        vb.load(a.B, a.B_stride, row0, fine ? rows : 0, k.group, a.N);
-        vc.load(a.C, a.C_stride, row0, fine ? rows : 0, k.group, a.N);
-        Four h0 = {both(0.f), both(0.f)};
-        {
-            const size_t at = ((size_t)(tile0 + t0 / kTile) * a.D + ch) * NP + n0;
-            if (in && dbg_ok(a.dbg, at + 3, a.saved_floats, DBG_LOAD)) h0 = four(*(const float4 *)(a.saved + at));
-        }
-#pragma unroll
-        for (int i = 0; i < S::kPer; ++i) {
-            const int t = qt + i * kStep;
-            if (t >= kTile) continue;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float d = dl[i][e] + bias[e];
-                if (a.softplus) d = softplus(d);
-                if (t >= rows) d = 0.f;
-                const float x = d * u[i][e];
-                s.dx[t][4 * q + e] = make_float4(d, d, x, x);
-                s.g[t][4 * q + e] = a.z ? dy[i][e] * z[i][e] * sigmoid(z[i][e]) : dy[i][e];
-            }
-        }
-        vb.put(s.B);
-        vc.put(s.C);
-        __syncthreads();
-#pragma unroll 1
-        for (int half = 1; half >= 0; --half) {
-            Four h = h0, pr[kHalf];
-            if (half == 1) {
-#pragma unroll
-                for (int t = 0; t < kHalf; ++t) {
-                    const float4 dx = s.dx[t][c];
-                    h = fma(decay(make_float2(dx.x, dx.y), A2), h,
-                            mul(make_float2(dx.z, dx.w), four(*(const float4 *)&s.B[t][n0])));
+        for (int j = 0; j < 2; ++j) {
+            const bool in = c[j] < k.channels;
+            const size_t ch = (size_t)k.c0 + c[j];
+            const Four Aj = scaled(load_states(a.A, ch, n0, a.N, in), kLog2e);
+            Four g = {both(0.f), both(0.f)};
+            if (!ENDS && p.len >= 0 && in) {  // from the segments behind this one
+                g = load_states(a.d_final, (size_t)p.seq * a.D + ch, n0, a.N, a.d_final);
+                const int behind = (p.total + a.segment - 1) / a.segment - 1 - p.index;
+                for (int i = k.slot + behind; i > k.slot; --i) {
+                    const size_t at = (size_t)i * a.D + ch;
+                    if (!dbg_ok(a.dbg, at * NP + NP - 1, a.segment_floats, DBG_LOAD)) break;
+                    g = fma(decay(both(a.sums[at]), Aj), g, four(*(const float4 *)(a.ends + at * NP + n0)));
                 }
             }
 #pragma unroll
-            for (int j = 0; j < kHalf; ++j) {
-                const int t = half * kHalf + j;
-                const float4 dx = s.dx[t][c];
-                pr[j] = mul(decay(make_float2(dx.x, dx.y), A2), h);
-                h = fma(make_float2(dx.z, dx.w), four(*(const float4 *)&s.B[t][n0]), pr[j]);
+            for (int n = 0; n < 4; ++n) {
+                A2[j][n] = Aj.get(n);
+                carry[j][n] = g.get(n);
             }
+        }
+        const long long tile0 = k.tiles0(a) + p.begin / kTile;
+        auto states = [&](int i) {
 #pragma unroll
-            for (int jb = kHalf - 4; jb >= 0; jb -= 4) {
-                float gb[4], gpa[4], y[4];
+            for (int j = 0; j < 2; ++j) {
+                const size_t at = ((size_t)(tile0 + tiles - 1 - i) * a.D + k.c0 + c[j]) * NP + n0;
+                const bool in = i < tiles && c[j] < k.channels && dbg_ok(a.dbg, at + 3, a.saved_floats, DBG_LOAD);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 (uint32_t)__cvta_generic_to_shared(&s.h[ENDS ? 0 : i & 1][j][tid])),
+                             "l"(a.saved + (in ? at : 0)), "r"(in ? 16 : 0)
+                             : "memory");
+            }
+            cp_async_commit();
+        };
+        Phase phase(smem);
+        if (!ENDS && tiles > 0) states(0);
+        if (tiles > 0) sync_all();
+        for (int i = 0; i < tiles; ++i) {
+            const int b = i & 1;
+            if (!ENDS) {
+                states(i + 1);
+                cp_async_wait_newest<1>();
+            }
+            phase.next();
+            auto off = [&](const void *at) { return (uint32_t)((const char *)at - smem); };
+            const uint32_t od[2] = {off(s.d[b] + place(c[0], 0)), off(s.d[b] + place(c[1], 0))};
+            const uint32_t ox = off(s.x[b]) - off(s.d[b]), og = off(s.g[b]) - off(s.d[b]);
+            const uint32_t oB = off(s.B[b][part]), oC = off(s.C[b][part]);
+            // token t of a channel is at its place: groups of four change places (a XOR)
+            const uint32_t turn[2] = {(uint32_t)(c[0] >> 3 & 3) << 4, (uint32_t)(c[1] >> 3 & 3) << 4};
+            auto at4 = [&](int j, int g) { return (od[j] & ~48u) + (((uint32_t)g << 4) ^ turn[j]); };
+            if (ENDS) {
 #pragma unroll
-                for (int i = 3; i >= 0; --i) {
-                    const int j = jb + i, t = half * kHalf + j;
-                    const float4 dx = s.dx[t][c];
-                    const float2 dd = make_float2(dx.x, dx.y), xx = make_float2(dx.z, dx.w);
-                    const float2 gg = both(s.g[t][c]);
-                    const Four Bv = four(*(const float4 *)&s.B[t][n0]), Cv = four(*(const float4 *)&s.C[t][n0]);
-                    const Four g = fma(gg, Cv, carry), hj = fma(xx, Bv, pr[j]), gp = mul(g, pr[j]);
-                    gb[i] = dot(g, Bv);
-                    gpa[i] = dot(gp, A2);
-                    y[i] = dot(hj, Cv);
-                    dA = fma(dd, gp, dA);
-                    carry = mul(g, decay(dd, A2));
-                    const Four b = mul(xx, g), cc = mul(gg, hj);
-                    float v[8] = {b.lo.x, b.lo.y, b.hi.x, b.hi.y, cc.lo.x, cc.lo.y, cc.hi.x, cc.hi.y};
-                    constexpr int CW = 32 / S::L, kLeft = CW < 8 ? 8 / CW : 1;
-                    scatter_sum<CW, S::L>(v, lane);
-                    const int cl = lane / S::L;  // channel in the warp
-                    if (CW <= 8 || cl % (CW / 8 > 0 ? CW / 8 : 1) == 0) {
-                        const int at = CW < 8 ? cl * kLeft : cl / (CW / 8 > 0 ? CW / 8 : 1);
+                for (int g = kTile / 4 - 1; g >= 0; --g)
 #pragma unroll
-                        for (int x = 0; x < kLeft; ++x) {
-                            const int idx = at + x;  // 0..3: dB, 4..7: dC of the lane's states
-                            s.bc[warp][j][(idx < 4 ? 0 : NP) + n0 + (idx & 3)] = v[x];
+                    for (int j = 0; j < 2; ++j) {
+                        float2 d[2], gg[2];
+                        phase.load4(at4(j, g), d);
+                        phase.load4(at4(j, g) + og, gg);
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            float2 C[2];
+                            phase.load4(oC + (n * kTile + 4 * g) * 4, C);
+#pragma unroll
+                            for (int t = 1; t >= 0; --t) {
+                                const float2 e = mul2(d[t], both(A2[j][n])), in = mul2(gg[t], C[t]);
+                                carry[j][n] = (carry[j][n] + in.y) * ex2(e.y);
+                                carry[j][n] = (carry[j][n] + in.x) * ex2(e.x);
+                            }
+                        }
+                    }
+            } else {
+#pragma unroll 1
+                for (int half = rows_of(i) > kHalf ? 1 : 0; half >= 0; --half) {
+                    float h[2][4];
+                    float2 P[2][4][4];  // p of a channel's state, of the half's pairs of tokens
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float4 v = s.h[b][j][tid];
+                        h[j][0] = v.x; h[j][1] = v.y; h[j][2] = v.z; h[j][3] = v.w;
+                    }
+                    if (half == 1) {
+#pragma unroll
+                        for (int g = 0; g < 2; ++g)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                float2 d[2], x[2];
+                                phase.load4(at4(j, g), d);
+                                phase.load4(at4(j, g) + ox, x);
+#pragma unroll
+                                for (int n = 0; n < 4; ++n) {
+                                    float2 B[2];
+                                    phase.load4(oB + (n * kTile + 4 * g) * 4, B);
+#pragma unroll
+                                    for (int t = 0; t < 2; ++t) {
+                                        const float2 e = mul2(d[t], both(A2[j][n])), in = mul2(x[t], B[t]);
+                                        h[j][n] = fmaf(ex2(e.x), h[j][n], in.x);
+                                        h[j][n] = fmaf(ex2(e.y), h[j][n], in.y);
+                                    }
+                                }
+                            }
+                    }
+#pragma unroll
+                    for (int gl = 0; gl < 2; ++gl) {
+                        const int g = 2 * half + gl;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float2 d[2], x[2];
+                            phase.load4(at4(j, g), d);
+                            phase.load4(at4(j, g) + ox, x);
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) {
+                                float2 B[2];
+                                phase.load4(oB + (n * kTile + 4 * g) * 4, B);
+#pragma unroll
+                                for (int t = 0; t < 2; ++t) {
+                                    const float2 e = mul2(d[t], both(A2[j][n]));
+                                    float2 &pp = P[j][n][2 * gl + t];
+                                    pp.x = ex2(e.x) * h[j][n];
+                                    pp.y = ex2(e.y) * fmaf(x[t].x, B[t].x, pp.x);
+                                    h[j][n] = fmaf(x[t].y, B[t].y, pp.y);
+                                }
+                            }
+                        }
+                    }
+                    // back through the half, a pair of tokens at a time
+#pragma unroll
+                    for (int pi = 3; pi >= 0; --pi) {
+                        const int g = 2 * half + pi / 2, t0 = half * kHalf + 2 * pi;
+                        const uint32_t to = (pi & 1) * 8;
+                        float2 B[4], C[4], dB[4], dC[4];
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            B[n] = phase.load2(oB + (n * kTile + t0) * 4);
+                            C[n] = phase.load2(oC + (n * kTile + t0) * 4);
+                        }
+                        float ys[4];
+                        using W = Share<S::L>;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t at = at4(j, g) + to;
+                            const float2 d = phase.load2(at), x = phase.load2(at + ox), gg = phase.load2(at + og);
+                            float2 s1, s2, s3;
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) {
+                                const float2 pp = P[j][n][pi];
+                                const float2 e = mul2(d, both(A2[j][n])), hh = fma2(x, B[n], pp);
+                                float2 G;
+                                G.y = fmaf(gg.y, C[n].y, carry[j][n]);
+                                G.x = fmaf(gg.x, C[n].x, G.y * ex2(e.y));
+                                carry[j][n] = G.x * ex2(e.x);
+                                const float2 gp = mul2(G, pp);
+                                s1 = n ? fma2(G, B[n], s1) : mul2(G, B[n]);
+                                s2 = n ? fma2(gp, both(A2[j][n]), s2) : mul2(gp, both(A2[j][n]));
+                                s3 = n ? fma2(hh, C[n], s3) : mul2(hh, C[n]);
+                                dA[j][n] = fma2(gp, d, dA[j][n]);
+                                dB[n] = j ? fma2(G, x, dB[n]) : mul2(G, x);
+                                dC[n] = j ? fma2(hh, gg, dC[n]) : mul2(hh, gg);
+                            }
+                            float v[4] = {s1.x, s1.y, s2.x, s2.y};
+                            ys[2 * j] = s3.x;
+                            ys[2 * j + 1] = s3.y;
+                            scatter_sum<S::L, 1>(v, tid);
+                            if (W::mine(part)) {
+#pragma unroll
+                                for (int y = 0; y < W::kCount; ++y) {
+                                    const int idx = W::first(part) + y;
+                                    s.sum[ENDS ? 0 : b][idx >> 1][(t0 + (idx & 1)) * S::kRow + c[j]] = v[y];
+                                }
+                            }
+                        }
+                        if (a.z) {
+                            scatter_sum<S::L, 1>(ys, tid);
+                            if (W::mine(part)) {
+#pragma unroll
+                                for (int y = 0; y < W::kCount; ++y) {
+                                    const int idx = W::first(part) + y;
+                                    s.sum[ENDS ? 0 : b][2][(t0 + (idx & 1)) * S::kRow + (idx >> 1 ? c[1] : c[0])] = ys[y];
+                                }
+                            }
+                        }
+                        constexpr int CW = 32 / S::L, kLeft = CW < 8 ? 8 / CW : 1, kSame = CW > 8 ? CW / 8 : 1;
+                        const int cl = lane / S::L;  // place among the warp's channels
+#pragma unroll
+                        for (int t = 1; t >= 0; --t) {
+                            float v[8];
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) {
+                                v[n] = t ? dB[n].y : dB[n].x;
+                                v[4 + n] = t ? dC[n].y : dC[n].x;
+                            }
+                            scatter_sum<CW, S::L>(v, lane);
+                            if (cl % kSame == 0) {
+#pragma unroll
+                                for (int y = 0; y < kLeft; ++y) {
+                                    const int idx = cl / kSame * kLeft + y;  // 0..3: dB, 4..7: dC of this part's states
+                                    s.bc[ENDS ? 0 : b][warp][t0 + t][(idx < 4 ? 0 : NP) + n0 + (idx & 3)] = v[y];
+                                }
+                            }
                         }
                     }
                 }
-                scatter_sum<S::L, 1>(gb, tid);
-                scatter_sum<S::L, 1>(gpa, tid);
-                scatter_sum<S::L, 1>(y, tid);
-                using W = Share<S::L>;
-                if (W::mine(part)) {
-#pragma unroll
-                    for (int i = 0; i < W::kCount; ++i) {
-                        const int t = half * kHalf + jb + W::first(part) + i;
-                        s.sum[0][t][c] = gb[i];
-                        s.sum[1][t][c] = gpa[i];
-                        s.sum[2][t][c] = y[i];
-                    }
-                }
             }
-            __syncthreads();
-            for (int e = tid; e < kHalf * 2 * NP; e += kThreads) {
-                const int j = e / (2 * NP), x = e % (2 * NP), t = half * kHalf + j;
-                float v = 0.f;
-#pragma unroll
-                for (int w = 0; w < kThreads / 32; ++w) v += s.bc[w][j][x];
-                if (t < rows && fine)
-                    a.part_bc[(((size_t)k.blk * a.tok.rows() + row0 + t) * a.G + k.group) * 2 * NP + x] = v;
-            }
-            if (half == 1) __syncthreads();
+            sync_all();
         }
+        cp_async_wait_newest<0>();
+        float *per_state = ENDS ? a.ends : a.part_A;
 #pragma unroll
-        for (int i = 0; i < S::kPer; ++i) {
-            const int t = qt + i * kStep;
-            if (t >= rows || !fine) continue;
-            Vec<T, 4> du, dd, dz;
+        for (int j = 0; j < 2; ++j) {
+            const size_t ch = (size_t)k.c0 + c[j];
+            if (c[j] >= k.channels) continue;
+            if (!ENDS && p.len >= 0 && p.begin == 0 && a.d_initial &&
+                dbg_ok(a.dbg, (size_t)p.seq, (size_t)a.tok.num_seqs, DBG_STORE))
+                store_states(a.d_initial, (size_t)p.seq * a.D + ch, n0, a.N,
+                             four(make_float4(carry[j][0], carry[j][1], carry[j][2], carry[j][3])));
+            // this segment's share of dA (or its end)
+            if (!dbg_ok(a.dbg, (seg + ch) * NP + NP - 1, a.segment_floats, DBG_STORE)) continue;
+            float v[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) v[n] = ENDS ? carry[j][n] : dA[j][n].x + dA[j][n].y;
+            *(float4 *)(per_state + (seg + ch) * NP + n0) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+        return;
+    }
+    if (!ENDS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    // this thread's chunks of a tile: tokens qt + x kStep, channels 8 q ..
+    const int tid = threadIdx.x - kThreads;
+    const int q = tid % S::kChunks, qt = tid / S::kChunks, qc = k.c0 + 8 * q, left = k.channels - 8 * q;
+    constexpr int kStep = kThreads / S::kChunks;
+    // (the parameters are read anew for every tile, out of the cache: they would be 16 registers)
+    auto param = [&](const float *v, int e) {
+        return make_float2(v && 2 * e < left ? v[qc + 2 * e] : 0.f, v && 2 * e + 1 < left ? v[qc + 2 * e + 1] : 0.f);
+    };
+    float2 dskip[4] = {}, dbias[4] = {};  // (ENDS: dskip is the sum of the step sizes)
+    auto row_of = [&](int i) { return first + (tiles - 1 - i) * kTile; };
+    auto fine = [&](int i) {
+        return i >= tiles || dbg_ok(a.dbg, (size_t)(row_of(i) + rows_of(i) - 1), (size_t)a.tok.rows(), DBG_LOAD);
+    };
+    auto fetch = [&](int i) {
+        const int rows = fine(i) ? rows_of(i) : 0;
+        auto &raw = s.raw[i % kStages];
+#pragma unroll
+        for (int x = 0; x < S::kPer; ++x) {
+            const int t = qt + x * kStep;
+            const bool ok = t < kTile && t < rows;
+            const long long row = ok ? row_of(i) + t : 0;
+            if (!ENDS) fetch_chunk<T>(&raw[0][x][tid], a.u, a.u_stride, row, qc, left, ok, unit);
+            fetch_chunk<T>(&raw[1][x][tid], a.delta, a.delta_stride, row, qc, left, ok, unit);
+            fetch_chunk<T>(&raw[2][x][tid], a.dy, a.dy_stride, row, qc, left, ok, unit);
+            if (a.z) fetch_chunk<T>(&raw[3][x][tid], a.z, a.z_stride, row, qc, left, ok, unit);
+        }
+        cp_async_commit();
+    };
+    Vectors<T, NP> vb, vc;
+    auto vectors = [&](int i) {
+        const int rows = fine(i) ? rows_of(i) : 0;
+        const long long row = rows ? row_of(i) : 0;
+        if (!ENDS) vb.load(tid, a.B, a.B_stride, row, rows, k.group, a.N);
+        vc.load(tid, a.C, a.C_stride, row, rows, k.group, a.N);
+    };
+    auto prepare = [&](int i) {
+        const int rows = rows_of(i), b = i & 1;
+        auto &raw = s.raw[i % kStages];
+#pragma unroll
+        for (int x = 0; x < S::kPer; ++x) {
+            const int t = qt + x * kStep;
+            if (t >= kTile) continue;
+            const Vec<T, 8> dl = raw[1][x][tid], dy = raw[2][x][tid];
+            Vec<T, 8> u, z;
+            if (!ENDS) u = raw[0][x][tid];
+            if (a.z) z = raw[3][x][tid];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int cc = 4 * q + e;
-                const float gb = s.sum[0][t][cc], gpa = s.sum[1][t][cc] * kLn2, y = s.sum[2][t][cc];
-                const float d = s.dx[t][cc].x, g = s.g[t][cc], uu = u[i][e];
-                du.v[e] = from_f32<T>(fmaf(d, gb, skip[e] * g));
-                float x = fmaf(uu, gb, gpa);
-                if (a.softplus) x *= sigmoid(dl[i][e] + bias[e]);
-                dd.v[e] = from_f32<T>(x);
-                dbias[e] += x;
-                dskip[e] = fmaf(g, uu, dskip[e]);
+                float2 d = add2(pair(dl, e), param(a.delta_bias, e)), g = pair(dy, e);
+                if (a.softplus) d = softplus(d);
+                if (t >= rows) d = both(0.f);
                 if (a.z) {
-                    const float zz = z[i][e];
-                    dz.v[e] = from_f32<T>(dy[i][e] * fmaf(skip[e], uu, y) * silu_slope(zz, sigmoid(zz)));
+                    const float2 zz = pair(z, e);
+                    g = mul2(g, mul2(zz, sigmoid2(zz)));
+                }
+                const int at = place(8 * q + 2 * e, t >> 2) + (t & 3);
+                s.d[b][at] = d.x;
+                s.d[b][at + kTile] = d.y;
+                s.g[b][at] = g.x;
+                s.g[b][at + kTile] = g.y;
+                if (ENDS) {
+                    dskip[e] = add2(dskip[e], d);
+                } else {
+                    const float2 v = mul2(d, pair(u, e));
+                    s.x[b][at] = v.x;
+                    s.x[b][at + kTile] = v.y;
                 }
             }
-            store_quad(a.du, a.du_stride, row0 + t, qc, left, du, vec);
-            store_quad(a.ddelta, a.ddelta_stride, row0 + t, qc, left, dd, vec);
-            if (a.z) store_quad(a.dz, a.dz_stride, row0 + t, qc, left, dz, vec);
         }
-        __syncthreads();
-    }
-    if (p.len >= 0 && p.begin == 0 && in && a.d_initial && dbg_ok(a.dbg, (size_t)p.seq, (size_t)a.tok.num_seqs, DBG_STORE))
-        store_states(a.d_initial, (size_t)p.seq * a.D + ch, n0, a.N, carry);
-    // the parameters' sums over this segment
-    const size_t at = (size_t)k.slot * a.D;
-    if (in && dbg_ok(a.dbg, (at + ch) * NP + NP - 1, a.segment_floats, DBG_STORE))
-        *(float4 *)(a.part_A + (at + ch) * NP + n0) = one(dA);
+        if (!ENDS) vb.put(tid, s.B[b]);
+        vc.put(tid, s.C[b]);
+    };
+    // What a tile's sums make: the gradients of its tokens (its d, x and g are this thread's own).
+    auto finish = [&](int i) {
+        const int rows = fine(i) ? rows_of(i) : 0, b = i & 1;
+        auto &raw = s.raw[i % kStages];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (qt < kTile) {
-            s.sum[0][qt][4 * q + e] = dskip[e];
-            s.sum[1][qt][4 * q + e] = dbias[e];
+        for (int x = 0; x < S::kPer; ++x) {
+            const int t = qt + x * kStep;
+            if (t >= kTile || t >= rows) continue;
+            const long long row = row_of(i) + t;
+            const Vec<T, 8> u = raw[0][x][tid], dl = raw[1][x][tid], dy = raw[2][x][tid];
+            Vec<T, 8> z, du, dd, dz;
+            if (a.z) z = raw[3][x][tid];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int cc = 8 * q + 2 * e, at = place(cc, t >> 2) + (t & 3), sat = t * S::kRow + cc;
+                const float2 gb = *(const float2 *)&s.sum[b][0][sat], gpa = *(const float2 *)&s.sum[b][1][sat];
+                const float2 d = make_float2(s.d[b][at], s.d[b][at + kTile]), skip = param(a.skip, e);
+                const float2 g = make_float2(s.g[b][at], s.g[b][at + kTile]), uu = pair(u, e);
+                put_pair(du, e, fma2(d, gb, mul2(skip, g)));
+                float2 v = fma2(uu, gb, mul2(gpa, both(kLn2)));
+                if (a.softplus) v = mul2(v, sigmoid2(add2(pair(dl, e), param(a.delta_bias, e))));
+                put_pair(dd, e, v);
+                dbias[e] = add2(dbias[e], v);
+                dskip[e] = fma2(g, uu, dskip[e]);
+                if (a.z) {
+                    const float2 y = fma2(skip, uu, *(const float2 *)&s.sum[b][2][sat]);
+                    const float2 zz = pair(z, e), sg = sigmoid2(zz);
+                    const float2 slope = mul2(sg, fma2(zz, fma2(sg, both(-1.f), both(1.f)), both(1.f)));
+                    put_pair(dz, e, mul2(mul2(pair(dy, e), y), slope));
+                }
+            }
+            store_chunk(a.du, a.du_stride, row, qc, left, du, unit);
+            store_chunk(a.ddelta, a.ddelta_stride, row, qc, left, dd, unit);
+            if (a.z) store_chunk(a.dz, a.dz_stride, row, qc, left, dz, unit);
         }
-    __syncthreads();
+        for (int e = tid; e < kTile * 2 * NP; e += kThreads) {
+            const int t = e / (2 * NP), x = e % (2 * NP);
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v += s.bc[b][w][t][x];
+            if (t < rows)
+                a.part_bc[(((size_t)k.blk * a.tok.rows() + row_of(i) + t) * a.G + k.group) * 2 * NP + x] = v;
+        }
+    };
+    if (tiles > 0) {
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) fetch(i);
+        vectors(0);
+        cp_async_wait_newest<kStages - 2>();
+        prepare(0);
+        vectors(1);
+        sync_all();
+    }
+    for (int i = 0; i < tiles; ++i) {
+        if (!ENDS && i > 0) finish(i - 1);
+        if (i + 1 < tiles) {
+            cp_async_wait_newest<kStages - 3>();
+            prepare(i + 1);
+            vectors(i + 2);
+        }
+        fetch(i + kStages - 1);
+        sync_all();
+    }
+    if (!ENDS && tiles > 0) finish(tiles - 1);
+    // sums of the threads of a chunk's channels, which each have some tokens
+    sync_half();
+    auto &sum = s.sum[0];
+    if (qt < kTile) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int at = qt * S::kRow + 8 * q + 2 * e;
+            sum[0][at] = dskip[e].x;
+            sum[0][at + 1] = dskip[e].y;
+            sum[1][at] = dbias[e].x;
+            sum[1][at + 1] = dbias[e].y;
+        }
+    }
+    sync_half();
     if (tid < k.channels) {
         float x = 0.f, y = 0.f;
         for (int t = 0; t < min(kTile, kStep); ++t) {
-            x += s.sum[0][t][tid];
-            y += s.sum[1][t][tid];
+            x += sum[0][t * S::kRow + tid];
+            y += sum[1][t * S::kRow + tid];
         }
-        a.part_D[2 * at + k.c0 + tid] = x;
-        a.part_D[2 * at + a.D + k.c0 + tid] = y;
+        if (ENDS) {
+            a.sums[seg + k.c0 + tid] = x;
+        } else {
+            a.part_D[2 * seg + k.c0 + tid] = x;
+            a.part_D[2 * seg + a.D + k.c0 + tid] = y;
+        }
     }
+    cp_async_wait_newest<0>();
 }
 
 // dB and dC of the tokens that are in a sequence: sums over the blocks of channels, in order.
@@ -337,25 +487,31 @@ __global__ void __launch_bounds__(256) kda_scan_sum_params_kernel(const ScanArgs
     }
 }
 
-template <typename T, int NP> cudaError_t launch(const ScanArgs &a, cudaStream_t stream) {
-    const int per = a.D / a.G, nb = (per + Shape<NP>::CH - 1) / Shape<NP>::CH;
-    const bool vec = per % 4 == 0 && vec_ok(a, a.u, a.u_stride) && vec_ok(a, a.delta, a.delta_stride) &&
-                     vec_ok(a, a.z, a.z_stride) && vec_ok(a, a.dy, a.dy_stride) &&
-                     vec_ok(a, a.du, a.du_stride) && vec_ok(a, a.ddelta, a.ddelta_stride) &&
-                     vec_ok(a, a.dz, a.dz_stride);
-    const long long slots = a.tok.pieces(a.segment);
-    const unsigned grid = (unsigned)(slots * nb * a.G);
-    constexpr int kBytes = sizeof(Smem<NP>);
+template <typename T, int NP, bool ENDS>
+cudaError_t walk(const ScanArgs &a, int nb, int unit, cudaStream_t stream) {
+    constexpr int kBytes = sizeof(Smem<T, NP, ENDS>);
+    static_assert(kBytes <= 227 * 1024, "");
     static volatile int done[kMaxDev];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = smem_limit_once(kda_scan_bwd_kernel<T, NP>, kBytes, dev, done);
+    if (e == cudaSuccess) e = smem_limit_once(kda_scan_bwd_kernel<T, NP, ENDS>, kBytes, dev, done);
     if (e != cudaSuccess) return e;
-    if (a.ends) {
-        e = launch_early(kda_scan_bwd_ends_kernel<T, NP>, grid, kThreads, 0, stream, a, nb, vec);
-        if (e != cudaSuccess) return e;
-    }
-    e = launch_early(kda_scan_bwd_kernel<T, NP>, grid, kThreads, kBytes, stream, a, nb, vec);
+    return launch_early(kda_scan_bwd_kernel<T, NP, ENDS>, (unsigned)(a.tok.pieces(a.segment) * nb * a.G),
+                        2 * kThreads, kBytes, stream, a, nb, unit);
+}
+template <typename T, int NP> cudaError_t launch(const ScanArgs &a, cudaStream_t stream) {
+    const int per = a.D / a.G, nb = (per + Shape<NP>::CH - 1) / Shape<NP>::CH;
+    const long long slots = a.tok.pieces(a.segment);
+    Unit u(a);
+    u.add(a.u, a.u_stride);
+    u.add(a.delta, a.delta_stride);
+    u.add(a.z, a.z_stride);
+    u.add(a.dy, a.dy_stride);
+    u.add(a.du, a.du_stride);
+    u.add(a.ddelta, a.ddelta_stride);
+    u.add(a.dz, a.dz_stride);
+    cudaError_t e = a.ends ? walk<T, NP, true>(a, nb, u.unit, stream) : cudaSuccess;
+    if (e == cudaSuccess) e = walk<T, NP, false>(a, nb, u.unit, stream);
     if (e != cudaSuccess) return e;
     const long long bc = a.tok.rows() * a.G * 2 * NP;
     if (bc) {
@@ -369,7 +525,7 @@ template <typename T, int NP> cudaError_t launch(const ScanArgs &a, cudaStream_t
 
 template <typename T> cudaError_t pick(const ScanArgs &a, cudaStream_t stream) {
     switch (scan_padded(a.N)) {
-        case 4: return launch<T, 4>(a, stream);
+        
         case 8: return launch<T, 8>(a, stream);
         case 16: return launch<T, 16>(a, stream);
         case 32: return launch<T, 32>(a, stream);

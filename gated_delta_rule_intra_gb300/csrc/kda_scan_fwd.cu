@@ -1,168 +1,282 @@
 // Selective scan, forward (kda_scan.cuh).
+//
+// A tile's three phases -- preparing the next tile, the scan of this one, finishing the one before --
+// have buffers of their own, so that one barrier a tile joins them; inputs are asked for three
+// tiles ahead.
 #include "kda_scan.cuh"
 
 namespace kda {
 namespace scan {
 namespace {
 
+constexpr int kStages = 4;
+
+template <typename T, int NP> struct Smem {
+    using S = Shape<NP>;
+    float d[2][S::CH * kTile], x[2][S::CH * kTile];  // step size, step size times input: place()
+    float B[2][S::L][S::kVec], C[2][S::L][S::kVec];
+    float y[2][kTile][S::kRow];                       // sums over a channel's states
+    Vec<T, 8> raw[kStages][3][S::kPer][kThreads];     // u, delta, z: a slot of each thread
+};
+
 // ENDS: the first pass, which leaves the segments' ends.
 template <typename T, int NP, bool ENDS>
-__global__ void __launch_bounds__(kThreads) kda_scan_fwd_kernel(const ScanArgs a, int nb, bool vec) {
+__global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const ScanArgs a, int nb, int unit) {
     wait_for_previous();
     using S = Shape<NP>;
-    __shared__ float4 sdx[kTile][S::CH];  // step size twice, step size times input twice
-    __shared__ __align__(16) float sB[kTile][NP], sC[kTile][NP], sy[kTile][S::kRow];
-    const int tid = threadIdx.x, c = tid / S::L, part = tid % S::L, n0 = 4 * part;
+    extern __shared__ __align__(16) char smem[];
+    Smem<T, NP> &s = *reinterpret_cast<Smem<T, NP> *>(smem);
     const Block<NP> k(a, nb);
     const Piece &p = k.p;
     if (p.len < 0 || (ENDS && p.begin + p.len == p.total)) return;
-    const bool in = c < k.channels;
-    const size_t ch = (size_t)k.c0 + c;
-    const Four A2 = scaled(load_states(a.A, ch, n0, a.N, in), kLog2e);
-    Four h = {both(0.f), both(0.f)};
-    if (!ENDS) {
-        h = load_states(a.initial, (size_t)p.seq * a.D + ch, n0, a.N, in && a.initial);
-        if (in) {
-            for (int j = k.slot - p.index; j < k.slot; ++j) {
-                const size_t at = (size_t)j * a.D + ch;
-                if (!dbg_ok(a.dbg, at * NP + NP - 1, a.segment_floats, DBG_LOAD)) break;
-                h = fma(decay(both(a.sums[at]), A2), h, four(*(const float4 *)(a.ends + at * NP + n0)));
+    const int tiles = (p.len + kTile - 1) / kTile;
+    const long long first = p.row0 + p.begin;
+    const size_t seg = (size_t)k.slot * a.D;
+    if (threadIdx.x < kThreads) {  // the scan
+        const int tid = threadIdx.x, part = tid % S::L, n0 = 4 * part;
+        const int c[2] = {tid / S::L, tid / S::L + S::HC};
+        float A2[2][4], h[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const bool in = c[j] < k.channels;
+            const size_t ch = (size_t)k.c0 + c[j];
+            const Four Aj = scaled(load_states(a.A, ch, n0, a.N, in), kLog2e);
+            Four hj = {both(0.f), both(0.f)};
+            if (!ENDS && in) {
+                hj = load_states(a.initial, (size_t)p.seq * a.D + ch, n0, a.N, a.initial);
+                for (int g = k.slot - p.index; g < k.slot; ++g) {
+                    const size_t at = (size_t)g * a.D + ch;
+                    if (!dbg_ok(a.dbg, at * NP + NP - 1, a.segment_floats, DBG_LOAD)) break;
+                    hj = fma(decay(both(a.sums[at]), Aj), hj, four(*(const float4 *)(a.ends + at * NP + n0)));
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                A2[j][n] = Aj.get(n);
+                h[j][n] = hj.get(n);
             }
         }
-    }
-    // this thread's quads of a tile: token q0 + i kThreads / kQuads, channels 4 q ..
-    const int q = tid % S::kQuads, qt = tid / S::kQuads, qc = k.c0 + 4 * q, left = k.channels - 4 * q;
-    constexpr int kStep = kThreads / S::kQuads;
-    float bias[4], skip[4];
+        const long long tile0 = k.tiles0(a) + p.begin / kTile;
+        Phase phase(smem);
+        if (tiles > 0) sync_all();
+        for (int tile = 0; tile < tiles; ++tile) {
+            const int b = tile & 1;
+            phase.next();
+            if (!ENDS && a.saved) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        bias[i] = a.delta_bias && i < left ? a.delta_bias[qc + i] : 0.f;
-        skip[i] = a.skip && i < left ? a.skip[qc + i] : 0.f;
-    }
-    Vec<T, 4> u[S::kPer], dl[S::kPer], z[S::kPer];
-    Vectors<T, NP> vb, vc;
-    auto fetch = [&](int t0) {
-        const int rows = p.len - t0;
-        const long long row0 = p.row0 + p.begin + t0;
-        const bool fine = rows <= 0 || dbg_ok(a.dbg, (size_t)(row0 + min(rows, kTile) - 1), (size_t)a.tok.rows(), DBG_LOAD);
+                for (int j = 0; j < 2; ++j) {
+                    const size_t at = ((size_t)(tile0 + tile) * a.D + k.c0 + c[j]) * NP + n0;
+                    if (c[j] < k.channels && dbg_ok(a.dbg, at + 3, a.saved_floats, DBG_STORE))
+                        *(float4 *)(a.saved + at) = make_float4(h[j][0], h[j][1], h[j][2], h[j][3]);
+                }
+            }
+            const uint32_t od = (uint32_t)((char *)s.d[b] - smem), ox = (uint32_t)((char *)s.x[b] - smem);
+            const uint32_t oB = (uint32_t)((char *)s.B[b][part] - smem), oC = (uint32_t)((char *)s.C[b][part] - smem);
 #pragma unroll
-        for (int i = 0; i < S::kPer; ++i) {
-            const int t = qt + i * kStep;
-            const bool ok = t < kTile && t < rows && fine;
-            u[i] = load_quad<T>(a.u, a.u_stride, row0 + t, qc, left, ok, vec);
-            dl[i] = load_quad<T>(a.delta, a.delta_stride, row0 + t, qc, left, ok, vec);
-            if (!ENDS && a.z) z[i] = load_quad<T>(a.z, a.z_stride, row0 + t, qc, left, ok, vec);
+            for (int g = 0; g < kTile / 4; ++g) {
+                float2 B[4][2], C[4][2];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    phase.load4(oB + (n * kTile + 4 * g) * 4, B[n]);
+                    if (!ENDS) phase.load4(oC + (n * kTile + 4 * g) * 4, C[n]);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float2 d[2], x[2];
+                    phase.load4(od + 4 * place(c[j], g), d);
+                    phase.load4(ox + 4 * place(c[j], g), x);
+                    float y[4];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        float2 sum;
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            const float2 e = mul2(d[t], both(A2[j][n])), in = mul2(x[t], B[n][t]);
+                            float2 hh;
+                            hh.x = fmaf(ex2(e.x), h[j][n], in.x);
+                            hh.y = fmaf(ex2(e.y), hh.x, in.y);
+                            h[j][n] = hh.y;
+                            if (!ENDS) sum = n ? fma2(C[n][t], hh, sum) : mul2(C[n][t], hh);
+                        }
+                        y[2 * t] = sum.x;
+                        y[2 * t + 1] = sum.y;
+                    }
+                    if (!ENDS) {
+                        scatter_sum<S::L, 1>(y, tid);
+                        using W = Share<S::L>;
+                        if (W::mine(part)) {
+#pragma unroll
+                            for (int i = 0; i < W::kCount; ++i) s.y[b][4 * g + W::first(part) + i][c[j]] = y[i];
+                        }
+                    }
+                }
+            }
+            sync_all();
         }
-        vb.load(a.B, a.B_stride, row0, fine ? rows : 0, k.group, a.N);
-        if (!ENDS) vc.load(a.C, a.C_stride, row0, fine ? rows : 0, k.group, a.N);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const size_t ch = (size_t)k.c0 + c[j];
+            if (c[j] >= k.channels) continue;
+            if (ENDS && dbg_ok(a.dbg, (seg + ch) * NP + NP - 1, a.segment_floats, DBG_STORE))
+                *(float4 *)(a.ends + (seg + ch) * NP + n0) = make_float4(h[j][0], h[j][1], h[j][2], h[j][3]);
+            if (!ENDS && a.final && p.begin + p.len == p.total &&
+                dbg_ok(a.dbg, (size_t)p.seq, (size_t)a.tok.num_seqs, DBG_STORE))
+                store_states(a.final, (size_t)p.seq * a.D + ch, n0, a.N,
+                             four(make_float4(h[j][0], h[j][1], h[j][2], h[j][3])));
+        }
+        return;
+    }
+    // this thread's chunks of a tile: tokens qt + i kStep, channels 8 q ..
+    const int tid = threadIdx.x - kThreads;
+    const int q = tid % S::kChunks, qt = tid / S::kChunks, qc = k.c0 + 8 * q, left = k.channels - 8 * q;
+    constexpr int kStep = kThreads / S::kChunks;
+    float2 bias[4], skip[4], total[4] = {};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        auto param = [&](const float *v, int i) { return v && i < left ? v[qc + i] : 0.f; };
+        bias[e] = make_float2(param(a.delta_bias, 2 * e), param(a.delta_bias, 2 * e + 1));
+        skip[e] = make_float2(param(a.skip, 2 * e), param(a.skip, 2 * e + 1));
+    }
+    auto rows_of = [&](int tile) { return p.len - tile * kTile; };
+    auto fine = [&](int tile) {
+        const int rows = rows_of(tile);
+        return rows <= 0 || dbg_ok(a.dbg, (size_t)(first + tile * kTile + min(rows, kTile) - 1), (size_t)a.tok.rows(), DBG_LOAD);
     };
-    fetch(0);
-    float total[4] = {};
-    const long long tile0 = k.tiles0(a) + p.begin / kTile;
-    for (int t0 = 0; t0 < p.len; t0 += kTile) {
-        const int rows = min(kTile, p.len - t0);
-        Vec<T, 4> cu[S::kPer], cz[S::kPer];
+    auto fetch = [&](int tile) {
+        const int rows = fine(tile) ? rows_of(tile) : 0;
+        auto &raw = s.raw[tile % kStages];
 #pragma unroll
         for (int i = 0; i < S::kPer; ++i) {
             const int t = qt + i * kStep;
-            cu[i] = u[i];
-            cz[i] = z[i];
+            const bool ok = t < kTile && t < rows;
+            const long long row = ok ? first + tile * kTile + t : 0;
+            fetch_chunk<T>(&raw[0][i][tid], a.u, a.u_stride, row, qc, left, ok, unit);
+            fetch_chunk<T>(&raw[1][i][tid], a.delta, a.delta_stride, row, qc, left, ok, unit);
+            if (!ENDS && a.z) fetch_chunk<T>(&raw[2][i][tid], a.z, a.z_stride, row, qc, left, ok, unit);
+        }
+        cp_async_commit();
+    };
+    Vectors<T, NP> vb, vc;
+    auto vectors = [&](int tile) {
+        const int rows = fine(tile) ? rows_of(tile) : 0;
+        vb.load(tid, a.B, a.B_stride, first + tile * kTile, rows, k.group, a.N);
+        if (!ENDS) vc.load(tid, a.C, a.C_stride, first + tile * kTile, rows, k.group, a.N);
+    };
+    auto prepare = [&](int tile) {
+        const int rows = rows_of(tile), b = tile & 1;
+        auto &raw = s.raw[tile % kStages];
+#pragma unroll
+        for (int i = 0; i < S::kPer; ++i) {
+            const int t = qt + i * kStep;
             if (t >= kTile) continue;
+            const Vec<T, 8> u = raw[0][i][tid], dl = raw[1][i][tid];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float d = dl[i][e] + bias[e];
+                float2 d = add2(pair(dl, e), bias[e]);
                 if (a.softplus) d = softplus(d);
-                if (t >= rows) d = 0.f;  // nothing decays and nothing comes in behind the end
-                const float x = d * u[i][e];
-                if (ENDS) total[e] += d;
-                sdx[t][4 * q + e] = make_float4(d, d, x, x);
+                if (t >= rows) d = both(0.f);  // nothing decays and nothing comes in behind the end
+                const float2 x = mul2(d, pair(u, e));
+                if (ENDS) total[e] = add2(total[e], d);
+                const int at = place(8 * q + 2 * e, t >> 2) + (t & 3);
+                s.d[b][at] = d.x;
+                s.d[b][at + kTile] = d.y;
+                s.x[b][at] = x.x;
+                s.x[b][at + kTile] = x.y;
             }
         }
-        vb.put(sB);
-        if (!ENDS) vc.put(sC);
-        fetch(t0 + kTile);
-        __syncthreads();
-        if (!ENDS && a.saved && in) {
-            const size_t at = ((size_t)(tile0 + t0 / kTile) * a.D + ch) * NP + n0;
-            if (dbg_ok(a.dbg, at + 3, a.saved_floats, DBG_STORE)) *(float4 *)(a.saved + at) = one(h);
-        }
+        vb.put(tid, s.B[b]);
+        if (!ENDS) vc.put(tid, s.C[b]);
+    };
+    auto finish = [&](int tile) {
+        const int rows = rows_of(tile), b = tile & 1;
+        auto &raw = s.raw[tile % kStages];
 #pragma unroll
-        for (int tb = 0; tb < kTile; tb += 4) {
-            float y[4];
+        for (int i = 0; i < S::kPer; ++i) {
+            const int t = qt + i * kStep;
+            const long long row = first + tile * kTile + t;
+            if (t >= kTile || t >= rows || !dbg_ok(a.dbg, (size_t)row, (size_t)a.tok.rows(), DBG_STORE)) continue;
+            const float4 lo = *(const float4 *)&s.y[b][t][8 * q], hi = *(const float4 *)&s.y[b][t][8 * q + 4];
+            const float2 sum[4] = {make_float2(lo.x, lo.y), make_float2(lo.z, lo.w), make_float2(hi.x, hi.y),
+                                   make_float2(hi.z, hi.w)};
+            const Vec<T, 8> u = raw[0][i][tid];
+            Vec<T, 8> z, out;
+            if (a.z) z = raw[2][i][tid];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4 dx = sdx[tb + j][c];
-                const Four Bv = four(*(const float4 *)&sB[tb + j][n0]);
-                h = fma(decay(make_float2(dx.x, dx.y), A2), h, mul(make_float2(dx.z, dx.w), Bv));
-                if (!ENDS) y[j] = dot(h, four(*(const float4 *)&sC[tb + j][n0]));
-            }
-            if (!ENDS) {
-                scatter_sum<S::L, 1>(y, tid);
-                using W = Share<S::L>;
-                if (W::mine(part)) {
-#pragma unroll
-                    for (int j = 0; j < W::kCount; ++j) sy[tb + W::first(part) + j][c] = y[j];
+            for (int e = 0; e < 4; ++e) {
+                float2 y = fma2(skip[e], pair(u, e), sum[e]);
+                if (a.z) {
+                    const float2 g = pair(z, e);
+                    y = mul2(y, mul2(g, sigmoid2(g)));
                 }
+                put_pair(out, e, y);
             }
+            store_chunk(a.y, a.y_stride, row, qc, left, out, unit);
         }
-        __syncthreads();
-        if (!ENDS) {
+    };
+    if (tiles > 0) {
 #pragma unroll
-            for (int i = 0; i < S::kPer; ++i) {
-                const int t = qt + i * kStep;
-                const long long row = p.row0 + p.begin + t0 + t;
-                if (t >= rows || !dbg_ok(a.dbg, (size_t)row, (size_t)a.tok.rows(), DBG_STORE)) continue;
-                const float4 s = *(const float4 *)&sy[t][4 * q];
-                const float sum[4] = {s.x, s.y, s.z, s.w};
-                Vec<T, 4> out;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float y = fmaf(skip[e], cu[i][e], sum[e]);
-                    if (a.z) {
-                        const float g = cz[i][e];
-                        y *= g * sigmoid(g);
-                    }
-                    out.v[e] = from_f32<T>(y);
-                }
-                store_quad(a.y, a.y_stride, row, qc, left, out, vec);
-            }
-        }
+        for (int i = 0; i < kStages - 1; ++i) fetch(i);
+        vectors(0);
+        cp_async_wait_newest<kStages - 2>();
+        prepare(0);
+        vectors(1);
+        sync_all();
     }
-    if (ENDS) {
-        const size_t at = (size_t)k.slot * a.D;
-        if (in && dbg_ok(a.dbg, (at + ch) * NP + NP - 1, a.segment_floats, DBG_STORE))
-            *(float4 *)(a.ends + (at + ch) * NP + n0) = one(h);
-        // step sizes: the threads of a quad each have some tokens' sums
+    for (int tile = 0; tile < tiles; ++tile) {
+        if (tile + 1 < tiles) {
+            cp_async_wait_newest<1>();
+            prepare(tile + 1);
+            vectors(tile + 2);
+        }
+        if (!ENDS && tile > 0) finish(tile - 1);
+        fetch(tile + kStages - 1);
+        sync_all();
+    }
+    if (!ENDS && tiles > 0) finish(tiles - 1);
+    if (ENDS) {  // step sizes: the threads of a chunk's channels each have some tokens' sums
+        auto &sum = s.y[0];
+        if (qt < kTile) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (qt < kTile) sy[qt][4 * q + e] = total[e];
-        __syncthreads();
+            for (int e = 0; e < 4; ++e) {
+                sum[qt][8 * q + 2 * e] = total[e].x;
+                sum[qt][8 * q + 2 * e + 1] = total[e].y;
+            }
+        }
+        sync_half();
         if (tid < k.channels) {
-            float s = 0.f;
-            for (int t = 0; t < min(kTile, kStep); ++t) s += sy[t][tid];
-            a.sums[at + k.c0 + tid] = s;
+            float x = 0.f;
+            for (int t = 0; t < min(kTile, kStep); ++t) x += sum[t][tid];
+            a.sums[seg + k.c0 + tid] = x;
         }
-    } else if (a.final && in && p.begin + p.len == p.total) {
-        if (dbg_ok(a.dbg, (size_t)p.seq, (size_t)a.tok.num_seqs, DBG_STORE))
-            store_states(a.final, (size_t)p.seq * a.D + ch, n0, a.N, h);
     }
+    cp_async_wait_newest<0>();
 }
 
 template <typename T, int NP> cudaError_t launch(const ScanArgs &a, cudaStream_t stream) {
     const int per = a.D / a.G, nb = (per + Shape<NP>::CH - 1) / Shape<NP>::CH;
-    const bool vec = per % 4 == 0 && vec_ok(a, a.u, a.u_stride) && vec_ok(a, a.delta, a.delta_stride) &&
-                     vec_ok(a, a.z, a.z_stride) && vec_ok(a, a.y, a.y_stride);
+    Unit u(a);
+    u.add(a.u, a.u_stride);
+    u.add(a.delta, a.delta_stride);
+    u.add(a.z, a.z_stride);
+    u.add(a.y, a.y_stride);
     const unsigned grid = (unsigned)(a.tok.pieces(a.segment) * nb * a.G);
+    constexpr int kBytes = sizeof(Smem<T, NP>);
+    static_assert(kBytes <= 227 * 1024, "");
+    static volatile int done[2][kMaxDev];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = smem_limit_once(kda_scan_fwd_kernel<T, NP, true>, kBytes, dev, done[0]);
+    if (e == cudaSuccess) e = smem_limit_once(kda_scan_fwd_kernel<T, NP, false>, kBytes, dev, done[1]);
+    if (e != cudaSuccess) return e;
     if (a.ends) {
-        const cudaError_t e = launch_early(kda_scan_fwd_kernel<T, NP, true>, grid, kThreads, 0, stream, a, nb, vec);
+        e = launch_early(kda_scan_fwd_kernel<T, NP, true>, grid, 2 * kThreads, kBytes, stream, a, nb, u.unit);
         if (e != cudaSuccess) return e;
     }
-    return launch_early(kda_scan_fwd_kernel<T, NP, false>, grid, kThreads, 0, stream, a, nb, vec);
+    return launch_early(kda_scan_fwd_kernel<T, NP, false>, grid, 2 * kThreads, kBytes, stream, a, nb, u.unit);
 }
 
 template <typename T> cudaError_t pick(const ScanArgs &a, cudaStream_t stream) {
     switch (scan_padded(a.N)) {
-        case 4: return launch<T, 4>(a, stream);
         case 8: return launch<T, 8>(a, stream);
         case 16: return launch<T, 16>(a, stream);
         case 32: return launch<T, 32>(a, stream);
@@ -173,15 +287,15 @@ template <typename T> cudaError_t pick(const ScanArgs &a, cudaStream_t stream) {
 }  // namespace
 }  // namespace scan
 
-// Tokens of a segment: whole sequences where they fill the card (some four CTAs a multiprocessor),
-// otherwise so many segments that they do.
+// Tokens of a segment: whole sequences where there is a CTA for every multiprocessor, otherwise so many
+// segments that there are some four.
 int scan_segment(const Tokens &tok, int D, int N, int G, bool back) {
     const long long blocks = scan_blocks(D, N, G), want = 4 * kSMs;
     const long long rows = tok.rows(), longest = tok.cu_seqlens ? rows : tok.T;
     long long cuts = want / blocks;  // segments of all tokens together
     if (cuts < 1) cuts = 1;
     const long long whole = (longest + kScanTile - 1) / kScanTile * kScanTile;
-    if (!tok.cu_seqlens && tok.num_seqs * blocks * 2 > want) return (int)(whole ? whole : kScanTile);
+    if (!tok.cu_seqlens && tok.num_seqs * blocks >= kSMs) return (int)(whole ? whole : kScanTile);
     long long seg = (rows / cuts + kScanTile - 1) / kScanTile * kScanTile;
     if (seg < 8 * kScanTile) seg = 8 * kScanTile;
     return (int)(seg < whole ? seg : whole ? whole : kScanTile);

@@ -14,7 +14,7 @@ template <typename T, int NP, int R, bool WIDE>
 __global__ void __launch_bounds__(kThreads) kda_scan_step_kernel(const ScanArgs a) {
     wait_for_previous();
     using S = Shape<NP>;
-    const int c = blockIdx.x * S::CH + threadIdx.x / S::L, part = threadIdx.x % S::L, n0 = 4 * part;
+    const int c = blockIdx.x * S::HC + threadIdx.x / S::L, part = threadIdx.x % S::L, n0 = 4 * part;
     const int r0 = blockIdx.y * R;
     const bool in = c < a.D;
     const int ch = in ? c : 0, group = ch / (a.D / a.G);
@@ -80,18 +80,18 @@ __global__ void __launch_bounds__(kThreads) kda_scan_step_kernel(const ScanArgs 
 }
 
 template <typename T, int NP, int R> cudaError_t launch(const ScanArgs &a, cudaStream_t stream) {
-    const dim3 grid((unsigned)((a.D + Shape<NP>::CH - 1) / Shape<NP>::CH), (unsigned)((a.requests + R - 1) / R));
+    const dim3 grid((unsigned)((a.D + Shape<NP>::HC - 1) / Shape<NP>::HC), (unsigned)((a.requests + R - 1) / R));
     return a.N % 4 == 0 ? launch_early(kda_scan_step_kernel<T, NP, R, true>, grid, kThreads, 0, stream, a)
                         : launch_early(kda_scan_step_kernel<T, NP, R, false>, grid, kThreads, 0, stream, a);
 }
 template <typename T, int NP> cudaError_t launch(const ScanArgs &a, cudaStream_t stream) {
-    const long long ctas = (long long)a.requests * ((a.D + Shape<NP>::CH - 1) / Shape<NP>::CH);
+    const long long ctas = (long long)a.requests * ((a.D + Shape<NP>::HC - 1) / Shape<NP>::HC);
     return ctas >= 32 * kSMs ? launch<T, NP, 4>(a, stream) : launch<T, NP, 1>(a, stream);
 }
 
 template <typename T> cudaError_t pick(const ScanArgs &a, cudaStream_t stream) {
     switch (scan_padded(a.N)) {
-        case 4: return launch<T, 4>(a, stream);
+        
         case 8: return launch<T, 8>(a, stream);
         case 16: return launch<T, 16>(a, stream);
         case 32: return launch<T, 32>(a, stream);
