@@ -82,7 +82,10 @@ kda_status_t scan_shape(int B, int T, int D, int N, int G, int num_seqs, Tokens 
     return grid_ok(tok.pieces(kda::kScanTile) * kda::scan_blocks(D, N, G)) ? KDA_OK : KDA_ERR_SHAPE;
 }
 size_t scan_saved_floats(const Tokens &t, int D, int N) {
-    return (size_t)t.pieces(kda::kScanTile) * D * kda::scan_padded(N);
+    return 2 * (size_t)t.pieces(kda::kScanTile) * D * kda::scan_padded(N);
+}
+size_t scan_saved_bytes(const Tokens &t, int D, int N, int dtype) {  // and y before the gate
+    return up256(scan_saved_floats(t, D, N) * 4) + up256((size_t)t.rows() * D * kda::esize(dtype));
 }
 // Floats of the first pass over segments; 0 where every sequence is one segment.
 struct Segments {
@@ -262,10 +265,10 @@ kda_status_t kda_conv_step(const void *x, const void *weight, const void *bias, 
     return finish(kda::launch_conv_step(a, (cudaStream_t)stream));
 }
 
-size_t kda_scan_saved_bytes(int B, int T, int D, int N, int num_seqs) {
+size_t kda_scan_saved_bytes(int B, int T, int D, int N, int num_seqs, int dtype) {
     Tokens tok;
-    if (scan_shape(B, T, D, N, 1, num_seqs, tok) != KDA_OK) return 0;
-    return up256(scan_saved_floats(tok, D, N) * 4);
+    if (scan_shape(B, T, D, N, 1, num_seqs, tok) != KDA_OK || !any_type(dtype)) return 0;
+    return scan_saved_bytes(tok, D, N, dtype);
 }
 
 size_t kda_scan_fwd_workspace_bytes(int B, int T, int D, int N, int G, int num_seqs) {
@@ -299,7 +302,7 @@ kda_status_t kda_scan_fwd(const void *u, const void *delta, const float *A, cons
     const void *a4[] = {A, op.skip, op.delta_bias, op.cu_seqlens, op.initial_state, op.final_state};
     const void *a256[] = {op.saved, op.workspace};
     if (misaligned(ae, es) || misaligned(a4, 4) || misaligned(a256, 256)) return KDA_ERR_ALIGN;
-    const size_t saved = kda_scan_saved_bytes(B, T, D, N, op.num_seqs);
+    const size_t saved = scan_saved_bytes(tok, D, N, dtype);
     const size_t need = kda_scan_fwd_workspace_bytes(B, T, D, N, G, op.num_seqs);
     if ((op.saved && op.saved_bytes != saved) || (need && (!op.workspace || op.workspace_bytes < need)))
         return KDA_ERR_WORKSPACE;
@@ -329,6 +332,7 @@ kda_status_t kda_scan_fwd(const void *u, const void *delta, const float *A, cons
     a.initial = op.initial_state;
     a.final = op.final_state;
     a.saved = (float *)op.saved;
+    if (op.saved && op.z) a.open = (char *)op.saved + up256(scan_saved_floats(tok, D, N) * 4);
     a.D = D; a.N = N; a.G = G; a.dtype = dtype;
     a.softplus = !op.plain_delta;
     a.u_stride = op.u_stride; a.delta_stride = op.delta_stride; a.z_stride = op.z_stride;
@@ -391,7 +395,7 @@ kda_status_t kda_scan_bwd(const void *dy, const void *u, const void *delta, cons
     if (misaligned(ae, es) || misaligned(a4, 4) || misaligned(a256, 256)) return KDA_ERR_ALIGN;
     const Segments s(tok, D, N, G, true);
     size_t part[5];
-    const size_t saved = kda_scan_saved_bytes(B, T, D, N, op.num_seqs);
+    const size_t saved = scan_saved_bytes(tok, D, N, dtype);
     const size_t need = scan_bwd_work(tok, D, N, G, s, part);
     if (!op.saved || op.saved_bytes != saved || !op.workspace || op.workspace_bytes < need)
         return KDA_ERR_WORKSPACE;
@@ -420,6 +424,7 @@ kda_status_t kda_scan_bwd(const void *dy, const void *u, const void *delta, cons
     a.u = u; a.delta = delta; a.z = op.z; a.B = Bm; a.C = Cm;
     a.A = A; a.skip = op.skip; a.delta_bias = op.delta_bias;
     a.saved = (float *)op.saved;
+    if (op.saved && op.z) a.open = (char *)op.saved + up256(scan_saved_floats(tok, D, N) * 4);
     a.D = D; a.N = N; a.G = G; a.dtype = dtype;
     a.softplus = !op.plain_delta;
     a.u_stride = op.u_stride; a.delta_stride = op.delta_stride; a.z_stride = op.z_stride;

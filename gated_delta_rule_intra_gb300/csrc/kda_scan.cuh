@@ -40,6 +40,15 @@ template <int NP_> struct Shape {
     static constexpr int kVec = kTile * 4 + 4;  // of an [L][..] array of four states' tokens: parts in other banks
 };
 
+// The order of a thread's four states: number i is state n0 + (i ^ turn).  The order changes with the
+// channel so that in the sums over a warp's channels that leave each lane with one state's, every
+// lane keeps the same of its numbers and sends the same ones.
+template <int NP> __device__ __forceinline__ int turn_of(int tid) {
+    constexpr int CW = 32 / Shape<NP>::L;  // a warp's channels, side by side
+    const int cl = tid % 32 / Shape<NP>::L;
+    return CW == 2 ? 0 : CW == 4 ? (cl & 1) << 1 : cl / (CW / 8) & 3;
+}
+
 // Where four tokens (4 q ..) of channel c are in a [CH][kTile] array.  The groups of four change
 // places with c / 8, so that threads which write one token of channels eight apart meet different
 // banks.
@@ -164,6 +173,24 @@ __device__ __forceinline__ void store_chunk(void *base, long long stride, long l
             if (i < left) at[i] = x.v[i];
     }
 }
+template <typename T>
+__device__ __forceinline__ Vec<T, 8> load_chunk(const void *base, long long stride, long long row, int c,
+                                                int left, int unit) {
+    const T *at = (const T *)base + row * stride + c;
+    constexpr int E = sizeof(T);
+    Vec<T, 8> x;
+    x.clear();
+    if (unit == 16) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 16 / E)
+            if (i < left) *(uint4 *)(x.v + i) = *(const uint4 *)(at + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) x.v[i] = at[i];
+    }
+    return x;
+}
 template <typename T> __device__ __forceinline__ float2 pair(const Vec<T, 8> &x, int i) { return x.two(2 * i); }
 template <typename T> __device__ __forceinline__ void put_pair(Vec<T, 8> &x, int i, float2 v) {
     x.v[2 * i] = from_f32<T>(v.x);
@@ -200,19 +227,45 @@ struct Four {
 };
 __device__ __forceinline__ Four four(float4 x) { return {make_float2(x.x, x.y), make_float2(x.z, x.w)}; }
 __device__ __forceinline__ float4 one(Four x) { return make_float4(x.lo.x, x.lo.y, x.hi.x, x.hi.y); }
-__device__ __forceinline__ Four load_states(const float *base, size_t channel, int n, int N, bool ok) {
+// (`turn`: number i is state n + (i ^ turn))
+__device__ __forceinline__ Four load_states(const float *base, size_t channel, int n, int N, bool ok, int turn = 0) {
     float v[4] = {};
     if (ok) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (n + i < N) v[i] = base[channel * N + n + i];
+            if (n + (i ^ turn) < N) v[i] = base[channel * N + n + (i ^ turn)];
     }
     return {make_float2(v[0], v[1]), make_float2(v[2], v[3])};
 }
-__device__ __forceinline__ void store_states(float *base, size_t channel, int n, int N, Four x) {
+__device__ __forceinline__ void store_states(float *base, size_t channel, int n, int N, Four x, int turn = 0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (n + i < N) base[channel * N + n + i] = x.get(i);
+        if (n + (i ^ turn) < N) base[channel * N + n + (i ^ turn)] = x.get(i);
+}
+using kda::fma2;
+using kda::mul2;
+
+// A number twice, as one operand of paired operations that stays where it is (the compiler would
+// copy it together anew for each: an instruction of eight).
+__device__ __forceinline__ uint64_t twice(float x) {
+    uint64_t r;
+    asm volatile("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, uint64_t b) {
+    float2 r;
+    asm("{\n.reg .b64 x;\nmov.b64 x, {%2, %3};\nmul.rn.f32x2 x, x, %4;\nmov.b64 {%0, %1}, x;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, uint64_t b, float2 c) {
+    float2 r;
+    asm("{\n.reg .b64 x, z;\nmov.b64 x, {%2, %3};\nmov.b64 z, {%5, %6};\nfma.rn.f32x2 x, x, %4, z;\n"
+        "mov.b64 {%0, %1}, x;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "l"(b), "f"(c.x), "f"(c.y));
+    return r;
 }
 __device__ __forceinline__ Four scaled(Four a, float x) { return {mul2(a.lo, both(x)), mul2(a.hi, both(x))}; }
 // 2^(d a)

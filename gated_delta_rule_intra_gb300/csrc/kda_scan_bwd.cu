@@ -5,9 +5,10 @@
 //   du_t = D_t sum_n g_t B_t + skip dy'_t,   dD_t = u_t sum_n g_t B_t + sum_n g_t p_t A,
 //   ddelta_t = dD_t softplus'(delta_t + delta_bias),   dskip = sum_t dy'_t u_t,
 //   dz_t = dy_t (sum_n C_t h_t + skip u_t) silu'(z_t).
-// The states come again from the ones that the forward left in front of every 16 tokens: half a
-// tile at a time, so that eight tokens' p stay in registers (h is p + D u B, without a difference
-// that would lose small p).  Sums over a channel's states as in the forward; dB and dC are summed
+// The states come again from the ones that the forward left in front of every eight tokens, whose p
+// stay in registers (h is p + D u B, without a difference that would lose small p); so does what the
+// gate multiplies.  (Checkpoints at every 16 tokens would halve their memory; the first eight would
+// then be walked twice, 8% of the instructions.)  Sums over a channel's states as in the forward; dB and dC are summed
 // over a thread's two channels, over a warp's by lanes that each end with one of the 8 values of
 // four states, over the CTA's warps in shared memory and over the CTAs by a second kernel,
 // always in the same order.
@@ -17,7 +18,7 @@ namespace kda {
 namespace scan {
 namespace {
 
-constexpr int kHalf = 8, kWarps = kThreads / 32;
+constexpr int kHalf = 8, kWarps = kThreads / 32, kStages = 3;
 
 // Registers: as many as a launch of two CTAs a multiprocessor has, moved to the half that walks.
 constexpr int kLaunchRegs = 128, kWalkRegs = 168, kOtherRegs = 88;
@@ -25,13 +26,13 @@ static_assert(kWalkRegs + kOtherRegs == 2 * kLaunchRegs, "");
 
 template <typename T, int NP, bool ENDS> struct Smem {
     using S = Shape<NP>;
-    static constexpr int kStages = sizeof(T) * S::kPer > 4 ? 3 : 4;
     static constexpr int kSum = kTile * S::kRow + 16;
     float d[2][S::CH * kTile], x[2][S::CH * kTile], g[2][S::CH * kTile];  // D, D u, dy': place()
     float B[2][S::L][S::kVec], C[2][S::L][S::kVec];
-    float sum[ENDS ? 1 : 2][3][kSum];  // over a channel's states: g B, g p A, C h, [kTile][kRow] each
+    float sum[ENDS ? 1 : 2][2][kSum];  // over a channel's states: g B, g p A, [kTile][kRow] each
     float bc[ENDS ? 1 : 2][kWarps][kTile][2 * NP];
-    float4 h[ENDS ? 1 : 2][2][kThreads];           // the states in front of a tile: each thread's own
+    float4 h[ENDS ? 1 : 2][2][2][kThreads];        // the states in front of half a tile: each thread's own
+    float param[2][S::CH];                         // delta_bias, skip
     Vec<T, 8> raw[kStages][4][S::kPer][kThreads];  // u, delta, dy, z: a slot of each thread
 };
 
@@ -43,7 +44,6 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
     using M = Smem<T, NP, ENDS>;
     extern __shared__ __align__(16) char smem[];
     M &s = *reinterpret_cast<M *>(smem);
-    constexpr int kStages = M::kStages;
     const Block<NP> k(a, nb);
     const Piece &p = k.p;
     if (ENDS && (p.len < 0 || p.begin == 0)) return;
@@ -55,17 +55,18 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
     if (threadIdx.x < kThreads) {  // the walk
         if (!ENDS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWalkRegs));
         const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, part = tid % S::L, n0 = 4 * part;
-        const int c[2] = {tid / S::L, tid / S::L + S::HC};
-        float A2[2][4], carry[2][4];
+        const int c[2] = {tid / S::L, tid / S::L + S::HC}, turn = turn_of<NP>(tid);
+        uint64_t A2[2][4];
+        float carry[2][4];
         float2 dA[2][4] = {};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const bool in = c[j] < k.channels;
             const size_t ch = (size_t)k.c0 + c[j];
-            const Four Aj = scaled(load_states(a.A, ch, n0, a.N, in), kLog2e);
+            const Four Aj = scaled(load_states(a.A, ch, n0, a.N, in, turn), kLog2e);
             Four g = {both(0.f), both(0.f)};
             if (!ENDS && p.len >= 0 && in) {  // from the segments behind this one
-                g = load_states(a.d_final, (size_t)p.seq * a.D + ch, n0, a.N, a.d_final);
+                g = load_states(a.d_final, (size_t)p.seq * a.D + ch, n0, a.N, a.d_final, turn);
                 const int behind = (p.total + a.segment - 1) / a.segment - 1 - p.index;
                 for (int i = k.slot + behind; i > k.slot; --i) {
                     const size_t at = (size_t)i * a.D + ch;
@@ -75,21 +76,24 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
             }
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                A2[j][n] = Aj.get(n);
+                A2[j][n] = twice(Aj.get(n));
                 carry[j][n] = g.get(n);
             }
         }
         const long long tile0 = k.tiles0(a) + p.begin / kTile;
         auto states = [&](int i) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const size_t at = ((size_t)(tile0 + tiles - 1 - i) * a.D + k.c0 + c[j]) * NP + n0;
-                const bool in = i < tiles && c[j] < k.channels && dbg_ok(a.dbg, at + 3, a.saved_floats, DBG_LOAD);
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                 (uint32_t)__cvta_generic_to_shared(&s.h[ENDS ? 0 : i & 1][j][tid])),
-                             "l"(a.saved + (in ? at : 0)), "r"(in ? 16 : 0)
-                             : "memory");
-            }
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const size_t at = ((size_t)(2 * (tile0 + tiles - 1 - i) + half) * a.D + k.c0 + c[j]) * NP + n0;
+                    const bool in = half * kHalf < rows_of(i) && c[j] < k.channels &&
+                                    dbg_ok(a.dbg, at + 3, a.saved_floats, DBG_LOAD);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                     (uint32_t)__cvta_generic_to_shared(&s.h[ENDS ? 0 : i & 1][half][j][tid])),
+                                 "l"(a.saved + (in ? at : 0)), "r"(in ? 16 : 0)
+                                 : "memory");
+                }
             cp_async_commit();
         };
         Phase phase(smem);
@@ -105,10 +109,12 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
             auto off = [&](const void *at) { return (uint32_t)((const char *)at - smem); };
             const uint32_t od[2] = {off(s.d[b] + place(c[0], 0)), off(s.d[b] + place(c[1], 0))};
             const uint32_t ox = off(s.x[b]) - off(s.d[b]), og = off(s.g[b]) - off(s.d[b]);
-            const uint32_t oB = off(s.B[b][part]), oC = off(s.C[b][part]);
+            uint32_t oB[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) oB[n] = off(&s.B[b][part][(n ^ turn) * kTile]);
+            constexpr uint32_t toC = offsetof(M, C) - offsetof(M, B);
             // token t of a channel is at its place: groups of four change places (a XOR)
-            const uint32_t turn[2] = {(uint32_t)(c[0] >> 3 & 3) << 4, (uint32_t)(c[1] >> 3 & 3) << 4};
-            auto at4 = [&](int j, int g) { return (od[j] & ~48u) + (((uint32_t)g << 4) ^ turn[j]); };
+            auto at4 = [&](int j, int g) { return od[j] ^ (uint32_t)g << 4; };
             if (ENDS) {
 #pragma unroll
                 for (int g = kTile / 4 - 1; g >= 0; --g)
@@ -120,10 +126,10 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
 #pragma unroll
                         for (int n = 0; n < 4; ++n) {
                             float2 C[2];
-                            phase.load4(oC + (n * kTile + 4 * g) * 4, C);
+                            phase.load4(oB[n] + toC + 16 * g, C);
 #pragma unroll
                             for (int t = 1; t >= 0; --t) {
-                                const float2 e = mul2(d[t], both(A2[j][n])), in = mul2(gg[t], C[t]);
+                                const float2 e = mul2(d[t], A2[j][n]), in = mul2(gg[t], C[t]);
                                 carry[j][n] = (carry[j][n] + in.y) * ex2(e.y);
                                 carry[j][n] = (carry[j][n] + in.x) * ex2(e.x);
                             }
@@ -136,29 +142,8 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
                     float2 P[2][4][4];  // p of a channel's state, of the half's pairs of tokens
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float4 v = s.h[b][j][tid];
+                        const float4 v = s.h[ENDS ? 0 : b][half][j][tid];
                         h[j][0] = v.x; h[j][1] = v.y; h[j][2] = v.z; h[j][3] = v.w;
-                    }
-                    if (half == 1) {
-#pragma unroll
-                        for (int g = 0; g < 2; ++g)
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                float2 d[2], x[2];
-                                phase.load4(at4(j, g), d);
-                                phase.load4(at4(j, g) + ox, x);
-#pragma unroll
-                                for (int n = 0; n < 4; ++n) {
-                                    float2 B[2];
-                                    phase.load4(oB + (n * kTile + 4 * g) * 4, B);
-#pragma unroll
-                                    for (int t = 0; t < 2; ++t) {
-                                        const float2 e = mul2(d[t], both(A2[j][n])), in = mul2(x[t], B[t]);
-                                        h[j][n] = fmaf(ex2(e.x), h[j][n], in.x);
-                                        h[j][n] = fmaf(ex2(e.y), h[j][n], in.y);
-                                    }
-                                }
-                            }
                     }
 #pragma unroll
                     for (int gl = 0; gl < 2; ++gl) {
@@ -171,10 +156,10 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
 #pragma unroll
                             for (int n = 0; n < 4; ++n) {
                                 float2 B[2];
-                                phase.load4(oB + (n * kTile + 4 * g) * 4, B);
+                                phase.load4(oB[n] + 16 * g, B);
 #pragma unroll
                                 for (int t = 0; t < 2; ++t) {
-                                    const float2 e = mul2(d[t], both(A2[j][n]));
+                                    const float2 e = mul2(d[t], A2[j][n]);
                                     float2 &pp = P[j][n][2 * gl + t];
                                     pp.x = ex2(e.x) * h[j][n];
                                     pp.y = ex2(e.y) * fmaf(x[t].x, B[t].x, pp.x);
@@ -191,35 +176,31 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
                         float2 B[4], C[4], dB[4], dC[4];
 #pragma unroll
                         for (int n = 0; n < 4; ++n) {
-                            B[n] = phase.load2(oB + (n * kTile + t0) * 4);
-                            C[n] = phase.load2(oC + (n * kTile + t0) * 4);
+                            B[n] = phase.load2(oB[n] + 4 * t0);
+                            C[n] = phase.load2(oB[n] + toC + 4 * t0);
                         }
-                        float ys[4];
                         using W = Share<S::L>;
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             const uint32_t at = at4(j, g) + to;
                             const float2 d = phase.load2(at), x = phase.load2(at + ox), gg = phase.load2(at + og);
-                            float2 s1, s2, s3;
+                            float2 s1, s2;
 #pragma unroll
                             for (int n = 0; n < 4; ++n) {
                                 const float2 pp = P[j][n][pi];
-                                const float2 e = mul2(d, both(A2[j][n])), hh = fma2(x, B[n], pp);
+                                const float2 e = mul2(d, A2[j][n]), hh = fma2(x, B[n], pp);
                                 float2 G;
                                 G.y = fmaf(gg.y, C[n].y, carry[j][n]);
                                 G.x = fmaf(gg.x, C[n].x, G.y * ex2(e.y));
                                 carry[j][n] = G.x * ex2(e.x);
                                 const float2 gp = mul2(G, pp);
                                 s1 = n ? fma2(G, B[n], s1) : mul2(G, B[n]);
-                                s2 = n ? fma2(gp, both(A2[j][n]), s2) : mul2(gp, both(A2[j][n]));
-                                s3 = n ? fma2(hh, C[n], s3) : mul2(hh, C[n]);
+                                s2 = n ? fma2(gp, A2[j][n], s2) : mul2(gp, A2[j][n]);
                                 dA[j][n] = fma2(gp, d, dA[j][n]);
                                 dB[n] = j ? fma2(G, x, dB[n]) : mul2(G, x);
                                 dC[n] = j ? fma2(hh, gg, dC[n]) : mul2(hh, gg);
                             }
                             float v[4] = {s1.x, s1.y, s2.x, s2.y};
-                            ys[2 * j] = s3.x;
-                            ys[2 * j + 1] = s3.y;
                             scatter_sum<S::L, 1>(v, tid);
                             if (W::mine(part)) {
 #pragma unroll
@@ -229,33 +210,29 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
                                 }
                             }
                         }
-                        if (a.z) {
-                            scatter_sum<S::L, 1>(ys, tid);
-                            if (W::mine(part)) {
-#pragma unroll
-                                for (int y = 0; y < W::kCount; ++y) {
-                                    const int idx = W::first(part) + y;
-                                    s.sum[ENDS ? 0 : b][2][(t0 + (idx & 1)) * S::kRow + (idx >> 1 ? c[1] : c[0])] = ys[y];
-                                }
-                            }
-                        }
-                        constexpr int CW = 32 / S::L, kLeft = CW < 8 ? 8 / CW : 1, kSame = CW > 8 ? CW / 8 : 1;
+                        constexpr int CW = 32 / S::L, kSame = CW > 8 ? CW / 8 : 1;
                         const int cl = lane / S::L;  // place among the warp's channels
 #pragma unroll
                         for (int t = 1; t >= 0; --t) {
-                            float v[8];
+                            // half of the lanes go on with dB, half with dC; then a lane keeps the first
+                            // of its numbers, which are other states in each
+                            const bool up = cl & CW / 2;
+                            float v[4];
 #pragma unroll
                             for (int n = 0; n < 4; ++n) {
-                                v[n] = t ? dB[n].y : dB[n].x;
-                                v[4 + n] = t ? dC[n].y : dC[n].x;
+                                const float x = t ? dB[n].y : dB[n].x, y = t ? dC[n].y : dC[n].x;
+                                v[n] = (up ? y : x) + __shfl_xor_sync(0xffffffffu, up ? x : y, 16);
                             }
-                            scatter_sum<CW, S::L>(v, lane);
+                            if (CW >= 4) {
+#pragma unroll
+                                for (int n = 0; n < 2; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n + 2], 8);
+                            }
+                            if (CW >= 8) v[0] += __shfl_xor_sync(0xffffffffu, v[1], 4);
+                            if (CW >= 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
                             if (cl % kSame == 0) {
 #pragma unroll
-                                for (int y = 0; y < kLeft; ++y) {
-                                    const int idx = cl / kSame * kLeft + y;  // 0..3: dB, 4..7: dC of this part's states
-                                    s.bc[ENDS ? 0 : b][warp][t0 + t][(idx < 4 ? 0 : NP) + n0 + (idx & 3)] = v[y];
-                                }
+                                for (int n = 0; n < (CW >= 8 ? 1 : CW == 4 ? 2 : 4); ++n)
+                                    s.bc[ENDS ? 0 : b][warp][t0 + t][(up ? NP : 0) + n0 + (n ^ turn)] = v[n];
                             }
                         }
                     }
@@ -264,21 +241,21 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
             sync_all();
         }
         cp_async_wait_newest<0>();
-        float *per_state = ENDS ? a.ends : a.part_A;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const size_t ch = (size_t)k.c0 + c[j];
+            const size_t ch = (size_t)k.c0 + c[j], at = (seg + ch) * NP + n0;
             if (c[j] >= k.channels) continue;
+            const Four g = four(make_float4(carry[j][0], carry[j][1], carry[j][2], carry[j][3]));
             if (!ENDS && p.len >= 0 && p.begin == 0 && a.d_initial &&
                 dbg_ok(a.dbg, (size_t)p.seq, (size_t)a.tok.num_seqs, DBG_STORE))
-                store_states(a.d_initial, (size_t)p.seq * a.D + ch, n0, a.N,
-                             four(make_float4(carry[j][0], carry[j][1], carry[j][2], carry[j][3])));
-            // this segment's share of dA (or its end)
-            if (!dbg_ok(a.dbg, (seg + ch) * NP + NP - 1, a.segment_floats, DBG_STORE)) continue;
-            float v[4];
+                store_states(a.d_initial, (size_t)p.seq * a.D + ch, n0, a.N, g, turn);
+            if (!dbg_ok(a.dbg, at + 3, a.segment_floats, DBG_STORE)) continue;
+            if (ENDS) {
+                *(float4 *)(a.ends + at) = one(g);
+            } else {
 #pragma unroll
-            for (int n = 0; n < 4; ++n) v[n] = ENDS ? carry[j][n] : dA[j][n].x + dA[j][n].y;
-            *(float4 *)(per_state + (seg + ch) * NP + n0) = make_float4(v[0], v[1], v[2], v[3]);
+                for (int n = 0; n < 4; ++n) a.part_A[at + (n ^ turn)] = dA[j][n].x + dA[j][n].y;
+            }
         }
         return;
     }
@@ -287,10 +264,12 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
     const int tid = threadIdx.x - kThreads;
     const int q = tid % S::kChunks, qt = tid / S::kChunks, qc = k.c0 + 8 * q, left = k.channels - 8 * q;
     constexpr int kStep = kThreads / S::kChunks;
-    // (the parameters are read anew for every tile, out of the cache: they would be 16 registers)
-    auto param = [&](const float *v, int e) {
-        return make_float2(v && 2 * e < left ? v[qc + 2 * e] : 0.f, v && 2 * e + 1 < left ? v[qc + 2 * e + 1] : 0.f);
-    };
+    for (int i = tid; i < S::CH; i += kThreads) {
+        s.param[0][i] = a.delta_bias && i < k.channels ? a.delta_bias[k.c0 + i] : 0.f;
+        s.param[1][i] = a.skip && i < k.channels ? a.skip[k.c0 + i] : 0.f;
+    }
+    sync_half();
+    auto bias = [&](int e) { return *(const float2 *)&s.param[0][8 * q + 2 * e]; };
     float2 dskip[4] = {}, dbias[4] = {};  // (ENDS: dskip is the sum of the step sizes)
     auto row_of = [&](int i) { return first + (tiles - 1 - i) * kTile; };
     auto fine = [&](int i) {
@@ -331,7 +310,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
             if (a.z) z = raw[3][x][tid];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float2 d = add2(pair(dl, e), param(a.delta_bias, e)), g = pair(dy, e);
+                float2 d = add2(pair(dl, e), bias(e)), g = pair(dy, e);
                 if (a.softplus) d = softplus(d);
                 if (t >= rows) d = both(0.f);
                 if (a.z) {
@@ -355,6 +334,16 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
         if (!ENDS) vb.put(tid, s.B[b]);
         vc.put(tid, s.C[b]);
     };
+    // What the gate multiplies, on its way a tile ahead of its use.
+    Vec<T, 8> open[S::kPer];
+    auto ungated = [&](int i) {
+        const int rows = fine(i) ? rows_of(i) : 0;
+#pragma unroll
+        for (int x = 0; x < S::kPer; ++x) {
+            const int t = qt + x * kStep;
+            if (!ENDS && a.z && t < kTile && t < rows) open[x] = load_chunk<T>(a.open, a.D, row_of(i) + t, qc, left, unit);
+        }
+    };
     // What a tile's sums make: the gradients of its tokens (its d, x and g are this thread's own).
     auto finish = [&](int i) {
         const int rows = fine(i) ? rows_of(i) : 0, b = i & 1;
@@ -371,19 +360,18 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
             for (int e = 0; e < 4; ++e) {
                 const int cc = 8 * q + 2 * e, at = place(cc, t >> 2) + (t & 3), sat = t * S::kRow + cc;
                 const float2 gb = *(const float2 *)&s.sum[b][0][sat], gpa = *(const float2 *)&s.sum[b][1][sat];
-                const float2 d = make_float2(s.d[b][at], s.d[b][at + kTile]), skip = param(a.skip, e);
+                const float2 d = make_float2(s.d[b][at], s.d[b][at + kTile]), skip = *(const float2 *)&s.param[1][cc];
                 const float2 g = make_float2(s.g[b][at], s.g[b][at + kTile]), uu = pair(u, e);
                 put_pair(du, e, fma2(d, gb, mul2(skip, g)));
                 float2 v = fma2(uu, gb, mul2(gpa, both(kLn2)));
-                if (a.softplus) v = mul2(v, sigmoid2(add2(pair(dl, e), param(a.delta_bias, e))));
+                if (a.softplus) v = mul2(v, sigmoid2(add2(pair(dl, e), bias(e))));
                 put_pair(dd, e, v);
                 dbias[e] = add2(dbias[e], v);
                 dskip[e] = fma2(g, uu, dskip[e]);
                 if (a.z) {
-                    const float2 y = fma2(skip, uu, *(const float2 *)&s.sum[b][2][sat]);
                     const float2 zz = pair(z, e), sg = sigmoid2(zz);
                     const float2 slope = mul2(sg, fma2(zz, fma2(sg, both(-1.f), both(1.f)), both(1.f)));
-                    put_pair(dz, e, mul2(mul2(pair(dy, e), y), slope));
+                    put_pair(dz, e, mul2(mul2(pair(dy, e), pair(open[x], e)), slope));
                 }
             }
             store_chunk(a.du, a.du_stride, row, qc, left, du, unit);
@@ -410,6 +398,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
     }
     for (int i = 0; i < tiles; ++i) {
         if (!ENDS && i > 0) finish(i - 1);
+        ungated(i);
         if (i + 1 < tiles) {
             cp_async_wait_newest<kStages - 3>();
             prepare(i + 1);
@@ -510,6 +499,7 @@ template <typename T, int NP> cudaError_t launch(const ScanArgs &a, cudaStream_t
     u.add(a.du, a.du_stride);
     u.add(a.ddelta, a.ddelta_stride);
     u.add(a.dz, a.dz_stride);
+    u.add(a.open, a.D);
     cudaError_t e = a.ends ? walk<T, NP, true>(a, nb, u.unit, stream) : cudaSuccess;
     if (e == cudaSuccess) e = walk<T, NP, false>(a, nb, u.unit, stream);
     if (e != cudaSuccess) return e;

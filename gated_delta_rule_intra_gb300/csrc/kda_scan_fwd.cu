@@ -25,7 +25,8 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
     wait_for_previous();
     using S = Shape<NP>;
     extern __shared__ __align__(16) char smem[];
-    Smem<T, NP> &s = *reinterpret_cast<Smem<T, NP> *>(smem);
+    using M = Smem<T, NP>;
+    M &s = *reinterpret_cast<M *>(smem);
     const Block<NP> k(a, nb);
     const Piece &p = k.p;
     if (p.len < 0 || (ENDS && p.begin + p.len == p.total)) return;
@@ -33,17 +34,18 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
     const long long first = p.row0 + p.begin;
     const size_t seg = (size_t)k.slot * a.D;
     if (threadIdx.x < kThreads) {  // the scan
-        const int tid = threadIdx.x, part = tid % S::L, n0 = 4 * part;
+        const int tid = threadIdx.x, part = tid % S::L, n0 = 4 * part, turn = turn_of<NP>(tid);
         const int c[2] = {tid / S::L, tid / S::L + S::HC};
-        float A2[2][4], h[2][4];
+        uint64_t A2[2][4];
+        float h[2][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const bool in = c[j] < k.channels;
             const size_t ch = (size_t)k.c0 + c[j];
-            const Four Aj = scaled(load_states(a.A, ch, n0, a.N, in), kLog2e);
+            const Four Aj = scaled(load_states(a.A, ch, n0, a.N, in, turn), kLog2e);
             Four hj = {both(0.f), both(0.f)};
             if (!ENDS && in) {
-                hj = load_states(a.initial, (size_t)p.seq * a.D + ch, n0, a.N, a.initial);
+                hj = load_states(a.initial, (size_t)p.seq * a.D + ch, n0, a.N, a.initial, turn);
                 for (int g = k.slot - p.index; g < k.slot; ++g) {
                     const size_t at = (size_t)g * a.D + ch;
                     if (!dbg_ok(a.dbg, at * NP + NP - 1, a.segment_floats, DBG_LOAD)) break;
@@ -52,7 +54,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
             }
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                A2[j][n] = Aj.get(n);
+                A2[j][n] = twice(Aj.get(n));
                 h[j][n] = hj.get(n);
             }
         }
@@ -62,23 +64,27 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
         for (int tile = 0; tile < tiles; ++tile) {
             const int b = tile & 1;
             phase.next();
-            if (!ENDS && a.saved) {
+            auto save = [&](int half) {  // the states in front of half a tile
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const size_t at = ((size_t)(tile0 + tile) * a.D + k.c0 + c[j]) * NP + n0;
+                    const size_t at = ((size_t)(2 * (tile0 + tile) + half) * a.D + k.c0 + c[j]) * NP + n0;
                     if (c[j] < k.channels && dbg_ok(a.dbg, at + 3, a.saved_floats, DBG_STORE))
                         *(float4 *)(a.saved + at) = make_float4(h[j][0], h[j][1], h[j][2], h[j][3]);
                 }
-            }
+            };
             const uint32_t od = (uint32_t)((char *)s.d[b] - smem), ox = (uint32_t)((char *)s.x[b] - smem);
-            const uint32_t oB = (uint32_t)((char *)s.B[b][part] - smem), oC = (uint32_t)((char *)s.C[b][part] - smem);
+            uint32_t oB[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) oB[n] = (uint32_t)((char *)&s.B[b][part][(n ^ turn) * kTile] - smem);
+            constexpr uint32_t toC = offsetof(M, C) - offsetof(M, B);
 #pragma unroll
             for (int g = 0; g < kTile / 4; ++g) {
+                if (!ENDS && a.saved && g % 2 == 0) save(g / 2);
                 float2 B[4][2], C[4][2];
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
-                    phase.load4(oB + (n * kTile + 4 * g) * 4, B[n]);
-                    if (!ENDS) phase.load4(oC + (n * kTile + 4 * g) * 4, C[n]);
+                    phase.load4(oB[n] + 16 * g, B[n]);
+                    if (!ENDS) phase.load4(oB[n] + toC + 16 * g, C[n]);
                 }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -91,7 +97,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
                         float2 sum;
 #pragma unroll
                         for (int n = 0; n < 4; ++n) {
-                            const float2 e = mul2(d[t], both(A2[j][n])), in = mul2(x[t], B[n][t]);
+                            const float2 e = mul2(d[t], A2[j][n]), in = mul2(x[t], B[n][t]);
                             float2 hh;
                             hh.x = fmaf(ex2(e.x), h[j][n], in.x);
                             hh.y = fmaf(ex2(e.y), hh.x, in.y);
@@ -122,7 +128,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
             if (!ENDS && a.final && p.begin + p.len == p.total &&
                 dbg_ok(a.dbg, (size_t)p.seq, (size_t)a.tok.num_seqs, DBG_STORE))
                 store_states(a.final, (size_t)p.seq * a.D + ch, n0, a.N,
-                             four(make_float4(h[j][0], h[j][1], h[j][2], h[j][3])));
+                             four(make_float4(h[j][0], h[j][1], h[j][2], h[j][3])), turn);
         }
         return;
     }
@@ -199,17 +205,20 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
             const float2 sum[4] = {make_float2(lo.x, lo.y), make_float2(lo.z, lo.w), make_float2(hi.x, hi.y),
                                    make_float2(hi.z, hi.w)};
             const Vec<T, 8> u = raw[0][i][tid];
-            Vec<T, 8> z, out;
+            Vec<T, 8> z, out, open;
             if (a.z) z = raw[2][i][tid];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float2 y = fma2(skip[e], pair(u, e), sum[e]);
                 if (a.z) {
                     const float2 g = pair(z, e);
+                    put_pair(open, e, y);
                     y = mul2(y, mul2(g, sigmoid2(g)));
                 }
                 put_pair(out, e, y);
             }
+            // what the gate multiplies, for the gate's gradient, rounded as that will be
+            if (a.open) store_chunk(a.open, a.D, row, qc, left, open, unit);
             store_chunk(a.y, a.y_stride, row, qc, left, out, unit);
         }
     };
@@ -259,6 +268,7 @@ template <typename T, int NP> cudaError_t launch(const ScanArgs &a, cudaStream_t
     u.add(a.delta, a.delta_stride);
     u.add(a.z, a.z_stride);
     u.add(a.y, a.y_stride);
+    u.add(a.open, a.D);
     const unsigned grid = (unsigned)(a.tok.pieces(a.segment) * nb * a.G);
     constexpr int kBytes = sizeof(Smem<T, NP>);
     static_assert(kBytes <= 227 * 1024, "");
