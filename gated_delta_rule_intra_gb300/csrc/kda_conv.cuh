@@ -63,12 +63,11 @@ __device__ __forceinline__ void load_params(const ConvArgs &a, int c0, float (*w
     }
 }
 
-// 16-byte (or 8-byte) accesses need rows on such boundaries.
-inline bool vec_ok(const ConvArgs &a, int v, bool back) {
+// Accesses of v elements need rows on such boundaries.
+inline bool vec_ok(const ConvArgs &a, int v) {
     const size_t b = (size_t)v * esize(a.dtype);
     auto ok = [&](const void *p, long long stride) { return aligned(p, b) && stride % v == 0; };
-    return a.D % v == 0 && ok(a.x, a.x_stride) && ok(a.initial, v) && ok(a.final, v) &&
-           (back ? ok(a.dy, a.dy_stride) && ok(a.dx, a.dx_stride) && ok(a.d_final, v) : ok(a.y, a.y_stride));
+    return a.D % v == 0 && ok(a.x, a.x_stride) && ok(a.initial, v) && ok(a.final, v) && ok(a.y, a.y_stride);
 }
 
 }  // namespace conv

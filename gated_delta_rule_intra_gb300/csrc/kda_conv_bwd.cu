@@ -3,145 +3,176 @@
 //   dweight[j] = sum over tokens of g[t] x[t - W + 1 + j],  dbias = sum over tokens of g.
 // The final state's gradient is that of the sequence's last inputs and is added to theirs.
 //
-// Bound by memory (x and dy read, dx written once).  A warp walks a run of 16 tokens of 32 V
-// channels with the last W inputs and the last W values of g in registers, and W - 1 tokens more
-// whose g its last inputs need; the next four tokens' rows are on their way.  A resident CTA takes
-// pieces of 128 tokens of its channels in turn and keeps the parameters' sums in registers; the
-// CTAs' sums are added up in a fixed order by a second kernel.
+// Bound by memory (x and dy read, dx written once) if instructions leave it room: a resident CTA takes
+// pieces of 128 tokens of one block of channels in turn, and the next piece's rows are on their
+// way into shared memory meanwhile, whatever their alignment.  A thread walks a run of tokens of four
+// channels with the last W inputs and the last W values of g in registers (the places of both go
+// round, so that nothing is moved), and W - 1 tokens more whose g its last inputs need.  The CTAs'
+// sums of the parameters' gradients are added up in a fixed order by a second kernel.
 #include "kda_conv.cuh"
 
 namespace kda {
 namespace conv {
 namespace {
 
-constexpr int kRun = 16, kWarps = 8, kPiece = kRun * kWarps, kAhead = 4;
-static_assert(kPiece == kConvPiece, "");
+constexpr int kThreads = 128, V = 4, kPiece = kConvPiece;
 
-template <typename T, int V, int W>
-__global__ void __launch_bounds__(32 * kWarps, 2) kda_conv_bwd_kernel(const ConvArgs a, long long pieces) {
+template <typename T, int W> struct Smem {
+    static constexpr int LANES = 64 / (V * sizeof(T)) * 2;  // of a row: 128 bytes
+    static constexpr int CH = LANES * V, kRuns = kThreads / LANES, kRun = kPiece / kRuns;
+    static constexpr int kX = kPiece + 2 * (W - 1), kDy = kPiece + W - 1;
+    T x[2][kX][CH], dy[2][kDy][CH];
+    float w[W + 1][CH], red[kRuns][CH];
+};
+
+template <typename T, int W>
+__global__ void __launch_bounds__(kThreads, 3)
+    kda_conv_bwd_kernel(const ConvArgs a, long long pieces, int unit_x, int unit_dy, int unit_dx) {
     wait_for_previous();
-    __shared__ __align__(16) float w[W + 1][32 * V];
-    __shared__ float red[kWarps][32 * V];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c0 = blockIdx.x * 32 * V, c = c0 + lane * V;
-    const bool in = c < a.D;
-    load_params<V, W>(a, c0, w, 32 * kWarps);
-    __syncthreads();
-    float wv[W][V], bias[V], dw[W][V] = {}, db[V] = {};
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) wv[j][i] = w[j][lane * V + i];
-        bias[i] = w[W][lane * V + i];
-    }
-    for (long long at = blockIdx.y; at < pieces; at += gridDim.y) {
-        const Piece p = find_piece(a.tok, at, kPiece);
-        if (p.len <= 0) continue;
-        const int t0 = p.begin + warp * kRun, n = min(kRun, p.begin + p.len - t0);
-        if (!in || n <= 0) continue;
-        const int steps = n + W - 1;
-        auto grad = [&](int pos) {  // dy at a position
-            Vec<T, V> x;
-            x.clear();
-            const long long row = p.row0 + pos;
-            if (pos < p.total && dbg_ok(a.dbg, (size_t)row, (size_t)a.tok.rows(), DBG_LOAD))
-                x = *reinterpret_cast<const Vec<T, V> *>((const T *)a.dy + row * a.dy_stride + c);
-            return x;
-        };
-        Vec<T, V> nx[kAhead], ny[kAhead];
-        float xw[W][V] = {}, gw[W][V] = {};
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j) widen(xw[j + 1], input<T, V>(a, p, t0 - (W - 1) + j, W, c));
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            nx[k] = input<T, V>(a, p, t0 + k, W, c);
-            ny[k] = grad(t0 + k);
+    using S = Smem<T, W>;
+    extern __shared__ __align__(16) char smem[];
+    S &s = *reinterpret_cast<S *>(smem);
+    const int tid = threadIdx.x, lane = tid % S::LANES, run = tid / S::LANES;
+    const int c0 = blockIdx.x * S::CH, c = c0 + lane * V, left = a.D - c;
+    constexpr int kChunks = S::CH / 8;
+    // rows of a piece: x from W - 1 in front of it to W - 1 behind, dy from its first token on
+    auto fetch = [&](const Piece &p, int b) {
+        const int nx = p.len + 2 * (W - 1), ny = p.len + W - 1;
+        for (int i = tid; i < nx * kChunks; i += kThreads) {
+            const int r = i / kChunks, e = i % kChunks * 8, pos = p.begin - (W - 1) + r;
+            const bool front = pos < 0;
+            const long long row = front ? (long long)p.seq * (W - 1) + pos + W - 1 : p.row0 + pos;
+            const bool ok = pos < p.total && (!front || a.initial) &&
+                            dbg_ok(a.dbg, (size_t)row, (size_t)(front ? (long long)a.tok.num_seqs * (W - 1) : a.tok.rows()), DBG_LOAD);
+            fetch_chunk<T>((Vec<T, 8> *)&s.x[b][r][e], front && a.initial ? a.initial : a.x,
+                           front ? a.D : a.x_stride, ok ? row : 0, c0 + e, a.D - c0 - e, ok, unit_x);
         }
-        for (int base = 0; base < steps; base += kAhead) {
-            Vec<T, V> x[kAhead], dy[kAhead];
+        for (int i = tid; i < ny * kChunks; i += kThreads) {
+            const int r = i / kChunks, e = i % kChunks * 8, pos = p.begin + r;
+            const long long row = p.row0 + pos;
+            const bool ok = pos < p.total && dbg_ok(a.dbg, (size_t)row, (size_t)a.tok.rows(), DBG_LOAD);
+            fetch_chunk<T>((Vec<T, 8> *)&s.dy[b][r][e], a.dy, a.dy_stride, ok ? row : 0, c0 + e,
+                           a.D - c0 - e, ok, unit_dy);
+        }
+    };
+    for (int i = tid; i < S::CH; i += kThreads) {
+        const bool in = c0 + i < a.D;
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                x[k] = nx[k];
-                dy[k] = ny[k];
-            }
-            if (base + kAhead < steps) {
+        for (int j = 0; j < W; ++j) s.w[j][i] = in ? param(a.weight, a.wdtype, (size_t)(c0 + i) * W + j, 0.f) : 0.f;
+        s.w[W][i] = in ? param(a.bias, a.wdtype, c0 + i, 0.f) : 0.f;
+    }
+    long long at = blockIdx.y;
+    Piece next = at < pieces ? find_piece(a.tok, at, kPiece) : Piece{};
+    if (at < pieces && next.len > 0) fetch(next, 0);
+    cp_async_commit();
+    __syncthreads();
+    float w[W][V], bias[V], dw[W][V] = {}, db[V] = {};
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    nx[k] = input<T, V>(a, p, t0 + base + kAhead + k, W, c);
-                    ny[k] = grad(t0 + base + kAhead + k);
-                }
-            }
+    for (int e = 0; e < V; ++e) {
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int i = base + k;
+        for (int j = 0; j < W; ++j) w[j][e] = s.w[j][lane * V + e];
+        bias[e] = s.w[W][lane * V + e];
+    }
+    for (int b = 0; at < pieces; at += gridDim.y, b ^= 1) {
+        const Piece p = next;
+        if (at + gridDim.y < pieces) {
+            next = find_piece(a.tok, at + gridDim.y, kPiece);
+            if (next.len > 0) fetch(next, b ^ 1);
+        }
+        cp_async_commit();
+        cp_async_wait_newest<1>();
+        __syncthreads();
+        const int r0 = run * S::kRun, t0 = p.begin + r0, n = min(S::kRun, p.len - r0);
+        if (n > 0 && left > 0) {
+            const T *xs = &s.x[b][r0][lane * V], *ys = &s.dy[b][r0][lane * V];
+            float xw[W][V], gw[W][V];  // input and g of step i are at i % W
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j)
+            for (int j = 0; j < W - 1; ++j)  // steps -(W - 1) .. -1
+                widen(xw[(j + 1) % W], *(const Vec<T, V> *)(xs + j * S::CH));
+            T *out = (T *)a.dx + (p.row0 + t0 - (W - 1)) * a.dx_stride + c;
+            const int steps = n + W - 1;
+            constexpr int U = W == 3 ? 3 : 4;
+            for (int base = 0; base < steps; base += U) {
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        xw[j][e] = xw[j + 1][e];
-                        gw[j][e] = gw[j + 1][e];
-                    }
-                widen(xw[W - 1], x[k]);
-                float g[V];
-                widen(g, dy[k]);
-                if (a.act == ACT_SILU) {
-                    float pre[V];
+                for (int k = 0; k < U; ++k) {
+                    const int i = base + k;  // token t0 + i (i % W = k % W)
+                    if (k > 0 && i >= steps) break;
+                    float(&x)[V] = xw[k % W], (&g)[V] = gw[k % W];
+                    widen(x, *(const Vec<T, V> *)(xs + (i + W - 1) * S::CH));
+                    widen(g, *(const Vec<T, V> *)(ys + i * S::CH));
+                    if (a.act == ACT_SILU) {
+                        float pre[V];
 #pragma unroll
-                    for (int e = 0; e < V; ++e) pre[e] = bias[e];
+                        for (int e = 0; e < V; ++e) pre[e] = bias[e];
 #pragma unroll
-                    for (int j = 0; j < W; ++j) vfma(pre, xw[j], wv[j]);
+                        for (int j = 0; j < W; ++j) vfma(pre, xw[(k + 1 + j) % W], w[j]);
+                        const bool in = t0 + i < p.total;  // (behind the sequence g is 0)
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        // (a position behind the sequence has dy = 0 and x = 0)
-                        const float s = sigmoid(pre[e]);
-                        g[e] = t0 + i < p.total ? g[e] * silu_slope(pre[e], s) : 0.f;
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < V; ++e) gw[W - 1][e] = g[e];
-                if (i < n) {
-#pragma unroll
-                    for (int j = 0; j < W; ++j) vfma(dw[j], g, xw[j]);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) db[e] += g[e];
-                }
-                if (i >= W - 1 && i < steps) {
-                    float dx[V] = {};
-#pragma unroll
-                    for (int j = 0; j < W; ++j) vfma(dx, wv[j], gw[W - 1 - j]);
-                    const int pos = t0 + i - (W - 1);
-                    const int last = pos - (p.total - (W - 1));
-                    if (a.d_final && last >= 0) {
-                        const size_t row = (size_t)p.seq * (W - 1) + last;
-                        if (dbg_ok(a.dbg, row, (size_t)a.tok.num_seqs * (W - 1), DBG_LOAD)) {
-                            const auto f = *reinterpret_cast<const Vec<T, V> *>((const T *)a.d_final + row * a.D + c);
-#pragma unroll
-                            for (int e = 0; e < V; ++e) dx[e] += f[e];
+                        for (int e = 0; e < V; e += 2) {
+                            const float2 z = make_float2(pre[e], pre[e + 1]);
+                            const float2 sg = make_float2(sigmoid(z.x), sigmoid(z.y));
+                            const float2 one = make_float2(1.f, 1.f);
+                            const float2 sl = mul2(sg, fma2(z, fma2(sg, make_float2(-1.f, -1.f), one), one));
+                            const float2 r = mul2(make_float2(g[e], g[e + 1]), sl);
+                            g[e] = in ? r.x : 0.f;
+                            g[e + 1] = in ? r.y : 0.f;
                         }
                     }
-                    Vec<T, V> out;
+                    if (i < n) {
 #pragma unroll
-                    for (int e = 0; e < V; ++e) out.v[e] = from_f32<T>(dx[e]);
-                    const long long row = p.row0 + pos;
-                    if (dbg_ok(a.dbg, (size_t)row, (size_t)a.tok.rows(), DBG_STORE))
-                        *reinterpret_cast<Vec<T, V> *>((T *)a.dx + row * a.dx_stride + c) = out;
+                        for (int j = 0; j < W; ++j) vfma(dw[j], g, xw[(k + 1 + j) % W]);
+#pragma unroll
+                        for (int e = 0; e < V; e += 2) {
+                            const float2 r = add2(make_float2(db[e], db[e + 1]), make_float2(g[e], g[e + 1]));
+                            db[e] = r.x;
+                            db[e + 1] = r.y;
+                        }
+                    }
+                    if (i >= W - 1) {  // the input W - 1 tokens back has all of its g
+                        float dx[V] = {};
+#pragma unroll
+                        for (int j = 0; j < W; ++j) vfma(dx, w[j], gw[(k + W - j) % W]);
+                        const int pos = t0 + i - (W - 1), last = pos - (p.total - (W - 1));
+                        if (a.d_final && last >= 0) {
+                            const size_t row = (size_t)p.seq * (W - 1) + last;
+#pragma unroll
+                            for (int e = 0; e < V; ++e)
+                                if (e < left && dbg_ok(a.dbg, row, (size_t)a.tok.num_seqs * (W - 1), DBG_LOAD))
+                                    dx[e] += as_f32(((const T *)a.d_final)[row * a.D + c + e]);
+                        }
+                        Vec<T, V> y;
+#pragma unroll
+                        for (int e = 0; e < V; ++e) y.v[e] = from_f32<T>(dx[e]);
+                        if (dbg_ok(a.dbg, (size_t)(p.row0 + pos), (size_t)a.tok.rows(), DBG_STORE)) {
+                            T *to = out + i * a.dx_stride;
+                            if (unit_dx >= (int)(V * sizeof(T))) {
+                                *(Vec<T, V> *)to = y;
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < V; ++e)
+                                    if (e < left) to[e] = y.v[e];
+                            }
+                        }
+                    }
                 }
             }
         }
+        __syncthreads();
     }
+    cp_async_wait_newest<0>();
     if (!a.dweight) return;
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < V; ++e) red[warp][lane * V + e] = j < W ? dw[j < W ? j : 0][e] : db[e];
+        for (int e = 0; e < V; ++e) s.red[run][lane * V + e] = j < W ? dw[j < W ? j : 0][e] : db[e];
         __syncthreads();
-        for (int i = threadIdx.x; i < 32 * V; i += 32 * kWarps) {
-            float s = 0.f;
+        for (int i = tid; i < S::CH; i += kThreads) {
+            float x = 0.f;
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) s += red[k][i];
+            for (int k = 0; k < S::kRuns; ++k) x += s.red[k][i];
             if (c0 + i < a.D && dbg_ok(a.dbg, blockIdx.y, (size_t)a.partials, DBG_STORE))
-                a.partial[((size_t)blockIdx.y * (W + 1) + j) * a.D + c0 + i] = s;
+                a.partial[((size_t)blockIdx.y * (W + 1) + j) * a.D + c0 + i] = x;
         }
     }
 }
@@ -199,21 +230,29 @@ template <typename T> __global__ void __launch_bounds__(256) kda_conv_initial_ke
     }
 }
 
-template <typename T, int V, int W> cudaError_t backward(const ConvArgs &a, cudaStream_t stream) {
-    const unsigned blocks = (unsigned)((a.D + 32 * V - 1) / (32 * V));
+template <typename T, int W> cudaError_t backward(const ConvArgs &a, cudaStream_t stream) {
+    using S = Smem<T, W>;
+    const unsigned blocks = (unsigned)((a.D + S::CH - 1) / S::CH);
     const long long pieces = a.tok.pieces(kPiece);
-    ConvArgs b = a;  // as many rows of sums as CTAs
-    const long long most = (2 * kSMs) / (long long)blocks > 1 ? (2 * kSMs) / (long long)blocks : 1;
+    ConvArgs b = a;  // as many rows of sums as CTAs: one wave, of three a multiprocessor
+    const long long most = 3 * kSMs / (long long)blocks > 1 ? 3 * kSMs / (long long)blocks : 1;
     const long long rows = pieces < most ? pieces : most;
     if (rows < b.partials || !a.dweight) b.partials = (int)rows;
-    cudaError_t e = launch_early(kda_conv_bwd_kernel<T, V, W>, dim3(blocks, (unsigned)b.partials),
-                                 32 * kWarps, 0, stream, b, pieces);
+    rows::Unit x(sizeof(T), a.D), dy(sizeof(T), a.D), dx(sizeof(T), a.D);
+    x.add(a.x, a.x_stride);
+    x.add(a.initial, a.D);
+    dy.add(a.dy, a.dy_stride);
+    dx.add(a.dx, a.dx_stride);
+    constexpr int kBytes = sizeof(S);
+    static volatile int done[kMaxDev];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = smem_limit_once(kda_conv_bwd_kernel<T, W>, kBytes, dev, done);
+    if (e != cudaSuccess) return e;
+    e = launch_early(kda_conv_bwd_kernel<T, W>, dim3(blocks, (unsigned)b.partials), kThreads, kBytes, stream, b,
+                     pieces, x.unit, dy.unit, dx.unit);
     if (e != cudaSuccess || !a.dweight) return e;
     return launch_early(kda_conv_sum_kernel, (unsigned)(((long long)(W + 1) * a.D + 255) / 256), 256, 0, stream, b);
-}
-template <typename T, int V> cudaError_t backward(const ConvArgs &a, cudaStream_t stream) {
-    return a.W == 4 ? backward<T, V, 4>(a, stream) : a.W == 3 ? backward<T, V, 3>(a, stream)
-                                                              : backward<T, V, 2>(a, stream);
 }
 template <typename T> cudaError_t backward(const ConvArgs &a, cudaStream_t stream) {
     if (a.d_initial) {
@@ -222,15 +261,15 @@ template <typename T> cudaError_t backward(const ConvArgs &a, cudaStream_t strea
                                            256, 0, stream, a);
         if (e != cudaSuccess) return e;
     }
-    return vec_ok(a, 4, true) ? backward<T, 4>(a, stream) : backward<T, 1>(a, stream);
+    return a.W == 4 ? backward<T, 4>(a, stream) : a.W == 3 ? backward<T, 3>(a, stream) : backward<T, 2>(a, stream);
 }
 
 }  // namespace
 }  // namespace conv
 
-// CTAs of a block of channels, each with a row of sums: one wave of them, of either block width.
+// CTAs of a block of channels, each with a row of sums, in the type with the fewest blocks.
 int conv_partials(long long pieces, int D) {
-    const long long blocks = (D + 127) / 128, most = 2 * kSMs / blocks > 1 ? 2 * kSMs / blocks : 1;
+    const long long blocks = (D + 63) / 64, most = 3 * kSMs / blocks > 1 ? 3 * kSMs / blocks : 1;
     return (int)(pieces < most ? pieces : most);
 }
 

@@ -1,9 +1,10 @@
 // Short causal convolution, forward, and its single-token form.
 //
 // Bound by memory: x is read and y written once.  A warp takes 8 tokens of 32 V channels, V those
-// of a 16-byte load; every row that they need (8 and the W - 1 in front) is asked for before the
-// first is used, so that a multiprocessor has some 100 KB on their way; the rows that two warps
-// both read come out of the cache.
+// of an 8-byte load (16 in FP32); every row that they need (8 and the W - 1 in front) is asked for before
+// the first is used, so that a multiprocessor has some 90 KB on their way in 32 warps; the rows that two
+// warps both read come out of the cache.  (With 16-byte loads of 16-bit types a thread needs 149
+// registers, and one CTA a multiprocessor is left: 644 us at B=8 T=4096 D=6144.)
 #include "kda_conv.cuh"
 
 namespace kda {
@@ -13,7 +14,7 @@ namespace {
 constexpr int kRun = 8, kWarps = 8, kPiece = kRun * kWarps;
 
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(32 * kWarps) kda_conv_fwd_kernel(const ConvArgs a, int blocks) {
+__global__ void __launch_bounds__(32 * kWarps, V == 1 ? 6 : 3) kda_conv_fwd_kernel(const ConvArgs a, int blocks) {
     wait_for_previous();
     __shared__ __align__(16) float w[W + 1][32 * V];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -25,8 +26,18 @@ __global__ void __launch_bounds__(32 * kWarps) kda_conv_fwd_kernel(const ConvArg
     const bool in = c < a.D;
     Vec<T, V> x[kRun + W - 1];
     if (in && n > 0) {
+        if (t0 >= W - 1 && t0 + kRun <= p.total &&
+            dbg_ok(a.dbg, (size_t)(p.row0 + t0 + kRun - 1), (size_t)a.tok.rows(), DBG_LOAD)) {
+            const T *at = (const T *)a.x + (p.row0 + t0 - (W - 1)) * a.x_stride + c;
 #pragma unroll
-        for (int i = 0; i < kRun + W - 1; ++i) x[i] = input<T, V>(a, p, t0 + i - (W - 1), W, c);
+            for (int i = 0; i < kRun + W - 1; ++i) {
+                x[i] = *reinterpret_cast<const Vec<T, V> *>(at);
+                at += a.x_stride;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kRun + W - 1; ++i) x[i] = input<T, V>(a, p, t0 + i - (W - 1), W, c);
+        }
     }
     __syncthreads();
     if (!in) return;
@@ -101,8 +112,7 @@ template <typename T, int V> cudaError_t forward(const ConvArgs &a, cudaStream_t
                                                              : forward<T, V, 2>(a, stream);
 }
 template <typename T> cudaError_t forward(const ConvArgs &a, cudaStream_t stream) {
-    constexpr int V = 16 / sizeof(T);
-    return vec_ok(a, V, false) ? forward<T, V>(a, stream) : forward<T, 1>(a, stream);
+    return vec_ok(a, 4) ? forward<T, 4>(a, stream) : forward<T, 1>(a, stream);
 }
 
 template <typename T, int V, int W> cudaError_t step(const ConvArgs &a, cudaStream_t stream) {
@@ -116,7 +126,7 @@ template <typename T, int V> cudaError_t step(const ConvArgs &a, cudaStream_t st
 }
 template <typename T> cudaError_t step(const ConvArgs &a, cudaStream_t stream) {
     constexpr int V = 8 / sizeof(T);
-    return vec_ok(a, V, false) && aligned(a.state, 8) ? step<T, V>(a, stream) : step<T, 1>(a, stream);
+    return vec_ok(a, V) && aligned(a.state, 8) ? step<T, V>(a, stream) : step<T, 1>(a, stream);
 }
 
 }  // namespace

@@ -90,5 +90,56 @@ __device__ __forceinline__ Piece find_piece(const Tokens &t, long long p, int si
 
 inline bool aligned(const void *p, size_t to) { return (uintptr_t)p % to == 0; }
 
+// The widest of 16, 8, 4 bytes and an element on whose boundaries all rows and blocks of `per` channels
+// begin.
+struct Unit {
+    int es, unit;
+    Unit(int es, int per) : es(es), unit(16) {
+        while (unit > es && (long long)per * es % unit) unit /= 2;
+    }
+    void add(const void *p, long long stride) {
+        while (p && unit > es && !(aligned(p, unit) && stride * es % unit == 0)) unit /= 2;
+    }
+};
+
+// Eight neighbouring channels of a token on their way into shared memory, `unit` bytes at a time (16,
+// 8 or 4 by asynchronous copies, or an element): rows and blocks of channels begin on such
+// boundaries.  Zeros where there are none (c + left is the first channel behind them).
+template <typename T>
+__device__ __forceinline__ void fetch_chunk(Vec<T, 8> *slot, const void *base, long long stride,
+                                            long long row, int c, int left, bool ok, int unit) {
+    const char *at = (const char *)((const T *)base + row * stride + c);
+    constexpr int E = sizeof(T);
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot);
+    if (unit == 16) {
+#pragma unroll
+        for (int i = 0; i < 8 * E; i += 16) {
+            const bool in = ok && i < left * E;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i), "l"(in ? at + i : base),
+                         "r"(in ? 16 : 0) : "memory");
+        }
+    } else if (unit == 8) {
+#pragma unroll
+        for (int i = 0; i < 8 * E; i += 8) {
+            const bool in = ok && i < left * E;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + i), "l"(in ? at + i : base),
+                         "r"(in ? 8 : 0) : "memory");
+        }
+    } else if (unit == 4) {
+#pragma unroll
+        for (int i = 0; i < 8 * E; i += 4) {
+            const bool in = ok && i < left * E;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + i), "l"(in ? at + i : base),
+                         "r"(in ? 4 : 0) : "memory");
+        }
+    } else {
+        T v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = ok && i < left ? ((const T *)at)[i] : from_f32<T>(0.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) slot->v[i] = v[i];
+    }
+}
+
 }  // namespace rows
 }  // namespace kda

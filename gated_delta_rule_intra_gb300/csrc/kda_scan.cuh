@@ -115,45 +115,6 @@ template <int NP> struct Block {
     }
 };
 
-// Eight neighbouring channels of a token on their way to the thread that takes them, which copies
-// them into a slot of its own in shared memory: nobody else's copies have to be waited for.  `unit`
-// bytes at a time (16, 8 or 4 by asynchronous copies, or an element): rows and blocks of channels
-// begin on such boundaries.  Zeros where there are none.
-template <typename T>
-__device__ __forceinline__ void fetch_chunk(Vec<T, 8> *slot, const void *base, long long stride,
-                                            long long row, int c, int left, bool ok, int unit) {
-    const char *at = (const char *)((const T *)base + row * stride + c);
-    constexpr int E = sizeof(T);
-    const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot);
-    if (unit == 16) {
-#pragma unroll
-        for (int i = 0; i < 8 * E; i += 16) {
-            const bool in = ok && i < left * E;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i), "l"(in ? at + i : base),
-                         "r"(in ? 16 : 0) : "memory");
-        }
-    } else if (unit == 8) {
-#pragma unroll
-        for (int i = 0; i < 8 * E; i += 8) {
-            const bool in = ok && i < left * E;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + i), "l"(in ? at + i : base),
-                         "r"(in ? 8 : 0) : "memory");
-        }
-    } else if (unit == 4) {
-#pragma unroll
-        for (int i = 0; i < 8 * E; i += 4) {
-            const bool in = ok && i < left * E;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + i), "l"(in ? at + i : base),
-                         "r"(in ? 4 : 0) : "memory");
-        }
-    } else {
-        T v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = ok && i < left ? ((const T *)at)[i] : from_f32<T>(0.f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) slot->v[i] = v[i];
-    }
-}
 template <typename T>
 __device__ __forceinline__ void store_chunk(void *base, long long stride, long long row, int c,
                                             int left, const Vec<T, 8> &x, int unit) {
@@ -310,15 +271,8 @@ template <int L> struct Share {
     static __device__ __forceinline__ bool mine(int part) { return L <= 4 || part % (L / 4 > 0 ? L / 4 : 1) == 0; }
 };
 
-// The widest of 16, 8, 4 bytes and an element on whose boundaries all rows and blocks begin.
-struct Unit {
-    int es, unit;
-    Unit(const ScanArgs &a) : es(esize(a.dtype)), unit(16) {
-        while (unit > es && (a.D / a.G) * es % unit) unit /= 2;
-    }
-    void add(const void *p, long long stride) {
-        while (p && unit > es && !(aligned(p, unit) && stride * es % unit == 0)) unit /= 2;
-    }
+struct Unit : rows::Unit {
+    Unit(const ScanArgs &a) : rows::Unit(esize(a.dtype), a.D / a.G) {}
 };
 
 }  // namespace scan
