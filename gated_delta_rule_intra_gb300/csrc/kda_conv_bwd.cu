@@ -3,68 +3,53 @@
 //   dweight[j] = sum over tokens of g[t] x[t - W + 1 + j],  dbias = sum over tokens of g.
 // The final state's gradient is that of the sequence's last inputs and is added to theirs.
 //
-// Bound by memory (x and dy read, dx written once) if instructions leave it room: a resident CTA takes
-// pieces of 128 tokens of one block of channels in turn, and the next piece's rows are on their
-// way into shared memory meanwhile, whatever their alignment.  A thread walks a run of tokens of four
-// channels with the last W inputs and the last W values of g in registers (the places of both go
-// round, so that nothing is moved), and W - 1 tokens more whose g its last inputs need.  The CTAs'
-// sums of the parameters' gradients are added up in a fixed order by a second kernel.
+// Bound by instructions (40 us of g alone) next to memory (x and dy read, dx written once).  Rows come
+// through shared memory, one piece ahead (kda_conv.cuh).  A thread has the last W values of g in
+// registers too, and walks W - 1 tokens more whose g its last inputs need; a whole run is one straight
+// piece of code.  The CTAs' sums of the parameters' gradients are added up in a fixed order by a
+// second kernel.
+#include <type_traits>
+
 #include "kda_conv.cuh"
 
 namespace kda {
 namespace conv {
 namespace {
 
-constexpr int kThreads = 128, V = 4, kPiece = kConvPiece;
-
 template <typename T, int W> struct Smem {
-    static constexpr int LANES = 64 / (V * sizeof(T)) * 2;  // of a row: 128 bytes
-    static constexpr int CH = LANES * V, kRuns = kThreads / LANES, kRun = kPiece / kRuns;
-    static constexpr int kX = kPiece + 2 * (W - 1), kDy = kPiece + W - 1;
-    T x[2][kX][CH], dy[2][kDy][CH];
-    float w[W + 1][CH], red[kRuns][CH];
+    static constexpr int kDy = kPiece + W - 1, kX = kDy + W - 1;
+    T x[2][kX][Shape<T>::CH], dy[2][kDy][Shape<T>::CH];
+    float w[W + 1][Shape<T>::CH], red[Shape<T>::kRuns][Shape<T>::CH];
 };
 
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads, 3)
     kda_conv_bwd_kernel(const ConvArgs a, long long pieces, int unit_x, int unit_dy, int unit_dx) {
     wait_for_previous();
-    using S = Smem<T, W>;
+    using S = Shape<T>;
     extern __shared__ __align__(16) char smem[];
-    S &s = *reinterpret_cast<S *>(smem);
+    Smem<T, W> &s = *reinterpret_cast<Smem<T, W> *>(smem);
     const int tid = threadIdx.x, lane = tid % S::LANES, run = tid / S::LANES;
     const int c0 = blockIdx.x * S::CH, c = c0 + lane * V, left = a.D - c;
-    constexpr int kChunks = S::CH / 8;
-    // rows of a piece: x from W - 1 in front of it to W - 1 behind, dy from its first token on
-    auto fetch = [&](const Piece &p, int b) {
-        const int nx = p.len + 2 * (W - 1), ny = p.len + W - 1;
-        for (int i = tid; i < nx * kChunks; i += kThreads) {
-            const int r = i / kChunks, e = i % kChunks * 8, pos = p.begin - (W - 1) + r;
-            const bool front = pos < 0;
-            const long long row = front ? (long long)p.seq * (W - 1) + pos + W - 1 : p.row0 + pos;
-            const bool ok = pos < p.total && (!front || a.initial) &&
-                            dbg_ok(a.dbg, (size_t)row, (size_t)(front ? (long long)a.tok.num_seqs * (W - 1) : a.tok.rows()), DBG_LOAD);
-            fetch_chunk<T>((Vec<T, 8> *)&s.x[b][r][e], front && a.initial ? a.initial : a.x,
-                           front ? a.D : a.x_stride, ok ? row : 0, c0 + e, a.D - c0 - e, ok, unit_x);
-        }
-        for (int i = tid; i < ny * kChunks; i += kThreads) {
-            const int r = i / kChunks, e = i % kChunks * 8, pos = p.begin + r;
-            const long long row = p.row0 + pos;
-            const bool ok = pos < p.total && dbg_ok(a.dbg, (size_t)row, (size_t)a.tok.rows(), DBG_LOAD);
-            fetch_chunk<T>((Vec<T, 8> *)&s.dy[b][r][e], a.dy, a.dy_stride, ok ? row : 0, c0 + e,
-                           a.D - c0 - e, ok, unit_dy);
-        }
+    const bool wide = unit_dx >= (int)(V * sizeof(T));
+    auto piece = [&](long long at) {
+        Piece p;
+        p.len = -1;
+        return at < pieces ? find_piece(a.tok, at, kPiece) : p;
     };
-    for (int i = tid; i < S::CH; i += kThreads) {
-        const bool in = c0 + i < a.D;
-#pragma unroll
-        for (int j = 0; j < W; ++j) s.w[j][i] = in ? param(a.weight, a.wdtype, (size_t)(c0 + i) * W + j, 0.f) : 0.f;
-        s.w[W][i] = in ? param(a.bias, a.wdtype, c0 + i, 0.f) : 0.f;
-    }
-    long long at = blockIdx.y;
-    Piece next = at < pieces ? find_piece(a.tok, at, kPiece) : Piece{};
-    if (at < pieces && next.len > 0) fetch(next, 0);
-    cp_async_commit();
+    // x from W - 1 rows in front of a piece to W - 1 behind it, dy from its first token on
+    auto fetch = [&](const Piece &p, int stage) {
+        if (p.len > 0) {
+            const int end = p.begin + p.len + W - 1, r = tid / S::kChunks, e = tid % S::kChunks * 8;
+            fetch_inputs<T, W>(s.x[stage], a, p, end, c0, unit_x);
+            fetch_rows<T>((T(*)[S::CH])&s.dy[stage][r][e], a, p, a.dy, a.dy_stride, p.begin + r, end, c0 + e,
+                          a.D - c0 - e, unit_dy);
+        }
+        cp_async_commit();
+    };
+    load_params<W>(a, c0, s.w);
+    Piece next = piece(blockIdx.y);
+    fetch(next, 0);
     __syncthreads();
     float w[W][V], bias[V], dw[W][V] = {}, db[V] = {};
 #pragma unroll
@@ -73,31 +58,28 @@ __global__ void __launch_bounds__(kThreads, 3)
         for (int j = 0; j < W; ++j) w[j][e] = s.w[j][lane * V + e];
         bias[e] = s.w[W][lane * V + e];
     }
-    for (int b = 0; at < pieces; at += gridDim.y, b ^= 1) {
+    int b = 0;
+    for (long long at = blockIdx.y; at < pieces; at += gridDim.y, b ^= 1) {
         const Piece p = next;
-        if (at + gridDim.y < pieces) {
-            next = find_piece(a.tok, at + gridDim.y, kPiece);
-            if (next.len > 0) fetch(next, b ^ 1);
-        }
-        cp_async_commit();
+        next = piece(at + gridDim.y);
+        fetch(next, b ^ 1);
         cp_async_wait_newest<1>();
         __syncthreads();
         const int r0 = run * S::kRun, t0 = p.begin + r0, n = min(S::kRun, p.len - r0);
         if (n > 0 && left > 0) {
             const T *xs = &s.x[b][r0][lane * V], *ys = &s.dy[b][r0][lane * V];
-            float xw[W][V], gw[W][V];  // input and g of step i are at i % W
+            const bool fin = a.d_final && t0 + n > p.total - (W - 1);  // of the last inputs
+            // whole: every token is in the sequence, the W - 1 behind the run too
+            auto walk = [&](auto whole) {
+                float xw[W][V], gw[W][V];  // input and g of step i are at i % W
+                T *out = (T *)a.dx + (p.row0 + t0) * a.dx_stride + c;
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j)  // steps -(W - 1) .. -1
-                widen(xw[(j + 1) % W], *(const Vec<T, V> *)(xs + j * S::CH));
-            T *out = (T *)a.dx + (p.row0 + t0 - (W - 1)) * a.dx_stride + c;
-            const int steps = n + W - 1;
-            constexpr int U = W == 3 ? 3 : 4;
-            for (int base = 0; base < steps; base += U) {
+                for (int j = 0; j < W - 1; ++j)  // steps -(W - 1) .. -1
+                    widen(xw[(j + 1) % W], *(const Vec<T, V> *)(xs + j * S::CH));
 #pragma unroll
-                for (int k = 0; k < U; ++k) {
-                    const int i = base + k;  // token t0 + i (i % W = k % W)
-                    if (k > 0 && i >= steps) break;
-                    float(&x)[V] = xw[k % W], (&g)[V] = gw[k % W];
+                for (int i = 0; i < S::kRun + W - 1; ++i) {  // token t0 + i
+                    if (!whole && i >= n + W - 1) break;
+                    float(&x)[V] = xw[i % W], (&g)[V] = gw[i % W];
                     widen(x, *(const Vec<T, V> *)(xs + (i + W - 1) * S::CH));
                     widen(g, *(const Vec<T, V> *)(ys + i * S::CH));
                     if (a.act == ACT_SILU) {
@@ -105,8 +87,7 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
                         for (int e = 0; e < V; ++e) pre[e] = bias[e];
 #pragma unroll
-                        for (int j = 0; j < W; ++j) vfma(pre, xw[(k + 1 + j) % W], w[j]);
-                        const bool in = t0 + i < p.total;  // (behind the sequence g is 0)
+                        for (int j = 0; j < W; ++j) vfma(pre, xw[(i + 1 + j) % W], w[j]);
 #pragma unroll
                         for (int e = 0; e < V; e += 2) {
                             const float2 z = make_float2(pre[e], pre[e + 1]);
@@ -114,13 +95,17 @@ __global__ void __launch_bounds__(kThreads, 3)
                             const float2 one = make_float2(1.f, 1.f);
                             const float2 sl = mul2(sg, fma2(z, fma2(sg, make_float2(-1.f, -1.f), one), one));
                             const float2 r = mul2(make_float2(g[e], g[e + 1]), sl);
-                            g[e] = in ? r.x : 0.f;
-                            g[e + 1] = in ? r.y : 0.f;
+                            g[e] = r.x;
+                            g[e + 1] = r.y;
+                        }
+                        if (!whole && t0 + i >= p.total) {  // behind the sequence, whatever its last inputs are
+#pragma unroll
+                            for (int e = 0; e < V; ++e) g[e] = 0.f;
                         }
                     }
-                    if (i < n) {
+                    if (whole ? i < S::kRun : i < n) {
 #pragma unroll
-                        for (int j = 0; j < W; ++j) vfma(dw[j], g, xw[(k + 1 + j) % W]);
+                        for (int j = 0; j < W; ++j) vfma(dw[j], g, xw[(i + 1 + j) % W]);
 #pragma unroll
                         for (int e = 0; e < V; e += 2) {
                             const float2 r = add2(make_float2(db[e], db[e + 1]), make_float2(g[e], g[e + 1]));
@@ -128,34 +113,29 @@ __global__ void __launch_bounds__(kThreads, 3)
                             db[e + 1] = r.y;
                         }
                     }
-                    if (i >= W - 1) {  // the input W - 1 tokens back has all of its g
-                        float dx[V] = {};
+                    if (i < W - 1) continue;
+                    float dx[V] = {};  // of the input W - 1 tokens back, which has all of its g
 #pragma unroll
-                        for (int j = 0; j < W; ++j) vfma(dx, w[j], gw[(k + W - j) % W]);
-                        const int pos = t0 + i - (W - 1), last = pos - (p.total - (W - 1));
-                        if (a.d_final && last >= 0) {
-                            const size_t row = (size_t)p.seq * (W - 1) + last;
+                    for (int j = 0; j < W; ++j) vfma(dx, w[j], gw[(i + W - j) % W]);
+                    const int pos = t0 + i - (W - 1), last = pos - (p.total - (W - 1));
+                    if (!whole && fin && last >= 0) {
+                        const size_t row = (size_t)p.seq * (W - 1) + last;
 #pragma unroll
-                            for (int e = 0; e < V; ++e)
-                                if (e < left && dbg_ok(a.dbg, row, (size_t)a.tok.num_seqs * (W - 1), DBG_LOAD))
-                                    dx[e] += as_f32(((const T *)a.d_final)[row * a.D + c + e]);
-                        }
-                        Vec<T, V> y;
-#pragma unroll
-                        for (int e = 0; e < V; ++e) y.v[e] = from_f32<T>(dx[e]);
-                        if (dbg_ok(a.dbg, (size_t)(p.row0 + pos), (size_t)a.tok.rows(), DBG_STORE)) {
-                            T *to = out + i * a.dx_stride;
-                            if (unit_dx >= (int)(V * sizeof(T))) {
-                                *(Vec<T, V> *)to = y;
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < V; ++e)
-                                    if (e < left) to[e] = y.v[e];
-                            }
-                        }
+                        for (int e = 0; e < V; ++e)
+                            if (e < left && dbg_ok(a.dbg, row, (size_t)a.tok.num_seqs * (W - 1), DBG_LOAD))
+                                dx[e] += as_f32(((const T *)a.d_final)[row * a.D + c + e]);
                     }
+                    Vec<T, V> y;
+                    narrow(y, dx);
+                    if (dbg_ok(a.dbg, (size_t)(p.row0 + pos), (size_t)a.tok.rows(), DBG_STORE))
+                        store_channels(out, y, left, wide);
+                    out += a.dx_stride;
                 }
-            }
+            };
+            if (n == S::kRun && t0 + n + W - 1 <= p.total)
+                walk(std::true_type());
+            else
+                walk(std::false_type());
         }
         __syncthreads();
     }
@@ -208,13 +188,17 @@ template <typename T> __global__ void __launch_bounds__(256) kda_conv_initial_ke
         p.row0 = (long long)n * a.tok.T;
         p.total = a.tok.T;
     }
+    auto input = [&](int pos) {
+        return pos >= 0 ? as_f32(((const T *)a.x)[(p.row0 + pos) * a.x_stride + c])
+               : a.initial ? as_f32(((const T *)a.initial)[((size_t)n * (W - 1) + pos + W - 1) * a.D + c]) : 0.f;
+    };
     float d[3] = {};
     for (int t = 0; t < W - 1 && t < p.total; ++t) {
         float g = as_f32(((const T *)a.dy)[(p.row0 + t) * a.dy_stride + c]);
         if (a.act == ACT_SILU) {
             float pre = param(a.bias, a.wdtype, c, 0.f);
             for (int j = 0; j < W; ++j)
-                pre = fmaf(input<T, 1>(a, p, t - (W - 1) + j, W, c)[0],
+                pre = fmaf(input(t - (W - 1) + j),
                            param(a.weight, a.wdtype, (size_t)c * W + j, 0.f), pre);
             g *= silu_slope(pre, sigmoid(pre));
         }
@@ -231,8 +215,7 @@ template <typename T> __global__ void __launch_bounds__(256) kda_conv_initial_ke
 }
 
 template <typename T, int W> cudaError_t backward(const ConvArgs &a, cudaStream_t stream) {
-    using S = Smem<T, W>;
-    const unsigned blocks = (unsigned)((a.D + S::CH - 1) / S::CH);
+    const unsigned blocks = (unsigned)((a.D + Shape<T>::CH - 1) / Shape<T>::CH);
     const long long pieces = a.tok.pieces(kPiece);
     ConvArgs b = a;  // as many rows of sums as CTAs: one wave, of three a multiprocessor
     const long long most = 3 * kSMs / (long long)blocks > 1 ? 3 * kSMs / (long long)blocks : 1;
@@ -243,7 +226,7 @@ template <typename T, int W> cudaError_t backward(const ConvArgs &a, cudaStream_
     x.add(a.initial, a.D);
     dy.add(a.dy, a.dy_stride);
     dx.add(a.dx, a.dx_stride);
-    constexpr int kBytes = sizeof(S);
+    constexpr int kBytes = sizeof(Smem<T, W>);
     static volatile int done[kMaxDev];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

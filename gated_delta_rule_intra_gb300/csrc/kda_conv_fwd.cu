@@ -1,76 +1,107 @@
 // Short causal convolution, forward, and its single-token form.
 //
-// Bound by memory: x is read and y written once.  A warp takes 8 tokens of 32 V channels, V those
-// of an 8-byte load (16 in FP32); every row that they need (8 and the W - 1 in front) is asked for before
-// the first is used, so that a multiprocessor has some 90 KB on their way in 32 warps; the rows that two
-// warps both read come out of the cache.  (With 16-byte loads of 16-bit types a thread needs 149
-// registers, and one CTA a multiprocessor is left: 644 us at B=8 T=4096 D=6144.)
+// Bound by memory: x is read and y written once.  Rows come through shared memory, two pieces ahead
+// (kda_conv.cuh).  (Loads into registers eight tokens ahead: 188 us at B=8 T=4096 D=6144, with a third
+// of the instructions moving and addressing them.)
+#include <type_traits>
+
 #include "kda_conv.cuh"
 
 namespace kda {
 namespace conv {
 namespace {
 
-constexpr int kRun = 8, kWarps = 8, kPiece = kRun * kWarps;
+constexpr int kStages = 3;
 
-template <typename T, int V, int W>
-__global__ void __launch_bounds__(32 * kWarps, V == 1 ? 6 : 3) kda_conv_fwd_kernel(const ConvArgs a, int blocks) {
+template <typename T, int W> struct Smem {
+    T x[kStages][kPiece + W - 1][Shape<T>::CH];
+    float w[W + 1][Shape<T>::CH];
+};
+
+template <typename T, int W>
+__global__ void __launch_bounds__(kThreads, 4)
+    kda_conv_fwd_kernel(const ConvArgs a, long long pieces, int unit_x, int unit_y) {
     wait_for_previous();
-    __shared__ __align__(16) float w[W + 1][32 * V];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c0 = (int)(blockIdx.x % (unsigned)blocks) * 32 * V, c = c0 + lane * V;
-    const Piece p = find_piece(a.tok, blockIdx.x / (unsigned)blocks, kPiece);
-    if (p.len < 0) return;
-    load_params<V, W>(a, c0, w, 32 * kWarps);
-    const int t0 = p.begin + warp * kRun, n = min(kRun, p.begin + p.len - t0);
-    const bool in = c < a.D;
-    Vec<T, V> x[kRun + W - 1];
-    if (in && n > 0) {
-        if (t0 >= W - 1 && t0 + kRun <= p.total &&
-            dbg_ok(a.dbg, (size_t)(p.row0 + t0 + kRun - 1), (size_t)a.tok.rows(), DBG_LOAD)) {
-            const T *at = (const T *)a.x + (p.row0 + t0 - (W - 1)) * a.x_stride + c;
-#pragma unroll
-            for (int i = 0; i < kRun + W - 1; ++i) {
-                x[i] = *reinterpret_cast<const Vec<T, V> *>(at);
-                at += a.x_stride;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kRun + W - 1; ++i) x[i] = input<T, V>(a, p, t0 + i - (W - 1), W, c);
-        }
-    }
+    using S = Shape<T>;
+    extern __shared__ __align__(16) char smem[];
+    Smem<T, W> &s = *reinterpret_cast<Smem<T, W> *>(smem);
+    const int lane = threadIdx.x % S::LANES, run = threadIdx.x / S::LANES;
+    const int c0 = blockIdx.x * S::CH, c = c0 + lane * V, left = a.D - c;
+    const bool wide = unit_y >= (int)(V * sizeof(T));
+    auto piece = [&](long long at) {
+        Piece p;
+        p.len = -1;
+        return at < pieces ? find_piece(a.tok, at, kPiece) : p;
+    };
+    auto fetch = [&](const Piece &p, int stage) {
+        if (p.len >= 0) fetch_inputs<T, W>(s.x[stage], a, p, p.begin + p.len, c0, unit_x);
+        cp_async_commit();
+    };
+    load_params<W>(a, c0, s.w);
+    Piece p = piece(blockIdx.y), p1 = piece(blockIdx.y + (long long)gridDim.y);
+    fetch(p, 0);
+    fetch(p1, 1);
     __syncthreads();
-    if (!in) return;
-    if (n > 0) {
+    float w[W][V], bias[V];
 #pragma unroll
-        for (int t = 0; t < kRun; ++t) {
-            float acc[V];
+    for (int e = 0; e < V; ++e) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = w[W][lane * V + i];
+        for (int j = 0; j < W; ++j) w[j][e] = s.w[j][lane * V + e];
+        bias[e] = s.w[W][lane * V + e];
+    }
+    int b = 0;
+    for (long long at = blockIdx.y; at < pieces; at += gridDim.y) {
+        const Piece p2 = piece(at + 2LL * gridDim.y);
+        fetch(p2, b > 0 ? b - 1 : kStages - 1);
+        cp_async_wait_newest<2>();
+        __syncthreads();
+        const int r0 = run * S::kRun, n = p.len - r0;
+        if (n > 0 && left > 0) {
+            const T *xs = &s.x[b][r0][lane * V];
+            T *out = (T *)a.y + (p.row0 + p.begin + r0) * a.y_stride + c;
+            auto walk = [&](auto whole) {
+                float x[W][V];  // the input of token i is at i % W
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                float xv[V], wv[V];
-                widen(xv, x[t + j]);
+                for (int j = 0; j < W - 1; ++j) widen(x[(j + 1) % W], *(const Vec<T, V> *)(xs + j * S::CH));
 #pragma unroll
-                for (int i = 0; i < V; ++i) wv[i] = w[j][lane * V + i];
-                vfma(acc, xv, wv);
-            }
-            const long long row = p.row0 + t0 + t;
-            if (t < n && dbg_ok(a.dbg, (size_t)row, (size_t)a.tok.rows(), DBG_STORE)) {
-                Vec<T, V> y;
+                for (int i = 0; i < S::kRun; ++i) {
+                    if (!whole && i >= n) break;
+                    widen(x[i % W], *(const Vec<T, V> *)(xs + (i + W - 1) * S::CH));
+                    float acc[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    y.v[i] = from_f32<T>(a.act == ACT_SILU ? acc[i] * sigmoid(acc[i]) : acc[i]);
-                *reinterpret_cast<Vec<T, V> *>((T *)a.y + row * a.y_stride + c) = y;
+                    for (int e = 0; e < V; ++e) acc[e] = bias[e];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) vfma(acc, x[(i + 1 + j) % W], w[j]);
+                    if (a.act == ACT_SILU) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) acc[e] *= sigmoid(acc[e]);
+                    }
+                    Vec<T, V> y;
+                    narrow(y, acc);
+                    if (dbg_ok(a.dbg, (size_t)(p.row0 + p.begin + r0 + i), (size_t)a.tok.rows(), DBG_STORE))
+                        store_channels(out, y, left, wide);
+                    out += a.y_stride;
+                }
+            };
+            if (n >= S::kRun)
+                walk(std::true_type());
+            else
+                walk(std::false_type());
+        }
+        if (a.final && p.len >= 0 && p.begin + p.len == p.total) {  // the sequence's last inputs
+            for (int i = threadIdx.x; i < (W - 1) * S::CH; i += kThreads) {
+                const int r = i / S::CH, e = i % S::CH;
+                const size_t row = (size_t)p.seq * (W - 1) + r;
+                if (c0 + e < a.D && dbg_ok(a.dbg, row, (size_t)a.tok.num_seqs * (W - 1), DBG_STORE))
+                    ((T *)a.final)[row * a.D + c0 + e] = s.x[b][p.len + r][e];
             }
         }
+        __syncthreads();
+        p = p1;
+        p1 = p2;
+        b = b + 1 < kStages ? b + 1 : 0;
     }
-    if (a.final && p.begin + p.len == p.total && warp < W - 1) {  // the sequence's last inputs
-        const size_t row = (size_t)p.seq * (W - 1) + warp;
-        if (dbg_ok(a.dbg, row, (size_t)a.tok.num_seqs * (W - 1), DBG_STORE))
-            *reinterpret_cast<Vec<T, V> *>((T *)a.final + row * a.D + c) =
-                input<T, V>(a, p, p.total - (W - 1) + warp, W, c);
-    }
+    cp_async_wait_newest<0>();
 }
 
 template <typename T, int V, int W>
@@ -102,17 +133,25 @@ __global__ void __launch_bounds__(256) kda_conv_step_kernel(const ConvArgs a) {
         *reinterpret_cast<Vec<T, V> *>((T *)a.y + n * a.y_stride + c) = y;
 }
 
-template <typename T, int V, int W> cudaError_t forward(const ConvArgs &a, cudaStream_t stream) {
-    const int blocks = (a.D + 32 * V - 1) / (32 * V);
-    return launch_early(kda_conv_fwd_kernel<T, V, W>, (unsigned)(a.tok.pieces(kPiece) * blocks),
-                        32 * kWarps, 0, stream, a, blocks);
-}
-template <typename T, int V> cudaError_t forward(const ConvArgs &a, cudaStream_t stream) {
-    return a.W == 4 ? forward<T, V, 4>(a, stream) : a.W == 3 ? forward<T, V, 3>(a, stream)
-                                                             : forward<T, V, 2>(a, stream);
+template <typename T, int W> cudaError_t forward(const ConvArgs &a, cudaStream_t stream) {
+    const long long pieces = a.tok.pieces(kPiece);
+    const unsigned blocks = (unsigned)((a.D + Shape<T>::CH - 1) / Shape<T>::CH);
+    const long long most = 4 * kSMs / (long long)blocks > 1 ? 4 * kSMs / (long long)blocks : 1;  // one wave
+    rows::Unit x(sizeof(T), a.D), y(sizeof(T), a.D);
+    x.add(a.x, a.x_stride);
+    x.add(a.initial, a.D);
+    y.add(a.y, a.y_stride);
+    constexpr int kBytes = sizeof(Smem<T, W>);
+    static volatile int done[kMaxDev];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = smem_limit_once(kda_conv_fwd_kernel<T, W>, kBytes, dev, done);
+    if (e != cudaSuccess) return e;
+    return launch_early(kda_conv_fwd_kernel<T, W>, dim3(blocks, (unsigned)(pieces < most ? pieces : most)), kThreads,
+                        kBytes, stream, a, pieces, x.unit, y.unit);
 }
 template <typename T> cudaError_t forward(const ConvArgs &a, cudaStream_t stream) {
-    return vec_ok(a, 4) ? forward<T, 4>(a, stream) : forward<T, 1>(a, stream);
+    return a.W == 4 ? forward<T, 4>(a, stream) : a.W == 3 ? forward<T, 3>(a, stream) : forward<T, 2>(a, stream);
 }
 
 template <typename T, int V, int W> cudaError_t step(const ConvArgs &a, cudaStream_t stream) {
@@ -126,7 +165,9 @@ template <typename T, int V> cudaError_t step(const ConvArgs &a, cudaStream_t st
 }
 template <typename T> cudaError_t step(const ConvArgs &a, cudaStream_t stream) {
     constexpr int V = 8 / sizeof(T);
-    return vec_ok(a, V) && aligned(a.state, 8) ? step<T, V>(a, stream) : step<T, 1>(a, stream);
+    const bool wide = a.D % V == 0 && aligned(a.x, 8) && aligned(a.y, 8) && aligned(a.state, 8) &&
+                      a.x_stride % V == 0 && a.y_stride % V == 0;
+    return wide ? step<T, V>(a, stream) : step<T, 1>(a, stream);
 }
 
 }  // namespace

@@ -20,6 +20,26 @@ template <> __device__ __forceinline__ __half from_f32<__half>(float x) {
     return __float2half_rn(x);
 }
 
+// Neighbouring elements as FP32 and back, two at a time.
+__device__ __forceinline__ float2 get_two(const float *p) { return make_float2(p[0], p[1]); }
+__device__ __forceinline__ float2 get_two(const __nv_bfloat16 *p) {
+    const uint32_t u = *reinterpret_cast<const uint32_t *>(p);
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ float2 get_two(const __half *p) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(p));
+}
+__device__ __forceinline__ void set_two(float *p, float2 x) {
+    p[0] = x.x;
+    p[1] = x.y;
+}
+__device__ __forceinline__ void set_two(__nv_bfloat16 *p, float2 x) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __float22bfloat162_rn(x);
+}
+__device__ __forceinline__ void set_two(__half *p, float2 x) {
+    *reinterpret_cast<__half2 *>(p) = __float22half2_rn(x);
+}
+
 // V neighbouring channels of a row.
 template <typename T, int V> struct alignas(sizeof(T) * V) Vec {
     T v[V];
@@ -28,9 +48,9 @@ template <typename T, int V> struct alignas(sizeof(T) * V) Vec {
         for (int i = 0; i < V; ++i) v[i] = from_f32<T>(0.f);
     }
     __device__ __forceinline__ float operator[](int i) const { return as_f32(v[i]); }
-    __device__ __forceinline__ float2 two(int i) const {
-        return make_float2(as_f32(v[i]), as_f32(v[i + 1]));
-    }
+    // (even i)
+    __device__ __forceinline__ float2 two(int i) const { return get_two(v + i); }
+    __device__ __forceinline__ void put(int i, float2 x) { set_two(v + i, x); }
 };
 
 // An element of a parameter, whose type may be x's or FP32.
@@ -104,11 +124,11 @@ struct Unit {
 
 // Eight neighbouring channels of a token on their way into shared memory, `unit` bytes at a time (16,
 // 8 or 4 by asynchronous copies, or an element): rows and blocks of channels begin on such
-// boundaries.  Zeros where there are none (c + left is the first channel behind them).
+// boundaries.  Zeros where there are none (from `left` on, or without ok).
 template <typename T>
-__device__ __forceinline__ void fetch_chunk(Vec<T, 8> *slot, const void *base, long long stride,
-                                            long long row, int c, int left, bool ok, int unit) {
-    const char *at = (const char *)((const T *)base + row * stride + c);
+__device__ __forceinline__ void fetch_chunk(Vec<T, 8> *slot, const void *base, const T *from, int left,
+                                            bool ok, int unit) {
+    const char *at = (const char *)from;  // (not looked at unless ok; base is any address that may be)
     constexpr int E = sizeof(T);
     const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot);
     if (unit == 16) {

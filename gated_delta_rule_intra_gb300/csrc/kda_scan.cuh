@@ -154,8 +154,7 @@ __device__ __forceinline__ Vec<T, 8> load_chunk(const void *base, long long stri
 }
 template <typename T> __device__ __forceinline__ float2 pair(const Vec<T, 8> &x, int i) { return x.two(2 * i); }
 template <typename T> __device__ __forceinline__ void put_pair(Vec<T, 8> &x, int i, float2 v) {
-    x.v[2 * i] = from_f32<T>(v.x);
-    x.v[2 * i + 1] = from_f32<T>(v.y);
+    x.put(2 * i, v);
 }
 __device__ __forceinline__ float2 sigmoid2(float2 x) { return make_float2(sigmoid(x.x), sigmoid(x.y)); }
 

@@ -283,10 +283,10 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
             const int t = qt + x * kStep;
             const bool ok = t < kTile && t < rows;
             const long long row = ok ? row_of(i) + t : 0;
-            if (!ENDS) fetch_chunk<T>(&raw[0][x][tid], a.u, a.u_stride, row, qc, left, ok, unit);
-            fetch_chunk<T>(&raw[1][x][tid], a.delta, a.delta_stride, row, qc, left, ok, unit);
-            fetch_chunk<T>(&raw[2][x][tid], a.dy, a.dy_stride, row, qc, left, ok, unit);
-            if (a.z) fetch_chunk<T>(&raw[3][x][tid], a.z, a.z_stride, row, qc, left, ok, unit);
+            if (!ENDS) fetch_chunk<T>(&raw[0][x][tid], a.u, (const T *)a.u + row * a.u_stride + qc, left, ok, unit);
+            fetch_chunk<T>(&raw[1][x][tid], a.delta, (const T *)a.delta + row * a.delta_stride + qc, left, ok, unit);
+            fetch_chunk<T>(&raw[2][x][tid], a.dy, (const T *)a.dy + row * a.dy_stride + qc, left, ok, unit);
+            if (a.z) fetch_chunk<T>(&raw[3][x][tid], a.z, (const T *)a.z + row * a.z_stride + qc, left, ok, unit);
         }
         cp_async_commit();
     };

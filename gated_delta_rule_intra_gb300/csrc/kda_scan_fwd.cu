@@ -156,9 +156,9 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
             const int t = qt + i * kStep;
             const bool ok = t < kTile && t < rows;
             const long long row = ok ? first + tile * kTile + t : 0;
-            fetch_chunk<T>(&raw[0][i][tid], a.u, a.u_stride, row, qc, left, ok, unit);
-            fetch_chunk<T>(&raw[1][i][tid], a.delta, a.delta_stride, row, qc, left, ok, unit);
-            if (!ENDS && a.z) fetch_chunk<T>(&raw[2][i][tid], a.z, a.z_stride, row, qc, left, ok, unit);
+            fetch_chunk<T>(&raw[0][i][tid], a.u, (const T *)a.u + row * a.u_stride + qc, left, ok, unit);
+            fetch_chunk<T>(&raw[1][i][tid], a.delta, (const T *)a.delta + row * a.delta_stride + qc, left, ok, unit);
+            if (!ENDS && a.z) fetch_chunk<T>(&raw[2][i][tid], a.z, (const T *)a.z + row * a.z_stride + qc, left, ok, unit);
         }
         cp_async_commit();
     };
