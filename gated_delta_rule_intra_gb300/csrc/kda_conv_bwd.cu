@@ -16,19 +16,22 @@ namespace kda {
 namespace conv {
 namespace {
 
-template <typename T, int W> struct Smem {
+template <typename T, int W, bool ODD> struct Smem {
+    using S = Shape<T, ODD>;
     static constexpr int kDy = kPiece + W - 1, kX = kDy + W - 1;
-    T x[2][kX][Shape<T>::CH], dy[2][kDy][Shape<T>::CH];
-    float w[W + 1][Shape<T>::CH], red[Shape<T>::kRuns][Shape<T>::CH];
+    char x[2][kX][S::kRow], dy[2][kDy][S::kRow];
+    float w[W + 1][S::CH], red[S::kRuns][S::CH];
+    T dx[kPiece][S::CH];  // only where dx's rows are on no boundary of V elements
 };
 
-template <typename T, int W>
+template <typename T, int W, bool ODD>
 __global__ void __launch_bounds__(kThreads, 3)
     kda_conv_bwd_kernel(const ConvArgs a, long long pieces, int unit_x, int unit_dy, int unit_dx) {
     wait_for_previous();
-    using S = Shape<T>;
+    using S = Shape<T, ODD>;
+    using M = Smem<T, W, ODD>;
     extern __shared__ __align__(16) char smem[];
-    Smem<T, W> &s = *reinterpret_cast<Smem<T, W> *>(smem);
+    M &s = *reinterpret_cast<M *>(smem);
     const int tid = threadIdx.x, lane = tid % S::LANES, run = tid / S::LANES;
     const int c0 = blockIdx.x * S::CH, c = c0 + lane * V, left = a.D - c;
     const bool wide = unit_dx >= (int)(V * sizeof(T));
@@ -40,10 +43,9 @@ __global__ void __launch_bounds__(kThreads, 3)
     // x from W - 1 rows in front of a piece to W - 1 behind it, dy from its first token on
     auto fetch = [&](const Piece &p, int stage) {
         if (p.len > 0) {
-            const int end = p.begin + p.len + W - 1, r = tid / S::kChunks, e = tid % S::kChunks * 8;
-            fetch_inputs<T, W>(s.x[stage], a, p, end, c0, unit_x);
-            fetch_rows<T>((T(*)[S::CH])&s.dy[stage][r][e], a, p, a.dy, a.dy_stride, p.begin + r, end, c0 + e,
-                          a.D - c0 - e, unit_dy);
+            const int end = p.begin + p.len + W - 1;
+            fetch_inputs<T, W, ODD>(s.x[stage][0], a, p, end, c0, unit_x);
+            fetch_rows<T, ODD>(s.dy[stage][0], a, p, a.dy, a.dy_stride, p.begin, end, c0, unit_dy);
         }
         cp_async_commit();
     };
@@ -67,21 +69,30 @@ __global__ void __launch_bounds__(kThreads, 3)
         __syncthreads();
         const int r0 = run * S::kRun, t0 = p.begin + r0, n = min(S::kRun, p.len - r0);
         if (n > 0 && left > 0) {
-            const T *xs = &s.x[b][r0][lane * V], *ys = &s.dy[b][r0][lane * V];
+            const char *xs = s.x[b][r0] + lane * V * sizeof(T), *ys = s.dy[b][r0] + lane * V * sizeof(T);
+            int xbits[2] = {}, ybits[2] = {};  // of rows an even and an odd number behind the first one
+            if (ODD) {
+                const long long ex = (p.row0 + t0 - (W - 1)) * a.x_stride + c0, ey = (p.row0 + t0) * a.dy_stride + c0;
+                xbits[0] = 16 * shifted<T>(a.x, ex);
+                xbits[1] = 16 * shifted<T>(a.x, ex + a.x_stride);
+                ybits[0] = 16 * shifted<T>(a.dy, ey);
+                ybits[1] = 16 * shifted<T>(a.dy, ey + a.dy_stride);
+            }
             const bool fin = a.d_final && t0 + n > p.total - (W - 1);  // of the last inputs
             // whole: every token is in the sequence, the W - 1 behind the run too
             auto walk = [&](auto whole) {
                 float xw[W][V], gw[W][V];  // input and g of step i are at i % W
-                T *out = (T *)a.dx + (p.row0 + t0) * a.dx_stride + c;
+                T *out = wide ? (T *)a.dx + (p.row0 + t0) * a.dx_stride + c : &s.dx[r0][lane * V];
+                const long long step = wide ? a.dx_stride : S::CH;
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j)  // steps -(W - 1) .. -1
-                    widen(xw[(j + 1) % W], *(const Vec<T, V> *)(xs + j * S::CH));
+                    widen(xw[(j + 1) % W], take<T, ODD>(xs + j * S::kRow, xbits[j & 1]));
 #pragma unroll
                 for (int i = 0; i < S::kRun + W - 1; ++i) {  // token t0 + i
                     if (!whole && i >= n + W - 1) break;
                     float(&x)[V] = xw[i % W], (&g)[V] = gw[i % W];
-                    widen(x, *(const Vec<T, V> *)(xs + (i + W - 1) * S::CH));
-                    widen(g, *(const Vec<T, V> *)(ys + i * S::CH));
+                    widen(x, take<T, ODD>(xs + (i + W - 1) * S::kRow, xbits[(i + W - 1) & 1]));
+                    widen(g, take<T, ODD>(ys + i * S::kRow, ybits[i & 1]));
                     if (a.act == ACT_SILU) {
                         float pre[V];
 #pragma unroll
@@ -128,8 +139,8 @@ __global__ void __launch_bounds__(kThreads, 3)
                     Vec<T, V> y;
                     narrow(y, dx);
                     if (dbg_ok(a.dbg, (size_t)(p.row0 + pos), (size_t)a.tok.rows(), DBG_STORE))
-                        store_channels(out, y, left, wide);
-                    out += a.dx_stride;
+                        *(Vec<T, V> *)out = y;
+                    out += step;
                 }
             };
             if (n == S::kRun && t0 + n + W - 1 <= p.total)
@@ -138,6 +149,7 @@ __global__ void __launch_bounds__(kThreads, 3)
                 walk(std::false_type());
         }
         __syncthreads();
+        if (!wide && p.len > 0) leave_rows<T, S::CH>(s.dx, a, p, a.dx, a.dx_stride, c0);
     }
     cp_async_wait_newest<0>();
     if (!a.dweight) return;
@@ -214,28 +226,35 @@ template <typename T> __global__ void __launch_bounds__(256) kda_conv_initial_ke
     }
 }
 
-template <typename T, int W> cudaError_t backward(const ConvArgs &a, cudaStream_t stream) {
-    const unsigned blocks = (unsigned)((a.D + Shape<T>::CH - 1) / Shape<T>::CH);
+template <typename T, int W, bool ODD>
+cudaError_t backward(const ConvArgs &a, int unit_x, int unit_dy, int unit_dx, cudaStream_t stream) {
+    using M = Smem<T, W, ODD>;
+    const unsigned blocks = (unsigned)((a.D + M::S::CH - 1) / M::S::CH);
     const long long pieces = a.tok.pieces(kPiece);
-    ConvArgs b = a;  // as many rows of sums as CTAs: one wave, of three a multiprocessor
-    const long long most = 3 * kSMs / (long long)blocks > 1 ? 3 * kSMs / (long long)blocks : 1;
+    constexpr int kBytes = sizeof(M);
+    const int bytes = unit_dx >= (int)(V * sizeof(T)) ? kBytes - (int)sizeof(M::dx) : kBytes;
+    ConvArgs b = a;  // as many rows of sums as CTAs: one wave
+    const long long wave = resident(bytes, 3) * kSMs / blocks, most = wave > 1 ? wave : 1;
     const long long rows = pieces < most ? pieces : most;
     if (rows < b.partials || !a.dweight) b.partials = (int)rows;
-    rows::Unit x(sizeof(T), a.D), dy(sizeof(T), a.D), dx(sizeof(T), a.D);
-    x.add(a.x, a.x_stride);
-    x.add(a.initial, a.D);
-    dy.add(a.dy, a.dy_stride);
-    dx.add(a.dx, a.dx_stride);
-    constexpr int kBytes = sizeof(Smem<T, W>);
     static volatile int done[kMaxDev];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = smem_limit_once(kda_conv_bwd_kernel<T, W>, kBytes, dev, done);
+    if (e == cudaSuccess) e = smem_limit_once(kda_conv_bwd_kernel<T, W, ODD>, kBytes, dev, done);
     if (e != cudaSuccess) return e;
-    e = launch_early(kda_conv_bwd_kernel<T, W>, dim3(blocks, (unsigned)b.partials), kThreads, kBytes, stream, b,
-                     pieces, x.unit, dy.unit, dx.unit);
+    e = launch_early(kda_conv_bwd_kernel<T, W, ODD>, dim3(blocks, (unsigned)b.partials), kThreads, bytes, stream, b,
+                     pieces, unit_x, unit_dy, unit_dx);
     if (e != cudaSuccess || !a.dweight) return e;
     return launch_early(kda_conv_sum_kernel, (unsigned)(((long long)(W + 1) * a.D + 255) / 256), 256, 0, stream, b);
+}
+template <typename T, int W> cudaError_t backward(const ConvArgs &a, cudaStream_t stream) {
+    rows::Unit x(sizeof(T), 16), dy(sizeof(T), 16), dx(sizeof(T), a.D);
+    x.add(a.x, a.x_stride);
+    dy.add(a.dy, a.dy_stride);
+    dx.add(a.dx, a.dx_stride);
+    if constexpr (sizeof(T) == 2)
+        if (x.unit < 4 || dy.unit < 4) return backward<T, W, true>(a, x.unit, dy.unit, dx.unit, stream);
+    return backward<T, W, false>(a, x.unit, dy.unit, dx.unit, stream);
 }
 template <typename T> cudaError_t backward(const ConvArgs &a, cudaStream_t stream) {
     if (a.d_initial) {

@@ -13,18 +13,21 @@ namespace {
 
 constexpr int kStages = 3;
 
-template <typename T, int W> struct Smem {
-    T x[kStages][kPiece + W - 1][Shape<T>::CH];
-    float w[W + 1][Shape<T>::CH];
+template <typename T, int W, bool ODD> struct Smem {
+    using S = Shape<T, ODD>;
+    char x[kStages][kPiece + W - 1][S::kRow];
+    float w[W + 1][S::CH];
+    T y[kPiece][S::CH];  // only where y's rows are on no boundary of V elements
 };
 
-template <typename T, int W>
+template <typename T, int W, bool ODD>
 __global__ void __launch_bounds__(kThreads, 4)
     kda_conv_fwd_kernel(const ConvArgs a, long long pieces, int unit_x, int unit_y) {
     wait_for_previous();
-    using S = Shape<T>;
+    using S = Shape<T, ODD>;
+    using M = Smem<T, W, ODD>;
     extern __shared__ __align__(16) char smem[];
-    Smem<T, W> &s = *reinterpret_cast<Smem<T, W> *>(smem);
+    M &s = *reinterpret_cast<M *>(smem);
     const int lane = threadIdx.x % S::LANES, run = threadIdx.x / S::LANES;
     const int c0 = blockIdx.x * S::CH, c = c0 + lane * V, left = a.D - c;
     const bool wide = unit_y >= (int)(V * sizeof(T));
@@ -34,7 +37,7 @@ __global__ void __launch_bounds__(kThreads, 4)
         return at < pieces ? find_piece(a.tok, at, kPiece) : p;
     };
     auto fetch = [&](const Piece &p, int stage) {
-        if (p.len >= 0) fetch_inputs<T, W>(s.x[stage], a, p, p.begin + p.len, c0, unit_x);
+        if (p.len >= 0) fetch_inputs<T, W, ODD>(s.x[stage][0], a, p, p.begin + p.len, c0, unit_x);
         cp_async_commit();
     };
     load_params<W>(a, c0, s.w);
@@ -57,16 +60,23 @@ __global__ void __launch_bounds__(kThreads, 4)
         __syncthreads();
         const int r0 = run * S::kRun, n = p.len - r0;
         if (n > 0 && left > 0) {
-            const T *xs = &s.x[b][r0][lane * V];
-            T *out = (T *)a.y + (p.row0 + p.begin + r0) * a.y_stride + c;
+            const char *xs = s.x[b][r0] + lane * V * sizeof(T);
+            int bits[2] = {};  // of rows an even and an odd number behind the run's first one
+            if (ODD) {
+                const long long e = (p.row0 + p.begin + r0 - (W - 1)) * a.x_stride + c0;
+                bits[0] = 16 * shifted<T>(a.x, e);
+                bits[1] = 16 * shifted<T>(a.x, e + a.x_stride);
+            }
+            T *out = wide ? (T *)a.y + (p.row0 + p.begin + r0) * a.y_stride + c : &s.y[r0][lane * V];
+            const long long step = wide ? a.y_stride : S::CH;
             auto walk = [&](auto whole) {
                 float x[W][V];  // the input of token i is at i % W
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) widen(x[(j + 1) % W], *(const Vec<T, V> *)(xs + j * S::CH));
+                for (int j = 0; j < W - 1; ++j) widen(x[(j + 1) % W], take<T, ODD>(xs + j * S::kRow, bits[j & 1]));
 #pragma unroll
                 for (int i = 0; i < S::kRun; ++i) {
                     if (!whole && i >= n) break;
-                    widen(x[i % W], *(const Vec<T, V> *)(xs + (i + W - 1) * S::CH));
+                    widen(x[i % W], take<T, ODD>(xs + (i + W - 1) * S::kRow, bits[(i + W - 1) & 1]));
                     float acc[V];
 #pragma unroll
                     for (int e = 0; e < V; ++e) acc[e] = bias[e];
@@ -79,8 +89,8 @@ __global__ void __launch_bounds__(kThreads, 4)
                     Vec<T, V> y;
                     narrow(y, acc);
                     if (dbg_ok(a.dbg, (size_t)(p.row0 + p.begin + r0 + i), (size_t)a.tok.rows(), DBG_STORE))
-                        store_channels(out, y, left, wide);
-                    out += a.y_stride;
+                        *(Vec<T, V> *)out = y;
+                    out += step;
                 }
             };
             if (n >= S::kRun)
@@ -92,11 +102,14 @@ __global__ void __launch_bounds__(kThreads, 4)
             for (int i = threadIdx.x; i < (W - 1) * S::CH; i += kThreads) {
                 const int r = i / S::CH, e = i % S::CH;
                 const size_t row = (size_t)p.seq * (W - 1) + r;
+                const long long at = (p.row0 + p.total - (W - 1) + r) * a.x_stride + c0;
                 if (c0 + e < a.D && dbg_ok(a.dbg, row, (size_t)a.tok.num_seqs * (W - 1), DBG_STORE))
-                    ((T *)a.final)[row * a.D + c0 + e] = s.x[b][p.len + r][e];
+                    ((T *)a.final)[row * a.D + c0 + e] =
+                        ((const T *)s.x[b][p.len + r])[(ODD ? shifted<T>(a.x, at) : 0) + e];
             }
         }
         __syncthreads();
+        if (!wide && p.len > 0) leave_rows<T, S::CH>(s.y, a, p, a.y, a.y_stride, c0);
         p = p1;
         p1 = p2;
         b = b + 1 < kStages ? b + 1 : 0;
@@ -133,22 +146,29 @@ __global__ void __launch_bounds__(256) kda_conv_step_kernel(const ConvArgs a) {
         *reinterpret_cast<Vec<T, V> *>((T *)a.y + n * a.y_stride + c) = y;
 }
 
-template <typename T, int W> cudaError_t forward(const ConvArgs &a, cudaStream_t stream) {
+template <typename T, int W, bool ODD>
+cudaError_t forward(const ConvArgs &a, int unit_x, int unit_y, cudaStream_t stream) {
+    using M = Smem<T, W, ODD>;
     const long long pieces = a.tok.pieces(kPiece);
-    const unsigned blocks = (unsigned)((a.D + Shape<T>::CH - 1) / Shape<T>::CH);
-    const long long most = 4 * kSMs / (long long)blocks > 1 ? 4 * kSMs / (long long)blocks : 1;  // one wave
-    rows::Unit x(sizeof(T), a.D), y(sizeof(T), a.D);
-    x.add(a.x, a.x_stride);
-    x.add(a.initial, a.D);
-    y.add(a.y, a.y_stride);
-    constexpr int kBytes = sizeof(Smem<T, W>);
+    const unsigned blocks = (unsigned)((a.D + M::S::CH - 1) / M::S::CH);
+    constexpr int kBytes = sizeof(M);
+    const int bytes = unit_y >= (int)(V * sizeof(T)) ? kBytes - (int)sizeof(M::y) : kBytes;
+    const long long wave = resident(bytes, 4) * kSMs / blocks, most = wave > 1 ? wave : 1;
     static volatile int done[kMaxDev];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = smem_limit_once(kda_conv_fwd_kernel<T, W>, kBytes, dev, done);
+    if (e == cudaSuccess) e = smem_limit_once(kda_conv_fwd_kernel<T, W, ODD>, kBytes, dev, done);
     if (e != cudaSuccess) return e;
-    return launch_early(kda_conv_fwd_kernel<T, W>, dim3(blocks, (unsigned)(pieces < most ? pieces : most)), kThreads,
-                        kBytes, stream, a, pieces, x.unit, y.unit);
+    return launch_early(kda_conv_fwd_kernel<T, W, ODD>, dim3(blocks, (unsigned)(pieces < most ? pieces : most)),
+                        kThreads, bytes, stream, a, pieces, unit_x, unit_y);
+}
+template <typename T, int W> cudaError_t forward(const ConvArgs &a, cudaStream_t stream) {
+    rows::Unit x(sizeof(T), 16), y(sizeof(T), a.D);  // (the last channels of a row may be part of a word)
+    x.add(a.x, a.x_stride);
+    y.add(a.y, a.y_stride);
+    if constexpr (sizeof(T) == 2)
+        if (x.unit < 4) return forward<T, W, true>(a, x.unit, y.unit, stream);
+    return forward<T, W, false>(a, x.unit, y.unit, stream);
 }
 template <typename T> cudaError_t forward(const ConvArgs &a, cudaStream_t stream) {
     return a.W == 4 ? forward<T, 4>(a, stream) : a.W == 3 ? forward<T, 3>(a, stream) : forward<T, 2>(a, stream);

@@ -91,10 +91,17 @@ __device__ __forceinline__ Piece find_piece(const Tokens &t, long long p, int si
         x.total = t.T;
     } else {
         auto token = [&](int v) { return v < 0 ? 0 : v > t.T ? t.T : v; };
-        int lo = 0, hi = t.num_seqs - 1;
-        while (lo < hi) {  // the last sequence whose pieces begin at or before this one
-            const int mid = (lo + hi + 1) >> 1;
-            if (token(t.cu_seqlens[mid]) / size + mid <= p) lo = mid; else hi = mid - 1;
+        // the last sequence whose pieces begin at or before this one, by 32 of them at a time: a step
+        // waits for memory once
+        int lo = 0, n = t.num_seqs;
+        const int lane = threadIdx.x & 31;
+        while (n > 1) {
+            const int step = (n + 31) / 32, at = lo + lane * step;
+            const bool before = lane * step < n && (lane == 0 || token(t.cu_seqlens[at]) / size + at <= p);
+            const unsigned mask = __ballot_sync(0xffffffffu, before);
+            const int last = mask == 0xffffffffu ? 31 : __ffs(~mask) - 2;
+            lo += last * step;
+            n = min(step, n - last * step);
         }
         const int a = token(t.cu_seqlens[lo]), b = token(t.cu_seqlens[lo + 1]);
         x.seq = lo;
