@@ -183,14 +183,21 @@ def _declare_quick(lib):
             ("chunk_bwd", ("kda_chunk_bwd", "kda_chunk_saved_bytes",
                            "kda_chunk_bwd_workspace_bytes")),
             ("layer_norm_fwd", ("kda_layer_norm_fwd",)),
-            ("layer_norm_bwd", ("kda_layer_norm_bwd", "kda_layer_norm_bwd_workspace_bytes"))):
+            ("layer_norm_bwd", ("kda_layer_norm_bwd", "kda_layer_norm_bwd_workspace_bytes")),
+            ("conv_fwd", ("kda_conv_fwd",)),
+            ("conv_bwd", ("kda_conv_bwd", "kda_conv_bwd_workspace_bytes")),
+            ("conv_step", ("kda_conv_step",)),
+            ("scan_fwd", ("kda_scan_fwd", "kda_scan_saved_bytes", "kda_scan_fwd_workspace_bytes")),
+            ("scan_bwd", ("kda_scan_bwd", "kda_scan_saved_bytes", "kda_scan_bwd_workspace_bytes")),
+            ("scan_step", ("kda_scan_step",)),
+            ("linear_fwd", ("kda_linear_fwd", "kda_linear_copies", "kda_linear_fwd_workspace_bytes")),
+            ("linear_bwd", ("kda_linear_bwd", "kda_linear_copies",
+                            "kda_linear_bwd_workspace_bytes"))):
         setattr(lib, "quick_" + name, quick(name, fns))
-    for name in ("conv_fwd", "conv_bwd", "conv_step", "scan_fwd", "scan_step", "linear_fwd"):
-        setattr(lib, "quick_" + name, lambda *a: None)
 
 
 @functools.cache
 def _without_native(why):
-    warnings.warn("_native.so is missing or of another torch: small calls of the recurrence, the "
-                  "single-token form and layer norm take longer on the host; build it with "
+    warnings.warn("_native.so is missing or of another torch: small calls of all but the "
+                  "intra-chunk functions take longer on the host; build it with "
                   f"gated_delta_rule_intra_gb300.build.build_native() ({why})", RuntimeWarning)

@@ -72,9 +72,9 @@ def kda_conv_fwd(x, weight, bias=None, initial_state=None, *, activation=None,
     None unless ``output_final_state``.  ``cu_seqlens`` (int32 [N + 1] on the device, B = 1) packs N
     sequences along T; y is zero at tokens in no sequence when it is allocated here.
     """
-    if stream is None and cu_seqlens is None and y is None:
-        out = library().quick_conv_fwd(x, weight, bias, initial_state, activation == "silu",
-                                       output_final_state) if activation in _ALLOWED else None
+    if stream is None and y is None and activation in _ALLOWED:
+        out = library().quick_conv_fwd(x, weight, bias, initial_state, activation is not None,
+                                       output_final_state, cu_seqlens)
         if out is not None:
             return out
     return _conv_fwd(x, weight, bias, initial_state, activation, output_final_state, cu_seqlens, y,
@@ -117,9 +117,9 @@ def kda_conv_bwd(dy, x, weight, bias=None, initial_state=None, d_final_state=Non
     in a fixed order (None unless ``param_grads``).  d_final_state (None: zeros) and d_initial_state
     (None unless ``output_d_initial_state``) are like the states.
     """
-    if (stream is None and cu_seqlens is None and initial_state is None and d_final_state is None
+    if (stream is None and initial_state is None and d_final_state is None
             and not output_d_initial_state and dx is None and param_grads and activation in _ALLOWED):
-        out = library().quick_conv_bwd(dy, x, weight, bias, activation == "silu")
+        out = library().quick_conv_bwd(dy, x, weight, bias, activation is not None, cu_seqlens)
         if out is not None:
             return out
     return _conv_bwd(dy, x, weight, bias, initial_state, d_final_state, activation,
@@ -173,7 +173,7 @@ def kda_conv_step(x, state, weight, bias=None, *, activation=None, state_indices
     no two rows may name one state.
     """
     if stream is None and y is None and activation in _ALLOWED:
-        out = library().quick_conv_step(x, state, weight, bias, activation == "silu", state_indices)
+        out = library().quick_conv_step(x, state, weight, bias, activation is not None, state_indices)
         if out is not None:
             return out
     return _conv_step(x, state, weight, bias, activation, state_indices, y, stream=stream)

@@ -102,6 +102,11 @@ def kda_linear_bwd(dy, x, weight, saved=None, *, activation=None, input_grad=Tru
     from FP32 sums in a fixed order (None where not wanted).  x and weight as given to the forward,
     dy like its y, ``saved`` what it returned with ``save=True``.  residual's gradient is dy itself.
     """
+    if stream is None and dx is None and activation in ACTIVATIONS:
+        out = library().quick_linear_bwd(dy, x, weight, saved, ACTIVATIONS[activation], input_grad,
+                                         weight_grad, bias_grad)
+        if out is not None:
+            return out
     return _linear_bwd(dy, x, weight, saved, activation, input_grad, weight_grad, bias_grad, dx,
                        stream=stream)
 

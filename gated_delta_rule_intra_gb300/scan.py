@@ -93,9 +93,9 @@ def kda_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, initial_sta
     element a token and channel), None unless ``save``.  ``cu_seqlens`` (int32 [N + 1] on the device, B = 1) packs
     sequences along T; y is zero at tokens in no sequence when it is allocated here.
     """
-    if stream is None and cu_seqlens is None and y is None and delta_softplus:
+    if stream is None and y is None and delta_softplus:
         out = library().quick_scan_fwd(u, delta, A, B, C, D, z, delta_bias, initial_state,
-                                       output_final_state, save)
+                                       output_final_state, save, cu_seqlens)
         if out is not None:
             return out
     return _scan_fwd(u, delta, A, B, C, D, z, delta_bias, initial_state, delta_softplus,
@@ -149,6 +149,11 @@ def kda_scan_bwd(dy, u, delta, A, B, C, saved, D=None, z=None, delta_bias=None, 
     the forward had none; d_final_state (fp32, None: zeros) and d_initial_state (None unless
     ``output_d_initial_state``) are like the states.  Deterministic.
     """
+    if (stream is None and d_final_state is None and delta_softplus
+            and not output_d_initial_state):
+        out = library().quick_scan_bwd(dy, u, delta, A, B, C, saved, D, z, delta_bias, cu_seqlens)
+        if out is not None:
+            return out
     return _scan_bwd(dy, u, delta, A, B, C, saved, D, z, delta_bias, d_final_state, delta_softplus,
                      output_d_initial_state, cu_seqlens, stream=stream)
 
