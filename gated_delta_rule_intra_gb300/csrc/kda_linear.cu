@@ -1,12 +1,17 @@
 // Matrix product with its epilogue on the tensor cores: C = A B^T, y = act(C + bias) + residual.
 //
-// Persistent, one CTA an SM, by role: one warp asks for the operands' tiles (TMA, 128-byte swizzle,
-// [128 x 64] of A and [BN x 64] of B a stage), one issues the products (tcgen05.mma, M = 128, N =
-// BN, accumulators in tensor memory), four take the accumulators out and finish them.  There are
-// two accumulators, so that a tile's products run while the one before it is finished.  Operands
-// may lie either way round: contracted along their rows' direction (K-major, boxes of 64 k) or
-// across it (MN-major, boxes of 64 columns x 64 k), which is what the gradients need of the
-// same tensors.  Where the tiles of C are too few for the card, the contraction is cut into parts
+// Persistent, by role: one warp asks for the operands' tiles (TMA, 128-byte swizzle, 64 of K a stage),
+// one issues the products (tcgen05.mma, accumulators in tensor memory), four take the accumulators out
+// and finish them.  There are two accumulators, so that a tile's products run while the one before it
+// is finished.  Operands may lie either way round: contracted along their rows' direction (K-major,
+// boxes of 64 k) or across it (MN-major, boxes of 64 columns x 64 k), which is what the gradients need
+// of the same tensors.
+//
+// Large products take pairs of CTAs on neighbouring multiprocessors (cta_group::2): a tile of 256 x 256,
+// each CTA holding 128 rows of A, 128 of B's rows and 128 of the accumulator's, and the first one's
+// thread issuing products that read both's shared memory.  Alone, a CTA's tile of 128 x 256 fetches and
+// reads half as much again a product, and shared memory is what runs out (B = 32768 x 2048 x 8192:
+// 729 us alone).  Where the tiles of C are too few for the card, the contraction is cut into parts
 // whose sums a second kernel joins, always in the same order.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -24,9 +29,11 @@ constexpr int BM = 128, BK = 64;
 constexpr int kThreads = 192;              // warps: copies, products, 4 of the epilogue
 constexpr uint32_t kWaitPolls = 1u << 22;  // then the kernel gives up (and writes NaN)
 
-template <int BN> struct Cfg {
-    static constexpr int kA = BM * BK * 2, kB = BN * BK * 2, kStage = kA + kB;
-    static constexpr int kStages = BN == 256 ? 4 : 6;
+// BN: columns of a tile.  PAIR: of two CTAs, each with half of the rows of A and of B.
+template <int BN, bool PAIR> struct Cfg {
+    static constexpr int kRowsB = PAIR ? BN / 2 : BN;  // of B in this CTA
+    static constexpr int kA = BM * BK * 2, kB = kRowsB * BK * 2, kStage = kA + kB;
+    static constexpr int kStages = kStage > 32768 ? 4 : 6;
     static constexpr int kOut = 4 * 4096;  // a [32 rows x 64 columns] box of each epilogue warp
     static constexpr int kBias = 4 * BN * 4;
     static constexpr int kBytes = 1024 + kStages * kStage + kOut + kBias + 256;
@@ -55,23 +62,102 @@ __device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lbo, uint32_
     return tc::smem_desc(addr, lbo, sbo) | (uint64_t)2 << 61;
 }
 // FP32 sums of 16-bit operands.
-constexpr uint32_t idesc16(bool fp16, bool a_mn, bool b_mn, int n) {
+constexpr uint32_t idesc16(bool fp16, bool a_mn, bool b_mn, int m, int n) {
     return 1u << 4 | (fp16 ? 0u : 1u) << 7 | (fp16 ? 0u : 1u) << 10 | (uint32_t)a_mn << 15 |
-           (uint32_t)b_mn << 16 | (uint32_t)(n >> 3) << 17 | (uint32_t)(BM >> 4) << 24;
+           (uint32_t)b_mn << 16 | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
 }
+template <bool PAIR>
 __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+            : "memory");
+}
+// Arrives on the barrier (of a pair: on both CTAs') when this thread's products so far are done.
+template <bool PAIR> __device__ __forceinline__ void commit(uint64_t *bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                tc::smem_u32(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        tc::mma_commit(bar);
+}
+// A pair's copies all report to the first CTA's barrier; `bar` is its address in the cluster then.
+template <bool PAIR>
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+}
+template <bool PAIR> __device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t columns) {
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(slot)),
+                     "r"(columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        tc::tmem_alloc(slot, columns);
+    }
+}
+template <bool PAIR> __device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns) : "memory");
+    else
+        tc::tmem_dealloc(at, columns);
+}
+// Bounded wait as tc::mbar_wait, with what the pair's other CTA did before it arrived.
+__device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t parity, uint32_t polls) {
+    const uint32_t a = tc::smem_u32(bar);
+    for (uint32_t i = 0; i < polls; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            "selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(done)
+            : "r"(a), "r"(parity)
+            : "memory");
+        if (done) return true;
+    }
+    return false;
+}
+// Arrives on the first CTA's barrier.
+__device__ __forceinline__ void arrive_first(uint64_t *bar) {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %0, 0;\n"
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(tc::smem_u32(bar))
         : "memory");
 }
-__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(tc::smem_u32(bar))
-        : "memory");
+__device__ __forceinline__ uint32_t in_first(uint64_t *bar) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(tc::smem_u32(bar)));
+    return a;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
 }
 __device__ __forceinline__ void store_2d(const CUtensorMap *map, uint32_t src, int x, int y) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
@@ -97,11 +183,11 @@ struct Tile {
 };
 // Tiles go down 16 rows of tiles before the next column, so that those at work at one time share
 // both operands' tiles in L2.
-__device__ __forceinline__ Tile tile_of(const Params &p, int i, int BN) {
+__device__ __forceinline__ Tile tile_of(const Params &p, int i, int rows_each, int BN) {
     Tile t;
     const int s = i / p.tiles, j = i - s * p.tiles, mt = p.tiles / p.nt;
     const int group = j / (16 * p.nt), rows = min(16, mt - group * 16), r = j - group * 16 * p.nt;
-    t.m = (group * 16 + r % rows) * BM;
+    t.m = (group * 16 + r % rows) * rows_each;
     t.n = r / rows * BN;
     t.kb = s * p.per;
     t.ke = min(t.kb + p.per, (p.K + BK - 1) / BK);
@@ -127,6 +213,7 @@ template <typename T>
 __device__ __forceinline__ void box_out(const char *box, void *base, long long ld, int m, int n, int M,
                                         int N, int lane, bool pair) {
     const int rows = min(32, M - m);
+#pragma unroll 8
     for (int r = 0; r < rows; ++r) {
         const uint32_t x = *(const uint32_t *)(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
         uint16_t *to = (uint16_t *)base + (size_t)(m + r) * ld + n + 2 * lane;
@@ -139,7 +226,7 @@ __device__ __forceinline__ void box_out(const char *box, void *base, long long l
     }
 }
 __device__ __forceinline__ void box_in(char *box, const void *base, long long ld, int m, int n, int M,
-                                       int N, int lane, bool wide) {
+                                       int N, int lane, bool wide, bool pair) {
     const int rows = min(32, M - m);
     if (wide) {  // eight lanes a row, 16 bytes each
 #pragma unroll
@@ -151,20 +238,39 @@ __device__ __forceinline__ void box_in(char *box, const void *base, long long ld
         }
         return;
     }
-    for (int r = 0; r < rows; ++r) {
-        const uint16_t *at = (const uint16_t *)base + (size_t)(m + r) * ld + n + 2 * lane;
-        uint32_t x = 0;
-        if (n + 2 * lane < N) x = at[0];
-        if (n + 2 * lane + 1 < N) x |= (uint32_t)at[1] << 16;
-        *(uint32_t *)(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) = x;
+    // sixteen rows at a time: each batch waits for memory once
+    const int c = n + 2 * lane;
+    const uint16_t *at = (const uint16_t *)base + (size_t)m * ld + c;
+#pragma unroll
+    for (int r0 = 0; r0 < 32; r0 += 16) {
+        uint32_t x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            x[i] = 0;
+            const uint16_t *f = at + (size_t)(r0 + i) * ld;
+            if (r0 + i < rows && c < N) {
+                if (pair && c + 1 < N) {
+                    x[i] = *(const uint32_t *)f;
+                } else {
+                    x[i] = f[0];
+                    if (c + 1 < N) x[i] |= (uint32_t)f[1] << 16;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int r = r0 + i;
+            *(uint32_t *)(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) = x[i];
+        }
     }
 }
 
-template <typename T, bool A_MN, bool B_MN, int BN>
+template <typename T, bool A_MN, bool B_MN, int BN, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     kda_linear_kernel(const __grid_constant__ Maps maps, const Params p) {
     wait_for_previous();
-    using C = Cfg<BN>;
+    using C = Cfg<BN, PAIR>;
+    constexpr int kRows = PAIR ? 2 * BM : BM;  // of a tile
     extern __shared__ char raw[];
     char *base = (char *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     char *out = base + C::kStages * C::kStage;
@@ -175,6 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile uint32_t *broken = slot + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int work = p.tiles * p.splits;
+    const int rank = PAIR ? (int)cluster_rank() : 0;
+    const int first = PAIR ? (int)blockIdx.x / 2 : (int)blockIdx.x, step = PAIR ? (int)gridDim.x / 2 : (int)gridDim.x;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             tc::mbar_init(full + i, 1);
@@ -182,18 +290,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(done + i, 1);
-            tc::mbar_init(taken + i, 4);
+            tc::mbar_init(taken + i, PAIR ? 8 : 4);
         }
         *broken = 0;
     }
-    if (warp == 1) tc::tmem_alloc(slot, C::kColumns);
+    if (warp == 1) tmem_alloc<PAIR>(slot, C::kColumns);
     __syncthreads();
+    if (PAIR) cluster_sync();  // both CTAs' barriers are there
     tc::fence_after_sync();
     const uint32_t tmem = *slot;
     // A wait that gives up ends this CTA's work; the other warps learn of it here.
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (*broken) return false;
-        if (tc::mbar_wait(bar, parity, kWaitPolls)) return true;
+        if (PAIR ? wait_pair(bar, parity, kWaitPolls) : tc::mbar_wait(bar, parity, kWaitPolls)) return true;
         *broken = 1;
         dbg_flag(p.dbg, true, DBG_WAIT);
         return false;
@@ -201,42 +310,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         if (lane == 0) {
             int n = 0;  // stages filled so far
-            for (int i = blockIdx.x; i < work; i += gridDim.x) {
-                const Tile t = tile_of(p, i, BN);
+            const uint32_t bars = PAIR ? in_first(full) : tc::smem_u32(full);
+            for (int i = first; i < work; i += step) {
+                const Tile t = tile_of(p, i, kRows, BN);
                 bool ok = true;
                 for (int kb = t.kb; kb < t.ke && ok; ++kb, ++n) {
                     const int st = n % C::kStages;
                     if (n >= C::kStages && !(ok = wait(empty + st, (n / C::kStages - 1) & 1))) break;
                     const uint32_t a = tc::smem_u32(base + st * C::kStage), b = a + C::kA;
-                    tc::mbar_arrive_expect_tx(full + st, C::kStage);
+                    // (a pair's first CTA waits for both's bytes)
+                    if (!PAIR || rank == 0) tc::mbar_arrive_expect_tx(full + st, (PAIR ? 2 : 1) * C::kStage);
+                    const int m = t.m + rank * BM, nn = t.n + rank * C::kRowsB;
                     if (A_MN) {
 #pragma unroll
                         for (int x = 0; x < BM / 64; ++x)
-                            load_2d(a + x * 8192, &maps.a, t.m + 64 * x, kb * BK, full + st);
+                            load_2d<PAIR>(a + x * 8192, &maps.a, m + 64 * x, kb * BK, bars + 8 * st);
                     } else {
-                        load_2d(a, &maps.a, kb * BK, t.m, full + st);
+                        load_2d<PAIR>(a, &maps.a, kb * BK, m, bars + 8 * st);
                     }
                     if (B_MN) {
 #pragma unroll
-                        for (int x = 0; x < BN / 64; ++x)
-                            load_2d(b + x * 8192, &maps.b, t.n + 64 * x, kb * BK, full + st);
+                        for (int x = 0; x < C::kRowsB / 64; ++x)
+                            load_2d<PAIR>(b + x * 8192, &maps.b, nn + 64 * x, kb * BK, bars + 8 * st);
                     } else {
-                        load_2d(b, &maps.b, kb * BK, t.n, full + st);
+                        load_2d<PAIR>(b, &maps.b, kb * BK, nn, bars + 8 * st);
                     }
                 }
                 if (!ok) break;
             }
-            // every copy has landed before the CTA ends
-            for (int s = max(0, n - C::kStages); s < n; ++s)
+            // every copy has landed before the CTA ends (a pair's: before its first CTA does)
+            for (int s = max(0, n - C::kStages); s < n && rank == 0; ++s)
                 tc::mbar_wait(full + s % C::kStages, (s / C::kStages) & 1, kWaitPolls);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc16(std::is_same<T, __half>::value, A_MN, B_MN, BN);
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = idesc16(std::is_same<T, __half>::value, A_MN, B_MN, kRows, BN);
             constexpr uint32_t kStepA = A_MN ? 2048 : 32, kStepB = B_MN ? 2048 : 32;  // 16 of K
             int n = 0, c = 0;
-            for (int i = blockIdx.x; i < work; i += gridDim.x, ++c) {
-                const Tile t = tile_of(p, i, BN);
+            for (int i = first; i < work; i += step, ++c) {
+                const Tile t = tile_of(p, i, kRows, BN);
                 bool ok = true;
                 if (c >= 2 && !wait(taken + (c & 1), (c / 2 - 1) & 1)) break;
                 tc::fence_after_sync();
@@ -248,12 +360,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t a = tc::smem_u32(base + st * C::kStage), b = a + C::kA;
 #pragma unroll
                     for (int k = 0; k < BK / 16; ++k)
-                        mma_f16(d, desc128(a + k * kStepA, A_MN ? 8192 : 16, 1024),
+                        mma_f16<PAIR>(d, desc128(a + k * kStepA, A_MN ? 8192 : 16, 1024),
                                 desc128(b + k * kStepB, B_MN ? 8192 : 16, 1024), idesc, kb > t.kb || k > 0);
-                    tc::mma_commit(empty + st);
+                    commit<PAIR>(empty + st);
                 }
                 if (!ok) break;
-                tc::mma_commit(done + (c & 1));
+                commit<PAIR>(done + (c & 1));
             }
             // the last products are done with the stages before the CTA ends
             if (n > 0) tc::mbar_wait(empty + (n - 1) % C::kStages, ((n - 1) / C::kStages) & 1, kWaitPolls);
@@ -262,11 +374,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int e = warp - 2, quarter = warp & 3;  // a warp reads its own 32 lanes of tensor memory
         char *box = out + e * 4096;
         float *bs = bias + e * BN;
+        const bool pair_r = (uintptr_t)p.residual % 4 == 0 && p.ldr % 2 == 0;
         const bool pair = ((uintptr_t)p.y | (uintptr_t)p.pre) % 4 == 0 && (p.ldy | p.ldp) % 2 == 0;
         int c = 0;
-        for (int i = blockIdx.x; i < work; i += gridDim.x, ++c) {
-            const Tile t = tile_of(p, i, BN);
-            const int m0 = t.m + 32 * quarter, n1 = min(p.N - t.n, BN);
+        for (int i = first; i < work; i += step, ++c) {
+            const Tile t = tile_of(p, i, kRows, BN);
+            const int m0 = t.m + rank * BM + 32 * quarter, n1 = min(p.N - t.n, BN);
             if (!p.partial) {
                 __syncwarp();
                 for (int j = lane; j < BN; j += 32)
@@ -289,7 +402,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n + 64 >= n1) {  // the accumulator may be written again
                     tc::fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(taken + (c & 1));
+                    if (lane == 0) {
+                        if (PAIR)
+                            arrive_first(taken + (c & 1));
+                        else
+                            tc::mbar_arrive(taken + (c & 1));
+                    }
                 }
                 if (p.partial) {
                     const int m = m0 + lane;
@@ -354,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 activate_all(v, p.act);
                 begin();
                 if (p.residual) {
-                    box_in(box, p.residual, p.ldr, m0, t.n + n, p.M, p.N, lane, p.wide_r);
+                    box_in(box, p.residual, p.ldr, m0, t.n + n, p.M, p.N, lane, p.wide_r, pair_r);
                     __syncwarp();
                 }
                 put(p.residual);
@@ -367,8 +485,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
+    if (PAIR) cluster_sync();  // neither CTA's shared memory is wanted any more
     tc::fence_after_sync();
-    if (warp == 1) tc::tmem_dealloc(tmem, C::kColumns);
+    if (warp == 1) tmem_free<PAIR>(tmem, C::kColumns);
 }
 
 // The parts of the contraction joined, with the epilogue: a thread has four columns of a row.
@@ -419,18 +538,19 @@ cudaError_t encode(CUtensorMap *m, bool fp16, const void *base, long long cols, 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Columns of a tile, and parts of the contraction.
+// Columns of a tile, pairs or not, and parts of the contraction.
 struct Plan {
     int bn, tiles, splits, per, ldw;
+    bool pair;
 };
 Plan plan_of(int M, int N, int K) {
     Plan q;
-    const long long mt = (M + BM - 1) / BM;
-    auto tiles = [&](int bn) { return mt * ((N + bn - 1) / bn); };
-    q.bn = tiles(256) >= kSMs ? 256 : tiles(128) >= kSMs / 2 || N > 64 ? 128 : 64;
-    q.tiles = (int)tiles(q.bn);
+    auto tiles = [&](int bm, int bn) { return (long long)((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+    q.pair = tiles(256, 256) >= kSMs / 2;
+    q.bn = q.pair || tiles(BM, 256) >= kSMs ? 256 : tiles(BM, 128) >= kSMs / 2 || N > 64 ? 128 : 64;
+    q.tiles = (int)tiles(q.pair ? 2 * BM : BM, q.bn);
     const int blocks = (K + BK - 1) / BK;
-    int splits = q.tiles * 2 <= kSMs ? kSMs / q.tiles : 1;
+    int splits = !q.pair && q.tiles * 2 <= kSMs ? kSMs / q.tiles : 1;
     if (splits > blocks / 4) splits = blocks / 4;  // four blocks of 64 at least
     if (splits > 16) splits = 16;
     if (splits < 1) splits = 1;
@@ -440,22 +560,38 @@ Plan plan_of(int M, int N, int K) {
     return q;
 }
 
-template <typename T, bool A_MN, bool B_MN, int BN>
+template <typename T, bool A_MN, bool B_MN, int BN, bool PAIR>
 cudaError_t launch(const Maps &maps, const Params &p, cudaStream_t stream) {
+    auto kernel = kda_linear_kernel<T, A_MN, B_MN, BN, PAIR>;
+    constexpr int kBytes = Cfg<BN, PAIR>::kBytes;
     static volatile int done[kMaxDev];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = smem_limit_once(kda_linear_kernel<T, A_MN, B_MN, BN>, Cfg<BN>::kBytes, dev, done);
+    if (e == cudaSuccess) e = smem_limit_once(kernel, kBytes, dev, done);
     if (e != cudaSuccess) return e;
     const int work = p.tiles * p.splits;
-    return launch_early(kda_linear_kernel<T, A_MN, B_MN, BN>, (unsigned)(work < kSMs ? work : kSMs), kThreads,
-                        Cfg<BN>::kBytes, stream, maps, p);
+    if (!PAIR) return launch_early(kernel, (unsigned)(work < kSMs ? work : kSMs), kThreads, kBytes, stream, maps, p);
+    cudaLaunchAttribute attrs[2] = {};
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = 2;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)(work < kSMs / 2 ? work : kSMs / 2));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kBytes;
+    cfg.stream = stream;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, maps, p);
 }
 template <typename T, bool A_MN, bool B_MN>
-cudaError_t pick(int bn, const Maps &maps, const Params &p, cudaStream_t stream) {
-    return bn == 256 ? launch<T, A_MN, B_MN, 256>(maps, p, stream)
-           : bn == 128 ? launch<T, A_MN, B_MN, 128>(maps, p, stream)
-                       : launch<T, A_MN, B_MN, 64>(maps, p, stream);
+cudaError_t pick(const Plan &q, const Maps &maps, const Params &p, cudaStream_t stream) {
+    if (q.pair) return launch<T, A_MN, B_MN, 256, true>(maps, p, stream);
+    return q.bn == 256 ? launch<T, A_MN, B_MN, 256, false>(maps, p, stream)
+           : q.bn == 128 ? launch<T, A_MN, B_MN, 128, false>(maps, p, stream)
+                         : launch<T, A_MN, B_MN, 64, false>(maps, p, stream);
 }
 template <typename T> cudaError_t run(const GemmArgs &a, cudaStream_t stream) {
     const Plan q = plan_of(a.M, a.N, a.K);
@@ -464,7 +600,7 @@ template <typename T> cudaError_t run(const GemmArgs &a, cudaStream_t stream) {
                            : encode(&maps.a, a.fp16, a.A, a.K, a.M, a.lda, BK, BM);
     if (e == cudaSuccess)
         e = a.b_mn ? encode(&maps.b, a.fp16, a.B, a.N, a.K, a.ldb, 64, BK)
-                   : encode(&maps.b, a.fp16, a.B, a.K, a.N, a.ldb, BK, q.bn);
+                   : encode(&maps.b, a.fp16, a.B, a.K, a.N, a.ldb, BK, q.pair ? q.bn / 2 : q.bn);
     if (e != cudaSuccess) return e;
     Params p = {};
     p.M = a.M; p.N = a.N; p.K = a.K;
@@ -483,8 +619,8 @@ template <typename T> cudaError_t run(const GemmArgs &a, cudaStream_t stream) {
         if (e == cudaSuccess && a.pre) e = encode(&maps.pre, a.fp16, a.pre, a.N, a.M, a.ldp, 64, 32);
         if (e != cudaSuccess) return e;
     }
-    e = a.a_mn ? pick<T, true, true>(q.bn, maps, p, stream)
-        : a.b_mn ? pick<T, false, true>(q.bn, maps, p, stream) : pick<T, false, false>(q.bn, maps, p, stream);
+    e = a.a_mn ? pick<T, true, true>(q, maps, p, stream)
+        : a.b_mn ? pick<T, false, true>(q, maps, p, stream) : pick<T, false, false>(q, maps, p, stream);
     if (e != cudaSuccess || !p.partial) return e;
     const long long quads = (long long)a.M * (q.ldw / 4);
     return launch_early(kda_linear_join_kernel<T>, (unsigned)((quads + 255) / 256), 256, 0, stream, p);
