@@ -279,7 +279,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *done = empty + C::kStages, *taken = done + 2;
     uint32_t *slot = (uint32_t *)(taken + 2);
     volatile uint32_t *broken = slot + 1;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (said to be the same in all lanes: in code that might diverge, every operand of an asynchronous
+    // instruction goes through a loop over the lanes, and a stage took 810 cycles instead of 512)
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int work = p.tiles * p.splits;
     const int rank = PAIR ? (int)cluster_rank() : 0;
     const int first = PAIR ? (int)blockIdx.x / 2 : (int)blockIdx.x, step = PAIR ? (int)gridDim.x / 2 : (int)gridDim.x;
@@ -308,19 +310,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         return false;
     };
     if (warp == 0) {
-        if (lane == 0) {
-            int n = 0;  // stages filled so far
-            const uint32_t bars = PAIR ? in_first(full) : tc::smem_u32(full);
-            for (int i = first; i < work; i += step) {
-                const Tile t = tile_of(p, i, kRows, BN);
-                bool ok = true;
-                for (int kb = t.kb; kb < t.ke && ok; ++kb, ++n) {
-                    const int st = n % C::kStages;
-                    if (n >= C::kStages && !(ok = wait(empty + st, (n / C::kStages - 1) & 1))) break;
+        int n = 0;  // stages filled so far
+        const uint32_t bars = PAIR ? in_first(full) : tc::smem_u32(full);
+        bool ok = true;
+        for (int i = first; i < work && ok; i += step) {
+            const Tile t = tile_of(p, i, kRows, BN);
+            const int m = t.m + rank * BM, nn = t.n + rank * C::kRowsB;
+            for (int kb = t.kb; kb < t.ke; ++kb, ++n) {
+                const int st = n % C::kStages;
+                if (n >= C::kStages && !(ok = wait(empty + st, (n / C::kStages - 1) & 1))) break;
+                if (tc::elect_one()) {
                     const uint32_t a = tc::smem_u32(base + st * C::kStage), b = a + C::kA;
                     // (a pair's first CTA waits for both's bytes)
                     if (!PAIR || rank == 0) tc::mbar_arrive_expect_tx(full + st, (PAIR ? 2 : 1) * C::kStage);
-                    const int m = t.m + rank * BM, nn = t.n + rank * C::kRowsB;
                     if (A_MN) {
 #pragma unroll
                         for (int x = 0; x < BM / 64; ++x)
@@ -336,20 +338,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         load_2d<PAIR>(b, &maps.b, kb * BK, nn, bars + 8 * st);
                     }
                 }
-                if (!ok) break;
+                __syncwarp();
             }
-            // every copy has landed before the CTA ends (a pair's: before its first CTA does)
-            for (int s = max(0, n - C::kStages); s < n && rank == 0; ++s)
-                tc::mbar_wait(full + s % C::kStages, (s / C::kStages) & 1, kWaitPolls);
         }
+        // every copy has landed before the CTA ends (a pair's: before its first CTA does)
+        for (int s = max(0, n - C::kStages); s < n && rank == 0; ++s)
+            tc::mbar_wait(full + s % C::kStages, (s / C::kStages) & 1, kWaitPolls);
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             constexpr uint32_t idesc = idesc16(std::is_same<T, __half>::value, A_MN, B_MN, kRows, BN);
             constexpr uint32_t kStepA = A_MN ? 2048 : 32, kStepB = B_MN ? 2048 : 32;  // 16 of K
             int n = 0, c = 0;
-            for (int i = first; i < work; i += step, ++c) {
+            bool ok = true;
+            for (int i = first; i < work && ok; i += step, ++c) {
                 const Tile t = tile_of(p, i, kRows, BN);
-                bool ok = true;
                 if (c >= 2 && !wait(taken + (c & 1), (c / 2 - 1) & 1)) break;
                 tc::fence_after_sync();
                 const uint32_t d = tmem + (c & 1) * BN;
@@ -358,14 +360,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = wait(full + st, (n / C::kStages) & 1))) break;
                     tc::fence_after_sync();
                     const uint32_t a = tc::smem_u32(base + st * C::kStage), b = a + C::kA;
+                    if (tc::elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < BK / 16; ++k)
-                        mma_f16<PAIR>(d, desc128(a + k * kStepA, A_MN ? 8192 : 16, 1024),
-                                desc128(b + k * kStepB, B_MN ? 8192 : 16, 1024), idesc, kb > t.kb || k > 0);
-                    commit<PAIR>(empty + st);
+                        for (int k = 0; k < BK / 16; ++k)
+                            mma_f16<PAIR>(d, desc128(a + k * kStepA, A_MN ? 8192 : 16, 1024),
+                                          desc128(b + k * kStepB, B_MN ? 8192 : 16, 1024), idesc,
+                                          kb > t.kb || k > 0);
+                        commit<PAIR>(empty + st);
+                        if (kb + 1 == t.ke) commit<PAIR>(done + (c & 1));
+                    }
+                    __syncwarp();
                 }
-                if (!ok) break;
-                commit<PAIR>(done + (c & 1));
             }
             // the last products are done with the stages before the CTA ends
             if (n > 0) tc::mbar_wait(empty + (n - 1) % C::kStages, ((n - 1) / C::kStages) & 1, kWaitPolls);
