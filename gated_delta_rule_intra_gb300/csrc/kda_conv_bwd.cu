@@ -248,7 +248,7 @@ cudaError_t backward(const ConvArgs &a, int unit_x, int unit_dy, int unit_dx, cu
     return launch_early(kda_conv_sum_kernel, (unsigned)(((long long)(W + 1) * a.D + 255) / 256), 256, 0, stream, b);
 }
 template <typename T, int W> cudaError_t backward(const ConvArgs &a, cudaStream_t stream) {
-    rows::Unit x(sizeof(T), 16), dy(sizeof(T), 16), dx(sizeof(T), a.D);
+    rows::Boundary x(sizeof(T), 16), dy(sizeof(T), 16), dx(sizeof(T), a.D);
     x.add(a.x, a.x_stride);
     dy.add(a.dy, a.dy_stride);
     dx.add(a.dx, a.dx_stride);

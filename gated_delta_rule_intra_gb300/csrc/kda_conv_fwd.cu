@@ -163,7 +163,7 @@ cudaError_t forward(const ConvArgs &a, int unit_x, int unit_y, cudaStream_t stre
                         kThreads, bytes, stream, a, pieces, unit_x, unit_y);
 }
 template <typename T, int W> cudaError_t forward(const ConvArgs &a, cudaStream_t stream) {
-    rows::Unit x(sizeof(T), 16), y(sizeof(T), a.D);  // (the last channels of a row may be part of a word)
+    rows::Boundary x(sizeof(T), 16), y(sizeof(T), a.D);  // (the last channels of a row may be part of a word)
     x.add(a.x, a.x_stride);
     y.add(a.y, a.y_stride);
     if constexpr (sizeof(T) == 2)

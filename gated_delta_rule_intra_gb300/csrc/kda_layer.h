@@ -138,7 +138,7 @@ struct CopyArgs {
     int width;
     unsigned *dbg;
 };
-cudaError_t launch_copy_rows(const CopyArgs &a, cudaStream_t stream);
+cudaError_t launch_copy_rows(const CopyArgs &a, const CopyArgs *b, cudaStream_t stream);  // b: or null
 
 // dpre = dy act'(pre) (dpre null: not wanted) and its column sums (dbias null: not wanted).
 struct DActArgs {

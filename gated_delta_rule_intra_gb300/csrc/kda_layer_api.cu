@@ -124,15 +124,22 @@ struct Work {  // parts of a workspace, one behind the other
         return p;
     }
 };
-kda_status_t copy_rows(const void *&p, long long &stride, long long rows, int width, Work &w, kda_stream_t stream) {
-    if (rows_ok(p, stride)) return KDA_OK;
-    const long long ld = up8(width);
-    void *to = w.take((size_t)rows * ld * 2);
-    const kda::CopyArgs c = {p, to, rows, stride, ld, width, kda::debug_flags()};
-    p = to;
-    stride = ld;
-    return finish(kda::launch_copy_rows(c, (cudaStream_t)stream));
-}
+// Copies of the tensors that need them, in one launch.
+struct Copies {
+    kda::CopyArgs jobs[2];
+    int count = 0;
+    void add(const void *&p, long long &stride, long long rows, int width, Work &w) {
+        if (rows_ok(p, stride)) return;
+        const long long ld = up8(width);
+        void *to = w.take((size_t)rows * ld * 2);
+        jobs[count++] = {p, to, rows, stride, ld, width, kda::debug_flags()};
+        p = to;
+        stride = ld;
+    }
+    cudaError_t run(cudaStream_t stream) const {
+        return count ? kda::launch_copy_rows(jobs[0], count > 1 ? jobs + 1 : nullptr, stream) : cudaSuccess;
+    }
+};
 
 }  // namespace
 
@@ -535,8 +542,11 @@ kda_status_t kda_linear_fwd(const void *x, const void *weight, void *y, int M, i
     (void)cudaGetLastError();
     if (M == 0) return KDA_OK;
     Work w = {(char *)op.workspace};
-    if ((st = copy_rows(x, op.x_stride, M, K, w, stream)) != KDA_OK) return st;
-    if ((st = copy_rows(weight, op.weight_stride, N, K, w, stream)) != KDA_OK) return st;
+    Copies c;
+    c.add(x, op.x_stride, M, K, w);
+    c.add(weight, op.weight_stride, N, K, w);
+    cudaError_t e = c.run((cudaStream_t)stream);
+    if (e != cudaSuccess) return finish(e);
     kda::GemmArgs a = {};
     a.A = x; a.B = weight;
     a.lda = op.x_stride; a.ldb = op.weight_stride;
@@ -625,24 +635,25 @@ kda_status_t kda_linear_bwd(const void *dy, const void *x, const void *weight, v
     kda::GemmArgs a = {};
     a.fp16 = dtype == KDA_FP16;
     a.dbg = kda::debug_flags();
-    if (dweight && (st = copy_rows(x, op.x_stride, M, K, w, stream)) != KDA_OK) return st;
-    if (dx && (st = copy_rows(weight, op.weight_stride, N, K, w, stream)) != KDA_OK) return st;
+    Copies c;
+    if (dweight) c.add(x, op.x_stride, M, K, w);
+    if (dx) c.add(weight, op.weight_stride, N, K, w);
+    cudaError_t e = c.run(cs);
+    if (e != cudaSuccess) return finish(e);
     a.partial = (float *)w.at;
     if (dx) {  // dpre weight: contracted over the weight's rows
         a.A = g; a.lda = ldg;
         a.B = weight; a.ldb = op.weight_stride; a.b_mn = true;
         a.M = M; a.N = K; a.K = N;
         a.y = dx; a.ldy = op.dx_stride;
-        const cudaError_t e = kda::launch_gemm(a, cs);
-        if (e != cudaSuccess) return finish(e);
+        if ((e = kda::launch_gemm(a, cs)) != cudaSuccess) return finish(e);
     }
     if (dweight) {  // dpre^T x: contracted over the rows of both
         a.A = g; a.lda = ldg; a.a_mn = true;
         a.B = x; a.ldb = op.x_stride; a.b_mn = true;
         a.M = N; a.N = K; a.K = M;
         a.y = dweight; a.ldy = K;
-        const cudaError_t e = kda::launch_gemm(a, cs);
-        if (e != cudaSuccess) return finish(e);
+        if ((e = kda::launch_gemm(a, cs)) != cudaSuccess) return finish(e);
     }
     return KDA_OK;
 }

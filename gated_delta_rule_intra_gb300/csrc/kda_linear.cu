@@ -1,8 +1,9 @@
 // Matrix product with its epilogue on the tensor cores: C = A B^T, y = act(C + bias) + residual.
 //
 // Persistent, by role: one warp asks for the operands' tiles (TMA, 128-byte swizzle, 64 of K a stage),
-// one issues the products (tcgen05.mma, accumulators in tensor memory), four take the accumulators out
-// and finish them.  There are two accumulators, so that a tile's products run while the one before it
+// one issues the products (tcgen05.mma, accumulators in tensor memory), eight take the accumulators out
+// and finish them (four are not enough beside 2048 of K where a gelu is taken and two results are
+// written: 254 us at 8192 x 2048 x 8192).  There are two accumulators, so that a tile's products run while the one before it
 // is finished.  Operands may lie either way round: contracted along their rows' direction (K-major,
 // boxes of 64 k) or across it (MN-major, boxes of 64 columns x 64 k), which is what the gradients need
 // of the same tensors.
@@ -26,18 +27,19 @@ namespace linear {
 namespace {
 
 constexpr int BM = 128, BK = 64;
-constexpr int kThreads = 192;              // warps: copies, products, 4 of the epilogue
+constexpr int kEpilogue = 8;               // warps that finish tiles, 32 columns at a time
+constexpr int kThreads = 64 + 32 * kEpilogue;
 constexpr uint32_t kWaitPolls = 1u << 22;  // then the kernel gives up (and writes NaN)
 
 // BN: columns of a tile.  PAIR: of two CTAs, each with half of the rows of A and of B.
 template <int BN, bool PAIR> struct Cfg {
     static constexpr int kRowsB = PAIR ? BN / 2 : BN;  // of B in this CTA
     static constexpr int kA = BM * BK * 2, kB = kRowsB * BK * 2, kStage = kA + kB;
-    static constexpr int kStages = kStage > 32768 ? 4 : 6;
-    static constexpr int kOut = 4 * 4096;  // a [32 rows x 64 columns] box of each epilogue warp
-    static constexpr int kBias = 4 * BN * 4;
+    static constexpr int kStages = 204800 / kStage < 6 ? 204800 / kStage : 6;
+    static constexpr int kOut = kEpilogue * 2048;  // a [32 rows x 32 columns] box of each epilogue warp
+    static constexpr int kBias = kEpilogue * (BN / 2) * 4;
     static constexpr int kBytes = 1024 + kStages * kStage + kOut + kBias + 256;
-    static constexpr int kColumns = 2 * BN;  // of tensor memory
+    static constexpr int kColumns = BN > 128 ? 512 : 2 * BN;  // of tensor memory: a power of two
 };
 
 struct Maps {
@@ -52,7 +54,8 @@ struct Params {
     int act, split_n;
     float *partial;  // [splits][M][ldw], or null
     int ldw;
-    bool tma_out, wide_r;  // y and pre leave by TMA; residual's rows are on 16-byte boundaries
+    bool tma_out;         // y and pre leave by TMA
+    int unit_o, unit_r;   // bytes on whose boundaries their rows begin, and residual's
     unsigned *dbg;
 };
 
@@ -194,75 +197,96 @@ __device__ __forceinline__ Tile tile_of(const Params &p, int i, int rows_each, i
     return t;
 }
 
-template <int V> __device__ __forceinline__ void activate_all(float (&v)[V], int act) {
-    if (act == ACT_SILU) {
+template <int ACT> __device__ __forceinline__ void activate_as(float (&v)[32]) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = activate(v[j], ACT_SILU);
-    } else if (act == ACT_GELU) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = activate(v[j], ACT_GELU);
-    } else if (act == ACT_RELU) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = activate(v[j], ACT_RELU);
+    for (int j = 0; j < 32; j += 2) {
+        const float2 y = activate<ACT>(make_float2(v[j], v[j + 1]));
+        v[j] = y.x;
+        v[j + 1] = y.y;
     }
+}
+__device__ __forceinline__ void activate_all(float (&v)[32], int act) {
+    if (act == ACT_SILU)
+        activate_as<ACT_SILU>(v);
+    else if (act == ACT_GELU)
+        activate_as<ACT_GELU>(v);
+    else if (act == ACT_RELU)
+        activate_as<ACT_RELU>(v);
 }
 
-// Elements of a row to (or from) a swizzled [32][64] box, where the row is not on a 16-byte boundary:
-// `pair` if it is on a 4-byte one.
-template <typename T>
-__device__ __forceinline__ void box_out(const char *box, void *base, long long ld, int m, int n, int M,
-                                        int N, int lane, bool pair) {
-    const int rows = min(32, M - m);
-#pragma unroll 8
-    for (int r = 0; r < rows; ++r) {
-        const uint32_t x = *(const uint32_t *)(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-        uint16_t *to = (uint16_t *)base + (size_t)(m + r) * ld + n + 2 * lane;
-        if (pair && n + 2 * lane + 1 < N) {
-            *(uint32_t *)to = x;
-        } else {
-            if (n + 2 * lane < N) to[0] = (uint16_t)x;
-            if (n + 2 * lane + 1 < N) to[1] = (uint16_t)(x >> 16);
-        }
-    }
-}
-__device__ __forceinline__ void box_in(char *box, const void *base, long long ld, int m, int n, int M,
-                                       int N, int lane, bool wide, bool pair) {
-    const int rows = min(32, M - m);
-    if (wide) {  // eight lanes a row, 16 bytes each
+// Where 16 bytes (chunk q) of row r are in a box of 32 rows of 64 bytes, swizzled as the tensor maps of
+// the results are.
+__device__ __forceinline__ int spot(int r, int q) { return r * 64 + ((q ^ (r >> 1 & 3)) << 4); }
+
+// A box from or to rows that begin on boundaries of a word W: neighbouring lanes have neighbouring words;
+// words that the last column ends in go by elements.
+template <typename W> struct Rows {
+    static constexpr int kWords = 64 / sizeof(W), kStep = 32 / kWords, kEach = sizeof(W) / 2;
+    int row, byte, left;  // this lane's first row, place in it, and elements from there to the last column
+    __device__ __forceinline__ Rows(int n, int N, int lane)
+        : row(lane / kWords), byte(lane % kWords * (int)sizeof(W)), left(N - n - byte / 2) {}
+    __device__ __forceinline__ void in(char *box, const void *base, long long ld, int m, int n, int M) const {
+        const uint16_t *at = (const uint16_t *)base + (size_t)(m + row) * ld + n + byte / 2;
+        const int rows = min(32, M - m);
+        constexpr int kBatch = 32 / kStep < 16 ? 32 / kStep : 16;  // each waits for memory once
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = i * 4 + (lane >> 3), c = lane & 7;
-            if (r < rows && n + c * 8 < N)
-                *(uint4 *)(box + r * 128 + ((c ^ (r & 7)) << 4)) =
-                    *(const uint4 *)((const uint16_t *)base + (size_t)(m + r) * ld + n + c * 8);
-        }
-        return;
-    }
-    // sixteen rows at a time: each batch waits for memory once
-    const int c = n + 2 * lane;
-    const uint16_t *at = (const uint16_t *)base + (size_t)m * ld + c;
+        for (int b = 0; b < 32 / kStep; b += kBatch) {
+            W x[kBatch];
 #pragma unroll
-    for (int r0 = 0; r0 < 32; r0 += 16) {
-        uint32_t x[16];
+            for (int i = 0; i < kBatch; ++i) {
+                const int r = row + (b + i) * kStep;
+                const uint16_t *f = at + (size_t)(b + i) * kStep * ld;
+                x[i] = W{};
+                if (r < rows && left >= kEach) {
+                    x[i] = *(const W *)f;
+                } else if (r < rows && left > 0) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            x[i] = 0;
-            const uint16_t *f = at + (size_t)(r0 + i) * ld;
-            if (r0 + i < rows && c < N) {
-                if (pair && c + 1 < N) {
-                    x[i] = *(const uint32_t *)f;
-                } else {
-                    x[i] = f[0];
-                    if (c + 1 < N) x[i] |= (uint32_t)f[1] << 16;
+                    for (int e = 0; e < kEach; ++e)
+                        if (e < left) ((uint16_t *)&x[i])[e] = f[e];
                 }
             }
-        }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int r = r0 + i;
-            *(uint32_t *)(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) = x[i];
+            for (int i = 0; i < kBatch; ++i)
+                *(W *)(box + spot(row + (b + i) * kStep, byte >> 4) + (byte & 15)) = x[i];
         }
     }
+    __device__ __forceinline__ void out(const char *box, void *base, long long ld, int m, int n, int M) const {
+        uint16_t *to = (uint16_t *)base + (size_t)(m + row) * ld + n + byte / 2;
+        const int rows = min(32, M - m);
+#pragma unroll 8
+        for (int r = row; r < rows; r += kStep, to += kStep * ld) {
+            const W x = *(const W *)(box + spot(r, byte >> 4) + (byte & 15));
+            if (left >= kEach) {
+                *(W *)to = x;
+            } else {
+#pragma unroll
+                for (int e = 0; e < kEach; ++e)
+                    if (e < left) to[e] = ((const uint16_t *)&x)[e];
+            }
+        }
+    }
+};
+__device__ __forceinline__ void box_in(char *box, const void *base, long long ld, int m, int n, int M, int N, int lane,
+                                       int unit) {
+    if (unit == 16)
+        Rows<uint4>(n, N, lane).in(box, base, ld, m, n, M);
+    else if (unit == 8)
+        Rows<uint2>(n, N, lane).in(box, base, ld, m, n, M);
+    else if (unit == 4)
+        Rows<uint32_t>(n, N, lane).in(box, base, ld, m, n, M);
+    else
+        Rows<uint16_t>(n, N, lane).in(box, base, ld, m, n, M);
+}
+__device__ __forceinline__ void box_out(const char *box, void *base, long long ld, int m, int n, int M, int N, int lane,
+                                        int unit) {
+    if (unit == 16)
+        Rows<uint4>(n, N, lane).out(box, base, ld, m, n, M);
+    else if (unit == 8)
+        Rows<uint2>(n, N, lane).out(box, base, ld, m, n, M);
+    else if (unit == 4)
+        Rows<uint32_t>(n, N, lane).out(box, base, ld, m, n, M);
+    else
+        Rows<uint16_t>(n, N, lane).out(box, base, ld, m, n, M);
 }
 
 template <typename T, bool A_MN, bool B_MN, int BN, bool PAIR>
@@ -292,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(done + i, 1);
-            tc::mbar_init(taken + i, PAIR ? 8 : 4);
+            tc::mbar_init(taken + i, PAIR ? 2 * kEpilogue : kEpilogue);
         }
         *broken = 0;
     }
@@ -376,35 +400,44 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n > 0) tc::mbar_wait(empty + (n - 1) % C::kStages, ((n - 1) / C::kStages) & 1, kWaitPolls);
         }
     } else {
-        const int e = warp - 2, quarter = warp & 3;  // a warp reads its own 32 lanes of tensor memory
-        char *box = out + e * 4096;
-        float *bs = bias + e * BN;
-        const bool pair_r = (uintptr_t)p.residual % 4 == 0 && p.ldr % 2 == 0;
-        const bool pair = ((uintptr_t)p.y | (uintptr_t)p.pre) % 4 == 0 && (p.ldy | p.ldp) % 2 == 0;
+        // a warp reads its own 32 lanes of tensor memory, and takes half of a tile's columns
+        const int e = warp - 2, quarter = warp & 3, c0 = e / 4 * (BN / 2);
+        char *box = out + e * 2048;
+        float *bs = bias + e * (BN / 2);
         int c = 0;
+        auto begin = [&] {  // the box may be written
+            if (p.tma_out) {
+                if (lane == 0) tc::bulk_wait_read_all();
+                __syncwarp();
+            }
+        };
         for (int i = first; i < work; i += step, ++c) {
             const Tile t = tile_of(p, i, kRows, BN);
-            const int m0 = t.m + rank * BM + 32 * quarter, n1 = min(p.N - t.n, BN);
+            const int m0 = t.m + rank * BM + 32 * quarter, n0 = t.n + c0, n1 = min(p.N - n0, BN / 2);
+            auto addend = [&](int n) {
+                begin();
+                box_in(box, p.residual, p.ldr, m0, n0 + n, p.M, p.N, lane, p.unit_r);
+                __syncwarp();
+            };
+            const bool early = p.residual && !p.pre && !p.partial && n1 > 0;
             if (!p.partial) {
                 __syncwarp();
-                for (int j = lane; j < BN; j += 32)
-                    bs[j] = p.bias && t.n + j < p.N ? as_f32(((const T *)p.bias)[t.n + j]) : 0.f;
+                for (int j = lane; j < BN / 2; j += 32)
+                    bs[j] = p.bias && n0 + j < p.N ? as_f32(((const T *)p.bias)[n0 + j]) : 0.f;
                 __syncwarp();
+                if (early) addend(0);
             }
             const bool ok = wait(done + (c & 1), (c / 2) & 1);
             tc::fence_after_sync();
-            const uint32_t d = tmem + (c & 1) * BN + ((uint32_t)quarter << 21);
-            for (int n = 0; n < n1; n += 64) {
-                float v[64];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float x[32];
-                    tmem_ld32(d + n + 32 * h, x);
+            const uint32_t d = tmem + (c & 1) * BN + c0 + ((uint32_t)quarter << 21);
+            int n = 0;
+            do {
+                float v[32];
+                if (n1 > 0) {
+                    tmem_ld32(d + n, v);
                     tc::tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[32 * h + j] = ok ? x[j] : __int_as_float(0x7fc00000);
                 }
-                if (n + 64 >= n1) {  // the accumulator may be written again
+                if (n + 32 >= n1) {  // the accumulator may be written again
                     tc::fence_before_sync();
                     __syncwarp();
                     if (lane == 0) {
@@ -413,34 +446,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else
                             tc::mbar_arrive(taken + (c & 1));
                     }
+                    if (n1 <= 0) break;
+                }
+                if (!ok) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __int_as_float(0x7fc00000);
                 }
                 if (p.partial) {
                     const int m = m0 + lane;
                     if (m < p.M) {
-                        float *to = p.partial + ((size_t)(i / p.tiles) * p.M + m) * p.ldw + t.n + n;
+                        float *to = p.partial + ((size_t)(i / p.tiles) * p.M + m) * p.ldw + n0 + n;
 #pragma unroll
-                        for (int j = 0; j < 64; j += 4)
-                            if (t.n + n + j < p.ldw)
+                        for (int j = 0; j < 32; j += 4)
+                            if (n0 + n + j < p.ldw)
                                 *(float4 *)(to + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
                     }
                     continue;
                 }
+                if (p.bias) {
 #pragma unroll
-                for (int j = 0; j < 64; j += 4) {
-                    const float4 b = *(const float4 *)(bs + n + j);
-                    v[j] += b.x; v[j + 1] += b.y; v[j + 2] += b.z; v[j + 3] += b.w;
-                }
-                // a box of 32 rows x 64 columns at a time: pre, then y
-                auto begin = [&] {  // the box may be written
-                    if (p.tma_out) {
-                        if (lane == 0) tc::bulk_wait_read_all();
-                        __syncwarp();
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 b = *(const float4 *)(bs + n + j);
+                        v[j] += b.x; v[j + 1] += b.y; v[j + 2] += b.z; v[j + 3] += b.w;
                     }
-                };
+                }
+                // a box of 32 rows x 32 columns at a time: pre, then y
                 auto put = [&](bool add) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        uint4 *at = (uint4 *)(box + lane * 128 + ((q ^ (lane & 7)) << 4));
+                    for (int q = 0; q < 4; ++q) {
+                        uint4 *at = (uint4 *)(box + spot(lane, q));
                         if (add) {
                             const uint4 r = *at;
                             const uint32_t rr[4] = {r.x, r.y, r.z, r.w};
@@ -460,12 +494,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0 && m0 < p.M) {
-                            store_2d(map, tc::smem_u32(box), t.n + n, m0);
+                            store_2d(map, tc::smem_u32(box), n0 + n, m0);
                             tc::bulk_commit_group();
                         }
                     } else {
                         __syncwarp();
-                        box_out<T>(box, to, ld, m0, t.n + n, p.M, p.N, lane, pair);
+                        box_out(box, to, ld, m0, n0 + n, p.M, p.N, lane, p.unit_o);
                         __syncwarp();
                     }
                 };
@@ -475,14 +509,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     leave(&maps.pre, p.pre, p.ldp);
                 }
                 activate_all(v, p.act);
-                begin();
-                if (p.residual) {
-                    box_in(box, p.residual, p.ldr, m0, t.n + n, p.M, p.N, lane, p.wide_r, pair_r);
-                    __syncwarp();
-                }
+                if (!p.residual)
+                    begin();
+                else if (!early || n > 0)
+                    addend(n);
                 put(p.residual);
                 leave(&maps.y, p.y, p.ldy);
-            }
+            } while ((n += 32) < n1);
             if (!ok) break;
         }
         if (lane == 0) tc::bulk_wait_all();
@@ -524,7 +557,7 @@ __global__ void __launch_bounds__(256) kda_linear_join_kernel(const Params p) {
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 cudaError_t encode(CUtensorMap *m, bool fp16, const void *base, long long cols, long long rows,
-                   long long ld, int box_cols, int box_rows) {
+                   long long ld, int box_cols, int box_rows, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     if (!g_encode) {
         void *fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -538,7 +571,7 @@ cudaError_t encode(CUtensorMap *m, bool fp16, const void *base, long long cols, 
     const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, one[2] = {1, 1};
     const CUresult r = g_encode(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                                 const_cast<void *>(base), dims, strides, box, one,
-                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -552,7 +585,21 @@ Plan plan_of(int M, int N, int K) {
     Plan q;
     auto tiles = [&](int bm, int bn) { return (long long)((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
     q.pair = tiles(256, 256) >= kSMs / 2;
-    q.bn = q.pair || tiles(BM, 256) >= kSMs ? 256 : tiles(BM, 128) >= kSMs / 2 || N > 64 ? 128 : 64;
+    q.bn = 256;
+    if (!q.pair) {
+        // the width whose rounds of tiles take least: a stage's products take BN / 4 of 64 cycles, its
+        // start and the tile's ends some 48 columns' worth (2021 x 1540 x 1111: 192 columns take one
+        // round of 144 tiles, 128 two of 208)
+        long long best = -1;
+        for (int bn = 64; bn <= 256; bn += 64) {
+            const long long cost = (tiles(BM, bn) + kSMs - 1) / kSMs * (bn + 48);
+            if (best < 0 || cost < best || (cost == best && tiles(BM, bn) * 2 <= kSMs)) {
+                best = cost;
+                q.bn = bn;
+            }
+        }
+        if (tiles(BM, q.bn) * 2 <= kSMs) q.bn = N > 64 ? 128 : 64;  // the contraction is cut anyway
+    }
     q.tiles = (int)tiles(q.pair ? 2 * BM : BM, q.bn);
     const int blocks = (K + BK - 1) / BK;
     int splits = !q.pair && q.tiles * 2 <= kSMs ? kSMs / q.tiles : 1;
@@ -595,6 +642,7 @@ template <typename T, bool A_MN, bool B_MN>
 cudaError_t pick(const Plan &q, const Maps &maps, const Params &p, cudaStream_t stream) {
     if (q.pair) return launch<T, A_MN, B_MN, 256, true>(maps, p, stream);
     return q.bn == 256 ? launch<T, A_MN, B_MN, 256, false>(maps, p, stream)
+           : q.bn == 192 ? launch<T, A_MN, B_MN, 192, false>(maps, p, stream)
            : q.bn == 128 ? launch<T, A_MN, B_MN, 128, false>(maps, p, stream)
                          : launch<T, A_MN, B_MN, 64, false>(maps, p, stream);
 }
@@ -617,11 +665,16 @@ template <typename T> cudaError_t run(const GemmArgs &a, cudaStream_t stream) {
     p.ldw = q.ldw;
     p.partial = q.splits > 1 ? a.partial : nullptr;
     p.dbg = a.dbg;
-    p.wide_r = aligned(a.residual, 16) && a.ldr % 8 == 0 && a.N % 8 == 0;
-    p.tma_out = !p.partial && aligned(a.y, 16) && a.ldy % 8 == 0 && (!a.pre || (aligned(a.pre, 16) && a.ldp % 8 == 0));
+    Boundary o(2, 8), r(2, 8);
+    o.add(a.y, a.ldy);
+    o.add(a.pre, a.ldp);
+    r.add(a.residual, a.ldr);
+    p.unit_o = o.unit;
+    p.unit_r = r.unit;
+    p.tma_out = !p.partial && o.unit == 16;
     if (p.tma_out) {
-        e = encode(&maps.y, a.fp16, a.y, a.N, a.M, a.ldy, 64, 32);
-        if (e == cudaSuccess && a.pre) e = encode(&maps.pre, a.fp16, a.pre, a.N, a.M, a.ldp, 64, 32);
+        e = encode(&maps.y, a.fp16, a.y, a.N, a.M, a.ldy, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+        if (e == cudaSuccess && a.pre) e = encode(&maps.pre, a.fp16, a.pre, a.N, a.M, a.ldp, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
         if (e != cudaSuccess) return e;
     }
     e = a.a_mn ? pick<T, true, true>(q, maps, p, stream)

@@ -86,16 +86,28 @@ __global__ void __launch_bounds__(32 * kWarps) kda_linear_small_kernel(const Gem
     }
 }
 
-__global__ void __launch_bounds__(256) kda_linear_copy_kernel(const CopyArgs a, int per) {
+// Rows copied, eight elements a thread, up to two tensors in one launch.  A thread reads the 4-byte words
+// that its elements lie in and shifts them by one where they begin in the middle of one (a word never
+// ends outside the allocation that one of its bytes is in).
+__global__ void __launch_bounds__(256) kda_linear_copy_kernel(const CopyArgs a0, const CopyArgs a1, unsigned first) {
     wait_for_previous();
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x, r = i / per;
-    const int c = (int)(i - r * per) * 8;
-    if (r >= a.rows) return;
-    const uint16_t *at = (const uint16_t *)a.src + r * a.lds + c;
-    alignas(16) uint16_t v[8];
+    const CopyArgs &a = blockIdx.x < first ? a0 : a1;
+    const int per = (a.width + 7) / 8;
+    const long long i = (long long)(blockIdx.x - (blockIdx.x < first ? 0 : first)) * 256 + threadIdx.x, r = i / per;
+    const int c = (int)(i - r * per) * 8, left = a.width - c;
+    if (r >= a.rows || !dbg_ok(a.dbg, (size_t)r, (size_t)a.rows, DBG_LOAD)) return;
+    const uintptr_t at = (uintptr_t)((const uint16_t *)a.src + r * a.lds + c);
+    const int s = at & 2 ? 1 : 0;  // elements of the first word in front of ours
+    const uint32_t *f = (const uint32_t *)(at & ~(uintptr_t)3);
+    uint32_t w[5];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < a.width ? at[j] : (uint16_t)0;
-    *(uint4 *)((uint16_t *)a.dst + r * a.ldd + c) = *(const uint4 *)v;
+    for (int j = 0; j < 5; ++j) w[j] = 2 * j - s < left && (j < 4 || s) ? f[j] : 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        w[j] = __funnelshift_r(w[j], w[j + 1], 16 * s);
+        if (2 * j + 1 >= left) w[j] &= 2 * j < left ? 0xffffu : 0u;
+    }
+    *(uint4 *)((uint16_t *)a.dst + r * a.ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // dpre and the sums of its columns.  A warp has 32 V neighbouring columns of every eighth row of its
@@ -114,11 +126,20 @@ __global__ void __launch_bounds__(256) kda_linear_dact_kernel(const DActArgs a, 
             const auto dy = *(const Vec<T, V> *)((const T *)a.dy + m * a.lddy + n);
             Vec<T, V> p, d;
             if (a.act != ACT_NONE) p = *(const Vec<T, V> *)((const T *)a.pre + m * a.ldp + n);
+            if constexpr (V == 1) {
+                const float g = a.act != ACT_NONE ? dy[0] * slope(twice(p[0]), a.act).x : dy[0];
+                sum[0] += g;
+                d.v[0] = from_f32<T>(g);
+            } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float g = a.act != ACT_NONE ? dy[i] * slope(p[i], a.act) : dy[i];
-                sum[i] += g;
-                d.v[i] = from_f32<T>(g);
+                for (int i = 0; i < V; i += 2) {
+                    float2 g = dy.two(i);
+                    if (a.act != ACT_NONE) g = mul2(g, slope(p.two(i), a.act));
+                    const float2 t = add2(make_float2(sum[i], sum[i + 1]), g);
+                    sum[i] = t.x;
+                    sum[i + 1] = t.y;
+                    d.put(i, g);
+                }
             }
             if (a.dpre) *(Vec<T, V> *)((T *)a.dpre + m * a.ldd + n) = d;
         }
@@ -154,9 +175,12 @@ template <typename T, int V> cudaError_t dact(const DActArgs &a, cudaStream_t st
     return launch_early(kda_linear_dbias_kernel<T>, (unsigned)((a.N + 255) / 256), 256, 0, stream, a, parts);
 }
 template <typename T> cudaError_t dact(const DActArgs &a, cudaStream_t stream) {
-    auto ok = [](const void *p, long long ld) { return !p || (aligned(p, 16) && ld % 8 == 0); };
-    return a.N % 8 == 0 && ok(a.dy, a.lddy) && ok(a.pre, a.ldp) && ok(a.dpre, a.ldd) ? dact<T, 8>(a, stream)
-                                                                                     : dact<T, 1>(a, stream);
+    Boundary u(2, a.N);
+    u.add(a.dy, a.lddy);
+    u.add(a.pre, a.ldp);
+    u.add(a.dpre, a.ldd);
+    return u.unit == 16 ? dact<T, 8>(a, stream) : u.unit == 8 ? dact<T, 4>(a, stream)
+           : u.unit == 4 ? dact<T, 2>(a, stream) : dact<T, 1>(a, stream);
 }
 
 template <typename T> cudaError_t small(const GemmArgs &a, cudaStream_t stream) {
@@ -180,9 +204,10 @@ cudaError_t launch_dact(const DActArgs &a, cudaStream_t stream) {
     return a.fp16 ? linear::dact<__half>(a, stream) : linear::dact<__nv_bfloat16>(a, stream);
 }
 
-cudaError_t launch_copy_rows(const CopyArgs &a, cudaStream_t stream) {
-    const int per = (a.width + 7) / 8;
-    return launch_early(linear::kda_linear_copy_kernel, (unsigned)((a.rows * per + 255) / 256), 256, 0, stream, a, per);
+cudaError_t launch_copy_rows(const CopyArgs &a, const CopyArgs *b, cudaStream_t stream) {
+    auto blocks = [](const CopyArgs &x) { return (unsigned)((x.rows * ((x.width + 7) / 8) + 255) / 256); };
+    const unsigned first = blocks(a);
+    return launch_early(linear::kda_linear_copy_kernel, first + (b ? blocks(*b) : 0), 256, 0, stream, a, b ? *b : a, first);
 }
 
 bool small_gemm_ok(const GemmArgs &a) { return a.M <= kSmallM && !a.a_mn && !a.b_mn && a.K % 8 == 0; }

@@ -119,9 +119,9 @@ inline bool aligned(const void *p, size_t to) { return (uintptr_t)p % to == 0; }
 
 // The widest of 16, 8, 4 bytes and an element on whose boundaries all rows and blocks of `per` channels
 // begin.
-struct Unit {
+struct Boundary {
     int es, unit;
-    Unit(int es, int per) : es(es), unit(16) {
+    Boundary(int es, int per) : es(es), unit(16) {
         while (unit > es && (long long)per * es % unit) unit /= 2;
     }
     void add(const void *p, long long stride) {

@@ -270,8 +270,8 @@ template <int L> struct Share {
     static __device__ __forceinline__ bool mine(int part) { return L <= 4 || part % (L / 4 > 0 ? L / 4 : 1) == 0; }
 };
 
-struct Unit : rows::Unit {
-    Unit(const ScanArgs &a) : rows::Unit(esize(a.dtype), a.D / a.G) {}
+struct Unit : rows::Boundary {
+    Unit(const ScanArgs &a) : rows::Boundary(esize(a.dtype), a.D / a.G) {}
 };
 
 }  // namespace scan
