@@ -1,87 +1,119 @@
 // Selective scan, single-token form: one token for each request, its states updated in place
 // (kda_scan.cuh has the formulas).
 //
-// Bound by memory: a state is read once and written once.  A thread has four states of a channel
-// and takes that channel of up to four requests, whose states are all asked for before the first is
-// used; A is read once for them.
+// Bound by memory: a state is read once and written once.  A thread has four states of a channel.
+// Where there are requests enough it takes that channel of four of them: their states are all asked for
+// before the first is used, A is read once for them, and the lanes of a channel share out what
+// there is once a request and channel (the step size, the input, the gate, the result).
 #include "kda_scan.cuh"
 
 namespace kda {
 namespace scan {
 namespace {
 
+// Four numbers of B or C from n0 on; zeros from N on.
+template <typename T, bool WIDE>
+__device__ __forceinline__ Four vector_of(const void *base, long long at, int n0, int N) {
+    const T *v = (const T *)base + at + n0;
+    if (WIDE) {
+        const Vec<T, 4> x = *(const Vec<T, 4> *)v;
+        return {x.two(0), x.two(2)};
+    }
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = n0 + i < N ? as_f32(v[i]) : 0.f;
+    return four(make_float4(f[0], f[1], f[2], f[3]));
+}
+
+// WIDE: N is a multiple of 4, and so is where rows of B and C begin.
 template <typename T, int NP, int R, bool WIDE>
 __global__ void __launch_bounds__(kThreads) kda_scan_step_kernel(const ScanArgs a) {
     wait_for_previous();
     using S = Shape<NP>;
+    // the requests of this lane: all of them, or its share
+    constexpr int kMine = R == 4 ? Share<S::L>::kCount : R;
     const int c = blockIdx.x * S::HC + threadIdx.x / S::L, part = threadIdx.x % S::L, n0 = 4 * part;
-    const int r0 = blockIdx.y * R;
-    const bool in = c < a.D;
-    const int ch = in ? c : 0, group = ch / (a.D / a.G);
+    const int r0 = blockIdx.y * R, mine = R == 4 ? Share<S::L>::first(part) : 0;
+    const bool in = c < a.D, some = n0 < a.N;
+    const int ch = in ? c : 0;
+    const long long group = (long long)(ch / (a.D / a.G)) * a.N;
     float *st[R];
-    Four h[R];
-    bool live[R];
+    Four h[R], B[R], C[R];
+    unsigned live = 0;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int r = r0 + i;
-        long long slot = r < a.requests ? a.state_indices ? a.state_indices[r] : r : -1;
-        live[i] = in && slot >= 0 && slot < a.num_states;
-        st[i] = a.state + ((size_t)(live[i] ? slot : 0) * a.D + ch) * a.N;
+        const long long slot = r < a.requests ? a.state_indices ? a.state_indices[r] : r : -1;
+        if (slot >= 0 && slot < a.num_states) live |= 1u << i;
+        st[i] = a.state + ((size_t)(live >> i & 1 ? slot : 0) * a.D + ch) * a.N + n0;
         h[i] = {both(0.f), both(0.f)};
-        if (live[i] && n0 < a.N) {
-            if (WIDE)
-                h[i] = four(*(const float4 *)(st[i] + n0));
-            else
-                h[i] = load_states(st[i], 0, n0, a.N, true);
+        if ((live >> i & 1) && in && some) h[i] = WIDE ? four(*(const float4 *)st[i]) : load_states(st[i], 0, 0, a.N - n0, true);
+    }
+    float u[kMine], d[kMine], z[kMine];
+    const float bias = a.delta_bias ? a.delta_bias[ch] : 0.f, skip = a.skip ? a.skip[ch] : 0.f;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const long long r = min(r0 + mine + i, a.requests - 1);
+        u[i] = as_f32(((const T *)a.u)[r * a.u_stride + ch]);
+        d[i] = as_f32(((const T *)a.delta)[r * a.delta_stride + ch]) + bias;
+        z[i] = a.z ? as_f32(((const T *)a.z)[r * a.z_stride + ch]) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const long long r = min(r0 + i, a.requests - 1);
+        B[i] = C[i] = {both(0.f), both(0.f)};
+        if (some) {
+            B[i] = vector_of<T, WIDE>(a.B, r * a.B_stride + group, n0, a.N);
+            C[i] = vector_of<T, WIDE>(a.C, r * a.C_stride + group, n0, a.N);
         }
     }
     const Four A2 = scaled(load_states(a.A, ch, n0, a.N, in), kLog2e);
-    const float bias = a.delta_bias ? a.delta_bias[ch] : 0.f, skip = a.skip ? a.skip[ch] : 0.f;
-    float y[R], u[R];
+    if (a.softplus) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) d[i] = softplus(d[i]);
+    }
+    float y[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        y[i] = u[i] = 0.f;
-        if (!live[i]) continue;
-        const size_t r = r0 + i;
-        u[i] = as_f32(((const T *)a.u)[r * a.u_stride + ch]);
-        float d = as_f32(((const T *)a.delta)[r * a.delta_stride + ch]) + bias;
-        if (a.softplus) d = softplus(d);
-        const T *B = (const T *)a.B + r * a.B_stride + (size_t)group * a.N;
-        const T *C = (const T *)a.C + r * a.C_stride + (size_t)group * a.N;
-        float b[4], cc[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            b[x] = n0 + x < a.N ? as_f32(B[n0 + x]) : 0.f;
-            cc[x] = n0 + x < a.N ? as_f32(C[n0 + x]) : 0.f;
+        float di = d[i % kMine], ui = u[i % kMine];
+        if (R == 4 && S::L > 1) {  // from the lane that has this request
+            constexpr int kEach = S::L > 4 ? S::L / 4 : 1;  // lanes of one request
+            const int from = i / kMine * kEach;
+            di = __shfl_sync(0xffffffffu, di, from, S::L);
+            ui = __shfl_sync(0xffffffffu, ui, from, S::L);
         }
-        h[i] = fma(decay(both(d), A2), h[i], mul(both(d * u[i]), four(make_float4(b[0], b[1], b[2], b[3]))));
-        y[i] = dot(h[i], four(make_float4(cc[0], cc[1], cc[2], cc[3])));
-        if (n0 < a.N) {
+        h[i] = fma(decay(both(di), A2), h[i], mul(both(di * ui), B[i]));
+        y[i] = dot(h[i], C[i]);
+        if ((live >> i & 1) && in && some) {
             if (WIDE)
-                *(float4 *)(st[i] + n0) = one(h[i]);
+                *(float4 *)st[i] = one(h[i]);
             else
-                store_states(st[i], 0, n0, a.N, h[i]);
+                store_states(st[i], 0, 0, a.N - n0, h[i]);
         }
     }
+    if (R == 4) {
+        scatter_sum<S::L, 1>(y, threadIdx.x);
+    } else {
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
+        for (int off = S::L / 2; off > 0; off >>= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], off);
+    }
+    if (!in || !(R == 4 ? Share<S::L>::mine(part) : part == 0)) return;
 #pragma unroll
-        for (int off = S::L / 2; off > 0; off >>= 1) y[i] += __shfl_xor_sync(0xffffffffu, y[i], off);
-        const int r = r0 + i;
-        if (part == 0 && in && r < a.requests && dbg_ok(a.dbg, (size_t)r, (size_t)a.requests, DBG_STORE)) {
-            float out = fmaf(skip, u[i], y[i]);
-            if (a.z && live[i]) {
-                const float z = as_f32(((const T *)a.z)[(size_t)r * a.z_stride + ch]);
-                out *= z * sigmoid(z);
-            }
-            ((T *)a.y)[(size_t)r * a.y_stride + ch] = from_f32<T>(out);  // a row without a request: zero
-        }
+    for (int i = 0; i < kMine; ++i) {
+        const int r = r0 + mine + i;
+        if (r >= a.requests || !dbg_ok(a.dbg, (size_t)r, (size_t)a.requests, DBG_STORE)) continue;
+        float out = fmaf(skip, u[i], y[i]);
+        if (a.z) out *= z[i] * sigmoid(z[i]);
+        if (!(live >> (mine + i) & 1)) out = 0.f;  // a row without a request
+        ((T *)a.y)[(size_t)r * a.y_stride + ch] = from_f32<T>(out);
     }
 }
 
 template <typename T, int NP, int R> cudaError_t launch(const ScanArgs &a, cudaStream_t stream) {
     const dim3 grid((unsigned)((a.D + Shape<NP>::HC - 1) / Shape<NP>::HC), (unsigned)((a.requests + R - 1) / R));
-    return a.N % 4 == 0 ? launch_early(kda_scan_step_kernel<T, NP, R, true>, grid, kThreads, 0, stream, a)
+    const size_t four = 4 * (size_t)esize(a.dtype);
+    const bool wide = a.N % 4 == 0 && aligned(a.B, four) && aligned(a.C, four) && a.B_stride % 4 == 0 && a.C_stride % 4 == 0;
+    return wide ? launch_early(kda_scan_step_kernel<T, NP, R, true>, grid, kThreads, 0, stream, a)
                         : launch_early(kda_scan_step_kernel<T, NP, R, false>, grid, kThreads, 0, stream, a);
 }
 template <typename T, int NP> cudaError_t launch(const ScanArgs &a, cudaStream_t stream) {
