@@ -25,7 +25,7 @@ template <typename T, int W, bool ODD> struct Smem {
 };
 
 template <typename T, int W, bool ODD>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
     kda_conv_bwd_kernel(const ConvArgs a, long long pieces, int unit_x, int unit_dy, int unit_dx) {
     wait_for_previous();
     using S = Shape<T, ODD>;
@@ -234,7 +234,7 @@ cudaError_t backward(const ConvArgs &a, int unit_x, int unit_dy, int unit_dx, cu
     constexpr int kBytes = sizeof(M);
     const int bytes = unit_dx >= (int)(V * sizeof(T)) ? kBytes - (int)sizeof(M::dx) : kBytes;
     ConvArgs b = a;  // as many rows of sums as CTAs: one wave
-    const long long wave = resident(bytes, 3) * kSMs / blocks, most = wave > 1 ? wave : 1;
+    const long long wave = resident(bytes, 4) * kSMs / blocks, most = wave > 1 ? wave : 1;
     const long long rows = pieces < most ? pieces : most;
     if (rows < b.partials || !a.dweight) b.partials = (int)rows;
     static volatile int done[kMaxDev];
@@ -271,7 +271,7 @@ template <typename T> cudaError_t backward(const ConvArgs &a, cudaStream_t strea
 
 // CTAs of a block of channels, each with a row of sums, in the type with the fewest blocks.
 int conv_partials(long long pieces, int D) {
-    const long long blocks = (D + 63) / 64, most = 3 * kSMs / blocks > 1 ? 3 * kSMs / blocks : 1;
+    const long long blocks = (D + 63) / 64, most = 4 * kSMs / blocks > 1 ? 4 * kSMs / blocks : 1;
     return (int)(pieces < most ? pieces : most);
 }
 

@@ -54,7 +54,7 @@ struct ConvArgs {
 cudaError_t launch_conv_fwd(const ConvArgs &a, cudaStream_t stream);
 cudaError_t launch_conv_bwd(const ConvArgs &a, cudaStream_t stream);
 cudaError_t launch_conv_step(const ConvArgs &a, cudaStream_t stream);
-constexpr int kConvPiece = 128;  // tokens that a CTA of the backward takes at a time
+constexpr int kConvPiece = 96;  // tokens that a CTA of the backward takes at a time
 int conv_partials(long long pieces, int D);
 
 struct ScanArgs {
