@@ -93,14 +93,14 @@ class Layer(torch.nn.Module):
 
 
 class Model(torch.nn.Module):
-    def __init__(self, vocabulary, width, heads, value_heads, layers):
+    def __init__(self, vocabulary, width, heads, value_heads, layers, layer=Layer):
         super().__init__()
         self.embed = torch.nn.Embedding(vocabulary, width)
         self.before = torch.nn.Embedding(vocabulary, width)  # of the token before
         torch.nn.init.normal_(self.embed.weight, std=width ** -0.5)
         torch.nn.init.normal_(self.before.weight, std=width ** -0.5)
         self.layers = torch.nn.ModuleList(
-            [Layer(width, heads, value_heads) for _ in range(layers)])
+            [layer(width, heads, value_heads) for _ in range(layers)])
         self.norm_w = torch.nn.Parameter(torch.ones(width))
         self.norm_b = torch.nn.Parameter(torch.zeros(width))
 
@@ -142,11 +142,11 @@ def batch(n, length, vocabulary, gen):
 
 
 def run(steps=200, sequences=32, length=32, vocabulary=64, width=256, heads=2, value_heads=4,
-        layers=2, lr=2e-3, seed=0, verbose=True):
+        layers=2, lr=2e-3, seed=0, verbose=True, layer=Layer):
     """Trains and serves; returns (first loss, last loss, share of repeated tokens right)."""
     torch.manual_seed(seed)
     gen = torch.Generator("cuda").manual_seed(seed)
-    model = Model(vocabulary, width, heads, value_heads, layers).cuda()
+    model = Model(vocabulary, width, heads, value_heads, layers, layer).cuda()
     optim = torch.optim.AdamW(model.parameters(), lr=lr)
     losses = []
     for i in range(steps):

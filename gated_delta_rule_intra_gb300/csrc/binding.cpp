@@ -302,18 +302,20 @@ bool row_stride(const Tensor *t, at::IntArrayRef shape, ScalarType type, int dev
         if (shape[i] > 1 && st[i] != width) return false;
         width *= shape[i];
     }
-    int64_t step = 0, run = 0;
+    int64_t step = width, run = 0;
+    bool any = false;
     for (size_t i = lead; i-- > 0;) {
         if (shape[i] == 1) continue;
-        if (!step)
+        if (!any)
             step = st[i];
         else if (st[i] != run)
             return false;
+        any = true;
         run = shape[i] * st[i];
     }
-    if (t->numel() == 0) step = 0;
-    if (step && step < width) return false;
-    stride = step ? step : width;
+    if (t->numel() == 0) step = width;
+    if (step < width) return false;  // rows on one another: an expanded dimension
+    stride = step;
     return true;
 }
 // Sequences packed along T, 0 without cu_seqlens; -1 for a table that is not taken.
