@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
                             phase.load4(oB[n] + toC + 16 * g, C);
 #pragma unroll
                             for (int t = 1; t >= 0; --t) {
-                                const float2 e = mul2(d[t], A2[j][n]), in = mul2(gg[t], C[t]);
+                                const float2 e = exponent(d[t], A2[j][n]), in = mul2(gg[t], C[t]);
                                 carry[j][n] = (carry[j][n] + in.y) * ex2(e.y);
                                 carry[j][n] = (carry[j][n] + in.x) * ex2(e.x);
                             }
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
                                 phase.load4(oB[n] + 16 * g, B);
 #pragma unroll
                                 for (int t = 0; t < 2; ++t) {
-                                    const float2 e = mul2(d[t], A2[j][n]);
+                                    const float2 e = exponent(d[t], A2[j][n]);
                                     float2 &pp = P[j][n][2 * gl + t];
                                     pp.x = ex2(e.x) * h[j][n];
                                     pp.y = ex2(e.y) * fmaf(x[t].x, B[t].x, pp.x);
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
 #pragma unroll
                             for (int n = 0; n < 4; ++n) {
                                 const float2 pp = P[j][n][pi];
-                                const float2 e = mul2(d, A2[j][n]), hh = fma2(x, B[n], pp);
+                                const float2 e = exponent(d, A2[j][n]), hh = fma2(x, B[n], pp);
                                 float2 G;
                                 G.y = fmaf(gg.y, C[n].y, carry[j][n]);
                                 G.x = fmaf(gg.x, C[n].x, G.y * ex2(e.y));

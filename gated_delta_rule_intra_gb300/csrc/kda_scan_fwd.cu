@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
                         float2 sum;
 #pragma unroll
                         for (int n = 0; n < 4; ++n) {
-                            const float2 e = mul2(d[t], A2[j][n]), in = mul2(x[t], B[n][t]);
+                            const float2 e = exponent(d[t], A2[j][n]), in = mul2(x[t], B[n][t]);
                             float2 hh;
                             hh.x = fmaf(ex2(e.x), h[j][n], in.x);
                             hh.y = fmaf(ex2(e.y), hh.x, in.y);
