@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(256) kda_conv_sum_kernel(const ConvArgs a) {
 // Gradients of the inputs in front of each sequence: its first W - 1 values of g again.
 template <typename T> __global__ void __launch_bounds__(256) kda_conv_initial_kernel(const ConvArgs a) {
     wait_for_previous();
-    const int c = blockIdx.x * 256 + threadIdx.x, n = blockIdx.y, W = a.W;
+    const int blocks = (a.D + 255) / 256, c = blockIdx.x % blocks * 256 + threadIdx.x, n = blockIdx.x / blocks, W = a.W;
     if (c >= a.D) return;
     Piece p;
     p.seq = n;
@@ -259,8 +259,8 @@ template <typename T, int W> cudaError_t backward(const ConvArgs &a, cudaStream_
 template <typename T> cudaError_t backward(const ConvArgs &a, cudaStream_t stream) {
     if (a.d_initial) {
         const cudaError_t e = launch_early(kda_conv_initial_kernel<T>,
-                                           dim3((unsigned)((a.D + 255) / 256), (unsigned)a.tok.num_seqs),
-                                           256, 0, stream, a);
+                                           (unsigned)((a.D + 255) / 256 * (long long)a.tok.num_seqs), 256, 0,
+                                           stream, a);
         if (e != cudaSuccess) return e;
     }
     return a.W == 4 ? backward<T, 4>(a, stream) : a.W == 3 ? backward<T, 3>(a, stream) : backward<T, 2>(a, stream);

@@ -125,9 +125,8 @@ struct GemmArgs {
 size_t gemm_partial_bytes(int M, int N, int K);
 cudaError_t launch_gemm(const GemmArgs &a, cudaStream_t stream);
 
-// The same for a few rows: M at most kSmallM, K-major operands.
-constexpr int kSmallM = 16;
-bool small_gemm_ok(const GemmArgs &a);
+// The same for a few rows of K-major operands, the contraction a multiple of 8.
+inline bool small_gemm_ok(int M, int K) { return M <= 16 && K % 8 == 0; }
 cudaError_t launch_small_gemm(const GemmArgs &a, cudaStream_t stream);
 
 // Rows copied to such boundaries: dst's rows are ld elements apart, a multiple of 8.

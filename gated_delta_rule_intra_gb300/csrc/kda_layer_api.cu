@@ -204,7 +204,7 @@ kda_status_t kda_conv_bwd(const void *dy, const void *x, const void *weight, con
     if (st != KDA_OK) return st;
     if (!weight || (T > 0 && (!x || !dy || !dx)) || !dweight != !dbias) return KDA_ERR_NULL;
     if (!stride_ok(op.x_stride, D) || !stride_ok(op.dy_stride, D) || !stride_ok(op.dx_stride, D) ||
-        tok.num_seqs > 65535 * 1LL * (op.d_initial_state ? 1 : 32768))
+        !grid_ok(tok.pieces(64) * ((D + 31) / 32)))
         return KDA_ERR_SHAPE;
     const int es = kda::esize(dtype), ws = kda::esize(wdtype);
     const void *ae[] = {x, dy, dx, op.initial_state, op.d_final_state, op.d_initial_state};
@@ -508,7 +508,7 @@ kda_status_t kda_scan_step(const void *u, const void *delta, const float *A, con
 size_t kda_linear_fwd_workspace_bytes(int M, int K, int N, int copies) {
     if (check_linear(M, K, N, KDA_BF16, 0) != KDA_OK || M == 0) return 0;
     return (copies & KDA_COPY_X ? copy_bytes(M, K) : 0) + (copies & KDA_COPY_WEIGHT ? copy_bytes(N, K) : 0) +
-           (M <= kda::kSmallM ? 0 : up256(kda::gemm_partial_bytes(M, N, K)));
+           (kda::small_gemm_ok(M, K) ? 0 : up256(kda::gemm_partial_bytes(M, N, K)));
 }
 
 int kda_linear_copies(const void *x, long long x_stride, const void *weight, long long weight_stride,
@@ -557,7 +557,7 @@ kda_status_t kda_linear_fwd(const void *x, const void *weight, void *y, int M, i
     a.fp16 = dtype == KDA_FP16;
     a.partial = (float *)w.at;
     a.dbg = kda::debug_flags();
-    return finish(kda::small_gemm_ok(a) ? kda::launch_small_gemm(a, (cudaStream_t)stream)
+    return finish(kda::small_gemm_ok(M, K) ? kda::launch_small_gemm(a, (cudaStream_t)stream)
                                         : kda::launch_gemm(a, (cudaStream_t)stream));
 }
 

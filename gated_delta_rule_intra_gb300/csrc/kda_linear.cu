@@ -51,7 +51,7 @@ struct Params {
     const void *bias, *residual;
     void *y, *pre;
     long long ldr, ldy, ldp;
-    int act, split_n;
+    int act;
     float *partial;  // [splits][M][ldw], or null
     int ldw;
     bool tma_out;         // y and pre leave by TMA

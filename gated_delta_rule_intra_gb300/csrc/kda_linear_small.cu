@@ -210,8 +210,6 @@ cudaError_t launch_copy_rows(const CopyArgs &a, const CopyArgs *b, cudaStream_t 
     return launch_early(linear::kda_linear_copy_kernel, first + (b ? blocks(*b) : 0), 256, 0, stream, a, b ? *b : a, first);
 }
 
-bool small_gemm_ok(const GemmArgs &a) { return a.M <= kSmallM && !a.a_mn && !a.b_mn && a.K % 8 == 0; }
-
 cudaError_t launch_small_gemm(const GemmArgs &a, cudaStream_t stream) {
     return a.fp16 ? linear::small<__half>(a, stream) : linear::small<__nv_bfloat16>(a, stream);
 }

@@ -515,7 +515,6 @@ template <typename T, int NP> cudaError_t launch(const ScanArgs &a, cudaStream_t
 
 template <typename T> cudaError_t pick(const ScanArgs &a, cudaStream_t stream) {
     switch (scan_padded(a.N)) {
-        
         case 8: return launch<T, 8>(a, stream);
         case 16: return launch<T, 16>(a, stream);
         case 32: return launch<T, 32>(a, stream);

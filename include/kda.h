@@ -502,8 +502,8 @@ kda_status_t kda_layer_norm_bwd(const void *dy, const void *x, const void *weigh
  * time.
  *
  * Backward: dx, and dweight [D, W], dbias [D] fp32 (both or neither), summed over the tokens in a
- * fixed order; d_final_state (NULL = zeros) and d_initial_state (written, NULL = not wanted, at most
- * 65535 sequences) are like the states.  `workspace` holds kda_conv_bwd_workspace_bytes() bytes,
+ * fixed order; d_final_state (NULL = zeros) and d_initial_state (written, NULL = not wanted)
+ * are like the states.  `workspace` holds kda_conv_bwd_workspace_bytes() bytes,
  * 16-byte aligned (not needed without dweight).
  *
  * kda_conv_step: one token for each of N <= 65535 requests, x, y [N, D], `state` [num_states, W - 1,

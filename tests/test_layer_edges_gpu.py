@@ -9,7 +9,7 @@ import torch
 import gated_delta_rule_intra_gb300 as kda
 from gated_delta_rule_intra_gb300 import conv, linear, scan
 from tests._layer import (BF, F32, F64, HF, SCAN, conv64, cu, cuda, make_conv, make_linear, make_scan,
-                          scan64)
+                          rel, scan64, tol)
 from tests.test_recurrence_edges_gpu import _debug
 
 pytestmark = pytest.mark.gpu
@@ -84,6 +84,51 @@ def test_debug_build_of_single_tokens(D, N, R, dtype):
         return y, cs, kda.kda_scan_step(*ins, ss, *more, state_indices=idx), ss
 
     _debug(call)
+
+
+# ---------------------------------------------------------------------------- sizes
+@pytest.mark.parametrize("M,K,N", [(5, 1111, 70), (16, 2049, 130), (1, 8191, 24)])
+def test_few_rows_of_an_odd_contraction(M, K, N):
+    """They take the tensor-memory kernel, the contraction cut into parts: with its workspace."""
+    x = make_linear(M, K, N, BF, seed=K)
+    c = cuda(x)
+    copies = 3 if K % 8 else 0
+    assert kda.load_library().kda_linear_fwd_workspace_bytes(M, K, N, copies) >= \
+        2 * (M + N) * K + 4 * 2 * M * N  # the rows' copies, two parts at least
+    y = kda.kda_linear_fwd(c["x"], c["weight"], c["bias"])[0]
+    assert rel(y, x["x"].to(F64) @ x["weight"].to(F64).T + x["bias"].to(F64)) <= tol(BF)
+
+
+def test_more_sequences_than_a_grid_is_high():
+    """70,000 sequences of one token, and their states."""
+    n, D = 70000, 8
+    x = cuda(make_conv(n, 1, D, 4, HF, seed=1))
+    y, last = kda.kda_conv_fwd(x["x"], x["weight"], x["bias"], x["initial"], output_final_state=True)
+    dx, dw, db, di = kda.kda_conv_bwd(x["dy"], x["x"], x["weight"], x["bias"], x["initial"], x["dfinal"],
+                                      output_d_initial_state=True)
+    seq = torch.cat([x["initial"], x["x"]], 1).double()
+    w, dy, df = x["weight"].double(), x["dy"].double(), x["dfinal"].double()
+    assert rel(y[:, 0], (seq * w.T).sum(1) + x["bias"].double()) <= tol(HF)
+    assert torch.equal(last, seq[:, 1:].to(HF))
+    ds = dy * w.T
+    ds[:, 1:] += df
+    assert rel(torch.cat([di, dx], 1), ds) <= tol(HF)
+    # FP32 sums of 70,000 terms of random sign: their 2^-24 each, some hundred times over
+    assert rel(dw, (dy * seq).sum(0).T) <= 1e-5 and rel(db, dy.sum((0, 1))) <= 1e-5
+    s = cuda(make_scan(n, 1, D, 4, 1, HF, seed=2))
+    ins, more = [s[m] for m in SCAN[:5]], [s[m] for m in SCAN[5:]]
+    y, last, saved = kda.kda_scan_fwd(*ins, *more, s["initial"], save=True, output_final_state=True)
+    out = kda.kda_scan_bwd(s["dy"], *ins, saved, *more, s["dfinal"], output_d_initial_state=True)
+    few = slice(n - 50, n)
+    part = {k: (t[few].cpu() if t.shape[0] == n else t.cpu()) for k, t in s.items()}
+    h = {k: part[k].to(F64).requires_grad_() for k in (*SCAN, "initial")}
+    want, final = scan64(*h.values())
+    loss = (want * part["dy"].to(F64)).sum() + (final * part["dfinal"].to(F64)).sum()
+    ref = dict(zip(h, torch.autograd.grad(loss, list(h.values()))))
+    assert rel(y[few], want) <= tol(HF) and rel(last[few], final) <= 1e-5
+    for got, name in zip(out, (*SCAN, "initial")):
+        if got.shape[0] == n:
+            assert rel(got[few], ref[name]) <= tol(HF) + 1e-5, name
 
 
 # ---------------------------------------------------------------------------- streams and graphs
