@@ -590,7 +590,11 @@ struct Plan {
 Plan plan_of(int M, int N, int K) {
     Plan q;
     auto tiles = [&](int bm, int bn) { return (long long)((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-    q.pair = tiles(256, 256) >= kSMs / 2;
+    // pairs of CTAs: where there is a tile for each, or where a long contraction outweighs the 3 us that
+    // they start later (alone and in pairs, us: 8192 x 2048 x 2048, 256 tiles, 60 and 44; 2560 x 2048 x
+    // 4096, 80 tiles, 48 and 42; 2048 x 1280 x 4096, 40 tiles, 26.5 and 25.4; 1536 x 2048 x 2048, 48
+    // tiles, 16.0 and 16.7; 32 x 8192 x 8192, 32 tiles, 40 and 42)
+    q.pair = tiles(256, 256) >= (K >= 4096 ? 40 : kSMs / 2);
     q.bn = 256;
     if (!q.pair) {
         // the width whose rounds of tiles take least: a stage's products take BN / 4 of 64 cycles, its

@@ -297,18 +297,34 @@ template <typename T> cudaError_t pick(const ScanArgs &a, cudaStream_t stream) {
 }  // namespace
 }  // namespace scan
 
-// Tokens of a segment: whole sequences where there is a CTA for every multiprocessor, otherwise so many
-// segments that there are some four.
+// Tokens of a segment.  Sequences of one length are cut where the rounds of two CTAs a multiprocessor
+// (in tokens that one walks, and 32 for its start) and the first pass, which costs 0.7 of the second
+// forward and 0.35 backward, take less than walking them whole; a CTA that is alone on its
+// multiprocessor takes nine tenths of the time of two.  4096 tokens, 16 states, forward and backward, us:
+//   64 chains of 64 channels: 9 segments 184 and 442, whole 331 and 968; 128: 7 segments 339 and 813,
+//   whole 425 and 1332; 192: 3 segments 506 and 1220, whole 478 and 1432; 256: 677 and 1612, 477 and 1438.
+// Packed ones, whose lengths the host does not know, take four segments a multiprocessor in all (9467 tokens
+// in 9 sequences, 16 chains: 120 and 285; two 118 and 293, six 129 and 304).
 int scan_segment(const Tokens &tok, int D, int N, int G, bool back) {
-    const long long blocks = scan_blocks(D, N, G), want = 4 * kSMs;
-    const long long rows = tok.rows(), longest = tok.cu_seqlens ? rows : tok.T;
-    long long cuts = want / blocks;  // segments of all tokens together
-    if (cuts < 1) cuts = 1;
-    const long long whole = (longest + kScanTile - 1) / kScanTile * kScanTile;
-    if (!tok.cu_seqlens && tok.num_seqs * blocks >= kSMs) return (int)(whole ? whole : kScanTile);
-    long long seg = (rows / cuts + kScanTile - 1) / kScanTile * kScanTile;
-    if (seg < 8 * kScanTile) seg = 8 * kScanTile;
-    return (int)(seg < whole ? seg : whole ? whole : kScanTile);
+    const long long blocks = scan_blocks(D, N, G), chains = tok.num_seqs * blocks, slots = 2 * kSMs;
+    auto tiles = [](long long tokens) { return (tokens + kScanTile - 1) / kScanTile * kScanTile; };
+    const long long whole = tok.T ? tiles(tok.T) : kScanTile, least = 8 * kScanTile;
+    long long best = whole;
+    if (tok.cu_seqlens) {
+        const long long cuts = 2 * slots / blocks, seg = tiles(tok.T / (cuts > 1 ? cuts : 1));
+        best = seg < least ? least : seg;
+    } else {
+        long long cost = (chains + slots - 1) / slots * (whole + 32) * (chains <= kSMs ? 18 : 20);
+        for (int rounds = 1; rounds <= 8; ++rounds) {
+            const long long n = rounds * slots / chains, even = n > 1 ? tiles((tok.T + n - 1) / n) : whole;
+            const long long seg = even < least ? least : even, c = rounds * (seg + 32) * (back ? 27 : 34);
+            if (seg < whole && c < cost) {
+                cost = c;
+                best = seg;
+            }
+        }
+    }
+    return (int)(best < whole ? best : whole);
 }
 
 cudaError_t launch_scan_fwd(const ScanArgs &a, cudaStream_t stream) {
