@@ -12,7 +12,8 @@ namespace {
 // left operands of mma.sync (16 rows of the weight a CTA, the contraction cut over its eight warps);
 // the few rows of x are the right operands.  Which k an operand's places stand for does not matter
 // as long as both agree, so a lane takes 16 consecutive bytes of its row: four of them are two
-// products' operands.  The tensor-memory path would move 128 rows of x for these few.
+// products' operands.  The tensor-memory path would move 128 rows of x for these few: 2048 x 8192 takes
+// 5.1 us for 4 rows (6.6 TB/s, from L2), 8.6 for 16, and 15 there; 8192 x 2048 11.1 for 16, and 12.8.
 constexpr int kWarps = 8, kAhead = 4;
 
 template <typename T>
@@ -111,7 +112,8 @@ __global__ void __launch_bounds__(256) kda_linear_copy_kernel(const CopyArgs a0,
 }
 
 // dpre and the sums of its columns.  A warp has 32 V neighbouring columns of every eighth row of its
-// CTA's part; the CTAs' sums are joined in order by a second kernel.
+// CTA's part; the CTAs' sums are joined in order by a second kernel.  Bound by memory: 8192 x 8192 with
+// gelu 77 us, 5.2 TB/s.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) kda_linear_dact_kernel(const DActArgs a, int rows_each) {
     wait_for_previous();

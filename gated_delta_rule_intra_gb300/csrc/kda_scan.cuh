@@ -11,8 +11,8 @@
 // tokens of a number at once, and products of neighbouring tokens are one instruction (f32x2).
 // Two channels a thread, because every byte that a lane reads from shared memory costs the same
 // whether or not its neighbours read it too: with one channel a thread, B and C alone are 2.5 of the
-// 4 cycles that the exponentials leave (scan_train's forward took 475 us).  Sums over a channel's
-// states are taken for four tokens at once, each lane ending with one token's.
+// 4 cycles that the exponentials leave.  Sums over a channel's states are taken for four tokens at once,
+// each lane ending with one token's.
 //
 // A sequence is one chain; where there are too few channels to fill the card it is cut into
 // segments.  A first pass walks them all from zero and leaves each one's end (and the sum of its
