@@ -18,7 +18,8 @@
 // Bound by the tensor cores: 32768 x 2048 x 8192 bf16 with silu 555 us, 1.98 PFLOP/s (the library's plain
 // product 543; 788 without pairs, 705 with copies and products issued under a test of the lane, which
 // makes the compiler take every operand of theirs through a loop); 8192 x 2048 x 8192 with gelu and a
-// second result 163, its gradients 167 and 168 (256 tiles are 3.4 rounds of 76 pairs).
+// second result 162, its gradients 395 with the 80 of their first step (256 tiles are 3.4 rounds of 76
+// pairs; with whole tiles in the last one too 449).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -53,6 +54,7 @@ struct Maps {
 
 struct Params {
     int M, N, K, nt, tiles, splits, per;  // tiles across N; of C; parts of K, blocks of 64 of each
+    int work, full;  // pieces of work; those from `full` on are halves of tiles
     const void *bias, *residual;
     void *y, *pre;
     long long ldr, ldy, ldp;
@@ -187,16 +189,19 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 }
 
 struct Tile {
-    int m, n, kb, ke;  // first row and column, blocks of K
+    int m, n, cols, kb, ke;  // first row and column, columns, blocks of K
 };
 // Tiles go down 16 rows of tiles before the next column, so that those at work at one time share
 // both operands' tiles in L2.
 __device__ __forceinline__ Tile tile_of(const Params &p, int i, int rows_each, int BN) {
     Tile t;
+    const bool half = i >= p.full, right = half && (i - p.full & 1);
+    if (half) i = p.full + (i - p.full) / 2;
     const int s = i / p.tiles, j = i - s * p.tiles, mt = p.tiles / p.nt;
     const int group = j / (16 * p.nt), rows = min(16, mt - group * 16), r = j - group * 16 * p.nt;
     t.m = (group * 16 + r % rows) * rows_each;
-    t.n = r / rows * BN;
+    t.n = r / rows * BN + (right ? BN / 2 : 0);
+    t.cols = half ? BN / 2 : BN;
     t.kb = s * p.per;
     t.ke = min(t.kb + p.per, (p.K + BK - 1) / BK);
     return t;
@@ -311,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (said to be the same in all lanes: in code that might diverge, every operand of an asynchronous
     // instruction goes through a loop over the lanes, and a stage took 810 cycles instead of 512)
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-    const int work = p.tiles * p.splits;
+    const int work = p.work;
     const int rank = PAIR ? (int)cluster_rank() : 0;
     const int first = PAIR ? (int)blockIdx.x / 2 : (int)blockIdx.x, step = PAIR ? (int)gridDim.x / 2 : (int)gridDim.x;
     if (threadIdx.x == 0) {
@@ -344,14 +349,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int i = first; i < work && ok; i += step) {
             const Tile t = tile_of(p, i, kRows, BN);
-            const int m = t.m + rank * BM, nn = t.n + rank * C::kRowsB;
+            const int rows = PAIR ? t.cols / 2 : C::kRowsB, m = t.m + rank * BM, nn = t.n + rank * rows;
             for (int kb = t.kb; kb < t.ke; ++kb, ++n) {
                 const int st = n % C::kStages;
                 if (n >= C::kStages && !(ok = wait(empty + st, (n / C::kStages - 1) & 1))) break;
                 if (tc::elect_one()) {
                     const uint32_t a = tc::smem_u32(base + st * C::kStage), b = a + C::kA;
                     // (a pair's first CTA waits for both's bytes)
-                    if (!PAIR || rank == 0) tc::mbar_arrive_expect_tx(full + st, (PAIR ? 2 : 1) * C::kStage);
+                    if (!PAIR || rank == 0) tc::mbar_arrive_expect_tx(full + st, (PAIR ? 2 : 1) * (C::kA + rows * BK * 2));
                     if (A_MN) {
 #pragma unroll
                         for (int x = 0; x < BM / 64; ++x)
@@ -359,10 +364,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         load_2d<PAIR>(a, &maps.a, kb * BK, m, bars + 8 * st);
                     }
-                    if (B_MN) {
+                    if (B_MN || PAIR) {
 #pragma unroll
                         for (int x = 0; x < C::kRowsB / 64; ++x)
-                            load_2d<PAIR>(b + x * 8192, &maps.b, nn + 64 * x, kb * BK, bars + 8 * st);
+                            if (64 * x < rows)
+                                load_2d<PAIR>(b + x * 8192, &maps.b, B_MN ? nn + 64 * x : kb * BK,
+                                              B_MN ? kb * BK : nn + 64 * x, bars + 8 * st);
                     } else {
                         load_2d<PAIR>(b, &maps.b, kb * BK, nn, bars + 8 * st);
                     }
@@ -375,7 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_wait(full + s % C::kStages, (s / C::kStages) & 1, kWaitPolls);
     } else if (warp == 1) {
         if (rank == 0) {
-            constexpr uint32_t idesc = idesc16(std::is_same<T, __half>::value, A_MN, B_MN, kRows, BN);
+            constexpr bool fp16 = std::is_same<T, __half>::value;
+            constexpr uint32_t whole = idesc16(fp16, A_MN, B_MN, kRows, BN), half = idesc16(fp16, A_MN, B_MN, kRows, BN / 2);
             constexpr uint32_t kStepA = A_MN ? 2048 : 32, kStepB = B_MN ? 2048 : 32;  // 16 of K
             int n = 0, c = 0;
             bool ok = true;
@@ -383,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Tile t = tile_of(p, i, kRows, BN);
                 if (c >= 2 && !wait(taken + (c & 1), (c / 2 - 1) & 1)) break;
                 tc::fence_after_sync();
-                const uint32_t d = tmem + (c & 1) * BN;
+                const uint32_t d = tmem + (c & 1) * BN, idesc = PAIR && t.cols < BN ? half : whole;
                 for (int kb = t.kb; kb < t.ke; ++kb, ++n) {
                     const int st = n % C::kStages;
                     if (!(ok = wait(full + st, (n / C::kStages) & 1))) break;
@@ -406,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // a warp reads its own 32 lanes of tensor memory, and takes half of a tile's columns
-        const int e = warp - 2, quarter = warp & 3, c0 = e / 4 * (BN / 2);
+        const int e = warp - 2, quarter = warp & 3;
         char *box = out + e * 2048;
         float *bs = bias + e * (BN / 2);
         int c = 0;
@@ -418,7 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         for (int i = first; i < work; i += step, ++c) {
             const Tile t = tile_of(p, i, kRows, BN);
-            const int m0 = t.m + rank * BM + 32 * quarter, n0 = t.n + c0, n1 = min(p.N - n0, BN / 2);
+            const int each = PAIR ? t.cols / 2 : BN / 2, c0 = e / 4 * each;
+            const int m0 = t.m + rank * BM + 32 * quarter, n0 = t.n + c0, n1 = min(p.N - n0, each);
             auto addend = [&](int n) {
                 begin();
                 box_in(box, p.residual, p.ldr, m0, n0 + n, p.M, p.N, lane, p.unit_r);
@@ -636,7 +645,7 @@ cudaError_t launch(const Maps &maps, const Params &p, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = smem_limit_once(kernel, kBytes, dev, done);
     if (e != cudaSuccess) return e;
-    const int work = p.tiles * p.splits;
+    const int work = p.work;
     if (!PAIR) return launch_early(kernel, (unsigned)(work < kSMs ? work : kSMs), kThreads, kBytes, stream, maps, p);
     cudaLaunchAttribute attrs[2] = {};
     attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -668,12 +677,20 @@ template <typename T> cudaError_t run(const GemmArgs &a, cudaStream_t stream) {
                            : encode(&maps.a, a.fp16, a.A, a.K, a.M, a.lda, BK, BM);
     if (e == cudaSuccess)
         e = a.b_mn ? encode(&maps.b, a.fp16, a.B, a.N, a.K, a.ldb, 64, BK)
-                   : encode(&maps.b, a.fp16, a.B, a.K, a.N, a.ldb, BK, q.pair ? q.bn / 2 : q.bn);
+                   : encode(&maps.b, a.fp16, a.B, a.K, a.N, a.ldb, BK, q.pair ? 64 : q.bn);
     if (e != cudaSuccess) return e;
     Params p = {};
     p.M = a.M; p.N = a.N; p.K = a.K;
     p.nt = (a.N + q.bn - 1) / q.bn;
     p.tiles = q.tiles; p.splits = q.splits; p.per = q.per;
+    p.work = q.tiles * q.splits;
+    p.full = p.work;
+    // pairs share the last round out by halves of tiles where that leaves no second one
+    const int rest = q.pair ? q.tiles % (kSMs / 2) : 0;
+    if (rest * 2 <= kSMs / 2) {
+        p.work += rest;
+        p.full -= rest;
+    }
     p.bias = a.bias; p.residual = a.residual; p.y = a.y; p.pre = a.pre;
     p.ldr = a.ldr; p.ldy = a.ldy; p.ldp = a.ldp;
     p.act = a.act;
