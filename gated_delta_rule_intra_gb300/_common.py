@@ -144,7 +144,7 @@ def declare(lib):
             ("kda_conv_bwd_workspace_bytes", z, [i] * 5),
             ("kda_conv_bwd", i, [vp] * 7 + [i] * 7 + [vp, vp]),
             ("kda_conv_step", i, [vp] * 5 + [i] * 6 + [vp, vp]),
-            ("kda_scan_saved_bytes", z, [i] * 6),
+            ("kda_scan_saved_bytes", z, [i] * 5),
             ("kda_scan_fwd_workspace_bytes", z, [i] * 6),
             ("kda_scan_fwd", i, [vp] * 6 + [i] * 6 + [vp, vp]),
             ("kda_scan_bwd_workspace_bytes", z, [i] * 6),

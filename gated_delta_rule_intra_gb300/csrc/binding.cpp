@@ -504,7 +504,7 @@ PyObject *scan_fwd(PyObject *const *a) {
         op.final_state = (float *)out[1].data_ptr();
     }
     if (save) {
-        op.saved_bytes = function<decltype(&kda_scan_saved_bytes)>(a[1])((int)B, (int)T, x.D, x.N, seqs, x.dtype);
+        op.saved_bytes = function<decltype(&kda_scan_saved_bytes)>(a[1])((int)B, (int)T, x.D, x.N, seqs);
         out[2] = bytes(op.saved_bytes, *x.u);
         op.saved = out[2].data_ptr();
     }
@@ -536,7 +536,7 @@ PyObject *scan_bwd(PyObject *const *a) {
     const int64_t B = x.u->size(0), T = x.u->size(1), n = saved->numel();
     const int seqs = sequences(a[13], B, x.dev, cu);
     if (seqs < 0 || B == 0 || !fits(saved, {n}, at::kByte, x.dev) ||
-        (size_t)n != function<decltype(&kda_scan_saved_bytes)>(a[1])((int)B, (int)T, x.D, x.N, seqs, x.dtype))
+        (size_t)n != function<decltype(&kda_scan_saved_bytes)>(a[1])((int)B, (int)T, x.D, x.N, seqs))
         Py_RETURN_NONE;
     const at::IntArrayRef s = x.u->sizes(), v = x.B->sizes();
     Tensor out[9] = {empty(s, x.type, *x.u), empty(s, x.type, *x.u), empty({x.D, x.N}, at::kFloat, *x.u),

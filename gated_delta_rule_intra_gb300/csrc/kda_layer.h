@@ -65,7 +65,7 @@ struct ScanArgs {
     const float *initial;                // [num_seqs, D, N] or null = zeros
     float *final;                        // the same, or null
     float *saved;                        // states in front of every kScanTile / 2 tokens, or null
-    void *open;                          // [rows, D]: y before the gate, or null
+    float *open;                         // [rows, D rounded up to 4]: y before the gate, or null
     int D, N, G, dtype;
     bool softplus;
     long long u_stride, delta_stride, z_stride, B_stride, C_stride, y_stride;

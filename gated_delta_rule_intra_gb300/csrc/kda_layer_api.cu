@@ -84,8 +84,8 @@ kda_status_t scan_shape(int B, int T, int D, int N, int G, int num_seqs, Tokens 
 size_t scan_saved_floats(const Tokens &t, int D, int N) {
     return 2 * (size_t)t.pieces(kda::kScanTile) * D * kda::scan_padded(N);
 }
-size_t scan_saved_bytes(const Tokens &t, int D, int N, int dtype) {  // and y before the gate
-    return up256(scan_saved_floats(t, D, N) * 4) + up256((size_t)t.rows() * D * kda::esize(dtype));
+size_t scan_saved_bytes(const Tokens &t, int D, int N) {  // and y before the gate
+    return up256(scan_saved_floats(t, D, N) * 4) + up256((size_t)t.rows() * (((size_t)D + 3) / 4 * 16));
 }
 // Floats of the first pass over segments; 0 where every sequence is one segment.
 struct Segments {
@@ -272,10 +272,10 @@ kda_status_t kda_conv_step(const void *x, const void *weight, const void *bias, 
     return finish(kda::launch_conv_step(a, (cudaStream_t)stream));
 }
 
-size_t kda_scan_saved_bytes(int B, int T, int D, int N, int num_seqs, int dtype) {
+size_t kda_scan_saved_bytes(int B, int T, int D, int N, int num_seqs) {
     Tokens tok;
-    if (scan_shape(B, T, D, N, 1, num_seqs, tok) != KDA_OK || !any_type(dtype)) return 0;
-    return scan_saved_bytes(tok, D, N, dtype);
+    if (scan_shape(B, T, D, N, 1, num_seqs, tok) != KDA_OK) return 0;
+    return scan_saved_bytes(tok, D, N);
 }
 
 size_t kda_scan_fwd_workspace_bytes(int B, int T, int D, int N, int G, int num_seqs) {
@@ -309,7 +309,7 @@ kda_status_t kda_scan_fwd(const void *u, const void *delta, const float *A, cons
     const void *a4[] = {A, op.skip, op.delta_bias, op.cu_seqlens, op.initial_state, op.final_state};
     const void *a256[] = {op.saved, op.workspace};
     if (misaligned(ae, es) || misaligned(a4, 4) || misaligned(a256, 256)) return KDA_ERR_ALIGN;
-    const size_t saved = scan_saved_bytes(tok, D, N, dtype);
+    const size_t saved = scan_saved_bytes(tok, D, N);
     const size_t need = kda_scan_fwd_workspace_bytes(B, T, D, N, G, op.num_seqs);
     if ((op.saved && op.saved_bytes != saved) || (need && (!op.workspace || op.workspace_bytes < need)))
         return KDA_ERR_WORKSPACE;
@@ -339,7 +339,7 @@ kda_status_t kda_scan_fwd(const void *u, const void *delta, const float *A, cons
     a.initial = op.initial_state;
     a.final = op.final_state;
     a.saved = (float *)op.saved;
-    if (op.saved && op.z) a.open = (char *)op.saved + up256(scan_saved_floats(tok, D, N) * 4);
+    if (op.saved && op.z) a.open = (float *)((char *)op.saved + up256(scan_saved_floats(tok, D, N) * 4));
     a.D = D; a.N = N; a.G = G; a.dtype = dtype;
     a.softplus = !op.plain_delta;
     a.u_stride = op.u_stride; a.delta_stride = op.delta_stride; a.z_stride = op.z_stride;
@@ -402,7 +402,7 @@ kda_status_t kda_scan_bwd(const void *dy, const void *u, const void *delta, cons
     if (misaligned(ae, es) || misaligned(a4, 4) || misaligned(a256, 256)) return KDA_ERR_ALIGN;
     const Segments s(tok, D, N, G, true);
     size_t part[5];
-    const size_t saved = scan_saved_bytes(tok, D, N, dtype);
+    const size_t saved = scan_saved_bytes(tok, D, N);
     const size_t need = scan_bwd_work(tok, D, N, G, s, part);
     if (!op.saved || op.saved_bytes != saved || !op.workspace || op.workspace_bytes < need)
         return KDA_ERR_WORKSPACE;
@@ -431,7 +431,7 @@ kda_status_t kda_scan_bwd(const void *dy, const void *u, const void *delta, cons
     a.u = u; a.delta = delta; a.z = op.z; a.B = Bm; a.C = Cm;
     a.A = A; a.skip = op.skip; a.delta_bias = op.delta_bias;
     a.saved = (float *)op.saved;
-    if (op.saved && op.z) a.open = (char *)op.saved + up256(scan_saved_floats(tok, D, N) * 4);
+    if (op.saved && op.z) a.open = (float *)((char *)op.saved + up256(scan_saved_floats(tok, D, N) * 4));
     a.D = D; a.N = N; a.G = G; a.dtype = dtype;
     a.softplus = !op.plain_delta;
     a.u_stride = op.u_stride; a.delta_stride = op.delta_stride; a.z_stride = op.z_stride;

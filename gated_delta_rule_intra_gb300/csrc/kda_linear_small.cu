@@ -111,7 +111,8 @@ __global__ void __launch_bounds__(256) kda_linear_copy_kernel(const CopyArgs a0,
     *(uint4 *)((uint16_t *)a.dst + r * a.ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// dpre and the sums of its columns.  A warp has 32 V neighbouring columns of every eighth row of its
+// dpre and the sums of its columns.  dpre is rounded to 16 bits because the products that read it take 16-bit
+// operands; its sums take it as it is.  A warp has 32 V neighbouring columns of every eighth row of its
 // CTA's part; the CTAs' sums are joined in order by a second kernel.  Bound by memory: 8192 x 8192 with
 // gelu 77 us, 5.2 TB/s.
 template <typename T, int V>

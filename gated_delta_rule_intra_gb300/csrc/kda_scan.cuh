@@ -134,23 +134,9 @@ __device__ __forceinline__ void store_chunk(void *base, long long stride, long l
             if (i < left) at[i] = x.v[i];
     }
 }
-template <typename T>
-__device__ __forceinline__ Vec<T, 8> load_chunk(const void *base, long long stride, long long row, int c,
-                                                int left, int unit) {
-    const T *at = (const T *)base + row * stride + c;
-    constexpr int E = sizeof(T);
-    Vec<T, 8> x;
-    x.clear();
-    if (unit == 16) {
-#pragma unroll
-        for (int i = 0; i < 8; i += 16 / E)
-            if (i < left) *(uint4 *)(x.v + i) = *(const uint4 *)(at + i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < left) x.v[i] = at[i];
-    }
-    return x;
+// The row of what the gate multiplies, FP32, rows on 16-byte boundaries.
+__device__ __forceinline__ float *open_row(const ScanArgs &a, long long row) {
+    return a.open + row * (long long)((a.D + 3) / 4 * 4);
 }
 template <typename T> __device__ __forceinline__ float2 pair(const Vec<T, 8> &x, int i) { return x.two(2 * i); }
 template <typename T> __device__ __forceinline__ void put_pair(Vec<T, 8> &x, int i, float2 v) {

@@ -13,9 +13,10 @@
 // four states, over the CTA's warps in shared memory and over the CTAs by a second kernel,
 // always in the same order.
 //
-// Bound by what a warp waits for (issue slots 54%, shared memory's data pipe 62%): 727 us at B=4 T=2048
+// Bound by what a warp waits for (issue slots 54%, shared memory's data pipe 62%): 730 us at B=4 T=2048
 // D=4096 N=16 bf16, where the bytes are 79 at a copy's rate and the exponentials 115.  With the gate's
-// factor computed again from the states instead of read it took 954 us, with both halves' registers
+// factor computed again from the states instead of read it took 954 us (the forward leaves it unrounded:
+// 16 bits would save 8 us both ways and make dz's error 1.4 times its rounding), with both halves' registers
 // alike 1038.
 #include "kda_scan.cuh"
 
@@ -340,13 +341,29 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
         vc.put(tid, s.C[b]);
     };
     // What the gate multiplies, on its way a tile ahead of its use.
-    Vec<T, 8> open[S::kPer];
+    float2 open[S::kPer][4];
+    const bool quads = a.D / a.G % 4 == 0;
     auto ungated = [&](int i) {
         const int rows = fine(i) ? rows_of(i) : 0;
 #pragma unroll
         for (int x = 0; x < S::kPer; ++x) {
             const int t = qt + x * kStep;
-            if (!ENDS && a.z && t < kTile && t < rows) open[x] = load_chunk<T>(a.open, a.D, row_of(i) + t, qc, left, unit);
+            if (ENDS || !a.z || t >= kTile || t >= rows) continue;
+            const float *at = open_row(a, row_of(i) + t) + qc;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (quads) {
+                    if (4 * h < left) v = *(const float4 *)(at + 4 * h);
+                } else {
+                    if (4 * h < left) v.x = at[4 * h];
+                    if (4 * h + 1 < left) v.y = at[4 * h + 1];
+                    if (4 * h + 2 < left) v.z = at[4 * h + 2];
+                    if (4 * h + 3 < left) v.w = at[4 * h + 3];
+                }
+                open[x][2 * h] = make_float2(v.x, v.y);
+                open[x][2 * h + 1] = make_float2(v.z, v.w);
+            }
         }
     };
     // What a tile's sums make: the gradients of its tokens (its d, x and g are this thread's own).
@@ -376,7 +393,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
                 if (a.z) {
                     const float2 zz = pair(z, e), sg = sigmoid2(zz);
                     const float2 slope = mul2(sg, fma2(zz, fma2(sg, both(-1.f), both(1.f)), both(1.f)));
-                    put_pair(dz, e, mul2(mul2(pair(dy, e), pair(open[x], e)), slope));
+                    put_pair(dz, e, mul2(mul2(pair(dy, e), open[x][e]), slope));
                 }
             }
             store_chunk(a.du, a.du_stride, row, qc, left, du, unit);
@@ -504,7 +521,6 @@ template <typename T, int NP> cudaError_t launch(const ScanArgs &a, cudaStream_t
     u.add(a.du, a.du_stride);
     u.add(a.ddelta, a.ddelta_stride);
     u.add(a.dz, a.dz_stride);
-    u.add(a.open, a.D);
     cudaError_t e = a.ends ? walk<T, NP, true>(a, nb, u.unit, stream) : cudaSuccess;
     if (e == cudaSuccess) e = walk<T, NP, false>(a, nb, u.unit, stream);
     if (e != cudaSuccess) return e;

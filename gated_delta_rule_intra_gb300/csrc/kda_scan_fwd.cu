@@ -5,7 +5,7 @@
 // tiles ahead.
 //
 // Bound by what a warp waits for (issue slots 55%, shared memory's data pipe 58%; two CTAs a
-// multiprocessor take 478 us for 4096 tokens of 64 channels each, one alone 425): 240 us at B=4 T=2048
+// multiprocessor take 478 us for 4096 tokens of 64 channels each, one alone 425): 245 us at B=4 T=2048
 // D=4096 N=16 bf16 (256 CTAs), where the bytes are 40 at a copy's rate and the exponentials 58.  One
 // channel a thread took 475 us, two without the order of states that lets their sums be shared 387.
 #include "kda_scan.cuh"
@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
         vb.put(tid, s.B[b]);
         if (!ENDS) vc.put(tid, s.C[b]);
     };
+    const bool quads = a.D / a.G % 4 == 0;  // blocks of channels begin on four
     auto finish = [&](int tile) {
         const int rows = rows_of(tile), b = tile & 1;
         auto &raw = s.raw[tile % kStages];
@@ -210,20 +211,33 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
             const float2 sum[4] = {make_float2(lo.x, lo.y), make_float2(lo.z, lo.w), make_float2(hi.x, hi.y),
                                    make_float2(hi.z, hi.w)};
             const Vec<T, 8> u = raw[0][i][tid];
-            Vec<T, 8> z, out, open;
+            Vec<T, 8> z, out;
+            float2 open[4];
             if (a.z) z = raw[2][i][tid];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float2 y = fma2(skip[e], pair(u, e), sum[e]);
                 if (a.z) {
                     const float2 g = pair(z, e);
-                    put_pair(open, e, y);
+                    open[e] = y;
                     y = mul2(y, mul2(g, sigmoid2(g)));
                 }
                 put_pair(out, e, y);
             }
-            // what the gate multiplies, for the gate's gradient, rounded as that will be
-            if (a.open) store_chunk(a.open, a.D, row, qc, left, open, unit);
+            if (a.open) {  // what the gate multiplies, for the gate's gradient
+                float *at = open_row(a, row) + qc;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float2 l = open[2 * h], r = open[2 * h + 1];
+                    if (quads && 4 * h < left) *(float4 *)(at + 4 * h) = make_float4(l.x, l.y, r.x, r.y);
+                    if (!quads) {
+                        const float v[4] = {l.x, l.y, r.x, r.y};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (4 * h + j < left) at[4 * h + j] = v[j];
+                    }
+                }
+            }
             store_chunk(a.y, a.y_stride, row, qc, left, out, unit);
         }
     };
@@ -273,7 +287,6 @@ template <typename T, int NP> cudaError_t launch(const ScanArgs &a, cudaStream_t
     u.add(a.delta, a.delta_stride);
     u.add(a.z, a.z_stride);
     u.add(a.y, a.y_stride);
-    u.add(a.open, a.D);
     const unsigned grid = (unsigned)(a.tok.pieces(a.segment) * nb * a.G);
     constexpr int kBytes = sizeof(Smem<T, NP>);
     static_assert(kBytes <= 227 * 1024, "");

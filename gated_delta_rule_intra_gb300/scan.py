@@ -89,8 +89,8 @@ def kda_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, initial_sta
     d // (D // groups).  A [D, N], D [D] (the skip) and delta_bias [D] fp32.  D, z and delta_bias
     may be None; without ``delta_softplus`` the step sizes are delta + delta_bias as they are.
     ``initial_state`` [sequences, D, N] fp32 defaults to zeros; final_state is None unless
-    ``output_final_state``; saved is what ``kda_scan_bwd`` needs (N / 2 bytes and an
-    element a token and channel), None unless ``save``.  ``cu_seqlens`` (int32 [N + 1] on the device, B = 1) packs
+    ``output_final_state``; saved is what ``kda_scan_bwd`` needs (N / 2 + 4 bytes
+    a token and channel), None unless ``save``.  ``cu_seqlens`` (int32 [N + 1] on the device, B = 1) packs
     sequences along T; y is zero at tokens in no sequence when it is allocated here.
     """
     if stream is None and y is None and delta_softplus:
@@ -126,7 +126,7 @@ def _scan_fwd(u, delta, A, B, C, D, z, delta_bias, initial_state, delta_softplus
         op.final_state = final.data_ptr()
     lib = library()
     if save:
-        size = lib.kda_scan_saved_bytes(batch, T, width, N, seqs, DTYPES[dt])
+        size = lib.kda_scan_saved_bytes(batch, T, width, N, seqs)
         saved = torch.empty(size, dtype=torch.uint8, device=u.device)
         op.saved, op.saved_bytes = saved.data_ptr(), size
     if batch:
@@ -167,7 +167,7 @@ def _scan_bwd(dy, u, delta, A, B, C, saved, D, z, delta_bias, d_final_state, del
     seqs = sequences(cu_seqlens, batch, dev)
     op.dy_stride = row_stride("dy", dy, u.shape, dt, dev)
     lib = library()
-    size = lib.kda_scan_saved_bytes(batch, T, width, N, seqs, DTYPES[dt])
+    size = lib.kda_scan_saved_bytes(batch, T, width, N, seqs)
     if saved.numel() != size:
         raise ValueError(f"saved has {saved.numel()} bytes: not from a forward of these inputs")
     check("saved", saved, (size,), torch.uint8, dev)

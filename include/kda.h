@@ -566,9 +566,9 @@ kda_status_t kda_conv_step(const void *x, const void *weight, const void *bias, 
  * Pointers need their element's alignment (rows on boundaries of four elements are read
  * four channels at a time), saved and workspace 256 bytes.  States, sums and exponentials are FP32.
  *   initial_state, final_state   [sequences, D, N] fp32 as in kda_chunk_fwd
- *   saved, saved_bytes           what kda_scan_bwd needs: kda_scan_saved_bytes(), N / 2 bytes (N rounded
- *                                up to 8, 16, 32 or 64) and an element a token and channel; NULL when
- *                                no backward follows
+ *   saved, saved_bytes           what kda_scan_bwd needs: kda_scan_saved_bytes(), N / 2 + 4 bytes (N
+ *                                rounded up to 8, 16, 32 or 64) a token and channel; NULL when no
+ *                                backward follows
  *   cu_seqlens, num_seqs,        as in kda_chunk_fwd (zero_rest: rows of y D apart)
  *   zero_rest
  *   workspace                    kda_scan_fwd_workspace_bytes() bytes (0 where the card is full of
@@ -599,7 +599,7 @@ typedef struct {
     size_t workspace_bytes;
 } kda_scan_fwd_opts_t;
 
-size_t kda_scan_saved_bytes(int B, int T, int D, int N, int num_seqs, int dtype);
+size_t kda_scan_saved_bytes(int B, int T, int D, int N, int num_seqs);
 size_t kda_scan_fwd_workspace_bytes(int B, int T, int D, int N, int G, int num_seqs);
 
 kda_status_t kda_scan_fwd(const void *u, const void *delta, const float *A, const void *Bm,

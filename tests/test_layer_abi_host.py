@@ -103,7 +103,7 @@ def test_conv_step_refusals(lib, case, want):
 def scan_fwd(lib, B=2, T=20, D=8, N=16, G=2, dtype=0, z=0, initial=0, final=0, saved=0, saved_bytes=None,
              cu=0, num_seqs=0, ws=at(15), need=None, us=0, Bs=0, ys=0, **ptr):
     if saved_bytes is None:
-        saved_bytes = lib.kda_scan_saved_bytes(B, T, D, N, num_seqs, dtype)
+        saved_bytes = lib.kda_scan_saved_bytes(B, T, D, N, num_seqs)
     if need is None:
         need = lib.kda_scan_fwd_workspace_bytes(B, T, D, N, G, num_seqs)
     op = ScanFwdOpts(z=z, initial_state=initial, final_state=final, saved=saved, saved_bytes=saved_bytes,
@@ -129,17 +129,15 @@ def test_scan_fwd_refusals(lib, case, want):
 
 
 def test_scan_buffers(lib):
-    """States in front of every eight tokens, two for each started 16, padded to 8, 16, 32 or 64, and an
-    element a token and channel; a packed call has a slot more for each sequence."""
+    """States in front of every eight tokens, two for each started 16, padded to 8, 16, 32 or 64, and a 32-bit
+    number a token and channel (rounded up to four); a packed call has a slot more for each sequence."""
     def up(n):
         return -(-n // 256) * 256
     for B, T, D, N, seqs, pad in ((2, 33, 8, 16, 0, 16), (1, 16, 5, 3, 0, 8), (1, 100, 8, 20, 4, 32), (1, 1, 1, 64, 0, 64)):
         slots = T // 16 + seqs if seqs else B * -(-T // 16)
-        for dtype, es in ((0, 2), (1, 2), (2, 4)):
-            want = up(2 * slots * D * pad * 4) + up(B * T * D * es)
-            assert lib.kda_scan_saved_bytes(B, T, D, N, seqs, dtype) == want
-    assert lib.kda_scan_saved_bytes(1, 16, 8, 65, 0, 0) == 0
-    assert lib.kda_scan_saved_bytes(1, 16, 8, 16, 0, 3) == 0
+        want = up(2 * slots * D * pad * 4) + up(B * T * -(-D // 4) * 16)
+        assert lib.kda_scan_saved_bytes(B, T, D, N, seqs) == want
+    assert lib.kda_scan_saved_bytes(1, 16, 8, 65, 0) == 0
     assert lib.kda_scan_fwd_workspace_bytes(8, 4096, 4096, 16, 1, 0) == 0  # channels enough
     assert lib.kda_scan_fwd_workspace_bytes(1, 4096, 64, 16, 1, 0) > 0
     assert lib.kda_scan_fwd_workspace_bytes(1, 4096, 64, 16, 3, 0) == 0  # no such call
@@ -149,7 +147,7 @@ def test_scan_buffers(lib):
 def scan_bwd(lib, B=2, T=20, D=8, N=16, G=2, dtype=0, z=0, dz=0, skip=0, dskip=0, bias=0, dbias=0,
              saved=at(14), saved_bytes=None, ws=at(15), need=None, dinitial=0, dfinal=0, dys=0, **ptr):
     if saved_bytes is None:
-        saved_bytes = lib.kda_scan_saved_bytes(B, T, D, N, 0, dtype)
+        saved_bytes = lib.kda_scan_saved_bytes(B, T, D, N, 0)
     if need is None:
         need = lib.kda_scan_bwd_workspace_bytes(B, T, D, N, G, 0)
     op = ScanBwdOpts(z=z, dz=dz, skip=skip, dskip=dskip, delta_bias=bias, ddelta_bias=dbias, saved=saved,
