@@ -119,11 +119,13 @@ class ScanLayer(torch.nn.Module):
         return self.after(x, kda.kda_scan_step(*ins, states[1], *more))
 
 
-def run(steps=400, **kw):
-    return kda_layer.run(steps, layer=lambda width, heads, value_heads: ScanLayer(width), **kw)
+def run(steps=300, length=8, vocabulary=16, **kw):
+    """(Shorter sequences than kda_layer.py's: this state holds on to fewer tokens.)"""
+    return kda_layer.run(steps, length=length, vocabulary=vocabulary,
+                         layer=lambda width, heads, value_heads: ScanLayer(width), **kw)
 
 
 if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
-    ap.add_argument("--steps", type=int, default=400)
+    ap.add_argument("--steps", type=int, default=300)
     run(ap.parse_args().steps)

@@ -131,6 +131,56 @@ def test_more_sequences_than_a_grid_is_high():
             assert rel(got[few], ref[name]) <= tol(HF) + 1e-5, name
 
 
+def test_a_scan_of_more_than_2_to_31_elements():
+    """The last tokens' results are those of a call on the last tokens alone, from the state that the
+    first ones leave (segments differ: FP32 rounding and the type's)."""
+    T, D, cut = 540000, 4000, 530000
+    gen = torch.Generator("cuda").manual_seed(1)
+    u, delta, dy = (torch.randn(1, T, D, device="cuda", generator=gen, dtype=BF) for _ in range(3))
+    B, C = (torch.randn(1, T, 1, 2, device="cuda", generator=gen, dtype=BF) for _ in range(2))
+    A = -torch.rand(D, 2, device="cuda", generator=gen) - 0.1
+    y, last, saved = kda.kda_scan_fwd(u, delta, A, B, C, save=True, output_final_state=True)
+    du, dd, _, dB, dC = kda.kda_scan_bwd(dy, u, delta, A, B, C, saved)[:5]
+    del saved
+    _, state, _ = kda.kda_scan_fwd(*(t[:, :cut] for t in (u, delta)), A, B[:, :cut], C[:, :cut],
+                                   output_final_state=True)
+    tail = [t[:, cut:] for t in (dy, u, delta, B, C)]
+    ty, tl, ts = kda.kda_scan_fwd(*tail[1:3], A, *tail[3:], initial_state=state, save=True, output_final_state=True)
+    out = kda.kda_scan_bwd(*tail[:3], A, *tail[3:], ts)
+    assert rel(tl, last) <= 1e-5 and rel(ty, y[:, cut:]) <= 2 * tol(BF)
+    for got, want in zip((out[0], out[1], out[3], out[4]), (du, dd, dB, dC)):
+        assert rel(got, want[:, cut:]) <= 2 * tol(BF)
+
+
+@pytest.mark.parametrize("D", [4000, 4001])
+def test_a_convolution_of_more_than_2_to_31_elements(D):
+    """Bit for bit: a token's sums do not depend on where it stands."""
+    T, cut = 540000, 530000
+    gen = torch.Generator("cuda").manual_seed(3)
+    x, dy = (torch.randn(1, T, D, device="cuda", generator=gen, dtype=BF) for _ in range(2))
+    w = torch.randn(D, 4, device="cuda", generator=gen)
+    y, last = kda.kda_conv_fwd(x, w, activation="silu", output_final_state=True)
+    dx = kda.kda_conv_bwd(dy, x, w, activation="silu")[0]
+    state = x[:, cut - 3:cut].contiguous()
+    ty, tl = kda.kda_conv_fwd(x[:, cut:], w, None, state, activation="silu", output_final_state=True)
+    tx = kda.kda_conv_bwd(dy[:, cut:], x[:, cut:], w, None, state, activation="silu")[0]
+    assert torch.equal(tl, last) and torch.equal(ty, y[:, cut:]) and torch.equal(tx, dx[:, cut:])
+
+
+@pytest.mark.parametrize("N", [2048, 2045])
+def test_a_product_of_more_than_2_to_31_elements(N):
+    M, K = 1100000, 24
+    gen = torch.Generator("cuda").manual_seed(2)
+    x = torch.randn(M, K, device="cuda", generator=gen, dtype=BF)
+    w, b = torch.randn(N, K, device="cuda", generator=gen, dtype=BF), torch.randn(N, device="cuda", generator=gen, dtype=BF)
+    y, saved = kda.kda_linear_fwd(x, w, b, activation="silu", save=True)
+    dx, _, _ = kda.kda_linear_bwd(y, x, w, saved, activation="silu", weight_grad=False, bias_grad=False)
+    for rows in (slice(0, 200), slice(M // 2, M // 2 + 200), slice(M - 200, M)):
+        part, _ = kda.kda_linear_fwd(x[rows], w, b, activation="silu")
+        dpart = kda.kda_linear_bwd(y[rows], x[rows], w, saved[rows], activation="silu")[0]
+        assert rel(part, y[rows]) <= 2 * tol(BF) and rel(dpart, dx[rows]) <= 2 * tol(BF)
+
+
 # ---------------------------------------------------------------------------- streams and graphs
 def jobs():
     c = cuda(make_conv(2, 150, 136, 4, BF, seed=3))
