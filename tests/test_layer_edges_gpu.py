@@ -99,6 +99,18 @@ def test_few_rows_of_an_odd_contraction(M, K, N):
     assert rel(y, x["x"].to(F64) @ x["weight"].to(F64).T + x["bias"].to(F64)) <= tol(BF)
 
 
+@pytest.mark.parametrize("M", [17, 23, 31, 47, 64, 90, 120, 127, 129])
+def test_rows_of_less_than_a_tile(M):
+    """Where x has no rows nothing is copied, and what lies there (NaN from the call before) stays out."""
+    bad = torch.full((300, 584), float("nan"), dtype=BF, device="cuda")
+    for N in (72, 200):
+        x = make_linear(M, 584, N, BF, seed=M)
+        c = cuda(x)
+        kda.kda_linear_fwd(bad, c["weight"])
+        y = kda.kda_linear_fwd(c["x"], c["weight"], c["bias"])[0]
+        assert rel(y, x["x"].to(F64) @ x["weight"].to(F64).T + x["bias"].to(F64)) <= tol(BF)
+
+
 def test_more_sequences_than_a_grid_is_high():
     """70,000 sequences of one token, and their states."""
     n, D = 70000, 8
