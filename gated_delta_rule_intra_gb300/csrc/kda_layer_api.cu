@@ -53,7 +53,7 @@ size_t cu_bytes(const Tokens &t) { return t.cu_seqlens ? ((size_t)t.num_seqs + 1
 
 // ---------------------------------------------------------------- convolution
 kda_status_t check_conv(int D, int W, int dtype, int wdtype, int act) {
-    if (D <= 0 || W < 2 || W > 4) return KDA_ERR_SHAPE;
+    if (D <= 0 || D > (1 << 28) || W < 2 || W > 4) return KDA_ERR_SHAPE;
     if (!any_type(dtype) || (wdtype != dtype && wdtype != KDA_FP32)) return KDA_ERR_DTYPE;
     if (act != KDA_ACT_NONE && act != KDA_ACT_SILU) return KDA_ERR_OPTION;
     return KDA_OK;
@@ -70,7 +70,8 @@ kda::ConvArgs conv_args(const void *x, const void *weight, const void *bias, int
 
 // ---------------------------------------------------------------- scan
 kda_status_t check_scan(int D, int N, int G, int dtype) {
-    if (D <= 0 || N <= 0 || N > kda::kScanMaxN || G <= 0 || D % G) return KDA_ERR_SHAPE;
+    if (D <= 0 || D > (1 << 28) || N <= 0 || N > kda::kScanMaxN || G <= 0 || D % G) return KDA_ERR_SHAPE;
+    if ((long long)G * N > (1 << 28)) return KDA_ERR_SHAPE;  // rows of B and C are counted in 32 bits
     return any_type(dtype) ? KDA_OK : KDA_ERR_DTYPE;
 }
 kda_status_t scan_shape(int B, int T, int D, int N, int G, int num_seqs, Tokens &tok) {

@@ -493,7 +493,7 @@ kda_status_t kda_layer_norm_bwd(const void *dy, const void *x, const void *weigh
  * Short causal convolution of each channel (the one in front of q, k and v, or of the scan below):
  *   pre[t, d] = bias[d] + sum_j weight[d, j] x[t - W + 1 + j, d],  y = act(pre)
  * over the tokens of a sequence, x, y [B, T, D] with a row stride each, in elements (0 = D), W 2 to
- * 4.  x, y, dy, dx and the states have one type (KDA_BF16, KDA_FP16 or KDA_FP32); weight [D, W] and
+ * 4, D up to 2^28.  x, y, dy, dx and the states have one type (KDA_BF16, KDA_FP16 or KDA_FP32); weight [D, W] and
  * bias [D] (NULL = 0) have `wdtype`, which is the same type or KDA_FP32.  The inputs in front of a
  * sequence come from initial_state [sequences, W - 1, D], oldest first (NULL = zeros); final_state
  * gets the last W - 1 of state and sequence (a sequence of no tokens: a copy).  Sums are FP32.
@@ -556,7 +556,7 @@ kda_status_t kda_conv_step(const void *x, const void *weight, const void *bias, 
                            const kda_conv_step_opts_t *opts, kda_stream_t stream);
 
 /*
- * Selective state-space scan.  Per channel d of D a state h of N <= 64 numbers:
+ * Selective state-space scan.  Per channel d of D a state h of N <= 64 numbers (D and G N up to 2^28):
  *   s_t = softplus(delta_t + delta_bias)              (plain_delta: without the softplus)
  *   h_t[n] = exp(s_t A[d, n]) h_{t-1}[n] + s_t u_t B_t[n],
  *   y_t = (sum_n C_t[n] h_t[n] + skip[d] u_t) silu(z_t)

@@ -49,7 +49,7 @@ def conv_fwd(lib, B=2, T=10, D=8, W=4, dtype=0, wdtype=0, act=1, initial=0, fina
 @pytest.mark.parametrize("case,want", [
     (dict(x=0), ERR_NULL), (dict(weight=0), ERR_NULL), (dict(y=0), ERR_NULL),
     (dict(B=0), ERR_SHAPE), (dict(T=-1), ERR_SHAPE), (dict(D=0), ERR_SHAPE), (dict(W=1), ERR_SHAPE),
-    (dict(W=5), ERR_SHAPE), (dict(xs=7), ERR_SHAPE), (dict(ys=-8), ERR_SHAPE),
+    (dict(W=5), ERR_SHAPE), (dict(D=(1 << 28) + 1), ERR_SHAPE), (dict(xs=7), ERR_SHAPE), (dict(ys=-8), ERR_SHAPE),
     (dict(cu=at(9)), ERR_SHAPE), (dict(num_seqs=2), ERR_SHAPE), (dict(B=2, cu=at(9), num_seqs=2), ERR_SHAPE),
     (dict(B=1 << 16, T=1 << 16), ERR_SHAPE),
     (dict(dtype=3), ERR_DTYPE), (dict(wdtype=1), ERR_DTYPE), (dict(dtype=-1, wdtype=-1), ERR_DTYPE),
@@ -115,7 +115,7 @@ def scan_fwd(lib, B=2, T=20, D=8, N=16, G=2, dtype=0, z=0, initial=0, final=0, s
 @pytest.mark.parametrize("case,want", [
     (dict(u=0), ERR_NULL), (dict(A=0), ERR_NULL), (dict(C=0), ERR_NULL), (dict(y=0), ERR_NULL),
     (dict(B=0), ERR_SHAPE), (dict(T=-2), ERR_SHAPE), (dict(D=0), ERR_SHAPE), (dict(N=0), ERR_SHAPE),
-    (dict(N=65), ERR_SHAPE), (dict(G=3), ERR_SHAPE), (dict(G=0), ERR_SHAPE), (dict(us=7), ERR_SHAPE),
+    (dict(N=65), ERR_SHAPE), (dict(D=1 << 23, G=1 << 23, N=64, T=1, B=1), ERR_SHAPE), (dict(G=3), ERR_SHAPE), (dict(G=0), ERR_SHAPE), (dict(us=7), ERR_SHAPE),
     (dict(Bs=31), ERR_SHAPE), (dict(B=2, cu=at(9), num_seqs=1), ERR_SHAPE), (dict(num_seqs=1), ERR_SHAPE),
     (dict(dtype=4, saved_bytes=0), ERR_DTYPE), (dict(u=at(0, 1)), ERR_ALIGN), (dict(A=at(2, 2)), ERR_ALIGN),
     (dict(saved=at(8, 16)), ERR_ALIGN), (dict(dtype=2, z=at(9, 2)), ERR_ALIGN),
