@@ -3,6 +3,7 @@
 #include <type_traits>
 
 #include "kda_linear.cuh"
+#include "tc_ptx.cuh"
 
 namespace kda {
 namespace linear {
@@ -13,7 +14,7 @@ namespace {
 // the few rows of x are the right operands.  Which k an operand's places stand for does not matter
 // as long as both agree, so a lane takes 16 consecutive bytes of its row: four of them are two
 // products' operands.  The tensor-memory path would move 128 rows of x for these few: 2048 x 8192 takes
-// 5.1 us for 4 rows (6.6 TB/s, from L2), 8.6 for 16, and 15 there; 8192 x 2048 11.1 for 16, and 12.8.
+// 5.1 us for 4 rows with the weight in L2, 8.6 for 16, and 15 there; 8192 x 2048 11.1 for 16, and 12.8.
 constexpr int kWarps = 8, kAhead = 4;
 
 template <typename T>
@@ -29,6 +30,26 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
             "{%0,%1,%2,%3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The warps' sums of 16 weight rows from n0 on, [warp][MT][lane][register of the fragment], and the epilogue.
+template <typename T, int MT>
+__device__ __forceinline__ void finish(const GemmArgs &a, const float (*red)[MT][32][4], int n0) {
+    // thread: one of 16 weight rows, one of 8 MT rows of x
+    for (int e = threadIdx.x; e < 128 * MT; e += 32 * kWarps) {
+        const int r = e & 15, m = e >> 4, t = m >> 3, n = n0 + r;
+        // row r, column m % 8 of the 16 x 8 block: lane and register of the fragment
+        const int l = (r & 7) * 4 + ((m & 7) >> 1), i = (r >> 3) * 2 + (m & 1);
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += red[w][t][l][i];
+        if (m >= a.M || n >= a.N || !dbg_ok(a.dbg, (size_t)m * a.N + n, (size_t)a.M * a.N, DBG_STORE)) continue;
+        if (a.bias) v += as_f32(((const T *)a.bias)[n]);
+        if (a.pre) ((T *)a.pre)[m * a.ldp + n] = from_f32<T>(v);
+        v = activate(v, a.act);
+        if (a.residual) v += as_f32(((const T *)a.residual)[m * a.ldr + n]);
+        ((T *)a.y)[m * a.ldy + n] = from_f32<T>(v);
+    }
 }
 
 template <typename T, int MT>
@@ -70,20 +91,122 @@ __global__ void __launch_bounds__(32 * kWarps) kda_linear_small_kernel(const Gem
 #pragma unroll
     for (int t = 0; t < MT; ++t) *(float4 *)red[warp][t][lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
     __syncthreads();
-    // thread: one of 16 weight rows, one of 8 MT rows of x
-    for (int e = threadIdx.x; e < 128 * MT; e += 32 * kWarps) {
-        const int r = e & 15, m = e >> 4, t = m >> 3, n = n0 + r;
-        // row r, column m % 8 of the 16 x 8 block: lane and register of the fragment
-        const int l = (r & 7) * 4 + ((m & 7) >> 1), i = (r >> 3) * 2 + (m & 1);
-        float v = 0.f;
+    finish<T, MT>(a, red, n0);
+}
+
+// The same for a long contraction of few columns, where one CTA a multiprocessor has to keep memory busy: a
+// warp of its own asks for whole rows of 1024 k several chunks ahead, also those of the CTA's next 16
+// (one copy a row), and the rows of x beside them; eight warps take them from shared memory.  What
+// lies in rows that are not there (behind N, behind M) becomes results that nobody takes.
+constexpr int kChunk = 1024, kPitch = 2 * kChunk + 64;  // (64: eight lanes' banks are all different)
+constexpr uint32_t kWaitPolls = 1u << 22;  // then the kernel gives up (and writes NaN)
+
+template <int MT> struct Long {
+    static constexpr int kStage = (16 + 8 * MT) * kPitch, kStages = 4 / MT + (MT > 1);
+    char raw[kStages][kStage];
+    float red[kWarps][MT][32][4];
+    uint64_t full[kStages], empty[kStages];
+    uint32_t broken;
+};
+
+__device__ __forceinline__ void copy_row(void *to, const void *from, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     tc::smem_u32(to)),
+                 "l"(from), "r"(bytes), "r"(tc::smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void sync_products() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+
+template <typename T, int MT>
+__global__ void __launch_bounds__(32 * kWarps + 32, 1) kda_linear_long_kernel(const GemmArgs a) {
+    wait_for_previous();
+    using S = Long<MT>;
+    extern __shared__ __align__(128) char smem[];
+    S &s = *reinterpret_cast<S *>(smem);
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const T *W = (const T *)a.B, *x = (const T *)a.A;
+    const int tiles = (a.N + 15) / 16, chunks = (a.K + kChunk - 1) / kChunk;
+    volatile uint32_t *broken = &s.broken;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            tc::mbar_init(s.full + i, 1);
+            tc::mbar_init(s.empty + i, kWarps);
+        }
+        *broken = 0;
+        tc::fence_proxy_async_smem();
+    }
+    __syncthreads();
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (*broken) return false;
+        if (tc::mbar_wait(bar, parity, kWaitPolls)) return true;
+        *broken = 1;
+        dbg_flag(a.dbg, true, DBG_WAIT);
+        return false;
+    };
+    int n = 0;  // chunks so far
+    if (warp == kWarps) {
+        bool ok = true;
+        for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            const int row = 16 * tile + lane, m = lane - 16;
+            const int there = min(16, a.N - 16 * tile) + a.M;
+            for (int c = 0; c < chunks; ++c, ++n) {
+                const int st = n % S::kStages, k = c * kChunk;
+                if (n >= S::kStages && !(ok = wait(s.empty + st, (n / S::kStages - 1) & 1))) break;
+                const uint32_t bytes = min(kChunk, a.K - k) * 2;
+                if (lane == 0) tc::mbar_arrive_expect_tx(s.full + st, there * bytes);
+                __syncwarp();
+                char *to = s.raw[st] + lane * kPitch;
+                if (lane < 16) {
+                    if (row < a.N) copy_row(to, W + (size_t)row * a.ldb + k, bytes, s.full + st);
+                } else if (m < a.M) {
+                    copy_row(to, x + (size_t)m * a.lda + k, bytes, s.full + st);
+                }
+                __syncwarp();
+            }
+        }
+        // every copy has landed before the CTA ends
+        for (int i = max(0, n - S::kStages); i < n; ++i)
+            tc::mbar_wait(s.full + i % S::kStages, (i / S::kStages) & 1, kWaitPolls);
+        return;
+    }
+    const int row = lane >> 2, quad = lane & 3;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int n0 = 16 * tile;
+        float acc[MT][4] = {};
+        bool ok = true;
+        for (int c = 0; c < chunks; ++c, ++n) {
+            const int st = n % S::kStages, left = a.K - c * kChunk;
+            ok = wait(s.full + st, (n / S::kStages) & 1) && ok;
+            const char *at = s.raw[st] + row * kPitch + quad * 16;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += red[w][t][l][i];
-        if (m >= a.M || n >= a.N || !dbg_ok(a.dbg, (size_t)m * a.N + n, (size_t)a.M * a.N, DBG_STORE)) continue;
-        if (a.bias) v += as_f32(((const T *)a.bias)[n]);
-        if (a.pre) ((T *)a.pre)[m * a.ldp + n] = from_f32<T>(v);
-        v = activate(v, a.act);
-        if (a.residual) v += as_f32(((const T *)a.residual)[m * a.ldr + n]);
-        ((T *)a.y)[m * a.ldy + n] = from_f32<T>(v);
+            for (int i = 0; i < kChunk / 32 / kWarps; ++i) {
+                const int k = (warp + kWarps * i) * 32;
+                if (k >= left) break;
+                const bool in = k + quad * 8 < left;
+                uint4 w[2], b[MT];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    w[h] = in ? *(const uint4 *)(at + 8 * h * kPitch + 2 * k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+                    b[t] = in ? *(const uint4 *)(at + (16 + 8 * t) * kPitch + 2 * k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    mma<T>(acc[t], w[0].x, w[1].x, w[0].y, w[1].y, b[t].x, b[t].y);
+                    mma<T>(acc[t], w[0].z, w[1].z, w[0].w, w[1].w, b[t].z, b[t].w);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(s.empty + st);
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            if (!ok) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = __int_as_float(0x7fc00000);
+            *(float4 *)s.red[warp][t][lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+        }
+        sync_products();
+        finish<T, MT>(a, s.red, n0);
+        sync_products();
     }
 }
 
@@ -186,10 +309,25 @@ template <typename T> cudaError_t dact(const DActArgs &a, cudaStream_t stream) {
            : u.unit == 4 ? dact<T, 2>(a, stream) : dact<T, 1>(a, stream);
 }
 
+template <typename T, int MT> cudaError_t few(const GemmArgs &a, cudaStream_t stream) {
+    // rows x K x N, weights from memory, us, straight and through shared memory: 4 x 2048 x 2048 5.8 and
+    // 4.3, 4 x 8192 x 2048 18.7 and 9.4, 4 x 4096 x 4096 10.7 and 9.2, 16 x 8192 x 2048 19.1 and 12.1; but 4 x
+    // 512 x 512 1.8 and 2.5, 4 x 1024 x 4096 4.1 and 4.7, 4 x 2048 x 8192 7.9 and 9.4, 8 x 8192 x 8192 26 and 33
+    const int tiles = (a.N + 15) / 16;
+    if (tiles > 2 * kSMs || a.K < 2 * kChunk)
+        return launch_early(kda_linear_small_kernel<T, MT>, (unsigned)tiles, 32 * kWarps, 0, stream, a);
+    constexpr int kBytes = sizeof(Long<MT>);
+    static_assert(kBytes <= 227 * 1024, "");
+    static volatile int done[kMaxDev];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = smem_limit_once(kda_linear_long_kernel<T, MT>, kBytes, dev, done);
+    if (e != cudaSuccess) return e;
+    return launch_early(kda_linear_long_kernel<T, MT>, (unsigned)(tiles < kSMs ? tiles : kSMs), 32 * kWarps + 32, kBytes,
+                        stream, a);
+}
 template <typename T> cudaError_t small(const GemmArgs &a, cudaStream_t stream) {
-    const unsigned grid = (unsigned)((a.N + 15) / 16);
-    return a.M <= 8 ? launch_early(kda_linear_small_kernel<T, 1>, grid, 32 * kWarps, 0, stream, a)
-                    : launch_early(kda_linear_small_kernel<T, 2>, grid, 32 * kWarps, 0, stream, a);
+    return a.M <= 8 ? few<T, 1>(a, stream) : few<T, 2>(a, stream);
 }
 
 }  // namespace

@@ -99,6 +99,19 @@ def test_few_rows_of_an_odd_contraction(M, K, N):
     assert rel(y, x["x"].to(F64) @ x["weight"].to(F64).T + x["bias"].to(F64)) <= tol(BF)
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("M,K,N", [(1, 2048, 8), (3, 2056, 40), (8, 4104, 2449), (9, 2048, 2432), (16, 6136, 4864),
+                                   (5, 8192, 17)])
+def test_few_rows_of_a_long_contraction(M, K, N, dtype):
+    """Chunks of 1024 k that end in the middle, several times 16 columns a CTA, columns behind the last."""
+    x = make_linear(M, K, N, dtype, seed=N)
+    c = cuda(x)
+    y, saved = kda.kda_linear_fwd(c["x"], c["weight"], c["bias"], c["residual"], activation="relu", save=True)
+    pre = x["x"].to(F64) @ x["weight"].to(F64).T + x["bias"].to(F64)
+    assert rel(saved, pre) <= tol(dtype) and rel(y, torch.relu(pre) + x["residual"].to(F64)) <= tol(dtype)
+    _debug(lambda: [kda.kda_linear_fwd(c["x"], c["weight"], c["bias"])[0]])
+
+
 @pytest.mark.parametrize("M", [17, 23, 31, 47, 64, 90, 120, 127, 129])
 def test_rows_of_less_than_a_tile(M):
     """Where x has no rows nothing is copied, and what lies there (NaN from the call before) stays out."""
