@@ -40,6 +40,7 @@ __device__ __forceinline__ float2 gelu_slope(float2 x) {  // Phi(x) + x phi(x)
     const float2 phi = make_float2(x.x < 0.f ? q.x : 1.f - q.x, x.y < 0.f ? q.y : 1.f - q.y);
     return fma2(mul2(y, twice(0.39894228f)), make_float2(ex2(e.x), ex2(e.y)), phi);
 }
+__device__ __forceinline__ float finite(float x) { return fminf(fmaxf(x, -3.4028235e38f), 3.4028235e38f); }
 __device__ __forceinline__ float2 sigmoid2(float2 x) { return make_float2(sigmoid(x.x), sigmoid(x.y)); }
 
 template <int ACT> __device__ __forceinline__ float2 activate(float2 x) {
@@ -56,8 +57,10 @@ __device__ __forceinline__ float activate(float x, int act) {
 // d act / dx; 0 in relu's corner.
 __device__ __forceinline__ float2 slope(float2 x, int act) {
     if (act == ACT_SILU) {
-        const float2 s = sigmoid2(x);
-        return mul2(s, fma2(x, fma2(s, twice(-1.f), twice(1.f)), twice(1.f)));
+        // (x may be infinite where the sum was beyond the 16-bit type: with the largest finite number beside 1 - s
+        // the ends are 0 and 1 instead of 0 times infinity; NaN stays, by s)
+        const float2 s = sigmoid2(x), y = make_float2(finite(x.x), finite(x.y));
+        return mul2(s, fma2(y, fma2(s, twice(-1.f), twice(1.f)), twice(1.f)));
     }
     if (act == ACT_GELU) return gelu_slope(x);
     auto step = [](float v) { return v > 0.f ? 1.f : v == v ? 0.f : v; };
