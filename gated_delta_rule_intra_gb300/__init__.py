@@ -30,8 +30,8 @@ The functions carry the C names of ``include/kda.h``:
 * ``kda_linear_fwd``, ``kda_linear_bwd`` -- matrix product with bias, activation and residual
   in its epilogue (``linear.py``)
 * ``kda_status_str``, ``kda_abi_version``
-* ``use_library``, ``kda_debug_checks``, ``kda_debug_set_flags`` -- run the same calls
-  through the bounds-checked debug build ``libkda_debug.so`` (tests)
+* ``use_library``, ``kda_debug_checks``, ``kda_debug_set_flags``, ``kda_debug_set_give_up`` --
+  run the same calls through the bounds-checked debug build ``libkda_debug.so`` (tests)
 """
 
 from __future__ import annotations
@@ -55,7 +55,7 @@ DEBUG_LIB_PATH = os.path.join(_HERE, "libkda_debug.so")
 
 # KDA_ABI_VERSION of the include/kda.h these ctypes mirrors follow (option structs,
 # signatures); a library of any other version is refused at load.
-ABI_VERSION = 12
+ABI_VERSION = 13
 KDA_OK = 0
 KDA_BF16 = 0
 KDA_FP16 = 1
@@ -131,6 +131,9 @@ def load_library(path: str | None = None):
         _common.declare(lib)
     lib.kda_debug_set_flags.argtypes = [vp]
     lib.kda_debug_set_flags.restype = st
+    if hasattr(lib, "kda_debug_set_give_up"):  # (as above)
+        lib.kda_debug_set_give_up.argtypes = [i]
+        lib.kda_debug_set_give_up.restype = st
     if lib.kda_abi_version() != ABI_VERSION:
         raise RuntimeError(
             f"{p} has ABI version {lib.kda_abi_version()}, this binding needs {ABI_VERSION}: "
@@ -168,6 +171,14 @@ def kda_debug_set_flags(word) -> None:
         ctypes.c_void_p(None if word is None else word.data_ptr()))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_debug_set_flags")
+
+
+def kda_debug_set_give_up(on) -> None:
+    """Debug build only: the matrix product's bounded waits give up at once, to see what a stalled
+    pipeline leaves."""
+    rc = load_library().kda_debug_set_give_up(int(bool(on)))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_debug_set_give_up")
 
 
 def kda_status_str(code: int) -> str:

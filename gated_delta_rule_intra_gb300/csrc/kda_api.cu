@@ -168,6 +168,7 @@ kda_status_t check_ex(const void *q, const void *k, const float *g, const float 
 // Bounds-checked debug build: the caller's device flag word (kda_debug_set_flags),
 // passed to every launch.  Always null in the normal build.
 unsigned *g_debug_flags = nullptr;
+bool g_debug_give_up = false;  // kda_debug_set_give_up
 
 kda::BwdArgs pack(const void *q, const void *k, const float *g, const float *beta,
                   const float *dAqk, const float *dAkk, float *dq, float *dk, float *db,
@@ -223,6 +224,7 @@ kda_status_t host_pipe(HostPipe **out) {
 namespace kda {
 kda_status_t require_device() { return check_device(); }
 unsigned *debug_flags() { return g_debug_flags; }
+bool debug_give_up() { return g_debug_give_up; }
 }  // namespace kda
 
 extern "C" {
@@ -613,10 +615,17 @@ kda_status_t kda_debug_set_flags(unsigned int *device_word) {
     g_debug_flags = device_word;
     return KDA_OK;
 }
+
+kda_status_t kda_debug_set_give_up(int on) {
+    g_debug_give_up = on != 0;
+    return KDA_OK;
+}
 #else
 int kda_debug_checks(void) { return 0; }
 
 kda_status_t kda_debug_set_flags(unsigned int *) { return KDA_ERR_OPTION; }
+
+kda_status_t kda_debug_set_give_up(int) { return KDA_ERR_OPTION; }
 #endif
 
 }  // extern "C"

@@ -13,6 +13,7 @@
 namespace kda {
 kda_status_t require_device();  // kda_api.cu
 unsigned *debug_flags();
+bool debug_give_up();
 
 // Bytes that a call reads or writes: one run, or rows of `row` bytes `step` apart.
 struct Range {

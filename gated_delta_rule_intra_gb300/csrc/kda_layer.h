@@ -121,6 +121,7 @@ struct GemmArgs {
     bool fp16;
     float *partial;  // gemm_partial_bytes()
     unsigned *dbg;
+    bool give_up;  // debug build: its bounded waits give up at once
 };
 size_t gemm_partial_bytes(int M, int N, int K);
 cudaError_t launch_gemm(const GemmArgs &a, cudaStream_t stream);

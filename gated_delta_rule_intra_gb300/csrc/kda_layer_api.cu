@@ -558,6 +558,7 @@ kda_status_t kda_linear_fwd(const void *x, const void *weight, void *y, int M, i
     a.fp16 = dtype == KDA_FP16;
     a.partial = (float *)w.at;
     a.dbg = kda::debug_flags();
+    a.give_up = kda::debug_give_up();
     return finish(kda::small_gemm_ok(M, K) ? kda::launch_small_gemm(a, (cudaStream_t)stream)
                                         : kda::launch_gemm(a, (cudaStream_t)stream));
 }
@@ -636,6 +637,7 @@ kda_status_t kda_linear_bwd(const void *dy, const void *x, const void *weight, v
     kda::GemmArgs a = {};
     a.fp16 = dtype == KDA_FP16;
     a.dbg = kda::debug_flags();
+    a.give_up = kda::debug_give_up();
     Copies c;
     if (dweight) c.add(x, op.x_stride, M, K, w);
     if (dx) c.add(weight, op.weight_stride, N, K, w);

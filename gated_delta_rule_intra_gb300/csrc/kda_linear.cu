@@ -35,7 +35,6 @@ namespace {
 constexpr int BM = 128, BK = 64;
 constexpr int kEpilogue = 8;               // warps that finish tiles, 32 columns at a time
 constexpr int kThreads = 64 + 32 * kEpilogue;
-constexpr uint32_t kWaitPolls = 1u << 22;  // then the kernel gives up (and writes NaN)
 
 // BN: columns of a tile.  PAIR: of two CTAs, each with half of the rows of A and of B.
 template <int BN, bool PAIR> struct Cfg {
@@ -65,6 +64,7 @@ struct Params {
     bool tma_out;         // y and pre leave by TMA
     int unit_o, unit_r;   // bytes on whose boundaries their rows begin, and residual's
     unsigned *dbg;
+    bool give_up;
 };
 
 // Shared-memory descriptor, 128-byte swizzle: K-major sbo = 1024 (eight rows); MN-major sbo = 1024
@@ -336,10 +336,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (PAIR) cluster_sync();  // both CTAs' barriers are there
     tc::fence_after_sync();
     const uint32_t tmem = *slot;
-    // A wait that gives up ends this CTA's work; the other warps learn of it here.
+    // A wait that gives up ends this CTA's copies and products; the other warps learn of it here, and the
+    // finishing ones write NaN to the tile at hand and to all that are left.
+    const uint32_t polls = wait_polls(p.give_up);
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (*broken) return false;
-        if (PAIR ? wait_pair(bar, parity, kWaitPolls) : tc::mbar_wait(bar, parity, kWaitPolls)) return true;
+        if (PAIR ? wait_pair(bar, parity, polls) : tc::mbar_wait(bar, parity, polls)) return true;
         *broken = 1;
         dbg_flag(p.dbg, true, DBG_WAIT);
         return false;
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int n = 0;
             do {
                 float v[32];
-                if (n1 > 0) {
+                if (n1 > 0 && ok) {
                     tmem_ld32(d + n, v);
                     tc::tmem_wait_ld();
                 }
@@ -531,7 +533,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 put(p.residual);
                 leave(&maps.y, p.y, p.ldy);
             } while ((n += 32) < n1);
-            if (!ok) break;
         }
         if (lane == 0) tc::bulk_wait_all();
     }
@@ -702,6 +703,7 @@ template <typename T> cudaError_t run(const GemmArgs &a, cudaStream_t stream) {
     p.ldw = q.ldw;
     p.partial = q.splits > 1 ? a.partial : nullptr;
     p.dbg = a.dbg;
+    p.give_up = a.give_up;
     Boundary o(2, 8), r(2, 8);
     o.add(a.y, a.ldy);
     o.add(a.pre, a.ldp);

@@ -8,6 +8,19 @@ namespace linear {
 
 using namespace rows;
 
+// Polls of a bounded wait, behind which the kernel gives up (and writes NaN).  In the debug build it may be told
+// to give up at once (kda_debug_set_give_up): none or all, because a pair's CTAs have asked for the same
+// copies then, as many as there are stages, and the first one's last waits, which are never shortened, see
+// them land.
+constexpr uint32_t kWaitPolls = 1u << 22;
+__device__ __forceinline__ uint32_t wait_polls(bool give_up) {
+#ifdef KDA_DEBUG_CHECKS
+    return give_up ? 0 : kWaitPolls;
+#else
+    return kWaitPolls;
+#endif
+}
+
 // erfc(|x| / sqrt 2) of two values.  With z = |x| / sqrt 2 and t = 1 / (1 + z / 2), log2(erfc(z) e^(z^2) / t)
 // is a smooth function of t on [0, 1]: its Chebyshev interpolation of degree 7 (nodes on z <= 9.5, behind
 // which e^(-z^2) is nothing), in powers of t.  Relative error 7e-7 before the exponential's own rounding

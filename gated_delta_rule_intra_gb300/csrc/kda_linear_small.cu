@@ -99,7 +99,6 @@ __global__ void __launch_bounds__(32 * kWarps) kda_linear_small_kernel(const Gem
 // (one copy a row), and the rows of x beside them; eight warps take them from shared memory.  What
 // lies in rows that are not there (behind N, behind M) becomes results that nobody takes.
 constexpr int kChunk = 1024, kPitch = 2 * kChunk + 64;  // (64: eight lanes' banks are all different)
-constexpr uint32_t kWaitPolls = 1u << 22;  // then the kernel gives up (and writes NaN)
 
 template <int MT> struct Long {
     static constexpr int kStage = (16 + 8 * MT) * kPitch, kStages = 4 / MT + (MT > 1);
@@ -138,7 +137,7 @@ __global__ void __launch_bounds__(32 * kWarps + 32, 1) kda_linear_long_kernel(co
     __syncthreads();
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (*broken) return false;
-        if (tc::mbar_wait(bar, parity, kWaitPolls)) return true;
+        if (tc::mbar_wait(bar, parity, wait_polls(a.give_up))) return true;
         *broken = 1;
         dbg_flag(a.dbg, true, DBG_WAIT);
         return false;

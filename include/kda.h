@@ -51,7 +51,8 @@
  *
  * Stalled pipelines: every wait of a kernel on its own copies or tensor-core work is
  * bounded (about 4M polls).  A wait that gives up does not hang or trap: the kernel
- * writes NaN into the outputs of the unit it was working on and carries on.  The call
+ * writes NaN into the outputs of the unit it was working on and carries on (the matrix
+ * product: NaN into all that this block of threads had still to write).  The call
  * has already returned KDA_OK when this happens (the status only covers the arguments
  * and the launch), so in the normal build a stalled pipeline is seen only as NaN
  * outputs, which NaN or Inf inputs can also produce.  The bounds-checked debug build
@@ -69,6 +70,7 @@ extern "C" {
 
 /*
  * ABI versions (kda_abi_version() returns the loaded library's):
+ *   13 kda_debug_set_give_up
  *   12 kda_conv_fwd, kda_conv_bwd, kda_conv_step, kda_scan_fwd, kda_scan_bwd, kda_scan_step,
  *      kda_linear_fwd, kda_linear_bwd and their option structs and size queries
  *   11 kda_chunk_bwd's zero_rest also takes KDA_GATE_GRADS_FP32, kda_chunk_fwd's saved either
@@ -90,7 +92,7 @@ extern "C" {
  * must check at start-up that kda_abi_version() equals the KDA_ABI_VERSION it was
  * compiled with (the Python binding refuses to load any other version).
  */
-#define KDA_ABI_VERSION 12
+#define KDA_ABI_VERSION 13
 #define KDA_BT 64  /* chunk length */
 #define KDA_BC 16  /* sub-block length inside a chunk */
 #define KDA_K 128  /* head dimension */
@@ -719,6 +721,14 @@ const char *kda_status_str(kda_status_t status);
 #define KDA_DBG_WAIT 4u
 int kda_debug_checks(void);
 kda_status_t kda_debug_set_flags(unsigned int *device_word);
+
+/*
+ * In such a build, with `on` other than 0, the matrix product's waits on copies and products give up
+ * at once, to see what a stalled pipeline leaves (kernels of up to 16 rows and a short contraction
+ * have no such waits).  Waits for copies in flight at a kernel's end are not shortened.
+ * KDA_ERR_OPTION in a build without checks.
+ */
+kda_status_t kda_debug_set_give_up(int on);
 
 /* KDA_ABI_VERSION of the loaded library. */
 int kda_abi_version(void);
