@@ -339,12 +339,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A wait that gives up ends this CTA's copies and products; the other warps learn of it here, and the
     // finishing ones write NaN to the tile at hand and to all that are left.
     const uint32_t polls = wait_polls(p.give_up);
+    // (the lanes of a warp agree: one of them may see that another warp gave up while the others see the barrier,
+    // and what follows is for whole warps)
+    auto poll = [&](uint64_t *bar, uint32_t parity, uint32_t n) {
+        return PAIR ? wait_pair(bar, parity, n) : tc::mbar_wait(bar, parity, n);
+    };
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (*broken) return false;
-        if (PAIR ? wait_pair(bar, parity, polls) : tc::mbar_wait(bar, parity, polls)) return true;
+        if (__all_sync(0xffffffffu, !*broken && poll(bar, parity, polls))) return true;
         *broken = 1;
         dbg_flag(p.dbg, true, DBG_WAIT);
         return false;
+    };
+    // The same for the warps that leave their loop at the first wait that fails, and so never wait for a phase
+    // behind one that they have not seen: most waits are over at the first poll, without a look at `broken`.
+    auto wait_in_order = [&](uint64_t *bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, poll(bar, parity, min(polls, 1u))) || wait(bar, parity);
     };
     if (warp == 0) {
         int n = 0;  // stages filled so far
@@ -355,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int rows = PAIR ? t.cols / 2 : C::kRowsB, m = t.m + rank * BM, nn = t.n + rank * rows;
             for (int kb = t.kb; kb < t.ke; ++kb, ++n) {
                 const int st = n % C::kStages;
-                if (n >= C::kStages && !(ok = wait(empty + st, (n / C::kStages - 1) & 1))) break;
+                if (n >= C::kStages && !(ok = wait_in_order(empty + st, (n / C::kStages - 1) & 1))) break;
                 if (tc::elect_one()) {
                     const uint32_t a = tc::smem_u32(base + st * C::kStage), b = a + C::kA;
                     // (a pair's first CTA waits for both's bytes)
@@ -392,12 +401,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int i = first; i < work && ok; i += step, ++c) {
                 const Tile t = tile_of(p, i, kRows, BN);
-                if (c >= 2 && !wait(taken + (c & 1), (c / 2 - 1) & 1)) break;
+                if (c >= 2 && !wait_in_order(taken + (c & 1), (c / 2 - 1) & 1)) break;
                 tc::fence_after_sync();
                 const uint32_t d = tmem + (c & 1) * BN, idesc = PAIR && t.cols < BN ? half : whole;
                 for (int kb = t.kb; kb < t.ke; ++kb, ++n) {
                     const int st = n % C::kStages;
-                    if (!(ok = wait(full + st, (n / C::kStages) & 1))) break;
+                    if (!(ok = wait_in_order(full + st, (n / C::kStages) & 1))) break;
                     tc::fence_after_sync();
                     const uint32_t a = tc::smem_u32(base + st * C::kStage), b = a + C::kA;
                     if (tc::elect_one()) {

@@ -135,9 +135,9 @@ __global__ void __launch_bounds__(32 * kWarps + 32, 1) kda_linear_long_kernel(co
         tc::fence_proxy_async_smem();
     }
     __syncthreads();
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (*broken) return false;
-        if (tc::mbar_wait(bar, parity, wait_polls(a.give_up))) return true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {  // (the lanes of a warp agree)
+        const bool mine = !*broken && tc::mbar_wait(bar, parity, wait_polls(a.give_up));
+        if (__all_sync(0xffffffffu, mine)) return true;
         *broken = 1;
         dbg_flag(a.dbg, true, DBG_WAIT);
         return false;
