@@ -191,7 +191,7 @@ inline long long resident(int bytes, int most) {
 template <int W, int CH>
 __device__ __forceinline__ void load_params(const ConvArgs &a, int c0, float (*w)[CH]) {
     for (int i = threadIdx.x; i < CH; i += kThreads) {
-        const bool in = c0 + i < a.D;
+        const bool in = c0 + i < a.D && dbg_ok(a.dbg, (size_t)(c0 + i), (size_t)a.D, DBG_LOAD);
 #pragma unroll
         for (int j = 0; j < W; ++j) w[j][i] = in ? param(a.weight, a.wdtype, (size_t)(c0 + i) * W + j, 0.f) : 0.f;
         w[W][i] = in ? param(a.bias, a.wdtype, c0 + i, 0.f) : 0.f;

@@ -165,8 +165,8 @@ __global__ void __launch_bounds__(kThreads, 4)
             float x = 0.f;
 #pragma unroll
             for (int k = 0; k < S::kRuns; ++k) x += s.red[k][i];
-            if (c0 + i < a.D && dbg_ok(a.dbg, blockIdx.y, (size_t)a.partials, DBG_STORE))
-                a.partial[((size_t)blockIdx.y * (W + 1) + j) * a.D + c0 + i] = x;
+            const size_t at = ((size_t)blockIdx.y * (W + 1) + j) * a.D + c0 + i;
+            if (c0 + i < a.D && dbg_ok(a.dbg, at, a.partial_floats, DBG_STORE)) a.partial[at] = x;
         }
     }
 }
@@ -179,11 +179,15 @@ __global__ void __launch_bounds__(256) kda_conv_sum_kernel(const ConvArgs a) {
     if (j > a.W) return;
     float s = 0.f;
 #pragma unroll 8
-    for (int k = 0; k < a.partials; ++k) s += a.partial[((size_t)k * (a.W + 1) + j) * a.D + c];
-    if (j < a.W)
-        a.dweight[(size_t)c * a.W + j] = s;
-    else
+    for (int k = 0; k < a.partials; ++k) {
+        const size_t at = ((size_t)k * (a.W + 1) + j) * a.D + c;
+        if (dbg_ok(a.dbg, at, a.partial_floats, DBG_LOAD)) s += a.partial[at];
+    }
+    if (j < a.W) {
+        if (dbg_ok(a.dbg, (size_t)c * a.W + j, (size_t)a.D * a.W, DBG_STORE)) a.dweight[(size_t)c * a.W + j] = s;
+    } else if (dbg_ok(a.dbg, (size_t)c, (size_t)a.D, DBG_STORE)) {
         a.dbias[c] = s;
+    }
 }
 
 // Gradients of the inputs in front of each sequence: its first W - 1 values of g again.
@@ -202,13 +206,18 @@ template <typename T> __global__ void __launch_bounds__(256) kda_conv_initial_ke
         p.row0 = (long long)n * a.tok.T;
         p.total = a.tok.T;
     }
+    auto row_ok = [&](int pos) { return dbg_ok(a.dbg, (size_t)(p.row0 + pos), (size_t)a.tok.rows(), DBG_LOAD); };
+    auto state = [&](const void *of, int row) {
+        const size_t at = (size_t)n * (W - 1) + row;
+        return dbg_ok(a.dbg, at, (size_t)a.tok.num_seqs * (W - 1), DBG_LOAD) ? as_f32(((const T *)of)[at * a.D + c]) : 0.f;
+    };
     auto input = [&](int pos) {
-        return pos >= 0 ? as_f32(((const T *)a.x)[(p.row0 + pos) * a.x_stride + c])
-               : a.initial ? as_f32(((const T *)a.initial)[((size_t)n * (W - 1) + pos + W - 1) * a.D + c]) : 0.f;
+        return pos >= 0 ? row_ok(pos) ? as_f32(((const T *)a.x)[(p.row0 + pos) * a.x_stride + c]) : 0.f
+               : a.initial ? state(a.initial, pos + W - 1) : 0.f;
     };
     float d[3] = {};
     for (int t = 0; t < W - 1 && t < p.total; ++t) {
-        float g = as_f32(((const T *)a.dy)[(p.row0 + t) * a.dy_stride + c]);
+        float g = row_ok(t) ? as_f32(((const T *)a.dy)[(p.row0 + t) * a.dy_stride + c]) : 0.f;
         if (a.act == ACT_SILU) {
             float pre = param(a.bias, a.wdtype, c, 0.f);
             for (int j = 0; j < W; ++j)
@@ -221,8 +230,7 @@ template <typename T> __global__ void __launch_bounds__(256) kda_conv_initial_ke
     }
     for (int r = 0; r < W - 1; ++r) {
         const int last = r - p.total;  // where it is still among the last inputs
-        if (a.d_final && last >= 0)
-            d[r] += as_f32(((const T *)a.d_final)[((size_t)n * (W - 1) + last) * a.D + c]);
+        if (a.d_final && last >= 0) d[r] += state(a.d_final, last);
         if (dbg_ok(a.dbg, (size_t)n, (size_t)a.tok.num_seqs, DBG_STORE))
             ((T *)a.d_initial)[((size_t)n * (W - 1) + r) * a.D + c] = from_f32<T>(d[r]);
     }

@@ -131,7 +131,8 @@ __global__ void __launch_bounds__(256) kda_conv_step_kernel(const ConvArgs a) {
     const bool none = slot < 0 || slot >= a.num_states;  // no request here: y is zero
     Vec<T, V> y, x[W];
     y.clear();
-    if (!none && dbg_ok(a.dbg, (size_t)n, (size_t)a.N, DBG_LOAD)) {
+    if (!none && dbg_ok(a.dbg, (size_t)n, (size_t)a.N, DBG_LOAD) &&
+        dbg_ok(a.dbg, ((size_t)(slot + 1) * (W - 1) - 1) * a.D + c + V - 1, (size_t)a.num_states * (W - 1) * a.D, DBG_STORE)) {
         T *st = (T *)a.state + (size_t)slot * (W - 1) * a.D + c;
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) x[j] = *reinterpret_cast<const Vec<T, V> *>(st + (size_t)j * a.D);

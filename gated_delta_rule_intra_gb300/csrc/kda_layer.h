@@ -43,6 +43,7 @@ struct ConvArgs {
     float *dweight, *dbias;         // [D, W], [D]; both or none
     float *partial;                 // [partials][W + 1][D]
     int partials;
+    size_t partial_floats;          // in the workspace, for the debug build's checks
     // single tokens
     void *state;                    // [num_states, W - 1, D]
     const int *state_indices;
@@ -70,7 +71,7 @@ struct ScanArgs {
     bool softplus;
     long long u_stride, delta_stride, z_stride, B_stride, C_stride, y_stride;
     int segment;                         // tokens that one CTA walks, a multiple of kScanTile
-    float *ends, *sums;                  // [segments][D][NP], [segments][D]: scan_segment_floats()
+    float *ends, *sums;                  // [segments][D][NP], [segments][D] (null: none)
     // backward
     const void *dy;
     void *du, *ddelta, *dz, *dB, *dC;    // dz null with z
@@ -84,8 +85,8 @@ struct ScanArgs {
     const int *state_indices;
     int requests;
     long long num_states;
-    // for the debug build's checks: elements of `saved`, and of `ends`, `part_A`
-    size_t saved_floats, segment_floats;
+    // for the debug build's checks: elements of `saved`, of `open`, of `ends` and `part_A`, of `sums`, ...
+    size_t saved_floats, open_floats, segment_floats, sum_floats, part_D_floats, part_bc_floats;
     unsigned *dbg;
 };
 
@@ -120,6 +121,7 @@ struct GemmArgs {
     int act;
     bool fp16;
     float *partial;  // gemm_partial_bytes()
+    size_t partial_floats;
     unsigned *dbg;
     bool give_up;  // debug build: its bounded waits give up at once
 };
@@ -145,6 +147,7 @@ struct DActArgs {
     const void *dy, *pre;
     void *dpre, *dbias;
     float *partial;  // [dact_partials(M, N)][N]
+    size_t partial_floats;
     long long lddy, ldp, ldd;
     int M, N, act;
     bool fp16;

@@ -237,6 +237,7 @@ kda_status_t kda_conv_bwd(const void *dy, const void *x, const void *weight, con
     a.dweight = dweight; a.dbias = dbias;
     a.partial = (float *)op.workspace;
     a.partials = kda::conv_partials(tok.pieces(kda::kConvPiece), D);
+    a.partial_floats = need / 4;
     a.x_stride = op.x_stride; a.dy_stride = op.dy_stride; a.dx_stride = op.dx_stride;
     return finish(kda::launch_conv_bwd(a, (cudaStream_t)stream));
 }
@@ -351,7 +352,9 @@ kda_status_t kda_scan_fwd(const void *u, const void *delta, const float *A, cons
         a.sums = (float *)((char *)op.workspace + up256(s.ends * 4));
     }
     a.saved_floats = scan_saved_floats(tok, D, N);
+    a.open_floats = (size_t)rows * ((D + 3) / 4 * 4);
     a.segment_floats = s.ends;
+    a.sum_floats = s.sums;
     a.dbg = kda::debug_flags();
     return finish(kda::launch_scan_fwd(a, (cudaStream_t)stream));
 }
@@ -453,7 +456,11 @@ kda_status_t kda_scan_bwd(const void *dy, const void *u, const void *delta, cons
     a.part_D = (float *)(at + part[2]);
     a.part_bc = (float *)(at + part[2] + part[3]);
     a.saved_floats = scan_saved_floats(tok, D, N);
+    a.open_floats = (size_t)rows * ((D + 3) / 4 * 4);
     a.segment_floats = s.slots * D * kda::scan_padded(N);
+    a.sum_floats = s.sums;
+    a.part_D_floats = s.slots * D * 2;
+    a.part_bc_floats = (size_t)rows * (size_t)kda::scan_blocks(D, N, G) * 2 * kda::scan_padded(N);
     a.dbg = kda::debug_flags();
     return finish(kda::launch_scan_bwd(a, (cudaStream_t)stream));
 }
@@ -557,6 +564,7 @@ kda_status_t kda_linear_fwd(const void *x, const void *weight, void *y, int M, i
     a.act = op.activation;
     a.fp16 = dtype == KDA_FP16;
     a.partial = (float *)w.at;
+    a.partial_floats = kda::gemm_partial_bytes(M, N, K) / 4;
     a.dbg = kda::debug_flags();
     a.give_up = kda::debug_give_up();
     return finish(kda::small_gemm_ok(M, K) ? kda::launch_small_gemm(a, (cudaStream_t)stream)
@@ -627,7 +635,8 @@ kda_status_t kda_linear_bwd(const void *dy, const void *x, const void *weight, v
         }
         if (dbias) {
             d.dbias = dbias;
-            d.partial = (float *)w.take((size_t)kda::dact_partials(M, N) * N * 4);
+            d.partial_floats = (size_t)kda::dact_partials(M, N) * N;
+            d.partial = (float *)w.take(d.partial_floats * 4);
         }
         d.M = M; d.N = N; d.act = op.activation; d.fp16 = dtype == KDA_FP16;
         d.dbg = kda::debug_flags();
@@ -648,6 +657,7 @@ kda_status_t kda_linear_bwd(const void *dy, const void *x, const void *weight, v
         a.A = g; a.lda = ldg;
         a.B = weight; a.ldb = op.weight_stride; a.b_mn = true;
         a.M = M; a.N = K; a.K = N;
+        a.partial_floats = kda::gemm_partial_bytes(M, K, N) / 4;
         a.y = dx; a.ldy = op.dx_stride;
         if ((e = kda::launch_gemm(a, cs)) != cudaSuccess) return finish(e);
     }
@@ -655,6 +665,7 @@ kda_status_t kda_linear_bwd(const void *dy, const void *x, const void *weight, v
         a.A = g; a.lda = ldg; a.a_mn = true;
         a.B = x; a.ldb = op.x_stride; a.b_mn = true;
         a.M = N; a.N = K; a.K = M;
+        a.partial_floats = kda::gemm_partial_bytes(N, K, M) / 4;
         a.y = dweight; a.ldy = K;
         if ((e = kda::launch_gemm(a, cs)) != cudaSuccess) return finish(e);
     }

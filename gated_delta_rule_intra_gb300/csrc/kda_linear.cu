@@ -60,6 +60,7 @@ struct Params {
     long long ldr, ldy, ldp;
     int act;
     float *partial;  // [splits][M][ldw], or null
+    size_t partial_floats;
     int ldw;
     bool tma_out;         // y and pre leave by TMA
     int unit_o, unit_r;   // bytes on whose boundaries their rows begin, and residual's
@@ -234,8 +235,14 @@ __device__ __forceinline__ int spot(int r, int q) { return r * 64 + ((q ^ (r >> 
 template <typename W> struct Rows {
     static constexpr int kWords = 64 / sizeof(W), kStep = 32 / kWords, kEach = sizeof(W) / 2;
     int row, byte, left;  // this lane's first row, place in it, and elements from there to the last column
-    __device__ __forceinline__ Rows(int n, int N, int lane)
-        : row(lane / kWords), byte(lane % kWords * (int)sizeof(W)), left(N - n - byte / 2) {}
+    int N;
+    unsigned *dbg;
+    __device__ __forceinline__ Rows(int n, int N, int lane, unsigned *dbg)
+        : row(lane / kWords), byte(lane % kWords * (int)sizeof(W)), left(N - n - byte / 2), N(N), dbg(dbg) {}
+    // Whether this lane's elements of row r, from column n on, are the tensor's.
+    __device__ __forceinline__ bool ok(long long ld, int r, int n, int M, unsigned bit) const {
+        return left <= 0 || dbg_ok(dbg, (size_t)r * ld + n + byte / 2 + min(left, kEach) - 1, (size_t)(M - 1) * ld + N, bit);
+    }
     __device__ __forceinline__ void in(char *box, const void *base, long long ld, int m, int n, int M) const {
         const uint16_t *at = (const uint16_t *)base + (size_t)(m + row) * ld + n + byte / 2;
         const int rows = min(32, M - m);
@@ -248,9 +255,10 @@ template <typename W> struct Rows {
                 const int r = row + (b + i) * kStep;
                 const uint16_t *f = at + (size_t)(b + i) * kStep * ld;
                 x[i] = W{};
-                if (r < rows && left >= kEach) {
+                const bool there = r < rows && ok(ld, m + r, n, M, DBG_LOAD);
+                if (there && left >= kEach) {
                     x[i] = *(const W *)f;
-                } else if (r < rows && left > 0) {
+                } else if (there && left > 0) {
 #pragma unroll
                     for (int e = 0; e < kEach; ++e)
                         if (e < left) ((uint16_t *)&x[i])[e] = f[e];
@@ -267,6 +275,7 @@ template <typename W> struct Rows {
 #pragma unroll 8
         for (int r = row; r < rows; r += kStep, to += kStep * ld) {
             const W x = *(const W *)(box + spot(r, byte >> 4) + (byte & 15));
+            if (!ok(ld, m + r, n, M, DBG_STORE)) continue;
             if (left >= kEach) {
                 *(W *)to = x;
             } else {
@@ -278,26 +287,26 @@ template <typename W> struct Rows {
     }
 };
 __device__ __forceinline__ void box_in(char *box, const void *base, long long ld, int m, int n, int M, int N, int lane,
-                                       int unit) {
+                                       int unit, unsigned *dbg) {
     if (unit == 16)
-        Rows<uint4>(n, N, lane).in(box, base, ld, m, n, M);
+        Rows<uint4>(n, N, lane, dbg).in(box, base, ld, m, n, M);
     else if (unit == 8)
-        Rows<uint2>(n, N, lane).in(box, base, ld, m, n, M);
+        Rows<uint2>(n, N, lane, dbg).in(box, base, ld, m, n, M);
     else if (unit == 4)
-        Rows<uint32_t>(n, N, lane).in(box, base, ld, m, n, M);
+        Rows<uint32_t>(n, N, lane, dbg).in(box, base, ld, m, n, M);
     else
-        Rows<uint16_t>(n, N, lane).in(box, base, ld, m, n, M);
+        Rows<uint16_t>(n, N, lane, dbg).in(box, base, ld, m, n, M);
 }
 __device__ __forceinline__ void box_out(const char *box, void *base, long long ld, int m, int n, int M, int N, int lane,
-                                        int unit) {
+                                        int unit, unsigned *dbg) {
     if (unit == 16)
-        Rows<uint4>(n, N, lane).out(box, base, ld, m, n, M);
+        Rows<uint4>(n, N, lane, dbg).out(box, base, ld, m, n, M);
     else if (unit == 8)
-        Rows<uint2>(n, N, lane).out(box, base, ld, m, n, M);
+        Rows<uint2>(n, N, lane, dbg).out(box, base, ld, m, n, M);
     else if (unit == 4)
-        Rows<uint32_t>(n, N, lane).out(box, base, ld, m, n, M);
+        Rows<uint32_t>(n, N, lane, dbg).out(box, base, ld, m, n, M);
     else
-        Rows<uint16_t>(n, N, lane).out(box, base, ld, m, n, M);
+        Rows<uint16_t>(n, N, lane, dbg).out(box, base, ld, m, n, M);
 }
 
 template <typename T, bool A_MN, bool B_MN, int BN, bool PAIR>
@@ -442,14 +451,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int m0 = t.m + rank * BM + 32 * quarter, n0 = t.n + c0, n1 = min(p.N - n0, each);
             auto addend = [&](int n) {
                 begin();
-                box_in(box, p.residual, p.ldr, m0, n0 + n, p.M, p.N, lane, p.unit_r);
+                box_in(box, p.residual, p.ldr, m0, n0 + n, p.M, p.N, lane, p.unit_r, p.dbg);
                 __syncwarp();
             };
             const bool early = p.residual && !p.pre && !p.partial && n1 > 0;
             if (!p.partial) {
                 __syncwarp();
                 for (int j = lane; j < BN / 2; j += 32)
-                    bs[j] = p.bias && n0 + j < p.N ? as_f32(((const T *)p.bias)[n0 + j]) : 0.f;
+                    bs[j] = p.bias && n0 + j < p.N && dbg_ok(p.dbg, (size_t)(n0 + j), (size_t)p.N, DBG_LOAD)
+                                ? as_f32(((const T *)p.bias)[n0 + j]) : 0.f;
                 __syncwarp();
                 if (early) addend(0);
             }
@@ -481,10 +491,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (p.partial) {
                     const int m = m0 + lane;
                     if (m < p.M) {
-                        float *to = p.partial + ((size_t)(i / p.tiles) * p.M + m) * p.ldw + n0 + n;
+                        const size_t at = ((size_t)(i / p.tiles) * p.M + m) * p.ldw + n0 + n;
+                        float *to = p.partial + at;
 #pragma unroll
                         for (int j = 0; j < 32; j += 4)
-                            if (n0 + n + j < p.ldw)
+                            if (n0 + n + j < p.ldw && dbg_ok(p.dbg, at + j + 3, p.partial_floats, DBG_STORE))
                                 *(float4 *)(to + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
                     }
                     continue;
@@ -525,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     } else {
                         __syncwarp();
-                        box_out(box, to, ld, m0, n0 + n, p.M, p.N, lane, p.unit_o);
+                        box_out(box, to, ld, m0, n0 + n, p.M, p.N, lane, p.unit_o, p.dbg);
                         __syncwarp();
                     }
                 };
@@ -565,12 +576,14 @@ __global__ void __launch_bounds__(256) kda_linear_join_kernel(const Params p) {
     const float *at = p.partial + m * p.ldw + n;
     float v[4] = {};
     for (int s = 0; s < p.splits; ++s) {
-        const float4 x = *(const float4 *)(at + (size_t)s * p.M * p.ldw);
+        const float *part = at + (size_t)s * p.M * p.ldw;
+        if (!dbg_ok(p.dbg, (size_t)(part - p.partial) + 3, p.partial_floats, DBG_LOAD)) continue;
+        const float4 x = *(const float4 *)part;
         v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        if (n + j >= p.N) break;
+        if (n + j >= p.N || !dbg_ok(p.dbg, (size_t)m * p.N + n + j, (size_t)p.M * p.N, DBG_STORE)) break;
         const float x = v[j] + (p.bias ? as_f32(((const T *)p.bias)[n + j]) : 0.f);
         if (p.pre) ((T *)p.pre)[m * p.ldp + n + j] = from_f32<T>(x);
         float y = activate(x, p.act);
@@ -711,6 +724,7 @@ template <typename T> cudaError_t run(const GemmArgs &a, cudaStream_t stream) {
     p.act = a.act;
     p.ldw = q.ldw;
     p.partial = q.splits > 1 ? a.partial : nullptr;
+    p.partial_floats = a.partial_floats;
     p.dbg = a.dbg;
     p.give_up = a.give_up;
     Boundary o(2, 8), r(2, 8);

@@ -72,12 +72,14 @@ __global__ void __launch_bounds__(32 * kWarps) kda_linear_small_kernel(const Gem
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int n = n0 + row + 8 * h;
-                w[i][h] = in && n < a.N ? *(const uint4 *)(W + (size_t)n * a.ldb + k) : none;
+                w[i][h] = in && n < a.N && dbg_ok(a.dbg, (size_t)n * a.K + k + 7, (size_t)a.N * a.K, DBG_LOAD)
+                              ? *(const uint4 *)(W + (size_t)n * a.ldb + k) : none;
             }
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 const int m = row + 8 * t;
-                b[i][t] = in && m < a.M ? *(const uint4 *)(x + (size_t)m * a.lda + k) : none;
+                b[i][t] = in && m < a.M && dbg_ok(a.dbg, (size_t)m * a.K + k + 7, (size_t)a.M * a.K, DBG_LOAD)
+                              ? *(const uint4 *)(x + (size_t)m * a.lda + k) : none;
             }
         }
 #pragma unroll
@@ -147,7 +149,9 @@ __global__ void __launch_bounds__(32 * kWarps + 32, 1) kda_linear_long_kernel(co
         bool ok = true;
         for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
             const int row = 16 * tile + lane, m = lane - 16;
-            const int there = min(16, a.N - 16 * tile) + a.M;
+            const bool mine = lane < 16 ? row < a.N && dbg_ok(a.dbg, (size_t)row, (size_t)a.N, DBG_LOAD)
+                                        : m < a.M && dbg_ok(a.dbg, (size_t)m, (size_t)a.M, DBG_LOAD);
+            const int there = __popc(__ballot_sync(0xffffffffu, mine));
             for (int c = 0; c < chunks; ++c, ++n) {
                 const int st = n % S::kStages, k = c * kChunk;
                 if (n >= S::kStages && !(ok = wait(s.empty + st, (n / S::kStages - 1) & 1))) break;
@@ -155,11 +159,7 @@ __global__ void __launch_bounds__(32 * kWarps + 32, 1) kda_linear_long_kernel(co
                 if (lane == 0) tc::mbar_arrive_expect_tx(s.full + st, there * bytes);
                 __syncwarp();
                 char *to = s.raw[st] + lane * kPitch;
-                if (lane < 16) {
-                    if (row < a.N) copy_row(to, W + (size_t)row * a.ldb + k, bytes, s.full + st);
-                } else if (m < a.M) {
-                    copy_row(to, x + (size_t)m * a.lda + k, bytes, s.full + st);
-                }
+                if (mine) copy_row(to, lane < 16 ? W + (size_t)row * a.ldb + k : x + (size_t)m * a.lda + k, bytes, s.full + st);
                 __syncwarp();
             }
         }
@@ -230,7 +230,8 @@ __global__ void __launch_bounds__(256) kda_linear_copy_kernel(const CopyArgs a0,
         w[j] = __funnelshift_r(w[j], w[j + 1], 16 * s);
         if (2 * j + 1 >= left) w[j] &= 2 * j < left ? 0xffffu : 0u;
     }
-    *(uint4 *)((uint16_t *)a.dst + r * a.ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (dbg_ok(a.dbg, (size_t)(r * a.ldd + c + 7), (size_t)(a.rows * a.ldd), DBG_STORE))
+        *(uint4 *)((uint16_t *)a.dst + r * a.ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // dpre and the sums of its columns.  dpre is rounded to 16 bits because the products that read it take 16-bit
@@ -266,7 +267,8 @@ __global__ void __launch_bounds__(256) kda_linear_dact_kernel(const DActArgs a, 
                     d.put(i, g);
                 }
             }
-            if (a.dpre) *(Vec<T, V> *)((T *)a.dpre + m * a.ldd + n) = d;
+            if (a.dpre && dbg_ok(a.dbg, (size_t)(m * a.ldd + n + V - 1), (size_t)((a.M - 1) * a.ldd + a.N), DBG_STORE))
+                *(Vec<T, V> *)((T *)a.dpre + m * a.ldd + n) = d;
         }
     }
     if (!a.dbias) return;
@@ -277,7 +279,8 @@ __global__ void __launch_bounds__(256) kda_linear_dact_kernel(const DActArgs a, 
         float s = 0.f;
 #pragma unroll
         for (int w = 0; w < 8; ++w) s += red[w][i];
-        if (blockIdx.x * 32 * V + i < a.N) a.partial[(size_t)blockIdx.y * a.N + blockIdx.x * 32 * V + i] = s;
+        const size_t at = (size_t)blockIdx.y * a.N + blockIdx.x * 32 * V + i;
+        if (blockIdx.x * 32 * V + i < a.N && dbg_ok(a.dbg, at, a.partial_floats, DBG_STORE)) a.partial[at] = s;
     }
 }
 template <typename T>
@@ -287,8 +290,9 @@ __global__ void __launch_bounds__(256) kda_linear_dbias_kernel(const DActArgs a,
     if (c >= a.N) return;
     float s = 0.f;
 #pragma unroll 8
-    for (int i = 0; i < n; ++i) s += a.partial[(size_t)i * a.N + c];
-    ((T *)a.dbias)[c] = from_f32<T>(s);
+    for (int i = 0; i < n; ++i)
+        if (dbg_ok(a.dbg, (size_t)i * a.N + c, a.partial_floats, DBG_LOAD)) s += a.partial[(size_t)i * a.N + c];
+    if (dbg_ok(a.dbg, (size_t)c, (size_t)a.N, DBG_STORE)) ((T *)a.dbias)[c] = from_f32<T>(s);
 }
 
 template <typename T, int V> cudaError_t dact(const DActArgs &a, cudaStream_t stream) {

@@ -72,11 +72,14 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
             const Four Aj = scaled(load_states(a.A, ch, n0, a.N, in, turn), kLog2e);
             Four g = {both(0.f), both(0.f)};
             if (!ENDS && p.len >= 0 && in) {  // from the segments behind this one
-                g = load_states(a.d_final, (size_t)p.seq * a.D + ch, n0, a.N, a.d_final, turn);
+                const bool given = a.d_final && dbg_ok(a.dbg, (size_t)p.seq, (size_t)a.tok.num_seqs, DBG_LOAD);
+                g = load_states(a.d_final, (size_t)p.seq * a.D + ch, n0, a.N, given, turn);
                 const int behind = (p.total + a.segment - 1) / a.segment - 1 - p.index;
                 for (int i = k.slot + behind; i > k.slot; --i) {
                     const size_t at = (size_t)i * a.D + ch;
-                    if (!dbg_ok(a.dbg, at * NP + NP - 1, a.segment_floats, DBG_LOAD)) break;
+                    if (!dbg_ok(a.dbg, at * NP + NP - 1, a.segment_floats, DBG_LOAD) ||
+                        !dbg_ok(a.dbg, at, a.sum_floats, DBG_LOAD))
+                        break;
                     g = fma(decay(both(a.sums[at]), Aj), g, four(*(const float4 *)(a.ends + at * NP + n0)));
                 }
             }
@@ -350,12 +353,13 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
             const int t = qt + x * kStep;
             if (ENDS || !a.z || t >= kTile || t >= rows) continue;
             const float *at = open_row(a, row_of(i) + t) + qc;
+            const bool there = left <= 0 || dbg_ok(a.dbg, (size_t)(at - a.open) + min(left, 8) - 1, a.open_floats, DBG_LOAD);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (quads) {
+                if (there && quads) {
                     if (4 * h < left) v = *(const float4 *)(at + 4 * h);
-                } else {
+                } else if (there) {
                     if (4 * h < left) v.x = at[4 * h];
                     if (4 * h + 1 < left) v.y = at[4 * h + 1];
                     if (4 * h + 2 < left) v.z = at[4 * h + 2];
@@ -375,6 +379,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
             const int t = qt + x * kStep;
             if (t >= kTile || t >= rows) continue;
             const long long row = row_of(i) + t;
+            if (!dbg_ok(a.dbg, (size_t)row, (size_t)a.tok.rows(), DBG_STORE)) continue;
             const Vec<T, 8> u = raw[0][x][tid], dl = raw[1][x][tid], dy = raw[2][x][tid];
             Vec<T, 8> z, du, dd, dz;
             if (a.z) z = raw[3][x][tid];
@@ -405,8 +410,8 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
             float v = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) v += s.bc[b][w][t][x];
-            if (t < rows)
-                a.part_bc[(((size_t)k.blk * a.tok.rows() + row_of(i) + t) * a.G + k.group) * 2 * NP + x] = v;
+            const size_t at = (((size_t)k.blk * a.tok.rows() + row_of(i) + t) * a.G + k.group) * 2 * NP + x;
+            if (t < rows && dbg_ok(a.dbg, at, a.part_bc_floats, DBG_STORE)) a.part_bc[at] = v;
         }
     };
     if (tiles > 0) {
@@ -450,11 +455,12 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
             x += sum[0][t * S::kRow + tid];
             y += sum[1][t * S::kRow + tid];
         }
+        const size_t at = ENDS ? seg + k.c0 + tid : 2 * seg + k.c0 + tid;
         if (ENDS) {
-            a.sums[seg + k.c0 + tid] = x;
-        } else {
-            a.part_D[2 * seg + k.c0 + tid] = x;
-            a.part_D[2 * seg + a.D + k.c0 + tid] = y;
+            if (dbg_ok(a.dbg, at, a.sum_floats, DBG_STORE)) a.sums[at] = x;
+        } else if (dbg_ok(a.dbg, at + a.D, a.part_D_floats, DBG_STORE)) {
+            a.part_D[at] = x;
+            a.part_D[at + a.D] = y;
         }
     }
     cp_async_wait_newest<0>();
@@ -474,8 +480,10 @@ __global__ void __launch_bounds__(256) kda_scan_sum_bc_kernel(const ScanArgs a, 
     float s = 0.f;
     const size_t step = (size_t)a.tok.rows() * wide;
 #pragma unroll 8
-    for (int b = 0; b < nb; ++b) s += a.part_bc[b * step + i];
-    ((T *)(x < np ? a.dB : a.dC))[((size_t)row * a.G + group) * a.N + n] = from_f32<T>(s);
+    for (int b = 0; b < nb; ++b)
+        if (dbg_ok(a.dbg, b * step + i, a.part_bc_floats, DBG_LOAD)) s += a.part_bc[b * step + i];
+    const size_t at = ((size_t)row * a.G + group) * a.N + n;
+    if (dbg_ok(a.dbg, at, (size_t)a.tok.rows() * a.G * a.N, DBG_STORE)) ((T *)(x < np ? a.dB : a.dC))[at] = from_f32<T>(s);
 }
 
 // dA, dskip and ddelta_bias: sums over the segments, in order.
@@ -487,14 +495,17 @@ __global__ void __launch_bounds__(256) kda_scan_sum_params_kernel(const ScanArgs
         const int n = (int)(i % np);
         if (n >= a.N) return;
 #pragma unroll 4
-        for (int j = 0; j < slots; ++j) s += a.part_A[j * states + i];
-        a.dA[i / np * a.N + n] = s;
+        for (int j = 0; j < slots; ++j)
+            if (dbg_ok(a.dbg, (size_t)(j * states + i), a.segment_floats, DBG_LOAD)) s += a.part_A[j * states + i];
+        if (dbg_ok(a.dbg, (size_t)(i / np * a.N + n), (size_t)a.D * a.N, DBG_STORE)) a.dA[i / np * a.N + n] = s;
     } else if (i < states + 2 * a.D) {
         const int x = (int)(i - states);
 #pragma unroll 4
-        for (int j = 0; j < slots; ++j) s += a.part_D[(size_t)j * 2 * a.D + x];
+        for (int j = 0; j < slots; ++j)
+            if (dbg_ok(a.dbg, (size_t)j * 2 * a.D + x, a.part_D_floats, DBG_LOAD)) s += a.part_D[(size_t)j * 2 * a.D + x];
         float *to = x < a.D ? a.dskip : a.ddelta_bias;
-        if (to) to[x < a.D ? x : x - a.D] = s;
+        const int c = x < a.D ? x : x - a.D;
+        if (to && dbg_ok(a.dbg, (size_t)c, (size_t)a.D, DBG_STORE)) to[c] = s;
     }
 }
 

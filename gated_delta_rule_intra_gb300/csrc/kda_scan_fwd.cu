@@ -50,10 +50,13 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
             const Four Aj = scaled(load_states(a.A, ch, n0, a.N, in, turn), kLog2e);
             Four hj = {both(0.f), both(0.f)};
             if (!ENDS && in) {
-                hj = load_states(a.initial, (size_t)p.seq * a.D + ch, n0, a.N, a.initial, turn);
+                const bool given = a.initial && dbg_ok(a.dbg, (size_t)p.seq, (size_t)a.tok.num_seqs, DBG_LOAD);
+                hj = load_states(a.initial, (size_t)p.seq * a.D + ch, n0, a.N, given, turn);
                 for (int g = k.slot - p.index; g < k.slot; ++g) {
                     const size_t at = (size_t)g * a.D + ch;
-                    if (!dbg_ok(a.dbg, at * NP + NP - 1, a.segment_floats, DBG_LOAD)) break;
+                    if (!dbg_ok(a.dbg, at * NP + NP - 1, a.segment_floats, DBG_LOAD) ||
+                        !dbg_ok(a.dbg, at, a.sum_floats, DBG_LOAD))
+                        break;
                     hj = fma(decay(both(a.sums[at]), Aj), hj, four(*(const float4 *)(a.ends + at * NP + n0)));
                 }
             }
@@ -224,7 +227,8 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
                 }
                 put_pair(out, e, y);
             }
-            if (a.open) {  // what the gate multiplies, for the gate's gradient
+            if (a.open && dbg_ok(a.dbg, (size_t)(open_row(a, row) - a.open) + qc + min(left, 8) - 1, a.open_floats, DBG_STORE)) {
+                // what the gate multiplies, for the gate's gradient
                 float *at = open_row(a, row) + qc;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -274,7 +278,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
         if (tid < k.channels) {
             float x = 0.f;
             for (int t = 0; t < min(kTile, kStep); ++t) x += sum[t][tid];
-            a.sums[seg + k.c0 + tid] = x;
+            if (dbg_ok(a.dbg, seg + k.c0 + tid, a.sum_floats, DBG_STORE)) a.sums[seg + k.c0 + tid] = x;
         }
     }
     cp_async_wait_newest<0>();

@@ -47,7 +47,9 @@ __global__ void __launch_bounds__(kThreads) kda_scan_step_kernel(const ScanArgs 
     for (int i = 0; i < R; ++i) {
         const int r = r0 + i;
         const long long slot = r < a.requests ? a.state_indices ? a.state_indices[r] : r : -1;
-        if (slot >= 0 && slot < a.num_states) live |= 1u << i;
+        if (slot >= 0 && slot < a.num_states &&
+            dbg_ok(a.dbg, ((size_t)slot * a.D + ch) * a.N + a.N - 1, (size_t)a.num_states * a.D * a.N, DBG_STORE))
+            live |= 1u << i;
         st[i] = a.state + ((size_t)(live >> i & 1 ? slot : 0) * a.D + ch) * a.N + n0;
         h[i] = {both(0.f), both(0.f)};
         if ((live >> i & 1) && in && some) h[i] = WIDE ? four(__ldcs((const float4 *)st[i])) : load_states(st[i], 0, 0, a.N - n0, true);

@@ -70,7 +70,7 @@ extern "C" {
 
 /*
  * ABI versions (kda_abi_version() returns the loaded library's):
- *   13 kda_debug_set_give_up
+ *   13 kda_debug_set_give_up, KDA_DBG_SHORT
  *   12 kda_conv_fwd, kda_conv_bwd, kda_conv_step, kda_scan_fwd, kda_scan_bwd, kda_scan_step,
  *      kda_linear_fwd, kda_linear_bwd and their option structs and size queries
  *   11 kda_chunk_bwd's zero_rest also takes KDA_GATE_GRADS_FP32, kda_chunk_fwd's saved either
@@ -707,18 +707,21 @@ const char *kda_status_str(kda_status_t status);
  * and layer norm the tokens and rows that are read, states, and the slots of saved and
  * workspace buffers too) against the extent of its buffer.  An index out of range sets
  * KDA_DBG_STORE or KDA_DBG_LOAD in a caller-owned device word and the access is skipped;
- * a bounded wait that gives up sets KDA_DBG_WAIT.  Nothing traps or asserts.  TMA tiles
+ * a bounded wait that gives up sets KDA_DBG_WAIT.  Where the caller has set KDA_DBG_SHORT in the
+ * word, every extent counts as one less: the checks of a buffer's last element or row then report and
+ * skip it, which shows that they are there.  Nothing traps or asserts.  TMA tiles
  * need no check: the tensor maps clip them.
  *
  * kda_debug_checks() is 1 in such a build, 0 otherwise.  kda_debug_set_flags(word)
  * makes every later launch of this library report into `word` (device memory, 4 bytes,
- * caller-owned; NULL stops reporting); the library never clears or reads it.  Set it
+ * caller-owned; NULL stops reporting); the library never clears it.  Set it
  * before launching, from one thread.  Returns KDA_ERR_OPTION in a build without checks
  * and KDA_ERR_ALIGN for a word that is not 4-byte aligned.
  */
 #define KDA_DBG_STORE 1u
 #define KDA_DBG_LOAD 2u
 #define KDA_DBG_WAIT 4u
+#define KDA_DBG_SHORT 8u
 int kda_debug_checks(void);
 kda_status_t kda_debug_set_flags(unsigned int *device_word);
 
