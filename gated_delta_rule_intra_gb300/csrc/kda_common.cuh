@@ -65,10 +65,9 @@ __device__ __forceinline__ void cp_async_wait_all() {
 constexpr unsigned DBG_STORE = 1u;  // an output index
 constexpr unsigned DBG_LOAD = 2u;   // an input index
 constexpr unsigned DBG_WAIT = 4u;   // a bounded wait gave up
-constexpr unsigned DBG_SHORT = 8u;  // set by the caller: every extent counts as one less
 #ifdef KDA_DEBUG_CHECKS
 __device__ __forceinline__ bool dbg_ok(unsigned *flags, size_t idx, size_t n, unsigned bit) {
-    if (idx + (flags && *(volatile unsigned *)flags & DBG_SHORT ? 1 : 0) < n) return true;
+    if (idx < n) return true;
     if (flags) atomicOr(flags, bit);
     return false;
 }

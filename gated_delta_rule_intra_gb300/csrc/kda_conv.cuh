@@ -104,7 +104,7 @@ __device__ __forceinline__ void fetch_rows(char *to, const ConvArgs &a, const Pi
     const long long ahead = step * stride * E;
     const bool last = ODD && s && word == 0;
     auto ok = [&](int x) {
-        return x >= 0 && x < p.total && dbg_ok(a.dbg, (size_t)(p.row0 + x), (size_t)a.tok.rows(), DBG_LOAD);
+        return x >= 0 && x < p.total && in_bounds(a.dbg, (size_t)(p.row0 + x), (size_t)a.tok.rows(), DBG_LOAD);
     };
     auto each = [&](auto copy) {
         int x = pos + row;
@@ -145,7 +145,7 @@ __device__ __forceinline__ void fetch_inputs(char *to, const ConvArgs &a, const 
     for (int i = threadIdx.x; i < front * S::CH; i += kThreads) {
         const int r = i / S::CH, e = i % S::CH;
         const size_t row = (size_t)p.seq * (W - 1) + r;
-        const bool ok = c0 + e < a.D && dbg_ok(a.dbg, row, (size_t)a.tok.num_seqs * (W - 1), DBG_LOAD);
+        const bool ok = c0 + e < a.D && in_bounds(a.dbg, row, (size_t)a.tok.num_seqs * (W - 1), DBG_LOAD);
         const int s = ODD ? shifted<T>(a.x, (p.row0 + r - (W - 1)) * a.x_stride + c0) : 0;
         ((T *)(to + r * S::kRow))[s + e] = ok ? ((const T *)a.initial)[row * a.D + c0 + e] : from_f32<T>(0.f);
     }
@@ -157,7 +157,7 @@ __device__ __forceinline__ void leave_rows(const T (*from)[CH], const ConvArgs &
                                            long long stride, int c0) {
     constexpr int kStep = kThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, left = min(CH, a.D - c0);
-    if (!dbg_ok(a.dbg, (size_t)(p.row0 + p.begin + p.len - 1), (size_t)a.tok.rows(), DBG_STORE)) return;
+    if (!in_bounds(a.dbg, (size_t)(p.row0 + p.begin + p.len - 1), (size_t)a.tok.rows(), DBG_STORE)) return;
     const long long first = (p.row0 + p.begin + warp) * stride + c0;
     T *to = (T *)base + first;
     if constexpr (sizeof(T) == 4) {
@@ -191,7 +191,7 @@ inline long long resident(int bytes, int most) {
 template <int W, int CH>
 __device__ __forceinline__ void load_params(const ConvArgs &a, int c0, float (*w)[CH]) {
     for (int i = threadIdx.x; i < CH; i += kThreads) {
-        const bool in = c0 + i < a.D && dbg_ok(a.dbg, (size_t)(c0 + i), (size_t)a.D, DBG_LOAD);
+        const bool in = c0 + i < a.D && in_bounds(a.dbg, (size_t)(c0 + i), (size_t)a.D, DBG_LOAD);
 #pragma unroll
         for (int j = 0; j < W; ++j) w[j][i] = in ? param(a.weight, a.wdtype, (size_t)(c0 + i) * W + j, 0.f) : 0.f;
         w[W][i] = in ? param(a.bias, a.wdtype, c0 + i, 0.f) : 0.f;

@@ -135,12 +135,12 @@ __global__ void __launch_bounds__(kThreads, 4)
                         const size_t row = (size_t)p.seq * (W - 1) + last;
 #pragma unroll
                         for (int e = 0; e < V; ++e)
-                            if (e < left && dbg_ok(a.dbg, row, (size_t)a.tok.num_seqs * (W - 1), DBG_LOAD))
+                            if (e < left && in_bounds(a.dbg, row, (size_t)a.tok.num_seqs * (W - 1), DBG_LOAD))
                                 dx[e] += as_f32(((const T *)a.d_final)[row * a.D + c + e]);
                     }
                     Vec<T, V> y;
                     narrow(y, dx);
-                    if (dbg_ok(a.dbg, (size_t)(p.row0 + pos), (size_t)a.tok.rows(), DBG_STORE))
+                    if (in_bounds(a.dbg, (size_t)(p.row0 + pos), (size_t)a.tok.rows(), DBG_STORE))
                         *(Vec<T, V> *)out = y;
                     out += step;
                 }
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 #pragma unroll
             for (int k = 0; k < S::kRuns; ++k) x += s.red[k][i];
             const size_t at = ((size_t)blockIdx.y * (W + 1) + j) * a.D + c0 + i;
-            if (c0 + i < a.D && dbg_ok(a.dbg, at, a.partial_floats, DBG_STORE)) a.partial[at] = x;
+            if (c0 + i < a.D && in_bounds(a.dbg, at, a.partial_floats, DBG_STORE)) a.partial[at] = x;
         }
     }
 }
@@ -181,11 +181,11 @@ __global__ void __launch_bounds__(256) kda_conv_sum_kernel(const ConvArgs a) {
 #pragma unroll 8
     for (int k = 0; k < a.partials; ++k) {
         const size_t at = ((size_t)k * (a.W + 1) + j) * a.D + c;
-        if (dbg_ok(a.dbg, at, a.partial_floats, DBG_LOAD)) s += a.partial[at];
+        if (in_bounds(a.dbg, at, a.partial_floats, DBG_LOAD)) s += a.partial[at];
     }
     if (j < a.W) {
-        if (dbg_ok(a.dbg, (size_t)c * a.W + j, (size_t)a.D * a.W, DBG_STORE)) a.dweight[(size_t)c * a.W + j] = s;
-    } else if (dbg_ok(a.dbg, (size_t)c, (size_t)a.D, DBG_STORE)) {
+        if (in_bounds(a.dbg, (size_t)c * a.W + j, (size_t)a.D * a.W, DBG_STORE)) a.dweight[(size_t)c * a.W + j] = s;
+    } else if (in_bounds(a.dbg, (size_t)c, (size_t)a.D, DBG_STORE)) {
         a.dbias[c] = s;
     }
 }
@@ -206,10 +206,10 @@ template <typename T> __global__ void __launch_bounds__(256) kda_conv_initial_ke
         p.row0 = (long long)n * a.tok.T;
         p.total = a.tok.T;
     }
-    auto row_ok = [&](int pos) { return dbg_ok(a.dbg, (size_t)(p.row0 + pos), (size_t)a.tok.rows(), DBG_LOAD); };
+    auto row_ok = [&](int pos) { return in_bounds(a.dbg, (size_t)(p.row0 + pos), (size_t)a.tok.rows(), DBG_LOAD); };
     auto state = [&](const void *of, int row) {
         const size_t at = (size_t)n * (W - 1) + row;
-        return dbg_ok(a.dbg, at, (size_t)a.tok.num_seqs * (W - 1), DBG_LOAD) ? as_f32(((const T *)of)[at * a.D + c]) : 0.f;
+        return in_bounds(a.dbg, at, (size_t)a.tok.num_seqs * (W - 1), DBG_LOAD) ? as_f32(((const T *)of)[at * a.D + c]) : 0.f;
     };
     auto input = [&](int pos) {
         return pos >= 0 ? row_ok(pos) ? as_f32(((const T *)a.x)[(p.row0 + pos) * a.x_stride + c]) : 0.f
@@ -231,7 +231,7 @@ template <typename T> __global__ void __launch_bounds__(256) kda_conv_initial_ke
     for (int r = 0; r < W - 1; ++r) {
         const int last = r - p.total;  // where it is still among the last inputs
         if (a.d_final && last >= 0) d[r] += state(a.d_final, last);
-        if (dbg_ok(a.dbg, (size_t)n, (size_t)a.tok.num_seqs, DBG_STORE))
+        if (in_bounds(a.dbg, (size_t)n, (size_t)a.tok.num_seqs, DBG_STORE))
             ((T *)a.d_initial)[((size_t)n * (W - 1) + r) * a.D + c] = from_f32<T>(d[r]);
     }
 }

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 4)
                     }
                     Vec<T, V> y;
                     narrow(y, acc);
-                    if (dbg_ok(a.dbg, (size_t)(p.row0 + p.begin + r0 + i), (size_t)a.tok.rows(), DBG_STORE))
+                    if (in_bounds(a.dbg, (size_t)(p.row0 + p.begin + r0 + i), (size_t)a.tok.rows(), DBG_STORE))
                         *(Vec<T, V> *)out = y;
                     out += step;
                 }
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 4)
                 const int r = i / S::CH, e = i % S::CH;
                 const size_t row = (size_t)p.seq * (W - 1) + r;
                 const long long at = (p.row0 + p.total - (W - 1) + r) * a.x_stride + c0;
-                if (c0 + e < a.D && dbg_ok(a.dbg, row, (size_t)a.tok.num_seqs * (W - 1), DBG_STORE))
+                if (c0 + e < a.D && in_bounds(a.dbg, row, (size_t)a.tok.num_seqs * (W - 1), DBG_STORE))
                     ((T *)a.final)[row * a.D + c0 + e] =
                         ((const T *)s.x[b][p.len + r])[(ODD ? shifted<T>(a.x, at) : 0) + e];
             }
@@ -131,8 +131,8 @@ __global__ void __launch_bounds__(256) kda_conv_step_kernel(const ConvArgs a) {
     const bool none = slot < 0 || slot >= a.num_states;  // no request here: y is zero
     Vec<T, V> y, x[W];
     y.clear();
-    if (!none && dbg_ok(a.dbg, (size_t)n, (size_t)a.N, DBG_LOAD) &&
-        dbg_ok(a.dbg, ((size_t)(slot + 1) * (W - 1) - 1) * a.D + c + V - 1, (size_t)a.num_states * (W - 1) * a.D, DBG_STORE)) {
+    if (!none && in_bounds(a.dbg, (size_t)n, (size_t)a.N, DBG_LOAD) &&
+        in_bounds(a.dbg, ((size_t)(slot + 1) * (W - 1) - 1) * a.D + c + V - 1, (size_t)a.num_states * (W - 1) * a.D, DBG_STORE)) {
         T *st = (T *)a.state + (size_t)slot * (W - 1) * a.D + c;
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) x[j] = *reinterpret_cast<const Vec<T, V> *>(st + (size_t)j * a.D);
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(256) kda_conv_step_kernel(const ConvArgs a) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) *reinterpret_cast<Vec<T, V> *>(st + (size_t)j * a.D) = x[j + 1];
     }
-    if (dbg_ok(a.dbg, (size_t)n, (size_t)a.N, DBG_STORE))
+    if (in_bounds(a.dbg, (size_t)n, (size_t)a.N, DBG_STORE))
         *reinterpret_cast<Vec<T, V> *>((T *)a.y + n * a.y_stride + c) = y;
 }
 

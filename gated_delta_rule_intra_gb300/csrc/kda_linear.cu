@@ -241,7 +241,7 @@ template <typename W> struct Rows {
         : row(lane / kWords), byte(lane % kWords * (int)sizeof(W)), left(N - n - byte / 2), N(N), dbg(dbg) {}
     // Whether this lane's elements of row r, from column n on, are the tensor's.
     __device__ __forceinline__ bool ok(long long ld, int r, int n, int M, unsigned bit) const {
-        return left <= 0 || dbg_ok(dbg, (size_t)r * ld + n + byte / 2 + min(left, kEach) - 1, (size_t)(M - 1) * ld + N, bit);
+        return left <= 0 || in_bounds(dbg, (size_t)r * ld + n + byte / 2 + min(left, kEach) - 1, (size_t)(M - 1) * ld + N, bit);
     }
     __device__ __forceinline__ void in(char *box, const void *base, long long ld, int m, int n, int M) const {
         const uint16_t *at = (const uint16_t *)base + (size_t)(m + row) * ld + n + byte / 2;
@@ -255,10 +255,10 @@ template <typename W> struct Rows {
                 const int r = row + (b + i) * kStep;
                 const uint16_t *f = at + (size_t)(b + i) * kStep * ld;
                 x[i] = W{};
-                const bool there = r < rows && ok(ld, m + r, n, M, DBG_LOAD);
-                if (there && left >= kEach) {
+                if (r < rows && !ok(ld, m + r, n, M, DBG_LOAD)) continue;
+                if (r < rows && left >= kEach) {
                     x[i] = *(const W *)f;
-                } else if (there && left > 0) {
+                } else if (r < rows && left > 0) {
 #pragma unroll
                     for (int e = 0; e < kEach; ++e)
                         if (e < left) ((uint16_t *)&x[i])[e] = f[e];
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!p.partial) {
                 __syncwarp();
                 for (int j = lane; j < BN / 2; j += 32)
-                    bs[j] = p.bias && n0 + j < p.N && dbg_ok(p.dbg, (size_t)(n0 + j), (size_t)p.N, DBG_LOAD)
+                    bs[j] = p.bias && n0 + j < p.N && in_bounds(p.dbg, (size_t)(n0 + j), (size_t)p.N, DBG_LOAD)
                                 ? as_f32(((const T *)p.bias)[n0 + j]) : 0.f;
                 __syncwarp();
                 if (early) addend(0);
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float *to = p.partial + at;
 #pragma unroll
                         for (int j = 0; j < 32; j += 4)
-                            if (n0 + n + j < p.ldw && dbg_ok(p.dbg, at + j + 3, p.partial_floats, DBG_STORE))
+                            if (n0 + n + j < p.ldw && in_bounds(p.dbg, at + j + 3, p.partial_floats, DBG_STORE))
                                 *(float4 *)(to + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
                     }
                     continue;
@@ -577,13 +577,13 @@ __global__ void __launch_bounds__(256) kda_linear_join_kernel(const Params p) {
     float v[4] = {};
     for (int s = 0; s < p.splits; ++s) {
         const float *part = at + (size_t)s * p.M * p.ldw;
-        if (!dbg_ok(p.dbg, (size_t)(part - p.partial) + 3, p.partial_floats, DBG_LOAD)) continue;
+        if (!in_bounds(p.dbg, (size_t)(part - p.partial) + 3, p.partial_floats, DBG_LOAD)) continue;
         const float4 x = *(const float4 *)part;
         v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        if (n + j >= p.N || !dbg_ok(p.dbg, (size_t)m * p.N + n + j, (size_t)p.M * p.N, DBG_STORE)) break;
+        if (n + j >= p.N || !in_bounds(p.dbg, (size_t)m * p.N + n + j, (size_t)p.M * p.N, DBG_STORE)) break;
         const float x = v[j] + (p.bias ? as_f32(((const T *)p.bias)[n + j]) : 0.f);
         if (p.pre) ((T *)p.pre)[m * p.ldp + n + j] = from_f32<T>(x);
         float y = activate(x, p.act);

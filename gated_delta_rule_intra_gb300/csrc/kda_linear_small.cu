@@ -43,7 +43,7 @@ __device__ __forceinline__ void finish(const GemmArgs &a, const float (*red)[MT]
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) v += red[w][t][l][i];
-        if (m >= a.M || n >= a.N || !dbg_ok(a.dbg, (size_t)m * a.N + n, (size_t)a.M * a.N, DBG_STORE)) continue;
+        if (m >= a.M || n >= a.N || !in_bounds(a.dbg, (size_t)m * a.N + n, (size_t)a.M * a.N, DBG_STORE)) continue;
         if (a.bias) v += as_f32(((const T *)a.bias)[n]);
         if (a.pre) ((T *)a.pre)[m * a.ldp + n] = from_f32<T>(v);
         v = activate(v, a.act);
@@ -72,13 +72,13 @@ __global__ void __launch_bounds__(32 * kWarps) kda_linear_small_kernel(const Gem
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int n = n0 + row + 8 * h;
-                w[i][h] = in && n < a.N && dbg_ok(a.dbg, (size_t)n * a.K + k + 7, (size_t)a.N * a.K, DBG_LOAD)
+                w[i][h] = in && n < a.N && in_bounds(a.dbg, (size_t)n * a.K + k + 7, (size_t)a.N * a.K, DBG_LOAD)
                               ? *(const uint4 *)(W + (size_t)n * a.ldb + k) : none;
             }
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 const int m = row + 8 * t;
-                b[i][t] = in && m < a.M && dbg_ok(a.dbg, (size_t)m * a.K + k + 7, (size_t)a.M * a.K, DBG_LOAD)
+                b[i][t] = in && m < a.M && in_bounds(a.dbg, (size_t)m * a.K + k + 7, (size_t)a.M * a.K, DBG_LOAD)
                               ? *(const uint4 *)(x + (size_t)m * a.lda + k) : none;
             }
         }
@@ -149,8 +149,8 @@ __global__ void __launch_bounds__(32 * kWarps + 32, 1) kda_linear_long_kernel(co
         bool ok = true;
         for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
             const int row = 16 * tile + lane, m = lane - 16;
-            const bool mine = lane < 16 ? row < a.N && dbg_ok(a.dbg, (size_t)row, (size_t)a.N, DBG_LOAD)
-                                        : m < a.M && dbg_ok(a.dbg, (size_t)m, (size_t)a.M, DBG_LOAD);
+            const bool mine = lane < 16 ? row < a.N && in_bounds(a.dbg, (size_t)row, (size_t)a.N, DBG_LOAD)
+                                        : m < a.M && in_bounds(a.dbg, (size_t)m, (size_t)a.M, DBG_LOAD);
             const int there = __popc(__ballot_sync(0xffffffffu, mine));
             for (int c = 0; c < chunks; ++c, ++n) {
                 const int st = n % S::kStages, k = c * kChunk;
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(256) kda_linear_copy_kernel(const CopyArgs a0,
     const int per = (a.width + 7) / 8;
     const long long i = (long long)(blockIdx.x - (blockIdx.x < first ? 0 : first)) * 256 + threadIdx.x, r = i / per;
     const int c = (int)(i - r * per) * 8, left = a.width - c;
-    if (r >= a.rows || !dbg_ok(a.dbg, (size_t)r, (size_t)a.rows, DBG_LOAD)) return;
+    if (r >= a.rows || !in_bounds(a.dbg, (size_t)r, (size_t)a.rows, DBG_LOAD)) return;
     const uintptr_t at = (uintptr_t)((const uint16_t *)a.src + r * a.lds + c);
     const int s = at & 2 ? 1 : 0;  // elements of the first word in front of ours
     const uint32_t *f = (const uint32_t *)(at & ~(uintptr_t)3);
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(256) kda_linear_copy_kernel(const CopyArgs a0,
         w[j] = __funnelshift_r(w[j], w[j + 1], 16 * s);
         if (2 * j + 1 >= left) w[j] &= 2 * j < left ? 0xffffu : 0u;
     }
-    if (dbg_ok(a.dbg, (size_t)(r * a.ldd + c + 7), (size_t)(a.rows * a.ldd), DBG_STORE))
+    if (in_bounds(a.dbg, (size_t)(r * a.ldd + c + 7), (size_t)(a.rows * a.ldd), DBG_STORE))
         *(uint4 *)((uint16_t *)a.dst + r * a.ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(256) kda_linear_dact_kernel(const DActArgs a, 
     if (n < a.N) {
 #pragma unroll 4
         for (long long m = m0 + warp; m < m1; m += 8) {
-            if (!dbg_ok(a.dbg, (size_t)m, (size_t)a.M, DBG_LOAD)) break;
+            if (!in_bounds(a.dbg, (size_t)m, (size_t)a.M, DBG_LOAD)) break;
             const auto dy = *(const Vec<T, V> *)((const T *)a.dy + m * a.lddy + n);
             Vec<T, V> p, d;
             if (a.act != ACT_NONE) p = *(const Vec<T, V> *)((const T *)a.pre + m * a.ldp + n);
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(256) kda_linear_dact_kernel(const DActArgs a, 
                     d.put(i, g);
                 }
             }
-            if (a.dpre && dbg_ok(a.dbg, (size_t)(m * a.ldd + n + V - 1), (size_t)((a.M - 1) * a.ldd + a.N), DBG_STORE))
+            if (a.dpre && in_bounds(a.dbg, (size_t)(m * a.ldd + n + V - 1), (size_t)((a.M - 1) * a.ldd + a.N), DBG_STORE))
                 *(Vec<T, V> *)((T *)a.dpre + m * a.ldd + n) = d;
         }
     }
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(256) kda_linear_dact_kernel(const DActArgs a, 
 #pragma unroll
         for (int w = 0; w < 8; ++w) s += red[w][i];
         const size_t at = (size_t)blockIdx.y * a.N + blockIdx.x * 32 * V + i;
-        if (blockIdx.x * 32 * V + i < a.N && dbg_ok(a.dbg, at, a.partial_floats, DBG_STORE)) a.partial[at] = s;
+        if (blockIdx.x * 32 * V + i < a.N && in_bounds(a.dbg, at, a.partial_floats, DBG_STORE)) a.partial[at] = s;
     }
 }
 template <typename T>
@@ -291,8 +291,8 @@ __global__ void __launch_bounds__(256) kda_linear_dbias_kernel(const DActArgs a,
     float s = 0.f;
 #pragma unroll 8
     for (int i = 0; i < n; ++i)
-        if (dbg_ok(a.dbg, (size_t)i * a.N + c, a.partial_floats, DBG_LOAD)) s += a.partial[(size_t)i * a.N + c];
-    if (dbg_ok(a.dbg, (size_t)c, (size_t)a.N, DBG_STORE)) ((T *)a.dbias)[c] = from_f32<T>(s);
+        if (in_bounds(a.dbg, (size_t)i * a.N + c, a.partial_floats, DBG_LOAD)) s += a.partial[(size_t)i * a.N + c];
+    if (in_bounds(a.dbg, (size_t)c, (size_t)a.N, DBG_STORE)) ((T *)a.dbias)[c] = from_f32<T>(s);
 }
 
 template <typename T, int V> cudaError_t dact(const DActArgs &a, cudaStream_t stream) {

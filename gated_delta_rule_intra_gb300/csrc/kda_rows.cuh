@@ -8,6 +8,17 @@
 namespace kda {
 namespace rows {
 
+// The debug build's check of an index (dbg_ok()).  Where its caller has set KDA_DBG_SHORT in the flag word, every
+// extent counts as one less, so that the checks of the last elements report.
+constexpr unsigned DBG_SHORT = 8u;
+__device__ __forceinline__ bool in_bounds(unsigned *flags, size_t idx, size_t n, unsigned bit) {
+#ifdef KDA_DEBUG_CHECKS
+    return dbg_ok(flags, idx + (flags && *(volatile unsigned *)flags & DBG_SHORT ? 1 : 0), n, bit);
+#else
+    return true;
+#endif
+}
+
 __device__ __forceinline__ float as_f32(float x) { return x; }
 __device__ __forceinline__ float as_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float as_f32(__half x) { return __half2float(x); }

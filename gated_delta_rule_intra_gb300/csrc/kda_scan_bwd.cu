@@ -72,13 +72,13 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
             const Four Aj = scaled(load_states(a.A, ch, n0, a.N, in, turn), kLog2e);
             Four g = {both(0.f), both(0.f)};
             if (!ENDS && p.len >= 0 && in) {  // from the segments behind this one
-                const bool given = a.d_final && dbg_ok(a.dbg, (size_t)p.seq, (size_t)a.tok.num_seqs, DBG_LOAD);
+                const bool given = a.d_final && in_bounds(a.dbg, (size_t)p.seq, (size_t)a.tok.num_seqs, DBG_LOAD);
                 g = load_states(a.d_final, (size_t)p.seq * a.D + ch, n0, a.N, given, turn);
                 const int behind = (p.total + a.segment - 1) / a.segment - 1 - p.index;
                 for (int i = k.slot + behind; i > k.slot; --i) {
                     const size_t at = (size_t)i * a.D + ch;
-                    if (!dbg_ok(a.dbg, at * NP + NP - 1, a.segment_floats, DBG_LOAD) ||
-                        !dbg_ok(a.dbg, at, a.sum_floats, DBG_LOAD))
+                    if (!in_bounds(a.dbg, at * NP + NP - 1, a.segment_floats, DBG_LOAD) ||
+                        !in_bounds(a.dbg, at, a.sum_floats, DBG_LOAD))
                         break;
                     g = fma(decay(both(a.sums[at]), Aj), g, four(*(const float4 *)(a.ends + at * NP + n0)));
                 }
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
                 for (int j = 0; j < 2; ++j) {
                     const size_t at = ((size_t)(2 * (tile0 + tiles - 1 - i) + half) * a.D + k.c0 + c[j]) * NP + n0;
                     const bool in = half * kHalf < rows_of(i) && c[j] < k.channels &&
-                                    dbg_ok(a.dbg, at + 3, a.saved_floats, DBG_LOAD);
+                                    in_bounds(a.dbg, at + 3, a.saved_floats, DBG_LOAD);
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                                      (uint32_t)__cvta_generic_to_shared(&s.h[ENDS ? 0 : i & 1][half][j][tid])),
                                  "l"(a.saved + (in ? at : 0)), "r"(in ? 16 : 0)
@@ -256,9 +256,9 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
             if (c[j] >= k.channels) continue;
             const Four g = four(make_float4(carry[j][0], carry[j][1], carry[j][2], carry[j][3]));
             if (!ENDS && p.len >= 0 && p.begin == 0 && a.d_initial &&
-                dbg_ok(a.dbg, (size_t)p.seq, (size_t)a.tok.num_seqs, DBG_STORE))
+                in_bounds(a.dbg, (size_t)p.seq, (size_t)a.tok.num_seqs, DBG_STORE))
                 store_states(a.d_initial, (size_t)p.seq * a.D + ch, n0, a.N, g, turn);
-            if (!dbg_ok(a.dbg, at + 3, a.segment_floats, DBG_STORE)) continue;
+            if (!in_bounds(a.dbg, at + 3, a.segment_floats, DBG_STORE)) continue;
             if (ENDS) {
                 *(float4 *)(a.ends + at) = one(g);
             } else {
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
     float2 dskip[4] = {}, dbias[4] = {};  // (ENDS: dskip is the sum of the step sizes)
     auto row_of = [&](int i) { return first + (tiles - 1 - i) * kTile; };
     auto fine = [&](int i) {
-        return i >= tiles || dbg_ok(a.dbg, (size_t)(row_of(i) + rows_of(i) - 1), (size_t)a.tok.rows(), DBG_LOAD);
+        return i >= tiles || in_bounds(a.dbg, (size_t)(row_of(i) + rows_of(i) - 1), (size_t)a.tok.rows(), DBG_LOAD);
     };
     auto fetch = [&](int i) {
         const int rows = fine(i) ? rows_of(i) : 0;
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
             const int t = qt + x * kStep;
             if (ENDS || !a.z || t >= kTile || t >= rows) continue;
             const float *at = open_row(a, row_of(i) + t) + qc;
-            const bool there = left <= 0 || dbg_ok(a.dbg, (size_t)(at - a.open) + min(left, 8) - 1, a.open_floats, DBG_LOAD);
+            const bool there = left <= 0 || in_bounds(a.dbg, (size_t)(at - a.open) + min(left, 8) - 1, a.open_floats, DBG_LOAD);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
             const int t = qt + x * kStep;
             if (t >= kTile || t >= rows) continue;
             const long long row = row_of(i) + t;
-            if (!dbg_ok(a.dbg, (size_t)row, (size_t)a.tok.rows(), DBG_STORE)) continue;
+            if (!in_bounds(a.dbg, (size_t)row, (size_t)a.tok.rows(), DBG_STORE)) continue;
             const Vec<T, 8> u = raw[0][x][tid], dl = raw[1][x][tid], dy = raw[2][x][tid];
             Vec<T, 8> z, du, dd, dz;
             if (a.z) z = raw[3][x][tid];
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) v += s.bc[b][w][t][x];
             const size_t at = (((size_t)k.blk * a.tok.rows() + row_of(i) + t) * a.G + k.group) * 2 * NP + x;
-            if (t < rows && dbg_ok(a.dbg, at, a.part_bc_floats, DBG_STORE)) a.part_bc[at] = v;
+            if (t < rows && in_bounds(a.dbg, at, a.part_bc_floats, DBG_STORE)) a.part_bc[at] = v;
         }
     };
     if (tiles > 0) {
@@ -457,8 +457,8 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
         }
         const size_t at = ENDS ? seg + k.c0 + tid : 2 * seg + k.c0 + tid;
         if (ENDS) {
-            if (dbg_ok(a.dbg, at, a.sum_floats, DBG_STORE)) a.sums[at] = x;
-        } else if (dbg_ok(a.dbg, at + a.D, a.part_D_floats, DBG_STORE)) {
+            if (in_bounds(a.dbg, at, a.sum_floats, DBG_STORE)) a.sums[at] = x;
+        } else if (in_bounds(a.dbg, at + a.D, a.part_D_floats, DBG_STORE)) {
             a.part_D[at] = x;
             a.part_D[at + a.D] = y;
         }
@@ -481,9 +481,9 @@ __global__ void __launch_bounds__(256) kda_scan_sum_bc_kernel(const ScanArgs a, 
     const size_t step = (size_t)a.tok.rows() * wide;
 #pragma unroll 8
     for (int b = 0; b < nb; ++b)
-        if (dbg_ok(a.dbg, b * step + i, a.part_bc_floats, DBG_LOAD)) s += a.part_bc[b * step + i];
+        if (in_bounds(a.dbg, b * step + i, a.part_bc_floats, DBG_LOAD)) s += a.part_bc[b * step + i];
     const size_t at = ((size_t)row * a.G + group) * a.N + n;
-    if (dbg_ok(a.dbg, at, (size_t)a.tok.rows() * a.G * a.N, DBG_STORE)) ((T *)(x < np ? a.dB : a.dC))[at] = from_f32<T>(s);
+    if (in_bounds(a.dbg, at, (size_t)a.tok.rows() * a.G * a.N, DBG_STORE)) ((T *)(x < np ? a.dB : a.dC))[at] = from_f32<T>(s);
 }
 
 // dA, dskip and ddelta_bias: sums over the segments, in order.
@@ -496,16 +496,16 @@ __global__ void __launch_bounds__(256) kda_scan_sum_params_kernel(const ScanArgs
         if (n >= a.N) return;
 #pragma unroll 4
         for (int j = 0; j < slots; ++j)
-            if (dbg_ok(a.dbg, (size_t)(j * states + i), a.segment_floats, DBG_LOAD)) s += a.part_A[j * states + i];
-        if (dbg_ok(a.dbg, (size_t)(i / np * a.N + n), (size_t)a.D * a.N, DBG_STORE)) a.dA[i / np * a.N + n] = s;
+            if (in_bounds(a.dbg, (size_t)(j * states + i), a.segment_floats, DBG_LOAD)) s += a.part_A[j * states + i];
+        if (in_bounds(a.dbg, (size_t)(i / np * a.N + n), (size_t)a.D * a.N, DBG_STORE)) a.dA[i / np * a.N + n] = s;
     } else if (i < states + 2 * a.D) {
         const int x = (int)(i - states);
 #pragma unroll 4
         for (int j = 0; j < slots; ++j)
-            if (dbg_ok(a.dbg, (size_t)j * 2 * a.D + x, a.part_D_floats, DBG_LOAD)) s += a.part_D[(size_t)j * 2 * a.D + x];
+            if (in_bounds(a.dbg, (size_t)j * 2 * a.D + x, a.part_D_floats, DBG_LOAD)) s += a.part_D[(size_t)j * 2 * a.D + x];
         float *to = x < a.D ? a.dskip : a.ddelta_bias;
         const int c = x < a.D ? x : x - a.D;
-        if (to && dbg_ok(a.dbg, (size_t)c, (size_t)a.D, DBG_STORE)) to[c] = s;
+        if (to && in_bounds(a.dbg, (size_t)c, (size_t)a.D, DBG_STORE)) to[c] = s;
     }
 }
 

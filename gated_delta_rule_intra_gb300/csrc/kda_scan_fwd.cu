@@ -50,12 +50,12 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
             const Four Aj = scaled(load_states(a.A, ch, n0, a.N, in, turn), kLog2e);
             Four hj = {both(0.f), both(0.f)};
             if (!ENDS && in) {
-                const bool given = a.initial && dbg_ok(a.dbg, (size_t)p.seq, (size_t)a.tok.num_seqs, DBG_LOAD);
+                const bool given = a.initial && in_bounds(a.dbg, (size_t)p.seq, (size_t)a.tok.num_seqs, DBG_LOAD);
                 hj = load_states(a.initial, (size_t)p.seq * a.D + ch, n0, a.N, given, turn);
                 for (int g = k.slot - p.index; g < k.slot; ++g) {
                     const size_t at = (size_t)g * a.D + ch;
-                    if (!dbg_ok(a.dbg, at * NP + NP - 1, a.segment_floats, DBG_LOAD) ||
-                        !dbg_ok(a.dbg, at, a.sum_floats, DBG_LOAD))
+                    if (!in_bounds(a.dbg, at * NP + NP - 1, a.segment_floats, DBG_LOAD) ||
+                        !in_bounds(a.dbg, at, a.sum_floats, DBG_LOAD))
                         break;
                     hj = fma(decay(both(a.sums[at]), Aj), hj, four(*(const float4 *)(a.ends + at * NP + n0)));
                 }
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const size_t at = ((size_t)(2 * (tile0 + tile) + half) * a.D + k.c0 + c[j]) * NP + n0;
-                    if (c[j] < k.channels && dbg_ok(a.dbg, at + 3, a.saved_floats, DBG_STORE))
+                    if (c[j] < k.channels && in_bounds(a.dbg, at + 3, a.saved_floats, DBG_STORE))
                         *(float4 *)(a.saved + at) = make_float4(h[j][0], h[j][1], h[j][2], h[j][3]);
                 }
             };
@@ -131,10 +131,10 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
         for (int j = 0; j < 2; ++j) {
             const size_t ch = (size_t)k.c0 + c[j];
             if (c[j] >= k.channels) continue;
-            if (ENDS && dbg_ok(a.dbg, (seg + ch) * NP + NP - 1, a.segment_floats, DBG_STORE))
+            if (ENDS && in_bounds(a.dbg, (seg + ch) * NP + NP - 1, a.segment_floats, DBG_STORE))
                 *(float4 *)(a.ends + (seg + ch) * NP + n0) = make_float4(h[j][0], h[j][1], h[j][2], h[j][3]);
             if (!ENDS && a.final && p.begin + p.len == p.total &&
-                dbg_ok(a.dbg, (size_t)p.seq, (size_t)a.tok.num_seqs, DBG_STORE))
+                in_bounds(a.dbg, (size_t)p.seq, (size_t)a.tok.num_seqs, DBG_STORE))
                 store_states(a.final, (size_t)p.seq * a.D + ch, n0, a.N,
                              four(make_float4(h[j][0], h[j][1], h[j][2], h[j][3])), turn);
         }
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
     auto rows_of = [&](int tile) { return p.len - tile * kTile; };
     auto fine = [&](int tile) {
         const int rows = rows_of(tile);
-        return rows <= 0 || dbg_ok(a.dbg, (size_t)(first + tile * kTile + min(rows, kTile) - 1), (size_t)a.tok.rows(), DBG_LOAD);
+        return rows <= 0 || in_bounds(a.dbg, (size_t)(first + tile * kTile + min(rows, kTile) - 1), (size_t)a.tok.rows(), DBG_LOAD);
     };
     auto fetch = [&](int tile) {
         const int rows = fine(tile) ? rows_of(tile) : 0;
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
         for (int i = 0; i < S::kPer; ++i) {
             const int t = qt + i * kStep;
             const long long row = first + tile * kTile + t;
-            if (t >= kTile || t >= rows || !dbg_ok(a.dbg, (size_t)row, (size_t)a.tok.rows(), DBG_STORE)) continue;
+            if (t >= kTile || t >= rows || !in_bounds(a.dbg, (size_t)row, (size_t)a.tok.rows(), DBG_STORE)) continue;
             const float4 lo = *(const float4 *)&s.y[b][t][8 * q], hi = *(const float4 *)&s.y[b][t][8 * q + 4];
             const float2 sum[4] = {make_float2(lo.x, lo.y), make_float2(lo.z, lo.w), make_float2(hi.x, hi.y),
                                    make_float2(hi.z, hi.w)};
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
                 }
                 put_pair(out, e, y);
             }
-            if (a.open && dbg_ok(a.dbg, (size_t)(open_row(a, row) - a.open) + qc + min(left, 8) - 1, a.open_floats, DBG_STORE)) {
+            if (a.open && in_bounds(a.dbg, (size_t)(open_row(a, row) - a.open) + qc + min(left, 8) - 1, a.open_floats, DBG_STORE)) {
                 // what the gate multiplies, for the gate's gradient
                 float *at = open_row(a, row) + qc;
 #pragma unroll
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
         if (tid < k.channels) {
             float x = 0.f;
             for (int t = 0; t < min(kTile, kStep); ++t) x += sum[t][tid];
-            if (dbg_ok(a.dbg, seg + k.c0 + tid, a.sum_floats, DBG_STORE)) a.sums[seg + k.c0 + tid] = x;
+            if (in_bounds(a.dbg, seg + k.c0 + tid, a.sum_floats, DBG_STORE)) a.sums[seg + k.c0 + tid] = x;
         }
     }
     cp_async_wait_newest<0>();

@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kThreads) kda_scan_step_kernel(const ScanArgs 
         const int r = r0 + i;
         const long long slot = r < a.requests ? a.state_indices ? a.state_indices[r] : r : -1;
         if (slot >= 0 && slot < a.num_states &&
-            dbg_ok(a.dbg, ((size_t)slot * a.D + ch) * a.N + a.N - 1, (size_t)a.num_states * a.D * a.N, DBG_STORE))
+            in_bounds(a.dbg, ((size_t)slot * a.D + ch) * a.N + a.N - 1, (size_t)a.num_states * a.D * a.N, DBG_STORE))
             live |= 1u << i;
         st[i] = a.state + ((size_t)(live >> i & 1 ? slot : 0) * a.D + ch) * a.N + n0;
         h[i] = {both(0.f), both(0.f)};
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) kda_scan_step_kernel(const ScanArgs 
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
         const int r = r0 + mine + i;
-        if (r >= a.requests || !dbg_ok(a.dbg, (size_t)r, (size_t)a.requests, DBG_STORE)) continue;
+        if (r >= a.requests || !in_bounds(a.dbg, (size_t)r, (size_t)a.requests, DBG_STORE)) continue;
         float out = fmaf(skip, u[i], y[i]);
         if (a.z) out *= z[i] * sigmoid(z[i]);
         if (!(live >> (mine + i) & 1)) out = 0.f;  // a row without a request

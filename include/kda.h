@@ -708,8 +708,8 @@ const char *kda_status_str(kda_status_t status);
  * workspace buffers too) against the extent of its buffer.  An index out of range sets
  * KDA_DBG_STORE or KDA_DBG_LOAD in a caller-owned device word and the access is skipped;
  * a bounded wait that gives up sets KDA_DBG_WAIT.  Where the caller has set KDA_DBG_SHORT in the
- * word, every extent counts as one less: the checks of a buffer's last element or row then report and
- * skip it, which shows that they are there.  Nothing traps or asserts.  TMA tiles
+ * word, every extent of the convolution, the scan and the matrix product counts as one less: the checks
+ * of a buffer's last element or row then report and skip it, which shows that they are there.  Nothing traps or asserts.  TMA tiles
  * need no check: the tensor maps clip them.
  *
  * kda_debug_checks() is 1 in such a build, 0 otherwise.  kda_debug_set_flags(word)

@@ -55,11 +55,11 @@ def test_the_scan_reports(B, T, D, N, G, dtype):
 
 
 def test_packed_sequences_report():
-    p = cu([20, 0, 45], 11)
+    p = cu([20, 0, 59], 11)
     x, s = cuda(make_conv(1, 90, 72, 4, BF, seqs=3)), cuda(make_scan(1, 90, 72, 16, 1, BF, seqs=3))
     ins, more = [s[n] for n in SCAN[:5]], [s[n] for n in SCAN[5:]]
     short(lambda: kda.kda_conv_fwd(x["x"], x["weight"], cu_seqlens=p)[:1], STORE | LOAD)
-    short(lambda: kda.kda_scan_fwd(*ins, *more, cu_seqlens=p)[:1], STORE)  # (no sequence ends in the last row)
+    short(lambda: kda.kda_scan_fwd(*ins, *more, cu_seqlens=p)[:1], STORE | LOAD)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
