@@ -214,14 +214,57 @@ __device__ __forceinline__ float2 fma2(float2 a, uint64_t b, float2 c) {
     return r;
 }
 __device__ __forceinline__ Four scaled(Four a, float x) { return {mul2(a.lo, both(x)), mul2(a.hi, both(x))}; }
-// The argument of a token's decay, d A log2(e).  Between 2^-12 and 2^-4 the exponential unit's results
-// are 0.6 to 3e-8 too small on the mean (measured), which states that last a thousand tokens add up;
-// an argument larger by 2.5e-8 takes most of that back, and 2^0 is still 1.
-__device__ __forceinline__ float2 exponent(float2 d, float2 A) { return fma2(d, A, both(2.5e-8f)); }
-__device__ __forceinline__ float2 exponent(float2 d, uint64_t A) { return fma2(d, A, both(2.5e-8f)); }
+__device__ __forceinline__ float2 fma2(float2 a, uint64_t b, uint64_t c) {
+    float2 r;
+    asm("{\n.reg .b64 x;\nmov.b64 x, {%2, %3};\nfma.rn.f32x2 x, x, %4, %5;\nmov.b64 {%0, %1}, x;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "l"(b), "l"(c));
+    return r;
+}
+// The argument of a token's decay, d A log2(e), is taken a little larger than that: the exponential unit's
+// results are too small on the mean, and a state adds that up over all tokens that it lasts.  Measured, for
+// arguments of a size in [1, 2) times 2^n, in 1e-8: n = -20 .. -15 0.7 to 1.1, -14 .. -9 0.5 to 0.9, -8 1.5 and
+// 2.2, -7 3.1 and 2.2, -6 2.2 and 2.9, -5 2.7 and 0.7, -4 .. -1 1.4 to 2.8.  So 2.5e-8 (1.7e-8 of the result), or
+// 1e-8 where the slowest of a thread's states is below 2^-8, of which no more than 0.3e-8 a token
+// is left.  2^0 is still 1.  Relative error of the final states of 8192 tokens, A from -0.001 to -1: 3.5e-6;
+// 3.9e-5 with 2.5e-8 for all, 2.6e-5 without.  (What is left of a step size that never changes is the unit's
+// rounding of that one decay, up to 8e-8 a token.)
+constexpr float kQuick = 2.5e-8f, kSlow = 1e-8f;
+// e: the smallest size of a thread's arguments.
+__device__ __forceinline__ float raise_of(float e) { return e < 0x1p-8f ? kSlow : kQuick; }
+__device__ __forceinline__ float slowest_of(Four A2, int n, int N, int turn) {
+    float x = 3e38f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (n + (i ^ turn) < N) x = fminf(x, fabsf(A2.get(i)));
+    return x;
+}
+// That number for each of the forward's walking threads, from the first token of the tile that was walked before:
+// the preparing half finds it, because the walking threads have no register left for it (found there, a prompt
+// of 32768 tokens takes 1290 us instead of 1249).
+template <int NP> struct Raise {
+    float slowest[2];
+    int at[2];
+    __device__ __forceinline__ Raise(const ScanArgs &a, int c0, int channels, int tid) {
+        using S = Shape<NP>;
+        const int n0 = 4 * (tid % S::L);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int c = tid / S::L + j * S::HC;
+            slowest[j] = slowest_of(scaled(load_states(a.A, (size_t)c0 + c, n0, a.N, c < channels), kLog2e), n0,
+                                    c < channels ? a.N : 0, 0);
+            at[j] = place(c, 0);
+        }
+    }
+    __device__ __forceinline__ float2 next(const float *d) const {
+        return both(raise_of(fminf(fabsf(d[at[0]]) * slowest[0], fabsf(d[at[1]]) * slowest[1])));
+    }
+};
+// The first pass over segments keeps to 2.5e-8: its sums are a segment's alone.
+__device__ __forceinline__ float2 exponent(float2 d, uint64_t A) { return fma2(d, A, both(kQuick)); }
 // 2^(d a)
-__device__ __forceinline__ Four decay(float2 dd, Four a2) {
-    const float2 l = exponent(dd, a2.lo), h = exponent(dd, a2.hi);
+__device__ __forceinline__ Four decay(float2 dd, Four a2, float raise) {
+    const float2 l = fma2(dd, a2.lo, both(raise)), h = fma2(dd, a2.hi, both(raise));
     return {make_float2(ex2(l.x), ex2(l.y)), make_float2(ex2(h.x), ex2(h.y))};
 }
 __device__ __forceinline__ Four mul(Four a, Four b) { return {mul2(a.lo, b.lo), mul2(a.hi, b.hi)}; }
@@ -243,6 +286,16 @@ struct Phase {
     __device__ __forceinline__ void load4(uint32_t off, float2 (&to)[2]) const {
         asm("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
             : "=f"(to[0].x), "=f"(to[0].y), "=f"(to[1].x), "=f"(to[1].y) : "r"(base + off));
+    }
+    __device__ __forceinline__ float load(uint32_t off) const {
+        float x;
+        asm("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(base + off));
+        return x;
+    }
+    __device__ __forceinline__ uint64_t load_pair(uint32_t off) const {
+        uint64_t x;
+        asm("ld.shared.b64 %0, [%1];" : "=l"(x) : "r"(base + off));
+        return x;
     }
     __device__ __forceinline__ float2 load2(uint32_t off) const {
         float2 x;

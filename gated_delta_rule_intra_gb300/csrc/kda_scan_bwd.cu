@@ -63,13 +63,14 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
         const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, part = tid % S::L, n0 = 4 * part;
         const int c[2] = {tid / S::L, tid / S::L + S::HC}, turn = turn_of<NP>(tid);
         uint64_t A2[2][4];
-        float carry[2][4];
+        float carry[2][4], slowest[2];
         float2 dA[2][4] = {};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const bool in = c[j] < k.channels;
             const size_t ch = (size_t)k.c0 + c[j];
             const Four Aj = scaled(load_states(a.A, ch, n0, a.N, in, turn), kLog2e);
+            slowest[j] = slowest_of(Aj, n0, in ? a.N : 0, turn);
             Four g = {both(0.f), both(0.f)};
             if (!ENDS && p.len >= 0 && in) {  // from the segments behind this one
                 const bool given = a.d_final && in_bounds(a.dbg, (size_t)p.seq, (size_t)a.tok.num_seqs, DBG_LOAD);
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
                     if (!in_bounds(a.dbg, at * NP + NP - 1, a.segment_floats, DBG_LOAD) ||
                         !in_bounds(a.dbg, at, a.sum_floats, DBG_LOAD))
                         break;
-                    g = fma(decay(both(a.sums[at]), Aj), g, four(*(const float4 *)(a.ends + at * NP + n0)));
+                    g = fma(decay(both(a.sums[at]), Aj, 0.f), g, four(*(const float4 *)(a.ends + at * NP + n0)));
                 }
             }
 #pragma unroll
@@ -122,6 +123,8 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
 #pragma unroll
             for (int n = 0; n < 4; ++n) oB[n] = off(&s.B[b][part][(n ^ turn) * kTile]);
             constexpr uint32_t toC = offsetof(M, C) - offsetof(M, B);
+            const uint64_t raise = ENDS ? 0 : twice(raise_of(fminf(fabsf(phase.load(od[0])) * slowest[0],
+                                                                   fabsf(phase.load(od[1])) * slowest[1])));
             // token t of a channel is at its place: groups of four change places (a XOR)
             auto at4 = [&](int j, int g) { return od[j] ^ (uint32_t)g << 4; };
             if (ENDS) {
@@ -168,7 +171,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
                                 phase.load4(oB[n] + 16 * g, B);
 #pragma unroll
                                 for (int t = 0; t < 2; ++t) {
-                                    const float2 e = exponent(d[t], A2[j][n]);
+                                    const float2 e = fma2(d[t], A2[j][n], raise);
                                     float2 &pp = P[j][n][2 * gl + t];
                                     pp.x = ex2(e.x) * h[j][n];
                                     pp.y = ex2(e.y) * fmaf(x[t].x, B[t].x, pp.x);
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_bwd_kernel(const Sca
 #pragma unroll
                             for (int n = 0; n < 4; ++n) {
                                 const float2 pp = P[j][n][pi];
-                                const float2 e = exponent(d, A2[j][n]), hh = fma2(x, B[n], pp);
+                                const float2 e = fma2(d, A2[j][n], raise), hh = fma2(x, B[n], pp);
                                 float2 G;
                                 G.y = fmaf(gg.y, C[n].y, carry[j][n]);
                                 G.x = fmaf(gg.x, C[n].x, G.y * ex2(e.y));

@@ -21,6 +21,7 @@ template <typename T, int NP> struct Smem {
     float d[2][S::CH * kTile], x[2][S::CH * kTile];  // step size, step size times input: place()
     float B[2][S::L][S::kVec], C[2][S::L][S::kVec];
     float y[2][kTile][S::kRow];                       // sums over a channel's states
+    float2 raise[2][kThreads];                        // Raise, of each walking thread
     Vec<T, 8> raw[kStages][3][S::kPer][kThreads];     // u, delta, z: a slot of each thread
 };
 
@@ -57,7 +58,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
                     if (!in_bounds(a.dbg, at * NP + NP - 1, a.segment_floats, DBG_LOAD) ||
                         !in_bounds(a.dbg, at, a.sum_floats, DBG_LOAD))
                         break;
-                    hj = fma(decay(both(a.sums[at]), Aj), hj, four(*(const float4 *)(a.ends + at * NP + n0)));
+                    hj = fma(decay(both(a.sums[at]), Aj, 0.f), hj, four(*(const float4 *)(a.ends + at * NP + n0)));
                 }
             }
 #pragma unroll
@@ -85,6 +86,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
 #pragma unroll
             for (int n = 0; n < 4; ++n) oB[n] = (uint32_t)((char *)&s.B[b][part][(n ^ turn) * kTile] - smem);
             constexpr uint32_t toC = offsetof(M, C) - offsetof(M, B);
+            const uint64_t raise = ENDS ? 0 : phase.load_pair((uint32_t)((char *)&s.raise[b][tid] - smem));
 #pragma unroll
             for (int g = 0; g < kTile / 4; ++g) {
                 if (!ENDS && a.saved && g % 2 == 0) save(g / 2);
@@ -105,7 +107,8 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
                         float2 sum;
 #pragma unroll
                         for (int n = 0; n < 4; ++n) {
-                            const float2 e = exponent(d[t], A2[j][n]), in = mul2(x[t], B[n][t]);
+                            const float2 e = ENDS ? exponent(d[t], A2[j][n]) : fma2(d[t], A2[j][n], raise);
+                            const float2 in = mul2(x[t], B[n][t]);
                             float2 hh;
                             hh.x = fmaf(ex2(e.x), h[j][n], in.x);
                             hh.y = fmaf(ex2(e.y), hh.x, in.y);
@@ -171,6 +174,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
         cp_async_commit();
     };
     Vectors<T, NP> vb, vc;
+    const Raise<NP> raise(a, k.c0, k.channels, tid);
     auto vectors = [&](int tile) {
         const int rows = fine(tile) ? rows_of(tile) : 0;
         vb.load(tid, a.B, a.B_stride, first + tile * kTile, rows, k.group, a.N);
@@ -199,7 +203,10 @@ __global__ void __launch_bounds__(2 * kThreads, 2) kda_scan_fwd_kernel(const Sca
             }
         }
         vb.put(tid, s.B[b]);
-        if (!ENDS) vc.put(tid, s.C[b]);
+        if (!ENDS) {
+            vc.put(tid, s.C[b]);
+            s.raise[b][tid] = tile > 0 ? raise.next(s.d[b ^ 1]) : both(kQuick);
+        }
     };
     const bool quads = a.D / a.G % 4 == 0;  // blocks of channels begin on four
     auto finish = [&](int tile) {

@@ -30,7 +30,7 @@ __device__ __forceinline__ Four vector_of(const void *base, long long at, int n0
 
 // WIDE: N is a multiple of 4, and so is where rows of B and C begin.
 template <typename T, int NP, int R, bool WIDE>
-__global__ void __launch_bounds__(kThreads) kda_scan_step_kernel(const ScanArgs a) {
+__global__ void __launch_bounds__(kThreads, R == 4 ? 6 : 1) kda_scan_step_kernel(const ScanArgs a) {
     wait_for_previous();
     using S = Shape<NP>;
     // the requests of this lane: all of them, or its share
@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(kThreads) kda_scan_step_kernel(const ScanArgs 
         }
     }
     const Four A2 = scaled(load_states(a.A, ch, n0, a.N, in), kLog2e);
+    const float slowest = slowest_of(A2, n0, a.N, 0);
     if (a.softplus) {
 #pragma unroll
         for (int i = 0; i < kMine; ++i) d[i] = softplus(d[i]);
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) kda_scan_step_kernel(const ScanArgs 
             di = __shfl_sync(0xffffffffu, di, from, S::L);
             ui = __shfl_sync(0xffffffffu, ui, from, S::L);
         }
-        h[i] = fma(decay(both(di), A2), h[i], mul(both(di * ui), B[i]));
+        h[i] = fma(decay(both(di), A2, raise_of(fabsf(di) * slowest)), h[i], mul(both(di * ui), B[i]));
         y[i] = dot(h[i], C[i]);
         if ((live >> i & 1) && in && some) {
             if (WIDE)

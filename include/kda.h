@@ -566,7 +566,9 @@ kda_status_t kda_conv_step(const void *x, const void *weight, const void *bias, 
  * (KDA_BF16, KDA_FP16 or KDA_FP32) with a row stride each, in elements (0 = D, G N); A [D, N], skip,
  * delta_bias [D] fp32.  skip, z, delta_bias: NULL = none.  A is finite, <= 0 for states that fade.
  * Pointers need their element's alignment (rows on boundaries of four elements are read
- * four channels at a time), saved and workspace 256 bytes.  States, sums and exponentials are FP32.
+ * four channels at a time), saved and workspace 256 bytes.  States, sums and exponentials are FP32: a token's
+ * decay is off by 3e-9 of the state on the mean, by 3e-8 at random (by the same number at every token where
+ * delta never changes, 8e-8 at most), which a state adds up over the tokens that it lasts.
  *   initial_state, final_state   [sequences, D, N] fp32 as in kda_chunk_fwd
  *   saved, saved_bytes           what kda_scan_bwd needs: kda_scan_saved_bytes(), N / 2 + 4 bytes (N
  *                                rounded up to 8, 16, 32 or 64) a token and channel; NULL when no

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import gated_delta_rule_intra_gb300 as kda
-from tests._layer import BF, F64, HF, act64, cuda, make_linear, rel, tol
+from tests._layer import BF, F64, HF, SCAN, act64, cuda, make_linear, rel, tol
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +83,63 @@ def test_what_a_kernel_that_gives_up_leaves(M, K, N, pre, dtype):
         assert rel(again, want) <= tol(dtype)
     with pytest.raises(kda.KdaError):
         kda.kda_debug_set_give_up(True)  # not in the normal build
+
+
+# ---------------------------------------------------------------------------- long memories
+def slow_scan(few, B, T, D, N, seed=3):
+    """Sequences whose states last thousands of tokens: (call's inputs, the first `few`'s 64-bit results).
+    Only those have a dy, so that all sums over tokens are theirs."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    x = {"u": torch.randn(B, T, D, device="cuda", generator=g), "z": torch.randn(B, T, D, device="cuda", generator=g),
+         "delta": 0.5 * torch.randn(B, T, D, device="cuda", generator=g),
+         "B": torch.randn(B, T, 1, N, device="cuda", generator=g),
+         "C": torch.randn(B, T, 1, N, device="cuda", generator=g),
+         "D": 1 + 0.2 * torch.randn(D, device="cuda", generator=g), "dy": torch.zeros(B, T, D, device="cuda")}
+    x["dy"][:few] = torch.randn(few, T, D, device="cuda", generator=g)
+    x["A"] = -0.003 * torch.exp(0.3 * torch.randn(D, N, device="cuda", generator=g))
+    x["delta_bias"] = torch.linspace(-3.0, -1.5, D, device="cuda")  # step sizes around 0.05 to 0.2
+    f = {n: x[n][:few].to(F64) if x[n].shape[0] == B else x[n].to(F64) for n in x}
+    s = torch.nn.functional.softplus(f["delta"] + f["delta_bias"])
+    h, hs, ys = torch.zeros(few, D, N, dtype=F64, device="cuda"), [], []
+    for t in range(T):
+        hs.append(h)
+        h = torch.exp(s[:, t, :, None] * f["A"]) * h + (s[:, t] * f["u"][:, t])[..., None] * f["B"][:, t]
+        ys.append((h * f["C"][:, t]).sum(-1))
+    gate = f["z"] * torch.sigmoid(f["z"])
+    want = {"y": (torch.stack(ys, 1) + f["D"] * f["u"]) * gate, "state": h}
+    dy, carry, dA = f["dy"] * gate, torch.zeros_like(h), torch.zeros_like(f["A"])
+    du = torch.empty_like(dy)
+    for t in reversed(range(T)):
+        a = torch.exp(s[:, t, :, None] * f["A"])
+        G = carry + dy[:, t, :, None] * f["C"][:, t]
+        du[:, t] = s[:, t] * (G * f["B"][:, t]).sum(-1) + f["D"] * dy[:, t]
+        carry = G * a
+        dA += (carry * hs[t] * s[:, t, :, None]).sum(0)
+    return x, {**want, "du": du, "dA": dA, "d_initial": carry}
+
+
+def test_states_that_last_thousands_of_tokens():
+    """Walked from end to end (as many sequences as fill the card), A around -0.003."""
+    few, B, T, D, N = 2, 256, 8192, 64, 16
+    x, want = slow_scan(few, B, T, D, N)
+    ins, more = [x[n] for n in SCAN[:5]], [x[n] for n in SCAN[5:]]
+    assert kda.load_library().kda_scan_fwd_workspace_bytes(B, T, D, N, 1, 0) == 0  # one segment
+    y, state, saved = kda.kda_scan_fwd(*ins, *more, save=True, output_final_state=True)
+    out = kda.kda_scan_bwd(x["dy"], *ins, saved, *more, output_d_initial_state=True)
+    got = {"y": y[:few], "state": state[:few], "du": out[0][:few], "dA": out[2], "d_initial": out[8][:few]}
+    # A decay's relative rounding to FP32 below 1 is 2^-25 on the mean of its size (RMS 2^-24 / sqrt 3 with that of
+    # the state itself) and of random sign: over the 3000 tokens that a state lasts, sqrt(3000) 4e-8 = 2e-6.
+    # What it is off on the mean, a tenth of 2^-25 = 3e-9 a token, is 3000 times that: 9e-6; dA's terms hold a
+    # state and its gradient, each of which is off so.
+    for name, ref in want.items():
+        assert rel(got[name], ref) <= (22e-6 if name == "dA" else 11e-6), name
+
+
+def test_states_that_last_thousands_of_single_tokens():
+    few, B, T, D, N = 2, 2, 8192, 64, 16
+    x, want = slow_scan(few, B, T, D, N)
+    state = torch.zeros(B, D, N, device="cuda")
+    for t in range(T):
+        kda.kda_scan_step(x["u"][:, t], x["delta"][:, t], x["A"], x["B"][:, t], x["C"][:, t], state, *(
+            x["D"], x["z"][:, t], x["delta_bias"]))
+    assert rel(state, want["state"]) <= 11e-6
