@@ -143,3 +143,20 @@ def test_states_that_last_thousands_of_single_tokens():
         kda.kda_scan_step(x["u"][:, t], x["delta"][:, t], x["A"], x["B"][:, t], x["C"][:, t], state, *(
             x["D"], x["z"][:, t], x["delta_bias"]))
     assert rel(state, want["state"]) <= 11e-6
+
+
+# ---------------------------------------------------------------------------- derivatives in the tails
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("M,N", [(1, 16), (40, 15)])
+def test_derivatives_in_the_tails(M, N, act):
+    """Relative to themselves, where an absolute allowance would let 0 pass."""
+    v = torch.tensor([-2.0, -2.5, -3.0, -4.0, -5.0, -6.5, -8.0, -10.0, -13.0, 2.0, 3.0, 5.0, 8.0, 0.5, 0.0, -0.25][:N], dtype=BF)
+    x, w = torch.zeros(M, 8, dtype=BF, device="cuda"), torch.zeros(N, 8, dtype=BF, device="cuda")
+    saved = kda.kda_linear_fwd(x, w, v.cuda(), activation=act, save=True)[1]
+    dy = torch.ones(M, N, dtype=BF, device="cuda")
+    got = kda.kda_linear_bwd(dy, x, w, saved, activation=act, input_grad=False, weight_grad=False)[2]
+    t = v.to(F64).requires_grad_()
+    want = torch.autograd.grad(act64(t, act).sum(), t)[0] * M
+    # BF16's rounding of the result, and the exponential's argument (some 120 at -13) rounded to FP32 beside
+    # the approximation's 7e-7: 120 2^-24 + 2e-6
+    assert ((got.cpu().to(F64) - want).abs() <= want.abs() * (2.0 ** -8 + 1e-5) + 2.0 ** -126).all()
