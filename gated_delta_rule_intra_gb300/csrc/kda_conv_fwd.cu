@@ -3,8 +3,10 @@
 // Bound by memory: x is read and y written once.  Rows come through shared memory, two pieces ahead
 // (kda_conv.cuh): 140 us at B=8 T=4096 D=6144 W=4 bf16 with silu, 5.7 TB/s, 85% of a copy's rate.  (Loads
 // into registers eight tokens ahead: 188 us, with a third of the instructions moving and addressing
-// them.  Stores marked as not to be kept in L2: 148.)  9467 tokens of 1111 fp16 channels, whose rows are on
-// no 4-byte boundary, take 28.5 us: copies of 4-byte words and their addresses bound those.
+// them.  Stores marked as not to be kept in L2: 148.)  9467 tokens of 1111 fp16 channels
+// take 28.7 us (x's rows, a slice's, begin on 4-byte boundaries there, y's on none), of 1112 15.0: what odd
+// rows add is copies of 4-byte words and y's way out through shared memory, at 38% of the issue slots and 9%
+// of memory's rate, four warps a scheduler that wait in turn.
 //
 // Single tokens (kda_conv_step_kernel): a thread has four channels of a request, the last inputs and
 // the token in registers; a few requests are the latency of one launch (2 us beside the host's 4).

@@ -15,10 +15,11 @@
 // few for the card, the contraction is cut into parts whose sums a second kernel joins, always in the
 // same order.
 //
-// Bound by the tensor cores: 32768 x 2048 x 8192 bf16 with silu 555 us, 1.98 PFLOP/s (the library's plain
-// product 543; 788 without pairs, 705 with copies and products issued under a test of the lane, which
-// makes the compiler take every operand of theirs through a loop); 8192 x 2048 x 8192 with gelu and a
-// second result 162, its gradients 395 with the 80 of their first step (256 tiles are 3.4 rounds of 76
+// Bound by the tensor cores, and by the power limit where calls follow one another for a second or more (1.5
+// GHz instead of 2.07): 32768 x 2048 x 8192 bf16 with silu 636 us, 1.73 PFLOP/s (the library's plain product
+// 613), and 557 in a burst (549).  In bursts: 788 without pairs, 705 with copies and products issued under a
+// test of the lane, which makes the compiler take every operand of theirs through a loop; 8192 x 2048 x 8192
+// with gelu and a second result 162, its gradients 395 with the 80 of their first step (256 tiles are 3.4 rounds of 76
 // pairs; with whole tiles in the last one too 449).
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -698,7 +699,7 @@ template <typename T> cudaError_t run(const GemmArgs &a, cudaStream_t stream) {
     const Plan q = plan_of(a.M, a.N, a.K);
     Maps maps;
     // what lies in shared memory behind the last row of a few becomes rows of the result that nobody takes
-    // (17 rows, 2048 x 8192: 13.4 us, 17.8 with zeros copied there)
+    // (17 rows, 2048 x 8192: 11.3 us with the weight in L2; zeros copied there cost 4.4 more)
     const int rows_a = !a.a_mn && a.M < BM ? (a.M + 7) / 8 * 8 : BM;
     cudaError_t e = a.a_mn ? encode(&maps.a, a.fp16, a.A, a.M, a.K, a.lda, 64, BK)
                            : encode(&maps.a, a.fp16, a.A, a.K, a.M, a.lda, BK, rows_a);

@@ -13,7 +13,7 @@
 // four states, over the CTA's warps in shared memory and over the CTAs by a second kernel,
 // always in the same order.
 //
-// Bound by what a warp waits for (issue slots 54%, shared memory's data pipe 62%): 730 us at B=4 T=2048
+// Bound by what a warp waits for (issue slots 54%, shared memory's data pipe 63%): 726 us (fp32 979) at B=4 T=2048
 // D=4096 N=16 bf16, where the bytes are 79 at a copy's rate and the exponentials 115.  With the gate's
 // factor computed again from the states instead of read it took 954 us (the forward leaves it unrounded:
 // 16 bits would save 8 us both ways and make dz's error 1.4 times its rounding), with both halves' registers

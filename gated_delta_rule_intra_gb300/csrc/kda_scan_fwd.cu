@@ -4,9 +4,10 @@
 // have buffers of their own, so that one barrier a tile joins them; inputs are asked for three
 // tiles ahead.
 //
-// Bound by what a warp waits for (issue slots 55%, shared memory's data pipe 58%; two CTAs a
-// multiprocessor take 478 us for 4096 tokens of 64 channels each, one alone 425): 245 us at B=4 T=2048
-// D=4096 N=16 bf16 (256 CTAs), where the bytes are 40 at a copy's rate and the exponentials 58.  One
+// Bound by what a warp waits for (issue slots 54%, shared memory's data pipe 59%; two CTAs a
+// multiprocessor take 478 us for 4096 tokens of 64 channels each, one alone 425): 256 us at B=4 T=2048
+// D=4096 N=16 bf16 (256 CTAs; 240 where nothing is saved; fp32 288), where the bytes are 40 at a copy's rate
+// and the exponentials 58; 32768 tokens 1250.  One
 // channel a thread took 475 us, two without the order of states that lets their sums be shared 387.
 #include "kda_scan.cuh"
 

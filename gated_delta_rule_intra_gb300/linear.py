@@ -98,9 +98,11 @@ def _linear_fwd(x, weight, bias, residual, activation, save, y):
 
 def kda_linear_bwd(dy, x, weight, saved=None, *, activation=None, input_grad=True, weight_grad=True,
                    bias_grad=True, dx=None, stream=None):
-    """Gradients of ``kda_linear_fwd``.  Returns (dx, dweight, dbias), all in x's dtype, rounded once
-    from FP32 sums in a fixed order (None where not wanted).  x and weight as given to the forward,
-    dy like its y, ``saved`` what it returned with ``save=True``.  residual's gradient is dy itself.
+    """Gradients of ``kda_linear_fwd``.  Returns (dx, dweight, dbias), all in x's dtype (None where not
+    wanted).  x and weight as given to the forward, dy like its y, ``saved`` what it returned with
+    ``save=True``.  residual's gradient is dy itself.  Sums are FP32, in a fixed order, and rounded at their
+    end.  With an activation what they are made of has 16 bits: the derivative is taken at ``saved``, and dx and
+    dweight are products of dpre = dy act'(saved), itself rounded (dbias sums it unrounded).
     """
     if stream is None and dx is None and activation in ACTIVATIONS:
         out = library().quick_linear_bwd(dy, x, weight, saved, ACTIVATIONS[activation], input_grad,

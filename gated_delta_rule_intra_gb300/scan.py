@@ -89,9 +89,11 @@ def kda_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, initial_sta
     d // (D // groups).  A [D, N], D [D] (the skip) and delta_bias [D] fp32.  D, z and delta_bias
     may be None; without ``delta_softplus`` the step sizes are delta + delta_bias as they are.
     ``initial_state`` [sequences, D, N] fp32 defaults to zeros; final_state is None unless
-    ``output_final_state``; saved is what ``kda_scan_bwd`` needs (N / 2 + 4 bytes
-    a token and channel), None unless ``save``.  ``cu_seqlens`` (int32 [N + 1] on the device, B = 1) packs
-    sequences along T; y is zero at tokens in no sequence when it is allocated here.
+    ``output_final_state``; saved is what ``kda_scan_bwd`` needs, None unless ``save``: P / 2 + 4 bytes a
+    token and channel, P being N rounded up to 8, 16, 32 or 64, with each sequence's tokens rounded up to 16 in
+    the first term (packed ones take up to 16 more), the 4 with or without z.  ``cu_seqlens`` (int32 [N + 1]
+    on the device, B = 1) packs sequences along T; y is zero at tokens in no sequence when it is allocated
+    here.
     """
     if stream is None and y is None and delta_softplus:
         out = library().quick_scan_fwd(u, delta, A, B, C, D, z, delta_bias, initial_state,
