@@ -8,9 +8,9 @@
 // come through shared memory, one piece ahead (kda_conv.cuh).  A thread has the last W values of g in
 // registers too, and walks W - 1 tokens more whose g its last inputs need; a whole run is one straight
 // piece of code (with a test in every token: 434 us).  Pieces of 96 tokens leave room for four CTAs a
-// multiprocessor; pieces of 128, three: 328 us.  Odd rows (9467 tokens of 1111 fp16 channels) take 52 us, 1112 channels 25: words
-// shifted when read, dx out through shared memory, 36% of the issue slots.  The CTAs' sums of the parameters' gradients are added up
-// in a fixed order by a second kernel.
+// multiprocessor; pieces of 128, three: 328 us.  Odd rows (9467 tokens of 1111 fp16 channels) take 52 us, 1112
+// channels 25: words shifted when read, dx out through shared memory, 36% of the issue slots.  The CTAs'
+// sums of the parameters' gradients are added up in a fixed order by a second kernel.
 #include <type_traits>
 
 #include "kda_conv.cuh"
