@@ -99,7 +99,9 @@ __device__ __forceinline__ void fetch_rows(char *to, const ConvArgs &a, const Pi
     const int left = (a.D - c0) * E + s;                          // bytes of the row from its first word on
     const int most = min(unit, left - word * unit), tail = min(4, left - 128);  // of this word, of the 33rd
     const char *at = (const char *)base + first * E - s + word * unit;
-    const char *any = (const char *)((uintptr_t)base & ~(uintptr_t)3);
+    // an address for copies of nothing: the rows' own, which a batch of no tokens may not have
+    const char *any = base ? (const char *)((uintptr_t)base & ~(uintptr_t)3)
+                           : (const char *)((uintptr_t)a.weight & ~(uintptr_t)15);
     uint32_t d = (uint32_t)__cvta_generic_to_shared(to) + row * kRow + word * unit;
     const long long ahead = step * stride * E;
     const bool last = ODD && s && word == 0;

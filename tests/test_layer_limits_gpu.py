@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import gated_delta_rule_intra_gb300 as kda
-from tests._layer import BF, F64, HF, SCAN, act64, cuda, make_linear, rel, tol
+from tests._layer import BF, F32, F64, HF, SCAN, act64, cu, cuda, make_conv, make_linear, rel, tol
 
 pytestmark = pytest.mark.gpu
 
@@ -160,3 +160,21 @@ def test_derivatives_in_the_tails(M, N, act):
     # BF16's rounding of the result, and the exponential's argument (some 120 at -13) rounded to FP32 beside
     # the approximation's 7e-7: 120 2^-24 + 2e-6
     assert ((got.cpu().to(F64) - want).abs() <= want.abs() * (2.0 ** -8 + 1e-5) + 2.0 ** -126).all()
+
+
+# ---------------------------------------------------------------------------- no tokens
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,W", [(16, 4), (77, 3)])
+@pytest.mark.parametrize("packed", [False, True])
+def test_a_convolution_of_no_tokens(D, W, packed, dtype):
+    """Tensors without elements have no address; the states pass through."""
+    x = cuda(make_conv(1 if packed else 2, 0, D, W, dtype, seqs=2))
+    p = cu([0, 0]) if packed else None
+    for initial in (None, x["initial"]):
+        y, last = kda.kda_conv_fwd(x["x"], x["weight"], x["bias"], initial, activation="silu", output_final_state=True,
+                                   cu_seqlens=p)
+        assert y.shape == x["x"].shape
+        assert torch.equal(last, torch.zeros_like(x["initial"]) if initial is None else initial)
+        dx, dw, db, di = kda.kda_conv_bwd(x["dy"], x["x"], x["weight"], x["bias"], initial, x["dfinal"],
+                                          activation="silu", output_d_initial_state=True, cu_seqlens=p)
+        assert dx.shape == y.shape and not dw.any() and not db.any() and torch.equal(di, x["dfinal"])
