@@ -519,6 +519,12 @@ cudaError_t walk(const ScanArgs &a, int nb, int unit, cudaStream_t stream) {
     static volatile int done[kMaxDev];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
+    // (with fewer registers at launch than it hands out, the walking half would wait for ever)
+    if (e == cudaSuccess && !ENDS && (dev >= kMaxDev || !done[dev])) {
+        cudaFuncAttributes f;
+        e = cudaFuncGetAttributes(&f, kda_scan_bwd_kernel<T, NP, ENDS>);
+        if (e == cudaSuccess && f.numRegs < kLaunchRegs) e = cudaErrorInvalidConfiguration;
+    }
     if (e == cudaSuccess) e = smem_limit_once(kda_scan_bwd_kernel<T, NP, ENDS>, kBytes, dev, done);
     if (e != cudaSuccess) return e;
     return launch_early(kda_scan_bwd_kernel<T, NP, ENDS>, (unsigned)(a.tok.pieces(a.segment) * nb * a.G),
